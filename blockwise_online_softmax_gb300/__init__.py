@@ -18,6 +18,12 @@ from .binding import (  # noqa: E402,F401
     ra_device_status,
     ra_finalize,
     ra_merge,
+    ra_paged_append,
+    ra_paged_decode,
+    ra_paged_extend,
+    ra_paged_release,
+    ra_qk_norm_rope,
+    ra_qk_norm_rope_backward,
     ra_release_cached_memory,
     ra_ring_forward,
     ra_ring_forward_host,
@@ -32,4 +38,6 @@ from .binding import (  # noqa: E402,F401
     ra_trace_enable,
     ra_trace_query,
     ra_trace_reset,
+    rope_freqs,
+    rope_phases,
 )

@@ -8,6 +8,7 @@ raises ``RaError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -39,6 +40,14 @@ KERNEL_KINDS = {
     "bwd_dkdv": 9,
     "ring_fused_bf16": 10,
     "ring_fused_f32": 11,
+    "paged_extend": 12,
+    "paged_release": 13,
+    "qk_norm_rope": 14,
+    "qk_norm_rope_bwd": 15,
+    "qk_norm_weight_grad": 16,
+    "paged_append": 17,
+    "paged_decode": 18,
+    "paged_combine": 19,
 }
 
 _lock = threading.Lock()
@@ -68,6 +77,12 @@ _SIGNATURES = {
     "ra_ring_backward": ("PPPPPPPPPLiiiiiiP", "i"),
     "ra_ring_backward_masked": ("PPPPPPPPPLiiiLLPiiiiiP", "i"),
     "ra_decode_forward": ("PPPPPLLiLiLiiiiP", "i"),
+    "ra_qk_norm_rope": ("PPPPLiiiLLPiiiiPfPPifiP", "i"),
+    "ra_qk_norm_rope_backward": ("PPPPPPPPLiiiLLLLPiiiiPfPPifiP", "i"),
+    "ra_paged_extend": ("PPiPiPiPiLPPPPPPP", "i"),
+    "ra_paged_release": ("PPiPiPiPiPPP", "i"),
+    "ra_paged_append": ("PPPPPPLiiiLLLiiLLPPiiPfPPifiP", "i"),
+    "ra_paged_decode": ("PPPPPLiiPPiPiiLLLiiiiiP", "i"),
     "ra_device_status": ("P", "i"),
     "ra_selftest_wait_timeout": ("LP", "i"),
     "ra_cached_memory": ("P", "i"),
@@ -79,7 +94,8 @@ _SIGNATURES = {
     "ra_last_error": ("", "s"),
     "ra_abi_version": ("", "i"),
 }
-_CT = {"P": ctypes.c_void_p, "L": ctypes.c_longlong, "i": ctypes.c_int, "s": ctypes.c_char_p}
+_CT = {"P": ctypes.c_void_p, "L": ctypes.c_longlong, "i": ctypes.c_int, "s": ctypes.c_char_p,
+       "f": ctypes.c_float}
 
 
 def lib():
@@ -408,6 +424,359 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
         _dev(q, "q"), kp, vp, _dev(out, "out", torch.float32), _dev(lse, "lse", torch.float32),
         n_q, n_kv, int(P), int(q_off), int(bool(causal)), int(window), d, heads, kv_heads,
         _qkv_dtype(q), _stream(stream)))
+    return out, lse
+
+
+# ------------------------------------------------------------------ rotary positions, pages
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+def _rows(t: torch.Tensor, name: str, heads: int, d: int, dtype=None) -> tuple[int, int]:
+    """Pointer and token stride of a [T, heads, d] CUDA tensor whose heads are
+    dense; tokens may lie further apart (a view of a packed projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _vector(t, name, n, dtype):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    return _dev(t, name, dtype)
+
+
+def _weight(q_weight, k_weight, d):
+    """Pointers of the norm weights (0 for none) and their dtype."""
+    given = [(w, n) for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")) if w is not None]
+    for w, n in given:
+        if w.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{n} must be float32 or bfloat16, got {w.dtype}")
+        if w.dtype != given[0][0].dtype:
+            raise TypeError("q_weight and k_weight must share a dtype")
+        _vector(w, n, d, w.dtype)
+    code = RA_BF16 if given and given[0][0].dtype == torch.bfloat16 else RA_F32
+    return (q_weight.data_ptr() if q_weight is not None else 0,
+            k_weight.data_ptr() if k_weight is not None else 0, code)
+
+
+def _phase_table(phases):
+    if phases is None:
+        return 0, 0
+    if phases.dim() != 1:
+        raise ValueError("phases must be 1-D with rot_dim / 2 entries")
+    return _dev(phases, "phases", torch.int64), 2 * phases.numel()
+
+
+def _qk_shapes(q, k):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q: [T, heads, d]; k: [T, kv_heads, d]")
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype:
+        raise ValueError("q and k must share their tokens, head dim and dtype")
+    return q.shape[0], q.shape[1], k.shape[1], q.shape[2]
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None,
+               factor: float = 1.0, original_length: int = 4096, fast_turns: float = 32.0,
+               slow_turns: float = 1.0) -> tuple[torch.Tensor, float]:
+    """Rotary frequencies (fp64 [rot_dim / 2], radians per position, CPU) and
+    the factor on cos and sin, for a head of rot_dim rotated columns.  Host
+    arithmetic for callers; pass the frequencies on through rope_phases.
+
+    scaling None: base^(-2i / rot_dim).  "linear": positions divided by
+    `factor`.  "ntk": the base raised by factor^(rot_dim / (rot_dim - 2)).
+    "yarn" (Peng et al. 2023): frequencies that make at least fast_turns
+    turns over original_length positions stay, those below slow_turns are
+    divided by `factor`, with a linear blend in pair index between, and cos
+    and sin are multiplied by 0.1 ln(factor) + 1."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim={rot_dim} must be even and positive")
+    if factor < 1.0:
+        raise ValueError(f"factor={factor} must be >= 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    f = float(base) ** (-i / rot_dim)
+    if scaling is None:
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        return (base * factor ** (rot_dim / (rot_dim - 2.0))) ** (-i / rot_dim), 1.0
+    if scaling != "yarn":
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+
+    def pair(turns):  # pair index that makes `turns` turns over original_length
+        return rot_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    lo, hi = max(math.floor(pair(fast_turns)), 0), min(math.ceil(pair(slow_turns)), rot_dim - 1)
+    ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+    return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
+
+
+def rope_phases(freqs: torch.Tensor) -> torch.Tensor:
+    """The table the rotary calls take (int64 [rot_dim / 2], on freqs' device)
+    from frequencies in radians per position: each as turns per position,
+    its fraction in units of 2^-64.  Pass fp64; fp32 values are taken as
+    they are."""
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be 1-D")
+    turns = freqs.detach().to(torch.float64) / (2 * math.pi)
+    turns = turns - torch.floor(turns)
+    hi = torch.floor(turns * 2.0 ** 32)
+    lo = torch.floor((turns * 2.0 ** 32 - hi) * 2.0 ** 32)
+    return (hi.to(torch.int64) << 32) | lo.to(torch.int64)
+
+
+def ra_qk_norm_rope(q, k, phases, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                    interleaved: bool = False, mscale: float = 1.0, positions=None, P: int = 1,
+                    layout="contiguous", q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm (where a weight is given) and rotary positions of
+    q [T, heads, d] and k [T, kv_heads, d]; returns dense (q_out, k_out) of
+    their dtype.  Rows sit at `positions` (int32 [T]), or where `layout` puts
+    the rows of a ring tensor of P blocks.  phases: see rope_phases; None
+    leaves the columns unturned."""
+    T, heads, kv_heads, d = _qk_shapes(q, k)
+    dt = _qkv_dtype(q)
+    if q_out is None:
+        q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must match q and k in shape")
+    _same_device(q, k=k, phases=phases, q_weight=q_weight, k_weight=k_weight,
+                 positions=positions, q_out=q_out, k_out=k_out)
+    qp, qs = _rows(q, "q", heads, d)
+    kp, ks = _rows(k, "k", kv_heads, d)
+    ph, rot = _phase_table(phases)
+    qw, kw, wt = _weight(q_weight, k_weight, d)
+    pos = _vector(positions, "positions", T, torch.int32) if positions is not None else 0
+    with torch.cuda.device(q.device):
+        _check(lib().ra_qk_norm_rope(
+            qp, kp, _dev(q_out, "q_out", q.dtype), _dev(k_out, "k_out", q.dtype), T, d, heads,
+            kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)), ph,
+            float(mscale), qw, kw, wt, float(eps), dt, _stream(stream)))
+    return q_out, k_out
+
+
+def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_weight=None,
+                             eps: float = 1e-6, interleaved: bool = False, mscale: float = 1.0,
+                             positions=None, P: int = 1, layout="contiguous", dq=None, dk=None,
+                             dq_weight=None, dk_weight=None, stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ra_qk_norm_rope's inputs
+    from those of its outputs (fp32, dense, as ra_ring_backward returns
+    them).  dq and dk have q's dtype and may be views of a packed gradient;
+    the weights' are fp32 [d], None without that weight."""
+    T, heads, kv_heads, d = _qk_shapes(q, k)
+    dt = _qkv_dtype(q)
+    if tuple(dq_out.shape) != (T, heads, d) or tuple(dk_out.shape) != (T, kv_heads, d):
+        raise ValueError("dq_out and dk_out must match q and k in shape")
+    if dq is None:
+        dq = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
+    if dq.shape != q.shape or dk.shape != k.shape:
+        raise ValueError("dq and dk must match q and k in shape")
+    qw, kw, wt = _weight(q_weight, k_weight, d)
+    for w, g, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and g is not None:
+            raise ValueError(f"{name} without its weight")
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    _same_device(q, k=k, phases=phases, q_weight=q_weight, k_weight=k_weight,
+                 positions=positions, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk,
+                 dq_weight=dq_weight, dk_weight=dk_weight)
+    qp, qs = _rows(q, "q", heads, d)
+    kp, ks = _rows(k, "k", kv_heads, d)
+    dqp, dqs = _rows(dq, "dq", heads, d, q.dtype)
+    dkp, dks = _rows(dk, "dk", kv_heads, d, q.dtype)
+    ph, rot = _phase_table(phases)
+    pos = _vector(positions, "positions", T, torch.int32) if positions is not None else 0
+    dqw = _vector(dq_weight, "dq_weight", d, torch.float32) if dq_weight is not None else 0
+    dkw = _vector(dk_weight, "dk_weight", d, torch.float32) if dk_weight is not None else 0
+    with torch.cuda.device(q.device):
+        _check(lib().ra_qk_norm_rope_backward(
+            qp, kp, _dev(dq_out, "dq_out", torch.float32), _dev(dk_out, "dk_out", torch.float32),
+            dqp, dkp, dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout),
+            int(P), rot, int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt,
+            _stream(stream)))
+    return dq, dk, dq_weight, dk_weight
+
+
+def _table(block_table, n_req):
+    if block_table.dim() != 2 or block_table.shape[0] != n_req:
+        raise ValueError(f"block_table must be [n_req={n_req}, max_pages], "
+                         f"got {tuple(block_table.shape)}")
+    return _dev(block_table, "block_table", torch.int32), block_table.shape[1]
+
+
+def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *, page_size: int,
+                    tokens: int, lengths_out=None, free_count_out=None, slots=None,
+                    positions=None, cu_tokens=None, status=None, stream=None):
+    """Hand out pages for a step's new tokens (all on the device, int32 but
+    for slots): block_table's rows are extended in place, and the call
+    returns (slots int64 [tokens], positions [tokens], cu_tokens [n_req + 1],
+    lengths_out [n_req], free_count_out [1], status [3]).  lengths_out and
+    free_count_out may be lengths and free_count themselves.  A nonzero
+    status (pages missing, rows too short, tokens beyond `tokens`) means
+    that the step changed nothing."""
+    n = lengths.numel()
+    dev = lengths.device
+
+    def make(t, m, dtype=torch.int32):
+        return torch.empty(m, dtype=dtype, device=dev) if t is None else t
+
+    lengths_out, free_count_out = make(lengths_out, n), make(free_count_out, 1)
+    slots, positions = make(slots, int(tokens), torch.int64), make(positions, int(tokens))
+    cu_tokens, status = make(cu_tokens, n + 1), make(status, 3)
+    _same_device(lengths, new_tokens=new_tokens, block_table=block_table, free_pages=free_pages,
+                 free_count=free_count, lengths_out=lengths_out, free_count_out=free_count_out,
+                 slots=slots, positions=positions, cu_tokens=cu_tokens, status=status)
+    i32 = torch.int32
+    table, width = _table(block_table, n)
+    with torch.cuda.device(dev):
+        _check(lib().ra_paged_extend(
+            _vector(lengths, "lengths", n, i32), _vector(new_tokens, "new_tokens", n, i32), n,
+            table, width, _vector(free_pages, "free_pages", free_pages.numel(), i32),
+            free_pages.numel(), _vector(free_count, "free_count", 1, i32), int(page_size),
+            int(tokens), _vector(lengths_out, "lengths_out", n, i32),
+            _vector(free_count_out, "free_count_out", 1, i32),
+            _vector(slots, "slots", int(tokens), torch.int64),
+            _vector(positions, "positions", int(tokens), i32),
+            _vector(cu_tokens, "cu_tokens", n + 1, i32), _vector(status, "status", 3, i32),
+            _stream(stream)))
+    return slots, positions, cu_tokens, lengths_out, free_count_out, status
+
+
+def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, page_size: int,
+                     lengths_out=None, free_count_out=None, stream=None):
+    """Push the pages of the requests with finished != 0 back on the stack
+    free_pages (in place) and set their lengths to 0; returns (lengths_out,
+    free_count_out), which may be lengths and free_count themselves."""
+    n = lengths.numel()
+    i32 = torch.int32
+    if lengths_out is None:
+        lengths_out = torch.empty(n, dtype=i32, device=lengths.device)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, dtype=i32, device=lengths.device)
+    _same_device(lengths, finished=finished, block_table=block_table, free_pages=free_pages,
+                 free_count=free_count, lengths_out=lengths_out, free_count_out=free_count_out)
+    table, width = _table(block_table, n)
+    with torch.cuda.device(lengths.device):
+        _check(lib().ra_paged_release(
+            _vector(lengths, "lengths", n, i32), _vector(finished, "finished", n, i32), n, table,
+            width, _vector(free_pages, "free_pages", free_pages.numel(), i32),
+            free_pages.numel(), _vector(free_count, "free_count", 1, i32), int(page_size),
+            _vector(lengths_out, "lengths_out", n, i32),
+            _vector(free_count_out, "free_count_out", 1, i32), _stream(stream)))
+    return lengths_out, free_count_out
+
+
+def _cache(t, name, kv_heads, d):
+    """Pointer, page count, page size and page stride of a cache tensor
+    [n_pages, page_size, kv_heads, d] (bf16, dense inside a page)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 4 or t.shape[2] != kv_heads or t.shape[3] != d:
+        raise ValueError(f"{name} must be [n_pages, page_size, {kv_heads}, {d}], "
+                         f"got {tuple(t.shape)}")
+    if t.shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name}: a page must be dense (strides {t.stride()})")
+    page = t.shape[1] * kv_heads * d
+    return t.data_ptr(), t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else page
+
+
+def _caches(k_cache, v_cache, kv_heads, d):
+    kp, n, ps, ks = _cache(k_cache, "k_cache", kv_heads, d)
+    vp, vn, vps, vs = _cache(v_cache, "v_cache", kv_heads, d)
+    if (vn, vps) != (n, ps):
+        raise ValueError("k_cache and v_cache must match in pages and page size")
+    return kp, vp, n, ps, ks, vs
+
+
+def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                    mscale: float = 1.0, q_out=None, stream=None):
+    """ra_qk_norm_rope on a step's rows (bf16) with k and v written to their
+    pages: row t goes to slots[t] (int64; outside the pages: padding, nothing
+    is written) at positions[t] (int32).  Returns q_out, dense like q."""
+    T, heads, kv_heads, d = _qk_shapes(q, k)
+    dt = _qkv_dtype(q)
+    if v.shape != k.shape or v.dtype != q.dtype:
+        raise ValueError("v must match k in shape and dtype")
+    if q_out is None:
+        q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must match q in shape")
+    _same_device(q, k=k, v=v, phases=phases, k_cache=k_cache, v_cache=v_cache, slots=slots,
+                 positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+    qp, qs = _rows(q, "q", heads, d)
+    kp, ks = _rows(k, "k", kv_heads, d)
+    vp, vs = _rows(v, "v", kv_heads, d)
+    kc, vc, n_pages, ps, kcs, vcs = _caches(k_cache, v_cache, kv_heads, d)
+    ph, rot = _phase_table(phases)
+    qw, kw, wt = _weight(q_weight, k_weight, d)
+    with torch.cuda.device(q.device):
+        _check(lib().ra_paged_append(
+            qp, kp, vp, _dev(q_out, "q_out", q.dtype), kc, vc, T, d, heads, kv_heads, qs, ks, vs,
+            n_pages, ps, kcs, vcs, _vector(slots, "slots", T, torch.int64),
+            _vector(positions, "positions", T, torch.int32), rot, int(bool(interleaved)), ph,
+            float(mscale), qw, kw, wt, float(eps), dt, _stream(stream)))
+    return q_out
+
+
+def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, window: int = 0,
+                    out=None, lse=None, stream=None):
+    """Attention of each request's newest tokens q [T, heads, d] (bf16) over
+    its pages.  T / n_req rows per request, or rows [cu_q[i], cu_q[i + 1]) of
+    request i (int32 [n_req + 1]); lengths (int32 [n_req]) include them.
+    Returns (out [T, heads, d], lse [T, heads]), fp32; pass a bf16 `out` for
+    that type."""
+    n = lengths.numel()
+    if q.dim() != 3:
+        raise ValueError("q: [T, heads, d]")
+    T, heads, d = q.shape
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: [n_pages, page_size, kv_heads, d]")
+    kv_heads = k_cache.shape[2]
+    if cu_q is None and (T % n if n else T):
+        raise ValueError(f"T={T} rows are not a multiple of {n} requests (and cu_q is None)")
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
+    _state_shapes(lse, lse, out, T, heads, d)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths,
+                 cu_q=cu_q, out=out, lse=lse)
+    kc, vc, n_pages, ps, ks, vs = _caches(k_cache, v_cache, kv_heads, d)
+    table, width = _table(block_table, n)
+    cu = _vector(cu_q, "cu_q", n + 1, torch.int32) if cu_q is not None else 0
+    with torch.cuda.device(q.device):
+        _check(lib().ra_paged_decode(
+            _dev(q, "q", torch.bfloat16), kc, vc, _dev(out, "out"),
+            _dev(lse, "lse", torch.float32), T, n, 0 if cu_q is not None or not n else T // n, cu,
+            table, width, _vector(lengths, "lengths", n, torch.int32), n_pages, ps, ks, vs,
+            int(window), d, heads, kv_heads, RA_BF16,
+            RA_BF16 if out.dtype == torch.bfloat16 else RA_F32, _stream(stream)))
     return out, lse
 
 

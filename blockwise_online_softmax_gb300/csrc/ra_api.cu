@@ -14,12 +14,15 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include "api_util.h"
 #include "ra.h"
 #include "ra_internal.h"
+#include "serve_internal.h"
 
-namespace {
+namespace ra {
+namespace api {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -37,9 +40,12 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Default wait bound for the kernels' mbarrier waits: 2^31 SM cycles,
-// about one second at the maximum SM clock.
-constexpr long long kWaitLimit = 1LL << 31;
+}  // namespace api
+}  // namespace ra
+
+using namespace ra::api;
+
+namespace {
 
 // ----------------------------------------------------------------- tracing
 struct TraceRec {
@@ -63,35 +69,38 @@ cudaEvent_t take_event() {
   return e;
 }
 
-// Brackets one kernel launch with an event pair on its stream while
-// tracing is on.
-struct TraceScope {
-  int kind;
-  cudaStream_t st;
-  cudaEvent_t a = nullptr, b = nullptr;
-  bool on = false;
-  TraceScope(int k, cudaStream_t s) : kind(k), st(s) {
-    std::lock_guard<std::mutex> g(g_trace_mu);
-    if (!g_trace_on) return;
-    a = take_event();
-    b = take_event();
-    if (a && b && cudaEventRecord(a, st) == cudaSuccess) on = true;
+}  // namespace
+
+namespace ra {
+namespace api {
+
+TraceScope::TraceScope(int k, cudaStream_t s) : kind(k), st(s) {
+  std::lock_guard<std::mutex> g(g_trace_mu);
+  if (!g_trace_on) return;
+  a = take_event();
+  b = take_event();
+  if (a && b && cudaEventRecord(a, st) == cudaSuccess) on = true;
+}
+
+void TraceScope::done(bool launched) {
+  std::lock_guard<std::mutex> g(g_trace_mu);
+  if (!on) {
+    if (a) g_ev_pool.push_back(a);
+    if (b) g_ev_pool.push_back(b);
+    return;
   }
-  void done(bool launched) {
-    std::lock_guard<std::mutex> g(g_trace_mu);
-    if (!on) {
-      if (a) g_ev_pool.push_back(a);
-      if (b) g_ev_pool.push_back(b);
-      return;
-    }
-    if (launched && cudaEventRecord(b, st) == cudaSuccess) {
-      g_trace.push_back({kind, a, b});
-    } else {
-      g_ev_pool.push_back(a);
-      g_ev_pool.push_back(b);
-    }
+  if (launched && cudaEventRecord(b, st) == cudaSuccess) {
+    g_trace.push_back({kind, a, b});
+  } else {
+    g_ev_pool.push_back(a);
+    g_ev_pool.push_back(b);
   }
-};
+}
+
+}  // namespace api
+}  // namespace ra
+
+namespace {
 
 // ----------------------------------------------------------------- scratch
 // Scratch and staging buffers come from a memory pool the library owns on
@@ -128,8 +137,11 @@ cudaError_t scratch_pool(cudaMemPool_t* out) {
   return cudaSuccess;
 }
 
-// Stream-ordered allocation from the current device's pool; the buffer is
-// returned with cudaFreeAsync like any other.
+}  // namespace
+
+namespace ra {
+namespace api {
+
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st) {
   cudaMemPool_t pool = nullptr;
   cudaError_t e = scratch_pool(&pool);
@@ -139,7 +151,7 @@ cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st) {
 
 // ----------------------------------------------------------------- TMA maps
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
+static std::once_flag g_encode_once;
 
 int get_encoder() {
   std::call_once(g_encode_once, [] {
@@ -153,6 +165,11 @@ int get_encoder() {
   if (!g_encode) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   return RA_OK;
 }
+
+}  // namespace api
+}  // namespace ra
+
+namespace {
 
 // 3-D map over a token-major bf16 tensor [rows, heads, d]: dims (d, heads,
 // rows).  The box is 64 elements (128 B, one swizzle span) x 1 head x
@@ -212,7 +229,12 @@ int encode_q_group_map(CUtensorMap* map, const void* base, long long n_q, int he
   return RA_OK;
 }
 
+}  // namespace
+
 // ----------------------------------------------------------------- checks
+namespace ra {
+namespace api {
+
 int check_common(int d, int heads, int dtype) {
   if (dtype != RA_F32 && dtype != RA_BF16) return fail(RA_ERR_INVALID, "dtype %d is not RA_F32 or RA_BF16", dtype);
   if (d != 64 && d != 128) return fail(RA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
@@ -235,6 +257,11 @@ int check_ptrs(std::initializer_list<const void*> ps) {
   }
   return RA_OK;
 }
+
+}  // namespace api
+}  // namespace ra
+
+namespace {
 
 // Run one block-update launch (mode 0 or 1), picking the kernel by dtype.
 int run_update(ra::FwdArgs& a, int d, int dtype, cudaStream_t st) {
@@ -1206,14 +1233,16 @@ int ra_decode_forward(const void* q, const void* k, const void* v, float* out, f
 int ra_device_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  int a = 0, b = 0, c = 0, w = 0;
+  int a = 0, b = 0, c = 0, w = 0, p = 0;
   if ((e = ra::take_umma_status(&a)) != cudaSuccess) return cuda_fail(e, "reading the tcgen05 kernel status");
   if ((e = ra::take_simt_status(&b)) != cudaSuccess) return cuda_fail(e, "reading the fp32 kernel status");
   if ((e = ra::take_decode_status(&c)) != cudaSuccess) return cuda_fail(e, "reading the decode kernel status");
   if ((e = ra::take_bwd_status(&w)) != cudaSuccess) return cuda_fail(e, "reading the backward kernel status");
-  if (a != 0 || b != 0 || c != 0 || w != 0)
-    return fail(RA_ERR_TIMEOUT, "a kernel gave up a bounded wait (codes 0x%x, 0x%x, 0x%x, 0x%x)",
-                a, b, c, w);
+  if ((e = ra::take_paged_status(&p)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
+  if (a != 0 || b != 0 || c != 0 || w != 0 || p != 0)
+    return fail(RA_ERR_TIMEOUT,
+                "a kernel gave up a bounded wait (codes 0x%x, 0x%x, 0x%x, 0x%x, 0x%x)", a, b, c, w,
+                p);
   return RA_OK;
 }
 

@@ -1,0 +1,120 @@
+// Internal interface of the serving and training operators around the
+// attention kernels (page bookkeeping, q/k norm with rotary positions,
+// paged decode) between serve_api.cu and the kernel units.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ra_internal.h"
+
+namespace ra {
+
+// ------------------------------------------------------------------ pages
+struct ExtendArgs {
+  const int* lengths;     // [n_req] tokens cached before
+  const int* new_tokens;  // [n_req]
+  int* block_table;       // [n_req, max_pages]
+  const int* free_pages;  // [free_capacity], a stack: entries [0, *free_count)
+  const int* free_count;
+  int* lengths_out;
+  int* free_count_out;
+  long long* slots;       // [tokens]
+  int* positions;         // [tokens]
+  int* cu_tokens;         // [n_req + 1]
+  int* status;            // [3]
+  long long tokens;
+  int n_req;
+  int max_pages;
+  int free_capacity;
+  int page_shift;         // log2 of the page size
+};
+cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st);
+
+struct ReleaseArgs {
+  const int* lengths;
+  const int* finished;
+  const int* block_table;
+  int* free_pages;
+  const int* free_count;
+  int* lengths_out;
+  int* free_count_out;
+  int n_req;
+  int max_pages;
+  int free_capacity;
+  int page_shift;
+};
+cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------------ q/k norm and rotary positions
+struct RopeArgs {
+  const void* q;  // [T, heads, d], tokens q_str elements apart
+  const void* k;  // [T, kv_heads, d]
+  const void* v;  // append: [T, kv_heads, d]
+  long long q_str, k_str, v_str;
+  void* qo;       // forward: rotated q; backward: dq
+  void* ko;       // forward: rotated k; backward: dk
+  long long qo_str, ko_str;
+  const float* dqo;  // backward: gradients of the outputs, dense fp32
+  const float* dko;
+  void* kc;          // append: pages [n_pages, page_size, kv_heads, d] bf16
+  void* vc;
+  long long kc_page, vc_page;  // elements from page to page
+  long long n_slots;           // n_pages * page_size
+  int page_shift;
+  const long long* slots;
+  const int* positions;  // null: by layout
+  int layout;
+  int P;
+  long long c;           // T / P
+  long long T;
+  int heads;
+  int kv_heads;
+  int rot;               // rotated columns (a multiple of 16, 0: none)
+  int interleaved;
+  const unsigned long long* phases;  // [rot / 2] turns per position, units of 2^-64
+  const void* qw;        // [d] weights of the norm; null: no norm
+  const void* kw;
+  int w_bf16;
+  float eps;
+  float mscale;
+  float* dw;             // backward: partial weight gradients [rope_grad_ctas][2][d]
+  float* dqw;            // [d] or null
+  float* dkw;
+  int parts;             // warps that share one token's rows (set by the launcher)
+};
+cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
+cudaError_t launch_rope_append(const RopeArgs& a, int d, cudaStream_t st);
+// CTAs of the backward launch, i.e. partial weight gradients it writes.
+int rope_grad_ctas(const RopeArgs& a);
+cudaError_t launch_rope_backward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
+// dqw, dkw = the sums of the n partial weight gradients.
+cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st);
+
+// ------------------------------------------------------------------ paged decode
+struct PagedArgs {
+  const void* q;   // [T, heads, d] bf16
+  const void* kc;  // [n_pages, page_size, kv_heads, d] bf16
+  const void* vc;
+  long long kc_page, vc_page;
+  const int* block_table;  // [n_req, max_pages]
+  const int* lengths;      // [n_req], the new tokens included
+  const int* cu_q;         // [n_req + 1], or null: n_q rows per request
+  void* out;               // [T, heads, d] fp32, or bf16 (out_bf16)
+  float* lse;              // [T, heads]
+  long long T;
+  long long n_q;
+  long long window;        // 0: none
+  int out_bf16;
+  int n_req;
+  int max_pages;
+  int n_pages;
+  int page_shift;
+  int heads;
+  int kv_heads;
+  float scale_log2;        // log2(e) / sqrt(d)
+  long long wait_limit;
+};
+cudaError_t launch_paged_decode(const PagedArgs& a, int d, cudaStream_t st);
+cudaError_t take_paged_status(int* code);
+
+}  // namespace ra

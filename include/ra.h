@@ -119,7 +119,15 @@ typedef enum {
   RA_KERNEL_BWD_DKDV = 9,       /* backward: dK, dV (tcgen05, K/V-stationary) */
   RA_KERNEL_RING_FUSED_BF16 = 10, /* the whole bf16 ring forward in one launch (tcgen05) */
   RA_KERNEL_RING_FUSED_F32 = 11,  /* the whole fp32 ring forward in one launch (FFMA) */
-  RA_KERNEL_KINDS = 12
+  RA_KERNEL_PAGED_EXTEND = 12,    /* block tables, slots and positions of a step */
+  RA_KERNEL_PAGED_RELEASE = 13,   /* pages of finished requests back to the free list */
+  RA_KERNEL_QK_NORM_ROPE = 14,    /* per-head norm of q and k, rotary positions */
+  RA_KERNEL_QK_NORM_ROPE_BWD = 15,
+  RA_KERNEL_QK_NORM_WEIGHT_GRAD = 16, /* sums the partial weight gradients of kind 15 */
+  RA_KERNEL_PAGED_APPEND = 17,    /* kind 14 with k and v written to their pages */
+  RA_KERNEL_PAGED_DECODE = 18,    /* attention over the pages */
+  RA_KERNEL_PAGED_COMBINE = 19,   /* joins the parts of a request that several CTAs took */
+  RA_KERNEL_KINDS = 20
 } ra_kernel_kind;
 
 /*
@@ -410,6 +418,133 @@ int ra_decode_forward(const void* q, const void* k, const void* v, float* out, f
                       long long n_q, long long n_kv, int P, long long q_off, int causal,
                       long long window, int d, int heads, int kv_heads, int dtype,
                       void* stream);
+
+/*
+ * Before and around the attention: rotary positions with a per-head norm,
+ * and a key/value history of many requests kept in pages.  The pages of
+ * the method have no counterpart but "位置编码必须使用全局位置" ([SP]): the
+ * rotation takes the *global* position of each row, which under a ring
+ * layout is not its row index.
+ *
+ * Rotary positions.  Column pair i < rot_dim / 2 of a head is columns
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with `interleaved`; at position p it
+ * turns by the angle 2 pi frac(p phases[i] / 2^64) and is multiplied by
+ * `mscale`.  Columns from rot_dim on are not turned.  rot_dim is 0 or a
+ * multiple of 16, at most d; `phases` is a device array of rot_dim / 2
+ * 64-bit words: each frequency as turns per position, its fraction in
+ * units of 2^-64, so the angle of any 32-bit position is exact to that
+ * unit however far the position is (scaled frequencies are the caller's).
+ * Norm.  With a weight, the head is first divided by sqrt(mean(x^2) + eps)
+ * over its d columns and multiplied by the weight ([d], fp32 or bf16 as
+ * w_dtype says).  q_weight and k_weight may each be NULL (that tensor is
+ * not normalised).  All of it is computed in fp32 and rounded once.
+ *
+ * ra_qk_norm_rope -- q_out, k_out (dense [T, heads, d], [T, kv_heads, d]) =
+ * norm and rotation of q, k (dtype bf16 or fp32), ready for the ring calls.
+ *   q, k: heads dense, tokens q_stride / k_stride elements apart (at least
+ *     a token's elements, a multiple of 16 bytes), so views of one packed
+ *     projection work.  q_out may be q, and k_out k, where those are dense.
+ *   positions: device int32 [T], or NULL: the position that `layout` gives
+ *     each row of a ring tensor of P blocks (T % P == 0, zigzag T / P even).
+ *
+ * ra_qk_norm_rope_backward -- the gradients of that call: dq, dk (dtype
+ * like q; heads dense, tokens dq_stride / dk_stride apart) and the weights'
+ * (fp32 [d], given exactly when the weight is) from those of its outputs,
+ * dq_out and dk_out, dense fp32 as ra_ring_backward writes them.  q and k
+ * are the forward's inputs.  dq may be q, and dk k.  The weight gradients
+ * are summed in a fixed order (scratch: partial sums, from the pool).
+ */
+int ra_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, long long T, int d,
+                    int heads, int kv_heads, long long q_stride, long long k_stride,
+                    const int* positions, int layout, int P, int rot_dim, int interleaved,
+                    const void* phases, float mscale, const void* q_weight, const void* k_weight,
+                    int w_dtype, float eps, int dtype, void* stream);
+int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
+                             const float* dk_out, void* dq, void* dk, float* dq_weight,
+                             float* dk_weight, long long T, int d, int heads, int kv_heads,
+                             long long q_stride, long long k_stride, long long dq_stride,
+                             long long dk_stride, const int* positions, int layout, int P,
+                             int rot_dim, int interleaved, const void* phases, float mscale,
+                             const void* q_weight, const void* k_weight, int w_dtype, float eps,
+                             int dtype, void* stream);
+
+/*
+ * Pages.  A history of many requests lives in pages of page_size tokens
+ * (8, 16, 32, 64, 128 or 256): k_cache, v_cache [n_pages, page_size,
+ * kv_heads, d] bf16, dense inside a page, pages k_page_stride /
+ * v_page_stride elements apart (a multiple of 8), so one tensor may hold
+ * both.  Token p of request i is row p % page_size of page
+ * block_table[i][p / page_size]; block_table is [n_req, max_pages] int32.
+ * The slot of a token is page * page_size + row.  Pages not in use form a
+ * stack: entries [0, *free_count) of free_pages.  All bookkeeping arrays
+ * are device memory, so a step needs no host read and can be captured.
+ * n_req * max_pages and max_pages * page_size must be < 2^31.
+ *
+ * ra_paged_extend -- hand out pages for the new tokens of a step and say
+ * where each goes.  Request i grows from lengths[i] by new_tokens[i] >= 0
+ * (negative values count as 0).  Its new pages are popped from the stack,
+ * requests in order, and written to its table row; entries that were there
+ * stay.
+ *   lengths_out [n_req], free_count_out [1]: the new values; each may be
+ *     the input array itself.
+ *   cu_tokens [n_req + 1]: prefix sums of new_tokens; token j of request i
+ *     is row cu_tokens[i] + j of the step's tensors of `tokens` rows.
+ *   slots [tokens] int64, positions [tokens] int32: slot and position of
+ *     each row; rows behind the last token get slot -1 and position 0.
+ *   status [3]: pages missing, requests whose row of max_pages is too
+ *     short, tokens beyond `tokens` (saturating).  Unless all are 0 the step changes
+ *     nothing: table and stack stay, lengths_out and free_count_out get the
+ *     old values, every slot is -1 and cu_tokens is all 0.
+ *
+ * ra_paged_release -- push the pages of every request with finished[i] != 0
+ * back (requests in order, pages in order) and set its length to 0.  Table
+ * rows are left as they are.  What does not fit in free_capacity is dropped.
+ *
+ * ra_paged_append -- ra_qk_norm_rope on a step's rows with k and v written to
+ * their pages: row t's k (normed, turned) and v go to slots[t], its q to
+ * row t of q_out (dense, bf16; may be q where that is dense).  A row whose
+ * slot is outside [0, n_pages * page_size) is padding: nothing is written
+ * for it.  Two rows with the same slot: one of them ends up there.  bf16.
+ *
+ * ra_paged_decode -- attention of each request's newest tokens over its
+ * pages: query row j of the n_i rows of request i sits at position
+ * lengths[i] - n_i + j (the new tokens are in the pages already, lengths
+ * includes them) and sees the keys up to itself, the last `window` of them
+ * when window > 0.
+ *   q: [T, heads, d] bf16.  cu_q NULL: n_q rows per request, T = n_req *
+ *     n_q.  Else a device array [n_req + 1]: the rows of request i are
+ *     [cu_q[i], cu_q[i + 1]), as ra_paged_extend's cu_tokens (nondecreasing,
+ *     cu_q[0] = 0); n_q is ignored, and rows behind cu_q[n_req] are left as
+ *     they were.
+ *   out: [T, heads, d], fp32 or bf16 as out_dtype says; lse: [T, heads] fp32.
+ *     A row that sees no key gets out = 0 and lse = -inf.
+ *   A request's table row is read up to ceil(lengths[i] / page_size)
+ *   entries; lengths beyond max_pages * page_size count as that.  A page
+ *   outside [0, n_pages) is not read, and that request's result is
+ *   undefined.  What lies behind a request's last token in its last page
+ *   does not matter, NaN included.
+ *   heads / kv_heads <= 128, T * heads < 2^31.
+ */
+int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* block_table,
+                    int max_pages, const int* free_pages, int free_capacity,
+                    const int* free_count, int page_size, long long tokens, int* lengths_out,
+                    int* free_count_out, long long* slots, int* positions, int* cu_tokens,
+                    int* status, void* stream);
+int ra_paged_release(const int* lengths, const int* finished, int n_req, const int* block_table,
+                     int max_pages, int* free_pages, int free_capacity, const int* free_count,
+                     int page_size, int* lengths_out, int* free_count_out, void* stream);
+int ra_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                    void* v_cache, long long T, int d, int heads, int kv_heads,
+                    long long q_stride, long long k_stride, long long v_stride, int n_pages,
+                    int page_size, long long k_page_stride, long long v_page_stride,
+                    const long long* slots, const int* positions, int rot_dim, int interleaved,
+                    const void* phases, float mscale, const void* q_weight, const void* k_weight,
+                    int w_dtype, float eps, int dtype, void* stream);
+int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                    long long T, int n_req, int n_q, const int* cu_q, const int* block_table,
+                    int max_pages, const int* lengths, int n_pages, int page_size,
+                    long long k_page_stride, long long v_page_stride, long long window, int d,
+                    int heads, int kv_heads, int dtype, int out_dtype, void* stream);
 
 /*
  * ra_device_status -- synchronize `stream`, then read and clear the
