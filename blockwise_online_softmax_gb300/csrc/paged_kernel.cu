@@ -1,5 +1,27 @@
-// Page bookkeeping on the GPU, and decode attention over paged keys and
-// values.
+// Decode attention over paged keys and values: the newest tokens of many
+// requests, each against its own pages (include/ra.h, ra_paged_decode).
+//
+// For a row (one head of one new token) with allowed keys t:
+//   s_t = q.k_t / sqrt(d),  m = max s,  l = sum exp(s_t - m),
+//   out = sum exp(s_t - m) v_t / l,  lse = m + ln l.
+//
+// The work is the read of the pages: each key meets only the rows of its KV
+// head (g heads x the request's new tokens).  Its units are 128-key tiles,
+// in the order (request, row tile, KV head, key tile), and every CTA of a
+// grid of one per SM takes an equal run of them, whatever the lengths are:
+// the lengths stay on the device.  A CTA finds its run by a prefix sum over
+// the requests.  A (request, row tile, KV head) that falls into one CTA is
+// finished there; one cut by a border between CTAs leaves a partial state
+// (m, l, O~) on each side, and a second launch joins them in CTA order.
+//
+// One warp feeds a ring of stages with TMA (a page, or half a page of 256,
+// is a box of one KV head; lane p looks up and requests page p of the
+// tile).  Eight warps take 16 keys of the tile each and keep their own
+// running (m, l, O~), so nothing in the loop waits for another warp.  The
+// products are mma.sync m16n8k16 with the keys, then the columns of V, as
+// the 16-wide side and 8 query rows as the other: a tcgen05 tile would be
+// 128 rows for the 4 or 8 there are, and its S -> P round trip through TMEM
+// is the longer chain.
 #include <cmath>
 #include <cstdint>
 
@@ -15,262 +37,668 @@ __device__ int g_paged_status = 0;
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int BT = 128;          // keys per tile
+constexpr int kCons = 8;         // consumer warps
+constexpr int kThreads = 32 * (kCons + 1);
+constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
 
-// ------------------------------------------------------------------ bookkeeping
-constexpr int kBook = 1024;  // threads of the bookkeeping CTA, requests per chunk
+template <int D>
+struct Cfg {
+  static constexpr int NCH = D / 64;
+  static constexpr uint32_t TILE = BT * D * 2;
+  static constexpr int NST = D == 128 ? 3 : 6;  // stages of one K and one V tile
+  static constexpr uint32_t OFF_BUF = NST * 2 * TILE;             // [kCons][8][D] fp32
+  static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 8 * D * 4;  // [2][kCons][16] fp32
+  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kCons * 16 * 4;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 3 * NST * 8;
+  static constexpr uint32_t SMEM = OFF_MISC + 32 + 1024;
+  static_assert(SMEM + 512 <= 232448, "shared memory budget");
+};
 
-// Exclusive prefix sum of one value per thread of the CTA; *total gets the
-// sum.  Every thread calls it; it synchronizes before it returns.
-__device__ __forceinline__ int block_scan(int v, int* total) {
-  __shared__ int s_warp[33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+// What a CTA that starts a cut item leaves for the joining launch.
+struct Cut {
+  int last;   // last CTA of the item; -1: none
+  int row0;   // first row of the q tensor of the request
+  int rr0;    // first row of the tile (row rr: token rr / g, head kh * g + rr % g)
+  int rows;
+  int kh;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                            int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------ the work list
+struct Request {
+  int row0;       // first row of q
+  int n;          // new tokens
+  long long len;  // keys, the new tokens' included
+};
+
+__device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
+  Request q;
+  if (a.cu_q) {
+    // A malformed cu_q must not reach outside q and out.
+    const long long x = a.cu_q[r], y = a.cu_q[r + 1];
+    const long long lo = x < 0 ? 0 : (x > a.T ? a.T : x), hi = y < lo ? lo : (y > a.T ? a.T : y);
+    q.row0 = static_cast<int>(lo);
+    q.n = static_cast<int>(hi - lo);
+  } else {
+    q.row0 = static_cast<int>(r * a.n_q);
+    q.n = static_cast<int>(a.n_q);
+  }
+  const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
+  const long long len = a.lengths[r];
+  q.len = len < 0 ? 0 : (len > most ? most : len);
+  return q;
+}
+
+// Keys [lo, hi) that token j of the request sees.
+__device__ __forceinline__ long long key_end(const Request& q, int j) {
+  const long long hi = q.len - q.n + j + 1;
+  return hi < 0 ? 0 : hi;
+}
+__device__ __forceinline__ long long key_begin(const PagedArgs& a, long long hi) {
+  return a.window > 0 && hi > a.window ? hi - a.window : 0;
+}
+
+// Row tile rt of a request: rows [rr0, rr1), keys [lo, hi) over all of them,
+// key tiles [t0, t0 + nt) (one, with no key, when there is none).
+struct RowTile {
+  int rr0, rr1;
+  long long lo, hi;
+  long long t0;
+  int nt;
+};
+
+__device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const Request& q, int g, int RT,
+                                            int rt) {
+  RowTile t;
+  t.rr0 = rt * RT;
+  const long long all = static_cast<long long>(q.n) * g, end = static_cast<long long>(t.rr0) + RT;
+  t.rr1 = static_cast<int>(end < all ? end : all);
+  t.hi = key_end(q, (t.rr1 - 1) / g);
+  t.lo = key_begin(a, key_end(q, t.rr0 / g));
+  t.t0 = t.lo / BT;
+  t.nt = t.hi > t.lo ? static_cast<int>((t.hi + BT - 1) / BT - t.t0) : 1;
+  return t;
+}
+
+__device__ __forceinline__ int row_tiles(const Request& q, int g, int RT) {
+  return static_cast<int>((static_cast<long long>(q.n) * g + RT - 1) / RT);
+}
+
+__device__ __forceinline__ long long request_units(const PagedArgs& a, int r, int g, int RT) {
+  const Request q = load_request(a, r);
+  const int n = row_tiles(q, g, RT);
+  long long u = 0;
+  for (int rt = 0; rt < n; ++rt) u += row_tile(a, q, g, RT, rt).nt;
+  return u * a.kv_heads;
+}
+
+// Where a CTA's run of units starts, and how the walk goes on.
+struct Walk {
+  int r, rt, kh, nrt;
+  Request q;
+  RowTile t;
+  int k;  // key tile inside the item
+
+  __device__ __forceinline__ void enter(const PagedArgs& a, int g, int RT) {
+    q = load_request(a, r);
+    nrt = row_tiles(q, g, RT);
+  }
+  // Start at unit x of request r.
+  __device__ __forceinline__ void start(const PagedArgs& a, int g, int RT, int r_, long long x) {
+    r = r_;
+    enter(a, g, RT);
+    for (rt = 0;; ++rt) {
+      t = row_tile(a, q, g, RT, rt);
+      const long long w = static_cast<long long>(t.nt) * a.kv_heads;
+      if (x < w || rt + 1 >= nrt) break;
+      x -= w;
+    }
+    kh = static_cast<int>(x / t.nt);
+    k = static_cast<int>(x % t.nt);
+  }
+  // To the next item; the caller knows that there is one (the bound on r only
+  // keeps arrays that change under the kernel from leading it outside).
+  __device__ __forceinline__ void next(const PagedArgs& a, int g, int RT) {
+    k = 0;
+    if (++kh < a.kv_heads) return;
+    kh = 0;
+    if (++rt >= nrt) {
+      rt = 0;
+      do {
+        if (r + 1 < a.n_req) ++r;
+        enter(a, g, RT);
+      } while (nrt == 0 && r + 1 < a.n_req);
+    }
+    t = row_tile(a, q, g, RT, rt);
+  }
+};
+
+// Prefix sum over the requests: every thread of the CTA gets the total; the
+// unit `first` = floor(c total / G) of CTA c is located as (request, offset).
+// With fewer units than CTAs only `ctas` of them work, one unit each, so the
+// CTAs of a cut item all hold a part of it.
+struct Run {
+  long long total, first, last;
+  int ctas;
+  int r;
+  long long x;
+};
+
+__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT) {
+  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_x;
+  __shared__ int s_r;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_req + kThreads - 1) / kThreads;
+  const int i0 = tid * per, i1 = i0 + per < a.n_req ? i0 + per : a.n_req;
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += request_units(a, i, g, RT);
+  long long x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, x, o);
+    const long long y = __shfl_up_sync(kAll, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();  // s_warp of an earlier call has been read
-  if (lane == 31) s_warp[warp] = x;
+  if (lane == 31) s_sum[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = s_warp[lane];
+  long long before = x - mine, total = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, w, o);
-      if (lane >= o) w += y;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  Run run;
+  run.total = total;
+  run.ctas = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+  run.first = run.last = total;
+  if (static_cast<int>(blockIdx.x) < run.ctas) {
+    run.first = static_cast<long long>(blockIdx.x) * total / run.ctas;
+    run.last = static_cast<long long>(blockIdx.x + 1) * total / run.ctas;
+  }
+  if (run.first < run.last && before <= run.first && run.first < before + mine) {
+    long long at = run.first - before;
+    int i = i0;
+    for (;; ++i) {
+      const long long u = request_units(a, i, g, RT);
+      if (at < u || i + 1 >= i1) break;
+      at -= u;
     }
-    s_warp[lane] = w;
+    s_r = i;
+    s_x = at;
   }
   __syncthreads();
-  *total = s_warp[31];
-  return x - v + (warp ? s_warp[warp - 1] : 0);
+  run.r = s_r;
+  run.x = s_x;
+  return run;
 }
 
-__device__ __forceinline__ long long block_sum(long long v) {
-  __shared__ long long s_sum[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  __syncthreads();
-  if (lane == 0) s_sum[warp] = v;
-  __syncthreads();
-  long long s = s_sum[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  return s;
+// CTA whose run holds unit u.
+__device__ __forceinline__ int cta_of(long long u, const Run& run) {
+  return static_cast<int>(((u + 1) * run.ctas - 1) / run.total);
 }
 
-// The last i in [0, n) with first[i] <= x (first nondecreasing, first[0] <= x).
-__device__ __forceinline__ int find_last(const int* first, int n, int x) {
-  int a = 0, b = n;
-  while (b - a > 1) {
-    const int mid = (a + b) >> 1;
-    if (first[mid] <= x) a = mid; else b = mid;
-  }
-  return a;
-}
-
-__device__ __forceinline__ int at_least_0(int x) { return x < 0 ? 0 : x; }
-
-// One CTA.  Pass 1 sums what the step needs and sets the status; with any
-// of it missing the step changes nothing.  Pass 2 takes the requests in
-// chunks of one per thread: prefix sums of the new pages and tokens, then
-// the chunk's pages, and after them its tokens, are dealt to the threads by
-// search in those sums.
-__global__ void __launch_bounds__(kBook) paged_extend_kernel(const ExtendArgs a) {
-  __shared__ int s_page[kBook + 1], s_cu[kBook + 1], s_len[kBook], s_old[kBook];
-  const int tid = threadIdx.x, sh = a.page_shift;
-  const long long ps1 = (1LL << sh) - 1;
-  int count = *a.free_count;
-  count = count < 0 ? 0 : (count > a.free_capacity ? a.free_capacity : count);
-  long long need = 0, toks = 0, bad = 0;
-  for (int i = tid; i < a.n_req; i += kBook) {
-    const long long len = at_least_0(a.lengths[i]), nw = at_least_0(a.new_tokens[i]);
-    const long long pages = (len + nw + ps1) >> sh;
-    need += pages - ((len + ps1) >> sh);
-    toks += nw;
-    bad += pages > a.max_pages;
-  }
-  need = block_sum(need);
-  toks = block_sum(toks);
-  bad = block_sum(bad);
-  const bool ok = need <= count && bad == 0 && toks <= a.tokens;
+// ------------------------------------------------------------------ the kernel
+// NT: 8-row groups of query rows; a row tile has RT = 8 NT rows.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const PagedArgs a) {
+  using C = Cfg<D>;
+  constexpr int RT = 8 * NT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
+  auto vfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NST + s); };
+  auto empty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NST + s); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.heads / a.kv_heads;
+  Cut* cuts = static_cast<Cut*>(a.cuts);
   if (tid == 0) {
-    const long long lack = need - count, over = toks - a.tokens;
-    a.status[0] = lack > 0 ? static_cast<int>(lack > 0x7fffffff ? 0x7fffffff : lack) : 0;
-    a.status[1] = static_cast<int>(bad);
-    a.status[2] = over > 0 ? static_cast<int>(over > 0x7fffffff ? 0x7fffffff : over) : 0;
-    *a.free_count_out = ok ? count - static_cast<int>(need) : count;
-    a.cu_tokens[0] = 0;
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(vfull(s), 1);
+      mbar_init(empty(s), kCons);
+    }
+    *abort_flag = *reinterpret_cast<volatile int*>(&g_paged_status) != 0 ? 1 : 0;
+    fence_mbar_init();
+    cuts[blockIdx.x].last = -1;
   }
-  int page0 = 0, tok0 = 0;  // pages and tokens of the chunks before
-  for (int i0 = 0; i0 < a.n_req; i0 += kBook) {
-    const int i = i0 + tid;
-    const bool in = i < a.n_req;
-    const int len = in ? at_least_0(a.lengths[i]) : 0;
-    const int nw = in && ok ? at_least_0(a.new_tokens[i]) : 0;
-    const int old = static_cast<int>((len + ps1) >> sh);
-    const int fresh = ok ? static_cast<int>((static_cast<long long>(len) + nw + ps1) >> sh) - old : 0;
-    int pages, tokens;
-    const int p = block_scan(fresh, &pages), t = block_scan(nw, &tokens);
-    s_page[tid] = p;
-    s_cu[tid] = t;
-    s_len[tid] = len;
-    s_old[tid] = old;
-    if (tid == 0) {
-      s_page[kBook] = pages;
-      s_cu[kBook] = tokens;
+  const Run run = find_run(a, g, RT);  // synchronizes
+  if (run.first >= run.last) return;
+  Walk w;
+  w.start(a, g, RT, run.r, run.x);
+  const long long lim = a.wait_limit;
+  long long u = run.first;  // unit of the item's tile w.k
+
+  if (warp == kCons) {
+    // ---------------------------------------------------------------- producer
+    const int sh = a.page_shift;
+    const int rows = sh < 7 ? 1 << sh : BT;  // of a box
+    const int npg = BT / rows;
+    const uint32_t box = static_cast<uint32_t>(rows) * 128u;
+    bool ok = true;
+    int i = 0;  // tiles requested
+    while (ok && u < run.last) {
+      const long long p_end = (w.t.hi + (1LL << sh) - 1) >> sh;
+      const long long p_begin = w.t.lo >> sh;
+      const int* table = a.block_table + static_cast<long long>(w.r) * a.max_pages;
+      for (; w.k < w.t.nt && u < run.last; ++w.k, ++u, ++i) {
+        const long long key0 = (w.t.t0 + w.k) * BT;
+        const long long p = (key0 >> sh) + lane;
+        int page = -1;
+        if (lane < npg && p >= p_begin && p < p_end) page = table[p];
+        const bool have = page >= 0 && page < a.n_pages;
+        const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(kAll, have)));
+        const int s = i % C::NST;
+        if (i >= C::NST) {
+          ok = wait_bar(empty(s), (static_cast<uint32_t>(i / C::NST) & 1u) ^ 1u, abort_flag,
+                        &g_paged_status, 0x81, lim);
+          ok = __all_sync(kAll, ok);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(kfull(s), n * box * C::NCH);
+          mbar_arrive_expect_tx(vfull(s), n * box * C::NCH);
+        }
+        __syncwarp();
+        if (have) {
+          const uint32_t dst = sb + s * 2 * C::TILE + lane * box;
+          const int row = static_cast<int>(key0 & ((1LL << sh) - 1));
+#pragma unroll
+          for (int ch = 0; ch < C::NCH; ++ch)
+            tma_load_4d(dst + ch * CHB, &tmK, kfull(s), ch * 64, w.kh, row, page);
+#pragma unroll
+          for (int ch = 0; ch < C::NCH; ++ch)
+            tma_load_4d(dst + C::TILE + ch * CHB, &tmV, vfull(s), ch * 64, w.kh, row, page);
+        }
+      }
+      if (ok && u < run.last) w.next(a, g, RT);
     }
-    if (in) {
-      a.lengths_out[i] = len + nw;
-      a.cu_tokens[i + 1] = tok0 + t + nw;
+    if (!ok) {  // let the copies in flight land before the CTA leaves
+      volatile int no_abort = 0;
+      for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j) {
+        wait_bar(kfull(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
+        wait_bar(vfull(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
+      }
     }
-    __syncthreads();
-    for (int x = tid; x < pages; x += kBook) {
-      const int r = find_last(s_page, kBook, x);
-      a.block_table[static_cast<long long>(i0 + r) * a.max_pages + s_old[r] + (x - s_page[r])] =
-          a.free_pages[count - 1 - (page0 + x)];
-    }
-    __syncthreads();
-    for (int x = tid; x < tokens; x += kBook) {
-      const int r = find_last(s_cu, kBook, x);
-      const int pos = s_len[r] + (x - s_cu[r]);
-      const long long page = a.block_table[static_cast<long long>(i0 + r) * a.max_pages + (pos >> sh)];
-      a.slots[tok0 + x] = page < 0 ? -1 : (page << sh) + (pos & ps1);
-      a.positions[tok0 + x] = pos;
-    }
-    page0 += pages;
-    tok0 += tokens;
-    __syncthreads();
+    return;
   }
-  for (long long x = tok0 + tid; x < a.tokens; x += kBook) {
-    a.slots[x] = -1;
-    a.positions[x] = 0;
+
+  // ------------------------------------------------------------------ consumers
+  // After a wait that gave up, a warp runs on without waiting (the status
+  // word says that the results are void), so the barriers still match.
+  float* buf = reinterpret_cast<float*>(smem + C::OFF_BUF);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_l = s_m + kCons * 16;
+  const float sl2 = a.scale_log2;
+  bool ok = true;
+  int i = 0;
+  // ldmatrix addresses of this lane inside a 64-column chunk of a tile: K
+  // rows are keys (8 x 8 blocks: keys 0-7 / 8-15 first, then columns), V the
+  // same blocks with columns first, read transposed.
+  const int kr = warp * 16 + (lane & 15), kc0 = lane >> 4;
+  const int vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
+  while (u < run.last) {
+    // The item's query rows: lane holds rows 8 nt + lane / 4 as the B side.
+    uint32_t bq[NT][D / 16][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int rr = w.t.rr0 + 8 * nt + (lane >> 2);
+      const bool in = rr < w.t.rr1;
+      const long long row = static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                                static_cast<const __nv_bfloat16*>(a.q) + row * D) + (lane & 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        bq[nt][kk][0] = in ? src[kk * 8] : 0u;
+        bq[nt][kk][1] = in ? src[kk * 8 + 4] : 0u;
+      }
+    }
+    // Keys [lo, hi) of the lane's rows 8 nt + 2 (lane & 3) + {0, 1}; the keys
+    // that every row of the tile sees are [lo_all, hi_all).
+    int rlo[NT][2], rhi[NT][2];
+    const long long base = w.t.t0 * BT;
+    const int hi = static_cast<int>(w.t.hi - base), lo = static_cast<int>(w.t.lo - base);
+    const int hi_all = static_cast<int>(key_end(w.q, w.t.rr0 / g) - base);
+    const int lo_all = static_cast<int>(key_begin(a, key_end(w.q, (w.t.rr1 - 1) / g)) - base);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int rr = w.t.rr0 + 8 * nt + 2 * (lane & 3) + c;
+        const long long e = key_end(w.q, (rr < w.t.rr1 ? rr : w.t.rr1 - 1) / g);
+        rhi[nt][c] = static_cast<int>(e - base);
+        rlo[nt][c] = static_cast<int>(key_begin(a, e) - base);
+      }
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
+    }
+    const long long item0 = u - w.k;  // the item's first unit
+    for (; w.k < w.t.nt && u < run.last; ++w.k, ++u, ++i) {
+      const int s = i % C::NST;
+      const uint32_t par = static_cast<uint32_t>(i / C::NST) & 1u;
+      const uint32_t kb = sb + s * 2 * C::TILE, vb = kb + C::TILE;
+      const int k0 = w.k * BT + warp * 16;  // the warp's first key, from base
+      ok = ok && wait_bar(kfull(s), par, abort_flag, &g_paged_status, 0x82, lim);
+      ok = __all_sync(kAll, ok);
+      const bool some = k0 < hi && k0 + 16 > lo;
+      float sc[NT][4];
+      uint32_t pb[NT][3][2];
+      float al[NT][2];
+      if (some) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t af[4];
+          const int ch = (2 * kk + kc0) & 7;
+          ldsm4(kb + (kk >> 2) * CHB + kr * 128 + ((ch ^ (kr & 7)) << 4), af);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], af, bq[nt][kk][0], bq[nt][kk][1]);
+        }
+        if (k0 < lo_all || k0 + 16 > hi_all) {
+          const int k1 = k0 + (lane >> 2);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int key = k1 + (c >> 1) * 8;
+              if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[nt][c] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaxf(sc[nt][c], sc[nt][c + 2]);
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+            const float mn = fmaxf(m[nt][c], x * sl2);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            al[nt][c] = ex2(m[nt][c] - ref);
+            m[nt][c] = mn;
+            const float p0 = ex2(fmaf(sc[nt][c], sl2, -ref)), p1 = ex2(fmaf(sc[nt][c + 2], sl2, -ref));
+            l[nt][c] = fmaf(l[nt][c], al[nt][c], p0 + p1);
+            sc[nt][c] = p0;
+            sc[nt][c + 2] = p1;
+          }
+        // P as three bf16 terms (8 + 8 + 8 bits): the product with V then has
+        // the weights' fp32 value, which an fp32 output shows; one bf16 term
+        // is off by 2^-9 of each weight.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float x = sc[nt][2 * half], y = sc[nt][2 * half + 1];
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const uint32_t h = bf16x2_rn(x, y);
+              pb[nt][term][half] = transpose8x8(h);
+              x -= __uint_as_float(h << 16);
+              y -= __uint_as_float(h & 0xffff0000u);
+            }
+          }
+      }
+      ok = ok && wait_bar(vfull(s), par, abort_flag, &g_paged_status, 0x83, lim);
+      ok = __all_sync(kAll, ok);
+      if (some) {
+        const bool edge = k0 < lo || k0 + 16 > hi;
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // V rows outside [lo, hi) may hold anything
+        if (edge) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int key = k0 + 8 * half + 2 * (lane & 3);
+            keep[half] = (key >= lo && key < hi ? 0xffffu : 0u) |
+                         (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm) {
+          uint32_t af[4];
+          const int ch = (2 * dm + vc0) & 7;
+          ldsm4_t(vb + (dm >> 2) * CHB + vr * 128 + ((ch ^ (vr & 7)) << 4), af);
+          if (edge) {
+            af[0] &= keep[0];
+            af[1] &= keep[0];
+            af[2] &= keep[1];
+            af[3] &= keep[1];
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            // The tile's product apart, small terms first, then one rounded
+            // fp32 step: the tensor core's own accumulation truncates.
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(t, af, pb[nt][2][0], pb[nt][2][1]);
+            mma16816(t, af, pb[nt][1][0], pb[nt][1][1]);
+            mma16816(t, af, pb[nt][0][0], pb[nt][0][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nt][dm][c] = fmaf(o[nt][dm][c], al[nt][c & 1], t[c]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+    }
+    // ---------------------------------------------------------------- the warps' states meet
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nt][c];
+        x += __shfl_xor_sync(kAll, x, 4);
+        x += __shfl_xor_sync(kAll, x, 8);
+        x += __shfl_xor_sync(kAll, x, 16);
+        if (lane < 4) {
+          s_m[warp * 16 + 8 * nt + 2 * lane + c] = m[nt][c];
+          s_l[warp * 16 + 8 * nt + 2 * lane + c] = x;
+        }
+      }
+    named_bar_sync(1, 32 * kCons);
+    const long long item1 = item0 + w.t.nt;
+    const int c0 = cta_of(item0, run), c1 = cta_of(item1 - 1, run);
+    const bool whole = c0 == c1;
+    const int slot = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
+    if (!whole && static_cast<int>(blockIdx.x) == c0 && tid == 0)
+      cuts[blockIdx.x] = Cut{c1, w.q.row0, w.t.rr0, w.t.rr1 - w.t.rr0, w.kh};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) named_bar_sync(1, 32 * kCons);  // the sums of group nt - 1 are read
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 2 * (lane & 3) + c;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * 16 + 8 * nt + r]);
+        const float e = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mx);
+        // Column d of row r at d ^ 8 (r / 2): the four row pairs of a store
+        // fall into different banks.
+        float* dst = buf + (warp * 8 + r) * D;
+        const int sw = (r >> 1) << 3;
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm) {
+          dst[(dm * 16 + (lane >> 2)) ^ sw] = o[nt][dm][c] * e;
+          dst[(dm * 16 + 8 + (lane >> 2)) ^ sw] = o[nt][dm][c + 2] * e;
+        }
+      }
+      // The thread's sums: row r, four columns.
+      constexpr int PT = 8 * D / 4;  // float4s of the group
+      const int r = tid / (D / 4), d0 = (tid % (D / 4)) * 4;
+      const int rr = w.t.rr0 + 8 * nt + r;
+      float mx = -INFINITY, lt = 0.f;
+      if (tid < PT) {
+#pragma unroll
+        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * 16 + 8 * nt + r]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int x = 0; x < kCons; ++x)
+          lt = fmaf(s_l[x * 16 + 8 * nt + r], ex2(s_m[x * 16 + 8 * nt + r] - ref), lt);
+      }
+      named_bar_sync(1, 32 * kCons);
+      if (tid < PT && rr < w.t.rr1) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kCons; ++x) {
+          const float4 z = *reinterpret_cast<const float4*>(
+              buf + (x * 8 + r) * D + (d0 ^ ((r >> 1) << 3)));
+          y.x += z.x;
+          y.y += z.y;
+          y.z += z.z;
+          y.w += z.w;
+        }
+        if (whole) {
+          const long long row = static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g;
+          const float inv = lt > 0.f ? 1.f / lt : 0.f;
+          if (a.out_bf16) {
+            const uint2 h = make_uint2(bf16x2_rn(y.x * inv, y.y * inv), bf16x2_rn(y.z * inv, y.w * inv));
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d0) = h;
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + d0) =
+                make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+          }
+          if (d0 == 0) a.lse[row] = lt > 0.f ? mx * kLn2 + logf(lt) : -INFINITY;
+        } else {
+          const int pr = slot * RT + 8 * nt + r;
+          *reinterpret_cast<float4*>(a.po + static_cast<long long>(pr) * D + d0) = y;
+          if (d0 == 0) {
+            a.pm[pr] = mx;
+            a.pl[pr] = lt;
+          }
+        }
+      }
+    }
+    if (u < run.last) w.next(a, g, RT);
   }
 }
 
-// One CTA; chunks as above.  Every access to the free list is checked
-// against its capacity, every table read against the row.
-__global__ void __launch_bounds__(kBook) paged_release_kernel(const ReleaseArgs a) {
-  __shared__ int s_page[kBook + 1];
-  const int tid = threadIdx.x, sh = a.page_shift;
-  const long long ps1 = (1LL << sh) - 1;
-  int count = *a.free_count;
-  count = count < 0 ? 0 : (count > a.free_capacity ? a.free_capacity : count);
-  long long top = count;
-  for (int i0 = 0; i0 < a.n_req; i0 += kBook) {
-    const int i = i0 + tid;
-    const bool in = i < a.n_req;
-    const int len = in ? at_least_0(a.lengths[i]) : 0;
-    const bool fin = in && a.finished[i] != 0;
-    const long long have = fin ? (len + ps1) >> sh : 0;
-    int pages;
-    s_page[tid] = block_scan(static_cast<int>(have < a.max_pages ? have : a.max_pages), &pages);
-    if (in) a.lengths_out[i] = fin ? 0 : len;
-    __syncthreads();
-    for (int x = tid; x < pages; x += kBook) {
-      const int r = find_last(s_page, kBook, x);
-      if (top + x < a.free_capacity)
-        a.free_pages[top + x] =
-            a.block_table[static_cast<long long>(i0 + r) * a.max_pages + (x - s_page[r])];
-    }
-    top += pages;
-    __syncthreads();
-  }
-  if (tid == 0) *a.free_count_out = static_cast<int>(top < a.free_capacity ? top : a.free_capacity);
-}
-
-// ------------------------------------------------------------------ paged decode
-// One CTA per (query row, head): warp w takes keys w, w + 8, ... with the
-// lanes over the columns and its own running (m, l, O~); the warps' states
-// meet in shared memory.
+// Joins the partial states of the item that CTA c = blockIdx.x began and
+// others went on with: slots 2c + 1, 2(c + 1), 2(c + 2), ...; one CTA per
+// row.  Its warps take every fourth partial and meet in shared memory.
+constexpr int kJoin = 4;
 template <int D>
-__global__ void __launch_bounds__(256) paged_decode_kernel(const PagedArgs a) {
-  constexpr int CPL = D / 32, W = 8;
-  __shared__ float s_m[W], s_l[W], s_o[W][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long t = blockIdx.x;
-  const int h = blockIdx.y, kh = h / (a.heads / a.kv_heads);
-  long long r = t / a.n_q, first = r * a.n_q, last = first + a.n_q;
-  if (a.cu_q) {
-    r = find_last(a.cu_q, a.n_req, static_cast<int>(t));
-    first = a.cu_q[r];
-    last = a.cu_q[r + 1];
-    if (t < first || t >= last) return;  // a row behind the last request: left as it was
-  }
-  const int sh = a.page_shift;
-  long long len = a.lengths[r];
-  const long long most = static_cast<long long>(a.max_pages) << sh;
-  len = len < 0 ? 0 : (len > most ? most : len);
-  long long hi = len - (last - t) + 1;
-  if (hi < 0) hi = 0;
-  const long long lo = a.window > 0 && hi - a.window > 0 ? hi - a.window : 0;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (t * a.heads + h) * D + CPL * lane;
-  float qv[CPL], o[CPL];
+__global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedArgs a, int RT) {
+  constexpr int CPL = D / 32;
+  __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][D];
+  const int c = blockIdx.x, r = blockIdx.y;
+  const Cut cut = static_cast<const Cut*>(a.cuts)[c];
+  if (cut.last < 0 || r >= cut.rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int np = cut.last - c + 1;
+  auto slot = [&](int p) { return static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * RT + r; };
+  float mx = -INFINITY;
+  for (int p = threadIdx.x; p < np; p += 32 * kJoin) mx = fmaxf(mx, a.pm[slot(p)]);
 #pragma unroll
-  for (int c = 0; c < CPL; ++c) {
-    qv[c] = __bfloat162float(q[c]);
-    o[c] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (long long key = lo + warp; key < hi; key += W) {
-    const int page = a.block_table[r * a.max_pages + (key >> sh)];
-    if (page < 0 || page >= a.n_pages) continue;
-    const long long in = ((key & ((1LL << sh) - 1)) * a.kv_heads + kh) * D + CPL * lane;
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.kc) + page * a.kc_page + in;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.vc) + page * a.vc_page + in;
-    float s = 0.f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) s = fmaf(qv[c], __bfloat162float(k[c]), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kAll, s, x);
-    s *= a.scale_log2;
-    if (s == -INFINITY) continue;
-    const float mn = fmaxf(m, s), al = exp2f(m - mn), p = exp2f(s - mn);
-    m = mn;
-    l = l * al + p;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) o[c] = fmaf(p, __bfloat162float(v[c]), o[c] * al);
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int c = 0; c < CPL; ++c) s_o[warp][CPL * lane + c] = o[c];
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+  if (lane == 0) s_m[warp] = mx;
   __syncthreads();
-  float mx = -INFINITY, lt = 0.f;
-  for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w]);
+#pragma unroll
+  for (int x = 0; x < kJoin; ++x) mx = fmaxf(mx, s_m[x]);
   const float ref = mx == -INFINITY ? 0.f : mx;
-  for (int w = 0; w < W; ++w) lt += s_l[w] * exp2f(s_m[w] - ref);
-  const float inv = lt > 0.f ? 1.f / lt : 0.f;
-  for (int x = threadIdx.x; x < D; x += 256) {
-    float y = 0.f;
-    for (int w = 0; w < W; ++w) y = fmaf(s_o[w][x], exp2f(s_m[w] - ref), y);
-    const long long at = (t * a.heads + h) * D + x;
-    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y * inv);
-    else static_cast<float*>(a.out)[at] = y * inv;
+  float acc[CPL], l = 0.f;
+#pragma unroll
+  for (int x = 0; x < CPL; ++x) acc[x] = 0.f;
+  for (int p = warp; p < np; p += kJoin) {
+    const long long at = slot(p);
+    const float e = ex2(a.pm[at] - ref);
+    l = fmaf(a.pl[at], e, l);
+#pragma unroll
+    for (int x = 0; x < CPL; ++x) acc[x] = fmaf(a.po[at * D + CPL * lane + x], e, acc[x]);
   }
-  if (threadIdx.x == 0) a.lse[t * a.heads + h] = lt > 0.f ? mx * kLn2 + logf(lt) : -INFINITY;
+#pragma unroll
+  for (int x = 0; x < CPL; ++x) s_o[warp][CPL * lane + x] = acc[x];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int x = 0; x < kJoin; ++x) l += s_l[x];
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int g = a.heads / a.kv_heads, rr = cut.rr0 + r;
+  const long long row = static_cast<long long>(cut.row0 + rr / g) * a.heads + cut.kh * g + rr % g;
+  for (int x = threadIdx.x; x < D; x += 32 * kJoin) {
+    float y = 0.f;
+#pragma unroll
+    for (int p = 0; p < kJoin; ++p) y += s_o[p][x];
+    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + x] = __float2bfloat16_rn(y * inv);
+    else static_cast<float*>(a.out)[row * D + x] = y * inv;
+  }
+  if (threadIdx.x == 0) a.lse[row] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+}
+
+template <int D, int NT>
+cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(Cfg<D>::SMEM));
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<D, NT><<<ctas, kThreads, Cfg<D>::SMEM, st>>>(tk, tv, a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st) {
-  paged_extend_kernel<<<1, kBook, 0, st>>>(a);
-  return cudaGetLastError();
+int paged_row_tile(const PagedArgs& a) {
+  // Rows per request and KV head on average (exact when every request has
+  // the same number of new tokens).
+  const long long rows = (a.T + a.n_req - 1) / a.n_req * (a.heads / a.kv_heads);
+  return rows <= 8 ? 8 : 16;
 }
 
-cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st) {
-  paged_release_kernel<<<1, kBook, 0, st>>>(a);
-  return cudaGetLastError();
+size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas); }
+
+cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
+                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  if (d == 128)
+    return row_tile == 8 ? decode_t<128, 1>(a, ctas, tk, tv, st) : decode_t<128, 2>(a, ctas, tk, tv, st);
+  return row_tile == 8 ? decode_t<64, 1>(a, ctas, tk, tv, st) : decode_t<64, 2>(a, ctas, tk, tv, st);
 }
 
-cudaError_t launch_paged_decode(const PagedArgs& a, int d, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>(a.heads));
-  if (d == 128) paged_decode_kernel<128><<<grid, 256, 0, st>>>(a);
-  else paged_decode_kernel<64><<<grid, 256, 0, st>>>(a);
+cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile));
+  if (d == 128) paged_combine_kernel<128><<<grid, 32 * kJoin, 0, st>>>(a, row_tile);
+  else paged_combine_kernel<64><<<grid, 32 * kJoin, 0, st>>>(a, row_tile);
   return cudaGetLastError();
 }
 

@@ -66,6 +66,23 @@ int check_stride(const char* name, long long stride, long long row, int dtype) {
   return RA_OK;
 }
 
+// 4-D map over the pages of one cache tensor; a box is one KV head's rows of
+// a page (half a page of 256), 64 columns wide, 128-byte swizzle.
+int page_map(CUtensorMap* map, const void* base, int n_pages, int page_size, long long page_stride,
+             int kv_heads, int d) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(kv_heads),
+                              static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(kv_heads) * d * 2;
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, row, static_cast<cuuint64_t>(page_stride) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(page_size < 128 ? page_size : 128), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (CUresult %d)", (int)r);
+  return RA_OK;
+}
+
 // What the three rope calls share.
 int rope_common(ra::RopeArgs& a, long long T, int d, int heads, int kv_heads, int dtype, int rot,
                 int interleaved, const void* phases, const void* qw, const void* kw, int w_dtype,
@@ -377,11 +394,41 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   a.kv_heads = kv_heads;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   a.wait_limit = kWaitLimit;
+  if ((rc = get_encoder()) != RA_OK) return rc;
+  CUtensorMap tk, tv;
+  // Without pages no load is ever issued; the maps still need an address.
+  if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
+  if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
+  int dev = 0, ctas = 152;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const int rt = ra::paged_row_tile(a);
+  const size_t rows = static_cast<size_t>(2) * ctas * rt;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
-  cudaError_t e = ra::launch_paged_decode(a, d, st);
-  ts.done(e == cudaSuccess);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-decode launch");
+  float* part = nullptr;
+  e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));
+  }
+  a.po = part;
+  a.pm = part + rows * d;
+  a.pl = a.pm + rows;
+  a.cuts = a.pl + rows;
+  {
+    TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
+    e = ra::launch_paged_decode(a, d, ctas, rt, tk, tv, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (e == cudaSuccess) {
+    TraceScope ts(RA_KERNEL_PAGED_COMBINE, st);
+    e = ra::launch_paged_combine(a, d, ctas, rt, st);
+    ts.done(e == cudaSuccess);
+  }
+  const cudaError_t ef = cudaFreeAsync(part, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged-decode launch");
+  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
 }
 
 }  // extern "C"

@@ -113,8 +113,21 @@ struct PagedArgs {
   int kv_heads;
   float scale_log2;        // log2(e) / sqrt(d)
   long long wait_limit;
+  // Scratch: partial states of cut items, two slots per CTA (po [slot][row
+  // tile][d]), and one record per CTA.
+  float* po;
+  float* pm;
+  float* pl;
+  void* cuts;
 };
-cudaError_t launch_paged_decode(const PagedArgs& a, int d, cudaStream_t st);
+// Query rows (of one request and KV head) that a CTA takes together.
+int paged_row_tile(const PagedArgs& a);
+size_t paged_cut_bytes(int ctas);
+// tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
+// 64 x 1 x min(page_size, 128) x 1, 128-byte swizzle.
+cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
+                                const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st);
 cudaError_t take_paged_status(int* code);
 
 }  // namespace ra
