@@ -34,6 +34,7 @@ struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   uint4 w;
+  __device__ __forceinline__ Vec() : w(make_uint4(0u, 0u, 0u, 0u)) {}
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     w = *reinterpret_cast<const uint4*>(p);  // not __ldg: the output may be the input
   }
@@ -58,6 +59,7 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
   float4 a, b;
+  __device__ __forceinline__ Vec() : a(make_float4(0.f, 0.f, 0.f, 0.f)), b(a) {}
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const float4*>(p);
     b = *(reinterpret_cast<const float4*>(p) + 1);
@@ -97,54 +99,81 @@ __device__ __forceinline__ long long row_position(const RopeArgs& a, long long t
 template <int D, bool INTER>
 struct Rot {
   static constexpr int LPR = D / 8;  // lanes per row
+  unsigned long long ph[2];  // phases of pairs 2 lane, 2 lane + 1
   float cs[8], sn[8];
   int mate;     // lane that holds the partner columns
+  int from;     // lane that computed this lane's first pair
   bool on;      // this lane's columns are rotated
+  bool minus;   // its columns are the `a` of their pairs (half layout)
 
-  __device__ __forceinline__ void place(int rot, int lane) {
-    const int s = lane % LPR, half = rot / 16;
-    on = s < rot / 8;
-    mate = !on ? lane : (s < half ? lane + half : lane - half);
-  }
-  __device__ __forceinline__ void angles(const RopeArgs& a, long long pos, int lane) {
+  __device__ __forceinline__ void place(const RopeArgs& a, int lane) {
     const int s = lane % LPR, half = a.rot / 16;
+    on = s < a.rot / 8;
+    minus = s < half;
+    mate = !on ? lane : (minus ? lane + half : lane - half);
+    from = !on ? lane : (INTER ? 2 * s : 4 * (minus ? s : s - half));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = 1.f;
-      sn[e] = 0.f;
+    for (int j = 0; j < 2; ++j) ph[j] = 2 * lane + j < a.rot / 2 ? a.phases[2 * lane + j] : 0;
+  }
+  // cos and sin at a position: each lane computes two of the (up to 64)
+  // pairs and the lanes exchange them, since every row of the warp and both
+  // halves of a row need the same ones.
+  __device__ __forceinline__ void angles(const RopeArgs& a, long long pos) {
+    float c[2], s[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const unsigned long long turn = static_cast<unsigned long long>(pos) * ph[j];
+      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s[j], &c[j]);
+      s[j] *= a.mscale;
+      c[j] *= a.mscale;
     }
-    if (!on) return;
     constexpr int N = INTER ? 4 : 8;
-    const int i0 = INTER ? 4 * s : 8 * (s < half ? s : s - half);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const unsigned long long turn = static_cast<unsigned long long>(pos) * __ldg(a.phases + i0 + j);
-      float sv, cv;
-      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sv, &cv);
-      sv *= a.mscale;
-      cv *= a.mscale;
+      const float cv = __shfl_sync(kAll, c[j & 1], from + j / 2);
+      const float sv = __shfl_sync(kAll, s[j & 1], from + j / 2);
       if (INTER) {
-        cs[2 * j] = cs[2 * j + 1] = cv;
-        sn[2 * j] = -sv;
-        sn[2 * j + 1] = sv;
+        cs[2 * j] = cs[2 * j + 1] = on ? cv : 1.f;
+        sn[2 * j] = on ? -sv : 0.f;
+        sn[2 * j + 1] = on ? sv : 0.f;
       } else {
-        cs[j] = cv;
-        sn[j] = s < half ? -sv : sv;
+        cs[j] = on ? cv : 1.f;
+        sn[j] = on ? (minus ? -sv : sv) : 0.f;
       }
     }
   }
-  // dir = 1: rotate; dir = -1: turn back (the transpose).
-  template <int DIR>
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
-    float p[8];
+  // The partner's value of each column; 0 where nothing is rotated, so an
+  // infinity there does not turn into a NaN with sn = 0.
+  __device__ __forceinline__ void partner(const float (&x)[8], float (&p)[8]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 8; ++e) {
       p[e] = INTER ? x[e ^ 1] : __shfl_sync(kAll, x[e], mate);
-    if (!on) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[e] + (DIR > 0 ? p[e] : -p[e]) * sn[e];
+      if (!on) p[e] = 0.f;
+    }
   }
 };
+
+// The same for a row as loaded: bf16 travels packed, two columns a shuffle.
+template <int D, bool INTER>
+__device__ __forceinline__ void partner_row(const Rot<D, INTER>& rot, const Vec<__nv_bfloat16>& v,
+                                            const float (&x)[8], float (&p)[8]) {
+  if (INTER) {
+    rot.partner(x, p);
+    return;
+  }
+  Vec<__nv_bfloat16> m;
+  m.w.x = __shfl_sync(kAll, v.w.x, rot.mate);
+  m.w.y = __shfl_sync(kAll, v.w.y, rot.mate);
+  m.w.z = __shfl_sync(kAll, v.w.z, rot.mate);
+  m.w.w = __shfl_sync(kAll, v.w.w, rot.mate);
+  if (!rot.on) m.w = make_uint4(0u, 0u, 0u, 0u);
+  m.get(p);
+}
+template <int D, bool INTER>
+__device__ __forceinline__ void partner_row(const Rot<D, INTER>& rot, const Vec<float>&,
+                                            const float (&x)[8], float (&p)[8]) {
+  rot.partner(x, p);
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -154,87 +183,121 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Forward (APPEND: with k and v written to their pages).  A warp takes a
-// token, or one of a.parts shares of its rows; LPR lanes hold a row, so an
-// iteration covers 32 / LPR rows.  cos and sin are computed once per token.
+// token, or one of a.parts shares of its rows; LPR lanes hold a row, so a
+// group is 32 / LPR rows, of q, k or v alone.  The loads of kBatch groups are
+// in flight together.  Norm weight and rotation are folded once per token,
+// out = r (x cw + partner sw) with cw = w cos and sw = w_partner sin, so a
+// row costs two products and a sum per column, and one exchange of its packed
+// columns with the partner lane.
+constexpr int kBatch = 4;
+
 template <typename T, int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kWarps * 32) rope_forward_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31, col = 8 * (lane % LPR), sub = lane / LPR;
-  const int rows = a.heads + a.kv_heads + (APPEND ? a.kv_heads : 0);
-  const int groups = (rows + RPI - 1) / RPI;
+  const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
+  const int groups = gq + gk + (APPEND ? gk : 0);
   const int per = (groups + a.parts - 1) / a.parts;
   const long long items = a.T * a.parts;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
-  float wq[8], wk[8];
-  if (a.qw) load_weight(a.qw, a.w_bf16, col, wq);
-  if (a.kw) load_weight(a.kw, a.w_bf16, col, wk);
   Rot<D, INTER> rot;
-  rot.place(a.rot, lane);
+  rot.place(a, lane);
   for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
        it += nwarps) {
-    const long long t = it / a.parts;
-    const int g0 = static_cast<int>(it % a.parts) * per;
+    const long long t = a.parts == 1 ? it : it / a.parts;
+    const int g0 = a.parts == 1 ? 0 : static_cast<int>(it - t * a.parts) * per;
     const int g1 = g0 + per < groups ? g0 + per : groups;
     long long slot = 0;
     if (APPEND) {
       slot = a.slots[t];
       if (slot < 0 || slot >= a.n_slots) continue;  // a padding row: nothing is written
     }
-    rot.angles(a, row_position(a, t), lane);
-    for (int g = g0; g < g1; ++g) {
-      const int row = g * RPI + sub;
-      const bool valid = row < rows;
-      const bool is_q = row < a.heads, is_v = APPEND && row >= a.heads + a.kv_heads;
-      const int h = is_q ? row : (is_v ? row - a.heads - a.kv_heads : row - a.heads);
-      const T* src = static_cast<const T*>(is_q ? a.q : (is_v ? a.v : a.k)) +
-                     t * (is_q ? a.q_str : (is_v ? a.v_str : a.k_str)) + h * D + col;
-      T* dst;
-      if (is_q) {
-        dst = static_cast<T*>(a.qo) + t * a.qo_str + h * D + col;
-      } else if (APPEND) {
-        const long long page = slot >> a.page_shift;
-        const long long in = slot & ((1LL << a.page_shift) - 1);
-        dst = static_cast<T*>(is_v ? a.vc : a.kc) + page * (is_v ? a.vc_page : a.kc_page) +
-              (in * a.kv_heads + h) * D + col;
-      } else {
-        dst = static_cast<T*>(a.ko) + t * a.ko_str + h * D + col;
-      }
-      Vec<T> raw;
-      float x[8];
+    if (g0 < gq + gk) rot.angles(a, row_position(a, t));
+    auto rows = [&](int ga, int gb, int n, const T* src, T* dst, const void* weight, bool copy) {
+      // Groups [ga, gb) of a tensor's n rows of this token.
+      float cw[8], sw[8];
+      if (!copy) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      if (valid) {
-        raw.load(src);
-        raw.get(x);
-      }
-      float ss = 0.f;
+        for (int e = 0; e < 8; ++e) {
+          cw[e] = rot.cs[e];
+          sw[e] = rot.sn[e];
+        }
+        if (weight) {
+          float w[8], wp[8];
+          load_weight(weight, a.w_bf16, col, w);
+          rot.partner(w, wp);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      ss = row_sum<LPR>(ss);
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = x[e];
-        if (is_q ? a.qw != nullptr : a.kw != nullptr) y[e] = x[e] * r * (is_q ? wq[e] : wk[e]);
+          for (int e = 0; e < 8; ++e) {
+            cw[e] *= w[e];
+            sw[e] *= wp[e];
+          }
+        }
       }
-      rot.template apply<1>(y);
-      if (valid) Vec<T>::store(dst, is_v ? x : y);
+      src += sub * D + col;
+      dst += sub * D + col;
+      for (int g = ga; g < gb; g += kBatch) {
+        Vec<T> raw[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          raw[j] = Vec<T>();
+          if (g + j < gb && (g + j) * RPI + sub < n) raw[j].load(src + (g + j) * RPI * D);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (g + j >= gb) break;
+          const bool valid = (g + j) * RPI + sub < n;
+          float x[8];
+          raw[j].get(x);
+          if (!copy) {
+            float p[8];
+            partner_row(rot, raw[j], x, p);
+            float r = 1.f;
+            if (weight) {
+              float ss = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+              r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = r * fmaf(p[e], sw[e], x[e] * cw[e]);
+          }
+          if (valid) Vec<T>::store(dst + (g + j) * RPI * D, x);
+        }
+      }
+    };
+    const T* qs = static_cast<const T*>(a.q) + t * a.q_str;
+    const T* ks = static_cast<const T*>(a.k) + t * a.k_str;
+    if (g0 < gq)
+      rows(g0, g1 < gq ? g1 : gq, a.heads, qs, static_cast<T*>(a.qo) + t * a.qo_str, a.qw, false);
+    long long in = 0, kpage = 0, vpage = 0;
+    if (APPEND) {
+      const long long page = slot >> a.page_shift;
+      in = (slot & ((1LL << a.page_shift) - 1)) * a.kv_heads * D;
+      kpage = page * a.kc_page;
+      vpage = page * a.vc_page;
     }
+    if (g1 > gq && g0 < gq + gk)
+      rows((g0 > gq ? g0 : gq) - gq, (g1 < gq + gk ? g1 : gq + gk) - gq, a.kv_heads, ks,
+           APPEND ? static_cast<T*>(a.kc) + kpage + in : static_cast<T*>(a.ko) + t * a.ko_str, a.kw,
+           false);
+    if (APPEND && g1 > gq + gk)
+      rows((g0 > gq + gk ? g0 : gq + gk) - gq - gk, g1 - gq - gk, a.kv_heads,
+           static_cast<const T*>(a.v) + t * a.v_str, static_cast<T*>(a.vc) + vpage + in, nullptr, true);
   }
 }
 
-// Backward.  Rows as in the forward; the weight gradients are summed in the
-// lanes, over the CTA's warps in shared memory, and written as one partial
-// sum per CTA, so their order is fixed.
+// Backward.  Groups as in the forward; the weight gradients are summed in
+// the lanes, over the CTA's warps in shared memory, and written as one
+// partial sum per CTA, so their order is fixed.
+constexpr int kGradBatch = 2;
+
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) rope_backward_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   __shared__ float s_dw[kWarps][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = 8 * (lane % LPR), sub = lane / LPR;
-  const int rows = a.heads + a.kv_heads;
-  const int groups = (rows + RPI - 1) / RPI;
+  const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
   float wq[8], wk[8], dwq[8], dwk[8];
 #pragma unroll
@@ -242,47 +305,61 @@ __global__ void __launch_bounds__(kWarps * 32) rope_backward_kernel(const RopeAr
   if (a.qw) load_weight(a.qw, a.w_bf16, col, wq);
   if (a.kw) load_weight(a.kw, a.w_bf16, col, wk);
   Rot<D, INTER> rot;
-  rot.place(a.rot, lane);
+  rot.place(a, lane);
   for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.T; t += nwarps) {
-    rot.angles(a, row_position(a, t), lane);
-    for (int g = 0; g < groups; ++g) {
-      const int row = g * RPI + sub;
-      const bool valid = row < rows, is_q = row < a.heads;
-      const int h = is_q ? row : row - a.heads;
-      float x[8], gy[8];
+    rot.angles(a, row_position(a, t));
+    auto rows = [&](int gb, int n, const T* src, const float* grad, T* dst, bool norm,
+                    const float (&w)[8], float (&dw)[8]) {
+      src += sub * D + col;
+      grad += sub * D + col;
+      dst += sub * D + col;
+      for (int g = 0; g < gb; g += kGradBatch) {
+        Vec<T> raw[kGradBatch];
+        Vec<float> gr[kGradBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = gy[e] = 0.f;
-      if (valid) {
-        Vec<T> raw;
-        Vec<float> gr;
-        raw.load(static_cast<const T*>(is_q ? a.q : a.k) + t * (is_q ? a.q_str : a.k_str) + h * D + col);
-        gr.load((is_q ? a.dqo : a.dko) + (t * (is_q ? a.heads : a.kv_heads) + h) * D + col);
-        raw.get(x);
-        gr.get(gy);
-      }
-      rot.template apply<-1>(gy);
-      const bool norm = is_q ? a.qw != nullptr : a.kw != nullptr;
-      float ss = 0.f, ux = 0.f;
+        for (int j = 0; j < kGradBatch; ++j) {
+          raw[j] = Vec<T>();
+          gr[j] = Vec<float>();
+          if (g + j < gb && (g + j) * RPI + sub < n) {
+            raw[j].load(src + (g + j) * RPI * D);
+            gr[j].load(grad + (g + j) * RPI * D);
+          }
+        }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        ux = fmaf(gy[e] * (is_q ? wq[e] : wk[e]), x[e], ux);
-      }
-      ss = row_sum<LPR>(ss);
-      ux = row_sum<LPR>(ux);
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float m = r * r * ux * (1.f / D);
-      float dx[8];
+        for (int j = 0; j < kGradBatch; ++j) {
+          if (g + j >= gb) break;
+          float x[8], gy[8], p[8];
+          raw[j].get(x);
+          gr[j].get(gy);
+          rot.partner(gy, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float hat = x[e] * r;
-        if (is_q) dwq[e] = fmaf(gy[e], hat, dwq[e]);
-        else dwk[e] = fmaf(gy[e], hat, dwk[e]);
-        dx[e] = norm ? r * (gy[e] * (is_q ? wq[e] : wk[e]) - x[e] * m) : gy[e];
+          for (int e = 0; e < 8; ++e) gy[e] = fmaf(-p[e], rot.sn[e], gy[e] * rot.cs[e]);
+          if (norm) {
+            float ss = 0.f, ux = 0.f, u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              u[e] = gy[e] * w[e];
+              ss = fmaf(x[e], x[e], ss);
+              ux = fmaf(u[e], x[e], ux);
+            }
+            ss = row_sum<LPR>(ss);
+            ux = row_sum<LPR>(ux);
+            const float r = rsqrtf(ss * (1.f / D) + a.eps);
+            const float m = r * r * ux * (1.f / D);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              dw[e] = fmaf(gy[e], x[e] * r, dw[e]);
+              gy[e] = r * fmaf(-x[e], m, u[e]);
+            }
+          }
+          if ((g + j) * RPI + sub < n) Vec<T>::store(dst + (g + j) * RPI * D, gy);
+        }
       }
-      if (valid)
-        Vec<T>::store(static_cast<T*>(is_q ? a.qo : a.ko) + t * (is_q ? a.qo_str : a.ko_str) + h * D + col, dx);
-    }
+    };
+    rows(gq, a.heads, static_cast<const T*>(a.q) + t * a.q_str, a.dqo + t * a.heads * D,
+         static_cast<T*>(a.qo) + t * a.qo_str, a.qw != nullptr, wq, dwq);
+    rows(gk, a.kv_heads, static_cast<const T*>(a.k) + t * a.k_str, a.dko + t * a.kv_heads * D,
+         static_cast<T*>(a.ko) + t * a.ko_str, a.kw != nullptr, wk, dwk);
   }
   if (!a.dw) return;
 #pragma unroll
@@ -333,7 +410,12 @@ int sm_count() {
 template <typename T, bool APPEND>
 cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  a.parts = 1;
+  // Few tokens: several warps share a token's rows, down to one batch of
+  // loads each, until there are some 16 warps per SM.
+  const int rpi = 256 / d, gq = (a.heads + rpi - 1) / rpi, gk = (a.kv_heads + rpi - 1) / rpi;
+  const int groups = gq + (APPEND ? 2 : 1) * gk;
+  const long long want = (16LL * sm_count() + a.T - 1) / a.T, most_parts = (groups + kBatch - 1) / kBatch;
+  a.parts = static_cast<int>(want < most_parts ? want : most_parts);
   long long ctas = (a.T * a.parts + kWarps - 1) / kWarps;
   const long long most = 8LL * sm_count();
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);

@@ -165,10 +165,20 @@ int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* b
   a.max_pages = max_pages;
   a.free_capacity = free_capacity;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (ra::paged_extend_needs_scratch(a)) {
+    e = scratch_alloc(reinterpret_cast<void**>(&a.first_page), (static_cast<size_t>(n_req) + 2) * sizeof(int), st);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(RA_ERR_ALLOC, "pool allocation of the page sums failed: %s", cudaGetErrorString(e));
+    }
+  }
   TraceScope ts(RA_KERNEL_PAGED_EXTEND, st);
-  cudaError_t e = ra::launch_paged_extend(a, st);
+  e = ra::launch_paged_extend(a, st);
   ts.done(e == cudaSuccess);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-extend launch");
+  const cudaError_t ef = a.first_page ? cudaFreeAsync(a.first_page, st) : cudaSuccess;
+  if (e != cudaSuccess) return cuda_fail(e, "paged-extend launch");
+  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
 }
 
 int ra_paged_release(const int* lengths, const int* finished, int n_req, const int* block_table,
@@ -192,10 +202,20 @@ int ra_paged_release(const int* lengths, const int* finished, int n_req, const i
   a.max_pages = max_pages;
   a.free_capacity = free_capacity;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (ra::paged_release_needs_scratch(a)) {
+    e = scratch_alloc(reinterpret_cast<void**>(&a.first_page), (static_cast<size_t>(n_req) + 2) * sizeof(int), st);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(RA_ERR_ALLOC, "pool allocation of the page sums failed: %s", cudaGetErrorString(e));
+    }
+  }
   TraceScope ts(RA_KERNEL_PAGED_RELEASE, st);
-  cudaError_t e = ra::launch_paged_release(a, st);
+  e = ra::launch_paged_release(a, st);
   ts.done(e == cudaSuccess);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-release launch");
+  const cudaError_t ef = a.first_page ? cudaFreeAsync(a.first_page, st) : cudaSuccess;
+  if (e != cudaSuccess) return cuda_fail(e, "paged-release launch");
+  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
 }
 
 int ra_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, long long T, int d,

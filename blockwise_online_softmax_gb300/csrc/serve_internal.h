@@ -27,7 +27,11 @@ struct ExtendArgs {
   int max_pages;
   int free_capacity;
   int page_shift;         // log2 of the page size
+  // Scratch of a large step, else null: per request the new pages of the
+  // requests before it, then the stack's count before the step.
+  int* first_page;        // [n_req + 1]
 };
+bool paged_extend_needs_scratch(const ExtendArgs& a);
 cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st);
 
 struct ReleaseArgs {
@@ -42,7 +46,9 @@ struct ReleaseArgs {
   int max_pages;
   int free_capacity;
   int page_shift;
+  int* first_page;  // [n_req + 2], or null: as above, the total, the count before
 };
+bool paged_release_needs_scratch(const ReleaseArgs& a);
 cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st);
 
 // ------------------------------------------------------------------ q/k norm and rotary positions
