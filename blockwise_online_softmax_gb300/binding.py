@@ -429,62 +429,110 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
 
 # ------------------------------------------------------------------ rotary positions, pages
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+# These calls are made once or more per layer of a serving step, where a few
+# microseconds of Python each are the step's time: their checks read every
+# tensor property once, and the device is switched only when it must be.
+
+def _device(t, name) -> int:
+    """Index of the CUDA device a tensor lives on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _rows(t: torch.Tensor, name: str, heads: int, d: int, dtype=None) -> tuple[int, int]:
-    """Pointer and token stride of a [T, heads, d] CUDA tensor whose heads are
+def _arg(t, name, dev, dtype):
+    """Pointer of a dense tensor of `dtype` on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                         f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _vec(t, name, n, dev, dtype):
+    """Pointer of a dense 1-D tensor of n entries."""
+    p = _arg(t, name, dev, dtype)
+    if t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    return p
+
+
+def _rows(t, name, T, heads, d, dev, dtype):
+    """Pointer and token stride of a [T, heads, d] tensor whose heads are
     dense; tokens may lie further apart (a view of a packed projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                         f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: the heads of a token must be dense (strides {t.stride()})")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+    st = t.stride()
+    if T and (st[2] != 1 or (heads > 1 and st[1] != d)):
+        raise ValueError(f"{name}: the heads of a token must be dense (strides {st})")
+    return t.data_ptr(), st[0] if T > 1 else heads * d
 
 
-def _vector(t, name, n, dtype):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 1 or t.numel() != n:
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    return _dev(t, name, dtype)
+class _On:
+    """Makes device `dev` current for the block if it is not, and resolves
+    the stream there.  `with _On(dev, stream) as st:`"""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.old = dev, stream, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.dev:
+            self.old = cur
+            torch.cuda.set_device(self.dev)
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.old is not None:
+            torch.cuda.set_device(self.old)
 
 
-def _weight(q_weight, k_weight, d):
+def _weights(q_weight, k_weight, d, dev):
     """Pointers of the norm weights (0 for none) and their dtype."""
-    given = [(w, n) for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")) if w is not None]
-    for w, n in given:
+    code, ptrs = RA_F32, []
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            ptrs.append(0)
+            continue
         if w.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"{n} must be float32 or bfloat16, got {w.dtype}")
-        if w.dtype != given[0][0].dtype:
-            raise TypeError("q_weight and k_weight must share a dtype")
-        _vector(w, n, d, w.dtype)
-    code = RA_BF16 if given and given[0][0].dtype == torch.bfloat16 else RA_F32
-    return (q_weight.data_ptr() if q_weight is not None else 0,
-            k_weight.data_ptr() if k_weight is not None else 0, code)
+            raise TypeError(f"{name} must be float32 or bfloat16, got {w.dtype}")
+        ptrs.append(_vec(w, name, d, dev, w.dtype))
+        if w.dtype is torch.bfloat16:
+            code = RA_BF16
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise TypeError("q_weight and k_weight must share a dtype")
+    return ptrs[0], ptrs[1], code
 
 
-def _phase_table(phases):
+def _phase_table(phases, dev):
     if phases is None:
         return 0, 0
-    if phases.dim() != 1:
-        raise ValueError("phases must be 1-D with rot_dim / 2 entries")
-    return _dev(phases, "phases", torch.int64), 2 * phases.numel()
+    n = phases.numel()
+    return _vec(phases, "phases", n, dev, torch.int64), 2 * n
 
 
 def _qk_shapes(q, k):
-    if q.dim() != 3 or k.dim() != 3:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3:
         raise ValueError("q: [T, heads, d]; k: [T, kv_heads, d]")
-    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or k.dtype != q.dtype:
+    if ks[0] != qs[0] or ks[2] != qs[2] or k.dtype is not q.dtype:
         raise ValueError("q and k must share their tokens, head dim and dtype")
-    return q.shape[0], q.shape[1], k.shape[1], q.shape[2]
+    return qs[0], qs[1], ks[1], qs[2]
 
 
 def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None,
@@ -551,22 +599,23 @@ def ra_qk_norm_rope(q, k, phases, *, q_weight=None, k_weight=None, eps: float = 
     dt = _qkv_dtype(q)
     if q_out is None:
         q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out and k_out must match q and k in shape")
     if k_out is None:
         k_out = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    elif k_out.shape != k.shape:
         raise ValueError("q_out and k_out must match q and k in shape")
-    _same_device(q, k=k, phases=phases, q_weight=q_weight, k_weight=k_weight,
-                 positions=positions, q_out=q_out, k_out=k_out)
-    qp, qs = _rows(q, "q", heads, d)
-    kp, ks = _rows(k, "k", kv_heads, d)
-    ph, rot = _phase_table(phases)
-    qw, kw, wt = _weight(q_weight, k_weight, d)
-    pos = _vector(positions, "positions", T, torch.int32) if positions is not None else 0
-    with torch.cuda.device(q.device):
+    dev, dtype = _device(q, "q"), q.dtype
+    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
+    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
+    ph, rot = _phase_table(phases, dev)
+    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
+    pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
+    with _On(dev, stream) as st:
         _check(lib().ra_qk_norm_rope(
-            qp, kp, _dev(q_out, "q_out", q.dtype), _dev(k_out, "k_out", q.dtype), T, d, heads,
-            kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)), ph,
-            float(mscale), qw, kw, wt, float(eps), dt, _stream(stream)))
+            qp, kp, _arg(q_out, "q_out", dev, dtype), _arg(k_out, "k_out", dev, dtype), T, d,
+            heads, kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)),
+            ph, float(mscale), qw, kw, wt, float(eps), dt, st))
     return q_out, k_out
 
 
@@ -580,7 +629,7 @@ def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_w
     the weights' are fp32 [d], None without that weight."""
     T, heads, kv_heads, d = _qk_shapes(q, k)
     dt = _qkv_dtype(q)
-    if tuple(dq_out.shape) != (T, heads, d) or tuple(dk_out.shape) != (T, kv_heads, d):
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
         raise ValueError("dq_out and dk_out must match q and k in shape")
     if dq is None:
         dq = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
@@ -588,7 +637,6 @@ def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_w
         dk = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
     if dq.shape != q.shape or dk.shape != k.shape:
         raise ValueError("dq and dk must match q and k in shape")
-    qw, kw, wt = _weight(q_weight, k_weight, d)
     for w, g, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
         if w is None and g is not None:
             raise ValueError(f"{name} without its weight")
@@ -596,31 +644,29 @@ def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_w
         dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
-    _same_device(q, k=k, phases=phases, q_weight=q_weight, k_weight=k_weight,
-                 positions=positions, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk,
-                 dq_weight=dq_weight, dk_weight=dk_weight)
-    qp, qs = _rows(q, "q", heads, d)
-    kp, ks = _rows(k, "k", kv_heads, d)
-    dqp, dqs = _rows(dq, "dq", heads, d, q.dtype)
-    dkp, dks = _rows(dk, "dk", kv_heads, d, q.dtype)
-    ph, rot = _phase_table(phases)
-    pos = _vector(positions, "positions", T, torch.int32) if positions is not None else 0
-    dqw = _vector(dq_weight, "dq_weight", d, torch.float32) if dq_weight is not None else 0
-    dkw = _vector(dk_weight, "dk_weight", d, torch.float32) if dk_weight is not None else 0
-    with torch.cuda.device(q.device):
+    dev, dtype, f32 = _device(q, "q"), q.dtype, torch.float32
+    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
+    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
+    dqp, dqs = _rows(dq, "dq", T, heads, d, dev, dtype)
+    dkp, dks = _rows(dk, "dk", T, kv_heads, d, dev, dtype)
+    ph, rot = _phase_table(phases, dev)
+    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
+    pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
+    dqw = 0 if dq_weight is None else _vec(dq_weight, "dq_weight", d, dev, f32)
+    dkw = 0 if dk_weight is None else _vec(dk_weight, "dk_weight", d, dev, f32)
+    with _On(dev, stream) as st:
         _check(lib().ra_qk_norm_rope_backward(
-            qp, kp, _dev(dq_out, "dq_out", torch.float32), _dev(dk_out, "dk_out", torch.float32),
-            dqp, dkp, dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout),
-            int(P), rot, int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt,
-            _stream(stream)))
+            qp, kp, _arg(dq_out, "dq_out", dev, f32), _arg(dk_out, "dk_out", dev, f32), dqp, dkp,
+            dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout), int(P), rot,
+            int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt, st))
     return dq, dk, dq_weight, dk_weight
 
 
-def _table(block_table, n_req):
-    if block_table.dim() != 2 or block_table.shape[0] != n_req:
-        raise ValueError(f"block_table must be [n_req={n_req}, max_pages], "
-                         f"got {tuple(block_table.shape)}")
-    return _dev(block_table, "block_table", torch.int32), block_table.shape[1]
+def _table(block_table, n_req, dev):
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != n_req:
+        raise ValueError(f"block_table must be [n_req={n_req}, max_pages], got {tuple(shape)}")
+    return _arg(block_table, "block_table", dev, torch.int32), shape[1]
 
 
 def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *, page_size: int,
@@ -633,31 +679,38 @@ def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *,
     free_count_out may be lengths and free_count themselves.  A nonzero
     status (pages missing, rows too short, tokens beyond `tokens`) means
     that the step changed nothing."""
-    n = lengths.numel()
-    dev = lengths.device
-
-    def make(t, m, dtype=torch.int32):
-        return torch.empty(m, dtype=dtype, device=dev) if t is None else t
-
-    lengths_out, free_count_out = make(lengths_out, n), make(free_count_out, 1)
-    slots, positions = make(slots, int(tokens), torch.int64), make(positions, int(tokens))
-    cu_tokens, status = make(cu_tokens, n + 1), make(status, 3)
-    _same_device(lengths, new_tokens=new_tokens, block_table=block_table, free_pages=free_pages,
-                 free_count=free_count, lengths_out=lengths_out, free_count_out=free_count_out,
-                 slots=slots, positions=positions, cu_tokens=cu_tokens, status=status)
+    n, tokens = lengths.numel(), int(tokens)
     i32 = torch.int32
-    table, width = _table(block_table, n)
-    with torch.cuda.device(dev):
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError(f"block_table must be [n_req={n}, max_pages], "
+                         f"got {tuple(block_table.shape)}")
+    dev = _device(lengths, "lengths")
+    where = lengths.device
+    if lengths_out is None:
+        lengths_out = torch.empty(n, dtype=i32, device=where)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, dtype=i32, device=where)
+    if slots is None:
+        slots = torch.empty(tokens, dtype=torch.int64, device=where)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=i32, device=where)
+    if cu_tokens is None:
+        cu_tokens = torch.empty(n + 1, dtype=i32, device=where)
+    if status is None:
+        status = torch.empty(3, dtype=i32, device=where)
+    table, width = _table(block_table, n, dev)
+    pool = free_pages.numel()
+    with _On(dev, stream) as st:
         _check(lib().ra_paged_extend(
-            _vector(lengths, "lengths", n, i32), _vector(new_tokens, "new_tokens", n, i32), n,
-            table, width, _vector(free_pages, "free_pages", free_pages.numel(), i32),
-            free_pages.numel(), _vector(free_count, "free_count", 1, i32), int(page_size),
-            int(tokens), _vector(lengths_out, "lengths_out", n, i32),
-            _vector(free_count_out, "free_count_out", 1, i32),
-            _vector(slots, "slots", int(tokens), torch.int64),
-            _vector(positions, "positions", int(tokens), i32),
-            _vector(cu_tokens, "cu_tokens", n + 1, i32), _vector(status, "status", 3, i32),
-            _stream(stream)))
+            _vec(lengths, "lengths", n, dev, i32), _vec(new_tokens, "new_tokens", n, dev, i32), n,
+            table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
+            _vec(free_count, "free_count", 1, dev, i32), int(page_size), tokens,
+            _vec(lengths_out, "lengths_out", n, dev, i32),
+            _vec(free_count_out, "free_count_out", 1, dev, i32),
+            _vec(slots, "slots", tokens, dev, torch.int64),
+            _vec(positions, "positions", tokens, dev, i32),
+            _vec(cu_tokens, "cu_tokens", n + 1, dev, i32), _vec(status, "status", 3, dev, i32),
+            st))
     return slots, positions, cu_tokens, lengths_out, free_count_out, status
 
 
@@ -666,47 +719,49 @@ def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, 
     """Push the pages of the requests with finished != 0 back on the stack
     free_pages (in place) and set their lengths to 0; returns (lengths_out,
     free_count_out), which may be lengths and free_count themselves."""
-    n = lengths.numel()
-    i32 = torch.int32
+    n, i32 = lengths.numel(), torch.int32
+    dev = _device(lengths, "lengths")
     if lengths_out is None:
         lengths_out = torch.empty(n, dtype=i32, device=lengths.device)
     if free_count_out is None:
         free_count_out = torch.empty(1, dtype=i32, device=lengths.device)
-    _same_device(lengths, finished=finished, block_table=block_table, free_pages=free_pages,
-                 free_count=free_count, lengths_out=lengths_out, free_count_out=free_count_out)
-    table, width = _table(block_table, n)
-    with torch.cuda.device(lengths.device):
+    table, width = _table(block_table, n, dev)
+    pool = free_pages.numel()
+    with _On(dev, stream) as st:
         _check(lib().ra_paged_release(
-            _vector(lengths, "lengths", n, i32), _vector(finished, "finished", n, i32), n, table,
-            width, _vector(free_pages, "free_pages", free_pages.numel(), i32),
-            free_pages.numel(), _vector(free_count, "free_count", 1, i32), int(page_size),
-            _vector(lengths_out, "lengths_out", n, i32),
-            _vector(free_count_out, "free_count_out", 1, i32), _stream(stream)))
+            _vec(lengths, "lengths", n, dev, i32), _vec(finished, "finished", n, dev, i32), n,
+            table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
+            _vec(free_count, "free_count", 1, dev, i32), int(page_size),
+            _vec(lengths_out, "lengths_out", n, dev, i32),
+            _vec(free_count_out, "free_count_out", 1, dev, i32), st))
     return lengths_out, free_count_out
 
 
-def _cache(t, name, kv_heads, d):
+def _cache(t, name, kv_heads, d, dev):
     """Pointer, page count, page size and page stride of a cache tensor
     [n_pages, page_size, kv_heads, d] (bf16, dense inside a page)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                         f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 4 or t.shape[2] != kv_heads or t.shape[3] != d:
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != kv_heads or shape[3] != d:
         raise ValueError(f"{name} must be [n_pages, page_size, {kv_heads}, {d}], "
-                         f"got {tuple(t.shape)}")
-    if t.shape[0] and not t[0].is_contiguous():
-        raise ValueError(f"{name}: a page must be dense (strides {t.stride()})")
-    page = t.shape[1] * kv_heads * d
-    return t.data_ptr(), t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else page
+                         f"got {tuple(shape)}")
+    n, ps = shape[0], shape[1]
+    st = t.stride()
+    if n and (st[3] != 1 or (kv_heads > 1 and st[2] != d) or (ps > 1 and st[1] != kv_heads * d)):
+        raise ValueError(f"{name}: a page must be dense (strides {st})")
+    return t.data_ptr(), n, ps, st[0] if n > 1 else ps * kv_heads * d
 
 
-def _caches(k_cache, v_cache, kv_heads, d):
-    kp, n, ps, ks = _cache(k_cache, "k_cache", kv_heads, d)
-    vp, vn, vps, vs = _cache(v_cache, "v_cache", kv_heads, d)
-    if (vn, vps) != (n, ps):
+def _caches(k_cache, v_cache, kv_heads, d, dev):
+    kp, n, ps, ks = _cache(k_cache, "k_cache", kv_heads, d, dev)
+    vp, vn, vps, vs = _cache(v_cache, "v_cache", kv_heads, d, dev)
+    if vn != n or vps != ps:
         raise ValueError("k_cache and v_cache must match in pages and page size")
     return kp, vp, n, ps, ks, vs
 
@@ -719,26 +774,25 @@ def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_we
     is written) at positions[t] (int32).  Returns q_out, dense like q."""
     T, heads, kv_heads, d = _qk_shapes(q, k)
     dt = _qkv_dtype(q)
-    if v.shape != k.shape or v.dtype != q.dtype:
+    if v.shape != k.shape or v.dtype is not q.dtype:
         raise ValueError("v must match k in shape and dtype")
     if q_out is None:
         q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
-    if q_out.shape != q.shape:
+    elif q_out.shape != q.shape:
         raise ValueError("q_out must match q in shape")
-    _same_device(q, k=k, v=v, phases=phases, k_cache=k_cache, v_cache=v_cache, slots=slots,
-                 positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out)
-    qp, qs = _rows(q, "q", heads, d)
-    kp, ks = _rows(k, "k", kv_heads, d)
-    vp, vs = _rows(v, "v", kv_heads, d)
-    kc, vc, n_pages, ps, kcs, vcs = _caches(k_cache, v_cache, kv_heads, d)
-    ph, rot = _phase_table(phases)
-    qw, kw, wt = _weight(q_weight, k_weight, d)
-    with torch.cuda.device(q.device):
+    dev, dtype = _device(q, "q"), q.dtype
+    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
+    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
+    vp, vs = _rows(v, "v", T, kv_heads, d, dev, dtype)
+    kc, vc, n_pages, ps, kcs, vcs = _caches(k_cache, v_cache, kv_heads, d, dev)
+    ph, rot = _phase_table(phases, dev)
+    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
+    with _On(dev, stream) as st:
         _check(lib().ra_paged_append(
-            qp, kp, vp, _dev(q_out, "q_out", q.dtype), kc, vc, T, d, heads, kv_heads, qs, ks, vs,
-            n_pages, ps, kcs, vcs, _vector(slots, "slots", T, torch.int64),
-            _vector(positions, "positions", T, torch.int32), rot, int(bool(interleaved)), ph,
-            float(mscale), qw, kw, wt, float(eps), dt, _stream(stream)))
+            qp, kp, vp, _arg(q_out, "q_out", dev, dtype), kc, vc, T, d, heads, kv_heads, qs, ks,
+            vs, n_pages, ps, kcs, vcs, _vec(slots, "slots", T, dev, torch.int64),
+            _vec(positions, "positions", T, dev, torch.int32), rot, int(bool(interleaved)), ph,
+            float(mscale), qw, kw, wt, float(eps), dt, st))
     return q_out
 
 
@@ -758,25 +812,27 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, win
     kv_heads = k_cache.shape[2]
     if cu_q is None and (T % n if n else T):
         raise ValueError(f"T={T} rows are not a multiple of {n} requests (and cu_q is None)")
+    f32 = torch.float32
     if out is None:
-        out = torch.empty((T, heads, d), dtype=torch.float32, device=q.device)
-    if lse is None:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
-    _state_shapes(lse, lse, out, T, heads, d)
-    if out.dtype not in (torch.float32, torch.bfloat16):
+        out = torch.empty((T, heads, d), dtype=f32, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError(f"out must have shape {(T, heads, d)}, got {tuple(out.shape)}")
+    elif out.dtype not in (f32, torch.bfloat16):
         raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
-    _same_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths,
-                 cu_q=cu_q, out=out, lse=lse)
-    kc, vc, n_pages, ps, ks, vs = _caches(k_cache, v_cache, kv_heads, d)
-    table, width = _table(block_table, n)
-    cu = _vector(cu_q, "cu_q", n + 1, torch.int32) if cu_q is not None else 0
-    with torch.cuda.device(q.device):
+    if lse is None:
+        lse = torch.empty((T, heads), dtype=f32, device=q.device)
+    elif tuple(lse.shape) != (T, heads):
+        raise ValueError(f"lse must have shape {(T, heads)}, got {tuple(lse.shape)}")
+    dev = _device(q, "q")
+    kc, vc, n_pages, ps, ks, vs = _caches(k_cache, v_cache, kv_heads, d, dev)
+    table, width = _table(block_table, n, dev)
+    cu = 0 if cu_q is None else _vec(cu_q, "cu_q", n + 1, dev, torch.int32)
+    with _On(dev, stream) as st:
         _check(lib().ra_paged_decode(
-            _dev(q, "q", torch.bfloat16), kc, vc, _dev(out, "out"),
-            _dev(lse, "lse", torch.float32), T, n, 0 if cu_q is not None or not n else T // n, cu,
-            table, width, _vector(lengths, "lengths", n, torch.int32), n_pages, ps, ks, vs,
-            int(window), d, heads, kv_heads, RA_BF16,
-            RA_BF16 if out.dtype == torch.bfloat16 else RA_F32, _stream(stream)))
+            _arg(q, "q", dev, torch.bfloat16), kc, vc, _arg(out, "out", dev, out.dtype),
+            _arg(lse, "lse", dev, f32), T, n, 0 if cu or not n else T // n, cu, table, width,
+            _vec(lengths, "lengths", n, dev, torch.int32), n_pages, ps, ks, vs, int(window), d,
+            heads, kv_heads, RA_BF16, RA_BF16 if out.dtype is torch.bfloat16 else RA_F32, st))
     return out, lse
 
 

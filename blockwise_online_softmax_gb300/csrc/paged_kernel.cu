@@ -22,6 +22,7 @@
 // the 16-wide side and 8 query rows as the other: a tcgen05 tile would be
 // 128 rows for the 4 or 8 there are, and its S -> P round trip through TMEM
 // is the longer chain.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -666,12 +667,24 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   if (threadIdx.x == 0) a.lse[row] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
 }
 
+// Opts a kernel into its dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K* kernel, uint32_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <int D, int NT>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(Cfg<D>::SMEM));
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(paged_decode_kernel<D, NT>, Cfg<D>::SMEM, done);
   if (e != cudaSuccess) return e;
   paged_decode_kernel<D, NT><<<ctas, kThreads, Cfg<D>::SMEM, st>>>(tk, tv, a);
   return cudaGetLastError();

@@ -400,13 +400,6 @@ __global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const Rop
   if (dst) dst[i % d] = x;
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 template <typename T, bool APPEND>
 cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;

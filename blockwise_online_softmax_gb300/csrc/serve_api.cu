@@ -1,6 +1,7 @@
 // Host side of the serving and training calls around the attention kernels
 // (declared in include/ra.h): argument checks, scratch and launches.  Host
 // code only.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -12,6 +13,22 @@
 #include "serve_internal.h"
 
 using namespace ra::api;
+
+namespace ra {
+
+int sm_count() {
+  constexpr int kMax = 64;
+  static std::atomic<int> known[kMax];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  int n = dev < kMax ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  if (dev < kMax) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace ra
 
 namespace {
 
@@ -419,15 +436,12 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   // Without pages no load is ever issued; the maps still need an address.
   if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
-  int dev = 0, ctas = 152;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  const int ctas = ra::sm_count();
   const int rt = ra::paged_row_tile(a);
   const size_t rows = static_cast<size_t>(2) * ctas * rt;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* part = nullptr;
-  e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
+  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));

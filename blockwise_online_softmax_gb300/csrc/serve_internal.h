@@ -9,6 +9,9 @@
 
 namespace ra {
 
+// SMs of the current device (looked up once per device).
+int sm_count();
+
 // ------------------------------------------------------------------ pages
 struct ExtendArgs {
   const int* lengths;     // [n_req] tokens cached before
