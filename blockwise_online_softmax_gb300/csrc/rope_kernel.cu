@@ -190,9 +190,10 @@ __device__ __forceinline__ float row_sum(float v) {
 // row costs two products and a sum per column, and one exchange of its packed
 // columns with the partner lane.
 constexpr int kBatch = 4;
+constexpr int kFwdCtas = 3;  // per SM
 
 template <typename T, int D, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32) rope_forward_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kFwdCtas) rope_forward_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31, col = 8 * (lane % LPR), sub = lane / LPR;
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
@@ -289,10 +290,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_forward_kernel(const RopeArg
 // Backward.  Groups as in the forward; the weight gradients are summed in
 // the lanes, over the CTA's warps in shared memory, and written as one
 // partial sum per CTA, so their order is fixed.
-constexpr int kGradBatch = 2;
+constexpr int kGradBatch = 3;
+constexpr int kGradCtas = 2;  // per SM
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) rope_backward_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   __shared__ float s_dw[kWarps][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -410,7 +412,7 @@ cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
   const long long want = (16LL * sm_count() + a.T - 1) / a.T, most_parts = (groups + kBatch - 1) / kBatch;
   a.parts = static_cast<int>(want < most_parts ? want : most_parts);
   long long ctas = (a.T * a.parts + kWarps - 1) / kWarps;
-  const long long most = 8LL * sm_count();
+  const long long most = static_cast<long long>(kFwdCtas) * sm_count();  // one wave
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
   if (d == 128) {
     if (a.interleaved) rope_forward_kernel<T, 128, true, APPEND><<<grid, kWarps * 32, 0, st>>>(a);
@@ -438,7 +440,7 @@ cudaError_t backward_t(const RopeArgs& a, int d, cudaStream_t st) {
 }  // namespace
 
 int rope_grad_ctas(const RopeArgs& a) {
-  const long long ctas = (a.T + kWarps - 1) / kWarps, most = 4LL * sm_count();
+  const long long ctas = (a.T + kWarps - 1) / kWarps, most = static_cast<long long>(kGradCtas) * sm_count();
   return static_cast<int>(ctas < 1 ? 1 : (ctas < most ? ctas : most));
 }
 
