@@ -14,14 +14,16 @@
 // finished there; one cut by a border between CTAs leaves a partial state
 // (m, l, O~) on each side, and a second launch joins them in CTA order.
 //
-// One warp feeds a ring of stages with TMA (a page, or half a page of 256,
-// is a box of one KV head; lane p looks up and requests page p of the
-// tile).  Eight warps take 16 keys of the tile each and keep their own
-// running (m, l, O~), so nothing in the loop waits for another warp.  The
-// products are mma.sync m16n8k16 with the keys, then the columns of V, as
-// the 16-wide side and 8 query rows as the other: a tcgen05 tile would be
-// 128 rows for the 4 or 8 there are, and its S -> P round trip through TMEM
-// is the longer chain.
+// Two warps feed a ring of stages with TMA, one K, one V (a page, or half a
+// page of 256, is a box of one KV head; lane p looks up and requests page p of
+// the tile).  The K warp also walks the items ahead of everybody, leaves a
+// record of each in shared memory and copies its query rows there.  Eight
+// warps consume, four to a tile, two tiles at a time; each takes 32 keys of
+// its tile and keeps its own running (m, l, O~), so nothing in the loop waits
+// for another warp, and the states meet at the item's end.  The products are
+// mma.sync m16n8k16 with the keys, then the columns of V, as the 16-wide side
+// and 8 query rows as the other: a tcgen05 tile would be 128 rows for the 4 or
+// 8 there are, and its S -> P round trip through TMEM is the longer chain.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -40,21 +42,41 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int BT = 128;          // keys per tile
 constexpr int kCons = 8;         // consumer warps
-constexpr int kThreads = 32 * (kCons + 1);
+constexpr int kThreads = 32 * (kCons + 2);
+constexpr int kItems = 4;        // item records and query tiles in flight
 constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
 
-template <int D>
+template <int D, int NT>
 struct Cfg {
   static constexpr int NCH = D / 64;
+  static constexpr int RT = 8 * NT;              // query rows of an item
   static constexpr uint32_t TILE = BT * D * 2;
-  static constexpr int NST = D == 128 ? 3 : 6;  // stages of one K and one V tile
-  static constexpr uint32_t OFF_BUF = NST * 2 * TILE;             // [kCons][8][D] fp32
-  static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 8 * D * 4;  // [2][kCons][16] fp32
-  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * kCons * 16 * 4;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 3 * NST * 8;
-  static constexpr uint32_t SMEM = OFF_MISC + 32 + 1024;
+  static constexpr int NST = D == 128 ? 3 : 6;   // stages of one K and one V tile
+  static constexpr uint32_t QT = RT * D * 2;     // query rows, 16-byte chunks swizzled
+  static constexpr uint32_t OFF_Q = NST * 2 * TILE;
+  static constexpr uint32_t OFF_BUF = OFF_Q + kItems * QT;         // [4][8][D] fp32
+  static constexpr uint32_t OFF_ML = OFF_BUF + 4 * 8 * D * 4;      // [2][kCons][RT] fp32
+  static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * kCons * RT * 4;
+  static constexpr uint32_t OFF_BAR = OFF_ITEM + kItems * 64;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + (3 * NST + 2 * kItems) * 8;
+  static constexpr uint32_t SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM + 512 <= 232448, "shared memory budget");
 };
+
+// An item, or the part of it that a CTA has, as its consumers need it.
+// Positions are relative to the item's first key tile.
+struct Item {
+  int rr0, rr1;    // query rows: row rr is token rr / g, head kh * g + rr % g
+  int row0;        // q row of the request's first token
+  int kh;
+  int end0;        // keys that token 0 of the request sees: [.., end0)
+  int base;        // position of the item's first key tile
+  int lo, hi;      // keys that any row sees
+  int k0;          // first key tile here
+  int tiles;       // key tiles here
+  int slot;        // partial slot, or -1: the item is whole
+};
+static_assert(sizeof(Item) <= 64, "record size");
 
 // What a CTA that starts a cut item leaves for the joining launch.
 struct Cut {
@@ -93,6 +115,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 16 bytes to shared memory, zeros when `bytes` is 0; the arrival on `bar`
+// follows when the calling thread's copies have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -101,62 +132,59 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // ------------------------------------------------------------------ the work list
 struct Request {
-  int row0;       // first row of q
-  int n;          // new tokens
-  long long len;  // keys, the new tokens' included
+  int row0;  // first row of q
+  int n;     // new tokens
+  int len;   // keys, the new tokens' included
 };
 
 __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
   Request q;
   if (a.cu_q) {
     // A malformed cu_q must not reach outside q and out.
-    const long long x = a.cu_q[r], y = a.cu_q[r + 1];
-    const long long lo = x < 0 ? 0 : (x > a.T ? a.T : x), hi = y < lo ? lo : (y > a.T ? a.T : y);
-    q.row0 = static_cast<int>(lo);
-    q.n = static_cast<int>(hi - lo);
+    const int T = static_cast<int>(a.T), x = a.cu_q[r], y = a.cu_q[r + 1];
+    q.row0 = x < 0 ? 0 : (x > T ? T : x);
+    q.n = (y < q.row0 ? q.row0 : (y > T ? T : y)) - q.row0;
   } else {
-    q.row0 = static_cast<int>(r * a.n_q);
+    q.row0 = r * static_cast<int>(a.n_q);
     q.n = static_cast<int>(a.n_q);
   }
-  const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
-  const long long len = a.lengths[r];
+  const int most = a.max_pages << a.page_shift, len = a.lengths[r];
   q.len = len < 0 ? 0 : (len > most ? most : len);
   return q;
 }
 
-// Keys [lo, hi) that token j of the request sees.
-__device__ __forceinline__ long long key_end(const Request& q, int j) {
-  const long long hi = q.len - q.n + j + 1;
-  return hi < 0 ? 0 : hi;
+// Token j of the request sees keys [begin, end).
+__device__ __forceinline__ int key_end(const Request& q, int j) {
+  const int e = q.len - q.n + j + 1;
+  return e < 0 ? 0 : e;
 }
-__device__ __forceinline__ long long key_begin(const PagedArgs& a, long long hi) {
-  return a.window > 0 && hi > a.window ? hi - a.window : 0;
+__device__ __forceinline__ int key_begin(const PagedArgs& a, int end) {
+  return a.window > 0 && end > a.window ? end - static_cast<int>(a.window) : 0;
 }
 
 // Row tile rt of a request: rows [rr0, rr1), keys [lo, hi) over all of them,
 // key tiles [t0, t0 + nt) (one, with no key, when there is none).
 struct RowTile {
   int rr0, rr1;
-  long long lo, hi;
-  long long t0;
-  int nt;
+  int lo, hi;
+  int t0, nt;
 };
 
 __device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const Request& q, int g, int RT,
                                             int rt) {
   RowTile t;
   t.rr0 = rt * RT;
-  const long long all = static_cast<long long>(q.n) * g, end = static_cast<long long>(t.rr0) + RT;
-  t.rr1 = static_cast<int>(end < all ? end : all);
+  const int all = q.n * g;
+  t.rr1 = t.rr0 + RT < all ? t.rr0 + RT : all;
   t.hi = key_end(q, (t.rr1 - 1) / g);
   t.lo = key_begin(a, key_end(q, t.rr0 / g));
   t.t0 = t.lo / BT;
-  t.nt = t.hi > t.lo ? static_cast<int>((t.hi + BT - 1) / BT - t.t0) : 1;
+  t.nt = t.hi > t.lo ? (t.hi - 1) / BT + 1 - t.t0 : 1;
   return t;
 }
 
 __device__ __forceinline__ int row_tiles(const Request& q, int g, int RT) {
-  return static_cast<int>((static_cast<long long>(q.n) * g + RT - 1) / RT);
+  return (q.n * g + RT - 1) / RT;
 }
 
 __device__ __forceinline__ long long request_units(const PagedArgs& a, int r, int g, int RT) {
@@ -273,13 +301,13 @@ __device__ __forceinline__ int cta_of(long long u, const Run& run) {
 }
 
 // ------------------------------------------------------------------ the kernel
-// NT: 8-row groups of query rows; a row tile has RT = 8 NT rows.
+// NT: 8-row groups of query rows of an item.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedArgs a) {
-  using C = Cfg<D>;
-  constexpr int RT = 8 * NT;
+  using C = Cfg<D, NT>;
+  constexpr int RT = C::RT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -287,15 +315,22 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
   auto vfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NST + s); };
   auto empty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NST + s); };
+  auto ifull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + s); };
+  auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + kItems + s); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
   Cut* cuts = static_cast<Cut*>(a.cuts);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(kfull(s), 1);
       mbar_init(vfull(s), 1);
       mbar_init(empty(s), kCons);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(ifull(s), 33);  // every lane's copies, and the record
+      mbar_init(iempty(s), kCons);
     }
     *abort_flag = *reinterpret_cast<volatile int*>(&g_paged_status) != 0 ? 1 : 0;
     fence_mbar_init();
@@ -303,26 +338,73 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
   const Run run = find_run(a, g, RT);  // synchronizes
   if (run.first >= run.last) return;
-  Walk w;
-  w.start(a, g, RT, run.r, run.x);
   const long long lim = a.wait_limit;
-  long long u = run.first;  // unit of the item's tile w.k
+  Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
-  if (warp == kCons) {
-    // ---------------------------------------------------------------- producer
+  if (warp >= kCons) {
+    // ---------------------------------------------------------------- producers
+    const bool is_k = warp == kCons;
+    const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
     const int sh = a.page_shift;
     const int rows = sh < 7 ? 1 << sh : BT;  // of a box
     const int npg = BT / rows;
     const uint32_t box = static_cast<uint32_t>(rows) * 128u;
+    auto full = [&](int s) -> uint32_t { return is_k ? kfull(s) : vfull(s); };
+    Walk w;
+    w.start(a, g, RT, run.r, run.x);
+    long long u = run.first;
     bool ok = true;
-    int i = 0;  // tiles requested
+    int i = 0;   // tiles requested
+    int it = 0;  // items begun
     while (ok && u < run.last) {
-      const long long p_end = (w.t.hi + (1LL << sh) - 1) >> sh;
-      const long long p_begin = w.t.lo >> sh;
+      const long long left = run.last - u;
+      const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
+      if (is_k) {
+        const int s = it % kItems;
+        if (it >= kItems) {
+          ok = wait_bar(iempty(s), (static_cast<uint32_t>(it / kItems) & 1u) ^ 1u, abort_flag,
+                        &g_paged_status, 0x84, lim);
+          ok = __all_sync(kAll, ok);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const long long item0 = u - w.k;
+          const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
+          const int me = static_cast<int>(blockIdx.x);
+          Item x;
+          x.rr0 = w.t.rr0;
+          x.rr1 = w.t.rr1;
+          x.row0 = w.q.row0;
+          x.kh = w.kh;
+          x.base = w.t.t0 * BT;
+          x.end0 = w.q.len - w.q.n + 1 - x.base;
+          x.lo = w.t.lo - x.base;
+          x.hi = w.t.hi - x.base;
+          x.k0 = w.k;
+          x.tiles = tiles;
+          x.slot = c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0);
+          items[s] = x;
+          if (c0 != c1 && me == c0) cuts[me] = Cut{c1, x.row0, x.rr0, x.rr1 - x.rr0, x.kh};
+          mbar_arrive(ifull(s));
+        }
+        // Chunk c of row r at c ^ (r % 8): the ldmatrix rows of a column
+        // block fall into different banks.
+#pragma unroll
+        for (int x = lane; x < RT * D / 8; x += 32) {
+          const int r = x / (D / 8), c = x % (D / 8), rr = w.t.rr0 + r;
+          const bool in = rr < w.t.rr1;
+          const long long row = in ? static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g : 0;
+          copy16(sb + C::OFF_Q + s * C::QT + r * (D * 2) + ((c ^ (r & 7)) << 4),
+                 static_cast<const __nv_bfloat16*>(a.q) + row * D + c * 8, in ? 16u : 0u);
+        }
+        copies_arrive(ifull(s));
+        ++it;
+      }
+      const int p_end = w.t.hi > w.t.lo ? ((w.t.hi - 1) >> sh) + 1 : 0, p_begin = w.t.lo >> sh;
       const int* table = a.block_table + static_cast<long long>(w.r) * a.max_pages;
-      for (; w.k < w.t.nt && u < run.last; ++w.k, ++u, ++i) {
-        const long long key0 = (w.t.t0 + w.k) * BT;
-        const long long p = (key0 >> sh) + lane;
+      for (int k = 0; k < tiles; ++k, ++i) {
+        const int key0 = (w.t.t0 + w.k + k) * BT;
+        const int p = (key0 >> sh) + lane;
         int page = -1;
         if (lane < npg && p >= p_begin && p < p_end) page = table[p];
         const bool have = page >= 0 && page < a.n_pages;
@@ -334,79 +416,78 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           ok = __all_sync(kAll, ok);
           if (!ok) break;
         }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(kfull(s), n * box * C::NCH);
-          mbar_arrive_expect_tx(vfull(s), n * box * C::NCH);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(full(s), n * box * C::NCH);
         __syncwarp();
         if (have) {
-          const uint32_t dst = sb + s * 2 * C::TILE + lane * box;
-          const int row = static_cast<int>(key0 & ((1LL << sh) - 1));
+          const uint32_t dst = sb + s * 2 * C::TILE + (is_k ? 0 : C::TILE) + lane * box;
+          const int row = key0 & ((1 << sh) - 1);
 #pragma unroll
           for (int ch = 0; ch < C::NCH; ++ch)
-            tma_load_4d(dst + ch * CHB, &tmK, kfull(s), ch * 64, w.kh, row, page);
-#pragma unroll
-          for (int ch = 0; ch < C::NCH; ++ch)
-            tma_load_4d(dst + C::TILE + ch * CHB, &tmV, vfull(s), ch * 64, w.kh, row, page);
+            tma_load_4d(dst + ch * CHB, tm, full(s), ch * 64, w.kh, row, page);
         }
       }
+      u += tiles;
       if (ok && u < run.last) w.next(a, g, RT);
     }
     if (!ok) {  // let the copies in flight land before the CTA leaves
       volatile int no_abort = 0;
-      for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j) {
-        wait_bar(kfull(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
-        wait_bar(vfull(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
-      }
+      for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j)
+        wait_bar(full(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
 
   // ------------------------------------------------------------------ consumers
   // After a wait that gave up, a warp runs on without waiting (the status
-  // word says that the results are void), so the barriers still match.
+  // word says that the results are void), so the barriers still match; it
+  // leaves at the next item.
   float* buf = reinterpret_cast<float*>(smem + C::OFF_BUF);
   float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
-  float* s_l = s_m + kCons * 16;
+  float* s_l = s_m + kCons * RT;
   const float sl2 = a.scale_log2;
   bool ok = true;
-  int i = 0;
-  // ldmatrix addresses of this lane inside a 64-column chunk of a tile: K
-  // rows are keys (8 x 8 blocks: keys 0-7 / 8-15 first, then columns), V the
-  // same blocks with columns first, read transposed.
-  const int kr = warp * 16 + (lane & 15), kc0 = lane >> 4;
-  const int vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
-  while (u < run.last) {
-    // The item's query rows: lane holds rows 8 nt + lane / 4 as the B side.
-    uint32_t bq[NT][D / 16][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int rr = w.t.rr0 + 8 * nt + (lane >> 2);
-      const bool in = rr < w.t.rr1;
-      const long long row = static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                                static_cast<const __nv_bfloat16*>(a.q) + row * D) + (lane & 3);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        bq[nt][kk][0] = in ? src[kk * 8] : 0u;
-        bq[nt][kk][1] = in ? src[kk * 8 + 4] : 0u;
-      }
-    }
+  // Warps 0-3 take the CTA's even tiles, warps 4-7 the odd ones.  Every warp
+  // waits for and releases every tile all the same: a wait names its phase by
+  // parity alone, so no warp may be a whole turn of the ring away from another.
+  const int grp = warp >> 2;
+  int turn = 0;              // parity of the next tile
+  int st = 0;                // its stage and phase
+  uint32_t par = 0;
+  long long u = run.first;
+  // ldmatrix addresses inside a 64-column chunk of a tile, for the warp's
+  // first 16 keys: K rows are keys (8 x 8 blocks: keys 0-7 / 8-15 first, then
+  // columns), V the same blocks with columns first, read transposed.
+  const int key_w = (warp & 3) * 32;
+  const int kr = key_w + (lane & 15), kc0 = lane >> 4;
+  const int vr = key_w + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
+  for (int it = 0; u < run.last; ++it) {
+    const int is = it % kItems;
+    ok = ok && wait_bar(ifull(is), static_cast<uint32_t>(it / kItems) & 1u, abort_flag,
+                        &g_paged_status, 0x85, lim);
+    // All consumer warps leave together, or none: nobody waits at a barrier
+    // for a warp that has gone.
+    if (!named_bar_and(1, 32 * kCons, ok)) return;
+    const Item item = items[is];
     // Keys [lo, hi) of the lane's rows 8 nt + 2 (lane & 3) + {0, 1}; the keys
-    // that every row of the tile sees are [lo_all, hi_all).
+    // that every row of the item sees are [lo_all, hi_all).
+    const int win = static_cast<int>(a.window);
+    auto end_of = [&](int rr) {
+      const int e = item.end0 + rr / g;
+      return e < -item.base ? -item.base : e;
+    };
+    auto begin_of = [&](int end) {
+      return win > 0 && end + item.base > win ? end - win : -item.base;
+    };
     int rlo[NT][2], rhi[NT][2];
-    const long long base = w.t.t0 * BT;
-    const int hi = static_cast<int>(w.t.hi - base), lo = static_cast<int>(w.t.lo - base);
-    const int hi_all = static_cast<int>(key_end(w.q, w.t.rr0 / g) - base);
-    const int lo_all = static_cast<int>(key_begin(a, key_end(w.q, (w.t.rr1 - 1) / g)) - base);
+    const int hi_all = end_of(item.rr0), lo_all = begin_of(end_of(item.rr1 - 1));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int rr = w.t.rr0 + 8 * nt + 2 * (lane & 3) + c;
-        const long long e = key_end(w.q, (rr < w.t.rr1 ? rr : w.t.rr1 - 1) / g);
-        rhi[nt][c] = static_cast<int>(e - base);
-        rlo[nt][c] = static_cast<int>(key_begin(a, e) - base);
+        const int rr = item.rr0 + 8 * nt + 2 * (lane & 3) + c;
+        rhi[nt][c] = end_of(rr < item.rr1 ? rr : item.rr1 - 1);
+        rlo[nt][c] = begin_of(rhi[nt][c]);
       }
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
@@ -416,44 +497,58 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
     }
-    const long long item0 = u - w.k;  // the item's first unit
-    for (; w.k < w.t.nt && u < run.last; ++w.k, ++u, ++i) {
-      const int s = i % C::NST;
-      const uint32_t par = static_cast<uint32_t>(i / C::NST) & 1u;
-      const uint32_t kb = sb + s * 2 * C::TILE, vb = kb + C::TILE;
-      const int k0 = w.k * BT + warp * 16;  // the warp's first key, from base
-      ok = ok && wait_bar(kfull(s), par, abort_flag, &g_paged_status, 0x82, lim);
+    // Query rows as the B side: one ldmatrix gives two 16-column steps.
+    const uint32_t qb = sb + C::OFF_Q + is * C::QT + (lane & 7) * (D * 2);
+    const int qc0 = lane >> 3, qx = lane & 7;
+    for (int k = 0; k < item.tiles; ++k) {
+      const uint32_t kb = sb + st * 2 * C::TILE, vb = kb + C::TILE;
+      const int k0 = (item.k0 + k) * BT + key_w;  // the warp's first key
+      ok = ok && wait_bar(kfull(st), par, abort_flag, &g_paged_status, 0x82, lim);
       ok = __all_sync(kAll, ok);
-      const bool some = k0 < hi && k0 + 16 > lo;
-      float sc[NT][4];
-      uint32_t pb[NT][3][2];
+      const bool some = turn == grp && k0 < item.hi && k0 + 32 > item.lo;
+      float sc[NT][2][4];
+      uint32_t pb[NT][2][3][2];
       float al[NT][2];
       if (some) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t af[4];
-          const int ch = (2 * kk + kc0) & 7;
-          ldsm4(kb + (kk >> 2) * CHB + kr * 128 + ((ch ^ (kr & 7)) << 4), af);
+          for (int b = 0; b < 2; ++b) sc[nt][b][0] = sc[nt][b][1] = sc[nt][b][2] = sc[nt][b][3] = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], af, bq[nt][kk][0], bq[nt][kk][1]);
+        for (int k2 = 0; k2 < D / 32; ++k2) {
+          uint32_t bq[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            ldsm4(qb + nt * 8 * (D * 2) + (((4 * k2 + qc0) ^ qx) << 4), bq[nt]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int kk = 2 * k2 + h, ch = (2 * kk + kc0) & 7;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint32_t af[4];
+              ldsm4(kb + (kk >> 2) * CHB + (kr + 16 * b) * 128 + ((ch ^ (kr & 7)) << 4), af);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][b], af, bq[nt][2 * h], bq[nt][2 * h + 1]);
+            }
+          }
         }
-        if (k0 < lo_all || k0 + 16 > hi_all) {
+        if (k0 < lo_all || k0 + 32 > hi_all) {
           const int k1 = k0 + (lane >> 2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int key = k1 + (c >> 1) * 8;
-              if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[nt][c] = -INFINITY;
-            }
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int key = k1 + 16 * b + (c >> 1) * 8;
+                if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[nt][b][c] = -INFINITY;
+              }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(sc[nt][c], sc[nt][c + 2]);
+            float x = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]), fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
@@ -461,10 +556,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const float ref = mn == -INFINITY ? 0.f : mn;
             al[nt][c] = ex2(m[nt][c] - ref);
             m[nt][c] = mn;
-            const float p0 = ex2(fmaf(sc[nt][c], sl2, -ref)), p1 = ex2(fmaf(sc[nt][c + 2], sl2, -ref));
-            l[nt][c] = fmaf(l[nt][c], al[nt][c], p0 + p1);
-            sc[nt][c] = p0;
-            sc[nt][c + 2] = p1;
+            float sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float p0 = ex2(fmaf(sc[nt][b][c], sl2, -ref));
+              const float p1 = ex2(fmaf(sc[nt][b][c + 2], sl2, -ref));
+              sum += p0 + p1;
+              sc[nt][b][c] = p0;
+              sc[nt][b][c + 2] = p1;
+            }
+            l[nt][c] = fmaf(l[nt][c], al[nt][c], sum);
           }
         // P as three bf16 terms (8 + 8 + 8 bits): the product with V then has
         // the weights' fp32 value, which an fp32 output shows; one bf16 term
@@ -472,57 +573,71 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float x = sc[nt][2 * half], y = sc[nt][2 * half + 1];
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const uint32_t h = bf16x2_rn(x, y);
-              pb[nt][term][half] = transpose8x8(h);
-              x -= __uint_as_float(h << 16);
-              y -= __uint_as_float(h & 0xffff0000u);
+            for (int half = 0; half < 2; ++half) {
+              float x = sc[nt][b][2 * half], y = sc[nt][b][2 * half + 1];
+#pragma unroll
+              for (int term = 0; term < 3; ++term) {
+                const uint32_t h = bf16x2_rn(x, y);
+                pb[nt][b][term][half] = transpose8x8(h);
+                x -= __uint_as_float(h << 16);
+                y -= __uint_as_float(h & 0xffff0000u);
+              }
             }
-          }
       }
-      ok = ok && wait_bar(vfull(s), par, abort_flag, &g_paged_status, 0x83, lim);
+      ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_status, 0x83, lim);
       ok = __all_sync(kAll, ok);
       if (some) {
-        const bool edge = k0 < lo || k0 + 16 > hi;
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // V rows outside [lo, hi) may hold anything
+        const bool edge = k0 < item.lo || k0 + 32 > item.hi;
+        uint32_t keep[2][2];  // V rows outside [lo, hi) may hold anything
         if (edge) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int key = k0 + 8 * half + 2 * (lane & 3);
-            keep[half] = (key >= lo && key < hi ? 0xffffu : 0u) |
-                         (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
-          }
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int key = k0 + 16 * b + 8 * half + 2 * (lane & 3);
+              keep[b][half] = (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
+                              (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
+            }
         }
 #pragma unroll
         for (int dm = 0; dm < D / 16; ++dm) {
-          uint32_t af[4];
+          uint32_t af[2][4];
           const int ch = (2 * dm + vc0) & 7;
-          ldsm4_t(vb + (dm >> 2) * CHB + vr * 128 + ((ch ^ (vr & 7)) << 4), af);
-          if (edge) {
-            af[0] &= keep[0];
-            af[1] &= keep[0];
-            af[2] &= keep[1];
-            af[3] &= keep[1];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            ldsm4_t(vb + (dm >> 2) * CHB + (vr + 16 * b) * 128 + ((ch ^ (vr & 7)) << 4), af[b]);
+            if (edge) {
+              af[b][0] &= keep[b][0];
+              af[b][1] &= keep[b][0];
+              af[b][2] &= keep[b][1];
+              af[b][3] &= keep[b][1];
+            }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // The tile's product apart, small terms first, then one rounded
             // fp32 step: the tensor core's own accumulation truncates.
             float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(t, af, pb[nt][2][0], pb[nt][2][1]);
-            mma16816(t, af, pb[nt][1][0], pb[nt][1][1]);
-            mma16816(t, af, pb[nt][0][0], pb[nt][0][1]);
+#pragma unroll
+            for (int term = 2; term >= 0; --term)
+#pragma unroll
+              for (int b = 0; b < 2; ++b) mma16816(t, af[b], pb[nt][b][term][0], pb[nt][b][term][1]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[nt][dm][c] = fmaf(o[nt][dm][c], al[nt][c & 1], t[c]);
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
+      if (lane == 0) mbar_arrive(empty(st));
+      turn ^= 1;
+      if (++st == C::NST) {
+        st = 0;
+        par ^= 1u;
+      }
     }
+    u += item.tiles;
     // ---------------------------------------------------------------- the warps' states meet
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -533,55 +648,76 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         x += __shfl_xor_sync(kAll, x, 8);
         x += __shfl_xor_sync(kAll, x, 16);
         if (lane < 4) {
-          s_m[warp * 16 + 8 * nt + 2 * lane + c] = m[nt][c];
-          s_l[warp * 16 + 8 * nt + 2 * lane + c] = x;
+          s_m[warp * RT + 8 * nt + 2 * lane + c] = m[nt][c];
+          s_l[warp * RT + 8 * nt + 2 * lane + c] = x;
         }
       }
     named_bar_sync(1, 32 * kCons);
-    const long long item1 = item0 + w.t.nt;
-    const int c0 = cta_of(item0, run), c1 = cta_of(item1 - 1, run);
-    const bool whole = c0 == c1;
-    const int slot = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
-    if (!whole && static_cast<int>(blockIdx.x) == c0 && tid == 0)
-      cuts[blockIdx.x] = Cut{c1, w.q.row0, w.t.rr0, w.t.rr1 - w.t.rr0, w.kh};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       if (nt > 0) named_bar_sync(1, 32 * kCons);  // the sums of group nt - 1 are read
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int r = 2 * (lane & 3) + c;
         float mx = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * 16 + 8 * nt + r]);
+        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * RT + 8 * nt + 2 * (lane & 3) + c]);
         const float e = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mx);
-        // Column d of row r at d ^ 8 (r / 2): the four row pairs of a store
-        // fall into different banks.
-        float* dst = buf + (warp * 8 + r) * D;
-        const int sw = (r >> 1) << 3;
 #pragma unroll
         for (int dm = 0; dm < D / 16; ++dm) {
-          dst[(dm * 16 + (lane >> 2)) ^ sw] = o[nt][dm][c] * e;
-          dst[(dm * 16 + 8 + (lane >> 2)) ^ sw] = o[nt][dm][c + 2] * e;
+          o[nt][dm][c] *= e;
+          o[nt][dm][c + 2] *= e;
         }
       }
-      // The thread's sums: row r, four columns.
+      // Warps 4-7 hand theirs to warps 0-3, lane by lane, ...
+      float* mine = buf + (warp & 3) * 8 * D;
+      if (warp >= 4) {
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm)
+          *reinterpret_cast<float4*>(mine + (dm * 32 + lane) * 4) =
+              make_float4(o[nt][dm][0], o[nt][dm][1], o[nt][dm][2], o[nt][dm][3]);
+      }
+      // ... and the thread's sums below: row r, four columns.
       constexpr int PT = 8 * D / 4;  // float4s of the group
       const int r = tid / (D / 4), d0 = (tid % (D / 4)) * 4;
-      const int rr = w.t.rr0 + 8 * nt + r;
+      const int rr = item.rr0 + 8 * nt + r;
       float mx = -INFINITY, lt = 0.f;
       if (tid < PT) {
 #pragma unroll
-        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * 16 + 8 * nt + r]);
+        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * RT + 8 * nt + r]);
         const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
         for (int x = 0; x < kCons; ++x)
-          lt = fmaf(s_l[x * 16 + 8 * nt + r], ex2(s_m[x * 16 + 8 * nt + r] - ref), lt);
+          lt = fmaf(s_l[x * RT + 8 * nt + r], ex2(s_m[x * RT + 8 * nt + r] - ref), lt);
       }
       named_bar_sync(1, 32 * kCons);
-      if (tid < PT && rr < w.t.rr1) {
+      if (warp < 4) {
+#pragma unroll
+        for (int dm = 0; dm < D / 16; ++dm) {
+          const float4 z = *reinterpret_cast<const float4*>(mine + (dm * 32 + lane) * 4);
+          o[nt][dm][0] += z.x;
+          o[nt][dm][1] += z.y;
+          o[nt][dm][2] += z.z;
+          o[nt][dm][3] += z.w;
+        }
+        __syncwarp();
+        // Column d of row r at d ^ 8 (r / 2): the four row pairs of a store
+        // fall into different banks.
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int sw = (lane & 3) << 3;
+          float* dst = mine + (2 * (lane & 3) + c) * D;
+#pragma unroll
+          for (int dm = 0; dm < D / 16; ++dm) {
+            dst[(dm * 16 + (lane >> 2)) ^ sw] = o[nt][dm][c];
+            dst[(dm * 16 + 8 + (lane >> 2)) ^ sw] = o[nt][dm][c + 2];
+          }
+        }
+      }
+      named_bar_sync(1, 32 * kCons);
+      if (tid < PT && rr < item.rr1) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int x = 0; x < kCons; ++x) {
+        for (int x = 0; x < 4; ++x) {
           const float4 z = *reinterpret_cast<const float4*>(
               buf + (x * 8 + r) * D + (d0 ^ ((r >> 1) << 3)));
           y.x += z.x;
@@ -589,8 +725,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           y.z += z.z;
           y.w += z.w;
         }
-        if (whole) {
-          const long long row = static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g;
+        if (item.slot < 0) {
+          const long long row = static_cast<long long>(item.row0 + rr / g) * a.heads + item.kh * g + rr % g;
           const float inv = lt > 0.f ? 1.f / lt : 0.f;
           if (a.out_bf16) {
             const uint2 h = make_uint2(bf16x2_rn(y.x * inv, y.y * inv), bf16x2_rn(y.z * inv, y.w * inv));
@@ -601,7 +737,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           }
           if (d0 == 0) a.lse[row] = lt > 0.f ? mx * kLn2 + logf(lt) : -INFINITY;
         } else {
-          const int pr = slot * RT + 8 * nt + r;
+          const int pr = item.slot * RT + 8 * nt + r;
           *reinterpret_cast<float4*>(a.po + static_cast<long long>(pr) * D + d0) = y;
           if (d0 == 0) {
             a.pm[pr] = mx;
@@ -610,7 +746,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
       }
     }
-    if (u < run.last) w.next(a, g, RT);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(iempty(is));
   }
 }
 
@@ -623,6 +760,7 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   constexpr int CPL = D / 32;
   __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][D];
   const int c = blockIdx.x, r = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel runs
   const Cut cut = static_cast<const Cut*>(a.cuts)[c];
   if (cut.last < 0 || r >= cut.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -684,9 +822,9 @@ template <int D, int NT>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(paged_decode_kernel<D, NT>, Cfg<D>::SMEM, done);
+  cudaError_t e = allow_smem(paged_decode_kernel<D, NT>, Cfg<D, NT>::SMEM, done);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, NT><<<ctas, kThreads, Cfg<D>::SMEM, st>>>(tk, tv, a);
+  paged_decode_kernel<D, NT><<<ctas, kThreads, Cfg<D, NT>::SMEM, st>>>(tk, tv, a);
   return cudaGetLastError();
 }
 
@@ -709,10 +847,17 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_til
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile));
-  if (d == 128) paged_combine_kernel<128><<<grid, 32 * kJoin, 0, st>>>(a, row_tile);
-  else paged_combine_kernel<64><<<grid, 32 * kJoin, 0, st>>>(a, row_tile);
-  return cudaGetLastError();
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile));
+  cfg.blockDim = dim3(32 * kJoin);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return d == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, a, row_tile)
+                  : cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, a, row_tile);
 }
 
 cudaError_t take_paged_status(int* code) {

@@ -62,8 +62,8 @@ int check_table(int n_req, int max_pages, int page_size, int* shift) {
   if (max_pages < 1) return fail(RA_ERR_INVALID, "max_pages=%d must be >= 1", max_pages);
   if (static_cast<long long>(n_req) * max_pages > kMaxInt)
     return fail(RA_ERR_UNSUPPORTED, "n_req * max_pages = %lld exceeds 2^31 - 1", static_cast<long long>(n_req) * max_pages);
-  if (static_cast<long long>(max_pages) * page_size > kMaxInt)
-    return fail(RA_ERR_UNSUPPORTED, "max_pages * page_size = %lld exceeds 2^31 - 1", static_cast<long long>(max_pages) * page_size);
+  if (static_cast<long long>(max_pages) * page_size > kMaxInt - 255)  // a tile of headroom for the kernels' 32-bit positions
+    return fail(RA_ERR_UNSUPPORTED, "max_pages * page_size = %lld exceeds 2^31 - 256", static_cast<long long>(max_pages) * page_size);
   return RA_OK;
 }
 
@@ -400,7 +400,7 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   if (n_q < 0) return fail(RA_ERR_INVALID, "n_q=%d is negative", n_q);
   if (!cu_q && static_cast<long long>(n_req) * n_q != T)
     return fail(RA_ERR_INVALID, "T=%lld is not n_req * n_q = %d * %d (and cu_q is NULL)", T, n_req, n_q);
-  if (T * heads > kMaxInt) return fail(RA_ERR_UNSUPPORTED, "T * heads = %lld rows exceeds 2^31 - 1", T * heads);
+  if (T * heads > kMaxInt - 255) return fail(RA_ERR_UNSUPPORTED, "T * heads = %lld rows exceeds 2^31 - 256", T * heads);
   if (window < 0) return fail(RA_ERR_INVALID, "window=%lld is negative", window);
   const long long page_elems = static_cast<long long>(page_size) * kv_heads * d;
   if ((rc = check_cache("k_page_stride", k_page_stride, page_elems)) != RA_OK) return rc;

@@ -478,7 +478,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
  * The slot of a token is page * page_size + row.  Pages not in use form a
  * stack: entries [0, *free_count) of free_pages.  All bookkeeping arrays
  * are device memory, so a step needs no host read and can be captured.
- * n_req * max_pages and max_pages * page_size must be < 2^31.
+ * n_req * max_pages must be < 2^31 and max_pages * page_size <= 2^31 - 256.
  *
  * ra_paged_extend -- hand out pages for the new tokens of a step and say
  * where each goes.  Request i grows from lengths[i] by new_tokens[i] >= 0
@@ -523,7 +523,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
  *   outside [0, n_pages) is not read, and that request's result is
  *   undefined.  What lies behind a request's last token in its last page
  *   does not matter, NaN included.
- *   heads / kv_heads <= 128, T * heads < 2^31.
+ *   heads / kv_heads <= 128, T * heads <= 2^31 - 256.
  */
 int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* block_table,
                     int max_pages, const int* free_pages, int free_capacity,
