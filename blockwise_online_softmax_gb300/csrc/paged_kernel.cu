@@ -6,24 +6,26 @@
 //   out = sum exp(s_t - m) v_t / l,  lse = m + ln l.
 //
 // The work is the read of the pages: each key meets only the rows of its KV
-// head (g heads x the request's new tokens).  Its units are 128-key tiles,
-// in the order (request, row tile, KV head, key tile), and every CTA of a
-// grid of one per SM takes an equal run of them, whatever the lengths are:
-// the lengths stay on the device.  A CTA finds its run by a prefix sum over
-// the requests.  A (request, row tile, KV head) that falls into one CTA is
-// finished there; one cut by a border between CTAs leaves a partial state
-// (m, l, O~) on each side, and a second launch joins them in CTA order.
+// head (g heads x the request's new tokens).  Its units are 64-key tiles, in
+// the order (request, row tile, KV head, key tile), and every CTA of a grid of
+// two per SM takes an equal run of them, whatever the lengths are: the lengths
+// stay on the device.  A CTA finds its run by a prefix sum over the requests.
+// An item (request, row tile, KV head) that falls into one CTA is finished
+// there; one cut by a border between CTAs leaves a partial state (m, l, O~) on
+// each side, and a second launch joins them in CTA order.
 //
-// Two warps feed a ring of stages with TMA, one K, one V (a page, or half a
-// page of 256, is a box of one KV head; lane p looks up and requests page p of
-// the tile).  The K warp also walks the items ahead of everybody, leaves a
-// record of each in shared memory and copies its query rows there.  Eight
-// warps consume, four to a tile, two tiles at a time; each takes 32 keys of
-// its tile and keeps its own running (m, l, O~), so nothing in the loop waits
-// for another warp, and the states meet at the item's end.  The products are
-// mma.sync m16n8k16 with the keys, then the columns of V, as the 16-wide side
-// and 8 query rows as the other: a tcgen05 tile would be 128 rows for the 4 or
-// 8 there are, and its S -> P round trip through TMEM is the longer chain.
+// Two warps feed a ring of stages with TMA, one K, one V (a page, or 64 rows
+// of a larger one, is a box of one KV head; lane p looks up and requests page
+// p of the tile).  The K warp also walks the items ahead of everybody, leaves
+// a record of each in shared memory and copies its query rows there.  Four
+// warps consume; each takes 16 keys of a tile and keeps its own running (m, l,
+// O~), so nothing in the loop waits for another warp, and the states meet at
+// the item's end.  Two such CTAs on an SM hide each other's item ends, which
+// one CTA of twice the warps and tile did not (a 128-key item: 2.4 against 1.6
+// us).  The products are mma.sync m16n8k16 with the keys, then the columns of
+// V, as the 16-wide side and 8 query rows as the other: a tcgen05 tile would be
+// 128 rows for the 4 or 8 there are, and its S -> P round trip through TMEM is
+// the longer chain.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -40,43 +42,44 @@ __device__ int g_paged_status = 0;
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int BT = 128;          // keys per tile
-constexpr int kCons = 8;         // consumer warps
-constexpr int kThreads = 32 * (kCons + 2);
-constexpr int kItems = 4;        // item records and query tiles in flight
+constexpr int BT = 64;           // keys per tile
+constexpr int kCons = 4;         // consumer warps
+constexpr int kThreads = 256;    // a consumer warpgroup and one with the producers
 constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int NCH = D / 64;
   static constexpr int RT = 8 * NT;              // query rows of an item
+  static constexpr int ITEMS = NT == 1 ? 3 : 2;  // records and query tiles in flight
   static constexpr uint32_t TILE = BT * D * 2;
   static constexpr int NST = D == 128 ? 3 : 6;   // stages of one K and one V tile
   static constexpr uint32_t QT = RT * D * 2;     // query rows, 16-byte chunks swizzled
+  static constexpr uint32_t REC = 32 + 8 * RT;   // Item, then rows and ends of its query rows
   static constexpr uint32_t OFF_Q = NST * 2 * TILE;
-  static constexpr uint32_t OFF_BUF = OFF_Q + kItems * QT;         // [4][8][D] fp32
-  static constexpr uint32_t OFF_ML = OFF_BUF + 4 * 8 * D * 4;      // [2][kCons][RT] fp32
+  static constexpr uint32_t OFF_BUF = OFF_Q + ITEMS * QT;        // [kCons][8][D / 2] fp32
+  static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 4 * D * 4;  // [2][RT][kCons] fp32
   static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * kCons * RT * 4;
-  static constexpr uint32_t OFF_BAR = OFF_ITEM + kItems * 64;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + (3 * NST + 2 * kItems) * 8;
-  static constexpr uint32_t SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM + 512 <= 232448, "shared memory budget");
+  static constexpr uint32_t OFF_BAR = OFF_ITEM + ITEMS * REC;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + (3 * NST + 2 * ITEMS) * 8;
+  static constexpr uint32_t SMEM = OFF_MISC + 16;
+  static_assert(SMEM <= 115712, "two CTAs per SM");
 };
 
 // An item, or the part of it that a CTA has, as its consumers need it.
-// Positions are relative to the item's first key tile.
+// Positions are relative to the item's first key tile.  The record goes on
+// with row[RT], each query row's index in out, and end[RT], the end of the
+// keys that it sees.
 struct Item {
-  int rr0, rr1;    // query rows: row rr is token rr / g, head kh * g + rr % g
-  int row0;        // q row of the request's first token
-  int kh;
-  int end0;        // keys that token 0 of the request sees: [.., end0)
-  int base;        // position of the item's first key tile
-  int lo, hi;      // keys that any row sees
-  int k0;          // first key tile here
-  int tiles;       // key tiles here
-  int slot;        // partial slot, or -1: the item is whole
+  int rows;            // query rows
+  int base;            // position of the item's first key tile
+  int lo, hi;          // keys that any row sees
+  int k0;              // first key tile here
+  int tiles;           // key tiles here
+  int slot;            // partial slot, or -1: the item is whole
+  int pad;
 };
-static_assert(sizeof(Item) <= 64, "record size");
+static_assert(sizeof(Item) == 32, "record layout");
 
 // What a CTA that starts a cut item leaves for the joining launch.
 struct Cut {
@@ -247,10 +250,8 @@ struct Run {
   long long x;
 };
 
-__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT) {
-  __shared__ long long s_sum[kThreads / 32];
-  __shared__ long long s_x;
-  __shared__ int s_r;
+__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch) {
+  long long* s_sum = static_cast<long long*>(scratch);  // [kThreads / 32], then the location
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_req + kThreads - 1) / kThreads;
   const int i0 = tid * per, i1 = i0 + per < a.n_req ? i0 + per : a.n_req;
@@ -286,12 +287,12 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT) {
       if (at < u || i + 1 >= i1) break;
       at -= u;
     }
-    s_r = i;
-    s_x = at;
+    s_sum[kThreads / 32] = at;
+    s_sum[kThreads / 32 + 1] = i;
   }
   __syncthreads();
-  run.r = s_r;
-  run.x = s_x;
+  run.x = s_sum[kThreads / 32];
+  run.r = static_cast<int>(s_sum[kThreads / 32 + 1]);
   return run;
 }
 
@@ -303,20 +304,18 @@ __device__ __forceinline__ int cta_of(long long u, const Run& run) {
 // ------------------------------------------------------------------ the kernel
 // NT: 8-row groups of query rows of an item.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedArgs a) {
   using C = Cfg<D, NT>;
   constexpr int RT = C::RT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
   auto vfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NST + s); };
   auto empty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NST + s); };
   auto ifull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + s); };
-  auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + kItems + s); };
+  auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + C::ITEMS + s); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
@@ -328,25 +327,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       mbar_init(vfull(s), 1);
       mbar_init(empty(s), kCons);
     }
-    for (int s = 0; s < kItems; ++s) {
+    for (int s = 0; s < C::ITEMS; ++s) {
       mbar_init(ifull(s), 33);  // every lane's copies, and the record
       mbar_init(iempty(s), kCons);
     }
-    *abort_flag = *reinterpret_cast<volatile int*>(&g_paged_status) != 0 ? 1 : 0;
+    int abort = *reinterpret_cast<volatile int*>(&g_paged_status);
+    // The swizzled tiles need 1024-byte alignment, which the declaration asks
+    // for; a loader that ignored it would be reported, not computed with.
+    if (sb & 1023u) abort = atomicCAS(&g_paged_status, 0, 0x8f) | 0x8f;
+    *abort_flag = abort;
     fence_mbar_init();
     cuts[blockIdx.x].last = -1;
   }
-  const Run run = find_run(a, g, RT);  // synchronizes
-  if (run.first >= run.last) return;
+  const Run run = find_run(a, g, RT, smem + C::OFF_BUF);  // synchronizes
+  if (run.first >= run.last || *abort_flag) return;
   const long long lim = a.wait_limit;
-  Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
 
   if (warp >= kCons) {
     // ---------------------------------------------------------------- producers
+    regs_dec<56>();
+    if (warp >= kCons + 2) return;
     const bool is_k = warp == kCons;
     const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
     const int sh = a.page_shift;
-    const int rows = sh < 7 ? 1 << sh : BT;  // of a box
+    const int rows = sh < 6 ? 1 << sh : BT;  // of a box
     const int npg = BT / rows;
     const uint32_t box = static_cast<uint32_t>(rows) * 128u;
     auto full = [&](int s) -> uint32_t { return is_k ? kfull(s) : vfull(s); };
@@ -360,42 +364,40 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       const long long left = run.last - u;
       const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
       if (is_k) {
-        const int s = it % kItems;
-        if (it >= kItems) {
-          ok = wait_bar(iempty(s), (static_cast<uint32_t>(it / kItems) & 1u) ^ 1u, abort_flag,
+        const int s = it % C::ITEMS;
+        if (it >= C::ITEMS) {
+          ok = wait_bar(iempty(s), (static_cast<uint32_t>(it / C::ITEMS) & 1u) ^ 1u, abort_flag,
                         &g_paged_status, 0x84, lim);
           ok = __all_sync(kAll, ok);
           if (!ok) break;
+        }
+        const int n = w.t.rr1 - w.t.rr0, base = w.t.t0 * BT;
+        int* rec = reinterpret_cast<int*>(smem + C::OFF_ITEM + s * C::REC);
+        int row = 0;
+        if (lane < RT) {  // rows past the item's get its last row's keys, and no output
+          const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = rr / g;
+          row = (w.q.row0 + j) * a.heads + w.kh * g + (rr - j * g);
+          rec[8 + lane] = row;
+          rec[8 + RT + lane] = key_end(w.q, j) - base;
         }
         if (lane == 0) {
           const long long item0 = u - w.k;
           const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
           const int me = static_cast<int>(blockIdx.x);
-          Item x;
-          x.rr0 = w.t.rr0;
-          x.rr1 = w.t.rr1;
-          x.row0 = w.q.row0;
-          x.kh = w.kh;
-          x.base = w.t.t0 * BT;
-          x.end0 = w.q.len - w.q.n + 1 - x.base;
-          x.lo = w.t.lo - x.base;
-          x.hi = w.t.hi - x.base;
-          x.k0 = w.k;
-          x.tiles = tiles;
-          x.slot = c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0);
-          items[s] = x;
-          if (c0 != c1 && me == c0) cuts[me] = Cut{c1, x.row0, x.rr0, x.rr1 - x.rr0, x.kh};
-          mbar_arrive(ifull(s));
+          *reinterpret_cast<Item*>(rec) =
+              Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), 0};
+          if (c0 != c1 && me == c0) cuts[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ifull(s));
         // Chunk c of row r at c ^ (r % 8): the ldmatrix rows of a column
         // block fall into different banks.
 #pragma unroll
-        for (int x = lane; x < RT * D / 8; x += 32) {
-          const int r = x / (D / 8), c = x % (D / 8), rr = w.t.rr0 + r;
-          const bool in = rr < w.t.rr1;
-          const long long row = in ? static_cast<long long>(w.q.row0 + rr / g) * a.heads + w.kh * g + rr % g : 0;
+        for (int x0 = 0; x0 < RT * D / 8; x0 += 32) {
+          const int x = x0 + lane, r = x / (D / 8), c = x % (D / 8);
+          const long long at = static_cast<long long>(__shfl_sync(kAll, row, r)) * D + c * 8;
           copy16(sb + C::OFF_Q + s * C::QT + r * (D * 2) + ((c ^ (r & 7)) << 4),
-                 static_cast<const __nv_bfloat16*>(a.q) + row * D + c * 8, in ? 16u : 0u);
+                 static_cast<const __nv_bfloat16*>(a.q) + at, r < n ? 16u : 0u);
         }
         copies_arrive(ifull(s));
         ++it;
@@ -439,54 +441,46 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
 
   // ------------------------------------------------------------------ consumers
+  regs_inc<200>();
   // After a wait that gave up, a warp runs on without waiting (the status
-  // word says that the results are void), so the barriers still match; it
-  // leaves at the next item.
+  // word says that the results are void) to the item's first barrier, where
+  // all of them learn of it and leave together.  Every warp waits for every
+  // tile: a wait names its phase by parity alone, so no warp may be a whole
+  // turn of the ring away from another.
   float* buf = reinterpret_cast<float*>(smem + C::OFF_BUF);
-  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);  // [row][warp]
   float* s_l = s_m + kCons * RT;
   const float sl2 = a.scale_log2;
+  const int win = static_cast<int>(a.window);
   bool ok = true;
-  // Warps 0-3 take the CTA's even tiles, warps 4-7 the odd ones.  Every warp
-  // waits for and releases every tile all the same: a wait names its phase by
-  // parity alone, so no warp may be a whole turn of the ring away from another.
-  const int grp = warp >> 2;
-  int turn = 0;              // parity of the next tile
-  int st = 0;                // its stage and phase
+  int st = 0;                // stage and phase of the next tile
   uint32_t par = 0;
   long long u = run.first;
-  // ldmatrix addresses inside a 64-column chunk of a tile, for the warp's
-  // first 16 keys: K rows are keys (8 x 8 blocks: keys 0-7 / 8-15 first, then
-  // columns), V the same blocks with columns first, read transposed.
-  const int key_w = (warp & 3) * 32;
-  const int kr = key_w + (lane & 15), kc0 = lane >> 4;
-  const int vr = key_w + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
+  // ldmatrix addresses inside a 64-column chunk of a tile: K rows are keys
+  // (8 x 8 blocks: keys 0-7 / 8-15 first, then columns), V the same blocks
+  // with columns first, read transposed.
+  const int kr = warp * 16 + (lane & 15), kc0 = lane >> 4;
+  const int vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
   for (int it = 0; u < run.last; ++it) {
-    const int is = it % kItems;
-    ok = ok && wait_bar(ifull(is), static_cast<uint32_t>(it / kItems) & 1u, abort_flag,
+    const int is = it % C::ITEMS;
+    ok = ok && wait_bar(ifull(is), static_cast<uint32_t>(it / C::ITEMS) & 1u, abort_flag,
                         &g_paged_status, 0x85, lim);
-    // All consumer warps leave together, or none: nobody waits at a barrier
-    // for a warp that has gone.
-    if (!named_bar_and(1, 32 * kCons, ok)) return;
-    const Item item = items[is];
+    ok = __all_sync(kAll, ok);
+    const int* rec = reinterpret_cast<const int*>(smem + C::OFF_ITEM + is * C::REC);
+    Item item = *reinterpret_cast<const Item*>(rec);
+    if (!ok) item.tiles = 0;
     // Keys [lo, hi) of the lane's rows 8 nt + 2 (lane & 3) + {0, 1}; the keys
     // that every row of the item sees are [lo_all, hi_all).
-    const int win = static_cast<int>(a.window);
-    auto end_of = [&](int rr) {
-      const int e = item.end0 + rr / g;
-      return e < -item.base ? -item.base : e;
-    };
     auto begin_of = [&](int end) {
       return win > 0 && end + item.base > win ? end - win : -item.base;
     };
     int rlo[NT][2], rhi[NT][2];
-    const int hi_all = end_of(item.rr0), lo_all = begin_of(end_of(item.rr1 - 1));
+    const int hi_all = rec[8 + RT], lo_all = begin_of(rec[8 + 2 * RT - 1]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int rr = item.rr0 + 8 * nt + 2 * (lane & 3) + c;
-        rhi[nt][c] = end_of(rr < item.rr1 ? rr : item.rr1 - 1);
+        rhi[nt][c] = rec[8 + RT + 8 * nt + 2 * (lane & 3) + c];
         rlo[nt][c] = begin_of(rhi[nt][c]);
       }
     float m[NT][2], l[NT][2], o[NT][D / 16][4];
@@ -502,18 +496,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int qc0 = lane >> 3, qx = lane & 7;
     for (int k = 0; k < item.tiles; ++k) {
       const uint32_t kb = sb + st * 2 * C::TILE, vb = kb + C::TILE;
-      const int k0 = (item.k0 + k) * BT + key_w;  // the warp's first key
+      const int k0 = (item.k0 + k) * BT + warp * 16;  // the warp's first key
       ok = ok && wait_bar(kfull(st), par, abort_flag, &g_paged_status, 0x82, lim);
       ok = __all_sync(kAll, ok);
-      const bool some = turn == grp && k0 < item.hi && k0 + 32 > item.lo;
-      float sc[NT][2][4];
-      uint32_t pb[NT][2][3][2];
+      const bool some = k0 < item.hi && k0 + 16 > item.lo;
+      float sc[NT][4];
+      uint32_t pb[NT][3][2];
       float al[NT][2];
       if (some) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) sc[nt][b][0] = sc[nt][b][1] = sc[nt][b][2] = sc[nt][b][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t bq[NT][4];
@@ -523,32 +515,27 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int kk = 2 * k2 + h, ch = (2 * kk + kc0) & 7;
+            uint32_t af[4];
+            ldsm4(kb + (kk >> 2) * CHB + kr * 128 + ((ch ^ (kr & 7)) << 4), af);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              uint32_t af[4];
-              ldsm4(kb + (kk >> 2) * CHB + (kr + 16 * b) * 128 + ((ch ^ (kr & 7)) << 4), af);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt][b], af, bq[nt][2 * h], bq[nt][2 * h + 1]);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], af, bq[nt][2 * h], bq[nt][2 * h + 1]);
           }
         }
-        if (k0 < lo_all || k0 + 32 > hi_all) {
+        if (k0 < lo_all || k0 + 16 > hi_all) {
           const int k1 = k0 + (lane >> 2);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int key = k1 + 16 * b + (c >> 1) * 8;
-                if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[nt][b][c] = -INFINITY;
-              }
+            for (int c = 0; c < 4; ++c) {
+              const int key = k1 + (c >> 1) * 8;
+              if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[nt][c] = -INFINITY;
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]), fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
+            float x = fmaxf(sc[nt][c], sc[nt][c + 2]);
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
@@ -556,16 +543,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             const float ref = mn == -INFINITY ? 0.f : mn;
             al[nt][c] = ex2(m[nt][c] - ref);
             m[nt][c] = mn;
-            float sum = 0.f;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float p0 = ex2(fmaf(sc[nt][b][c], sl2, -ref));
-              const float p1 = ex2(fmaf(sc[nt][b][c + 2], sl2, -ref));
-              sum += p0 + p1;
-              sc[nt][b][c] = p0;
-              sc[nt][b][c + 2] = p1;
-            }
-            l[nt][c] = fmaf(l[nt][c], al[nt][c], sum);
+            const float p0 = ex2(fmaf(sc[nt][c], sl2, -ref)), p1 = ex2(fmaf(sc[nt][c + 2], sl2, -ref));
+            l[nt][c] = fmaf(l[nt][c], al[nt][c], p0 + p1);
+            sc[nt][c] = p0;
+            sc[nt][c + 2] = p1;
           }
         // P as three bf16 terms (8 + 8 + 8 bits): the product with V then has
         // the weights' fp32 value, which an fp32 output shows; one bf16 term
@@ -573,47 +554,40 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int half = 0; half < 2; ++half) {
+            float x = sc[nt][2 * half], y = sc[nt][2 * half + 1];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float x = sc[nt][b][2 * half], y = sc[nt][b][2 * half + 1];
-#pragma unroll
-              for (int term = 0; term < 3; ++term) {
-                const uint32_t h = bf16x2_rn(x, y);
-                pb[nt][b][term][half] = transpose8x8(h);
-                x -= __uint_as_float(h << 16);
-                y -= __uint_as_float(h & 0xffff0000u);
-              }
+            for (int term = 0; term < 3; ++term) {
+              const uint32_t h = bf16x2_rn(x, y);
+              pb[nt][term][half] = transpose8x8(h);
+              x -= __uint_as_float(h << 16);
+              y -= __uint_as_float(h & 0xffff0000u);
             }
+          }
       }
       ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_status, 0x83, lim);
       ok = __all_sync(kAll, ok);
       if (some) {
-        const bool edge = k0 < item.lo || k0 + 32 > item.hi;
-        uint32_t keep[2][2];  // V rows outside [lo, hi) may hold anything
+        const bool edge = k0 < item.lo || k0 + 16 > item.hi;
+        uint32_t keep[2] = {kAll, kAll};  // V rows outside [lo, hi) may hold anything
         if (edge) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int key = k0 + 16 * b + 8 * half + 2 * (lane & 3);
-              keep[b][half] = (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
-                              (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
-            }
+          for (int half = 0; half < 2; ++half) {
+            const int key = k0 + 8 * half + 2 * (lane & 3);
+            keep[half] = (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
+                         (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
+          }
         }
 #pragma unroll
         for (int dm = 0; dm < D / 16; ++dm) {
-          uint32_t af[2][4];
+          uint32_t af[4];
           const int ch = (2 * dm + vc0) & 7;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            ldsm4_t(vb + (dm >> 2) * CHB + (vr + 16 * b) * 128 + ((ch ^ (vr & 7)) << 4), af[b]);
-            if (edge) {
-              af[b][0] &= keep[b][0];
-              af[b][1] &= keep[b][0];
-              af[b][2] &= keep[b][1];
-              af[b][3] &= keep[b][1];
-            }
+          ldsm4_t(vb + (dm >> 2) * CHB + vr * 128 + ((ch ^ (vr & 7)) << 4), af);
+          if (edge) {
+            af[0] &= keep[0];
+            af[1] &= keep[0];
+            af[2] &= keep[1];
+            af[3] &= keep[1];
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -621,9 +595,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             // fp32 step: the tensor core's own accumulation truncates.
             float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int term = 2; term >= 0; --term)
-#pragma unroll
-              for (int b = 0; b < 2; ++b) mma16816(t, af[b], pb[nt][b][term][0], pb[nt][b][term][1]);
+            for (int term = 2; term >= 0; --term) mma16816(t, af, pb[nt][term][0], pb[nt][term][1]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[nt][dm][c] = fmaf(o[nt][dm][c], al[nt][c & 1], t[c]);
           }
@@ -631,7 +603,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
-      turn ^= 1;
       if (++st == C::NST) {
         st = 0;
         par ^= 1u;
@@ -647,101 +618,105 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         x += __shfl_xor_sync(kAll, x, 4);
         x += __shfl_xor_sync(kAll, x, 8);
         x += __shfl_xor_sync(kAll, x, 16);
+        l[nt][c] = x;
         if (lane < 4) {
-          s_m[warp * RT + 8 * nt + 2 * lane + c] = m[nt][c];
-          s_l[warp * RT + 8 * nt + 2 * lane + c] = x;
+          s_m[(8 * nt + 2 * lane + c) * kCons + warp] = m[nt][c];
+          s_l[(8 * nt + 2 * lane + c) * kCons + warp] = x;
         }
       }
-    named_bar_sync(1, 32 * kCons);
+    if (!named_bar_and(1, 32 * kCons, ok)) return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0) named_bar_sync(1, 32 * kCons);  // the sums of group nt - 1 are read
+      constexpr int H = D / 32, Q = D / 64;  // 16-column groups of a half and of a quarter
+      float inv[2], mx[2], lt[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * RT + 8 * nt + 2 * (lane & 3) + c]);
-        const float e = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - mx);
+        const int r = 8 * nt + 2 * (lane & 3) + c;
+        const float4 vm = *reinterpret_cast<const float4*>(s_m + r * kCons);
+        const float4 vl = *reinterpret_cast<const float4*>(s_l + r * kCons);
+        mx[c] = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
+        const float ref = mx[c] == -INFINITY ? 0.f : mx[c];
+        lt[c] = (vl.x * ex2(vm.x - ref) + vl.y * ex2(vm.y - ref)) +
+                (vl.z * ex2(vm.z - ref) + vl.w * ex2(vm.w - ref));
+        inv[c] = item.slot >= 0 ? 1.f : (lt[c] > 0.f ? 1.f / lt[c] : 0.f);
+        const float e = ex2(m[nt][c] - ref);
 #pragma unroll
         for (int dm = 0; dm < D / 16; ++dm) {
           o[nt][dm][c] *= e;
           o[nt][dm][c + 2] *= e;
         }
       }
-      // Warps 4-7 hand theirs to warps 0-3, lane by lane, ...
-      float* mine = buf + (warp & 3) * 8 * D;
-      if (warp >= 4) {
+      // Warps w and w ^ 1 swap halves of the columns and add, then w and
+      // w ^ 2 quarters: warp w ends with columns [D / 4 * (2 (w & 1) + w / 2)
+      // ..) of the sum.  A warp's second message goes where it read its first.
+      const bool odd = warp & 1, high = warp & 2;
+      float* from = buf + warp * (4 * D);
+      float* to = buf + (warp ^ 1) * (4 * D);
+      if (nt > 0) named_bar_sync(1, 32 * kCons);  // the messages of group nt - 1 are read
+      float h[H][4];
 #pragma unroll
-        for (int dm = 0; dm < D / 16; ++dm)
-          *reinterpret_cast<float4*>(mine + (dm * 32 + lane) * 4) =
-              make_float4(o[nt][dm][0], o[nt][dm][1], o[nt][dm][2], o[nt][dm][3]);
-      }
-      // ... and the thread's sums below: row r, four columns.
-      constexpr int PT = 8 * D / 4;  // float4s of the group
-      const int r = tid / (D / 4), d0 = (tid % (D / 4)) * 4;
-      const int rr = item.rr0 + 8 * nt + r;
-      float mx = -INFINITY, lt = 0.f;
-      if (tid < PT) {
+      for (int x = 0; x < H; ++x) {
+        float y[4];
 #pragma unroll
-        for (int x = 0; x < kCons; ++x) mx = fmaxf(mx, s_m[x * RT + 8 * nt + r]);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-        for (int x = 0; x < kCons; ++x)
-          lt = fmaf(s_l[x * RT + 8 * nt + r], ex2(s_m[x * RT + 8 * nt + r] - ref), lt);
+        for (int c = 0; c < 4; ++c) {
+          h[x][c] = odd ? o[nt][H + x][c] : o[nt][x][c];
+          y[c] = odd ? o[nt][x][c] : o[nt][H + x][c];
+        }
+        *reinterpret_cast<float4*>(to + (x * 32 + lane) * 4) = make_float4(y[0], y[1], y[2], y[3]);
       }
       named_bar_sync(1, 32 * kCons);
-      if (warp < 4) {
 #pragma unroll
-        for (int dm = 0; dm < D / 16; ++dm) {
-          const float4 z = *reinterpret_cast<const float4*>(mine + (dm * 32 + lane) * 4);
-          o[nt][dm][0] += z.x;
-          o[nt][dm][1] += z.y;
-          o[nt][dm][2] += z.z;
-          o[nt][dm][3] += z.w;
+      for (int x = 0; x < H; ++x) {
+        const float4 z = *reinterpret_cast<const float4*>(from + (x * 32 + lane) * 4);
+        h[x][0] += z.x;
+        h[x][1] += z.y;
+        h[x][2] += z.z;
+        h[x][3] += z.w;
+      }
+      __syncwarp();
+      float q[Q][4];
+#pragma unroll
+      for (int x = 0; x < Q; ++x) {
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          q[x][c] = high ? h[Q + x][c] : h[x][c];
+          y[c] = high ? h[x][c] : h[Q + x][c];
         }
-        __syncwarp();
-        // Column d of row r at d ^ 8 (r / 2): the four row pairs of a store
-        // fall into different banks.
+        *reinterpret_cast<float4*>(from + (x * 32 + lane) * 4) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+      named_bar_sync(1, 32 * kCons);
+      const float* last = buf + (warp ^ 2) * (4 * D);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int sw = (lane & 3) << 3;
-          float* dst = mine + (2 * (lane & 3) + c) * D;
+      for (int x = 0; x < Q; ++x) {
+        const float4 z = *reinterpret_cast<const float4*>(last + (x * 32 + lane) * 4);
+        q[x][0] += z.x;
+        q[x][1] += z.y;
+        q[x][2] += z.z;
+        q[x][3] += z.w;
+      }
+      const int d0 = (odd ? D / 2 : 0) + (high ? D / 4 : 0) + (lane >> 2);
 #pragma unroll
-          for (int dm = 0; dm < D / 16; ++dm) {
-            dst[(dm * 16 + (lane >> 2)) ^ sw] = o[nt][dm][c];
-            dst[(dm * 16 + 8 + (lane >> 2)) ^ sw] = o[nt][dm][c + 2];
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * nt + 2 * (lane & 3) + c;
+        if (r >= item.rows) continue;
+        const long long row = item.slot >= 0 ? item.slot * RT + r : rec[8 + r];
+#pragma unroll
+        for (int x = 0; x < Q; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float y = q[x][c + 2 * e] * inv[c];
+            const long long at = row * D + d0 + 16 * x + 8 * e;
+            if (item.slot >= 0) a.po[at] = y;
+            else if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+            else static_cast<float*>(a.out)[at] = y;
           }
-        }
-      }
-      named_bar_sync(1, 32 * kCons);
-      if (tid < PT && rr < item.rr1) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 z = *reinterpret_cast<const float4*>(
-              buf + (x * 8 + r) * D + (d0 ^ ((r >> 1) << 3)));
-          y.x += z.x;
-          y.y += z.y;
-          y.z += z.z;
-          y.w += z.w;
-        }
-        if (item.slot < 0) {
-          const long long row = static_cast<long long>(item.row0 + rr / g) * a.heads + item.kh * g + rr % g;
-          const float inv = lt > 0.f ? 1.f / lt : 0.f;
-          if (a.out_bf16) {
-            const uint2 h = make_uint2(bf16x2_rn(y.x * inv, y.y * inv), bf16x2_rn(y.z * inv, y.w * inv));
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + d0) = h;
+        if (warp == 0 && lane < 4) {
+          if (item.slot >= 0) {
+            a.pm[row] = mx[c];
+            a.pl[row] = lt[c];
           } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + d0) =
-                make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-          }
-          if (d0 == 0) a.lse[row] = lt > 0.f ? mx * kLn2 + logf(lt) : -INFINITY;
-        } else {
-          const int pr = item.slot * RT + 8 * nt + r;
-          *reinterpret_cast<float4*>(a.po + static_cast<long long>(pr) * D + d0) = y;
-          if (d0 == 0) {
-            a.pm[pr] = mx;
-            a.pl[pr] = lt;
+            a.lse[row] = lt[c] > 0.f ? mx[c] * kLn2 + logf(lt[c]) : -INFINITY;
           }
         }
       }

@@ -84,14 +84,14 @@ int check_stride(const char* name, long long stride, long long row, int dtype) {
 }
 
 // 4-D map over the pages of one cache tensor; a box is one KV head's rows of
-// a page (half a page of 256), 64 columns wide, 128-byte swizzle.
+// a page (64 of a larger one), 64 columns wide, 128-byte swizzle.
 int page_map(CUtensorMap* map, const void* base, int n_pages, int page_size, long long page_stride,
              int kv_heads, int d) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(kv_heads),
                               static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(n_pages)};
   const cuuint64_t row = static_cast<cuuint64_t>(kv_heads) * d * 2;
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, row, static_cast<cuuint64_t>(page_stride) * 2};
-  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(page_size < 128 ? page_size : 128), 1};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(page_size < 64 ? page_size : 64), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
                         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -436,7 +436,7 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   // Without pages no load is ever issued; the maps still need an address.
   if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
-  const int ctas = ra::sm_count();
+  const int ctas = 2 * ra::sm_count();
   const int rt = ra::paged_row_tile(a);
   const size_t rows = static_cast<size_t>(2) * ctas * rt;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -133,7 +133,7 @@ struct PagedArgs {
 int paged_row_tile(const PagedArgs& a);
 size_t paged_cut_bytes(int ctas);
 // tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
-// 64 x 1 x min(page_size, 128) x 1, 128-byte swizzle.
+// 64 x 1 x min(page_size, 64) x 1, 128-byte swizzle.
 cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st);
