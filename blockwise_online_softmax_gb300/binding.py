@@ -481,25 +481,18 @@ def _rows(t, name, T, heads, d, dev, dtype):
     return t.data_ptr(), st[0] if T > 1 else heads * d
 
 
-class _On:
-    """Makes device `dev` current for the block if it is not, and resolves
-    the stream there.  `with _On(dev, stream) as st:`"""
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.old = dev, stream, None
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev:
-            self.old = cur
-            torch.cuda.set_device(self.dev)
-        if self.stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.dev)
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.old is not None:
-            torch.cuda.set_device(self.old)
+def _call(name, dev, stream, *args):
+    """Call a library function with device `dev` current, on `stream` (None:
+    the device's current stream), the last argument."""
+    f = getattr(_lib or lib(), name)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == dev:
+        rc = f(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, st)
+    if rc:
+        _check(rc)
 
 
 def _weights(q_weight, k_weight, d, dev):
@@ -611,11 +604,10 @@ def ra_qk_norm_rope(q, k, phases, *, q_weight=None, k_weight=None, eps: float = 
     ph, rot = _phase_table(phases, dev)
     qw, kw, wt = _weights(q_weight, k_weight, d, dev)
     pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
-    with _On(dev, stream) as st:
-        _check(lib().ra_qk_norm_rope(
-            qp, kp, _arg(q_out, "q_out", dev, dtype), _arg(k_out, "k_out", dev, dtype), T, d,
-            heads, kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)),
-            ph, float(mscale), qw, kw, wt, float(eps), dt, st))
+    _call("ra_qk_norm_rope", dev, stream,
+        qp, kp, _arg(q_out, "q_out", dev, dtype), _arg(k_out, "k_out", dev, dtype), T, d,
+        heads, kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)),
+        ph, float(mscale), qw, kw, wt, float(eps), dt)
     return q_out, k_out
 
 
@@ -654,11 +646,10 @@ def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_w
     pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
     dqw = 0 if dq_weight is None else _vec(dq_weight, "dq_weight", d, dev, f32)
     dkw = 0 if dk_weight is None else _vec(dk_weight, "dk_weight", d, dev, f32)
-    with _On(dev, stream) as st:
-        _check(lib().ra_qk_norm_rope_backward(
-            qp, kp, _arg(dq_out, "dq_out", dev, f32), _arg(dk_out, "dk_out", dev, f32), dqp, dkp,
-            dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout), int(P), rot,
-            int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt, st))
+    _call("ra_qk_norm_rope_backward", dev, stream,
+        qp, kp, _arg(dq_out, "dq_out", dev, f32), _arg(dk_out, "dk_out", dev, f32), dqp, dkp,
+        dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout), int(P), rot,
+        int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt)
     return dq, dk, dq_weight, dk_weight
 
 
@@ -700,17 +691,15 @@ def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *,
         status = torch.empty(3, dtype=i32, device=where)
     table, width = _table(block_table, n, dev)
     pool = free_pages.numel()
-    with _On(dev, stream) as st:
-        _check(lib().ra_paged_extend(
-            _vec(lengths, "lengths", n, dev, i32), _vec(new_tokens, "new_tokens", n, dev, i32), n,
-            table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
-            _vec(free_count, "free_count", 1, dev, i32), int(page_size), tokens,
-            _vec(lengths_out, "lengths_out", n, dev, i32),
-            _vec(free_count_out, "free_count_out", 1, dev, i32),
-            _vec(slots, "slots", tokens, dev, torch.int64),
-            _vec(positions, "positions", tokens, dev, i32),
-            _vec(cu_tokens, "cu_tokens", n + 1, dev, i32), _vec(status, "status", 3, dev, i32),
-            st))
+    _call("ra_paged_extend", dev, stream,
+        _vec(lengths, "lengths", n, dev, i32), _vec(new_tokens, "new_tokens", n, dev, i32), n,
+        table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
+        _vec(free_count, "free_count", 1, dev, i32), int(page_size), tokens,
+        _vec(lengths_out, "lengths_out", n, dev, i32),
+        _vec(free_count_out, "free_count_out", 1, dev, i32),
+        _vec(slots, "slots", tokens, dev, torch.int64),
+        _vec(positions, "positions", tokens, dev, i32),
+        _vec(cu_tokens, "cu_tokens", n + 1, dev, i32), _vec(status, "status", 3, dev, i32))
     return slots, positions, cu_tokens, lengths_out, free_count_out, status
 
 
@@ -727,13 +716,12 @@ def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, 
         free_count_out = torch.empty(1, dtype=i32, device=lengths.device)
     table, width = _table(block_table, n, dev)
     pool = free_pages.numel()
-    with _On(dev, stream) as st:
-        _check(lib().ra_paged_release(
-            _vec(lengths, "lengths", n, dev, i32), _vec(finished, "finished", n, dev, i32), n,
-            table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
-            _vec(free_count, "free_count", 1, dev, i32), int(page_size),
-            _vec(lengths_out, "lengths_out", n, dev, i32),
-            _vec(free_count_out, "free_count_out", 1, dev, i32), st))
+    _call("ra_paged_release", dev, stream,
+        _vec(lengths, "lengths", n, dev, i32), _vec(finished, "finished", n, dev, i32), n,
+        table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
+        _vec(free_count, "free_count", 1, dev, i32), int(page_size),
+        _vec(lengths_out, "lengths_out", n, dev, i32),
+        _vec(free_count_out, "free_count_out", 1, dev, i32))
     return lengths_out, free_count_out
 
 
@@ -787,12 +775,11 @@ def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_we
     kc, vc, n_pages, ps, kcs, vcs = _caches(k_cache, v_cache, kv_heads, d, dev)
     ph, rot = _phase_table(phases, dev)
     qw, kw, wt = _weights(q_weight, k_weight, d, dev)
-    with _On(dev, stream) as st:
-        _check(lib().ra_paged_append(
-            qp, kp, vp, _arg(q_out, "q_out", dev, dtype), kc, vc, T, d, heads, kv_heads, qs, ks,
-            vs, n_pages, ps, kcs, vcs, _vec(slots, "slots", T, dev, torch.int64),
-            _vec(positions, "positions", T, dev, torch.int32), rot, int(bool(interleaved)), ph,
-            float(mscale), qw, kw, wt, float(eps), dt, st))
+    _call("ra_paged_append", dev, stream,
+        qp, kp, vp, _arg(q_out, "q_out", dev, dtype), kc, vc, T, d, heads, kv_heads, qs, ks,
+        vs, n_pages, ps, kcs, vcs, _vec(slots, "slots", T, dev, torch.int64),
+        _vec(positions, "positions", T, dev, torch.int32), rot, int(bool(interleaved)), ph,
+        float(mscale), qw, kw, wt, float(eps), dt)
     return q_out
 
 
@@ -827,12 +814,11 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, win
     kc, vc, n_pages, ps, ks, vs = _caches(k_cache, v_cache, kv_heads, d, dev)
     table, width = _table(block_table, n, dev)
     cu = 0 if cu_q is None else _vec(cu_q, "cu_q", n + 1, dev, torch.int32)
-    with _On(dev, stream) as st:
-        _check(lib().ra_paged_decode(
-            _arg(q, "q", dev, torch.bfloat16), kc, vc, _arg(out, "out", dev, out.dtype),
-            _arg(lse, "lse", dev, f32), T, n, 0 if cu or not n else T // n, cu, table, width,
-            _vec(lengths, "lengths", n, dev, torch.int32), n_pages, ps, ks, vs, int(window), d,
-            heads, kv_heads, RA_BF16, RA_BF16 if out.dtype is torch.bfloat16 else RA_F32, st))
+    _call("ra_paged_decode", dev, stream,
+        _arg(q, "q", dev, torch.bfloat16), kc, vc, _arg(out, "out", dev, out.dtype),
+        _arg(lse, "lse", dev, f32), T, n, 0 if cu or not n else T // n, cu, table, width,
+        _vec(lengths, "lengths", n, dev, torch.int32), n_pages, ps, ks, vs, int(window), d,
+        heads, kv_heads, RA_BF16, RA_BF16 if out.dtype is torch.bfloat16 else RA_F32)
     return out, lse
 
 

@@ -402,13 +402,23 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         copies_arrive(ifull(s));
         ++it;
       }
+      // Table entries [p_begin, p_end) hold the item's pages.  They are read 32
+      // at a time, and the next 32 before they are needed: a lookup per tile
+      // would put its latency (some 700 cycles) between the requests.
       const int p_end = w.t.hi > w.t.lo ? ((w.t.hi - 1) >> sh) + 1 : 0, p_begin = w.t.lo >> sh;
       const int* table = a.block_table + static_cast<long long>(w.r) * a.max_pages;
+      auto lookup = [&](int p) { return p >= p_begin && p < p_end ? table[p] : -1; };
+      int first = ((w.t.t0 + w.k) * BT) >> sh;  // page of lane 0's entry in `ids`
+      int ids = lookup(first + lane), more = lookup(first + 32 + lane);
       for (int k = 0; k < tiles; ++k, ++i) {
         const int key0 = (w.t.t0 + w.k + k) * BT;
-        const int p = (key0 >> sh) + lane;
-        int page = -1;
-        if (lane < npg && p >= p_begin && p < p_end) page = table[p];
+        if ((key0 >> sh) >= first + 32) {
+          first += 32;
+          ids = more;
+          more = lookup(first + 32 + lane);
+        }
+        int page = __shfl_sync(kAll, ids, ((key0 >> sh) - first + lane) & 31);
+        if (lane >= npg) page = -1;
         const bool have = page >= 0 && page < a.n_pages;
         const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(kAll, have)));
         const int s = i % C::NST;
