@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libra.so")
 SOURCES = ["ra_api.cu", "state_kernels.cu", "simt_kernel.cu", "umma_kernel.cu", "decode_kernel.cu",
            "bwd_kernel.cu", "serve_api.cu", "rope_kernel.cu", "pages_kernel.cu",
-           "paged_kernel.cu"]
+           "paged_kernel.cu", "paged_tc_kernel.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

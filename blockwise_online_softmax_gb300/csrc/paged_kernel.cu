@@ -32,8 +32,7 @@
 
 #include <cuda_bf16.h>
 
-#include "ptx.cuh"
-#include "serve_internal.h"
+#include "paged_walk.cuh"
 
 namespace ra {
 
@@ -41,7 +40,8 @@ __device__ int g_paged_status = 0;
 
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
+using namespace paged;
+
 constexpr int BT = 64;           // keys per tile
 constexpr int kCons = 4;         // consumer warps
 constexpr int kThreads = 256;    // a consumer warpgroup and one with the producers
@@ -81,23 +81,6 @@ struct Item {
 };
 static_assert(sizeof(Item) == 32, "record layout");
 
-// What a CTA that starts a cut item leaves for the joining launch.
-struct Cut {
-  int last;   // last CTA of the item; -1: none
-  int row0;   // first row of the q tensor of the request
-  int rr0;    // first row of the tile (row rr: token rr / g, head kh * g + rr % g)
-  int rows;
-  int kh;
-};
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
-                                            int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -118,187 +101,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 16 bytes to shared memory, zeros when `bytes` is 0; the arrival on `bar`
-// follows when the calling thread's copies have landed.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// ------------------------------------------------------------------ the work list
-struct Request {
-  int row0;  // first row of q
-  int n;     // new tokens
-  int len;   // keys, the new tokens' included
-};
-
-__device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
-  Request q;
-  if (a.cu_q) {
-    // A malformed cu_q must not reach outside q and out.
-    const int T = static_cast<int>(a.T), x = a.cu_q[r], y = a.cu_q[r + 1];
-    q.row0 = x < 0 ? 0 : (x > T ? T : x);
-    q.n = (y < q.row0 ? q.row0 : (y > T ? T : y)) - q.row0;
-  } else {
-    q.row0 = r * static_cast<int>(a.n_q);
-    q.n = static_cast<int>(a.n_q);
-  }
-  const int most = a.max_pages << a.page_shift, len = a.lengths[r];
-  q.len = len < 0 ? 0 : (len > most ? most : len);
-  return q;
-}
-
-// Token j of the request sees keys [begin, end).
-__device__ __forceinline__ int key_end(const Request& q, int j) {
-  const int e = q.len - q.n + j + 1;
-  return e < 0 ? 0 : e;
-}
-__device__ __forceinline__ int key_begin(const PagedArgs& a, int end) {
-  return a.window > 0 && end > a.window ? end - static_cast<int>(a.window) : 0;
-}
-
-// Row tile rt of a request: rows [rr0, rr1), keys [lo, hi) over all of them,
-// key tiles [t0, t0 + nt) (one, with no key, when there is none).
-struct RowTile {
-  int rr0, rr1;
-  int lo, hi;
-  int t0, nt;
-};
-
-__device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const Request& q, int g, int RT,
-                                            int rt) {
-  RowTile t;
-  t.rr0 = rt * RT;
-  const int all = q.n * g;
-  t.rr1 = t.rr0 + RT < all ? t.rr0 + RT : all;
-  t.hi = key_end(q, (t.rr1 - 1) / g);
-  t.lo = key_begin(a, key_end(q, t.rr0 / g));
-  t.t0 = t.lo / BT;
-  t.nt = t.hi > t.lo ? (t.hi - 1) / BT + 1 - t.t0 : 1;
-  return t;
-}
-
-__device__ __forceinline__ int row_tiles(const Request& q, int g, int RT) {
-  return (q.n * g + RT - 1) / RT;
-}
-
-__device__ __forceinline__ long long request_units(const PagedArgs& a, int r, int g, int RT) {
-  const Request q = load_request(a, r);
-  const int n = row_tiles(q, g, RT);
-  long long u = 0;
-  for (int rt = 0; rt < n; ++rt) u += row_tile(a, q, g, RT, rt).nt;
-  return u * a.kv_heads;
-}
-
-// Where a CTA's run of units starts, and how the walk goes on.
-struct Walk {
-  int r, rt, kh, nrt;
-  Request q;
-  RowTile t;
-  int k;  // key tile inside the item
-
-  __device__ __forceinline__ void enter(const PagedArgs& a, int g, int RT) {
-    q = load_request(a, r);
-    nrt = row_tiles(q, g, RT);
-  }
-  // Start at unit x of request r.
-  __device__ __forceinline__ void start(const PagedArgs& a, int g, int RT, int r_, long long x) {
-    r = r_;
-    enter(a, g, RT);
-    for (rt = 0;; ++rt) {
-      t = row_tile(a, q, g, RT, rt);
-      const long long w = static_cast<long long>(t.nt) * a.kv_heads;
-      if (x < w || rt + 1 >= nrt) break;
-      x -= w;
-    }
-    kh = static_cast<int>(x / t.nt);
-    k = static_cast<int>(x % t.nt);
-  }
-  // To the next item; the caller knows that there is one (the bound on r only
-  // keeps arrays that change under the kernel from leading it outside).
-  __device__ __forceinline__ void next(const PagedArgs& a, int g, int RT) {
-    k = 0;
-    if (++kh < a.kv_heads) return;
-    kh = 0;
-    if (++rt >= nrt) {
-      rt = 0;
-      do {
-        if (r + 1 < a.n_req) ++r;
-        enter(a, g, RT);
-      } while (nrt == 0 && r + 1 < a.n_req);
-    }
-    t = row_tile(a, q, g, RT, rt);
-  }
-};
-
-// Prefix sum over the requests: every thread of the CTA gets the total; the
-// unit `first` = floor(c total / G) of CTA c is located as (request, offset).
-// With fewer units than CTAs only `ctas` of them work, one unit each, so the
-// CTAs of a cut item all hold a part of it.
-struct Run {
-  long long total, first, last;
-  int ctas;
-  int r;
-  long long x;
-};
-
-__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch) {
-  long long* s_sum = static_cast<long long*>(scratch);  // [kThreads / 32], then the location
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.n_req + kThreads - 1) / kThreads;
-  const int i0 = tid * per, i1 = i0 + per < a.n_req ? i0 + per : a.n_req;
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_units(a, i, g, RT);
-  long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  long long before = x - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
-  Run run;
-  run.total = total;
-  run.ctas = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
-  run.first = run.last = total;
-  if (static_cast<int>(blockIdx.x) < run.ctas) {
-    run.first = static_cast<long long>(blockIdx.x) * total / run.ctas;
-    run.last = static_cast<long long>(blockIdx.x + 1) * total / run.ctas;
-  }
-  if (run.first < run.last && before <= run.first && run.first < before + mine) {
-    long long at = run.first - before;
-    int i = i0;
-    for (;; ++i) {
-      const long long u = request_units(a, i, g, RT);
-      if (at < u || i + 1 >= i1) break;
-      at -= u;
-    }
-    s_sum[kThreads / 32] = at;
-    s_sum[kThreads / 32 + 1] = i;
-  }
-  __syncthreads();
-  run.x = s_sum[kThreads / 32];
-  run.r = static_cast<int>(s_sum[kThreads / 32 + 1]);
-  return run;
-}
-
-// CTA whose run holds unit u.
-__device__ __forceinline__ int cta_of(long long u, const Run& run) {
-  return static_cast<int>(((u + 1) * run.ctas - 1) / run.total);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -339,7 +145,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     fence_mbar_init();
     cuts[blockIdx.x].last = -1;
   }
-  const Run run = find_run(a, g, RT, smem + C::OFF_BUF);  // synchronizes
+  const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_BUF);  // synchronizes
   if (run.first >= run.last || *abort_flag) return;
   const long long lim = a.wait_limit;
 
@@ -354,7 +160,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int npg = BT / rows;
     const uint32_t box = static_cast<uint32_t>(rows) * 128u;
     auto full = [&](int s) -> uint32_t { return is_k ? kfull(s) : vfull(s); };
-    Walk w;
+    Walk<BT> w;
     w.start(a, g, RT, run.r, run.x);
     long long u = run.first;
     bool ok = true;
@@ -402,24 +208,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         copies_arrive(ifull(s));
         ++it;
       }
-      // Table entries [p_begin, p_end) hold the item's pages.  They are read 32
-      // at a time, and the next 32 before they are needed: a lookup per tile
-      // would put its latency (some 700 cycles) between the requests.
-      const int p_end = w.t.hi > w.t.lo ? ((w.t.hi - 1) >> sh) + 1 : 0, p_begin = w.t.lo >> sh;
-      const int* table = a.block_table + static_cast<long long>(w.r) * a.max_pages;
-      auto lookup = [&](int p) { return p >= p_begin && p < p_end ? table[p] : -1; };
-      int first = ((w.t.t0 + w.k) * BT) >> sh;  // page of lane 0's entry in `ids`
-      int ids = lookup(first + lane), more = lookup(first + 32 + lane);
+      PageIds ids;
+      ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
       for (int k = 0; k < tiles; ++k, ++i) {
         const int key0 = (w.t.t0 + w.k + k) * BT;
-        if ((key0 >> sh) >= first + 32) {
-          first += 32;
-          ids = more;
-          more = lookup(first + 32 + lane);
-        }
-        int page = __shfl_sync(kAll, ids, ((key0 >> sh) - first + lane) & 31);
-        if (lane >= npg) page = -1;
-        const bool have = page >= 0 && page < a.n_pages;
+        const int page = ids.get(a, key0, rows, npg, lane);
+        const bool have = page >= 0;
         const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(kAll, have)));
         const int s = i % C::NST;
         if (i >= C::NST) {
@@ -737,70 +531,62 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 }
 
 // Joins the partial states of the item that CTA c = blockIdx.x began and
-// others went on with: slots 2c + 1, 2(c + 1), 2(c + 2), ...; one CTA per
-// row.  Its warps take every fourth partial and meet in shared memory.
+// others went on with: slots 2c + 1, 2(c + 1), 2(c + 2), ...; a CTA takes every
+// gridDim.y-th of its rows.  Its warps take every fourth partial and meet in
+// shared memory.
 constexpr int kJoin = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedArgs a, int RT) {
   constexpr int CPL = D / 32;
   __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][D];
-  const int c = blockIdx.x, r = blockIdx.y;
+  const int c = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel runs
   const Cut cut = static_cast<const Cut*>(a.cuts)[c];
-  if (cut.last < 0 || r >= cut.rows) return;
+  if (cut.last < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int np = cut.last - c + 1;
-  auto slot = [&](int p) { return static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * RT + r; };
-  float mx = -INFINITY;
-  for (int p = threadIdx.x; p < np; p += 32 * kJoin) mx = fmaxf(mx, a.pm[slot(p)]);
+  const int np = cut.last - c + 1, g = a.heads / a.kv_heads;
+  for (int r = blockIdx.y; r < cut.rows; r += gridDim.y) {
+    auto slot = [&](int p) { return static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * RT + r; };
+    float mx = -INFINITY;
+    for (int p = threadIdx.x; p < np; p += 32 * kJoin) mx = fmaxf(mx, a.pm[slot(p)]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-  if (lane == 0) s_m[warp] = mx;
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+    if (lane == 0) s_m[warp] = mx;
+    __syncthreads();
 #pragma unroll
-  for (int x = 0; x < kJoin; ++x) mx = fmaxf(mx, s_m[x]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float acc[CPL], l = 0.f;
+    for (int x = 0; x < kJoin; ++x) mx = fmaxf(mx, s_m[x]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float acc[CPL], l = 0.f;
 #pragma unroll
-  for (int x = 0; x < CPL; ++x) acc[x] = 0.f;
-  for (int p = warp; p < np; p += kJoin) {
-    const long long at = slot(p);
-    const float e = ex2(a.pm[at] - ref);
-    l = fmaf(a.pl[at], e, l);
+    for (int x = 0; x < CPL; ++x) acc[x] = 0.f;
+#pragma unroll 4
+    for (int p = warp; p < np; p += kJoin) {
+      const long long at = slot(p);
+      const float e = ex2(a.pm[at] - ref);
+      l = fmaf(a.pl[at], e, l);
 #pragma unroll
-    for (int x = 0; x < CPL; ++x) acc[x] = fmaf(a.po[at * D + CPL * lane + x], e, acc[x]);
+      for (int x = 0; x < CPL; ++x) acc[x] = fmaf(a.po[at * D + CPL * lane + x], e, acc[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < CPL; ++x) s_o[warp][CPL * lane + x] = acc[x];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int x = 0; x < kJoin; ++x) l += s_l[x];
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int rr = cut.rr0 + r, j = rr / g;
+    const long long row = static_cast<long long>(cut.row0 + j) * a.heads + cut.kh * g + (rr - j * g);
+    for (int x = threadIdx.x; x < D; x += 32 * kJoin) {
+      float y = 0.f;
+#pragma unroll
+      for (int p = 0; p < kJoin; ++p) y += s_o[p][x];
+      if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + x] = __float2bfloat16_rn(y * inv);
+      else static_cast<float*>(a.out)[row * D + x] = y * inv;
+    }
+    if (threadIdx.x == 0) a.lse[row] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+    __syncthreads();
   }
-#pragma unroll
-  for (int x = 0; x < CPL; ++x) s_o[warp][CPL * lane + x] = acc[x];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int x = 0; x < kJoin; ++x) l += s_l[x];
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int g = a.heads / a.kv_heads, rr = cut.rr0 + r;
-  const long long row = static_cast<long long>(cut.row0 + rr / g) * a.heads + cut.kh * g + rr % g;
-  for (int x = threadIdx.x; x < D; x += 32 * kJoin) {
-    float y = 0.f;
-#pragma unroll
-    for (int p = 0; p < kJoin; ++p) y += s_o[p][x];
-    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + x] = __float2bfloat16_rn(y * inv);
-    else static_cast<float*>(a.out)[row * D + x] = y * inv;
-  }
-  if (threadIdx.x == 0) a.lse[row] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
-}
-
-// Opts a kernel into its dynamic shared memory, once per device.
-template <typename K>
-cudaError_t allow_smem(K* kernel, uint32_t bytes, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <int D, int NT>
@@ -819,13 +605,14 @@ int paged_row_tile(const PagedArgs& a) {
   // Rows per request and KV head on average (exact when every request has
   // the same number of new tokens).
   const long long rows = (a.T + a.n_req - 1) / a.n_req * (a.heads / a.kv_heads);
-  return rows <= 8 ? 8 : 16;
+  return rows <= 8 ? 8 : (rows <= 16 ? 16 : 128);
 }
 
 size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas); }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  if (row_tile == 128) return launch_paged_tc(a, d, ctas, tk, tv, st);
   if (d == 128)
     return row_tile == 8 ? decode_t<128, 1>(a, ctas, tk, tv, st) : decode_t<128, 2>(a, ctas, tk, tv, st);
   return row_tile == 8 ? decode_t<64, 1>(a, ctas, tk, tv, st) : decode_t<64, 2>(a, ctas, tk, tv, st);
@@ -836,7 +623,7 @@ cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_ti
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile < 16 ? row_tile : 16));
   cfg.blockDim = dim3(32 * kJoin);
   cfg.stream = st;
   cfg.attrs = &at;

@@ -1,0 +1,511 @@
+// Paged decode for more than 16 query rows of a KV head (many new tokens, or
+// many heads on one KV head): row tiles of 128 on tcgen05.  Same mathematics,
+// work list, partial states and joining launch as paged_kernel.cu, with key
+// tiles of 128 and one CTA per SM.
+//
+// With rows this many the mma.sync form is bound by its products (each 8 rows
+// cost another 13 cycles per 16 x 16 block and SM quarter: 2.5 TB/s of pages
+// at 32 rows, 0.7 at 128); here a tile's products are 128 rows at once, and
+// the read of the pages is the bound again.
+//
+// Roles of the 12 warps: 0-3 softmax (a thread has a row), 4-7 the output sum
+// (a thread has a row), 8 K loads and the walk over the items, 9 V loads, 10
+// the products, 11 query rows.
+//   S(k) = Q K(k)^T, two buffers in TMEM.  The softmax writes P(k) as three
+//   bf16 terms (8 + 8 + 8 bits of the weights, so that the fp32 result has
+//   them in fp32): two over S(k), one beside.  T = P(k) V(k), the small terms
+//   first, goes to a buffer of its own, and the output sum takes it as
+//   o = o alpha + T in fp32 registers: the tensor core's own accumulation over
+//   many tiles truncates, and O never needs a rescale in TMEM.
+// Rows of V outside the item's keys may hold anything (NaN times a zero weight
+// is NaN): in tiles that such rows are part of, the softmax warps zero them in
+// shared memory before P(k) is handed over.
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "paged_walk.cuh"
+
+namespace ra {
+
+__device__ int g_paged_tc_status = 0;
+
+namespace {
+
+using namespace paged;
+
+constexpr int BT = 128;          // keys per tile
+constexpr int RT = 128;          // query rows of an item
+constexpr int kThreads = 384;
+constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
+
+// An item, or the part of it that a CTA has.  Positions are relative to the
+// item's first key tile.
+struct Item {
+  int rows;   // query rows
+  int rr0;    // the first: row rr is token rr / g, head kh * g + rr % g
+  int row0;   // q row of the request's first token
+  int kh;
+  int end0;   // keys that token 0 of the request sees end here
+  int base;   // position of the item's first key tile
+  int lo, hi; // keys that any row sees
+  int k0;     // first key tile here
+  int tiles;  // key tiles here
+  int slot;   // partial slot, or -1: the item is whole
+  int pad;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int NCH = D / 64;
+  static constexpr uint32_t TILE = BT * D * 2;
+  static constexpr int NST = D == 128 ? 3 : 6;  // stages of one K and one V tile
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_ST = TILE;      // stage s: K at OFF_ST + 2 s TILE, V after it
+  static constexpr uint32_t OFF_AL = OFF_ST + NST * 2 * TILE;  // alpha of three tiles
+  static constexpr uint32_t OFF_ML = OFF_AL + 3 * RT * 4;      // m and l of an item
+  static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * RT * 4;
+  // Barriers: K and V tiles in, stage free; S(k), P(k) (two buffers each);
+  // T(k) ready and read; alpha of a tile; query rows in and read; item record
+  // in and read; an item's m and l in and read; drain.
+  static constexpr int B_KF = 0, B_VF = B_KF + NST, B_E = B_VF + NST, B_S = B_E + NST,
+                       B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 1, B_AL = B_TF + 1,
+                       B_Q = B_AL + 3, B_QF = B_Q + 1, B_I = B_QF + 1, B_IF = B_I + 2,
+                       B_ML = B_IF + 2, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 1, NBAR = B_DRAIN + 1;
+  static constexpr uint32_t OFF_BAR = OFF_ITEM + 2 * sizeof(Item);
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr uint32_t SMEM = OFF_MISC + 16;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  // TMEM columns: S buffers (fp32; P's first two terms over them), the third
+  // terms, T.
+  static constexpr uint32_t C_S = 0, C_LO = 256, C_T = 384;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const PagedArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* const status = &g_paged_tc_status;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.heads / a.kv_heads;
+  Cut* cuts = static_cast<Cut*>(a.cuts);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < C::NBAR; ++i) {
+      uint32_t n = 1;
+      if (i == C::B_P || i == C::B_P + 1 || i == C::B_TF || i == C::B_ML || i == C::B_MLF ||
+          (i >= C::B_AL && i < C::B_AL + 3))
+        n = 128;
+      if (i == C::B_Q) n = 32;
+      if (i == C::B_IF || i == C::B_IF + 1) n = 10;  // warps 0-7, 10, 11
+      mbar_init(bar(i), n);
+    }
+    int abort = *reinterpret_cast<volatile int*>(status);
+    // The swizzled tiles need 1024-byte alignment, which the declaration asks
+    // for; a loader that ignored it would be reported, not computed with.
+    if (sb & 1023u) abort = atomicCAS(status, 0, 0x9f) | 0x9f;
+    *abort_flag = abort;
+    fence_mbar_init();
+    cuts[blockIdx.x].last = -1;
+  }
+  const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_AL);  // synchronizes
+  if (run.first >= run.last || *abort_flag) return;
+  if (warp == 10) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();  // also: the scratch of find_run has been read
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long lim = a.wait_limit;
+  const int total = static_cast<int>(run.last - run.first);  // tiles of this CTA
+  Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
+  float* s_al = reinterpret_cast<float*>(smem + C::OFF_AL);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_l = s_m + RT;
+  auto wait = [&](int b, uint32_t parity, int code) {
+    const bool w = wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
+    return static_cast<bool>(__all_sync(kAll, w));
+  };
+  // The record of item n, once it is there; its reader releases it itself.
+  auto wait_item = [&](int n) { return wait(C::B_I + (n & 1), static_cast<uint32_t>(n >> 1), 0x91); };
+  auto free_item = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_IF + (n & 1)));
+  };
+
+  if (warp >= 8) {
+    regs_dec<96>();
+    if (warp == 8 || warp == 9) {
+      // -------------------------------------------------------------- K and V loads
+      const bool is_k = warp == 8;
+      const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
+      const int full = is_k ? C::B_KF : C::B_VF;
+      const int sh = a.page_shift;
+      const int rows = sh < 6 ? 1 << sh : 64;  // of a box
+      const int boxes = BT / rows;
+      const uint32_t box = static_cast<uint32_t>(rows) * 128u;
+      Walk<BT> w;
+      w.start(a, g, RT, run.r, run.x);
+      long long u = run.first;
+      bool ok = true;
+      int i = 0, it = 0;
+      while (ok && u < run.last) {
+        const long long left = run.last - u;
+        const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
+        if (is_k) {
+          if (it >= 2) ok = wait(C::B_IF + (it & 1), static_cast<uint32_t>(it >> 1) ^ 1u, 0x92);
+          if (!ok) break;
+          if (lane == 0) {
+            const long long item0 = u - w.k;
+            const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
+            const int me = static_cast<int>(blockIdx.x);
+            const int base = w.t.t0 * BT, n = w.t.rr1 - w.t.rr0;
+            items[it & 1] = Item{n, w.t.rr0, w.q.row0, w.kh, w.q.len - w.q.n + 1 - base, base,
+                                 w.t.lo - base, w.t.hi - base, w.k, tiles,
+                                 c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), 0};
+            if (c0 != c1 && me == c0) cuts[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
+            mbar_arrive(bar(C::B_I + (it & 1)));
+          }
+          __syncwarp();
+          ++it;
+        }
+        PageIds ids;
+        ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
+        for (int k = 0; k < tiles; ++k, ++i) {
+          const int key0 = (w.t.t0 + w.k + k) * BT;
+          const int page = ids.get(a, key0, rows, boxes, lane);
+          const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(kAll, page >= 0)));
+          const int s = i % C::NST;
+          if (i >= C::NST) ok = wait(C::B_E + s, static_cast<uint32_t>(i / C::NST) ^ 1u, 0x93);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full + s), n * box * C::NCH);
+          __syncwarp();
+          if (page >= 0) {
+            const uint32_t dst = sb + C::OFF_ST + s * 2 * C::TILE + (is_k ? 0 : C::TILE) + lane * box;
+            const int row = (key0 + lane * rows) & ((1 << sh) - 1);
+#pragma unroll
+            for (int ch = 0; ch < C::NCH; ++ch)
+              tma_load_4d(dst + ch * CHB, tm, bar(full + s), ch * 64, w.kh, row, page);
+          }
+        }
+        u += tiles;
+        if (ok && u < run.last) w.next(a, g, RT);
+      }
+      if (!ok) {  // let the copies in flight land before the CTA leaves
+        volatile int no_abort = 0;
+        for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j)
+          wait_bar(bar(full + j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
+      }
+    } else if (warp == 11) {
+      // -------------------------------------------------------------- query rows
+      for (int it = 0, done = 0; done < total; ++it) {
+        if (!wait_item(it)) break;
+        const Item x = items[it & 1];
+        free_item(it);
+        done += x.tiles;
+        if (it > 0 && !wait(C::B_QF, static_cast<uint32_t>(it - 1), 0x94)) break;
+        // Chunk c of row r at c ^ (r % 8) inside its 64 columns, as a TMA load
+        // with 128-byte swizzle would put it; rows past the item's are zero.
+        for (int y = lane; y < RT * D / 8; y += 32) {
+          const int r = y / (D / 8), c = y % (D / 8), rr = x.rr0 + r, j = rr / g;
+          const bool in = r < x.rows;
+          const long long row = in ? static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g) : 0;
+          copy16(sb + C::OFF_Q + (c >> 3) * CHB + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                 static_cast<const __nv_bfloat16*>(a.q) + row * D + c * 8, in ? 16u : 0u);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::B_Q));
+      }
+    } else {
+      // -------------------------------------------------------------- products (warp 10)
+      const uint32_t lead = lane == 0 ? 1u : 0u;
+      constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
+      const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
+      int it = 0, left = 0;  // of the item whose S come next
+      bool ok = true;
+      // S(k) = Q K(k)^T into buffer k % 2.
+      auto qk = [&](int k) {
+        if (left == 0) {
+          ok = wait_item(it);
+          if (!ok) return;
+          left = items[it & 1].tiles;
+          free_item(it);
+          ok = wait(C::B_Q, static_cast<uint32_t>(it), 0x95);
+          if (!ok) return;
+          ++it;
+        }
+        const int st = k % C::NST;
+        ok = wait(C::B_KF + st, static_cast<uint32_t>(k / C::NST), 0x96);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
+        const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
+          mma_ss_lead(lead, sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit_lead(lead, bar(C::B_S + (k & 1)));
+        if (--left == 0) tc_commit_lead(lead, bar(C::B_QF));
+      };
+      qk(0);
+      if (ok && total > 1) qk(1);
+      for (int k = 0; k < total && ok; ++k) {
+        const int st = k % C::NST;
+        ok = wait(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97) &&
+             wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
+             (k == 0 || wait(C::B_TF, static_cast<uint32_t>(k - 1), 0x99));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
+        const uint32_t pbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
+        const uint32_t term[3] = {tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64, pbuf + 64, pbuf};
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int kk = 0; kk < BT / 16; ++kk)
+            mma_ts_lead(lead, tmem + C::C_T, term[x] + kk * 8,
+                        vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, x + kk > 0 ? 1u : 0u);
+        tc_commit_lead(lead, bar(C::B_E + st));
+        tc_commit_lead(lead, bar(C::B_T));
+        if (k + 2 < total) qk(k + 2);  // after P(k)'s product, which reads that buffer, in issue order
+      }
+      volatile int no_abort = 0;
+      tc_commit_lead(lead, bar(C::B_DRAIN));
+      wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    regs_inc<200>();
+    const int r = tid;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float sl2 = a.scale_log2;
+    const uint64_t sl2x2 = f2pack(sl2, sl2);
+    const int win = static_cast<int>(a.window);
+    bool ok = true;
+    int k = 0;  // tile
+    for (int it = 0; ok && k < total; ++it) {
+      ok = wait_item(it);
+      if (!ok) break;
+      const Item x = items[it & 1];
+      free_item(it);
+      // Keys [lo, hi) of the row (rows past the item's do as its last).
+      const int rr = x.rr0 + (r < x.rows ? r : x.rows - 1);
+      int hi = x.end0 + rr / g;
+      if (hi < -x.base) hi = -x.base;
+      const int lo = win > 0 && hi + x.base > win ? hi - win : -x.base;
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < x.tiles; ++t, ++k) {
+        const uint32_t s_col = C::C_S + static_cast<uint32_t>(k & 1) * BT;
+        const uint32_t lo_col = C::C_LO + static_cast<uint32_t>(k & 1) * 64;
+        ok = wait(C::B_S + (k & 1), static_cast<uint32_t>(k >> 1), 0x9a);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tl + s_col + cc * 32, sr[cc]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) reg_fence32(sr[cc]);
+        const int k0 = (x.k0 + t) * BT;
+        const int lo_j = lo - k0, hi_j = hi - k0;
+        if (lo_j > 0 || hi_j < BT) {
+#pragma unroll
+          for (int j = 0; j < BT; ++j)
+            if (j < lo_j || j >= hi_j) sr[j >> 5][j & 31] = 0xff800000u;  // -inf
+        }
+#define RA_S(j) __uint_as_float(sr[(j) >> 5][(j) & 31])
+        float mx0 = fmaxf(RA_S(0), RA_S(4)), mx1 = fmaxf(RA_S(1), RA_S(5));
+        float mx2 = fmaxf(RA_S(2), RA_S(6)), mx3 = fmaxf(RA_S(3), RA_S(7));
+#pragma unroll
+        for (int j = 8; j < BT; j += 8) {
+          mx0 = fmax3(mx0, RA_S(j + 0), RA_S(j + 4));
+          mx1 = fmax3(mx1, RA_S(j + 1), RA_S(j + 5));
+          mx2 = fmax3(mx2, RA_S(j + 2), RA_S(j + 6));
+          mx3 = fmax3(mx3, RA_S(j + 3), RA_S(j + 7));
+        }
+        const float mn = fmaxf(m, fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2(m - ref);
+        m = mn;
+        s_al[(k % 3) * RT + r] = alpha;
+        mbar_arrive(bar(C::B_AL + k % 3));
+        const uint64_t nm2 = f2pack(-ref, -ref);
+        uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t p0[16], p1[16], p2[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float y0, y1;
+            f2unpack(ffma2(f2pack(__uint_as_float(sr[cc][j]), __uint_as_float(sr[cc][j + 1])), sl2x2, nm2), y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            uint64_t y = f2pack(y0, y1);
+            if (j & 2) acc1 = fadd2(acc1, y);
+            else acc0 = fadd2(acc0, y);
+            uint32_t h = bf16x2_rn(y0, y1);
+            p0[j / 2] = h;
+            y0 -= __uint_as_float(h << 16);
+            y1 -= __uint_as_float(h & 0xffff0000u);
+            h = bf16x2_rn(y0, y1);
+            p1[j / 2] = h;
+            y0 -= __uint_as_float(h << 16);
+            y1 -= __uint_as_float(h & 0xffff0000u);
+            p2[j / 2] = bf16x2_rn(y0, y1);
+          }
+          tmem_st16(tl + s_col + cc * 16, p0);
+          tmem_st16(tl + s_col + 64 + cc * 16, p1);
+          tmem_st16(tl + lo_col + cc * 16, p2);
+        }
+#undef RA_S
+        if (x.lo > k0 || x.hi < k0 + BT) {
+          // Key row r of this tile is nobody's: zero it for the product.
+          const int st = k % C::NST;
+          ok = wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x9b);
+          if (!ok) break;
+          const int key = k0 + r;
+          if (key < x.lo || key >= x.hi) {
+#pragma unroll
+            for (int ch = 0; ch < C::NCH; ++ch)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                st_shared_v4(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE + ch * CHB + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(C::B_P + (k & 1)));
+        float sa, sc;
+        f2unpack(fadd2(acc0, acc1), sa, sc);
+        l = fmaf(l, alpha, sa + sc);
+      }
+      if (!ok) break;
+      // The output warps have read the m and l of the item before.
+      if (it > 0) ok = wait(C::B_MLF, static_cast<uint32_t>(it - 1), 0x9c);
+      if (!ok) break;
+      s_m[r] = m;
+      s_l[r] = l;
+      mbar_arrive(bar(C::B_ML));
+    }
+  } else {
+    // ---------------------------------------------------------------- output sum
+    regs_inc<208>();
+    const int r = tid - 128;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool ok = true;
+    int k = 0;
+    for (int it = 0; ok && k < total; ++it) {
+      ok = wait_item(it);
+      if (!ok) break;
+      const Item x = items[it & 1];
+      free_item(it);
+      uint64_t o[D / 2];
+#pragma unroll
+      for (int j = 0; j < D / 2; ++j) o[j] = f2pack(0.f, 0.f);
+      for (int t = 0; t < x.tiles; ++t, ++k) {
+        ok = wait(C::B_AL + k % 3, static_cast<uint32_t>(k / 3), 0x9d);
+        if (!ok) break;
+        const float al = s_al[(k % 3) * RT + r];
+        const uint64_t al2 = f2pack(al, al);
+        ok = wait(C::B_T, static_cast<uint32_t>(k), 0x9e);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t v[32];
+          tmem_ld32(tl + C::C_T + cc * 32, v);
+          tmem_wait_ld();
+          reg_fence32(v);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            o[cc * 16 + j / 2] = ffma2(o[cc * 16 + j / 2], al2,
+                                       f2pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::B_TF));
+      }
+      if (!ok) break;
+      ok = wait(C::B_ML, static_cast<uint32_t>(it), 0xa0);
+      if (!ok) break;
+      const float m = s_m[r], l = s_l[r];
+      mbar_arrive(bar(C::B_MLF));
+      if (r >= x.rows) continue;
+      const int rr = x.rr0 + r, j0 = rr / g;
+      const long long row = x.slot >= 0 ? static_cast<long long>(x.slot) * RT + r
+                                        : static_cast<long long>(x.row0 + j0) * a.heads + x.kh * g + (rr - j0 * g);
+      const float inv = x.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      const bool bf16 = x.slot < 0 && a.out_bf16;
+      float* dst = (x.slot >= 0 ? a.po : static_cast<float*>(a.out)) + row * D;
+      __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(a.out) + row * D;
+#pragma unroll
+      for (int j = 0; j < D / 2; j += 4) {
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f2unpack(o[j + c], y[2 * c], y[2 * c + 1]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) y[c] *= inv;
+        if (bf16) {
+          *reinterpret_cast<uint4*>(dst16 + 2 * j) = make_uint4(bf16x2_rn(y[0], y[1]), bf16x2_rn(y[2], y[3]),
+                                                                bf16x2_rn(y[4], y[5]), bf16x2_rn(y[6], y[7]));
+        } else {
+          reinterpret_cast<float4*>(dst + 2 * j)[0] = make_float4(y[0], y[1], y[2], y[3]);
+          reinterpret_cast<float4*>(dst + 2 * j)[1] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      }
+      if (x.slot >= 0) {
+        a.pm[row] = m;
+        a.pl[row] = l;
+      } else {
+        a.lse[row] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(paged_tc_kernel<D>, Cfg<D>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  paged_tc_kernel<D><<<ctas, kThreads, Cfg<D>::SMEM, st>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk,
+                            const CUtensorMap& tv, cudaStream_t st) {
+  return d == 128 ? launch_d<128>(a, ctas, tk, tv, st) : launch_d<64>(a, ctas, tk, tv, st);
+}
+
+cudaError_t take_paged_tc_status(int* code) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_paged_tc_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_paged_tc_status, &zero, sizeof(int));
+}
+
+}  // namespace ra

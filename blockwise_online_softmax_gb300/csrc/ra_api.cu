@@ -1239,6 +1239,9 @@ int ra_device_status(void* stream) {
   if ((e = ra::take_decode_status(&c)) != cudaSuccess) return cuda_fail(e, "reading the decode kernel status");
   if ((e = ra::take_bwd_status(&w)) != cudaSuccess) return cuda_fail(e, "reading the backward kernel status");
   if ((e = ra::take_paged_status(&p)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
+  int pt = 0;
+  if ((e = ra::take_paged_tc_status(&pt)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
+  if (p == 0) p = pt;
   if (a != 0 || b != 0 || c != 0 || w != 0 || p != 0)
     return fail(RA_ERR_TIMEOUT,
                 "a kernel gave up a bounded wait (codes 0x%x, 0x%x, 0x%x, 0x%x, 0x%x)", a, b, c, w,

@@ -129,7 +129,8 @@ struct PagedArgs {
   float* pl;
   void* cuts;
 };
-// Query rows (of one request and KV head) that a CTA takes together.
+// Query rows (of one request and KV head) that a CTA takes together: 8 or 16
+// (paged_kernel.cu, two CTAs per SM) or 128 (paged_tc_kernel.cu, one).
 int paged_row_tile(const PagedArgs& a);
 size_t paged_cut_bytes(int ctas);
 // tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
@@ -137,6 +138,9 @@ size_t paged_cut_bytes(int ctas);
 cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st);
+cudaError_t launch_paged_tc(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk,
+                            const CUtensorMap& tv, cudaStream_t st);
 cudaError_t take_paged_status(int* code);
+cudaError_t take_paged_tc_status(int* code);
 
 }  // namespace ra
