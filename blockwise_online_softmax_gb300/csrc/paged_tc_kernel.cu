@@ -8,9 +8,11 @@
 // at 32 rows, 0.7 at 128); here a tile's products are 128 rows at once, and
 // the read of the pages is the bound again.
 //
-// Roles of the 12 warps: 0-3 softmax (a thread has a row), 4-7 the output sum
-// (a thread has a row), 8 K loads and the walk over the items, 9 V loads, 10
-// the products, 11 query rows.
+// Roles of the 16 warps: 0-7 softmax (a row has two threads, one for each half
+// of a tile's keys, that exchange their maxima), 8-11 the output sum (a thread
+// has a row), 12 K loads and the walk over the items, 13 V loads, 14 the
+// products, 15 query rows.  With one softmax thread per row its 128 weights,
+// split in three terms each, took 4700 cycles a tile, twice the products.
 //   S(k) = Q K(k)^T, two buffers in TMEM.  The softmax writes P(k) as three
 //   bf16 terms (8 + 8 + 8 bits of the weights, so that the fp32 result has
 //   them in fp32): two over S(k), one beside.  T = P(k) V(k), the small terms
@@ -38,7 +40,7 @@ using namespace paged;
 
 constexpr int BT = 128;          // keys per tile
 constexpr int RT = 128;          // query rows of an item
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
 
 // An item, or the part of it that a CTA has.  Positions are relative to the
@@ -64,15 +66,16 @@ struct Cfg {
   static constexpr int NST = D == 128 ? 3 : 6;  // stages of one K and one V tile
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_ST = TILE;      // stage s: K at OFF_ST + 2 s TILE, V after it
-  static constexpr uint32_t OFF_AL = OFF_ST + NST * 2 * TILE;  // alpha of three tiles
-  static constexpr uint32_t OFF_ML = OFF_AL + 3 * RT * 4;      // m and l of an item
-  static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * RT * 4;
+  static constexpr uint32_t OFF_AL = OFF_ST + NST * 2 * TILE;  // alpha of two tiles
+  static constexpr uint32_t OFF_X = OFF_AL + 2 * RT * 4;       // exchange of a row's two threads
+  static constexpr uint32_t OFF_INV = OFF_X + 2 * RT * 4;      // 1 / l of an item's rows
+  static constexpr uint32_t OFF_ITEM = OFF_INV + RT * 4;
   // Barriers: K and V tiles in, stage free; S(k), P(k) (two buffers each);
-  // T(k) ready and read; alpha of a tile; query rows in and read; item record
-  // in and read; an item's m and l in and read; drain.
+  // T(k) ready; T(k) and alpha(k) read; alpha(k) there; query rows in and
+  // read; item record in and read; an item's 1 / l in and read; drain.
   static constexpr int B_KF = 0, B_VF = B_KF + NST, B_E = B_VF + NST, B_S = B_E + NST,
-                       B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 1, B_AL = B_TF + 1,
-                       B_Q = B_AL + 3, B_QF = B_Q + 1, B_I = B_QF + 1, B_IF = B_I + 2,
+                       B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 1, B_AL = B_TF + 2,
+                       B_Q = B_AL + 2, B_QF = B_Q + 1, B_I = B_QF + 1, B_IF = B_I + 2,
                        B_ML = B_IF + 2, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 1, NBAR = B_DRAIN + 1;
   static constexpr uint32_t OFF_BAR = OFF_ITEM + 2 * sizeof(Item);
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
@@ -82,6 +85,13 @@ struct Cfg {
   // terms, T.
   static constexpr uint32_t C_S = 0, C_LO = 256, C_T = 384;
 };
+
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -101,11 +111,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < C::NBAR; ++i) {
       uint32_t n = 1;
-      if (i == C::B_P || i == C::B_P + 1 || i == C::B_TF || i == C::B_ML || i == C::B_MLF ||
-          (i >= C::B_AL && i < C::B_AL + 3))
-        n = 128;
+      if (i == C::B_P || i == C::B_P + 1) n = 256;
+      if ((i >= C::B_TF && i < C::B_AL + 2) || i == C::B_ML || i == C::B_MLF) n = 128;
       if (i == C::B_Q) n = 32;
-      if (i == C::B_IF || i == C::B_IF + 1) n = 10;  // warps 0-7, 10, 11
+      if (i == C::B_IF || i == C::B_IF + 1) n = 14;  // warps 0-11, 14, 15
       mbar_init(bar(i), n);
     }
     int abort = *reinterpret_cast<volatile int*>(status);
@@ -118,7 +127,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   }
   const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_AL);  // synchronizes
   if (run.first >= run.last || *abort_flag) return;
-  if (warp == 10) {
+  if (warp == 14) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -130,8 +139,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const int total = static_cast<int>(run.last - run.first);  // tiles of this CTA
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   float* s_al = reinterpret_cast<float*>(smem + C::OFF_AL);
-  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
-  float* s_l = s_m + RT;
+  float* s_x = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* s_inv = reinterpret_cast<float*>(smem + C::OFF_INV);
   auto wait = [&](int b, uint32_t parity, int code) {
     const bool w = wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
     return static_cast<bool>(__all_sync(kAll, w));
@@ -143,11 +152,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     if (lane == 0) mbar_arrive(bar(C::B_IF + (n & 1)));
   };
 
-  if (warp >= 8) {
-    regs_dec<96>();
-    if (warp == 8 || warp == 9) {
+  if (warp >= 12) {
+    regs_dec<88>();
+    if (warp == 12 || warp == 13) {
       // -------------------------------------------------------------- K and V loads
-      const bool is_k = warp == 8;
+      const bool is_k = warp == 12;
       const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
       const int full = is_k ? C::B_KF : C::B_VF;
       const int sh = a.page_shift;
@@ -206,7 +215,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j)
           wait_bar(bar(full + j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
       }
-    } else if (warp == 11) {
+    } else if (warp == 15) {
       // -------------------------------------------------------------- query rows
       for (int it = 0, done = 0; done < total; ++it) {
         if (!wait_item(it)) break;
@@ -214,22 +223,31 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         free_item(it);
         done += x.tiles;
         if (it > 0 && !wait(C::B_QF, static_cast<uint32_t>(it - 1), 0x94)) break;
+        // Rows lane, lane + 32, ...: their index in q, found once.
+        int row[RT / 32];
+#pragma unroll
+        for (int y = 0; y < RT / 32; ++y) {
+          const int r = 32 * y + lane, rr = x.rr0 + (r < x.rows ? r : 0), j = rr / g;
+          row[y] = (x.row0 + j) * a.heads + x.kh * g + (rr - j * g);
+        }
         // Chunk c of row r at c ^ (r % 8) inside its 64 columns, as a TMA load
         // with 128-byte swizzle would put it; rows past the item's are zero.
-        for (int y = lane; y < RT * D / 8; y += 32) {
-          const int r = y / (D / 8), c = y % (D / 8), rr = x.rr0 + r, j = rr / g;
-          const bool in = r < x.rows;
-          const long long row = in ? static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g) : 0;
-          copy16(sb + C::OFF_Q + (c >> 3) * CHB + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                 static_cast<const __nv_bfloat16*>(a.q) + row * D + c * 8, in ? 16u : 0u);
-        }
+        constexpr int CPR = D / 8;  // chunks of a row
+#pragma unroll
+        for (int y = 0; y < RT / 32; ++y)
+#pragma unroll 4
+          for (int z = 0; z < CPR; ++z) {
+            const int r = 32 * y + (z * 32 + lane) / CPR, c = (z * 32 + lane) % CPR;
+            const long long at = static_cast<long long>(__shfl_sync(kAll, row[y], r & 31)) * D + c * 8;
+            copy16(sb + C::OFF_Q + (c >> 3) * CHB + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   static_cast<const __nv_bfloat16*>(a.q) + at, r < x.rows ? 16u : 0u);
+          }
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         mbar_arrive(bar(C::B_Q));
       }
     } else {
-      // -------------------------------------------------------------- products (warp 10)
-      const uint32_t lead = lane == 0 ? 1u : 0u;
+      // -------------------------------------------------------------- products (warp 14)
       constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
       const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
@@ -252,13 +270,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         tc_fence_after();
         const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
         const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
+        --left;
+        if (lane == 0) {  // one lane issues at the pipe's rate, a predicated warp does not
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
-          mma_ss_lead(lead, sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
+            mma_ss(sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(bar(C::B_S + (k & 1)));
+          if (left == 0) tc_commit(bar(C::B_QF));
         }
-        tc_commit_lead(lead, bar(C::B_S + (k & 1)));
-        if (--left == 0) tc_commit_lead(lead, bar(C::B_QF));
+        __syncwarp();
       };
       qk(0);
       if (ok && total > 1) qk(1);
@@ -266,95 +288,117 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int st = k % C::NST;
         ok = wait(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97) &&
              wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
-             (k == 0 || wait(C::B_TF, static_cast<uint32_t>(k - 1), 0x99));
+             (k == 0 || wait(C::B_TF + ((k - 1) & 1), static_cast<uint32_t>((k - 1) >> 1), 0x99));
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
         const uint32_t pbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
         const uint32_t term[3] = {tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64, pbuf + 64, pbuf};
+        if (lane == 0) {
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
+          for (int x = 0; x < 3; ++x)
 #pragma unroll
-          for (int kk = 0; kk < BT / 16; ++kk)
-            mma_ts_lead(lead, tmem + C::C_T, term[x] + kk * 8,
-                        vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, x + kk > 0 ? 1u : 0u);
-        tc_commit_lead(lead, bar(C::B_E + st));
-        tc_commit_lead(lead, bar(C::B_T));
+            for (int kk = 0; kk < BT / 16; ++kk)
+              mma_ts(tmem + C::C_T, term[x] + kk * 8, vd + static_cast<uint64_t>((kk * 2048) >> 4),
+                     idesc_pv, x + kk > 0 ? 1u : 0u);
+          tc_commit(bar(C::B_E + st));
+          tc_commit(bar(C::B_T));
+        }
+        __syncwarp();
         if (k + 2 < total) qk(k + 2);  // after P(k)'s product, which reads that buffer, in issue order
       }
       volatile int no_abort = 0;
-      tc_commit_lead(lead, bar(C::B_DRAIN));
+      if (lane == 0) tc_commit(bar(C::B_DRAIN));
       wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_inc<200>();
-    const int r = tid;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    // Warps 0-3 take keys 0-63 of a tile, warps 4-7 keys 64-127.  A wait that
+    // gave up shows at the next barrier of the two, where all of them leave.
+    regs_dec<120>();
+    constexpr int HT = BT / 2;
+    const int r = tid & 127, half = warp >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sl2 = a.scale_log2;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
     const int win = static_cast<int>(a.window);
     bool ok = true;
     int k = 0;  // tile
-    for (int it = 0; ok && k < total; ++it) {
-      ok = wait_item(it);
-      if (!ok) break;
-      const Item x = items[it & 1];
-      free_item(it);
+    for (int it = 0; k < total; ++it) {
+      ok = ok && wait_item(it);
+      Item x = items[it & 1];
+      if (ok) free_item(it);
+      else x.tiles = 1;
       // Keys [lo, hi) of the row (rows past the item's do as its last).
       const int rr = x.rr0 + (r < x.rows ? r : x.rows - 1);
       int hi = x.end0 + rr / g;
       if (hi < -x.base) hi = -x.base;
       const int lo = win > 0 && hi + x.base > win ? hi - win : -x.base;
       float m = -INFINITY, l = 0.f;
+      bool left = false;
       for (int t = 0; t < x.tiles; ++t, ++k) {
         const uint32_t s_col = C::C_S + static_cast<uint32_t>(k & 1) * BT;
-        const uint32_t lo_col = C::C_LO + static_cast<uint32_t>(k & 1) * 64;
-        ok = wait(C::B_S + (k & 1), static_cast<uint32_t>(k >> 1), 0x9a);
-        if (!ok) break;
+        const uint32_t lo_col = C::C_LO + static_cast<uint32_t>(k & 1) * (BT / 2);
+        ok = ok && wait(C::B_S + (k & 1), static_cast<uint32_t>(k >> 1), 0x9a);
         tc_fence_after();
-        uint32_t sr[4][32];
+        uint32_t sr[2][32];
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tl + s_col + cc * 32, sr[cc]);
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(tl + s_col + half * HT + cc * 32, sr[cc]);
         tmem_wait_ld();
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) reg_fence32(sr[cc]);
-        const int k0 = (x.k0 + t) * BT;
-        const int lo_j = lo - k0, hi_j = hi - k0;
-        if (lo_j > 0 || hi_j < BT) {
+        for (int cc = 0; cc < 2; ++cc) reg_fence32(sr[cc]);
+        const int k0 = (x.k0 + t) * BT, kh0 = k0 + half * HT;
+        const int lo_j = lo - kh0, hi_j = hi - kh0;
+        if (lo_j > 0 || hi_j < HT) {
 #pragma unroll
-          for (int j = 0; j < BT; ++j)
+          for (int j = 0; j < HT; ++j)
             if (j < lo_j || j >= hi_j) sr[j >> 5][j & 31] = 0xff800000u;  // -inf
         }
 #define RA_S(j) __uint_as_float(sr[(j) >> 5][(j) & 31])
         float mx0 = fmaxf(RA_S(0), RA_S(4)), mx1 = fmaxf(RA_S(1), RA_S(5));
         float mx2 = fmaxf(RA_S(2), RA_S(6)), mx3 = fmaxf(RA_S(3), RA_S(7));
 #pragma unroll
-        for (int j = 8; j < BT; j += 8) {
+        for (int j = 8; j < HT; j += 8) {
           mx0 = fmax3(mx0, RA_S(j + 0), RA_S(j + 4));
           mx1 = fmax3(mx1, RA_S(j + 1), RA_S(j + 5));
           mx2 = fmax3(mx2, RA_S(j + 2), RA_S(j + 6));
           mx3 = fmax3(mx3, RA_S(j + 3), RA_S(j + 7));
         }
-        const float mn = fmaxf(m, fmax3(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+        const float mine = fmax3(mx0, mx1, fmaxf(mx2, mx3));
+        // Everyone has read the exchange of the tile before, ...
+        tc_fence_before();
+        if (!named_bar_and(1, 256, ok)) {
+          left = true;
+          break;
+        }
+        s_x[half * RT + r] = mine;
+        // ... and has S in registers, over which P is written below.
+        named_bar_sync(2, 256);
+        tc_fence_after();
+        const float mn = fmaxf(m, fmaxf(mine, s_x[(half ^ 1) * RT + r]) * sl2);
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float alpha = ex2(m - ref);
         m = mn;
-        s_al[(k % 3) * RT + r] = alpha;
-        mbar_arrive(bar(C::B_AL + k % 3));
+        if (half == 0) {
+          // alpha(k - 2), in the same place, has been read.
+          if (k >= 2) ok = wait(C::B_TF + (k & 1), static_cast<uint32_t>((k - 2) >> 1), 0xa1);
+          s_al[(k & 1) * RT + r] = alpha;
+          mbar_arrive(bar(C::B_AL + (k & 1)));
+        }
         const uint64_t nm2 = f2pack(-ref, -ref);
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t p0[16], p1[16], p2[16];
+        for (int cc = 0; cc < 4; ++cc) {  // 16 keys
+          uint32_t p0[8], p1[8], p2[8];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+          for (int j = 0; j < 16; j += 2) {
+            const int e = cc * 16 + j;
             float y0, y1;
-            f2unpack(ffma2(f2pack(__uint_as_float(sr[cc][j]), __uint_as_float(sr[cc][j + 1])), sl2x2, nm2), y0, y1);
+            f2unpack(ffma2(f2pack(RA_S(e), RA_S(e + 1)), sl2x2, nm2), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
-            uint64_t y = f2pack(y0, y1);
+            const uint64_t y = f2pack(y0, y1);
             if (j & 2) acc1 = fadd2(acc1, y);
             else acc0 = fadd2(acc0, y);
             uint32_t h = bf16x2_rn(y0, y1);
@@ -367,23 +411,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             y1 -= __uint_as_float(h & 0xffff0000u);
             p2[j / 2] = bf16x2_rn(y0, y1);
           }
-          tmem_st16(tl + s_col + cc * 16, p0);
-          tmem_st16(tl + s_col + 64 + cc * 16, p1);
-          tmem_st16(tl + lo_col + cc * 16, p2);
+          const uint32_t col = tl + half * (HT / 2) + cc * 8;
+          tmem_st8(col + s_col, p0);
+          tmem_st8(col + s_col + BT / 2, p1);
+          tmem_st8(col + lo_col, p2);
         }
 #undef RA_S
-        if (x.lo > k0 || x.hi < k0 + BT) {
-          // Key row r of this tile is nobody's: zero it for the product.
+        if (half < C::NCH && (x.lo > k0 || x.hi < k0 + BT)) {
+          // Key row r of this tile is nobody's: zero (half of) it for the product.
           const int st = k % C::NST;
-          ok = wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x9b);
-          if (!ok) break;
+          ok = ok && wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x9b);
           const int key = k0 + r;
           if (key < x.lo || key >= x.hi) {
 #pragma unroll
-            for (int ch = 0; ch < C::NCH; ++ch)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                st_shared_v4(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE + ch * CHB + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c)
+              st_shared_v4(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE + half * CHB + r * 128 + c * 16, 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
@@ -394,18 +436,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         f2unpack(fadd2(acc0, acc1), sa, sc);
         l = fmaf(l, alpha, sa + sc);
       }
-      if (!ok) break;
-      // The output warps have read the m and l of the item before.
-      if (it > 0) ok = wait(C::B_MLF, static_cast<uint32_t>(it - 1), 0x9c);
-      if (!ok) break;
-      s_m[r] = m;
-      s_l[r] = l;
-      mbar_arrive(bar(C::B_ML));
+      if (left) break;
+      // A row's two sums meet; the first thread hands 1 / l to the output and
+      // writes the row's statistics.
+      if (!named_bar_and(1, 256, ok)) break;
+      if (half == 1) s_x[RT + r] = l;
+      named_bar_sync(2, 256);
+      if (half == 0) {
+        l += s_x[RT + r];
+        if (it > 0) ok = wait(C::B_MLF, static_cast<uint32_t>(it - 1), 0x9c);
+        s_inv[r] = x.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+        mbar_arrive(bar(C::B_ML));
+        if (r < x.rows) {
+          if (x.slot >= 0) {
+            a.pm[x.slot * RT + r] = m;
+            a.pl[x.slot * RT + r] = l;
+          } else {
+            const int j = rr / g;
+            a.lse[static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g)] =
+                l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+          }
+        }
+      }
     }
   } else {
     // ---------------------------------------------------------------- output sum
-    regs_inc<208>();
-    const int r = tid - 128;
+    regs_inc<184>();
+    const int r = tid & 127;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool ok = true;
     int k = 0;
@@ -418,9 +475,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
       for (int j = 0; j < D / 2; ++j) o[j] = f2pack(0.f, 0.f);
       for (int t = 0; t < x.tiles; ++t, ++k) {
-        ok = wait(C::B_AL + k % 3, static_cast<uint32_t>(k / 3), 0x9d);
+        ok = wait(C::B_AL + (k & 1), static_cast<uint32_t>(k >> 1), 0x9d);
         if (!ok) break;
-        const float al = s_al[(k % 3) * RT + r];
+        const float al = s_al[(k & 1) * RT + r];
         const uint64_t al2 = f2pack(al, al);
         ok = wait(C::B_T, static_cast<uint32_t>(k), 0x9e);
         if (!ok) break;
@@ -437,18 +494,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                                        f2pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
         }
         tc_fence_before();
-        mbar_arrive(bar(C::B_TF));
+        mbar_arrive(bar(C::B_TF + (k & 1)));
       }
       if (!ok) break;
       ok = wait(C::B_ML, static_cast<uint32_t>(it), 0xa0);
       if (!ok) break;
-      const float m = s_m[r], l = s_l[r];
+      const float inv = s_inv[r];
       mbar_arrive(bar(C::B_MLF));
       if (r >= x.rows) continue;
       const int rr = x.rr0 + r, j0 = rr / g;
       const long long row = x.slot >= 0 ? static_cast<long long>(x.slot) * RT + r
                                         : static_cast<long long>(x.row0 + j0) * a.heads + x.kh * g + (rr - j0 * g);
-      const float inv = x.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
       const bool bf16 = x.slot < 0 && a.out_bf16;
       float* dst = (x.slot >= 0 ? a.po : static_cast<float*>(a.out)) + row * D;
       __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(a.out) + row * D;
@@ -467,18 +523,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           reinterpret_cast<float4*>(dst + 2 * j)[1] = make_float4(y[4], y[5], y[6], y[7]);
         }
       }
-      if (x.slot >= 0) {
-        a.pm[row] = m;
-        a.pl[row] = l;
-      } else {
-        a.lse[row] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
-      }
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == 14) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
