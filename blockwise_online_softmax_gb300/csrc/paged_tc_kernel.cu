@@ -248,53 +248,55 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       }
     } else {
       // -------------------------------------------------------------- products (warp 14)
-      constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
-      constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
-      const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
-      int it = 0, left = 0;  // of the item whose S come next
-      bool ok = true;
-      // S(k) = Q K(k)^T into buffer k % 2.
-      auto qk = [&](int k) {
-        if (left == 0) {
-          ok = wait_item(it);
+      // Lane 0 alone runs the whole loop: it issues at the pipe's rate (65
+      // cycles a product), a warp that issues under a predicate, or branches
+      // around every burst, does not.
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
+        constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
+        const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
+        auto wait1 = [&](int b, uint32_t parity, int code) {
+          return wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
+        };
+        int it = 0, left = 0;  // of the item whose S come next
+        bool ok = true;
+        // S(k) = Q K(k)^T into buffer k % 2.
+        auto qk = [&](int k) {
+          if (left == 0) {
+            ok = wait1(C::B_I + (it & 1), static_cast<uint32_t>(it >> 1), 0x91);
+            if (!ok) return;
+            left = items[it & 1].tiles;
+            mbar_arrive(bar(C::B_IF + (it & 1)));
+            ok = wait1(C::B_Q, static_cast<uint32_t>(it), 0x95);
+            if (!ok) return;
+            ++it;
+          }
+          const int st = k % C::NST;
+          ok = wait1(C::B_KF + st, static_cast<uint32_t>(k / C::NST), 0x96);
           if (!ok) return;
-          left = items[it & 1].tiles;
-          free_item(it);
-          ok = wait(C::B_Q, static_cast<uint32_t>(it), 0x95);
-          if (!ok) return;
-          ++it;
-        }
-        const int st = k % C::NST;
-        ok = wait(C::B_KF + st, static_cast<uint32_t>(k / C::NST), 0x96);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
-        const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
-        --left;
-        if (lane == 0) {  // one lane issues at the pipe's rate, a predicated warp does not
+          tc_fence_after();
+          const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
+          const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
             mma_ss(sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
           }
           tc_commit(bar(C::B_S + (k & 1)));
-          if (left == 0) tc_commit(bar(C::B_QF));
-        }
-        __syncwarp();
-      };
-      qk(0);
-      if (ok && total > 1) qk(1);
-      for (int k = 0; k < total && ok; ++k) {
-        const int st = k % C::NST;
-        ok = wait(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97) &&
-             wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
-             (k == 0 || wait(C::B_TF + ((k - 1) & 1), static_cast<uint32_t>((k - 1) >> 1), 0x99));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
-        const uint32_t pbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
-        const uint32_t term[3] = {tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64, pbuf + 64, pbuf};
-        if (lane == 0) {
+          if (--left == 0) tc_commit(bar(C::B_QF));
+        };
+        qk(0);
+        if (ok && total > 1) qk(1);
+        for (int k = 0; k < total && ok; ++k) {
+          const int st = k % C::NST;
+          ok = wait1(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97) &&
+               wait1(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
+               (k == 0 || wait1(C::B_TF + ((k - 1) & 1), static_cast<uint32_t>((k - 1) >> 1), 0x99));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
+          const uint32_t pbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
+          const uint32_t term[3] = {tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64, pbuf + 64, pbuf};
 #pragma unroll
           for (int x = 0; x < 3; ++x)
 #pragma unroll
@@ -303,13 +305,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                      idesc_pv, x + kk > 0 ? 1u : 0u);
           tc_commit(bar(C::B_E + st));
           tc_commit(bar(C::B_T));
+          if (k + 2 < total) qk(k + 2);  // after P(k)'s product, which reads that buffer, in issue order
         }
-        __syncwarp();
-        if (k + 2 < total) qk(k + 2);  // after P(k)'s product, which reads that buffer, in issue order
+        volatile int no_abort = 0;
+        tc_commit(bar(C::B_DRAIN));
+        wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
       }
-      volatile int no_abort = 0;
-      if (lane == 0) tc_commit(bar(C::B_DRAIN));
-      wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
     }
     __syncwarp();
   } else if (warp < 8) {
