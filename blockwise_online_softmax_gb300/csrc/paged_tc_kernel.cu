@@ -10,8 +10,9 @@
 //
 // Roles of the 16 warps: 0-7 softmax (a row has two threads, one for each half
 // of a tile's keys, that exchange their maxima), 8-11 the output sum (a thread
-// has a row), 12 K loads and the walk over the items, 13 V loads, 14 the
-// products, 15 query rows.  With one softmax thread per row its 128 weights,
+// has a row), 12 K loads and the walk over the items, 13 V loads, 14 the P V
+// products, 15 the query rows and the Q K products (one issuer for both spent a
+// third of a tile between the two: 163 us where two take 152).  With one softmax thread per row its 128 weights,
 // split in three terms each, took 4700 cycles a tile, twice the products.
 //   S(k) = Q K(k)^T, two buffers in TMEM.  The softmax writes P(k) as three
 //   bf16 terms (8 + 8 + 8 bits of the weights, so that the fp32 result has
@@ -70,13 +71,14 @@ struct Cfg {
   static constexpr uint32_t OFF_X = OFF_AL + 2 * RT * 4;       // exchange of a row's two threads
   static constexpr uint32_t OFF_INV = OFF_X + 2 * RT * 4;      // 1 / l of an item's rows
   static constexpr uint32_t OFF_ITEM = OFF_INV + RT * 4;
-  // Barriers: K and V tiles in, stage free; S(k), P(k) (two buffers each);
-  // T(k) ready; T(k) and alpha(k) read; alpha(k) there; query rows in and
-  // read; item record in and read; an item's 1 / l in and read; drain.
+  // Barriers: K and V tiles in, stage free; S(k); P(k); T(k) ready, which also
+  // frees P(k)'s columns; T(k) and alpha(k) read; alpha(k) there; query rows
+  // read; item record in and read; an item's 1 / l in and read; the two
+  // issuers' drains.  Those of a tile come in pairs, by its parity.
   static constexpr int B_KF = 0, B_VF = B_KF + NST, B_E = B_VF + NST, B_S = B_E + NST,
-                       B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 1, B_AL = B_TF + 2,
-                       B_Q = B_AL + 2, B_QF = B_Q + 1, B_I = B_QF + 1, B_IF = B_I + 2,
-                       B_ML = B_IF + 2, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 1, NBAR = B_DRAIN + 1;
+                       B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 2, B_AL = B_TF + 2,
+                       B_QF = B_AL + 2, B_I = B_QF + 1, B_IF = B_I + 2,
+                       B_ML = B_IF + 2, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 1, NBAR = B_DRAIN + 2;
   static constexpr uint32_t OFF_BAR = OFF_ITEM + 2 * sizeof(Item);
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = OFF_MISC + 16;
@@ -113,8 +115,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       uint32_t n = 1;
       if (i == C::B_P || i == C::B_P + 1) n = 256;
       if ((i >= C::B_TF && i < C::B_AL + 2) || i == C::B_ML || i == C::B_MLF) n = 128;
-      if (i == C::B_Q) n = 32;
-      if (i == C::B_IF || i == C::B_IF + 1) n = 14;  // warps 0-11, 14, 15
+      if (i == C::B_IF || i == C::B_IF + 1) n = 13;  // warps 0-11 and 15
       mbar_init(bar(i), n);
     }
     int abort = *reinterpret_cast<volatile int*>(status);
@@ -144,6 +145,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   auto wait = [&](int b, uint32_t parity, int code) {
     const bool w = wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
     return static_cast<bool>(__all_sync(kAll, w));
+  };
+  auto wait1 = [&](int b, uint32_t parity, int code) {  // one lane alone
+    return wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
   };
   // The record of item n, once it is there; its reader releases it itself.
   auto wait_item = [&](int n) { return wait(C::B_I + (n & 1), static_cast<uint32_t>(n >> 1), 0x91); };
@@ -216,13 +220,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           wait_bar(bar(full + j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
       }
     } else if (warp == 15) {
-      // -------------------------------------------------------------- query rows
-      for (int it = 0, done = 0; done < total; ++it) {
-        if (!wait_item(it)) break;
+      // -------------------------------------------------------------- query rows, S(k) = Q K(k)^T
+      constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
+      const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
+      bool ok = true;
+      for (int it = 0, k = 0; ok && k < total; ++it) {
+        ok = wait_item(it);
+        if (!ok) break;
         const Item x = items[it & 1];
         free_item(it);
-        done += x.tiles;
-        if (it > 0 && !wait(C::B_QF, static_cast<uint32_t>(it - 1), 0x94)) break;
         // Rows lane, lane + 32, ...: their index in q, found once.
         int row[RT / 32];
 #pragma unroll
@@ -230,6 +236,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const int r = 32 * y + lane, rr = x.rr0 + (r < x.rows ? r : 0), j = rr / g;
           row[y] = (x.row0 + j) * a.heads + x.kh * g + (rr - j * g);
         }
+        if (it > 0) ok = wait(C::B_QF, static_cast<uint32_t>(it - 1), 0x94);
+        if (!ok) break;
         // Chunk c of row r at c ^ (r % 8) inside its 64 columns, as a TMA load
         // with 128-byte swizzle would put it; rows past the item's are zero.
         constexpr int CPR = D / 8;  // chunks of a row
@@ -244,54 +252,43 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
-        mbar_arrive(bar(C::B_Q));
+        __syncwarp();
+        if (lane == 0) {  // one lane issues at the pipe's rate, a predicated warp does not
+          for (int t = 0; t < x.tiles && ok; ++t, ++k) {
+            const int st = k % C::NST;
+            ok = wait1(C::B_KF + st, static_cast<uint32_t>(k / C::NST), 0x96) &&
+                 (k < 2 || wait1(C::B_T + (k & 1), static_cast<uint32_t>((k - 2) >> 1), 0x95));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
+            const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
+              mma_ss(sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(bar(C::B_S + (k & 1)));
+          }
+          if (ok) tc_commit(bar(C::B_QF));
+        }
+        k = __shfl_sync(kAll, k, 0);
+        ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0) {
+        volatile int no_abort = 0;
+        tc_commit(bar(C::B_DRAIN));
+        wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
       }
     } else {
-      // -------------------------------------------------------------- products (warp 14)
-      // Lane 0 alone runs the whole loop: it issues at the pipe's rate (65
-      // cycles a product), a warp that issues under a predicate, or branches
-      // around every burst, does not.
+      // -------------------------------------------------------------- T(k) = P(k) V(k) (warp 14)
       if (lane == 0) {
-        constexpr uint32_t idesc_qk = idesc_bf16(RT, BT, 0);
         constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
-        const uint64_t qdesc = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
-        auto wait1 = [&](int b, uint32_t parity, int code) {
-          return wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
-        };
-        int it = 0, left = 0;  // of the item whose S come next
         bool ok = true;
-        // S(k) = Q K(k)^T into buffer k % 2.
-        auto qk = [&](int k) {
-          if (left == 0) {
-            ok = wait1(C::B_I + (it & 1), static_cast<uint32_t>(it >> 1), 0x91);
-            if (!ok) return;
-            left = items[it & 1].tiles;
-            mbar_arrive(bar(C::B_IF + (it & 1)));
-            ok = wait1(C::B_Q, static_cast<uint32_t>(it), 0x95);
-            if (!ok) return;
-            ++it;
-          }
-          const int st = k % C::NST;
-          ok = wait1(C::B_KF + st, static_cast<uint32_t>(k / C::NST), 0x96);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t sbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
-          const uint64_t kd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = ((kk >> 2) * CHB + (kk & 3) * 32) >> 4;
-            mma_ss(sbuf, qdesc + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(bar(C::B_S + (k & 1)));
-          if (--left == 0) tc_commit(bar(C::B_QF));
-        };
-        qk(0);
-        if (ok && total > 1) qk(1);
         for (int k = 0; k < total && ok; ++k) {
           const int st = k % C::NST;
-          ok = wait1(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97) &&
-               wait1(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
-               (k == 0 || wait1(C::B_TF + ((k - 1) & 1), static_cast<uint32_t>((k - 1) >> 1), 0x99));
+          ok = wait1(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x98) &&
+               (k == 0 || wait1(C::B_TF + ((k - 1) & 1), static_cast<uint32_t>((k - 1) >> 1), 0x99)) &&
+               wait1(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0x97);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
@@ -304,12 +301,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               mma_ts(tmem + C::C_T, term[x] + kk * 8, vd + static_cast<uint64_t>((kk * 2048) >> 4),
                      idesc_pv, x + kk > 0 ? 1u : 0u);
           tc_commit(bar(C::B_E + st));
-          tc_commit(bar(C::B_T));
-          if (k + 2 < total) qk(k + 2);  // after P(k)'s product, which reads that buffer, in issue order
+          tc_commit(bar(C::B_T + (k & 1)));
         }
         volatile int no_abort = 0;
-        tc_commit(bar(C::B_DRAIN));
-        wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
+        tc_commit(bar(C::B_DRAIN + 1));
+        wait_bar(bar(C::B_DRAIN + 1), 0, &no_abort, nullptr, 0, lim);
       }
     }
     __syncwarp();
@@ -480,7 +476,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) break;
         const float al = s_al[(k & 1) * RT + r];
         const uint64_t al2 = f2pack(al, al);
-        ok = wait(C::B_T, static_cast<uint32_t>(k), 0x9e);
+        ok = wait(C::B_T + (k & 1), static_cast<uint32_t>(k >> 1), 0x9e);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
