@@ -441,7 +441,7 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   // Without pages no load is ever issued; the maps still need an address.
   if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
-  const int rt = ra::paged_row_tile(a);
+  const int rt = ra::paged_row_tile(a, d);
   const int ctas = (rt == 128 ? 1 : 2) * ra::sm_count();
   const size_t rows = static_cast<size_t>(2) * ctas * rt;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

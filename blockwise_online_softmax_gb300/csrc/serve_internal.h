@@ -131,7 +131,7 @@ struct PagedArgs {
 };
 // Query rows (of one request and KV head) that a CTA takes together: 8 or 16
 // (paged_kernel.cu, two CTAs per SM) or 128 (paged_tc_kernel.cu, one).
-int paged_row_tile(const PagedArgs& a);
+int paged_row_tile(const PagedArgs& a, int d);
 size_t paged_cut_bytes(int ctas);
 // tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
 // 64 x 1 x min(page_size, 64) x 1, 128-byte swizzle.
