@@ -16,6 +16,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libra.so")
+SERVE_PATH = os.path.join(_PKG, "_serve.so")
 
 RA_OK = 0
 RA_ERR_INVALID = -1
@@ -94,8 +95,8 @@ _SIGNATURES = {
     "ra_last_error": ("", "s"),
     "ra_abi_version": ("", "i"),
 }
-_CT = {"P": ctypes.c_void_p, "L": ctypes.c_longlong, "i": ctypes.c_int, "s": ctypes.c_char_p,
-       "f": ctypes.c_float}
+_CT = {"P": ctypes.c_void_p, "L": ctypes.c_longlong, "i": ctypes.c_int, "f": ctypes.c_float,
+       "s": ctypes.c_char_p}
 
 
 def lib():
@@ -429,103 +430,27 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
 
 # ------------------------------------------------------------------ rotary positions, pages
 
-# These calls are made once or more per layer of a serving step, where a few
-# microseconds of Python each are the step's time: their checks read every
-# tensor property once, and the device is switched only when it must be.
+# These calls are one or two short kernels each, made once or more per layer
+# of a serving step.  Their arguments are marshalled by the extension _serve
+# (csrc/serve_binding.cpp): the same checks and the same C ABI calls as the
+# functions above, at a few microseconds instead of tens.
 
-def _device(t, name) -> int:
-    """Index of the CUDA device a tensor lives on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+_serve = None
 
 
-def _arg(t, name, dev, dtype):
-    """Pointer of a dense tensor of `dtype` on device `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
-                         f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _fast():
+    """Load the extension once (after libra.so, which it is linked to)."""
+    global _serve
+    if _serve is None:
+        lib()
+        if not os.path.exists(SERVE_PATH):
+            raise RaError(RA_ERR_UNSUPPORTED,
+                          f"{SERVE_PATH} is not built; run __graft_entry__.build()")
+        from . import _serve as m
 
-
-def _vec(t, name, n, dev, dtype):
-    """Pointer of a dense 1-D tensor of n entries."""
-    p = _arg(t, name, dev, dtype)
-    if t.dim() != 1 or t.numel() != n:
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    return p
-
-
-def _rows(t, name, T, heads, d, dev, dtype):
-    """Pointer and token stride of a [T, heads, d] tensor whose heads are
-    dense; tokens may lie further apart (a view of a packed projection)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
-                         f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    st = t.stride()
-    if T and (st[2] != 1 or (heads > 1 and st[1] != d)):
-        raise ValueError(f"{name}: the heads of a token must be dense (strides {st})")
-    return t.data_ptr(), st[0] if T > 1 else heads * d
-
-
-def _call(name, dev, stream, *args):
-    """Call a library function with device `dev` current, on `stream` (None:
-    the device's current stream), the last argument."""
-    f = getattr(_lib or lib(), name)
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    if torch._C._cuda_getDevice() == dev:
-        rc = f(*args, st)
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*args, st)
-    if rc:
-        _check(rc)
-
-
-def _weights(q_weight, k_weight, d, dev):
-    """Pointers of the norm weights (0 for none) and their dtype."""
-    code, ptrs = RA_F32, []
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            ptrs.append(0)
-            continue
-        if w.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"{name} must be float32 or bfloat16, got {w.dtype}")
-        ptrs.append(_vec(w, name, d, dev, w.dtype))
-        if w.dtype is torch.bfloat16:
-            code = RA_BF16
-    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
-        raise TypeError("q_weight and k_weight must share a dtype")
-    return ptrs[0], ptrs[1], code
-
-
-def _phase_table(phases, dev):
-    if phases is None:
-        return 0, 0
-    n = phases.numel()
-    return _vec(phases, "phases", n, dev, torch.int64), 2 * n
-
-
-def _qk_shapes(q, k):
-    qs, ks = q.shape, k.shape
-    if len(qs) != 3 or len(ks) != 3:
-        raise ValueError("q: [T, heads, d]; k: [T, kv_heads, d]")
-    if ks[0] != qs[0] or ks[2] != qs[2] or k.dtype is not q.dtype:
-        raise ValueError("q and k must share their tokens, head dim and dtype")
-    return qs[0], qs[1], ks[1], qs[2]
+        m.on_status(_check)
+        _serve = m
+    return _serve
 
 
 def rope_freqs(rot_dim: int, base: float = 10000.0, *, scaling: str | None = None,
@@ -588,27 +513,9 @@ def ra_qk_norm_rope(q, k, phases, *, q_weight=None, k_weight=None, eps: float = 
     their dtype.  Rows sit at `positions` (int32 [T]), or where `layout` puts
     the rows of a ring tensor of P blocks.  phases: see rope_phases; None
     leaves the columns unturned."""
-    T, heads, kv_heads, d = _qk_shapes(q, k)
-    dt = _qkv_dtype(q)
-    if q_out is None:
-        q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out and k_out must match q and k in shape")
-    if k_out is None:
-        k_out = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
-    elif k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must match q and k in shape")
-    dev, dtype = _device(q, "q"), q.dtype
-    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
-    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
-    ph, rot = _phase_table(phases, dev)
-    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
-    pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
-    _call("ra_qk_norm_rope", dev, stream,
-        qp, kp, _arg(q_out, "q_out", dev, dtype), _arg(k_out, "k_out", dev, dtype), T, d,
-        heads, kv_heads, qs, ks, pos, _layout(layout), int(P), rot, int(bool(interleaved)),
-        ph, float(mscale), qw, kw, wt, float(eps), dt)
-    return q_out, k_out
+    return (_serve or _fast()).qk_norm_rope(
+        q, k, phases, q_weight, k_weight, eps, interleaved, mscale, positions, P,
+        _layout(layout), q_out, k_out, stream)
 
 
 def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_weight=None,
@@ -619,45 +526,9 @@ def ra_qk_norm_rope_backward(q, k, phases, dq_out, dk_out, *, q_weight=None, k_w
     from those of its outputs (fp32, dense, as ra_ring_backward returns
     them).  dq and dk have q's dtype and may be views of a packed gradient;
     the weights' are fp32 [d], None without that weight."""
-    T, heads, kv_heads, d = _qk_shapes(q, k)
-    dt = _qkv_dtype(q)
-    if dq_out.shape != q.shape or dk_out.shape != k.shape:
-        raise ValueError("dq_out and dk_out must match q and k in shape")
-    if dq is None:
-        dq = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
-    if dk is None:
-        dk = torch.empty((T, kv_heads, d), dtype=q.dtype, device=q.device)
-    if dq.shape != q.shape or dk.shape != k.shape:
-        raise ValueError("dq and dk must match q and k in shape")
-    for w, g, name in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
-        if w is None and g is not None:
-            raise ValueError(f"{name} without its weight")
-    if q_weight is not None and dq_weight is None:
-        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
-    if k_weight is not None and dk_weight is None:
-        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
-    dev, dtype, f32 = _device(q, "q"), q.dtype, torch.float32
-    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
-    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
-    dqp, dqs = _rows(dq, "dq", T, heads, d, dev, dtype)
-    dkp, dks = _rows(dk, "dk", T, kv_heads, d, dev, dtype)
-    ph, rot = _phase_table(phases, dev)
-    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
-    pos = 0 if positions is None else _vec(positions, "positions", T, dev, torch.int32)
-    dqw = 0 if dq_weight is None else _vec(dq_weight, "dq_weight", d, dev, f32)
-    dkw = 0 if dk_weight is None else _vec(dk_weight, "dk_weight", d, dev, f32)
-    _call("ra_qk_norm_rope_backward", dev, stream,
-        qp, kp, _arg(dq_out, "dq_out", dev, f32), _arg(dk_out, "dk_out", dev, f32), dqp, dkp,
-        dqw, dkw, T, d, heads, kv_heads, qs, ks, dqs, dks, pos, _layout(layout), int(P), rot,
-        int(bool(interleaved)), ph, float(mscale), qw, kw, wt, float(eps), dt)
-    return dq, dk, dq_weight, dk_weight
-
-
-def _table(block_table, n_req, dev):
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != n_req:
-        raise ValueError(f"block_table must be [n_req={n_req}, max_pages], got {tuple(shape)}")
-    return _arg(block_table, "block_table", dev, torch.int32), shape[1]
+    return (_serve or _fast()).qk_norm_rope_backward(
+        q, k, phases, dq_out, dk_out, q_weight, k_weight, eps, interleaved, mscale, positions, P,
+        _layout(layout), dq, dk, dq_weight, dk_weight, stream)
 
 
 def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *, page_size: int,
@@ -670,37 +541,9 @@ def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *,
     free_count_out may be lengths and free_count themselves.  A nonzero
     status (pages missing, rows too short, tokens beyond `tokens`) means
     that the step changed nothing."""
-    n, tokens = lengths.numel(), int(tokens)
-    i32 = torch.int32
-    if block_table.dim() != 2 or block_table.shape[0] != n:
-        raise ValueError(f"block_table must be [n_req={n}, max_pages], "
-                         f"got {tuple(block_table.shape)}")
-    dev = _device(lengths, "lengths")
-    where = lengths.device
-    if lengths_out is None:
-        lengths_out = torch.empty(n, dtype=i32, device=where)
-    if free_count_out is None:
-        free_count_out = torch.empty(1, dtype=i32, device=where)
-    if slots is None:
-        slots = torch.empty(tokens, dtype=torch.int64, device=where)
-    if positions is None:
-        positions = torch.empty(tokens, dtype=i32, device=where)
-    if cu_tokens is None:
-        cu_tokens = torch.empty(n + 1, dtype=i32, device=where)
-    if status is None:
-        status = torch.empty(3, dtype=i32, device=where)
-    table, width = _table(block_table, n, dev)
-    pool = free_pages.numel()
-    _call("ra_paged_extend", dev, stream,
-        _vec(lengths, "lengths", n, dev, i32), _vec(new_tokens, "new_tokens", n, dev, i32), n,
-        table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
-        _vec(free_count, "free_count", 1, dev, i32), int(page_size), tokens,
-        _vec(lengths_out, "lengths_out", n, dev, i32),
-        _vec(free_count_out, "free_count_out", 1, dev, i32),
-        _vec(slots, "slots", tokens, dev, torch.int64),
-        _vec(positions, "positions", tokens, dev, i32),
-        _vec(cu_tokens, "cu_tokens", n + 1, dev, i32), _vec(status, "status", 3, dev, i32))
-    return slots, positions, cu_tokens, lengths_out, free_count_out, status
+    return (_serve or _fast()).paged_extend(
+        lengths, new_tokens, block_table, free_pages, free_count, page_size, tokens, lengths_out,
+        free_count_out, slots, positions, cu_tokens, status, stream)
 
 
 def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, page_size: int,
@@ -708,50 +551,9 @@ def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, 
     """Push the pages of the requests with finished != 0 back on the stack
     free_pages (in place) and set their lengths to 0; returns (lengths_out,
     free_count_out), which may be lengths and free_count themselves."""
-    n, i32 = lengths.numel(), torch.int32
-    dev = _device(lengths, "lengths")
-    if lengths_out is None:
-        lengths_out = torch.empty(n, dtype=i32, device=lengths.device)
-    if free_count_out is None:
-        free_count_out = torch.empty(1, dtype=i32, device=lengths.device)
-    table, width = _table(block_table, n, dev)
-    pool = free_pages.numel()
-    _call("ra_paged_release", dev, stream,
-        _vec(lengths, "lengths", n, dev, i32), _vec(finished, "finished", n, dev, i32), n,
-        table, width, _vec(free_pages, "free_pages", pool, dev, i32), pool,
-        _vec(free_count, "free_count", 1, dev, i32), int(page_size),
-        _vec(lengths_out, "lengths_out", n, dev, i32),
-        _vec(free_count_out, "free_count_out", 1, dev, i32))
-    return lengths_out, free_count_out
-
-
-def _cache(t, name, kv_heads, d, dev):
-    """Pointer, page count, page size and page stride of a cache tensor
-    [n_pages, page_size, kv_heads, d] (bf16, dense inside a page)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
-                         f"{name} is on {t.device}, not on cuda:{dev}")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 4 or shape[2] != kv_heads or shape[3] != d:
-        raise ValueError(f"{name} must be [n_pages, page_size, {kv_heads}, {d}], "
-                         f"got {tuple(shape)}")
-    n, ps = shape[0], shape[1]
-    st = t.stride()
-    if n and (st[3] != 1 or (kv_heads > 1 and st[2] != d) or (ps > 1 and st[1] != kv_heads * d)):
-        raise ValueError(f"{name}: a page must be dense (strides {st})")
-    return t.data_ptr(), n, ps, st[0] if n > 1 else ps * kv_heads * d
-
-
-def _caches(k_cache, v_cache, kv_heads, d, dev):
-    kp, n, ps, ks = _cache(k_cache, "k_cache", kv_heads, d, dev)
-    vp, vn, vps, vs = _cache(v_cache, "v_cache", kv_heads, d, dev)
-    if vn != n or vps != ps:
-        raise ValueError("k_cache and v_cache must match in pages and page size")
-    return kp, vp, n, ps, ks, vs
+    return (_serve or _fast()).paged_release(
+        lengths, finished, block_table, free_pages, free_count, page_size, lengths_out,
+        free_count_out, stream)
 
 
 def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_weight=None,
@@ -760,27 +562,9 @@ def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_we
     """ra_qk_norm_rope on a step's rows (bf16) with k and v written to their
     pages: row t goes to slots[t] (int64; outside the pages: padding, nothing
     is written) at positions[t] (int32).  Returns q_out, dense like q."""
-    T, heads, kv_heads, d = _qk_shapes(q, k)
-    dt = _qkv_dtype(q)
-    if v.shape != k.shape or v.dtype is not q.dtype:
-        raise ValueError("v must match k in shape and dtype")
-    if q_out is None:
-        q_out = torch.empty((T, heads, d), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must match q in shape")
-    dev, dtype = _device(q, "q"), q.dtype
-    qp, qs = _rows(q, "q", T, heads, d, dev, dtype)
-    kp, ks = _rows(k, "k", T, kv_heads, d, dev, dtype)
-    vp, vs = _rows(v, "v", T, kv_heads, d, dev, dtype)
-    kc, vc, n_pages, ps, kcs, vcs = _caches(k_cache, v_cache, kv_heads, d, dev)
-    ph, rot = _phase_table(phases, dev)
-    qw, kw, wt = _weights(q_weight, k_weight, d, dev)
-    _call("ra_paged_append", dev, stream,
-        qp, kp, vp, _arg(q_out, "q_out", dev, dtype), kc, vc, T, d, heads, kv_heads, qs, ks,
-        vs, n_pages, ps, kcs, vcs, _vec(slots, "slots", T, dev, torch.int64),
-        _vec(positions, "positions", T, dev, torch.int32), rot, int(bool(interleaved)), ph,
-        float(mscale), qw, kw, wt, float(eps), dt)
-    return q_out
+    return (_serve or _fast()).paged_append(
+        q, k, v, phases, k_cache, v_cache, slots, positions, q_weight, k_weight, eps,
+        interleaved, mscale, q_out, stream)
 
 
 def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, window: int = 0,
@@ -790,36 +574,8 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, win
     request i (int32 [n_req + 1]); lengths (int32 [n_req]) include them.
     Returns (out [T, heads, d], lse [T, heads]), fp32; pass a bf16 `out` for
     that type."""
-    n = lengths.numel()
-    if q.dim() != 3:
-        raise ValueError("q: [T, heads, d]")
-    T, heads, d = q.shape
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: [n_pages, page_size, kv_heads, d]")
-    kv_heads = k_cache.shape[2]
-    if cu_q is None and (T % n if n else T):
-        raise ValueError(f"T={T} rows are not a multiple of {n} requests (and cu_q is None)")
-    f32 = torch.float32
-    if out is None:
-        out = torch.empty((T, heads, d), dtype=f32, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError(f"out must have shape {(T, heads, d)}, got {tuple(out.shape)}")
-    elif out.dtype not in (f32, torch.bfloat16):
-        raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
-    if lse is None:
-        lse = torch.empty((T, heads), dtype=f32, device=q.device)
-    elif tuple(lse.shape) != (T, heads):
-        raise ValueError(f"lse must have shape {(T, heads)}, got {tuple(lse.shape)}")
-    dev = _device(q, "q")
-    kc, vc, n_pages, ps, ks, vs = _caches(k_cache, v_cache, kv_heads, d, dev)
-    table, width = _table(block_table, n, dev)
-    cu = 0 if cu_q is None else _vec(cu_q, "cu_q", n + 1, dev, torch.int32)
-    _call("ra_paged_decode", dev, stream,
-        _arg(q, "q", dev, torch.bfloat16), kc, vc, _arg(out, "out", dev, out.dtype),
-        _arg(lse, "lse", dev, f32), T, n, 0 if cu or not n else T // n, cu, table, width,
-        _vec(lengths, "lengths", n, dev, torch.int32), n_pages, ps, ks, vs, int(window), d,
-        heads, kv_heads, RA_BF16, RA_BF16 if out.dtype is torch.bfloat16 else RA_F32)
-    return out, lse
+    return (_serve or _fast()).paged_decode(
+        q, k_cache, v_cache, block_table, lengths, cu_q, window, out, lse, stream)
 
 
 def ra_ring_forward_noalloc(q, k, v, *, P: int, causal: bool, out=None, lse=None,

@@ -1,9 +1,11 @@
-"""Build ``libra.so`` in-tree with nvcc, for sm_103a only.
+"""Build ``libra.so`` in-tree with nvcc, for sm_103a only, and the extension
+``_serve.so`` that marshals the serving calls' tensors into it.
 
 Each translation unit is compiled in parallel into ``_build/``.  The
 objects are then linked into ``blockwise_online_softmax_gb300/libra.so``
 with the CUDA runtime linked statically, so the library needs only the
-driver at run time.  Run ``python -m blockwise_online_softmax_gb300.build``
+driver at run time.  ``_serve.so`` is a CPython extension (g++, torch's
+headers) linked to it.  Run ``python -m blockwise_online_softmax_gb300.build``
 or call ``build()``.
 """
 from __future__ import annotations
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libra.so")
+SERVE = os.path.join(PKG, "_serve.so")
+SERVE_SOURCE = "serve_binding.cpp"
 SOURCES = ["ra_api.cu", "state_kernels.cu", "simt_kernel.cu", "umma_kernel.cu", "decode_kernel.cu",
            "bwd_kernel.cu", "serve_api.cu", "rope_kernel.cu", "pages_kernel.cu",
            "paged_kernel.cu", "paged_tc_kernel.cu"]
@@ -37,10 +42,26 @@ def _flags(extra=()):
                     "-I" + INCLUDE, "-I" + CSRC] + list(extra))
 
 
+def _serve_flags():
+    """Compile and link flags of the extension: torch as it is installed."""
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    lib = os.path.join(t, "lib")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}"]
+            + [f"-I{i}" if i == INCLUDE else f"-isystem{i}" for i in inc],
+            ["-L" + PKG, "-lra", "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+             "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib])
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(SERVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(SERVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ra.h"),
                                                                os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
@@ -52,7 +73,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
-    procs = []
+    cflags, ldflags = _serve_flags()
+    serve_obj = os.path.join(BUILD_DIR, "serve_binding.o")
+    procs = [(SERVE_SOURCE, None, subprocess.Popen(
+        ["g++"] + cflags + ["-c", os.path.join(CSRC, SERVE_SOURCE), "-o", serve_obj],
+        stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))]
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [nvcc()] + _flags(extra) + ["-c", os.path.join(CSRC, src), "-o", obj]
@@ -67,9 +92,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             errors.append(f"--- {src} ---\n{out}")
         elif out and (verbose or ptxas_info):
             print(f"--- {src} ---\n{out}", flush=True)
-        objs.append(obj)
+        if obj:
+            objs.append(obj)
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
     if verbose:
@@ -78,6 +104,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout)
     os.replace(tmp, LIB)
+    tmp = SERVE + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, serve_obj] + ldflags, stdout=subprocess.PIPE,
+                       stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link of the extension failed:\n" + r.stdout)
+    os.replace(tmp, SERVE)
     return LIB
 
 

@@ -441,3 +441,29 @@ def test_serving_steps_equal_the_ring_over_the_whole_sequences(norm):
             assert int(count) == before + sum(-(-int(x) // ps) for x, y in zip(keep, fin) if y)
     ra.ra_device_status()
     assert sorted(free.tolist()) == list(range(n_pages))
+
+
+def test_refusals_reach_python_with_the_library_s_message():
+    """A status of the C ABI raises RaError with the message of the same
+    thread; shapes, types and placement raise before the call."""
+    q, kc, vc, table, lens, _, _ = make_decode([64, 32], [1, 1], 4, 2, 64, 16)
+    with pytest.raises(binding.RaError, match="page_size=12"):
+        ra.ra_paged_extend(lens, lens, table, lens, lens[:1], page_size=12, tokens=4)
+    with pytest.raises(binding.RaError, match="window"):
+        ra.ra_paged_decode(q, kc, vc, table, lens, window=-1)
+    with pytest.raises(ValueError, match="CUDA"):
+        ra.ra_paged_decode(q, kc, vc, table, lens.cpu())
+    with pytest.raises(TypeError, match="int32"):
+        ra.ra_paged_decode(q, kc, vc, table, lens.long())
+    with pytest.raises(TypeError, match="bfloat16"):
+        ra.ra_paged_decode(q.float(), kc, vc, table, lens)
+    with pytest.raises(ValueError, match="dense"):
+        ra.ra_paged_decode(q, kc.transpose(1, 2).contiguous().transpose(1, 2), vc, table, lens)
+    with pytest.raises(ValueError, match="match in pages"):
+        ra.ra_paged_decode(q, kc, vc[:1], table, lens)
+    with pytest.raises(ValueError, match="block_table"):
+        ra.ra_paged_decode(q, kc, vc, table[:1], lens)
+    with pytest.raises(TypeError, match="tensor"):
+        ra.ra_paged_decode(q, kc, vc, table, [64, 32])
+    out = ra.ra_paged_decode(q, kc, vc, table, lens, stream=torch.cuda.current_stream())
+    assert torch.equal(out[0], ra.ra_paged_decode(q, kc, vc, table, lens)[0])
