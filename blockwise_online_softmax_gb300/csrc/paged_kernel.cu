@@ -126,7 +126,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
   Cut* cuts = static_cast<Cut*>(a.cuts);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(kfull(s), 1);
@@ -143,8 +143,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     if (sb & 1023u) abort = atomicCAS(&g_paged_status, 0, 0x8f) | 0x8f;
     *abort_flag = abort;
     fence_mbar_init();
-    cuts[blockIdx.x].last = -1;
   }
+  wait_for_previous();
+  if (tid == 0) cuts[blockIdx.x].last = -1;
   const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_BUF);  // synchronizes
   if (run.first >= run.last || *abort_flag) return;
   const long long lim = a.wait_limit;
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   constexpr int CPL = D / 32;
   __shared__ float s_m[kJoin], s_l[kJoin], s_o[kJoin][D];
   const int c = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel runs
+  let_next_start();
+  wait_for_previous();
   const Cut cut = static_cast<const Cut*>(a.cuts)[c];
   if (cut.last < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,8 +597,8 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(paged_decode_kernel<D, NT>, Cfg<D, NT>::SMEM, done);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, NT><<<ctas, kThreads, Cfg<D, NT>::SMEM, st>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_early(paged_decode_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D, NT>::SMEM, st, tk, tv,
+                      a);
 }
 
 }  // namespace
@@ -623,17 +625,9 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_til
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile < 16 ? row_tile : 16));
-  cfg.blockDim = dim3(32 * kJoin);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return d == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, a, row_tile)
-                  : cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, a, row_tile);
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(row_tile < 16 ? row_tile : 16));
+  return launch_early(d == 128 ? paged_combine_kernel<128> : paged_combine_kernel<64>, grid, 32 * kJoin, 0, st, a,
+                      row_tile);
 }
 
 cudaError_t take_paged_status(int* code) {

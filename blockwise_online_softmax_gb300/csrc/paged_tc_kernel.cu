@@ -109,7 +109,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
   Cut* cuts = static_cast<Cut*>(a.cuts);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_start();
   if (tid == 0) {
     for (int i = 0; i < C::NBAR; ++i) {
       uint32_t n = 1;
@@ -124,8 +124,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     if (sb & 1023u) abort = atomicCAS(status, 0, 0x9f) | 0x9f;
     *abort_flag = abort;
     fence_mbar_init();
-    cuts[blockIdx.x].last = -1;
   }
+  wait_for_previous();
+  if (tid == 0) cuts[blockIdx.x].last = -1;
   const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_AL);  // synchronizes
   if (run.first >= run.last || *abort_flag) return;
   if (warp == 14) {
@@ -537,8 +538,7 @@ cudaError_t launch_d(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(paged_tc_kernel<D>, Cfg<D>::SMEM, done);
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<ctas, kThreads, Cfg<D>::SMEM, st>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_early(paged_tc_kernel<D>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D>::SMEM, st, tk, tv, a);
 }
 
 }  // namespace

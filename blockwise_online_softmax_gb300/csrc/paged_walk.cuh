@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "serve_internal.h"
 

@@ -12,6 +12,7 @@
 // sense, or a status, but no access outside the arrays.
 #include <cstdint>
 
+#include "launch.cuh"
 #include "serve_internal.h"
 
 namespace ra {
@@ -20,12 +21,6 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBook = 1024;  // threads of the bookkeeping CTA, requests per chunk
 constexpr int kSpread = 256; // threads of the second launch's CTAs
-
-// The second launch may start while the first still runs; it waits here.
-__device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_second_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // Exclusive prefix sum of one value per thread of the CTA; *total gets the
 // sum.  Every thread calls it; it synchronizes before it returns.
@@ -84,7 +79,8 @@ __global__ void __launch_bounds__(kBook) paged_extend_kernel(const ExtendArgs a)
   __shared__ int s_bad;
   const int tid = threadIdx.x, sh = a.page_shift;
   const long long ps1 = (1LL << sh) - 1;
-  if (!ALL) let_second_start();
+  let_next_start();
+  wait_for_previous();
   const int count = stack_count(a.free_count, a.free_capacity);
   if (tid == 0) {
     s_need = s_toks = 0;
@@ -191,7 +187,8 @@ __global__ void __launch_bounds__(kSpread) paged_extend_tokens_kernel(const Exte
   const long long x = static_cast<long long>(blockIdx.x) * kSpread + threadIdx.x;
   const int sh = a.page_shift;
   const long long ps1 = (1LL << sh) - 1;
-  wait_for_first();
+  let_next_start();
+  wait_for_previous();
   if (x >= a.tokens) return;
   const int t = static_cast<int>(x);
   if (a.n_req == 0 || t >= a.cu_tokens[a.n_req]) {
@@ -223,7 +220,8 @@ __global__ void __launch_bounds__(kBook) paged_release_kernel(const ReleaseArgs 
   __shared__ int s_page[kBook];
   const int tid = threadIdx.x, sh = a.page_shift;
   const long long ps1 = (1LL << sh) - 1;
-  if (!ALL) let_second_start();
+  let_next_start();
+  wait_for_previous();
   const long long count = stack_count(a.free_count, a.free_capacity);
   int top = 0;  // pages of the chunks before (at most the table's entries)
   for (int i0 = 0; i0 < a.n_req; i0 += kBook) {
@@ -261,7 +259,8 @@ __global__ void __launch_bounds__(kBook) paged_release_kernel(const ReleaseArgs 
 }
 
 __global__ void __launch_bounds__(kSpread) paged_release_pages_kernel(const ReleaseArgs a) {
-  wait_for_first();
+  let_next_start();
+  wait_for_previous();
   const int total = a.first_page[a.n_req];
   const long long count = a.first_page[a.n_req + 1];
   for (long long x = static_cast<long long>(blockIdx.x) * kSpread + threadIdx.x; x < total;
@@ -271,21 +270,6 @@ __global__ void __launch_bounds__(kSpread) paged_release_pages_kernel(const Rele
     a.free_pages[count + x] =
         a.block_table[static_cast<long long>(r) * a.max_pages + (x - a.first_page[r])];
   }
-}
-
-// A launch that may start before the one in front of it in the stream ends.
-template <typename A>
-cudaError_t launch_second(void (*k)(A), unsigned grid, const A& a, cudaStream_t st) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kSpread);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 }  // namespace
@@ -298,27 +282,20 @@ bool paged_release_needs_scratch(const ReleaseArgs& a) {
 }
 
 cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st) {
-  if (!a.first_page) {
-    paged_extend_kernel<true><<<1, kBook, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  paged_extend_kernel<false><<<1, kBook, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  if (!a.first_page) return launch_early(paged_extend_kernel<true>, dim3(1), kBook, 0, st, a);
+  cudaError_t e = launch_early(paged_extend_kernel<false>, dim3(1), kBook, 0, st, a);
   if (e != cudaSuccess) return e;
-  return launch_second(paged_extend_tokens_kernel,
-                       static_cast<unsigned>((a.tokens + kSpread - 1) / kSpread), a, st);
+  return launch_early(paged_extend_tokens_kernel,
+                      dim3(static_cast<unsigned>((a.tokens + kSpread - 1) / kSpread)), kSpread, 0, st, a);
 }
 
 cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st) {
-  if (!a.first_page) {
-    paged_release_kernel<true><<<1, kBook, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  paged_release_kernel<false><<<1, kBook, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  if (!a.first_page) return launch_early(paged_release_kernel<true>, dim3(1), kBook, 0, st, a);
+  cudaError_t e = launch_early(paged_release_kernel<false>, dim3(1), kBook, 0, st, a);
   if (e != cudaSuccess) return e;
   const long long most = (static_cast<long long>(a.n_req) * a.max_pages + kSpread - 1) / kSpread;
-  return launch_second(paged_release_pages_kernel, static_cast<unsigned>(most < 608 ? most : 608), a, st);
+  return launch_early(paged_release_pages_kernel, dim3(static_cast<unsigned>(most < 608 ? most : 608)), kSpread, 0,
+                      st, a);
 }
 
 }  // namespace ra

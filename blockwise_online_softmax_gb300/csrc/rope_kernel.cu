@@ -20,6 +20,7 @@
 
 #include <cuda_bf16.h>
 
+#include "launch.cuh"
 #include "serve_internal.h"
 
 namespace ra {
@@ -194,6 +195,8 @@ constexpr int kFwdCtas = 3;  // per SM
 
 template <typename T, int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(kWarps * 32, kFwdCtas) rope_forward_kernel(const RopeArgs a) {
+  let_next_start();
+  wait_for_previous();
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31, col = 8 * (lane % LPR), sub = lane / LPR;
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
@@ -295,6 +298,8 @@ constexpr int kGradCtas = 2;  // per SM
 
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(const RopeArgs a) {
+  let_next_start();
+  wait_for_previous();
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   __shared__ float s_dw[kWarps][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -388,6 +393,8 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
 // One CTA per 32 of the 2 d weight gradients: warp w sums the partials w,
 // w + 8, ... of its 32 columns, then the warps' sums meet in shared memory.
 __global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const RopeArgs a, int n, int d) {
+  let_next_start();
+  wait_for_previous();
   __shared__ float s[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
@@ -414,27 +421,19 @@ cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
   long long ctas = (a.T * a.parts + kWarps - 1) / kWarps;
   const long long most = static_cast<long long>(kFwdCtas) * sm_count();  // one wave
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-  if (d == 128) {
-    if (a.interleaved) rope_forward_kernel<T, 128, true, APPEND><<<grid, kWarps * 32, 0, st>>>(a);
-    else rope_forward_kernel<T, 128, false, APPEND><<<grid, kWarps * 32, 0, st>>>(a);
-  } else {
-    if (a.interleaved) rope_forward_kernel<T, 64, true, APPEND><<<grid, kWarps * 32, 0, st>>>(a);
-    else rope_forward_kernel<T, 64, false, APPEND><<<grid, kWarps * 32, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kernel = d == 128 ? (a.interleaved ? rope_forward_kernel<T, 128, true, APPEND>
+                                          : rope_forward_kernel<T, 128, false, APPEND>)
+                         : (a.interleaved ? rope_forward_kernel<T, 64, true, APPEND>
+                                          : rope_forward_kernel<T, 64, false, APPEND>);
+  return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
 template <typename T>
 cudaError_t backward_t(const RopeArgs& a, int d, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(rope_grad_ctas(a));
-  if (d == 128) {
-    if (a.interleaved) rope_backward_kernel<T, 128, true><<<grid, kWarps * 32, 0, st>>>(a);
-    else rope_backward_kernel<T, 128, false><<<grid, kWarps * 32, 0, st>>>(a);
-  } else {
-    if (a.interleaved) rope_backward_kernel<T, 64, true><<<grid, kWarps * 32, 0, st>>>(a);
-    else rope_backward_kernel<T, 64, false><<<grid, kWarps * 32, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kernel = d == 128 ? (a.interleaved ? rope_backward_kernel<T, 128, true> : rope_backward_kernel<T, 128, false>)
+                         : (a.interleaved ? rope_backward_kernel<T, 64, true> : rope_backward_kernel<T, 64, false>);
+  return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
 }  // namespace
@@ -457,8 +456,7 @@ cudaError_t launch_rope_backward(const RopeArgs& a, int d, bool bf16, cudaStream
 }
 
 cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st) {
-  rope_weight_grad_kernel<<<2 * d / 32, kWarps * 32, 0, st>>>(a, n, d);
-  return cudaGetLastError();
+  return launch_early(rope_weight_grad_kernel, dim3(2 * d / 32), kWarps * 32, 0, st, a, n, d);
 }
 
 }  // namespace ra
