@@ -55,7 +55,8 @@ def _serve_flags():
     return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}"]
             + [f"-I{i}" if i == INCLUDE else f"-isystem{i}" for i in inc],
             ["-L" + PKG, "-lra", "-L" + lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-             "-lc10_cuda", "-Wl,-rpath,$ORIGIN:" + lib])
+             "-ltorch_cuda", "-lc10_cuda",
+             "-Wl,-rpath,$ORIGIN:" + lib])
 
 
 def _stale() -> bool:

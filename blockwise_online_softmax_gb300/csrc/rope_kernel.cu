@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
+#include "ptx.cuh"
 #include "serve_internal.h"
 
 namespace ra {
@@ -47,6 +48,7 @@ struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ void put(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
     uint32_t u[4];
 #pragma unroll
@@ -68,6 +70,10 @@ struct Vec<float> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ __forceinline__ void put(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
   }
   static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -183,24 +189,26 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Forward (APPEND: with k and v written to their pages).  A warp takes a
-// token, or one of a.parts shares of its rows; LPR lanes hold a row, so a
-// group is 32 / LPR rows, of q, k or v alone.  The loads of kBatch groups are
-// in flight together.  Norm weight and rotation are folded once per token,
-// out = r (x cw + partner sw) with cw = w cos and sw = w_partner sin, so a
-// row costs two products and a sum per column, and one exchange of its packed
-// columns with the partner lane.
+// Forward.  A warp takes a token, or one of a.parts shares of its rows; LPR
+// lanes hold a row, so a group is 32 / LPR rows, of q or k alone, and the loads
+// of kBatch groups are in flight together.  A row costs two products and a sum
+// per column and one exchange of its packed columns with the partner lane.
+// The 128K-token GQA q and k (32/8 heads, d = 128) take 444 us, 0.90 of the copy
+// bandwidth; with the arithmetic one column at a time 469, with 2 or 4 CTAs per
+// SM or other batches 450 to 585.  (The row is written out here: through turn()
+// below the compiler's schedule costs 6%.)
 constexpr int kBatch = 4;
-constexpr int kFwdCtas = 3;  // per SM
+template <typename T>
+constexpr int kFwdCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: 80 or 128 registers
 
-template <typename T, int D, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32, kFwdCtas) rope_forward_kernel(const RopeArgs a) {
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, kFwdCtas<T>) rope_forward_kernel(const RopeArgs a) {
   let_next_start();
   wait_for_previous();
   constexpr int LPR = D / 8, RPI = 32 / LPR;
   const int lane = threadIdx.x & 31, col = 8 * (lane % LPR), sub = lane / LPR;
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
-  const int groups = gq + gk + (APPEND ? gk : 0);
+  const int groups = gq + gk;
   const int per = (groups + a.parts - 1) / a.parts;
   const long long items = a.T * a.parts;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
@@ -211,31 +219,23 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdCtas) rope_forward_kernel(con
     const long long t = a.parts == 1 ? it : it / a.parts;
     const int g0 = a.parts == 1 ? 0 : static_cast<int>(it - t * a.parts) * per;
     const int g1 = g0 + per < groups ? g0 + per : groups;
-    long long slot = 0;
-    if (APPEND) {
-      slot = a.slots[t];
-      if (slot < 0 || slot >= a.n_slots) continue;  // a padding row: nothing is written
-    }
-    if (g0 < gq + gk) rot.angles(a, row_position(a, t));
-    auto rows = [&](int ga, int gb, int n, const T* src, T* dst, const void* weight, bool copy) {
+    // A last share may be empty.  (The test also keeps the compiler from moving
+    // row loads above the angles, which costs 7%.)
+    if (g0 < groups) rot.angles(a, row_position(a, t));
+    auto rows = [&](int ga, int gb, int n, const T* src, T* dst, const void* weight) {
       // Groups [ga, gb) of a tensor's n rows of this token.
-      float cw[8], sw[8];
-      if (!copy) {
+      uint64_t cw[4], sw[4];  // pairs of columns: the arithmetic is two-wide
+      float w[8], wp[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          cw[e] = rot.cs[e];
-          sw[e] = rot.sn[e];
-        }
-        if (weight) {
-          float w[8], wp[8];
-          load_weight(weight, a.w_bf16, col, w);
-          rot.partner(w, wp);
+      for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+      if (weight) {
+        load_weight(weight, a.w_bf16, col, w);
+        rot.partner(w, wp);
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            cw[e] *= w[e];
-            sw[e] *= wp[e];
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        cw[e] = f2pack(rot.cs[2 * e] * w[2 * e], rot.cs[2 * e + 1] * w[2 * e + 1]);
+        sw[e] = f2pack(rot.sn[2 * e] * wp[2 * e], rot.sn[2 * e + 1] * wp[2 * e + 1]);
       }
       src += sub * D + col;
       dst += sub * D + col;
@@ -250,43 +250,181 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdCtas) rope_forward_kernel(con
         for (int j = 0; j < kBatch; ++j) {
           if (g + j >= gb) break;
           const bool valid = (g + j) * RPI + sub < n;
-          float x[8];
+          float x[8], p[8];
           raw[j].get(x);
-          if (!copy) {
-            float p[8];
-            partner_row(rot, raw[j], x, p);
-            float r = 1.f;
-            if (weight) {
-              float ss = 0.f;
+          partner_row(rot, raw[j], x, p);
+          uint64_t x2[4];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-              r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-            }
+          for (int e = 0; e < 4; ++e) x2[e] = f2pack(x[2 * e], x[2 * e + 1]);
+          float r = 1.f;
+          if (weight) {
+            uint64_t s2 = fmul2(x2[0], x2[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = r * fmaf(p[e], sw[e], x[e] * cw[e]);
+            for (int e = 1; e < 4; ++e) s2 = ffma2(x2[e], x2[e], s2);
+            float sa, sb;
+            f2unpack(s2, sa, sb);
+            r = rsqrtf(row_sum<LPR>(sa + sb) * (1.f / D) + a.eps);
           }
+          const uint64_t r2 = f2pack(r, r);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            f2unpack(fmul2(r2, ffma2(f2pack(p[2 * e], p[2 * e + 1]), sw[e], fmul2(x2[e], cw[e]))), x[2 * e],
+                     x[2 * e + 1]);
           if (valid) Vec<T>::store(dst + (g + j) * RPI * D, x);
         }
       }
     };
-    const T* qs = static_cast<const T*>(a.q) + t * a.q_str;
-    const T* ks = static_cast<const T*>(a.k) + t * a.k_str;
     if (g0 < gq)
-      rows(g0, g1 < gq ? g1 : gq, a.heads, qs, static_cast<T*>(a.qo) + t * a.qo_str, a.qw, false);
-    long long in = 0, kpage = 0, vpage = 0;
-    if (APPEND) {
-      const long long page = slot >> a.page_shift;
-      in = (slot & ((1LL << a.page_shift) - 1)) * a.kv_heads * D;
-      kpage = page * a.kc_page;
-      vpage = page * a.vc_page;
+      rows(g0, g1 < gq ? g1 : gq, a.heads, static_cast<const T*>(a.q) + t * a.q_str,
+           static_cast<T*>(a.qo) + t * a.qo_str, a.qw);
+    if (g1 > gq)
+      rows((g0 > gq ? g0 : gq) - gq, g1 - gq, a.kv_heads, static_cast<const T*>(a.k) + t * a.k_str,
+           static_cast<T*>(a.ko) + t * a.ko_str, a.kw);
+  }
+}
+
+// Norm weight and rotation of a token, folded: a row is out = r (x cw + partner
+// sw) with cw = w cos and sw = w_partner sin, two columns at a time.
+template <int D, bool INTER>
+__device__ __forceinline__ void fold(const RopeArgs& a, const Rot<D, INTER>& rot, const void* weight, int col,
+                                     uint64_t (&cw)[4], uint64_t (&sw)[4]) {
+  float w[8], wp[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+  if (weight) {
+    load_weight(weight, a.w_bf16, col, w);
+    rot.partner(w, wp);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    cw[e] = f2pack(rot.cs[2 * e] * w[2 * e], rot.cs[2 * e + 1] * w[2 * e + 1]);
+    sw[e] = f2pack(rot.sn[2 * e] * wp[2 * e], rot.sn[2 * e + 1] * wp[2 * e + 1]);
+  }
+}
+
+// The rows of one group, normed and turned, to dst.
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, bool norm, float eps,
+                                     const uint64_t (&cw)[4], const uint64_t (&sw)[4], bool valid, T* dst) {
+  constexpr int LPR = D / 8;
+  float x[8], p[8];
+  v.get(x);
+  partner_row(rot, v, x, p);
+  uint64_t x2[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x2[e] = f2pack(x[2 * e], x[2 * e + 1]);
+  float r = 1.f;
+  if (norm) {
+    uint64_t s2 = fmul2(x2[0], x2[0]);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) s2 = ffma2(x2[e], x2[e], s2);
+    float sa, sb;
+    f2unpack(s2, sa, sb);
+    r = rsqrtf(row_sum<LPR>(sa + sb) * (1.f / D) + eps);
+  }
+  const uint64_t r2 = f2pack(r, r);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    f2unpack(fmul2(r2, ffma2(f2pack(p[2 * e], p[2 * e + 1]), sw[e], fmul2(x2[e], cw[e]))), x[2 * e],
+             x[2 * e + 1]);
+  if (valid) Vec<T>::store(dst, x);
+}
+
+// Append: the same with k and v written to their pages.  Its calls are short,
+// so a token's first loads go out before its angles are computed, its slot and
+// position come with the token before, and k and v share a batch of loads (17K
+// tokens of 12/4 heads, d = 64, without norm: 20.0 -> 15.7 us; in the forward
+// the registers that this takes cost long calls 7%).
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeArgs a) {
+  let_next_start();
+  wait_for_previous();
+  using T = __nv_bfloat16;
+  constexpr int LPR = D / 8, RPI = 32 / LPR, N = kBatch / 2;
+  const int lane = threadIdx.x & 31, col = 8 * (lane % LPR), sub = lane / LPR;
+  const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
+  const int groups = gq + gk;  // v goes with k
+  const int per = (groups + a.parts - 1) / a.parts;
+  const long long items = a.T * a.parts;
+  const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
+  const int off = sub * D + col;
+  Rot<D, INTER> rot;
+  rot.place(a, lane);
+  auto token = [&](long long it) { return a.parts == 1 ? it : it / a.parts; };
+  // Group g of n rows from src, if it is below gb.
+  auto fetch = [&](Vec<T>& raw, const T* src, int g, int gb, int n) {
+    raw = Vec<T>();
+    if (g < gb && g * RPI + sub < n) raw.load(src + g * RPI * D + off);
+  };
+  uint64_t cw[4], sw[4];
+  long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (it >= items) return;
+  long long t = token(it), pos = a.positions[t], slot = a.slots[t];
+  for (;;) {
+    const int g0 = a.parts == 1 ? 0 : static_cast<int>(it - t * a.parts) * per;
+    const int g1 = g0 + per < groups ? g0 + per : groups;
+    const int q1 = g1 < gq ? g1 : gq;  // q groups [g0, q1), then k and v groups [k0, k1)
+    const int k0 = g0 > gq ? g0 - gq : 0, k1 = g1 - gq;
+    const bool real = slot >= 0 && slot < a.n_slots;  // else padding: nothing is written
+    const T* const qsrc = static_cast<const T*>(a.q) + t * a.q_str;
+    Vec<T> raw[kBatch];
+    if (real && g0 < q1) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) fetch(raw[j], qsrc, g0 + j, q1, a.heads);
     }
-    if (g1 > gq && g0 < gq + gk)
-      rows((g0 > gq ? g0 : gq) - gq, (g1 < gq + gk ? g1 : gq + gk) - gq, a.kv_heads, ks,
-           APPEND ? static_cast<T*>(a.kc) + kpage + in : static_cast<T*>(a.ko) + t * a.ko_str, a.kw,
-           false);
-    if (APPEND && g1 > gq + gk)
-      rows((g0 > gq + gk ? g0 : gq + gk) - gq - gk, g1 - gq - gk, a.kv_heads,
-           static_cast<const T*>(a.v) + t * a.v_str, static_cast<T*>(a.vc) + vpage + in, nullptr, true);
+    long long pos2 = 0, slot2 = 0;
+    if (it + nwarps < items) {
+      const long long t2 = token(it + nwarps);
+      pos2 = a.positions[t2];
+      slot2 = a.slots[t2];
+    }
+    if (real) {
+      rot.angles(a, pos);
+      if (g0 < q1) {
+        fold(a, rot, a.qw, col, cw, sw);
+        T* const dst = static_cast<T*>(a.qo) + t * a.qo_str + off;
+        for (int g = g0; g < q1; g += kBatch) {
+          if (g > g0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) fetch(raw[j], qsrc, g + j, q1, a.heads);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            if (g + j >= q1) break;
+            turn(rot, raw[j], a.qw != nullptr, a.eps, cw, sw, (g + j) * RPI + sub < a.heads,
+                 dst + (g + j) * RPI * D);
+          }
+        }
+      }
+      if (k0 < k1) {
+        fold(a, rot, a.kw, col, cw, sw);
+        const T* const ksrc = static_cast<const T*>(a.k) + t * a.k_str;
+        const T* const vsrc = static_cast<const T*>(a.v) + t * a.v_str;
+        const long long page = slot >> a.page_shift;
+        const long long in = (slot & ((1LL << a.page_shift) - 1)) * a.kv_heads * D + off;
+        T* const kdst = static_cast<T*>(a.kc) + page * a.kc_page + in;
+        T* const vdst = static_cast<T*>(a.vc) + page * a.vc_page + in;
+        for (int g = k0; g < k1; g += N) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            fetch(raw[j], ksrc, g + j, k1, a.kv_heads);
+            fetch(raw[N + j], vsrc, g + j, k1, a.kv_heads);
+          }
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            if (g + j >= k1) break;
+            const bool valid = (g + j) * RPI + sub < a.kv_heads;
+            turn(rot, raw[j], a.kw != nullptr, a.eps, cw, sw, valid, kdst + (g + j) * RPI * D);
+            if (valid) raw[N + j].put(vdst + (g + j) * RPI * D);
+          }
+        }
+      }
+    }
+    it += nwarps;
+    if (it >= items) return;
+    t = token(it);
+    pos = pos2;
+    slot = slot2;
   }
 }
 
@@ -409,22 +547,23 @@ __global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const Rop
   if (dst) dst[i % d] = x;
 }
 
-template <typename T, bool APPEND>
-cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
-  if (a.T == 0) return cudaSuccess;
-  // Few tokens: several warps share a token's rows, down to one batch of
-  // loads each, until there are some 16 warps per SM.
-  const int rpi = 256 / d, gq = (a.heads + rpi - 1) / rpi, gk = (a.kv_heads + rpi - 1) / rpi;
-  const int groups = gq + (APPEND ? 2 : 1) * gk;
+// Few tokens: several warps share a token's rows, down to one batch of loads
+// each, until there are some 16 warps per SM.  Sets a.parts; the grid is one
+// wave of `ctas` per SM at most.
+unsigned share(RopeArgs& a, int d, int ctas) {
+  const int rpi = 256 / d, groups = (a.heads + rpi - 1) / rpi + (a.kv_heads + rpi - 1) / rpi;
   const long long want = (16LL * sm_count() + a.T - 1) / a.T, most_parts = (groups + kBatch - 1) / kBatch;
   a.parts = static_cast<int>(want < most_parts ? want : most_parts);
-  long long ctas = (a.T * a.parts + kWarps - 1) / kWarps;
-  const long long most = static_cast<long long>(kFwdCtas) * sm_count();  // one wave
-  const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-  auto* kernel = d == 128 ? (a.interleaved ? rope_forward_kernel<T, 128, true, APPEND>
-                                          : rope_forward_kernel<T, 128, false, APPEND>)
-                         : (a.interleaved ? rope_forward_kernel<T, 64, true, APPEND>
-                                          : rope_forward_kernel<T, 64, false, APPEND>);
+  const long long need = (a.T * a.parts + kWarps - 1) / kWarps, most = static_cast<long long>(ctas) * sm_count();
+  return static_cast<unsigned>(need < most ? need : most);
+}
+
+template <typename T>
+cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
+  if (a.T == 0) return cudaSuccess;
+  const unsigned grid = share(a, d, kFwdCtas<T>);
+  auto* kernel = d == 128 ? (a.interleaved ? rope_forward_kernel<T, 128, true> : rope_forward_kernel<T, 128, false>)
+                         : (a.interleaved ? rope_forward_kernel<T, 64, true> : rope_forward_kernel<T, 64, false>);
   return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
@@ -444,11 +583,16 @@ int rope_grad_ctas(const RopeArgs& a) {
 }
 
 cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st) {
-  return bf16 ? forward_t<__nv_bfloat16, false>(a, d, st) : forward_t<float, false>(a, d, st);
+  return bf16 ? forward_t<__nv_bfloat16>(a, d, st) : forward_t<float>(a, d, st);
 }
 
-cudaError_t launch_rope_append(const RopeArgs& a, int d, cudaStream_t st) {
-  return forward_t<__nv_bfloat16, true>(a, d, st);
+cudaError_t launch_rope_append(const RopeArgs& args, int d, cudaStream_t st) {
+  RopeArgs a = args;
+  if (a.T == 0) return cudaSuccess;
+  const unsigned grid = share(a, d, 3);
+  auto* kernel = d == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
+                         : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
+  return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
 cudaError_t launch_rope_backward(const RopeArgs& a, int d, bool bf16, cudaStream_t st) {

@@ -12,7 +12,7 @@
 #include <exception>
 #include <string>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -223,7 +223,7 @@ struct Out {
   Out(PyObject* o, const char* name) : t(maybe(o, name)), given(o == Py_None ? nullptr : o) {}
   const Tensor& get(at::IntArrayRef sizes, ScalarType type, const Tensor& like) {
     if (!t) {
-      made = at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+      made = at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
       t = &made;
     }
     return *t;
