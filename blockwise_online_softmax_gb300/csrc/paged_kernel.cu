@@ -45,6 +45,7 @@ using namespace paged;
 constexpr int BT = 64;           // keys per tile
 constexpr int kCons = 4;         // consumer warps
 constexpr int kThreads = 256;    // a consumer warpgroup and one with the producers
+constexpr int kExtra = 1;        // what an item's beginning and end cost, in tiles
 constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
 
 template <int D, int NT>
@@ -77,7 +78,7 @@ struct Item {
   int k0;              // first key tile here
   int tiles;           // key tiles here
   int slot;            // partial slot, or -1: the item is whole
-  int pad;
+  int last;            // the CTA's last item; 2: not even an item
 };
 static_assert(sizeof(Item) == 32, "record layout");
 
@@ -146,7 +147,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
   wait_for_previous();
   if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, kThreads>(a, g, RT, smem + C::OFF_BUF);  // synchronizes
+  const Run run = find_run<BT, kExtra, kThreads>(a, g, RT, smem + C::OFF_BUF);  // synchronizes
   if (run.first >= run.last || *abort_flag) return;
   const long long lim = a.wait_limit;
 
@@ -161,15 +162,27 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     const int npg = BT / rows;
     const uint32_t box = static_cast<uint32_t>(rows) * 128u;
     auto full = [&](int s) -> uint32_t { return is_k ? kfull(s) : vfull(s); };
-    Walk<BT> w;
+    Walk<BT, kExtra> w;
     w.start(a, g, RT, run.r, run.x);
     long long u = run.first;
+    if (w.k >= w.t.nt) {  // the run begins behind an item's last tile
+      u += w.t.nt + kExtra - w.k;
+      if (u < run.last) w.next(a, g, RT);
+      else if (is_k && lane == 0) {
+        reinterpret_cast<Item*>(smem + C::OFF_ITEM)->last = 2;
+        mbar_arrive(ifull(0));
+      }
+      if (u >= run.last && is_k) copies_arrive(ifull(0));
+    }
     bool ok = true;
     int i = 0;   // tiles requested
     int it = 0;  // items begun
     while (ok && u < run.last) {
       const long long left = run.last - u;
       const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
+      const long long after = u + tiles + (w.k + tiles == w.t.nt ? kExtra : 0);
+      PageIds ids;  // first: the record and the query rows hide its latency
+      ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
       if (is_k) {
         const int s = it % C::ITEMS;
         if (it >= C::ITEMS) {
@@ -182,7 +195,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         int* rec = reinterpret_cast<int*>(smem + C::OFF_ITEM + s * C::REC);
         int row = 0;
         if (lane < RT) {  // rows past the item's get its last row's keys, and no output
-          const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = rr / g;
+          const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = token_of(rr, g);
           row = (w.q.row0 + j) * a.heads + w.kh * g + (rr - j * g);
           rec[8 + lane] = row;
           rec[8 + RT + lane] = key_end(w.q, j) - base;
@@ -192,7 +205,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
           const int me = static_cast<int>(blockIdx.x);
           *reinterpret_cast<Item*>(rec) =
-              Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), 0};
+              Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), after >= run.last};
           if (c0 != c1 && me == c0) cuts[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
         }
         __syncwarp();
@@ -209,8 +222,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         copies_arrive(ifull(s));
         ++it;
       }
-      PageIds ids;
-      ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
       for (int k = 0; k < tiles; ++k, ++i) {
         const int key0 = (w.t.t0 + w.k + k) * BT;
         const int page = ids.get(a, key0, rows, npg, lane);
@@ -233,7 +244,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             tma_load_4d(dst + ch * CHB, tm, full(s), ch * 64, w.kh, row, page);
         }
       }
-      u += tiles;
+      u = after;
       if (ok && u < run.last) w.next(a, g, RT);
     }
     if (!ok) {  // let the copies in flight land before the CTA leaves
@@ -260,20 +271,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   bool ok = true;
   int st = 0;                // stage and phase of the next tile
   uint32_t par = 0;
-  long long u = run.first;
   // ldmatrix addresses inside a 64-column chunk of a tile: K rows are keys
   // (8 x 8 blocks: keys 0-7 / 8-15 first, then columns), V the same blocks
   // with columns first, read transposed.
   const int kr = warp * 16 + (lane & 15), kc0 = lane >> 4;
   const int vr = warp * 16 + (lane & 7) + ((lane >> 4) << 3), vc0 = (lane >> 3) & 1;
-  for (int it = 0; u < run.last; ++it) {
+  for (int it = 0;; ++it) {
     const int is = it % C::ITEMS;
     ok = ok && wait_bar(ifull(is), static_cast<uint32_t>(it / C::ITEMS) & 1u, abort_flag,
                         &g_paged_status, 0x85, lim);
     ok = __all_sync(kAll, ok);
     const int* rec = reinterpret_cast<const int*>(smem + C::OFF_ITEM + is * C::REC);
     Item item = *reinterpret_cast<const Item*>(rec);
-    if (!ok) item.tiles = 0;
+    if (!ok || item.last == 2) item.tiles = 0;
     // Keys [lo, hi) of the lane's rows 8 nt + 2 (lane & 3) + {0, 1}; the keys
     // that every row of the item sees are [lo_all, hi_all).
     auto begin_of = [&](int end) {
@@ -413,7 +423,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         par ^= 1u;
       }
     }
-    u += item.tiles;
     // ---------------------------------------------------------------- the warps' states meet
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -429,7 +438,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           s_l[(8 * nt + 2 * lane + c) * kCons + warp] = x;
         }
       }
-    if (!named_bar_and(1, 32 * kCons, ok)) return;
+    if (!named_bar_and(1, 32 * kCons, ok) || item.last == 2) return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       constexpr int H = D / 32, Q = D / 64;  // 16-column groups of a half and of a quarter
@@ -526,6 +535,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
       }
     }
+    if (item.last) return;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));
   }

@@ -62,6 +62,16 @@ __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
   return q;
 }
 
+// Row rr of a request belongs to token rr / g (mostly the first one).
+__device__ __forceinline__ int token_of(int rr, int g) { return rr < g ? 0 : rr / g; }
+
+// a / b for b > 0, in 32 bits where that is enough.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((static_cast<unsigned long long>(a) | static_cast<unsigned long long>(b)) >> 32) == 0)
+    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 // Token j of the request sees keys [begin, end).
 __device__ __forceinline__ int key_end(const Request& q, int j) {
   const int e = q.len - q.n + j + 1;
@@ -86,8 +96,8 @@ __device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const Request& q
   t.rr0 = rt * RT;
   const int all = q.n * g;
   t.rr1 = t.rr0 + RT < all ? t.rr0 + RT : all;
-  t.hi = key_end(q, (t.rr1 - 1) / g);
-  t.lo = key_begin(a, key_end(q, t.rr0 / g));
+  t.hi = key_end(q, token_of(t.rr1 - 1, g));
+  t.lo = key_begin(a, key_end(q, token_of(t.rr0, g)));
   t.t0 = t.lo / BT;
   t.nt = t.hi > t.lo ? (t.hi - 1) / BT + 1 - t.t0 : 1;
   return t;
@@ -97,17 +107,20 @@ __device__ __forceinline__ int row_tiles(const Request& q, int g, int RT) {
   return (q.n * g + RT - 1) / RT;
 }
 
-template <int BT>
+// The units of a request: its key tiles, and EXTRA for every item, what an
+// item's beginning and end cost in tiles.
+template <int BT, int EXTRA>
 __device__ __forceinline__ long long request_units(const PagedArgs& a, int r, int g, int RT) {
   const Request q = load_request(a, r);
   const int n = row_tiles(q, g, RT);
   long long u = 0;
-  for (int rt = 0; rt < n; ++rt) u += row_tile<BT>(a, q, g, RT, rt).nt;
+  for (int rt = 0; rt < n; ++rt) u += row_tile<BT>(a, q, g, RT, rt).nt + EXTRA;
   return u * a.kv_heads;
 }
 
-// Where a CTA's run of units starts, and how the walk goes on.
-template <int BT>
+// A walk over a CTA's run of units, item by item.  An item's units are its key
+// tiles and, after them, its EXTRA.
+template <int BT, int EXTRA>
 struct Walk {
   int r, rt, kh, nrt;
   Request q;
@@ -118,18 +131,19 @@ struct Walk {
     q = load_request(a, r);
     nrt = row_tiles(q, g, RT);
   }
-  // Start at unit x of request r.
+  // Start at unit x of request r; k may be past the last tile (in the EXTRA).
   __device__ __forceinline__ void start(const PagedArgs& a, int g, int RT, int r_, long long x) {
     r = r_;
     enter(a, g, RT);
     for (rt = 0;; ++rt) {
       t = row_tile<BT>(a, q, g, RT, rt);
-      const long long w = static_cast<long long>(t.nt) * a.kv_heads;
+      const long long w = static_cast<long long>(t.nt + EXTRA) * a.kv_heads;
       if (x < w || rt + 1 >= nrt) break;
       x -= w;
     }
-    kh = static_cast<int>(x / t.nt);
-    k = static_cast<int>(x % t.nt);
+    const long long h = divide(x, t.nt + EXTRA);
+    kh = static_cast<int>(h);
+    k = static_cast<int>(x - h * (t.nt + EXTRA));
   }
   // To the next item; the caller knows that there is one (the bound on r only
   // keeps arrays that change under the kernel from leading it outside).
@@ -148,25 +162,26 @@ struct Walk {
   }
 };
 
-// Prefix sum over the requests: every thread of the CTA gets the total; the
-// unit `first` = floor(c total / G) of CTA c is located as (request, offset).
-// With fewer units than CTAs only `ctas` of them work, one unit each, so the
-// CTAs of a cut item all hold a part of it.
+// Prefix sum over the requests: every thread of the CTA gets the total, split
+// into runs of `size` or, the first `longer` of them, size + 1 units; the first
+// unit of the CTA's own is located as (request, offset).  With fewer units than
+// CTAs only `ctas` of them work, so the CTAs of a cut item all hold a part of it.
 struct Run {
   long long total, first, last;
-  int ctas;
+  long long size;
+  int longer, ctas;
   int r;
   long long x;
 };
 
-template <int BT, int kThreads>
+template <int BT, int EXTRA, int kThreads>
 __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch) {
   long long* s_sum = static_cast<long long*>(scratch);  // [kThreads / 32], then the location
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_req + kThreads - 1) / kThreads;
   const int i0 = tid * per, i1 = i0 + per < a.n_req ? i0 + per : a.n_req;
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_units<BT>(a, i, g, RT);
+  for (int i = i0; i < i1; ++i) mine += request_units<BT, EXTRA>(a, i, g, RT);
   long long x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -185,16 +200,21 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
   run.total = total;
   run.ctas = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   run.first = run.last = total;
-  if (static_cast<int>(blockIdx.x) < run.ctas) {
-    run.first = static_cast<long long>(blockIdx.x) * total / run.ctas;
-    run.last = static_cast<long long>(blockIdx.x + 1) * total / run.ctas;
+  const int me = static_cast<int>(blockIdx.x);
+  if (run.ctas > 0) {
+    run.size = divide(total, run.ctas);
+    run.longer = static_cast<int>(total - run.size * run.ctas);
+    if (me < run.ctas) {
+      run.first = run.size * me + (me < run.longer ? me : run.longer);
+      run.last = run.first + run.size + (me < run.longer ? 1 : 0);
+    }
   }
   if (run.first < run.last && before <= run.first && run.first < before + mine) {
     long long at = run.first - before;
     int i = i0;
-    for (;; ++i) {
-      const long long u = request_units<BT>(a, i, g, RT);
-      if (at < u || i + 1 >= i1) break;
+    for (; i + 1 < i1; ++i) {
+      const long long u = request_units<BT, EXTRA>(a, i, g, RT);
+      if (at < u) break;
       at -= u;
     }
     s_sum[kThreads / 32] = at;
@@ -208,7 +228,8 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
 
 // CTA whose run holds unit u.
 __device__ __forceinline__ int cta_of(long long u, const Run& run) {
-  return static_cast<int>(((u + 1) * run.ctas - 1) / run.total);
+  const long long big = run.longer * (run.size + 1);
+  return static_cast<int>(u < big ? divide(u, run.size + 1) : run.longer + divide(u - big, run.size));
 }
 
 // The page ids of an item's key tiles, as a producer warp needs them: 32 table
