@@ -7,10 +7,13 @@
 //
 // The work is the read of the pages: each key meets only the rows of its KV
 // head (g heads x the request's new tokens).  Its units are 64-key tiles, in
-// the order (request, row tile, KV head, key tile), and every CTA of a grid of
-// two per SM takes an equal run of them, whatever the lengths are: the lengths
-// stay on the device.  A CTA finds its run by a prefix sum over the requests.
-// An item (request, row tile, KV head) that falls into one CTA is finished
+// the order (request, row tile, KV head, key tile), with one unit more for what
+// an item (request, row tile, KV head) costs besides its tiles, and every CTA
+// of a grid of two per SM takes an equal run of them, whatever the lengths are:
+// the lengths stay on the device.  (Without that unit the CTA with the short
+// requests ended last: 16 requests of up to 2K keys, 18.3 against 14.4 us.)  A
+// CTA finds its run by a prefix sum over the requests.
+// An item that falls into one CTA is finished
 // there; one cut by a border between CTAs leaves a partial state (m, l, O~) on
 // each side, and a second launch joins them in CTA order.
 //
@@ -52,6 +55,9 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int NCH = D / 64;
   static constexpr int RT = 8 * NT;              // query rows of an item
+  // Registers of the two warpgroups; together the launch's 2 x 128.  (200 and
+  // 56 spill in the producers: 152 requests of 128 keys 19.3 against 18.5 us.)
+  static constexpr int CONS_REGS = NT == 1 ? 152 : 192, PROD_REGS = 256 - CONS_REGS;
   static constexpr int ITEMS = NT == 1 ? 3 : 2;  // records and query tiles in flight
   static constexpr uint32_t TILE = BT * D * 2;
   static constexpr int NST = D == 128 ? 3 : 6;   // stages of one K and one V tile
@@ -153,7 +159,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 
   if (warp >= kCons) {
     // ---------------------------------------------------------------- producers
-    regs_dec<56>();
+    regs_dec<C::PROD_REGS>();
     if (warp >= kCons + 2) return;
     const bool is_k = warp == kCons;
     const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
@@ -257,7 +263,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
 
   // ------------------------------------------------------------------ consumers
-  regs_inc<200>();
+  regs_inc<C::CONS_REGS>();
   // After a wait that gave up, a warp runs on without waiting (the status
   // word says that the results are void) to the item's first barrier, where
   // all of them learn of it and leave together.  Every warp waits for every

@@ -504,7 +504,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
  * their pages: row t's k (normed, turned) and v go to slots[t], its q to
  * row t of q_out (dense, bf16; may be q where that is dense).  A row whose
  * slot is outside [0, n_pages * page_size) is padding: nothing is written
- * for it.  Two rows with the same slot: one of them ends up there.  bf16.
+ * for it.  Two rows with the same slot leave a mix of both there.  bf16.
  *
  * ra_paged_decode -- attention of each request's newest tokens over its
  * pages: query row j of the n_i rows of request i sits at position
@@ -522,7 +522,9 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
  *   entries; lengths beyond max_pages * page_size count as that.  A page
  *   outside [0, n_pages) is not read, and that request's result is
  *   undefined.  What lies behind a request's last token in its last page
- *   does not matter, NaN included.
+ *   does not matter, NaN included.  Keys and values that a request does see
+ *   should be finite: a value that is not gives NaN in every row of that
+ *   request's new tokens, in those that do not see its key too.
  *   heads / kv_heads <= 128, T * heads <= 2^31 - 256.
  */
 int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* block_table,
