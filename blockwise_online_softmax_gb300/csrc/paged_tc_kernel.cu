@@ -68,8 +68,8 @@ struct Cfg {
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_ST = TILE;      // stage s: K at OFF_ST + 2 s TILE, V after it
   static constexpr uint32_t OFF_AL = OFF_ST + NST * 2 * TILE;  // alpha of two tiles
-  static constexpr uint32_t OFF_X = OFF_AL + 2 * RT * 4;       // exchange of a row's two threads
-  static constexpr uint32_t OFF_INV = OFF_X + 2 * RT * 4;      // 1 / l of an item's rows
+  static constexpr uint32_t OFF_X = OFF_AL + 2 * RT * 4;       // running maximum after two tiles
+  static constexpr uint32_t OFF_INV = OFF_X + 2 * RT * 4;      // l of one group, then 1 / l, of an item's rows
   static constexpr uint32_t OFF_ITEM = OFF_INV + RT * 4;
   // Barriers: K and V tiles in, stage free; S(k); P(k); T(k) ready, which also
   // frees P(k)'s columns; T(k) and alpha(k) read; alpha(k) there; query rows
@@ -77,8 +77,8 @@ struct Cfg {
   // issuers' drains.  Those of a tile come in pairs, by its parity.
   static constexpr int B_KF = 0, B_VF = B_KF + NST, B_E = B_VF + NST, B_S = B_E + NST,
                        B_P = B_S + 2, B_T = B_P + 2, B_TF = B_T + 2, B_AL = B_TF + 2,
-                       B_QF = B_AL + 2, B_I = B_QF + 1, B_IF = B_I + 2,
-                       B_ML = B_IF + 2, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 1, NBAR = B_DRAIN + 2;
+                       B_M = B_AL + 2, B_QF = B_M + 2, B_I = B_QF + 1, B_IF = B_I + 2,
+                       B_L = B_IF + 2, B_ML = B_L + 1, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 2, NBAR = B_DRAIN + 2;
   static constexpr uint32_t OFF_BAR = OFF_ITEM + 2 * sizeof(Item);
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr uint32_t SMEM = OFF_MISC + 16;
@@ -93,6 +93,29 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  // (valid after tmem_wait_ld)
+}
+
+// The two values cut to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t high_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+// What that leaves of them, exactly.
+__device__ __forceinline__ void drop_high(float& a, float& b) {
+  const float na = __uint_as_float((__float_as_uint(a) & 0xffff0000u) ^ 0x80000000u);
+  const float nb = __uint_as_float((__float_as_uint(b) & 0xffff0000u) ^ 0x80000000u);
+  f2unpack(fadd2(f2pack(a, b), f2pack(na, nb)), a, b);
 }
 
 template <int D>
@@ -113,8 +136,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (tid == 0) {
     for (int i = 0; i < C::NBAR; ++i) {
       uint32_t n = 1;
-      if (i == C::B_P || i == C::B_P + 1) n = 256;
-      if ((i >= C::B_TF && i < C::B_AL + 2) || i == C::B_ML || i == C::B_MLF) n = 128;
+      if ((i >= C::B_P && i < C::B_P + 2) || (i >= C::B_TF && i < C::B_M + 2) || (i >= C::B_L && i < C::B_DRAIN)) n = 128;
       if (i == C::B_IF || i == C::B_IF + 1) n = 13;  // warps 0-11 and 15
       mbar_init(bar(i), n);
     }
@@ -141,7 +163,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   const int total = static_cast<int>(run.last - run.first);  // tiles of this CTA
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
   float* s_al = reinterpret_cast<float*>(smem + C::OFF_AL);
-  float* s_x = reinterpret_cast<float*>(smem + C::OFF_X);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_X);
   float* s_inv = reinterpret_cast<float*>(smem + C::OFF_INV);
   auto wait = [&](int b, uint32_t parity, int code) {
     const bool w = wait_bar(bar(b), parity & 1u, abort_flag, status, code, lim);
@@ -294,12 +316,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE, CHB, 1024);
           const uint32_t pbuf = tmem + C::C_S + static_cast<uint32_t>(k & 1) * BT;
-          const uint32_t term[3] = {tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64, pbuf + 64, pbuf};
-#pragma unroll
+          // 16 keys: eight columns of each term, the first two side by side.
+          const uint32_t third = tmem + C::C_LO + static_cast<uint32_t>(k & 1) * 64;
+#pragma unroll 1
           for (int x = 0; x < 3; ++x)
 #pragma unroll
             for (int kk = 0; kk < BT / 16; ++kk)
-              mma_ts(tmem + C::C_T, term[x] + kk * 8, vd + static_cast<uint64_t>((kk * 2048) >> 4),
+              mma_ts(tmem + C::C_T, x ? pbuf + (2 - x) * 8 + kk * 16 : third + kk * 8, vd + static_cast<uint64_t>((kk * 2048) >> 4),
                      idesc_pv, x + kk > 0 ? 1u : 0u);
           tc_commit(bar(C::B_E + st));
           tc_commit(bar(C::B_T + (k & 1)));
@@ -312,137 +335,159 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     __syncwarp();
   } else if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    // Warps 0-3 take keys 0-63 of a tile, warps 4-7 keys 64-127.  A wait that
-    // gave up shows at the next barrier of the two, where all of them leave.
+    // Warps 0-3 take the CTA's even tiles, warps 4-7 the odd ones.
     regs_dec<120>();
-    constexpr int HT = BT / 2;
-    const int r = tid & 127, half = warp >> 2;
+    const int r = tid & 127, gi = warp >> 2;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const float sl2 = a.scale_log2;
     const uint64_t sl2x2 = f2pack(sl2, sl2);
     const int win = static_cast<int>(a.window);
+    const uint32_t s_col = tl + C::C_S + static_cast<uint32_t>(gi) * BT;
+    const uint32_t lo_col = tl + C::C_LO + static_cast<uint32_t>(gi) * (BT / 2);
     bool ok = true;
-    int k = 0;  // tile
-    for (int it = 0; k < total; ++it) {
-      ok = ok && wait_item(it);
-      Item x = items[it & 1];
-      if (ok) free_item(it);
-      else x.tiles = 1;
+    int joins = 0;  // items so far that both groups had tiles of
+    for (int it = 0, first = 0; ok && first < total; ++it) {
+      ok = wait_item(it);
+      if (!ok) break;
+      const Item x = items[it & 1];
+      free_item(it);
       // Keys [lo, hi) of the row (rows past the item's do as its last).
       const int rr = x.rr0 + (r < x.rows ? r : x.rows - 1);
       int hi = x.end0 + rr / g;
       if (hi < -x.base) hi = -x.base;
       const int lo = win > 0 && hi + x.base > win ? hi - win : -x.base;
-      float m = -INFINITY, l = 0.f;
-      bool left = false;
-      for (int t = 0; t < x.tiles; ++t, ++k) {
-        const uint32_t s_col = C::C_S + static_cast<uint32_t>(k & 1) * BT;
-        const uint32_t lo_col = C::C_LO + static_cast<uint32_t>(k & 1) * (BT / 2);
-        ok = ok && wait(C::B_S + (k & 1), static_cast<uint32_t>(k >> 1), 0x9a);
+      float m = -INFINITY, l = 0.f, alpha = 0.f;
+      for (int t = (first ^ gi) & 1; t < x.tiles; t += 2) {
+        const int k = first + t;
+        const int k0 = (x.k0 + t) * BT;
+        const int lo_j = lo - k0, hi_j = hi - k0;
+        // Of any of the warp's rows: the branches below hold warp-wide accesses.
+        const bool cut = __any_sync(kAll, lo_j > 0 || hi_j < BT);
+        ok = wait(C::B_S + gi, static_cast<uint32_t>(k >> 1), 0x9a);
+        if (!ok) break;
         tc_fence_after();
-        uint32_t sr[2][32];
+        // Both passes are rolled: unrolled, a tile's code was fetched anew
+        // tile after tile and the warps waited for it most of the time.
+        float mine = -INFINITY;
+#pragma unroll 1
+        for (int c0 = 0; c0 < BT; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(s_col + c0, v);
+          tmem_wait_ld();
+          reg_fence32(v);
+          if (cut) {  // masked keys become -inf in place
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) tmem_ld32(tl + s_col + half * HT + cc * 32, sr[cc]);
-        tmem_wait_ld();
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[8];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) reg_fence32(sr[cc]);
-        const int k0 = (x.k0 + t) * BT, kh0 = k0 + half * HT;
-        const int lo_j = lo - kh0, hi_j = hi - kh0;
-        if (lo_j > 0 || hi_j < HT) {
+              for (int e = 0; e < 8; ++e) {
+                if (c0 + j + e < lo_j || c0 + j + e >= hi_j) v[j + e] = 0xff800000u;
+                w[e] = v[j + e];
+              }
+              tmem_st8(s_col + c0 + j, w);
+            }
+          }
+#define RA_S(j) __uint_as_float(v[j])
+          float mx0 = fmaxf(RA_S(0), RA_S(2)), mx1 = fmaxf(RA_S(1), RA_S(3));
 #pragma unroll
-          for (int j = 0; j < HT; ++j)
-            if (j < lo_j || j >= hi_j) sr[j >> 5][j & 31] = 0xff800000u;  // -inf
+          for (int j = 4; j < 32; j += 4) {
+            mx0 = fmax3(mx0, RA_S(j + 0), RA_S(j + 2));
+            mx1 = fmax3(mx1, RA_S(j + 1), RA_S(j + 3));
+          }
+          mine = fmax3(mine, mx0, mx1);
         }
-#define RA_S(j) __uint_as_float(sr[(j) >> 5][(j) & 31])
-        float mx0 = fmaxf(RA_S(0), RA_S(4)), mx1 = fmaxf(RA_S(1), RA_S(5));
-        float mx2 = fmaxf(RA_S(2), RA_S(6)), mx3 = fmaxf(RA_S(3), RA_S(7));
-#pragma unroll
-        for (int j = 8; j < HT; j += 8) {
-          mx0 = fmax3(mx0, RA_S(j + 0), RA_S(j + 4));
-          mx1 = fmax3(mx1, RA_S(j + 1), RA_S(j + 5));
-          mx2 = fmax3(mx2, RA_S(j + 2), RA_S(j + 6));
-          mx3 = fmax3(mx3, RA_S(j + 3), RA_S(j + 7));
-        }
-        const float mine = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        // Everyone has read the exchange of the tile before, ...
-        tc_fence_before();
-        if (!named_bar_and(1, 256, ok)) {
-          left = true;
-          break;
-        }
-        s_x[half * RT + r] = mine;
-        // ... and has S in registers, over which P is written below.
-        named_bar_sync(2, 256);
-        tc_fence_after();
-        const float mn = fmaxf(m, fmaxf(mine, s_x[(half ^ 1) * RT + r]) * sl2);
+        // The running maximum goes from group to group.
+        if (k > 0) ok = wait(C::B_M + (gi ^ 1), static_cast<uint32_t>((k - 1) >> 1), 0xa2);
+        if (!ok) break;
+        const float mp = t > 0 ? s_m[(gi ^ 1) * RT + r] : -INFINITY;
+        const float mn = fmaxf(mp, mine * sl2);
+        s_m[gi * RT + r] = mn;
+        mbar_arrive(bar(C::B_M + gi));
         const float ref = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m - ref);
+        alpha = ex2(mp - ref);
+        l *= ex2(m - ref);
         m = mn;
-        if (half == 0) {
-          // alpha(k - 2), in the same place, has been read.
-          if (k >= 2) ok = wait(C::B_TF + (k & 1), static_cast<uint32_t>((k - 2) >> 1), 0xa1);
-          s_al[(k & 1) * RT + r] = alpha;
-          mbar_arrive(bar(C::B_AL + (k & 1)));
-        }
+        // alpha(k - 2), in the same place, has been read.
+        if (k >= 2) ok = wait(C::B_TF + gi, static_cast<uint32_t>((k - 2) >> 1), 0xa1);
+        if (!ok) break;
+        s_al[gi * RT + r] = alpha;
+        mbar_arrive(bar(C::B_AL + gi));
         const uint64_t nm2 = f2pack(-ref, -ref);
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+        if (cut) tmem_wait_st();
+#pragma unroll 1
+        for (int c0 = 0; c0 < BT; c0 += 16) {  // the terms of 16 keys go where S was
+          uint32_t v[16];
+          tmem_ld16(s_col + c0, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {  // 16 keys
+          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[j]));
           uint32_t p0[8], p1[8], p2[8];
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            const int e = cc * 16 + j;
             float y0, y1;
-            f2unpack(ffma2(f2pack(RA_S(e), RA_S(e + 1)), sl2x2, nm2), y0, y1);
+            f2unpack(ffma2(f2pack(RA_S(j), RA_S(j + 1)), sl2x2, nm2), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
             const uint64_t y = f2pack(y0, y1);
             if (j & 2) acc1 = fadd2(acc1, y);
             else acc0 = fadd2(acc0, y);
-            uint32_t h = bf16x2_rn(y0, y1);
-            p0[j / 2] = h;
-            y0 -= __uint_as_float(h << 16);
-            y1 -= __uint_as_float(h & 0xffff0000u);
-            h = bf16x2_rn(y0, y1);
-            p1[j / 2] = h;
-            y0 -= __uint_as_float(h << 16);
-            y1 -= __uint_as_float(h & 0xffff0000u);
-            p2[j / 2] = bf16x2_rn(y0, y1);
+            p0[j / 2] = high_halves(y0, y1);
+            drop_high(y0, y1);
+            p1[j / 2] = high_halves(y0, y1);
+            drop_high(y0, y1);
+            p2[j / 2] = high_halves(y0, y1);
           }
-          const uint32_t col = tl + half * (HT / 2) + cc * 8;
-          tmem_st8(col + s_col, p0);
-          tmem_st8(col + s_col + BT / 2, p1);
-          tmem_st8(col + lo_col, p2);
+          tmem_st8(s_col + c0, p0);
+          tmem_st8(s_col + c0 + 8, p1);
+          tmem_st8(lo_col + c0 / 2, p2);
         }
 #undef RA_S
-        if (half < C::NCH && (x.lo > k0 || x.hi < k0 + BT)) {
-          // Key row r of this tile is nobody's: zero (half of) it for the product.
+        if (x.lo > k0 || x.hi < k0 + BT) {
+          // Key row r of this tile may be nobody's: zero it for the product.
           const int st = k % C::NST;
-          ok = ok && wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x9b);
+          ok = wait(C::B_VF + st, static_cast<uint32_t>(k / C::NST), 0x9b);
+          if (!ok) break;
           const int key = k0 + r;
           if (key < x.lo || key >= x.hi) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              st_shared_v4(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE + half * CHB + r * 128 + c * 16, 0u, 0u, 0u, 0u);
+            for (int ch = 0; ch < C::NCH; ++ch)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                st_shared_v4(sb + C::OFF_ST + st * 2 * C::TILE + C::TILE + ch * CHB + r * 128 + c * 16, 0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+          __syncwarp();
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::B_P + (k & 1)));
+        mbar_arrive(bar(C::B_P + gi));
         float sa, sc;
         f2unpack(fadd2(acc0, acc1), sa, sc);
-        l = fmaf(l, alpha, sa + sc);
+        l += sa + sc;
       }
-      if (left) break;
-      // A row's two sums meet; the first thread hands 1 / l to the output and
-      // writes the row's statistics.
-      if (!named_bar_and(1, 256, ok)) break;
-      if (half == 1) s_x[RT + r] = l;
-      named_bar_sync(2, 256);
-      if (half == 0) {
-        l += s_x[RT + r];
-        if (it > 0) ok = wait(C::B_MLF, static_cast<uint32_t>(it - 1), 0x9c);
+      if (!ok) break;
+      // A row's two sums meet in the group that had the item's last tile: the
+      // other's refers to the maximum of the tile before, alpha joins them.
+      // That group hands 1 / l to the output and writes the row's statistics.
+      const bool last = ((first + x.tiles - 1) & 1) == gi;
+      first += x.tiles;
+      // s_inv may be written once the item before has been read.  A group that
+      // had no tile of that item did not wait for the one before it, hence two
+      // barriers by parity: among three items in a row it had one.
+      if (it > 0 && last == (x.tiles == 1))
+        ok = wait(C::B_MLF + ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1), 0x9c);
+      if (!ok) break;
+      if (!last && x.tiles > 1) {
+        s_inv[r] = l;
+        mbar_arrive(bar(C::B_L));
+      }
+      if (last) {
+        if (x.tiles > 1) {
+          ok = wait(C::B_L, static_cast<uint32_t>(joins), 0xa3);
+          if (!ok) break;
+          l = fmaf(s_inv[r], alpha, l);
+        }
         s_inv[r] = x.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
         mbar_arrive(bar(C::B_ML));
         if (r < x.rows) {
@@ -456,6 +501,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
         }
       }
+      if (x.tiles > 1) ++joins;
     }
   } else {
     // ---------------------------------------------------------------- output sum
@@ -498,7 +544,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       ok = wait(C::B_ML, static_cast<uint32_t>(it), 0xa0);
       if (!ok) break;
       const float inv = s_inv[r];
-      mbar_arrive(bar(C::B_MLF));
+      mbar_arrive(bar(C::B_MLF + (it & 1)));
       if (r >= x.rows) continue;
       const int rr = x.rr0 + r, j0 = rr / g;
       const long long row = x.slot >= 0 ? static_cast<long long>(x.slot) * RT + r
