@@ -621,10 +621,10 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
 
 // Rows per request and KV head on average (exact when every request has the
 // same number of new tokens; with cu_q any mix is computed right, the average
-// only picks the kernel).  Rows past a tile read the pages again.  152 requests
-// of 1K keys, 32 rows: 16-row tiles 185 us, 128-row tiles 152 us at d = 128;
-// 64 requests of 2K keys, 32 rows at d = 64: 111 against 120 us; 128 rows at d =
-// 128: 707 against 168 us.
+// only picks the kernel).  Rows past a tile read the pages again.  16-row tiles
+// against 128-row tiles, 32 rows: d = 128, 152 requests of 1K keys 185 / 142 us;
+// d = 64, the same 131 / 119, 64 of 2K keys 110 / 107, 64 of 500 41 / 44, 16 of
+// 300 17 / 20.  128 rows, d = 128, 152 requests of 1K keys: 707 / 166 us.
 int paged_row_tile(const PagedArgs& a, int d) {
   const long long rows = (a.T + a.n_req - 1) / a.n_req * (a.heads / a.kv_heads);
   return rows <= 8 ? 8 : (rows <= (d == 64 ? 32 : 16) ? 16 : 128);

@@ -8,18 +8,24 @@
 // at 32 rows, 0.7 at 128); here a tile's products are 128 rows at once, and
 // the read of the pages is the bound again.
 //
-// Roles of the 16 warps: 0-7 softmax (a row has two threads, one for each half
-// of a tile's keys, that exchange their maxima), 8-11 the output sum (a thread
-// has a row), 12 K loads and the walk over the items, 13 V loads, 14 the P V
-// products, 15 the query rows and the Q K products (one issuer for both spent a
-// third of a tile between the two: 163 us where two take 152).  With one softmax thread per row its 128 weights,
-// split in three terms each, took 4700 cycles a tile, twice the products.
-//   S(k) = Q K(k)^T, two buffers in TMEM.  The softmax writes P(k) as three
-//   bf16 terms (8 + 8 + 8 bits of the weights, so that the fp32 result has
-//   them in fp32): two over S(k), one beside.  T = P(k) V(k), the small terms
-//   first, goes to a buffer of its own, and the output sum takes it as
-//   o = o alpha + T in fp32 registers: the tensor core's own accumulation over
-//   many tiles truncates, and O never needs a rescale in TMEM.
+// Roles of the 16 warps: 0-3 and 4-7 softmax, a thread has a row, the two groups
+// take a CTA's tiles in turn and hand the running maximum from one to the other;
+// 8-11 the output sum (a thread has a row), 12 K loads and the walk over the
+// items, 13 V loads, 14 the P V products, 15 the query rows and the Q K products
+// (one issuer for both, waiting for each in turn, took 163 us where two took 152).
+//   S(k) = Q K(k)^T, two buffers in TMEM.  The softmax cuts P(k) into three bf16
+//   terms of 8 bits each, exactly, so that the fp32 result has all 24 of the
+//   weights: for each 16 keys two terms where their scores were, one beside.
+//   T = P(k) V(k), the small terms first, goes to a buffer of its own, and the
+//   output sum takes it as o = o alpha + T in fp32 registers: the tensor core's
+//   own accumulation over many tiles truncates, and O never needs a rescale in
+//   TMEM.
+// The softmax loops are rolled, 16 keys of weights to a turn.  Unrolled over a
+// tile their code outgrew the instruction cache next to the other warps' and was
+// fetched again for every tile: 152 requests of 1K keys, 128 rows, took 267 us,
+// with 32 keys to a turn 167, with 16 166 (20 rows 218, 151, 142).  What bounds it
+// now is a tile's chain: a group's pass over its scores, P V, then the next Q K
+// into the same columns (2.0 us a tile of 128 keys, its loads 1.5).
 // Rows of V outside the item's keys may hold anything (NaN times a zero weight
 // is NaN): in tiles that such rows are part of, the softmax warps zero them in
 // shared memory before P(k) is handed over.
@@ -366,8 +372,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         ok = wait(C::B_S + gi, static_cast<uint32_t>(k >> 1), 0x9a);
         if (!ok) break;
         tc_fence_after();
-        // Both passes are rolled: unrolled, a tile's code was fetched anew
-        // tile after tile and the warps waited for it most of the time.
         float mine = -INFINITY;
 #pragma unroll 1
         for (int c0 = 0; c0 < BT; c0 += 32) {
