@@ -12,10 +12,9 @@
 // of a grid of two per SM takes an equal run of them, whatever the lengths are:
 // the lengths stay on the device.  (Without that unit the CTA with the short
 // requests ended last: 16 requests of up to 2K keys, 18.3 against 14.4 us.)  A
-// CTA finds its run by a prefix sum over the requests.
-// An item that falls into one CTA is finished
-// there; one cut by a border between CTAs leaves a partial state (m, l, O~) on
-// each side, and a second launch joins them in CTA order.
+// CTA finds its run by a prefix sum over the requests.  An item that falls into
+// one CTA is finished there; one cut by a border between CTAs leaves a partial
+// state (m, l, O~) on each side, and a second launch joins them in CTA order.
 //
 // Two warps feed a ring of stages with TMA, one K, one V (a page, or 64 rows
 // of a larger one, is a box of one KV head; lane p looks up and requests page
