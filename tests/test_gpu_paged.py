@@ -357,6 +357,54 @@ def test_decode_captured_and_replayed_with_longer_histories():
     ra.ra_device_status()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 200])
+def test_decode_many_rows_over_items_of_every_length(d, window):
+    """More rows than a 16-row tile holds, items of 0 to 5 key tiles whole and
+    cut between CTAs, idle requests among them: the two softmax groups meet in
+    every order."""
+    rng = np.random.default_rng(d + window)
+    lengths = [int(x) for x in rng.choice([0, 1, 60, 128, 129, 250, 256, 300, 520, 640], 170)]
+    rows = [int(x) for x in rng.choice([0, 9, 12, 40], 170, p=[0.1, 0.4, 0.4, 0.1])]
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, rows, 8, 2, d, 32, extra=3)
+    cu = i32(np.concatenate([[0], np.cumsum(rows)]))
+    out, lse = torch.full(q.shape, 9.0, device=DEV), torch.full(q.shape[:2], 9.0, device=DEV)
+    ra.ra_paged_decode(q, kc, vc, table, lens, cu_q=cu, window=window, out=out, lse=lse)
+    ra.ra_device_status()
+    check_decode(out, lse, q, ks, vs, rows, window)
+    assert (out[-3:] == 9.0).all() and (lse[-3:] == 9.0).all()
+    for _ in range(5):
+        o2, l2 = ra.ra_paged_decode(q, kc, vc, table, lens, cu_q=cu, window=window)
+        assert torch.equal(o2[:-3], out[:-3]) and torch.equal(l2[:-3], lse[:-3])
+
+
+def test_decode_of_an_empty_cache():
+    q = torch.randn(3, 8, 128, device=DEV).bfloat16()
+    kc = torch.empty(0, 16, 2, 128, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(3, 2, dtype=torch.int32, device=DEV)
+    out, lse = ra.ra_paged_decode(q, kc, torch.empty_like(kc), table, i32([0, 0, 0]))
+    ra.ra_device_status()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_decode_two_eager_calls_at_once():
+    """Two streams, calls in turn, no synchronisation between them."""
+    cases = [make_decode([3000, 40, 900], [1] * 3, 32, 8, 128, 16, seed=1),
+             make_decode([2000, 700], [16] * 2, 8, 2, 128, 16, seed=2)]
+    want = [ra.ra_paged_decode(*c[:5]) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(20):
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(ra.ra_paged_decode(*c[:5]))
+    torch.cuda.synchronize()
+    ra.ra_device_status()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
 def test_decode_equals_the_contiguous_decode():
     """One request's pages against ra_decode_forward on the same history."""
     q, kc, vc, table, lens, ks, vs = make_decode([5000], [3], 32, 8, 128, 64)
