@@ -268,10 +268,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (it > 0) ok = wait(C::B_QF, static_cast<uint32_t>(it - 1), 0x94);
         if (!ok) break;
         // Chunk c of row r at c ^ (r % 8) inside its 64 columns, as a TMA load
-        // with 128-byte swizzle would put it; rows past the item's are zero.
+        // with 128-byte swizzle would put it.  Of 32 rows those past the item's
+        // are zero; where all are, they keep what they hold (a row's scores and
+        // output come from that row alone).
         constexpr int CPR = D / 8;  // chunks of a row
 #pragma unroll
-        for (int y = 0; y < RT / 32; ++y)
+        for (int y = 0; y < RT / 32; ++y) {
+          if (32 * y >= x.rows) break;
 #pragma unroll 4
           for (int z = 0; z < CPR; ++z) {
             const int r = 32 * y + (z * 32 + lane) / CPR, c = (z * 32 + lane) % CPR;
@@ -279,6 +282,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             copy16(sb + C::OFF_Q + (c >> 3) * CHB + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                    static_cast<const __nv_bfloat16*>(a.q) + at, r < x.rows ? 16u : 0u);
           }
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
