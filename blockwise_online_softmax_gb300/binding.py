@@ -538,9 +538,10 @@ def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *,
     for slots): block_table's rows are extended in place, and the call
     returns (slots int64 [tokens], positions [tokens], cu_tokens [n_req + 1],
     lengths_out [n_req], free_count_out [1], status [3]).  lengths_out and
-    free_count_out may be lengths and free_count themselves.  A nonzero
-    status (pages missing, rows too short, tokens beyond `tokens`) means
-    that the step changed nothing."""
+    free_count_out may be lengths and free_count themselves; outputs that are
+    not passed in share one allocation.  A nonzero status (pages missing,
+    rows too short, tokens beyond `tokens`) means that the step changed
+    nothing."""
     return (_serve or _fast()).paged_extend(
         lengths, new_tokens, block_table, free_pages, free_count, page_size, tokens, lengths_out,
         free_count_out, slots, positions, cu_tokens, status, stream)
