@@ -331,12 +331,15 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
 }
 
 // Append: the same with k and v written to their pages.  Its calls are short,
-// so a token's first loads go out before its angles are computed, its slot and
-// position come with the token before, and k and v share a batch of loads (17K
-// tokens of 12/4 heads, d = 64, without norm: 20.0 -> 15.7 us; in the forward
-// the registers that this takes cost long calls 7%).
+// so a token's first loads, of q, k and v, go out before its angles are
+// computed, its slot and position come with the token before, and k and v share
+// a batch of loads.  17K tokens of 12/4 heads, d = 64, without norm: 20.0 us as
+// the forward does it, 15.7 with q's loads and the slots early (80 registers),
+// 13.8 with the first group of k and v early too, at two CTAs per SM (in three
+// that spills: 16.9).
+constexpr int kAppendCtas = 2;  // per SM
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(const RopeArgs a) {
   let_next_start();
   wait_for_previous();
   using T = __nv_bfloat16;
@@ -372,6 +375,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeA
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) fetch(raw[j], qsrc, g0 + j, q1, a.heads);
     }
+    const T* const ksrc = static_cast<const T*>(a.k) + t * a.k_str;
+    const T* const vsrc = static_cast<const T*>(a.v) + t * a.v_str;
+    Vec<T> k_raw, v_raw;  // the first group's
+    if (real && k0 < k1) {
+      fetch(k_raw, ksrc, k0, k1, a.kv_heads);
+      fetch(v_raw, vsrc, k0, k1, a.kv_heads);
+    }
     long long pos2 = 0, slot2 = 0;
     if (it + nwarps < items) {
       const long long t2 = token(it + nwarps);
@@ -398,13 +408,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeA
       }
       if (k0 < k1) {
         fold(a, rot, a.kw, col, cw, sw);
-        const T* const ksrc = static_cast<const T*>(a.k) + t * a.k_str;
-        const T* const vsrc = static_cast<const T*>(a.v) + t * a.v_str;
         const long long page = slot >> a.page_shift;
         const long long in = (slot & ((1LL << a.page_shift) - 1)) * a.kv_heads * D + off;
         T* const kdst = static_cast<T*>(a.kc) + page * a.kc_page + in;
         T* const vdst = static_cast<T*>(a.vc) + page * a.vc_page + in;
-        for (int g = k0; g < k1; g += N) {
+        if (k0 * RPI + sub < a.kv_heads) v_raw.put(vdst + k0 * RPI * D);
+        turn(rot, k_raw, a.kw != nullptr, a.eps, cw, sw, k0 * RPI + sub < a.kv_heads, kdst + k0 * RPI * D);
+        for (int g = k0 + 1; g < k1; g += N) {
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             fetch(raw[j], ksrc, g + j, k1, a.kv_heads);
@@ -589,7 +599,7 @@ cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_
 cudaError_t launch_rope_append(const RopeArgs& args, int d, cudaStream_t st) {
   RopeArgs a = args;
   if (a.T == 0) return cudaSuccess;
-  const unsigned grid = share(a, d, 3);
+  const unsigned grid = share(a, d, kAppendCtas);
   auto* kernel = d == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
                          : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
   return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
