@@ -189,7 +189,7 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Forward.  A warp takes a token, or one of a.parts shares of its rows; LPR
+// Forward.  A warp takes a token, or a share of its rows (see share()); LPR
 // lanes hold a row, so a group is 32 / LPR rows, of q or k alone, and the loads
 // of kBatch groups are in flight together.  A row costs two products and a sum
 // per column and one exchange of its packed columns with the partner lane.
@@ -210,15 +210,17 @@ __global__ void __launch_bounds__(kWarps * 32, kFwdCtas<T>) rope_forward_kernel(
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
   const int groups = gq + gk;
   const int per = (groups + a.parts - 1) / a.parts;
-  const long long items = a.T * a.parts;
+  const long long items = a.whole + (a.T - a.whole) * a.parts;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
   Rot<D, INTER> rot;
   rot.place(a, lane);
   for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
        it += nwarps) {
-    const long long t = a.parts == 1 ? it : it / a.parts;
-    const int g0 = a.parts == 1 ? 0 : static_cast<int>(it - t * a.parts) * per;
-    const int g1 = g0 + per < groups ? g0 + per : groups;
+    const bool cut = it >= a.whole;
+    // (64-bit divisions: with 32-bit ones the compiler's schedule costs long calls 2.5%.)
+    const long long t = cut ? a.whole + (it - a.whole) / a.parts : it;
+    const int g0 = cut ? static_cast<int>(it - a.whole - (t - a.whole) * a.parts) * per : 0;
+    const int g1 = cut && g0 + per < groups ? g0 + per : groups;
     // A last share may be empty.  (The test also keeps the compiler from moving
     // row loads above the angles, which costs 7%.)
     if (g0 < groups) rot.angles(a, row_position(a, t));
@@ -336,7 +338,8 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
 // a batch of loads.  17K tokens of 12/4 heads, d = 64, without norm: 20.0 us as
 // the forward does it, 15.7 with q's loads and the slots early (80 registers),
 // 13.8 with the first group of k and v early too, at two CTAs per SM (in three
-// that spills: 16.9).
+// that spills: 16.9).  The forward done this way takes 0.5 us less of a call of
+// 300 tokens and 1.2 times as long over 60K of 32/8 heads, d = 128.
 constexpr int kAppendCtas = 2;  // per SM
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(const RopeArgs a) {
@@ -348,12 +351,14 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
   const int groups = gq + gk;  // v goes with k
   const int per = (groups + a.parts - 1) / a.parts;
-  const long long items = a.T * a.parts;
+  const long long items = a.whole + (a.T - a.whole) * a.parts;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
   const int off = sub * D + col;
   Rot<D, INTER> rot;
   rot.place(a, lane);
-  auto token = [&](long long it) { return a.parts == 1 ? it : it / a.parts; };
+  auto token = [&](long long it) {
+    return it < a.whole ? it : a.whole + static_cast<unsigned>(it - a.whole) / static_cast<unsigned>(a.parts);
+  };
   // Group g of n rows from src, if it is below gb.
   auto fetch = [&](Vec<T>& raw, const T* src, int g, int gb, int n) {
     raw = Vec<T>();
@@ -364,8 +369,9 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
   if (it >= items) return;
   long long t = token(it), pos = a.positions[t], slot = a.slots[t];
   for (;;) {
-    const int g0 = a.parts == 1 ? 0 : static_cast<int>(it - t * a.parts) * per;
-    const int g1 = g0 + per < groups ? g0 + per : groups;
+    const bool cut = it >= a.whole;
+    const int g0 = cut ? (static_cast<int>(it - a.whole) - static_cast<int>(t - a.whole) * a.parts) * per : 0;
+    const int g1 = cut && g0 + per < groups ? g0 + per : groups;
     const int q1 = g1 < gq ? g1 : gq;  // q groups [g0, q1), then k and v groups [k0, k1)
     const int k0 = g0 > gq ? g0 - gq : 0, k1 = g1 - gq;
     const bool real = slot >= 0 && slot < a.n_slots;  // else padding: nothing is written
@@ -557,15 +563,23 @@ __global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const Rop
   if (dst) dst[i % d] = x;
 }
 
-// Few tokens: several warps share a token's rows, down to one batch of loads
-// each, until there are some 16 warps per SM.  Sets a.parts; the grid is one
-// wave of `ctas` per SM at most.
+// Tokens are taken whole, one warp each, in turns of all warps of the grid; the
+// rest of them, or all when there are few, by shares of their rows, kBatch
+// groups each or more, so that the last turn is not a few warps' long one:
+// 8192 tokens of 32/8 heads, d = 128, 35.9 -> 32.0 us, 4096 19.2 -> 15.6.  A
+// share computes the token's angles again, so the rest is cut into no more than
+// one turn (6000 tokens: 26.0, with more 26.8); with fewer tokens than warps,
+// into some 16 warps per SM (2000: 10.3; in one turn at most 11.6).
 unsigned share(RopeArgs& a, int d, int ctas) {
   const int rpi = 256 / d, groups = (a.heads + rpi - 1) / rpi + (a.kv_heads + rpi - 1) / rpi;
-  const long long want = (16LL * sm_count() + a.T - 1) / a.T, most_parts = (groups + kBatch - 1) / kBatch;
+  const long long warps = static_cast<long long>(ctas) * kWarps * sm_count();
+  a.whole = a.T / warps * warps;
+  const long long rest = a.T - a.whole, most_parts = (groups + kBatch - 1) / kBatch;
+  const long long want = rest == 0 ? 1 : (a.whole ? warps / rest : (16LL * sm_count() + rest - 1) / rest);
   a.parts = static_cast<int>(want < most_parts ? want : most_parts);
-  const long long need = (a.T * a.parts + kWarps - 1) / kWarps, most = static_cast<long long>(ctas) * sm_count();
-  return static_cast<unsigned>(need < most ? need : most);
+  if (a.parts == 1) a.whole = a.T;
+  const long long items = a.whole + (a.T - a.whole) * a.parts, need = (items + kWarps - 1) / kWarps;
+  return static_cast<unsigned>(need < warps / kWarps ? need : warps / kWarps);
 }
 
 template <typename T>

@@ -89,7 +89,10 @@ struct RopeArgs {
   float* dw;             // backward: partial weight gradients [rope_grad_ctas][2][d]
   float* dqw;            // [d] or null
   float* dkw;
-  int parts;             // warps that share one token's rows (set by the launcher)
+  // Set by the launcher: a warp takes a token as a whole, from token `whole` on
+  // one of `parts` shares of its rows.
+  long long whole;
+  int parts;
 };
 cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_rope_append(const RopeArgs& a, int d, cudaStream_t st);

@@ -163,7 +163,7 @@ def test_extend_then_release_returns_every_page():
 @pytest.mark.parametrize("T, H, Hkv, d, ps, rot, inter, norm", [
     (1, 1, 1, 64, 8, 64, False, True), (5, 32, 8, 128, 16, 128, False, True),
     (300, 12, 4, 64, 64, 32, True, False), (77, 8, 1, 128, 256, 96, True, True),
-    (40, 3, 3, 128, 32, 0, False, True),
+    (40, 3, 3, 128, 32, 0, False, True), (2700, 32, 8, 128, 16, 128, False, True),
 ])
 @pytest.mark.parametrize("together", [False, True])
 def test_append(T, H, Hkv, d, ps, rot, inter, norm, together):

@@ -62,6 +62,9 @@ CASES = [
     (64, 2, 2, 128, 0, False, "bf16", True, True, "f32", 1.0),
     (65, 64, 8, 64, 48, False, "f32", True, True, "bf16", 1.0),
     (2000, 4, 2, 128, 128, True, "f32", True, True, "f32", 1.0),
+    # more tokens than warps: whole ones first, then shares of the rest's rows
+    (4099, 32, 8, 128, 128, False, "bf16", True, True, "f32", 1.0),
+    (2701, 24, 8, 64, 32, True, "f32", True, True, "f32", 1.1),
 ]
 
 
