@@ -446,11 +446,14 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
 
 // Backward.  Groups as in the forward; the weight gradients are summed in
 // the lanes, over the CTA's warps in shared memory, and written as one
-// partial sum per CTA, so their order is fixed.
+// partial sum per CTA, so their order is fixed.  CUT: some tokens are taken in
+// shares; without it that arithmetic stays out, whose registers cost a long call
+// 3% (128K tokens of 32/8 heads, d = 128: 863 us, 0.93 of the copy bandwidth;
+// 300 tokens 8.0, taken whole 12.2).
 constexpr int kGradBatch = 3;
 constexpr int kGradCtas = 2;  // per SM
 
-template <typename T, int D, bool INTER>
+template <typename T, int D, bool INTER, bool CUT>
 __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(const RopeArgs a) {
   let_next_start();
   wait_for_previous();
@@ -459,6 +462,8 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = 8 * (lane % LPR), sub = lane / LPR;
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
+  const int groups = gq + gk, per = (groups + a.parts - 1) / a.parts;
+  const long long items = CUT ? a.whole + (a.T - a.whole) * a.parts : a.T;
   const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
   float wq[8], wk[8], dwq[8], dwk[8];
 #pragma unroll
@@ -467,14 +472,18 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
   if (a.kw) load_weight(a.kw, a.w_bf16, col, wk);
   Rot<D, INTER> rot;
   rot.place(a, lane);
-  for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.T; t += nwarps) {
-    rot.angles(a, row_position(a, t));
-    auto rows = [&](int gb, int n, const T* src, const float* grad, T* dst, bool norm,
+  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items; it += nwarps) {
+    const bool cut = CUT && it >= a.whole;
+    const long long t = cut ? a.whole + (it - a.whole) / a.parts : it;
+    const int g0 = cut ? static_cast<int>(it - a.whole - (t - a.whole) * a.parts) * per : 0;
+    const int g1 = cut && g0 + per < groups ? g0 + per : groups;
+    if (!CUT || g0 < groups) rot.angles(a, row_position(a, t));
+    auto rows = [&](int ga, int gb, int n, const T* src, const float* grad, T* dst, bool norm,
                     const float (&w)[8], float (&dw)[8]) {
       src += sub * D + col;
       grad += sub * D + col;
       dst += sub * D + col;
-      for (int g = 0; g < gb; g += kGradBatch) {
+      for (int g = CUT ? ga : 0; g < gb; g += kGradBatch) {
         Vec<T> raw[kGradBatch];
         Vec<float> gr[kGradBatch];
 #pragma unroll
@@ -517,9 +526,9 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
         }
       }
     };
-    rows(gq, a.heads, static_cast<const T*>(a.q) + t * a.q_str, a.dqo + t * a.heads * D,
+    rows(g0, CUT && g1 < gq ? g1 : gq, a.heads, static_cast<const T*>(a.q) + t * a.q_str, a.dqo + t * a.heads * D,
          static_cast<T*>(a.qo) + t * a.qo_str, a.qw != nullptr, wq, dwq);
-    rows(gk, a.kv_heads, static_cast<const T*>(a.k) + t * a.k_str, a.dko + t * a.kv_heads * D,
+    rows(g0 > gq ? g0 - gq : 0, CUT ? g1 - gq : gk, a.kv_heads, static_cast<const T*>(a.k) + t * a.k_str, a.dko + t * a.kv_heads * D,
          static_cast<T*>(a.ko) + t * a.ko_str, a.kw != nullptr, wk, dwk);
   }
   if (!a.dw) return;
@@ -564,19 +573,24 @@ __global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const Rop
 }
 
 // Tokens are taken whole, one warp each, in turns of all warps of the grid; the
-// rest of them, or all when there are few, by shares of their rows, kBatch
-// groups each or more, so that the last turn is not a few warps' long one:
-// 8192 tokens of 32/8 heads, d = 128, 35.9 -> 32.0 us, 4096 19.2 -> 15.6.  A
-// share computes the token's angles again, so the rest is cut into no more than
-// one turn (6000 tokens: 26.0, with more 26.8); with fewer tokens than warps,
-// into some 16 warps per SM (2000: 10.3; in one turn at most 11.6).
-unsigned share(RopeArgs& a, int d, int ctas) {
+// rest of them, or all when there are few, by shares of their rows, a batch of
+// loads each or more, so that the last turn is not a few warps' long one.  32/8
+// heads, d = 128: forward of 8192 tokens 35.9 -> 32.0 us, 4096 19.2 -> 15.6;
+// gradient of 300 12.6 -> 7.8, 3000 35.3 -> 28.6; append of 1000 7.7 -> 6.1.  A
+// share computes the token's angles again, so the rest fills no more than one
+// turn (forward of 6000 tokens: 26.0, with more 26.8), but for few tokens in the
+// forward's three CTAs per SM, which come to some 16 warps per SM (2000 tokens:
+// 10.3; in one turn at most 11.6).  After more than eight turns the last is too
+// small a part of the call to matter.
+unsigned share(RopeArgs& a, int d, int ctas, int batch) {
   const int rpi = 256 / d, groups = (a.heads + rpi - 1) / rpi + (a.kv_heads + rpi - 1) / rpi;
   const long long warps = static_cast<long long>(ctas) * kWarps * sm_count();
   a.whole = a.T / warps * warps;
-  const long long rest = a.T - a.whole, most_parts = (groups + kBatch - 1) / kBatch;
-  const long long want = rest == 0 ? 1 : (a.whole ? warps / rest : (16LL * sm_count() + rest - 1) / rest);
-  a.parts = static_cast<int>(want < most_parts ? want : most_parts);
+  const long long rest = a.T - a.whole, most = groups / batch;
+  long long want = rest && a.whole <= 8 * warps ? warps / rest : 1;
+  if (rest && !a.whole && ctas > 2) want = (16LL * sm_count() + rest - 1) / rest;
+  if (want > most) want = most;
+  a.parts = want < 1 ? 1 : static_cast<int>(want);
   if (a.parts == 1) a.whole = a.T;
   const long long items = a.whole + (a.T - a.whole) * a.parts, need = (items + kWarps - 1) / kWarps;
   return static_cast<unsigned>(need < warps / kWarps ? need : warps / kWarps);
@@ -585,26 +599,22 @@ unsigned share(RopeArgs& a, int d, int ctas) {
 template <typename T>
 cudaError_t forward_t(RopeArgs a, int d, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  const unsigned grid = share(a, d, kFwdCtas<T>);
+  const unsigned grid = share(a, d, kFwdCtas<T>, kBatch);
   auto* kernel = d == 128 ? (a.interleaved ? rope_forward_kernel<T, 128, true> : rope_forward_kernel<T, 128, false>)
                          : (a.interleaved ? rope_forward_kernel<T, 64, true> : rope_forward_kernel<T, 64, false>);
   return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
-template <typename T>
-cudaError_t backward_t(const RopeArgs& a, int d, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(rope_grad_ctas(a));
-  auto* kernel = d == 128 ? (a.interleaved ? rope_backward_kernel<T, 128, true> : rope_backward_kernel<T, 128, false>)
-                         : (a.interleaved ? rope_backward_kernel<T, 64, true> : rope_backward_kernel<T, 64, false>);
-  return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
+template <typename T, bool CUT>
+cudaError_t backward_t(const RopeArgs& a, int ctas, int d, cudaStream_t st) {
+  auto* kernel = d == 128 ? (a.interleaved ? rope_backward_kernel<T, 128, true, CUT> : rope_backward_kernel<T, 128, false, CUT>)
+                         : (a.interleaved ? rope_backward_kernel<T, 64, true, CUT> : rope_backward_kernel<T, 64, false, CUT>);
+  return launch_early(kernel, dim3(static_cast<unsigned>(ctas)), kWarps * 32, 0, st, a);
 }
 
 }  // namespace
 
-int rope_grad_ctas(const RopeArgs& a) {
-  const long long ctas = (a.T + kWarps - 1) / kWarps, most = static_cast<long long>(kGradCtas) * sm_count();
-  return static_cast<int>(ctas < 1 ? 1 : (ctas < most ? ctas : most));
-}
+int rope_grad_ctas(RopeArgs& a, int d) { return static_cast<int>(share(a, d, kGradCtas, kGradBatch)); }
 
 cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st) {
   return bf16 ? forward_t<__nv_bfloat16>(a, d, st) : forward_t<float>(a, d, st);
@@ -613,14 +623,15 @@ cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_
 cudaError_t launch_rope_append(const RopeArgs& args, int d, cudaStream_t st) {
   RopeArgs a = args;
   if (a.T == 0) return cudaSuccess;
-  const unsigned grid = share(a, d, kAppendCtas);
+  const unsigned grid = share(a, d, kAppendCtas, kBatch);
   auto* kernel = d == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
                          : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
   return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 
-cudaError_t launch_rope_backward(const RopeArgs& a, int d, bool bf16, cudaStream_t st) {
-  return bf16 ? backward_t<__nv_bfloat16>(a, d, st) : backward_t<float>(a, d, st);
+cudaError_t launch_rope_backward(const RopeArgs& a, int ctas, int d, bool bf16, cudaStream_t st) {
+  if (a.parts == 1) return bf16 ? backward_t<__nv_bfloat16, false>(a, ctas, d, st) : backward_t<float, false>(a, ctas, d, st);
+  return bf16 ? backward_t<__nv_bfloat16, true>(a, ctas, d, st) : backward_t<float, true>(a, ctas, d, st);
 }
 
 cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st) {

@@ -311,7 +311,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
   a.dko = dk_out;
   a.dqw = dq_weight;
   a.dkw = dk_weight;
-  const int ctas = ra::rope_grad_ctas(a);
+  const int ctas = ra::rope_grad_ctas(a, d);
   if (dq_weight || dk_weight) {
     e = scratch_alloc(reinterpret_cast<void**>(&a.dw), static_cast<size_t>(ctas) * 2 * d * sizeof(float), st);
     if (e != cudaSuccess) {
@@ -321,7 +321,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
   }
   {
     TraceScope ts(RA_KERNEL_QK_NORM_ROPE_BWD, st);
-    e = ra::launch_rope_backward(a, d, dtype == RA_BF16, st);
+    e = ra::launch_rope_backward(a, ctas, d, dtype == RA_BF16, st);
     ts.done(e == cudaSuccess);
   }
   if (a.dw) {

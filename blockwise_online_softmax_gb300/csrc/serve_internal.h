@@ -97,8 +97,9 @@ struct RopeArgs {
 cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
 cudaError_t launch_rope_append(const RopeArgs& a, int d, cudaStream_t st);
 // CTAs of the backward launch, i.e. partial weight gradients it writes.
-int rope_grad_ctas(const RopeArgs& a);
-cudaError_t launch_rope_backward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
+// Sets how they share the tokens.
+int rope_grad_ctas(RopeArgs& a, int d);
+cudaError_t launch_rope_backward(const RopeArgs& a, int ctas, int d, bool bf16, cudaStream_t st);
 // dqw, dkw = the sums of the n partial weight gradients.
 cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st);
 
