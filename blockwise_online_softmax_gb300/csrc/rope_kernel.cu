@@ -193,7 +193,7 @@ __device__ __forceinline__ float row_sum(float v) {
 // lanes hold a row, so a group is 32 / LPR rows, of q or k alone, and the loads
 // of kBatch groups are in flight together.  A row costs two products and a sum
 // per column and one exchange of its packed columns with the partner lane.
-// The 128K-token GQA q and k (32/8 heads, d = 128) take 444 us, 0.90 of the copy
+// The 128K-token GQA q and k (32/8 heads, d = 128) take 442 us, 0.91 of the copy
 // bandwidth; with the arithmetic one column at a time 469, with 2 or 4 CTAs per
 // SM or other batches 450 to 585.  (The row is written out here: through turn()
 // below the compiler's schedule costs 6%.)
