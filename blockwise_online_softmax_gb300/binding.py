@@ -573,8 +573,8 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, win
     """Attention of each request's newest tokens q [T, heads, d] (bf16) over
     its pages.  T / n_req rows per request, or rows [cu_q[i], cu_q[i + 1]) of
     request i (int32 [n_req + 1]); lengths (int32 [n_req]) include them.
-    Returns (out [T, heads, d], lse [T, heads]), fp32; pass a bf16 `out` for
-    that type."""
+    Returns (out [T, heads, d], lse [T, heads]), fp32, in one allocation where
+    not passed in; pass a bf16 `out` for that type."""
     return (_serve or _fast()).paged_decode(
         q, k_cache, v_cache, block_table, lengths, cu_q, window, out, lse, stream)
 

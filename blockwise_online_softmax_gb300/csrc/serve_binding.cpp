@@ -238,14 +238,17 @@ struct Out {
   }
 };
 
-// The 1-D outputs that the caller did not give, as views of one allocation: an
+// The small outputs that the caller did not give, as views of one allocation: an
 // allocation each took 0.7 us of host time, most of a small step's call.
 class Block {
  public:
-  void add(Out& o, int64_t n, ScalarType type) {
+  void add(Out& o, at::IntArrayRef sizes, ScalarType type) {
     if (o.t) return;
-    parts_[count_++] = {&o, n, bytes_, type};
-    bytes_ += (n * static_cast<int64_t>(c10::elementSize(type)) + 255) / 256 * 256;
+    Part& p = parts_[count_++];
+    p = {&o, {}, sizes.size(), bytes_, type};
+    int64_t n = static_cast<int64_t>(c10::elementSize(type));
+    for (size_t i = 0; i < sizes.size(); ++i) n *= p.sizes[i] = sizes[i];
+    bytes_ += (n + 255) / 256 * 256;
   }
   void make(const Tensor& like) {
     if (count_ == 0) return;
@@ -255,7 +258,7 @@ class Block {
       Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
                                                           c10::scalarTypeToTypeMeta(p.type));
       t.unsafeGetTensorImpl()->set_storage_offset(p.at / static_cast<int64_t>(c10::elementSize(p.type)));
-      t.unsafeGetTensorImpl()->set_sizes_contiguous({p.n});
+      t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(p.sizes, p.dim));
       p.o->made = std::move(t);
       p.o->t = &p.o->made;
     }
@@ -264,7 +267,9 @@ class Block {
  private:
   struct Part {
     Out* o;
-    int64_t n, at;
+    int64_t sizes[3];
+    size_t dim;
+    int64_t at;
     ScalarType type;
   };
   Part parts_[6];
@@ -419,12 +424,12 @@ PyObject* extend(PyObject* const* a) {
   const int* pc = ints(fc, "free_count", 1, dev);
   const int pool = to_int(fp.numel(), "free_pages");
   Block made;
-  made.add(sl, tokens, ScalarType::Long);
-  made.add(po, tokens, i32);
-  made.add(cu, n + 1, i32);
-  made.add(lo, n, i32);
-  made.add(co, 1, i32);
-  made.add(stt, 3, i32);
+  made.add(sl, {tokens}, ScalarType::Long);
+  made.add(po, {tokens}, i32);
+  made.add(cu, {n + 1}, i32);
+  made.add(lo, {n}, i32);
+  made.add(co, {1}, i32);
+  made.add(stt, {3}, i32);
   made.make(len);
   int* plo = ints(*lo.t, "lengths_out", n, dev);
   int* pco = ints(*co.t, "free_count_out", 1, dev);
@@ -454,8 +459,8 @@ PyObject* release(PyObject* const* a) {
   const int* pc = ints(fc, "free_count", 1, dev);
   const int pool = to_int(fp.numel(), "free_pages");
   Block made;
-  made.add(lo, n, ScalarType::Int);
-  made.add(co, 1, ScalarType::Int);
+  made.add(lo, {n}, ScalarType::Int);
+  made.add(co, {1}, ScalarType::Int);
   made.make(len);
   int* plo = ints(*lo.t, "lengths_out", n, dev);
   int* pco = ints(*co.t, "free_count_out", 1, dev);
@@ -525,9 +530,13 @@ PyObject* decode(PyObject* const* a) {
   const Table tb = block_table(tab, n, dev);
   const int* pc = cu ? ints(*cu, "cu_q", n + 1, dev) : nullptr;
   const int* pl = ints(len, "lengths", n, dev);
-  const Tensor& to = out.get(q.sizes(), ScalarType::Float, q);
+  Block made;
+  made.add(out, q.sizes(), ScalarType::Float);
+  made.add(lse, {T, heads}, ScalarType::Float);
+  made.make(q);
+  const Tensor& to = *out.t;
   void* po = dense(to, "out", dev, to.scalar_type());
-  auto* ps = static_cast<float*>(dense(lse.get({T, heads}, ScalarType::Float, q), "lse", dev, ScalarType::Float));
+  auto* ps = static_cast<float*>(dense(*lse.t, "lse", dev, ScalarType::Float));
   const int n_q = cu || !n ? 0 : to_int(T / n, "rows per request"), code = type_code(to.scalar_type());
   call(dev, a[9], [&](void* st) {
     return ra_paged_decode(pq, ck.p, cv.p, po, ps, T, tb.n_req, n_q, pc, tb.p, tb.width, pl, ck.pages, ck.page_size,
