@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
 #pragma unroll
         for (int j = 0; j < kGradBatch; ++j) {
           if (g + j >= gb) break;
+          const bool valid = (g + j) * RPI + sub < n;
           float x[8], gy[8], p[8];
           raw[j].get(x);
           gr[j].get(gy);
@@ -514,7 +515,8 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
             }
             ss = row_sum<LPR>(ss);
             ux = row_sum<LPR>(ux);
-            const float r = rsqrtf(ss * (1.f / D) + a.eps);
+            // (0 for the rows of nobody: without eps theirs would be infinite.)
+            const float r = valid ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
             const float m = r * r * ux * (1.f / D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
               gy[e] = r * fmaf(-x[e], m, u[e]);
             }
           }
-          if ((g + j) * RPI + sub < n) Vec<T>::store(dst + (g + j) * RPI * D, gy);
+          if (valid) Vec<T>::store(dst + (g + j) * RPI * D, gy);
         }
       }
     };
