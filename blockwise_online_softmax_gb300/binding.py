@@ -434,6 +434,11 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
 # of a serving step.  Their arguments are marshalled by the extension _serve
 # (csrc/serve_binding.cpp): the same checks and the same C ABI calls as the
 # functions above, at a few microseconds instead of tens.
+#
+# stream= takes a torch.cuda.Stream or a cudaStream_t as an integer.  Outputs
+# that are not passed in belong to that stream's memory and are recorded as
+# used by the current one; ordering the streams stays with the caller, and so
+# does keeping the inputs, and outputs that are passed in, until it is done.
 
 _serve = None
 

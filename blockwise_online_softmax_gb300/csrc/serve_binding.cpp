@@ -10,9 +10,11 @@
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
+#include <optional>
 #include <string>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -215,15 +217,53 @@ void same_pages(const Cache& k, const Cache& v) {
 }
 
 // ------------------------------------------------------------------ outputs
+// Device and stream of a call.  Outputs that the caller left out are made with
+// that stream current: what work on another stream still holds is not handed
+// out, and a result that is dropped goes back in the stream's order.  The
+// current stream, which may read them too, is recorded as their user.
+struct Place {
+  int dev;
+  void* stream;
+  c10::cuda::CUDAStream current;
+  std::optional<c10::cuda::CUDAStream> other;  // the stream, if it is not the current one
+
+  Place(int dev_, PyObject* o)
+      : dev(dev_), stream(nullptr), current(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev_))) {
+    if (o == Py_None) {
+      stream = current.stream();
+      return;
+    }
+    PyObject* h = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
+    if (!h) throw PythonError();
+    stream = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (!stream && PyErr_Occurred()) throw PythonError();
+    const auto st = static_cast<cudaStream_t>(stream);
+    if (st == current.stream()) return;
+    const auto index = static_cast<c10::DeviceIndex>(dev);
+    // (The legacy default stream goes by two names, of which torch knows one.)
+    other = st && st != cudaStreamLegacy ? c10::cuda::getStreamFromExternal(st, index)
+                                         : c10::cuda::getDefaultCUDAStream(index);
+  }
+  Tensor make(at::IntArrayRef sizes, ScalarType type) const {
+    const c10::Device d(c10::DeviceType::CUDA, static_cast<c10::DeviceIndex>(dev));
+    if (!other) return at::detail::empty_cuda(sizes, type, d, std::nullopt);
+    c10::cuda::CUDAStreamGuard guard(*other);
+    Tensor t = at::detail::empty_cuda(sizes, type, d, std::nullopt);
+    if (t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
+    return t;
+  }
+};
+
 // An output the caller gave, or a new one.
 struct Out {
   Tensor made;
   const Tensor* t;
   PyObject* given;
   Out(PyObject* o, const char* name) : t(maybe(o, name)), given(o == Py_None ? nullptr : o) {}
-  const Tensor& get(at::IntArrayRef sizes, ScalarType type, const Tensor& like) {
+  const Tensor& get(at::IntArrayRef sizes, ScalarType type, const Place& at) {
     if (!t) {
-      made = at::detail::empty_cuda(sizes, type, like.device(), std::nullopt);
+      made = at.make(sizes, type);
       t = &made;
     }
     return *t;
@@ -250,9 +290,9 @@ class Block {
     for (size_t i = 0; i < sizes.size(); ++i) n *= p.sizes[i] = sizes[i];
     bytes_ += (n + 255) / 256 * 256;
   }
-  void make(const Tensor& like) {
+  void make(const Place& at) {
     if (count_ == 0) return;
-    const Tensor all = at::detail::empty_cuda({bytes_}, ScalarType::Byte, like.device(), std::nullopt);
+    const Tensor all = at.make({bytes_}, ScalarType::Byte);
     for (int i = 0; i < count_; ++i) {
       const Part& p = parts_[i];
       Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
@@ -295,23 +335,12 @@ PyObject* pack(std::initializer_list<Out*> outs) {
 // Runs f(stream) with the tensors' device current and without the GIL; a
 // status other than RA_OK raises.
 template <typename F>
-void call(int dev, PyObject* stream, F f) {
-  void* st = nullptr;
-  if (stream == Py_None) {
-    st = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  } else {
-    PyObject* h = PyObject_HasAttrString(stream, "cuda_stream") ? PyObject_GetAttrString(stream, "cuda_stream")
-                                                                 : PyNumber_Long(stream);
-    if (!h) throw PythonError();
-    st = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!st && PyErr_Occurred()) throw PythonError();
-  }
+void call(const Place& at, F f) {
   c10::cuda::OptionalCUDAGuard guard;
-  if (c10::cuda::current_device() != dev) guard.set_index(static_cast<c10::DeviceIndex>(dev));
+  if (c10::cuda::current_device() != at.dev) guard.set_index(static_cast<c10::DeviceIndex>(at.dev));
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = f(st);
+  rc = f(at.stream);
   Py_END_ALLOW_THREADS;
   if (rc == RA_OK) return;
   PyObject* r = PyObject_CallFunction(g_on_status, "i", rc);
@@ -357,9 +386,10 @@ PyObject* norm_rope(PyObject* const* a) {
   const int* pp = pos ? ints(*pos, "positions", h.T, dev) : nullptr;
   const float eps = real(a[5]), ms = real(a[7]);
   const int inter = truth(a[6]), P = small(a[9], "P"), layout = small(a[10], "layout");
-  void* po = dense(qo.get(q.sizes(), h.type, q), "q_out", dev, h.type);
-  void* pk = dense(ko.get(k.sizes(), h.type, k), "k_out", dev, h.type);
-  call(dev, a[13], [&](void* st) {
+  const Place at(dev, a[13]);
+  void* po = dense(qo.get(q.sizes(), h.type, at), "q_out", dev, h.type);
+  void* pk = dense(ko.get(k.sizes(), h.type, at), "k_out", dev, h.type);
+  call(at, [&](void* st) {
     return ra_qk_norm_rope(rq.p, rk.p, po, pk, h.T, h.d, h.heads, h.kv_heads, rq.stride, rk.stride, pp, layout, P,
                            ph.rot, inter, ph.p, ms, w.q, w.k, w.type, eps, type_code(h.type), st);
   });
@@ -391,11 +421,12 @@ PyObject* norm_rope_backward(PyObject* const* a) {
   const auto f32 = ScalarType::Float;
   const auto* pgq = static_cast<const float*>(dense(gq, "dq_out", dev, f32));
   const auto* pgk = static_cast<const float*>(dense(gk, "dk_out", dev, f32));
-  const Rows oq = rows(dq.get(q.sizes(), h.type, q), "dq", dev, h.type);
-  const Rows ok = rows(dk.get(k.sizes(), h.type, k), "dk", dev, h.type);
-  float* wq = qw ? vec<float>(dqw.get({h.d}, f32, q), "dq_weight", h.d, dev, f32) : nullptr;
-  float* wk = kw ? vec<float>(dkw.get({h.d}, f32, q), "dk_weight", h.d, dev, f32) : nullptr;
-  call(dev, a[17], [&](void* st) {
+  const Place at(dev, a[17]);
+  const Rows oq = rows(dq.get(q.sizes(), h.type, at), "dq", dev, h.type);
+  const Rows ok = rows(dk.get(k.sizes(), h.type, at), "dk", dev, h.type);
+  float* wq = qw ? vec<float>(dqw.get({h.d}, f32, at), "dq_weight", h.d, dev, f32) : nullptr;
+  float* wk = kw ? vec<float>(dkw.get({h.d}, f32, at), "dk_weight", h.d, dev, f32) : nullptr;
+  call(at, [&](void* st) {
     return ra_qk_norm_rope_backward(rq.p, rk.p, pgq, pgk, oq.p, ok.p, wq, wk, h.T, h.d, h.heads, h.kv_heads,
                                     rq.stride, rk.stride, oq.stride, ok.stride, pp, layout, P, ph.rot, inter, ph.p,
                                     ms, w.q, w.k, w.type, eps, type_code(h.type), st);
@@ -430,14 +461,15 @@ PyObject* extend(PyObject* const* a) {
   made.add(lo, {n}, i32);
   made.add(co, {1}, i32);
   made.add(stt, {3}, i32);
-  made.make(len);
+  const Place at(dev, a[13]);
+  made.make(at);
   int* plo = ints(*lo.t, "lengths_out", n, dev);
   int* pco = ints(*co.t, "free_count_out", 1, dev);
   auto* psl = reinterpret_cast<long long*>(vec<int64_t>(*sl.t, "slots", tokens, dev, ScalarType::Long));
   int* ppo = ints(*po.t, "positions", tokens, dev);
   int* pcu = ints(*cu.t, "cu_tokens", n + 1, dev);
   int* pst = ints(*stt.t, "status", 3, dev);
-  call(dev, a[13], [&](void* st) {
+  call(at, [&](void* st) {
     return ra_paged_extend(pl, pn, tb.n_req, tb.p, tb.width, pf, pool, pc, ps, tokens, plo, pco, psl, ppo, pcu, pst,
                            st);
   });
@@ -461,10 +493,11 @@ PyObject* release(PyObject* const* a) {
   Block made;
   made.add(lo, {n}, ScalarType::Int);
   made.add(co, {1}, ScalarType::Int);
-  made.make(len);
+  const Place at(dev, a[8]);
+  made.make(at);
   int* plo = ints(*lo.t, "lengths_out", n, dev);
   int* pco = ints(*co.t, "free_count_out", 1, dev);
-  call(dev, a[8], [&](void* st) {
+  call(at, [&](void* st) {
     return ra_paged_release(pl, pn, tb.n_req, tb.p, tb.width, pf, pool, pc, ps, plo, pco, st);
   });
   return pack({&lo, &co});
@@ -491,8 +524,9 @@ PyObject* append(PyObject* const* a) {
   const int* pp = ints(pos, "positions", h.T, dev);
   const float eps = real(a[10]), ms = real(a[12]);
   const int inter = truth(a[11]);
-  void* po = dense(qo.get(q.sizes(), h.type, q), "q_out", dev, h.type);
-  call(dev, a[14], [&](void* st) {
+  const Place at(dev, a[14]);
+  void* po = dense(qo.get(q.sizes(), h.type, at), "q_out", dev, h.type);
+  call(at, [&](void* st) {
     return ra_paged_append(rq.p, rk.p, rv.p, po, ck.p, cv.p, h.T, h.d, h.heads, h.kv_heads, rq.stride, rk.stride,
                            rv.stride, ck.pages, ck.page_size, ck.stride, cv.stride, psl, pp, ph.rot, inter, ph.p, ms,
                            w.q, w.k, w.type, eps, type_code(h.type), st);
@@ -533,12 +567,13 @@ PyObject* decode(PyObject* const* a) {
   Block made;
   made.add(out, q.sizes(), ScalarType::Float);
   made.add(lse, {T, heads}, ScalarType::Float);
-  made.make(q);
+  const Place at(dev, a[9]);
+  made.make(at);
   const Tensor& to = *out.t;
   void* po = dense(to, "out", dev, to.scalar_type());
   auto* ps = static_cast<float*>(dense(*lse.t, "lse", dev, ScalarType::Float));
   const int n_q = cu || !n ? 0 : to_int(T / n, "rows per request"), code = type_code(to.scalar_type());
-  call(dev, a[9], [&](void* st) {
+  call(at, [&](void* st) {
     return ra_paged_decode(pq, ck.p, cv.p, po, ps, T, tb.n_req, n_q, pc, tb.p, tb.width, pl, ck.pages, ck.page_size,
                            ck.stride, cv.stride, window, d, heads, kv_heads, RA_BF16, code, st);
   });

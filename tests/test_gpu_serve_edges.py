@@ -9,6 +9,7 @@ import torch
 import blockwise_online_softmax_gb300 as ra
 import serve_ref
 from blockwise_online_softmax_gb300 import binding
+from test_gpu_paged import i32
 from test_gpu_rope import np64
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,119 @@ def test_weight_gradient_without_eps(d, H, Hkv):
                                                   np64(dy), eps=0.0)
         assert (np.abs(np64(dx) - rx) <= 128 * U * size + 1e-30).all()
         assert (np.abs(np64(dw) - rw) <= (64 + T * x.shape[1]) * U * wsize).all()
+
+
+# ------------------------------------------------------------------ streams
+
+def side_calls():
+    """Each call as f(stream) -> its outputs (what it updates in place it
+    updates to the same every time), and the bytes of its first allocation."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+
+    def randn(*shape, dtype=torch.bfloat16):
+        return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+    T, H, Hkv, d, ps = 8192, 8, 2, 128, 16
+    q, k, v = randn(T, H, d), randn(T, Hkv, d), randn(T, Hkv, d)
+    ph = ra.rope_phases(ra.rope_freqs(d)[0]).to(DEV)
+    dqo, dko = randn(T, H, d, dtype=torch.float32), randn(T, Hkv, d, dtype=torch.float32)
+    n = 1 << 20
+    lens, news = i32(np.arange(n) % 7), i32(np.arange(n) % 3)
+    tokens = int(news.sum())
+    table = i32(np.arange(n)).view(n, 1)
+    free, count = i32(np.arange(n)), i32([n // 2])
+    kc, vc = randn(T // ps, ps, Hkv, d), randn(T // ps, ps, Hkv, d)
+    slots, pos = torch.arange(T, device=DEV), i32(np.arange(T))
+    ptab, plen = i32(np.arange(T // ps)).view(16, -1), i32(np.full(16, T // 16))
+
+    def up(*sizes):
+        return sum(-(-x // 512) * 512 for x in sizes)
+
+    return {
+        "rope": (lambda s: ra.ra_qk_norm_rope(q, k, ph, stream=s), up(q.numel() * 2)),
+        "rope backward": (lambda s: ra.ra_qk_norm_rope_backward(q, k, ph, dqo, dko, stream=s)[:2],
+                          up(q.numel() * 2)),
+        "extend": (lambda s: ra.ra_paged_extend(lens, news, table, free, count, page_size=16,
+                                                tokens=tokens, stream=s),
+                   up(tokens * 8, tokens * 4, n * 4 + 4, n * 4, 4, 12)),
+        "release": (lambda s: ra.ra_paged_release(lens, news, table, free, count,
+                                                  page_size=16, stream=s), up(n * 4, 4)),
+        "append": (lambda s: (ra.ra_paged_append(q, k, v, ph, kc, vc, slots, pos, stream=s),),
+                   up(q.numel() * 2)),
+        "decode": (lambda s: ra.ra_paged_decode(q, kc, vc, ptab, plen, stream=s),
+                   up(q.numel() * 4, T * H * 4)),
+    }
+
+
+CALLS = ["rope", "rope backward", "extend", "release", "append", "decode"]
+BUSY = 200_000_000  # cycles of a sleeping kernel: about 0.1 s
+
+
+def same(a, b):
+    return len(a) == len(b) and all((x is None and y is None) or torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("form", ["object", "handle"])
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_left_out_belong_to_the_stream_of_the_call(name, form):
+    """stream= other than the current one, outputs left out.  They must not
+    take memory that work on the current stream still uses; a result that is
+    dropped must not be written after its memory went to the current stream;
+    and one that the current stream still reads must not go back early."""
+    f, size = side_calls()[name]
+    side = torch.cuda.Stream()
+    s = side if form == "object" else side.cuda_stream
+    torch.cuda.synchronize()
+    want = [x if x is None else x.clone() for x in f(None)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        f(None)  # the scratch pool has memory for the side stream
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+    # 1. Memory that the current stream has yet to write.
+    block = torch.empty(size, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    block.fill_(171)
+    del block
+    got = f(s)
+    torch.cuda.synchronize()
+    assert same(got, want)
+
+    # 2. A dropped result's memory, taken by the current stream.
+    del got
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    got = f(s)
+    del got
+    block = torch.empty(size, dtype=torch.uint8, device=DEV).fill_(171)
+    torch.cuda.synchronize()
+    assert bool((block == 171).all())
+    del block
+
+    # 3. A dropped result that the current stream has yet to read.
+    torch.cuda.empty_cache()
+    got = f(s)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    keep = [x if x is None else x.clone() for x in got]
+    del got
+    with torch.cuda.stream(side):
+        block = torch.empty(size, dtype=torch.uint8, device=DEV).fill_(171)
+    torch.cuda.synchronize()
+    assert same(keep, want)
+    ra.ra_device_status()
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_handles(handle):
+    """NULL and cudaStreamLegacy, with another stream current."""
+    f, _ = side_calls()["decode"]
+    want = f(None)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = f(handle)
+    torch.cuda.synchronize()
+    assert same(got, want)
