@@ -133,6 +133,30 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+# stream= takes a torch.cuda.Stream or a cudaStream_t as an integer.  Ordering
+# the streams stays with the caller, and so does keeping the inputs, and the
+# outputs that are passed in, until the call's work is done.
+
+
+def _new(shape, device, stream) -> torch.Tensor:
+    """An fp32 output that the caller left out.  Its memory belongs to the
+    stream of the call (work on another stream does not hold it, and dropped
+    it goes back in that stream's order); the current stream, which may read
+    it too, is recorded as its user."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    current, handle = torch.cuda.current_stream(device), _stream(stream)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    # (The legacy default stream goes by two handles, of which torch knows one.)
+    other = (torch.cuda.default_stream(device) if handle in (0, 1)
+             else torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=torch.float32, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -203,9 +227,9 @@ def ra_finalize(m, l, o, out=None, lse=None, stream=None):
     rows, heads, d = o.shape
     _state_shapes(m, l, o, rows, heads, d)
     if out is None:
-        out = torch.empty_like(o)
+        out = _new(o.shape, o.device, stream)
     if lse is None:
-        lse = torch.empty_like(m)
+        lse = _new(m.shape, m.device, stream)
     _state_shapes(lse, lse, out, rows, heads, d)
     _check(lib().ra_finalize(_dev(m, "m", torch.float32), _dev(l, "l", torch.float32),
                              _dev(o, "o", torch.float32), _dev(out, "out", torch.float32),
@@ -230,9 +254,9 @@ def ra_ring_forward(q, k, v, *, P: int, causal: bool, out=None, lse=None, stream
     if k.shape[0] != N:
         raise ValueError("q, k and v must cover the same N tokens")
     if out is None:
-        out = torch.empty((N, heads, d), dtype=torch.float32, device=q.device)
+        out = _new((N, heads, d), q.device, stream)
     if lse is None:
-        lse = torch.empty((N, heads), dtype=torch.float32, device=q.device)
+        lse = _new((N, heads), q.device, stream)
     _state_shapes(lse, lse, out, N, heads, d)
     _check(lib().ra_ring_forward(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(out, "out", torch.float32),
@@ -325,9 +349,9 @@ def ra_ring_forward_masked(q, k, v, *, P: int, layout="contiguous", causal: bool
     if k.shape[0] != N:
         raise ValueError("q, k and v must cover the same N tokens")
     if out is None:
-        out = torch.empty((N, heads, d), dtype=torch.float32, device=q.device)
+        out = _new((N, heads, d), q.device, stream)
     if lse is None:
-        lse = torch.empty((N, heads), dtype=torch.float32, device=q.device)
+        lse = _new((N, heads), q.device, stream)
     _state_shapes(lse, lse, out, N, heads, d)
     cu_ptr, ndocs = _docs(cu_seqlens)
     _check(lib().ra_ring_forward_masked(
@@ -351,11 +375,11 @@ def ra_ring_backward_masked(q, k, v, out, lse, dout, *, P: int, layout="contiguo
     if tuple(dout.shape) != (N, heads, d) or dout.dtype != q.dtype:
         raise ValueError("dout must match q in shape and dtype")
     if dq is None:
-        dq = torch.empty((N, heads, d), dtype=torch.float32, device=q.device)
+        dq = _new((N, heads, d), q.device, stream)
     if dk is None:
-        dk = torch.empty((N, kv_heads, d), dtype=torch.float32, device=q.device)
+        dk = _new((N, kv_heads, d), q.device, stream)
     if dv is None:
-        dv = torch.empty((N, kv_heads, d), dtype=torch.float32, device=q.device)
+        dv = _new((N, kv_heads, d), q.device, stream)
     cu_ptr, ndocs = _docs(cu_seqlens)
     _check(lib().ra_ring_backward_masked(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(out, "out", torch.float32),
@@ -374,11 +398,11 @@ def ra_ring_backward(q, k, v, out, lse, dout, *, P: int, causal: bool, dq=None, 
     if tuple(dout.shape) != (N, heads, d) or dout.dtype != q.dtype:
         raise ValueError("dout must match q in shape and dtype")
     if dq is None:
-        dq = torch.empty((N, heads, d), dtype=torch.float32, device=q.device)
+        dq = _new((N, heads, d), q.device, stream)
     if dk is None:
-        dk = torch.empty((N, kv_heads, d), dtype=torch.float32, device=q.device)
+        dk = _new((N, kv_heads, d), q.device, stream)
     if dv is None:
-        dv = torch.empty((N, kv_heads, d), dtype=torch.float32, device=q.device)
+        dv = _new((N, kv_heads, d), q.device, stream)
     _check(lib().ra_ring_backward(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(out, "out", torch.float32),
         _dev(lse, "lse", torch.float32), _dev(dout, "dout"), _dev(dq, "dq", torch.float32),
@@ -415,9 +439,9 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
     if q_off is None:
         q_off = n_kv - n_q
     if out is None:
-        out = torch.empty((n_q, heads, d), dtype=torch.float32, device=q.device)
+        out = _new((n_q, heads, d), q.device, stream)
     if lse is None:
-        lse = torch.empty((n_q, heads), dtype=torch.float32, device=q.device)
+        lse = _new((n_q, heads), q.device, stream)
     _state_shapes(lse, lse, out, n_q, heads, d)
     kp = _dev(k, "k") if n_kv else 0
     vp = _dev(v, "v") if n_kv else 0
@@ -434,11 +458,6 @@ def ra_decode_forward(q, k, v, *, P: int, q_off: int | None = None, causal: bool
 # of a serving step.  Their arguments are marshalled by the extension _serve
 # (csrc/serve_binding.cpp): the same checks and the same C ABI calls as the
 # functions above, at a few microseconds instead of tens.
-#
-# stream= takes a torch.cuda.Stream or a cudaStream_t as an integer.  Outputs
-# that are not passed in belong to that stream's memory and are recorded as
-# used by the current one; ordering the streams stays with the caller, and so
-# does keeping the inputs, and outputs that are passed in, until it is done.
 
 _serve = None
 
@@ -594,9 +613,9 @@ def ra_ring_forward_noalloc(q, k, v, *, P: int, causal: bool, out=None, lse=None
     if k.shape[0] != N:
         raise ValueError("q, k and v must cover the same N tokens")
     if out is None:
-        out = torch.empty((N, heads, d), dtype=torch.float32, device=q.device)
+        out = _new((N, heads, d), q.device, stream)
     if lse is None:
-        lse = torch.empty((N, heads), dtype=torch.float32, device=q.device)
+        lse = _new((N, heads), q.device, stream)
     _state_shapes(lse, lse, out, N, heads, d)
     _check(lib().ra_ring_forward_noalloc(
         _dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(out, "out", torch.float32),

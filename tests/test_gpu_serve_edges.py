@@ -70,6 +70,8 @@ def side_calls():
     slots, pos = torch.arange(T, device=DEV), i32(np.arange(T))
     ptab, plen = i32(np.arange(T // ps)).view(16, -1), i32(np.full(16, T // 16))
 
+    out, lse = torch.zeros_like(dqo), torch.full((T, H), 5.0, device=DEV)
+
     def up(*sizes):
         return sum(-(-x // 512) * 512 for x in sizes)
 
@@ -86,10 +88,16 @@ def side_calls():
                    up(q.numel() * 2)),
         "decode": (lambda s: ra.ra_paged_decode(q, kc, vc, ptab, plen, stream=s),
                    up(q.numel() * 4, T * H * 4)),
+        "ring": (lambda s: ra.ra_ring_forward(q, k, v, P=4, causal=True, stream=s), up(q.numel() * 4)),
+        "ring backward": (lambda s: ra.ra_ring_backward(q, k, v, out, lse, q, P=4, causal=True,
+                                                        stream=s), up(q.numel() * 4)),
+        "contiguous decode": (lambda s: ra.ra_decode_forward(q[:4096], k, v, P=4, stream=s),
+                              up(4096 * H * d * 4)),
     }
 
 
-CALLS = ["rope", "rope backward", "extend", "release", "append", "decode"]
+CALLS = ["rope", "rope backward", "extend", "release", "append", "decode", "ring", "ring backward",
+         "contiguous decode"]
 BUSY = 200_000_000  # cycles of a sleeping kernel: about 0.1 s
 
 
@@ -151,10 +159,11 @@ def test_outputs_left_out_belong_to_the_stream_of_the_call(name, form):
     ra.ra_device_status()
 
 
+@pytest.mark.parametrize("name", ["decode", "ring"])
 @pytest.mark.parametrize("handle", [0, 1])
-def test_the_default_stream_by_its_handles(handle):
+def test_the_default_stream_by_its_handles(handle, name):
     """NULL and cudaStreamLegacy, with another stream current."""
-    f, _ = side_calls()["decode"]
+    f, _ = side_calls()[name]
     want = f(None)
     torch.cuda.synchronize()
     with torch.cuda.stream(torch.cuda.Stream()):
