@@ -457,7 +457,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const float ref = mx[c] == -INFINITY ? 0.f : mx[c];
         lt[c] = (vl.x * ex2(vm.x - ref) + vl.y * ex2(vm.y - ref)) +
                 (vl.z * ex2(vm.z - ref) + vl.w * ex2(vm.w - ref));
-        inv[c] = item.slot >= 0 ? 1.f : (lt[c] > 0.f ? 1.f / lt[c] : 0.f);
+        inv[c] = item.slot >= 0 ? 1.f : (lt[c] == 0.f ? 0.f : 1.f / lt[c]);
         const float e = ex2(m[nt][c] - ref);
 #pragma unroll
         for (int dm = 0; dm < D / 16; ++dm) {
@@ -535,7 +535,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             a.pm[row] = mx[c];
             a.pl[row] = lt[c];
           } else {
-            a.lse[row] = lt[c] > 0.f ? mx[c] * kLn2 + logf(lt[c]) : -INFINITY;
+            a.lse[row] = lt[c] == 0.f ? -INFINITY : mx[c] * kLn2 + logf(lt[c]);  // (NaN stays)
           }
         }
       }
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
       e[w] = ex2(s_m[w] - ref);
       l = fmaf(s_l[w], e[w], l);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int rr = cut.rr0 + r, j = rr / g;
     const long long row = static_cast<long long>(cut.row0 + j) * a.heads + cut.kh * g + (rr - j * g);
     for (int i = threadIdx.x; i < D; i += 32 * kJoin) {
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
       if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + i] = __float2bfloat16_rn(y * inv);
       else static_cast<float*>(a.out)[row * D + i] = y * inv;
     }
-    if (threadIdx.x == 0) a.lse[row] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+    if (threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : mx * kLn2 + logf(l);
     __syncthreads();
   }
 }

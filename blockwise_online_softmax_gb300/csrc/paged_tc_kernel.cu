@@ -496,7 +496,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (!ok) break;
           l = fmaf(s_inv[r], alpha, l);
         }
-        s_inv[r] = x.slot >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+        s_inv[r] = x.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
         mbar_arrive(bar(C::B_ML));
         if (r < x.rows) {
           if (x.slot >= 0) {
@@ -505,7 +505,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           } else {
             const int j = rr / g;
             a.lse[static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g)] =
-                l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
+                l == 0.f ? -INFINITY : m * kLn2 + logf(l);
           }
         }
       }

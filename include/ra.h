@@ -524,7 +524,8 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
  *   undefined.  What lies behind a request's last token in its last page
  *   does not matter, NaN included.  Keys and values that a request does see
  *   should be finite: a value that is not gives NaN in every row of that
- *   request's new tokens, in those that do not see its key too.
+ *   request's new tokens, in those that do not see its key too; a key that
+ *   is NaN gives NaN, in out and in lse, in the rows that see it.
  *   heads / kv_heads <= 128, T * heads <= 2^31 - 256.
  */
 int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* block_table,

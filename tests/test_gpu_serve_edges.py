@@ -9,7 +9,7 @@ import torch
 import blockwise_online_softmax_gb300 as ra
 import serve_ref
 from blockwise_online_softmax_gb300 import binding
-from test_gpu_paged import i32
+from test_gpu_paged import check_decode, i32, make_decode
 from test_gpu_rope import np64
 
 pytestmark = pytest.mark.gpu
@@ -170,3 +170,20 @@ def test_the_default_stream_by_its_handles(handle, name):
         got = f(handle)
     torch.cuda.synchronize()
     assert same(got, want)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("lengths, n_q, H, Hkv, d", [
+    ([40, 30], 1, 8, 2, 128), ([60000, 50], 1, 8, 2, 64), ([300, 200], 16, 64, 8, 128),
+    ([40000, 100], 16, 8, 1, 64),
+])
+def test_a_nan_key_gives_nan_and_not_an_empty_row(lengths, n_q, H, Hkv, d):
+    """A key that is NaN makes the rows that see it NaN, the LSE too: -inf
+    there says that a row sees no key.  Other requests are as without it."""
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, [n_q] * 2, H, Hkv, d, 16)
+    kc[table[0, 0].long(), 3] = float("nan")
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, lens)
+    ra.ra_device_status()
+    assert torch.isnan(out[:n_q]).all() and torch.isnan(lse[:n_q]).all()
+    check_decode(out[n_q:], lse[n_q:], q[n_q:], ks[1:], vs[1:], [n_q])
