@@ -124,14 +124,20 @@ cudaError_t scratch_pool(cudaMemPool_t* out) {
     props.handleTypes = cudaMemHandleTypeNone;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
+    // The first call may come inside a stream capture, where creating a pool
+    // is refused unless the thread's capture mode is relaxed.  It enqueues
+    // nothing, so nothing is missing from the graph.
     cudaMemPool_t pool = nullptr;
-    if ((e = cudaMemPoolCreate(&pool, &props)) != cudaSuccess) return e;
     uint64_t keep = UINT64_MAX;
-    if ((e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return e;
+    e = cudaMemPoolCreate(&pool, &props);
+    if (e == cudaSuccess && (e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
       cudaMemPoolDestroy(pool);
-      return e;
-    }
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
     g_pool[dev] = pool;
+    if (back != cudaSuccess) return back;
   }
   *out = g_pool[dev];
   return cudaSuccess;

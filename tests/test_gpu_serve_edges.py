@@ -2,6 +2,10 @@
 
 u = 2^-24 throughout (half a step of fp32, relative).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -187,3 +191,40 @@ def test_a_nan_key_gives_nan_and_not_an_empty_row(lengths, n_q, H, Hkv, d):
     ra.ra_device_status()
     assert torch.isnan(out[:n_q]).all() and torch.isnan(lse[:n_q]).all()
     check_decode(out[n_q:], lse[n_q:], q[n_q:], ks[1:], vs[1:], [n_q])
+
+
+# ------------------------------------------------------------------ a capture first
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import blockwise_online_softmax_gb300 as ra
+from test_gpu_paged import check_decode, make_decode
+q, kc, vc, table, lens, ks, vs = make_decode([700, 64, 3000], [{n_q}] * 3, 32, 8, 128, 16)
+f, w = ra.rope_freqs(128)[0], torch.ones(128, device="cuda")
+ph, dy = ra.rope_phases(f).cuda(), torch.randn(q.shape, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, lens)
+    grads = ra.ra_qk_norm_rope_backward(q, q, ph, dy, dy, q_weight=w, k_weight=w)
+for _ in range(3):
+    g.replay()
+torch.cuda.synchronize()
+check_decode(out, lse, q, ks, vs, [{n_q}] * 3)
+want = ra.ra_qk_norm_rope_backward(q, q, ph, dy, dy, q_weight=w, k_weight=w)
+assert all(torch.equal(a, b) for a, b in zip(grads, want))
+ra.ra_device_status()
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("n_q", [1, 8])
+def test_first_call_of_a_process_may_be_captured(n_q):
+    """No call has to run before a capture: pools, attributes and symbols are
+    set up inside it."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests, n_q=n_q)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
