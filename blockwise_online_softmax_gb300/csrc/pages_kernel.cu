@@ -282,17 +282,19 @@ bool paged_release_needs_scratch(const ReleaseArgs& a) {
 }
 
 cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st) {
-  if (!a.first_page) return launch_early(paged_extend_kernel<true>, dim3(1), kBook, 0, st, a);
-  cudaError_t e = launch_early(paged_extend_kernel<false>, dim3(1), kBook, 0, st, a);
-  if (e != cudaSuccess) return e;
+  return launch_early(a.first_page ? paged_extend_kernel<false> : paged_extend_kernel<true>, dim3(1), kBook, 0, st, a);
+}
+
+cudaError_t launch_paged_extend_tokens(const ExtendArgs& a, cudaStream_t st) {
   return launch_early(paged_extend_tokens_kernel,
                       dim3(static_cast<unsigned>((a.tokens + kSpread - 1) / kSpread)), kSpread, 0, st, a);
 }
 
 cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st) {
-  if (!a.first_page) return launch_early(paged_release_kernel<true>, dim3(1), kBook, 0, st, a);
-  cudaError_t e = launch_early(paged_release_kernel<false>, dim3(1), kBook, 0, st, a);
-  if (e != cudaSuccess) return e;
+  return launch_early(a.first_page ? paged_release_kernel<false> : paged_release_kernel<true>, dim3(1), kBook, 0, st, a);
+}
+
+cudaError_t launch_paged_release_pages(const ReleaseArgs& a, cudaStream_t st) {
   const long long most = (static_cast<long long>(a.n_req) * a.max_pages + kSpread - 1) / kSpread;
   return launch_early(paged_release_pages_kernel, dim3(static_cast<unsigned>(most < 608 ? most : 608)), kSpread, 0,
                       st, a);

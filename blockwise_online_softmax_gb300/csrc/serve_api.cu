@@ -195,9 +195,16 @@ int ra_paged_extend(const int* lengths, const int* new_tokens, int n_req, int* b
       return fail(RA_ERR_ALLOC, "pool allocation of the page sums failed: %s", cudaGetErrorString(e));
     }
   }
-  TraceScope ts(RA_KERNEL_PAGED_EXTEND, st);
-  e = ra::launch_paged_extend(a, st);
-  ts.done(e == cudaSuccess);
+  {
+    TraceScope ts(RA_KERNEL_PAGED_EXTEND, st);
+    e = ra::launch_paged_extend(a, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (a.first_page && e == cudaSuccess) {
+    TraceScope ts(RA_KERNEL_PAGED_EXTEND, st);
+    e = ra::launch_paged_extend_tokens(a, st);
+    ts.done(e == cudaSuccess);
+  }
   const cudaError_t ef = a.first_page ? cudaFreeAsync(a.first_page, st) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "paged-extend launch");
   return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
@@ -232,9 +239,16 @@ int ra_paged_release(const int* lengths, const int* finished, int n_req, const i
       return fail(RA_ERR_ALLOC, "pool allocation of the page sums failed: %s", cudaGetErrorString(e));
     }
   }
-  TraceScope ts(RA_KERNEL_PAGED_RELEASE, st);
-  e = ra::launch_paged_release(a, st);
-  ts.done(e == cudaSuccess);
+  {
+    TraceScope ts(RA_KERNEL_PAGED_RELEASE, st);
+    e = ra::launch_paged_release(a, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (a.first_page && e == cudaSuccess) {
+    TraceScope ts(RA_KERNEL_PAGED_RELEASE, st);
+    e = ra::launch_paged_release_pages(a, st);
+    ts.done(e == cudaSuccess);
+  }
   const cudaError_t ef = a.first_page ? cudaFreeAsync(a.first_page, st) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "paged-release launch");
   return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");

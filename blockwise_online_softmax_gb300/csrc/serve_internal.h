@@ -36,6 +36,8 @@ struct ExtendArgs {
 };
 bool paged_extend_needs_scratch(const ExtendArgs& a);
 cudaError_t launch_paged_extend(const ExtendArgs& a, cudaStream_t st);
+// The second launch of a large step (with scratch).
+cudaError_t launch_paged_extend_tokens(const ExtendArgs& a, cudaStream_t st);
 
 struct ReleaseArgs {
   const int* lengths;
@@ -53,6 +55,7 @@ struct ReleaseArgs {
 };
 bool paged_release_needs_scratch(const ReleaseArgs& a);
 cudaError_t launch_paged_release(const ReleaseArgs& a, cudaStream_t st);
+cudaError_t launch_paged_release_pages(const ReleaseArgs& a, cudaStream_t st);
 
 // ------------------------------------------------------------------ q/k norm and rotary positions
 struct RopeArgs {

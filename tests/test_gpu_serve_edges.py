@@ -176,6 +176,31 @@ def test_the_default_stream_by_its_handles(handle, name):
     assert same(got, want)
 
 
+# ------------------------------------------------------------------ launches counted
+
+def test_trace_counts_every_launch_of_the_bookkeeping():
+    """A large step is two launches, a small one is one."""
+    def count(kind, run):
+        ra.ra_trace_reset()
+        ra.ra_trace_enable(True)
+        try:
+            run()
+            return ra.ra_trace_query(kind)[0]
+        finally:
+            ra.ra_trace_enable(False)
+            ra.ra_trace_reset()
+
+    for n, launches in ((16, 1), (6000, 2)):
+        lens, ones = i32(np.zeros(n)), i32(np.ones(n))
+        table, free = i32(np.zeros(4 * n)).view(n, 4), i32(np.arange(n))
+        got = count("paged_extend", lambda: ra.ra_paged_extend(
+            lens, ones, table, free, i32([n]), page_size=16, tokens=n))
+        assert got == launches
+        got = count("paged_release", lambda: ra.ra_paged_release(
+            ones, ones, table, free, i32([0]), page_size=16))
+        assert got == launches
+
+
 # ------------------------------------------------------------------ values that are not finite
 
 @pytest.mark.parametrize("lengths, n_q, H, Hkv, d", [
