@@ -152,8 +152,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
   wait_for_previous();
   if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, kExtra, kThreads>(a, g, RT, smem + C::OFF_BUF);  // synchronizes
-  if (run.first >= run.last || *abort_flag) return;
+  const Run run = find_run<BT, kExtra, kThreads>(a, g, RT, smem + C::OFF_BUF, abort_flag);  // synchronizes
+  if (run.first >= run.last || run.stop) return;
   const long long lim = a.wait_limit;
 
   if (warp >= kCons) {

@@ -155,8 +155,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   }
   wait_for_previous();
   if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, 0, kThreads>(a, g, RT, smem + C::OFF_AL);  // synchronizes
-  if (run.first >= run.last || *abort_flag) return;
+  const Run run = find_run<BT, 0, kThreads>(a, g, RT, smem + C::OFF_AL, abort_flag);  // synchronizes
+  if (run.first >= run.last || run.stop) return;
   if (warp == 14) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();

@@ -166,16 +166,22 @@ struct Walk {
 // into runs of `size` or, the first `longer` of them, size + 1 units; the first
 // unit of the CTA's own is located as (request, offset).  With fewer units than
 // CTAs only `ctas` of them work, so the CTAs of a cut item all hold a part of it.
+// `stop`: the abort flag as the CTA's thread 0 set it.  It is read between the
+// two barriers here: a wait may raise it as soon as a warp is past the second,
+// and warps that read it later could part ways, some leaving while the others
+// meet them at a barrier.
 struct Run {
   long long total, first, last;
   long long size;
   int longer, ctas;
   int r;
   long long x;
+  bool stop;
 };
 
 template <int BT, int EXTRA, int kThreads>
-__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch) {
+__device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch,
+                                        const volatile int* abort_flag) {
   long long* s_sum = static_cast<long long*>(scratch);  // [kThreads / 32], then the location
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_req + kThreads - 1) / kThreads;
@@ -198,6 +204,7 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
   }
   Run run;
   run.total = total;
+  run.stop = *abort_flag != 0;
   run.ctas = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   run.first = run.last = total;
   const int me = static_cast<int>(blockIdx.x);
