@@ -980,11 +980,13 @@ umma_ring_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   for (int s = tid; s < a.P; s += NTHREADS) rec[s] = step_visit(a, i, s, row0, vb);
   if (tid == 0) *abort_flag = launch_status != 0 ? 1 : 0;
   tc_fence_before();
-  __syncthreads();
+  // The barrier carries the decision: a warp that read the flag behind it
+  // could find it raised by a faster warp's first wait, and leave alone.
+  const bool stop = __syncthreads_or(launch_status) != 0;
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool no_keys = next_step(rec, a.P, 0) == a.P;
-  if (no_keys || *abort_flag) {  // uniform across the CTA: read after the barrier
+  if (no_keys || stop) {  // uniform across the CTA
     // Rows that see no key anywhere: O = 0 and LSE = -inf, and no pipeline.
     if (no_keys && tid < NQ * BM) {
       const long long grow = row0 + tid;

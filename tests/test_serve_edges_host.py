@@ -1,5 +1,5 @@
-"""The serving calls' sources and arithmetic, as far as they can be checked
-without a GPU."""
+"""The kernels' sources and arithmetic, as far as they can be checked without
+a GPU."""
 import os
 import re
 
@@ -28,3 +28,14 @@ def test_a_cta_decides_once_whether_it_runs(name):
     body = body[:body.index("return run;")]
     first, second = (m.start() for m in re.finditer(r"__syncthreads\(\)", body))
     assert first < body.index("*abort_flag != 0") < second
+
+
+def test_the_fused_ring_decides_once_whether_it_runs():
+    """The same in the fused ring forward, where the barrier in front of the
+    roles carries the decision.  (The other kernels read the flag between two
+    barriers.)"""
+    code = source("umma_kernel.cu")
+    ring = code[code.index("umma_ring_kernel(const __grid_constant__"):]
+    ring = ring[:ring.index("regs_dec")]
+    assert "__syncthreads_or(launch_status)" in ring
+    assert not re.search(r"(if|\|\||&&|while)[^;{]*[^&\w]\*abort_flag(?!\s*=[^=])", ring)
