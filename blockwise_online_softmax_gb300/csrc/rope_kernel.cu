@@ -28,6 +28,7 @@ namespace ra {
 namespace {
 
 constexpr int kWarps = 8;  // per CTA
+constexpr float kRest = 6.283185307179586f * 0x1p-48f;  // radians of 2^-48 turns
 constexpr unsigned kAll = 0xffffffffu;
 
 // Eight consecutive columns as a lane loads and stores them.
@@ -37,6 +38,11 @@ template <>
 struct Vec<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ Vec() : w(make_uint4(0u, 0u, 0u, 0u)) {}
+  static __device__ __forceinline__ Vec ones() {
+    Vec v;
+    v.w = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    return v;
+  }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     w = *reinterpret_cast<const uint4*>(p);  // not __ldg: the output may be the input
   }
@@ -63,6 +69,11 @@ template <>
 struct Vec<float> {
   float4 a, b;
   __device__ __forceinline__ Vec() : a(make_float4(0.f, 0.f, 0.f, 0.f)), b(a) {}
+  static __device__ __forceinline__ Vec ones() {
+    Vec v;
+    v.a = v.b = make_float4(1.f, 1.f, 1.f, 1.f);
+    return v;
+  }
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const float4*>(p);
     b = *(reinterpret_cast<const float4*>(p) + 1);
@@ -484,11 +495,13 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
       grad += sub * D + col;
       dst += sub * D + col;
       for (int g = CUT ? ga : 0; g < gb; g += kGradBatch) {
+        // Rows of nobody are ones with no gradient: without eps, the norm of a row
+        // of zeros would be infinite.
         Vec<T> raw[kGradBatch];
         Vec<float> gr[kGradBatch];
 #pragma unroll
         for (int j = 0; j < kGradBatch; ++j) {
-          raw[j] = Vec<T>();
+          raw[j] = Vec<T>::ones();
           gr[j] = Vec<float>();
           if (g + j < gb && (g + j) * RPI + sub < n) {
             raw[j].load(src + (g + j) * RPI * D);
@@ -498,7 +511,6 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
 #pragma unroll
         for (int j = 0; j < kGradBatch; ++j) {
           if (g + j >= gb) break;
-          const bool valid = (g + j) * RPI + sub < n;
           float x[8], gy[8], p[8];
           raw[j].get(x);
           gr[j].get(gy);
@@ -515,8 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
             }
             ss = row_sum<LPR>(ss);
             ux = row_sum<LPR>(ux);
-            // (0 for the rows of nobody: without eps theirs would be infinite.)
-            const float r = valid ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
+            const float r = rsqrtf(ss * (1.f / D) + a.eps);
             const float m = r * r * ux * (1.f / D);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -524,7 +535,7 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
               gy[e] = r * fmaf(-x[e], m, u[e]);
             }
           }
-          if (valid) Vec<T>::store(dst + (g + j) * RPI * D, gy);
+          if ((g + j) * RPI + sub < n) Vec<T>::store(dst + (g + j) * RPI * D, gy);
         }
       }
     };
