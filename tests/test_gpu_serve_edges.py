@@ -2,6 +2,7 @@
 
 u = 2^-24 throughout (half a step of fp32, relative).
 """
+import math
 import os
 import subprocess
 import sys
@@ -216,6 +217,33 @@ def test_a_nan_key_gives_nan_and_not_an_empty_row(lengths, n_q, H, Hkv, d):
     ra.ra_device_status()
     assert torch.isnan(out[:n_q]).all() and torch.isnan(lse[:n_q]).all()
     check_decode(out[n_q:], lse[n_q:], q[n_q:], ks[1:], vs[1:], [n_q])
+
+
+# ------------------------------------------------------------------ angles and sums
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_cos_and_sin_to_their_last_bits(inter):
+    """Pairs (1, 0) give cos and sin themselves.  sincospif is good to an ulp
+    (u here: the values are at most 1), its argument carries no rounding, the
+    correction for the turn's low bits is one rounding (u / 2) with a factor
+    below 4e-7: 1.6 u.  An argument rounded to 24 bits of half a turn costs
+    pi 2^-25 = 1.6 u more."""
+    d, T = 128, 4096
+    f = ra.rope_freqs(d)[0]
+    ph = ra.rope_phases(f)
+    a, b = serve_ref.pairs(d, inter)
+    x = torch.zeros(T, 1, d)
+    x[..., a] = 1.0
+    r = np.random.default_rng(0)
+    pos = r.integers(-2 ** 31, 2 ** 31, T)
+    pos[:1024] = np.arange(1024)
+    x = x.to(DEV)
+    out, _ = ra.ra_qk_norm_rope(x, x, ph.to(DEV), positions=i32(pos), interleaved=inter)
+    turn = (pos.astype(np.int64)[:, None] * ph.numpy()[None, :])  # wraps, as the kernel's does
+    ang = turn.astype(np.float64) * (2 * math.pi / 2.0 ** 64)
+    got = np64(out)[:, 0]
+    err = max(np.abs(got[:, a] - np.cos(ang)).max(), np.abs(got[:, b] - np.sin(ang)).max())
+    assert err <= 1.6 * U, f"{err / U:.2f} u"
 
 
 # ------------------------------------------------------------------ a capture first
