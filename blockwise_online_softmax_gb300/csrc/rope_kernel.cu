@@ -461,13 +461,33 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
   }
 }
 
-// Backward.  Groups as in the forward; the weight gradients are summed in
-// the lanes, over the CTA's warps in shared memory, and written as one
-// partial sum per CTA, so their order is fixed.  CUT: some tokens are taken in
-// shares; without it that arithmetic stays out, whose registers cost a long call
-// 3% (128K tokens of 32/8 heads, d = 128: 863 us, 0.93 of the copy bandwidth;
-// 300 tokens 8.0, taken whole 12.2).
+// A sum in two words: hi + lo takes x, and lo what that addition rounds off
+// (Knuth's two-sum; six fp32 operations, where one in fp64 takes the time of
+// 64).
+__device__ __forceinline__ void add_to(float2& s, float x) {
+  const float t = s.x + x, b = t - s.x;
+  s.y += (s.x - (t - b)) + (x - b);
+  s.x = t;
+}
+__device__ __forceinline__ void add_to(float2& s, const float2& x) {
+  add_to(s, x.x);
+  s.y += x.y;
+}
+// (An infinity stays one; its lo is NaN.)
+__device__ __forceinline__ float value(const float2& s) { return isfinite(s.x) ? s.x + s.y : s.x; }
+
+// Backward.  Groups as in the forward.  The weight gradients are summed in a
+// fixed order: in the lanes over at most kRun rows (or a token's), then in two
+// words, from run to run (shared memory), over the CTA's warps and over the CTAs
+// (another launch).  In one word throughout, a lane added some 860 rows at 128K
+// tokens, and the sums were 5.1e-7 off, 7 times the plain form's error, now
+// 1.7e-7 (4099 tokens of 8/8 heads: 2.2e-7, now 0.9e-7); that took 864 us
+// instead of 871, runs of 32 rows 873.  CUT: some tokens are taken in shares;
+// without it that arithmetic stays out, whose registers cost a long call 3%
+// (128K tokens of 32/8 heads, d = 128: 871 us, 0.92 of the copy bandwidth; 300
+// tokens 8.0, taken whole 12.2).
 constexpr int kGradBatch = 3;
+constexpr int kRun = 64;
 constexpr int kGradCtas = 2;  // per SM
 
 template <typename T, int D, bool INTER, bool CUT>
@@ -475,13 +495,13 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
   let_next_start();
   wait_for_previous();
   constexpr int LPR = D / 8, RPI = 32 / LPR;
-  __shared__ float s_dw[kWarps][2][D];
+  __shared__ float2 s_dw[kWarps][16][32];  // [warp][q's eight columns, k's][lane]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = 8 * (lane % LPR), sub = lane / LPR;
   const int gq = (a.heads + RPI - 1) / RPI, gk = (a.kv_heads + RPI - 1) / RPI;
   const int groups = gq + gk, per = (groups + a.parts - 1) / a.parts;
-  const long long items = CUT ? a.whole + (a.T - a.whole) * a.parts : a.T;
-  const long long nwarps = static_cast<long long>(gridDim.x) * kWarps;
+  const unsigned items = static_cast<unsigned>(CUT ? a.whole + (a.T - a.whole) * a.parts : a.T);
+  const unsigned nwarps = gridDim.x * kWarps;
   float wq[8], wk[8], dwq[8], dwk[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) wq[e] = wk[e] = dwq[e] = dwk[e] = 0.f;
@@ -489,7 +509,23 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
   if (a.kw) load_weight(a.kw, a.w_bf16, col, wk);
   Rot<D, INTER> rot;
   rot.place(a, lane);
-  for (long long it = static_cast<long long>(blockIdx.x) * kWarps + warp; it < items; it += nwarps) {
+  // The runs' sums so far, and this one's added to them.
+  auto keep = [&](bool first) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float2 x = first ? make_float2(0.f, 0.f) : s_dw[warp][e][lane];
+      add_to(x, e < 8 ? dwq[e] : dwk[e - 8]);
+      s_dw[warp][e][lane] = x;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
+  };
+  const int turns = gq < kRun ? kRun / gq : 1;  // tokens of a run (k has no more groups than q)
+  unsigned it = blockIdx.x * kWarps + warp;
+  // (32-bit counters: with 64-bit ones 878 us instead of 871 below.)
+  bool first = true;
+  int left = turns;
+  for (; it < items; it += nwarps) {
     const bool cut = CUT && it >= a.whole;
     const long long t = cut ? a.whole + (it - a.whole) / a.parts : it;
     const int g0 = cut ? static_cast<int>(it - a.whole - (t - a.whole) * a.parts) * per : 0;
@@ -549,46 +585,56 @@ __global__ void __launch_bounds__(kWarps * 32, kGradCtas) rope_backward_kernel(c
          static_cast<T*>(a.qo) + t * a.qo_str, a.qw != nullptr, wq, dwq);
     rows(g0 > gq ? g0 - gq : 0, CUT ? g1 - gq : gk, a.kv_heads, static_cast<const T*>(a.k) + t * a.k_str, a.dko + t * a.kv_heads * D,
          static_cast<T*>(a.ko) + t * a.ko_str, a.kw != nullptr, wk, dwk);
+    if (--left == 0 && a.dw) {
+      asm volatile("" ::: "memory");  // the sums' loads stay in here: their registers are the rows'
+      keep(first);
+      first = false;
+      left = turns;
+      asm volatile("" ::: "memory");
+    }
   }
   if (!a.dw) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 16; ++e) {
+    float2 x = first ? make_float2(0.f, 0.f) : s_dw[warp][e][lane];
+    add_to(x, e < 8 ? dwq[e] : dwk[e - 8]);
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
-      dwq[e] += __shfl_xor_sync(kAll, dwq[e], o);
-      dwk[e] += __shfl_xor_sync(kAll, dwk[e], o);
+      x.x += __shfl_xor_sync(kAll, x.x, o);
+      x.y += __shfl_xor_sync(kAll, x.y, o);
     }
-    if (sub == 0) {
-      s_dw[warp][0][col + e] = dwq[e];
-      s_dw[warp][1][col + e] = dwk[e];
-    }
+    if (sub == 0) s_dw[warp][e][lane] = x;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
-    float s = 0.f;
+    const int e = i / D * 8 + i % 8, l = i % D / 8;
+    float2 x = s_dw[0][e][l];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += s_dw[w][i / D][i % D];
-    a.dw[static_cast<long long>(blockIdx.x) * 2 * D + i] = s;
+    for (int w = 1; w < kWarps; ++w) add_to(x, s_dw[w][e][l]);
+    a.dw[static_cast<long long>(blockIdx.x) * 2 * D + i] = x;
   }
 }
 
 // One CTA per 32 of the 2 d weight gradients: warp w sums the partials w,
-// w + 8, ... of its 32 columns, then the warps' sums meet in shared memory.
-__global__ void __launch_bounds__(kWarps * 32) rope_weight_grad_kernel(const RopeArgs a, int n, int d) {
+// w + 32, ... of its 32 columns, then the warps' sums of column w.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) rope_weight_grad_kernel(const RopeArgs a, int n, int d) {
   let_next_start();
   wait_for_previous();
-  __shared__ float s[kWarps][32];
+  __shared__ float2 s[kSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + lane;
-  float x = 0.f;
-  for (int p = warp; p < n; p += kWarps) x += a.dw[static_cast<long long>(p) * 2 * d + i];
+  float2 x = make_float2(0.f, 0.f);
+  for (int p = warp; p < n; p += kSumWarps)
+    add_to(x, a.dw[static_cast<long long>(p) * 2 * d + blockIdx.x * 32 + lane]);
   s[warp][lane] = x;
   __syncthreads();
-  if (warp) return;
+  x = s[lane][warp];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) x += s[w][lane];
+  for (int o = 16; o > 0; o >>= 1)
+    add_to(x, make_float2(__shfl_xor_sync(kAll, x.x, o), __shfl_xor_sync(kAll, x.y, o)));
+  const int i = blockIdx.x * 32 + warp;
   float* dst = i < d ? a.dqw : a.dkw;
-  if (dst) dst[i % d] = x;
+  if (lane == 0 && dst) dst[i % d] = value(x);
 }
 
 // Tokens are taken whole, one warp each, in turns of all warps of the grid; the
@@ -654,7 +700,7 @@ cudaError_t launch_rope_backward(const RopeArgs& a, int ctas, int d, bool bf16, 
 }
 
 cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st) {
-  return launch_early(rope_weight_grad_kernel, dim3(2 * d / 32), kWarps * 32, 0, st, a, n, d);
+  return launch_early(rope_weight_grad_kernel, dim3(2 * d / 32), kSumWarps * 32, 0, st, a, n, d);
 }
 
 }  // namespace ra

@@ -327,7 +327,7 @@ int ra_qk_norm_rope_backward(const void* q, const void* k, const float* dq_out,
   a.dkw = dk_weight;
   const int ctas = ra::rope_grad_ctas(a, d);
   if (dq_weight || dk_weight) {
-    e = scratch_alloc(reinterpret_cast<void**>(&a.dw), static_cast<size_t>(ctas) * 2 * d * sizeof(float), st);
+    e = scratch_alloc(reinterpret_cast<void**>(&a.dw), static_cast<size_t>(ctas) * 2 * d * sizeof(float2), st);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return fail(RA_ERR_ALLOC, "pool allocation of the partial weight gradients failed: %s", cudaGetErrorString(e));

@@ -89,7 +89,7 @@ struct RopeArgs {
   int w_bf16;
   float eps;
   float mscale;
-  float* dw;             // backward: partial weight gradients [rope_grad_ctas][2][d]
+  float2* dw;            // backward: partial weight gradients [rope_grad_ctas][2][d], in two words
   float* dqw;            // [d] or null
   float* dkw;
   // Set by the launcher: a warp takes a token as a whole, from token `whole` on

@@ -15,7 +15,7 @@ import blockwise_online_softmax_gb300 as ra
 import serve_ref
 from blockwise_online_softmax_gb300 import binding
 from test_gpu_paged import check_decode, i32, make_decode
-from test_gpu_rope import np64
+from test_gpu_rope import check_rope, np64
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -244,6 +244,58 @@ def test_cos_and_sin_to_their_last_bits(inter):
     got = np64(out)[:, 0]
     err = max(np.abs(got[:, a] - np.cos(ang)).max(), np.abs(got[:, b] - np.sin(ang)).max())
     assert err <= 1.6 * U, f"{err / U:.2f} u"
+
+
+LONG = [
+    # T, heads, kv_heads, d, rot, interleaved: whole tokens with shares of the rest's rows, and
+    # sequences past eight turns of every warp
+    (2701, 24, 8, 64, 32, True), (4099, 32, 8, 128, 128, False), (33001, 3, 1, 64, 64, False),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(str(x) for x in c))
+def test_weight_gradients_of_long_sequences(case):
+    """A term is off by 64 u of its size (see test_gpu_rope.py); up to 64 of
+    them and four lanes are added in one word, the rest in two, and one
+    rounding: 130 u of the absolute sum, however many there are.  What one CTA contributes is
+    thousands of times that."""
+    T, H, Hkv, d, rot, inter = case
+    g = torch.Generator().manual_seed(T)
+    q, k, dqo, dko = (torch.randn(T, h, d, generator=g).to(DEV) for h in (H, Hkv, H, Hkv))
+    w = (1 + 0.2 * torch.randn(d, generator=g)).to(DEV)
+    f = ra.rope_freqs(rot)[0]
+    ph = ra.rope_phases(f).to(DEV)
+    how = dict(q_weight=w, k_weight=w, interleaved=inter)
+    qo, ko = ra.ra_qk_norm_rope(q, k, ph, **how)
+    pos = np.arange(T)
+    check_rope(qo, q, w, pos, f.numpy(), interleaved=inter)
+    check_rope(ko, k, w, pos, f.numpy(), interleaved=inter)
+    got = ra.ra_qk_norm_rope_backward(q, k, ph, dqo, dko, **how)
+    for x, dy, dx, dw in ((q, dqo, got[0], got[2]), (k, dko, got[1], got[3])):
+        rx, rw, size, wsize = serve_ref.rope_grad(np64(x), np64(w), pos, f.numpy(), np64(dy),
+                                                  eps=1e-6, interleaved=inter)
+        assert (np.abs(np64(dx) - rx) <= 128 * U * size + 1e-30).all()
+        assert (np.abs(np64(dw) - rw) <= 130 * U * wsize).all()
+        assert np.abs(rw).max() > 1000 * 130 * U * wsize.max() / math.sqrt(T)  # the bar bites
+
+
+@pytest.mark.parametrize("H, d", [(32, 128), (4, 64)])
+def test_weight_gradients_keep_small_terms_beside_a_large_one(H, d):
+    """Terms that are exact (rows of +-1 normalise to themselves without eps,
+    nothing turns): one of 2^24 among ones.  In one fp32 word every addition
+    after it is off by up to half a step, 1; here the 63 of its run are and two
+    that join lanes, and the result has its own half step."""
+    T = 40000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q = (torch.randint(0, 2, (T, H, d), generator=g, device=DEV) * 2 - 1).float()
+    dy = q.clone()          # every term is dy x = 1
+    dy[5, 1] *= 2.0 ** 24
+    w = torch.ones(d, device=DEV)
+    dw = ra.ra_qk_norm_rope_backward(q, q[:, :1].contiguous(), None, dy, dy[:, :1].contiguous(),
+                                     q_weight=w, k_weight=w, eps=0.0)
+    want = T * H - 1 + 2 ** 24
+    assert (dw[2].double() - want).abs().max().item() <= 64 + want * U
+    assert (dw[3] == T).all()
 
 
 # ------------------------------------------------------------------ a capture first
