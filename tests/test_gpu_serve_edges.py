@@ -1,4 +1,7 @@
-"""The serving and rotary calls at their edges.
+"""The serving and rotary calls at their edges: streams other than the current
+one, values that are not finite, launches counted, long sequences and offsets
+past 32 bits, and tolerances tight enough to see a lost term of the softmax
+weights or a lost partial sum.
 
 u = 2^-24 throughout (half a step of fp32, relative).
 """
@@ -6,12 +9,14 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
 import torch
 
 import blockwise_online_softmax_gb300 as ra
+import oracle
 import serve_ref
 from blockwise_online_softmax_gb300 import binding
 from test_gpu_paged import check_decode, i32, make_decode
@@ -219,6 +224,84 @@ def test_a_nan_key_gives_nan_and_not_an_empty_row(lengths, n_q, H, Hkv, d):
     check_decode(out[n_q:], lse[n_q:], q[n_q:], ks[1:], vs[1:], [n_q])
 
 
+# ------------------------------------------------------------------ softmax weights to 24 bits
+
+def one_hot_case(lengths, n_q, H, Hkv, d, ps, spread, seed):
+    """A decode whose scores are exact and whose outputs are single weights.
+    Each query row picks one column of K (one product, no sum).  Of a
+    request's keys three are live, with scores in [-1, 1]; the others are so
+    far below that their weight is exactly 0 in fp32.  Column c of V is 1 at
+    live key c % 3 and 0 at the two others."""
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, [n_q] * len(lengths), H, Hkv, d, ps, seed=seed)
+    r = np.random.default_rng(seed)
+    g = H // Hkv
+    q.zero_()
+    for i in range(len(lengths)):
+        for j in range(n_q):
+            for h in range(H):
+                q[i * n_q + j, h, (j * g + h % g) % d] = 1.0
+    tab = table.cpu().numpy()
+    for i, n in enumerate(lengths):
+        live = np.sort(r.choice(n - n_q + 1, 3, replace=False)) if spread else np.arange(3)
+        at = torch.from_numpy(live).to(DEV)
+        ks[i].fill_(-200.0 * math.sqrt(d))
+        ks[i][at] = torch.from_numpy(r.uniform(-1, 1, (3, Hkv, d)) * math.sqrt(d)).to(DEV).bfloat16()
+        vs[i][at] = 0.0
+        for c in range(3):
+            vs[i][at[c], :, c::3] = 1.0
+        for p in range(-(-n // ps)):
+            part = slice(p * ps, min(n, p * ps + ps))
+            kc[tab[i, p], :part.stop - part.start] = ks[i][part]
+            vc[tab[i, p], :part.stop - part.start] = vs[i][part]
+    return q, kc, vc, table, lens, ks, vs
+
+
+WHOLE = [
+    # n_q, heads, kv_heads, d: row tiles of 8, 16 and 128
+    (1, 8, 2, 64), (1, 8, 2, 128), (3, 8, 2, 64), (3, 8, 2, 128), (5, 32, 4, 64), (16, 8, 1, 64),
+    (5, 32, 8, 128), (16, 16, 2, 128),
+]
+
+
+@pytest.mark.parametrize("where", ["whole", "cut"])
+@pytest.mark.parametrize("n_q, H, Hkv, d", WHOLE)
+def test_weights_have_24_bits(n_q, H, Hkv, d, where):
+    """An output is one weight p_i / l.  With scores s exact, y = s sl2 - m in
+    one rounding (|y| <= 3: 2 u, times ln 2) with sl2 off by u of |s| log2 e
+    (times ln 2: 1 u), and ex2 good to 2^-22 = 4 u: a weight is off by 6.4 u.
+    Three terms of it meet V = 1 in a sum that truncates twice (2 u each) and
+    one rounding; l adds two; 1 / l and the product one each: in an item of
+    one tile 2 * 6.4 + 4 + 1 + 2 + 2 = 22 u, 32 u is used.  Where tiles, warps
+    and parts meet, each of up to six levels brings a factor ex2(m - m') good
+    to 6.4 u, in numerator and denominator: 22 + 2 * 6 * 6.4 = 99 u, 112 u is used.
+    A weight in two bf16 terms is off by up to 2^-17 = 128 u (rounded) or
+    2^-15 = 512 u (cut), which the first bar, or both, refuse."""
+    lengths = [n_q + 2, n_q + 5, n_q + 9] if where == "whole" else [3000 + n_q, 70000, 500]
+    got = one_hot_case(lengths, n_q, H, Hkv, d, 16, where == "cut", seed=d + n_q)
+    q, kc, vc, table, lens, ks, vs = got
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, lens)
+    ra.ra_device_status()
+    bar = 32 if where == "whole" else 112
+    for i, n in enumerate(lengths):
+        rows = slice(i * n_q, (i + 1) * n_q)
+        ro, rl = oracle.attention(q[rows].cpu(), ks[i].cpu(), vs[i].cpu(), causal=True,
+                                  q_pos=n - n_q + np.arange(n_q), k_pos=np.arange(n))
+        err = np.abs(np64(out[rows]) - ro)
+        assert (err <= bar * U * ro).all(), f"max error {(err / (U * ro)).max():.1f} u"
+        # The LSE: the weights' sum to the same, m ln 2 and the logarithm 2 u of |m ln 2| <= 1 each.
+        assert (np.abs(np64(lse[rows]) - rl) <= (bar + 4) * U).all()
+
+
+def test_bf16_output_of_every_row_tile():
+    """bf16 outputs are the fp32 ones rounded once."""
+    for n_q, H, Hkv, d in WHOLE:
+        q, kc, vc, table, lens, _, _ = make_decode([700, 45, 3000], [n_q] * 3, H, Hkv, d, 32)
+        want = ra.ra_paged_decode(q, kc, vc, table, lens)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+        _, lse = ra.ra_paged_decode(q, kc, vc, table, lens, out=out)
+        assert torch.equal(out, want[0].bfloat16()) and torch.equal(lse, want[1])
+
+
 # ------------------------------------------------------------------ angles and sums
 
 @pytest.mark.parametrize("inter", [False, True])
@@ -296,6 +379,121 @@ def test_weight_gradients_keep_small_terms_beside_a_large_one(H, d):
     want = T * H - 1 + 2 ** 24
     assert (dw[2].double() - want).abs().max().item() <= 64 + want * U
     assert (dw[3] == T).all()
+
+
+# ------------------------------------------------------------------ sizes past the others
+
+def test_decode_more_requests_than_threads_on_the_large_row_tile():
+    """The 128-row kernel with several requests to a thread of its sums."""
+    r = np.random.default_rng(5)
+    lengths = [int(x) for x in r.integers(0, 200, 1300)]
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, [5] * 1300, 8, 1, 128, 16)
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, lens)
+    ra.ra_device_status()
+    check_decode(out, lse, q, ks, vs, [5] * 1300)
+
+
+def test_append_past_eight_turns_of_the_warps():
+    T, H, Hkv, d, ps = 33001, 3, 1, 64, 32
+    g = torch.Generator().manual_seed(T)
+    q, k, v = (torch.randn(T, h, d, generator=g).bfloat16().to(DEV) for h in (H, Hkv, Hkv))
+    n_pages = -(-T // ps)
+    kc, vc = (torch.zeros(n_pages, ps, Hkv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    slots = torch.randperm(n_pages * ps, generator=g)[:T].to(DEV)
+    f = ra.rope_freqs(d)[0]
+    qo = ra.ra_paged_append(q, k, v, ra.rope_phases(f).to(DEV), kc, vc, slots, i32(np.arange(T)))
+    check_rope(qo, q, None, np.arange(T), f.numpy())
+    check_rope(kc.view(-1, Hkv, d)[slots], k, None, np.arange(T), f.numpy())
+    assert torch.equal(vc.view(-1, Hkv, d)[slots], v)
+
+
+def test_rotary_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the first and last tokens, forward
+    and backward; then token strides whose product with the index passes 2^32."""
+    H, d = 128, 128
+    T = (1 << 31) // (H * d) + 3
+    g = torch.Generator(device=DEV).manual_seed(2)
+    f = ra.rope_freqs(d)[0]
+    ph = ra.rope_phases(f).to(DEV)
+    w = torch.linspace(0.5, 1.5, d, device=DEV)
+    q = torch.empty(T, H, d, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    k = torch.randn(T, 1, d, generator=g, device=DEV).bfloat16()
+    at = [0, 1, T // 2, T - 2, T - 1]
+    idx = torch.tensor(at, device=DEV)
+    qo, _ = ra.ra_qk_norm_rope(q, k, ph, q_weight=w)
+    check_rope(qo[idx], q[idx], w, np.array(at), f.numpy())
+    del qo
+    dqo = torch.empty(T, H, d, device=DEV).normal_(generator=g)
+    dko = torch.randn(T, 1, d, generator=g, device=DEV)
+    dq = ra.ra_qk_norm_rope_backward(q, k, ph, dqo, dko, q_weight=w)[0]
+    ref, _, size, _ = serve_ref.rope_grad(np64(q[idx]), np64(w), np.array(at), f.numpy(), np64(dqo[idx]), eps=1e-6)
+    assert (np.abs(np64(dq[idx]) - ref) <= 128 * U * size + 2.0 ** -8 * np.abs(ref)).all()
+    del dq, dqo, dko
+    stride = (1 << 29) + 8
+    buf = torch.empty(4 * stride + 2 * d, dtype=torch.bfloat16, device=DEV)
+    far = buf.as_strided((5, 2, d), (stride, d, 1))
+    far.copy_(q[:5, :2])
+    qo, ko = ra.ra_qk_norm_rope(far, far, ph, q_weight=w)
+    check_rope(qo, far, w, np.arange(5), f.numpy())
+    assert torch.equal(ko, ra.ra_qk_norm_rope(far.contiguous(), far.contiguous(), ph)[1])
+    dy = torch.randn(5, 2, d, generator=g, device=DEV)
+    want = ra.ra_qk_norm_rope_backward(far.contiguous(), far.contiguous(), ph, dy, dy, q_weight=w)
+    got = ra.ra_qk_norm_rope_backward(far, far.contiguous(), ph, dy, dy, q_weight=w, dq=far)  # dq is q
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+def test_append_offsets_past_32_bits():
+    """Slots whose elements lie past 2^32, and q, k, v as views with tokens
+    2^29 elements apart."""
+    ps, Hkv, d = 256, 8, 128
+    n_pages = (1 << 32) // (ps * Hkv * d) + 4
+    g = torch.Generator(device=DEV).manual_seed(3)
+    kc = torch.empty(n_pages, ps, Hkv, d, dtype=torch.bfloat16, device=DEV)
+    vc = torch.empty_like(kc)
+    stride = (1 << 29) + 8
+    buf = torch.empty(4 * stride + 3 * Hkv * d, dtype=torch.bfloat16, device=DEV)
+    q, k, v = (buf.as_strided((5, Hkv, d), (stride, d, 1), i * Hkv * d) for i in range(3))
+    for x in (q, k, v):
+        x.copy_(torch.randn(5, Hkv, d, generator=g, device=DEV))
+    last = n_pages * ps - 1
+    slots = torch.tensor([0, last, -1, last - 300, last + 1], device=DEV)
+    kc[-3:], vc[-3:] = 3.0, 3.0
+    f = ra.rope_freqs(d)[0]
+    pos = i32([5, 6, 7, 8, 9])
+    qo = ra.ra_paged_append(q, k, v, ra.rope_phases(f).to(DEV), kc, vc, slots, pos)
+    at, p = torch.tensor([0, 1, 3], device=DEV), np.array([5, 6, 8])
+    page, row = slots[at] // ps, slots[at] % ps
+    check_rope(qo[at], q[at], None, p, f.numpy())
+    check_rope(kc[page, row], k[at], None, p, f.numpy())
+    assert torch.equal(vc[page, row], v[at])
+    assert int((vc[-3:] != 3.0).any(-1).any(-1).sum()) == 2  # two rows written there, no other
+
+
+# ------------------------------------------------------------------ two callers
+
+def test_decode_from_two_threads():
+    cases = [make_decode([3000, 40, 900], [1] * 3, 32, 8, 128, 16, seed=1),
+             make_decode([2000, 700], [16] * 2, 8, 2, 128, 16, seed=2)]
+    want = [ra.ra_paged_decode(*c[:5]) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(30):
+                out, lse = ra.ra_paged_decode(*cases[i][:5])
+                st.synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    ra.ra_device_status()
+    assert not bad
 
 
 # ------------------------------------------------------------------ a capture first

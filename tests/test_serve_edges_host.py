@@ -3,6 +3,7 @@ a GPU."""
 import os
 import re
 
+import numpy as np
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
@@ -39,3 +40,32 @@ def test_the_fused_ring_decides_once_whether_it_runs():
     ring = ring[:ring.index("regs_dec")]
     assert "__syncthreads_or(launch_status)" in ring
     assert not re.search(r"(if|\|\||&&|while)[^;{]*[^&\w]\*abort_flag(?!\s*=[^=])", ring)
+
+
+# ------------------------------------------------------------------ the weights' bar
+
+def rounded(x):
+    """fp32 to bf16, to nearest even."""
+    u = x.astype(np.float32).view(np.uint32).astype(np.uint64)
+    return (((u + 0x7fff + ((u >> 16) & 1)) >> 16 << 16).astype(np.uint32)).view(np.float32)
+
+
+def cut(x):
+    return (x.astype(np.float32).view(np.uint32) & np.uint32(0xffff0000)).view(np.float32)
+
+
+@pytest.mark.parametrize("head", [rounded, cut])
+def test_the_bar_on_the_weights_sees_a_lost_term(head):
+    """The GPU test of the paged decode's weights (three live keys, scores in
+    [-1, 1], an output is one weight of their sum) refuses more than 32 u.
+    Three bf16 terms hold fp32's 24 bits; two miss the bar, at the fewest
+    rows that the test has (24 of three keys)."""
+    s = np.random.default_rng(0).uniform(-1, 1, (24, 3))
+    p = np.exp(s - s.max(1, keepdims=True)).astype(np.float32)
+    total, rest, err = np.zeros_like(p, dtype=np.float64), p, []
+    for _ in range(3):
+        h = head(rest)
+        total += h
+        rest = rest - h
+        err.append(np.abs(total / p - 1).max() * 2.0 ** 24)
+    assert err[0] > 1000 and err[1] > 2 * 32 and err[2] <= 1
