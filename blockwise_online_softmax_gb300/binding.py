@@ -592,15 +592,18 @@ def ra_paged_append(q, k, v, phases, k_cache, v_cache, slots, positions, *, q_we
         interleaved, mscale, q_out, stream)
 
 
-def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, window: int = 0,
-                    out=None, lse=None, stream=None):
+def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, n_q: int = 0,
+                    window: int = 0, out=None, lse=None, stream=None):
     """Attention of each request's newest tokens q [T, heads, d] (bf16) over
     its pages.  T / n_req rows per request, or rows [cu_q[i], cu_q[i + 1]) of
     request i (int32 [n_req + 1]); lengths (int32 [n_req]) include them.
+    With cu_q, n_q says how many rows a request should be expected to have
+    (0: T / n_req, the padding rows of a fixed-size step included): it picks
+    the kernel, not the result.
     Returns (out [T, heads, d], lse [T, heads]), fp32, in one allocation where
     not passed in; pass a bf16 `out` for that type."""
     return (_serve or _fast()).paged_decode(
-        q, k_cache, v_cache, block_table, lengths, cu_q, window, out, lse, stream)
+        q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream)
 
 
 def ra_ring_forward_noalloc(q, k, v, *, P: int, causal: bool, out=None, lse=None,

@@ -643,14 +643,20 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
 
 }  // namespace
 
-// Rows per request and KV head on average (exact when every request has the
-// same number of new tokens; with cu_q any mix is computed right, the average
-// only picks the kernel).  Rows past a tile read the pages again.  16-row tiles
-// against 128-row tiles, 32 rows: d = 128, 152 requests of 1K keys 185 / 142 us;
-// d = 64, the same 131 / 119, 64 of 2K keys 110 / 107, 64 of 500 41 / 44, 16 of
-// 300 17 / 20.  128 rows, d = 128, 152 requests of 1K keys: 707 / 166 us.
+// Rows per request and KV head: exact without cu_q; with it those that the
+// caller expects, or T / n_req, which counts padding rows too.  It picks the
+// kernel; any mix is computed right by each.  A request's rows past a tile read
+// its pages again, and a 128-row tile takes its time for fewer rows.  16-row tiles
+// against 128-row tiles, us, 8 KV heads, requests x keys, from HBM:
+//   d = 128      20 rows    40 rows        d = 64    20 rows    40 rows
+//   152 x 1K    189/140    303/144                  132/122    194/123
+//   64 x 2K     172/116    252/120                  108/102    155/105
+//   64 x 500   56.8/52.5  77.0/55.3                41.7/42.0  56.1/45.0
+//   16 x 300   20.8/21.4  24.1/23.4                17.0/19.1  19.5/21.2
+// (16 rows, d = 128: 113/139, d = 64: 74/121.)  At d = 64 up to 32 rows the border
+// leaves some 7% to the large works, for 4 to 19% of those below 35 us.
 int paged_row_tile(const PagedArgs& a, int d) {
-  const long long rows = (a.T + a.n_req - 1) / a.n_req * (a.heads / a.kv_heads);
+  const long long rows = a.n_q * (a.heads / a.kv_heads);
   return rows <= 8 ? 8 : (rows <= (d == 64 ? 32 : 16) ? 16 : 128);
 }
 

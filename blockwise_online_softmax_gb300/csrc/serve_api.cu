@@ -440,7 +440,7 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   a.out = out;
   a.lse = lse;
   a.T = T;
-  a.n_q = n_q < 1 ? 1 : n_q;
+  a.n_q = !cu_q || n_q > 0 ? n_q : (T + n_req - 1) / n_req;
   a.window = window > kMaxInt ? 0 : window;  // wider than any sequence
   a.out_bf16 = out_dtype == RA_BF16;
   a.n_req = n_req;

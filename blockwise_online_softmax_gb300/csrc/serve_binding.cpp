@@ -534,13 +534,14 @@ PyObject* append(PyObject* const* a) {
   return qo.release();
 }
 
-// q, k_cache, v_cache, block_table, lengths, cu_q, window, out, lse, stream
+// q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream
 PyObject* decode(PyObject* const* a) {
   const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
   const Tensor &tab = tensor(a[3], "block_table"), &len = tensor(a[4], "lengths");
   const Tensor* cu = maybe(a[5], "cu_q");
-  const long long window = integer(a[6]);
-  Out out(a[7], "out"), lse(a[8], "lse");
+  const int expect = small(a[6], "n_q");
+  const long long window = integer(a[7]);
+  Out out(a[8], "out"), lse(a[9], "lse");
   if (q.dim() != 3) refuse(PyExc_ValueError, "q: [T, heads, d]");
   if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache: [n_pages, page_size, kv_heads, d]");
   const int64_t n = len.numel(), T = q.size(0);
@@ -548,6 +549,9 @@ PyObject* decode(PyObject* const* a) {
   if (!cu && (n ? T % n != 0 : T != 0))
     refuse(PyExc_ValueError, "T=%lld rows are not a multiple of %lld requests (and cu_q is None)",
            static_cast<long long>(T), static_cast<long long>(n));
+  if (!cu && expect && expect * n != T)
+    refuse(PyExc_ValueError, "n_q=%d rows for each of %lld requests are not the %lld of q (and cu_q is None)", expect,
+           static_cast<long long>(n), static_cast<long long>(T));
   if (out.t) {
     if (out.t->sizes() != q.sizes())
       refuse(PyExc_ValueError, "out must have shape %s, got %s", shape_of(q).c_str(), shape_of(*out.t).c_str());
@@ -567,12 +571,12 @@ PyObject* decode(PyObject* const* a) {
   Block made;
   made.add(out, q.sizes(), ScalarType::Float);
   made.add(lse, {T, heads}, ScalarType::Float);
-  const Place at(dev, a[9]);
+  const Place at(dev, a[10]);
   made.make(at);
   const Tensor& to = *out.t;
   void* po = dense(to, "out", dev, to.scalar_type());
   auto* ps = static_cast<float*>(dense(*lse.t, "lse", dev, ScalarType::Float));
-  const int n_q = cu || !n ? 0 : to_int(T / n, "rows per request"), code = type_code(to.scalar_type());
+  const int n_q = cu ? expect : !n ? 0 : to_int(T / n, "rows per request"), code = type_code(to.scalar_type());
   call(at, [&](void* st) {
     return ra_paged_decode(pq, ck.p, cv.p, po, ps, T, tb.n_req, n_q, pc, tb.p, tb.width, pl, ck.pages, ck.page_size,
                            ck.stride, cv.stride, window, d, heads, kv_heads, RA_BF16, code, st);
@@ -595,7 +599,7 @@ RA_ENTRY(norm_rope_backward, 18)
 RA_ENTRY(extend, 14)
 RA_ENTRY(release, 9)
 RA_ENTRY(append, 15)
-RA_ENTRY(decode, 10)
+RA_ENTRY(decode, 11)
 #undef RA_ENTRY
 
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {

@@ -118,7 +118,7 @@ struct PagedArgs {
   void* out;               // [T, heads, d] fp32, or bf16 (out_bf16)
   float* lse;              // [T, heads]
   long long T;
-  long long n_q;
+  long long n_q;           // rows per request; with cu_q those to expect
   long long window;        // 0: none
   int out_bf16;
   int n_req;

@@ -381,6 +381,41 @@ def test_weight_gradients_keep_small_terms_beside_a_large_one(H, d):
     assert (dw[3] == T).all()
 
 
+# ------------------------------------------------------------------ rows to expect
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_padding_rows_do_not_pick_the_kernel(d):
+    """A fixed-size step with cu_q and the rows to expect gives the bits of the
+    call on its real rows, whatever the padding, and leaves that as it was."""
+    rows, extra = [1] * 16, 240
+    lengths = [int(x) for x in np.linspace(5, 900, 16)]
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, rows, 32, 8, d, 16, extra=extra)
+    want = ra.ra_paged_decode(q[:16], kc, vc, table, lens)
+    out, lse = torch.full(q.shape, 9.0, device=DEV), torch.full(q.shape[:2], 9.0, device=DEV)
+    ra.ra_paged_decode(q, kc, vc, table, lens, cu_q=i32(np.arange(17)), n_q=1, out=out, lse=lse)
+    assert torch.equal(out[:16], want[0]) and torch.equal(lse[:16], want[1])
+    assert (out[16:] == 9.0).all() and (lse[16:] == 9.0).all()
+
+
+@pytest.mark.parametrize("n_q", [0, 1, 3, 5, 40, 2**31 - 1])
+def test_rows_other_than_the_expected(n_q):
+    lengths, rows = [500, 77, 300, 1025, 9], [300, 2, 0, 1, 1]
+    q, kc, vc, table, lens, ks, vs = make_decode(lengths, rows, 8, 2, 128, 16)
+    cu = i32(np.concatenate([[0], np.cumsum(rows)]))
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, lens, cu_q=cu, n_q=n_q)
+    ra.ra_device_status()
+    check_decode(out, lse, q, ks, vs, rows)
+
+
+def test_rows_to_expect_without_cu_q_are_the_rows():
+    q, kc, vc, table, lens, ks, vs = make_decode([60, 20], [2, 2], 8, 2, 128, 16)
+    check_decode(*ra.ra_paged_decode(q, kc, vc, table, lens, n_q=2), q, ks, vs, [2, 2])
+    with pytest.raises(ValueError, match="n_q=3"):
+        ra.ra_paged_decode(q, kc, vc, table, lens, n_q=3)
+    with pytest.raises(binding.RaError, match="n_q=-1"):
+        ra.ra_paged_decode(q, kc, vc, table, lens, cu_q=i32([0, 2, 4]), n_q=-1)
+
+
 # ------------------------------------------------------------------ sizes past the others
 
 def test_decode_more_requests_than_threads_on_the_large_row_tile():
