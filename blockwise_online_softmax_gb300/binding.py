@@ -563,7 +563,8 @@ def ra_paged_extend(lengths, new_tokens, block_table, free_pages, free_count, *,
     returns (slots int64 [tokens], positions [tokens], cu_tokens [n_req + 1],
     lengths_out [n_req], free_count_out [1], status [3]).  lengths_out and
     free_count_out may be lengths and free_count themselves; outputs that are
-    not passed in share one allocation.  A nonzero status (pages missing,
+    not passed in are views of one allocation, which lives as long as any of
+    them.  A nonzero status (pages missing,
     rows too short, tokens beyond `tokens`) means that the step changed
     nothing."""
     return (_serve or _fast()).paged_extend(
@@ -575,7 +576,8 @@ def ra_paged_release(lengths, finished, block_table, free_pages, free_count, *, 
                      lengths_out=None, free_count_out=None, stream=None):
     """Push the pages of the requests with finished != 0 back on the stack
     free_pages (in place) and set their lengths to 0; returns (lengths_out,
-    free_count_out), which may be lengths and free_count themselves."""
+    free_count_out), which may be lengths and free_count themselves; where
+    neither is passed in, both are views of one allocation."""
     return (_serve or _fast()).paged_release(
         lengths, finished, block_table, free_pages, free_count, page_size, lengths_out,
         free_count_out, stream)
@@ -600,8 +602,9 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, n_q
     With cu_q, n_q says how many rows a request should be expected to have
     (0: T / n_req, the padding rows of a fixed-size step included): it picks
     the kernel, not the result.
-    Returns (out [T, heads, d], lse [T, heads]), fp32, in one allocation where
-    not passed in; pass a bf16 `out` for that type."""
+    Returns (out [T, heads, d], lse [T, heads]), fp32, views of one allocation
+    where not passed in (keeping the LSE keeps both: pass `lse` in, or clone
+    it); pass a bf16 `out` for that type."""
     return (_serve or _fast()).paged_decode(
         q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream)
 

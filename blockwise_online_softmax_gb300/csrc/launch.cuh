@@ -1,8 +1,9 @@
 // Launches of the serving kernels with programmatic dependence: a kernel may be
 // put on the SMs while the one in front of it in the stream still drains, and
-// waits for its end (wait_for_previous) before it touches global memory.  Each
-// of these kernels is a few microseconds, of which a full launch behind
-// another kernel is one or two.
+// waits for its end (wait_for_previous) before it touches global memory (but for
+// the decode kernels' status word, which only says that nothing more need be
+// done).  Each of these kernels is a few microseconds, of which a full launch
+// behind another kernel is one or two.
 #pragma once
 #include <cuda_runtime.h>
 

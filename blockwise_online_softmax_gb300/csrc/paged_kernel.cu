@@ -11,7 +11,8 @@
 // an item (request, row tile, KV head) costs besides its tiles, and every CTA
 // of a grid of two per SM takes an equal run of them, whatever the lengths are:
 // the lengths stay on the device.  (Without that unit the CTA with the short
-// requests ended last: 16 requests of up to 2K keys, 18.3 against 14.4 us.)  A
+// requests ended last: 16 requests of up to 2K keys, 18.3 against 14.4 us, one set
+// of pages over and over, so partly from L2; from HBM 16.1 now.)  A
 // CTA finds its run by a prefix sum over the requests.  An item that falls into
 // one CTA is finished there; one cut by a border between CTAs leaves a partial
 // state (m, l, O~) on each side, and a second launch joins them in CTA order.
@@ -55,7 +56,7 @@ struct Cfg {
   static constexpr int NCH = D / 64;
   static constexpr int RT = 8 * NT;              // query rows of an item
   // Registers of the two warpgroups; together the launch's 2 x 128.  (200 and
-  // 56 spill in the producers: 152 requests of 128 keys 19.3 against 18.5 us.)
+  // 56 spill in the producers: 152 requests of 128 keys, from L2, 19.3 against 18.5 us.)
   static constexpr int CONS_REGS = NT == 1 ? 152 : 192, PROD_REGS = 256 - CONS_REGS;
   static constexpr int ITEMS = NT == 1 ? 3 : 2;  // records and query tiles in flight
   static constexpr uint32_t TILE = BT * D * 2;
@@ -551,8 +552,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 // gridDim.y-th of its rows.  Its warps take every fourth partial, each with a
 // running maximum of its own, and meet in shared memory.  A short launch's time
 // is its chain of loads, so a warp's first partial is requested together with
-// the record that says whether there is one (16 requests of up to 2K keys, both
-// launches: 13.3 us; 14.1 with the record, the maxima and the partials in turn).
+// the record that says whether there is one (16 requests of up to 2K keys partly in
+// L2, both launches: 13.3 us; 14.1 with the record, the maxima and the partials in
+// turn; from HBM 16.1).
 constexpr int kJoin = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedArgs a, int RT) {

@@ -4,9 +4,10 @@
 // tiles of 128 and one CTA per SM.
 //
 // With rows this many the mma.sync form is bound by its products (each 8 rows
-// cost another 13 cycles per 16 x 16 block and SM quarter: 2.5 TB/s of pages
-// at 32 rows, 0.7 at 128); here a tile's products are 128 rows at once (4.6 TB/s
-// at 20 rows and at 128).
+// cost another 13 cycles per 16 x 16 block and SM quarter; 152 requests of 1K
+// keys, 8 KV heads, d = 128, 16-row tiles: 3.3 TB/s of pages at 20 and 32 rows,
+// 0.9 at 128); here a tile's products are 128 rows at once (4.5 TB/s at 20 rows,
+// 3.8 at 128; at d = 64, where a tile takes as long, 2.6 and 2.4).
 //
 // Roles of the 16 warps: 0-3 and 4-7 softmax, a thread has a row, the two groups
 // take a CTA's tiles in turn and hand the running maximum from one to the other;

@@ -162,16 +162,16 @@ struct Walk {
   }
 };
 
-// Prefix sum over the requests: every thread of the CTA gets the total, split
-// into runs of `size` or, the first `longer` of them, size + 1 units; the first
-// unit of the CTA's own is located as (request, offset).  With fewer units than
+// Prefix sum over the requests: every thread of the CTA learns how the total is cut
+// into runs of `size` or, the first `longer` of them, size + 1 units, and the first
+// unit of the CTA's own as (request, offset).  With fewer units than
 // CTAs only `ctas` of them work, so the CTAs of a cut item all hold a part of it.
 // `stop`: the abort flag as the CTA's thread 0 set it.  It is read between the
 // two barriers here: a wait may raise it as soon as a warp is past the second,
 // and warps that read it later could part ways, some leaving while the others
 // meet them at a barrier.
 struct Run {
-  long long total, first, last;
+  long long first, last;
   long long size;
   int longer, ctas;
   int r;
@@ -203,7 +203,6 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
     total += s_sum[w];
   }
   Run run;
-  run.total = total;
   run.stop = *abort_flag != 0;
   run.ctas = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
   run.first = run.last = total;

@@ -352,10 +352,10 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
 // Append: the same with k and v written to their pages.  Its calls are short,
 // so a token's first loads, of q, k and v, go out before its angles are
 // computed, its slot and position come with the token before, and k and v share
-// a batch of loads.  17K tokens of 12/4 heads, d = 64, without norm: 20.0 us as
-// the forward does it, 15.7 with q's loads and the slots early (80 registers),
-// 13.8 with the first group of k and v early too, at two CTAs per SM (in three
-// that spills: 16.9).  The forward done this way takes 0.5 us less of a call of
+// a batch of loads.  17K tokens of 12/4 heads, d = 64, without norm, partly from
+// L2: 20.0 us as the forward does it, 15.7 with q's loads and the slots early (80
+// registers), 13.8 with the first group of k and v early too, at two CTAs per SM
+// (in three that spills: 16.9); from HBM 17.8.  The forward done this way takes 0.5 us less of a call of
 // 300 tokens and 1.2 times as long over 60K of 32/8 heads, d = 128.
 constexpr int kAppendCtas = 2;  // per SM
 template <int D, bool INTER>
@@ -484,8 +484,7 @@ __device__ __forceinline__ float value(const float2& s) { return isfinite(s.x) ?
 // 1.7e-7 (4099 tokens of 8/8 heads: 2.2e-7, now 0.9e-7); that took 864 us
 // instead of 871, runs of 32 rows 873.  CUT: some tokens are taken in shares;
 // without it that arithmetic stays out, whose registers cost a long call 3%
-// (128K tokens of 32/8 heads, d = 128: 871 us, 0.92 of the copy bandwidth; 300
-// tokens 8.0, taken whole 12.2).
+// (128K tokens of 32/8 heads, d = 128: 871 us, 0.92 of the copy bandwidth).
 constexpr int kGradBatch = 3;
 constexpr int kRun = 64;
 constexpr int kGradCtas = 2;  // per SM
@@ -639,14 +638,16 @@ __global__ void __launch_bounds__(kSumWarps * 32) rope_weight_grad_kernel(const 
 
 // Tokens are taken whole, one warp each, in turns of all warps of the grid; the
 // rest of them, or all when there are few, by shares of their rows, a batch of
-// loads each or more, so that the last turn is not a few warps' long one.  32/8
-// heads, d = 128: forward of 8192 tokens 35.9 -> 32.0 us, 4096 19.2 -> 15.6;
-// gradient of 300 12.6 -> 7.8, 3000 35.3 -> 28.6; append of 1000 7.7 -> 6.1.  A
-// share computes the token's angles again, so the rest fills no more than one
-// turn (forward of 6000 tokens: 26.0, with more 26.8), but for few tokens in the
-// forward's three CTAs per SM, which come to some 16 warps per SM (2000 tokens:
-// 10.3; in one turn at most 11.6).  After more than eight turns the last is too
-// small a part of the call to matter.
+// loads each or more, so that the last turn is not a few warps' long one.  Whole
+// and in shares, us, 32/8 heads, d = 128, from HBM: forward of 300 tokens 9.4 and
+// 5.0, 2000 13.6 and 14.3, 4096 23.4 and 18.8, 8192 36.6 and 32.7, 20000 75.1 and
+// 71.8; gradient of 300 16.6 and 11.0, 1000 21.0 and 16.5, 3000 37.7 and 31.8,
+// 8192 70.9 and 70.0; append of 256 10.1 and 5.3, 1000 11.8 and 8.7, 8192 45.9 and
+// 42.9.  A share computes the token's angles again, so the rest fills no more than
+// one turn (forward of 6000 tokens, partly from L2: 26.0, with more 26.8), but for
+// few tokens in the forward's three CTAs per SM, which come to some 16 warps per SM
+// (2000 tokens so: 10.3; in one turn at most 11.6).  After more than eight turns
+// the last is too small a part of the call to matter.
 unsigned share(RopeArgs& a, int d, int ctas, int batch) {
   const int rpi = 256 / d, groups = (a.heads + rpi - 1) / rpi + (a.kv_heads + rpi - 1) / rpi;
   const long long warps = static_cast<long long>(ctas) * kWarps * sm_count();

@@ -430,10 +430,6 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   if ((rc = check_words({block_table, lengths}, 4)) != RA_OK) return rc;
   if (cu_q && !aligned(cu_q, 4)) return fail(RA_ERR_INVALID, "cu_q is not 4-byte aligned");
   a.q = q;
-  a.kc = k_cache;
-  a.vc = v_cache;
-  a.kc_page = k_page_stride;
-  a.vc_page = v_page_stride;
   a.block_table = block_table;
   a.lengths = lengths;
   a.cu_q = cu_q;

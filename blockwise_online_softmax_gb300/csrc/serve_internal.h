@@ -109,9 +109,6 @@ cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_
 // ------------------------------------------------------------------ paged decode
 struct PagedArgs {
   const void* q;   // [T, heads, d] bf16
-  const void* kc;  // [n_pages, page_size, kv_heads, d] bf16
-  const void* vc;
-  long long kc_page, vc_page;
   const int* block_table;  // [n_req, max_pages]
   const int* lengths;      // [n_req], the new tokens included
   const int* cu_q;         // [n_req + 1], or null: n_q rows per request

@@ -582,13 +582,14 @@ int ra_selftest_wait_timeout(long long limit_cycles, void* stream);
  * Cached scratch memory.  Every buffer the library allocates for itself
  * (the l state of ra_ring_forward on the step path, the device staging of
  * ra_ring_forward_host, the D vector of the backward, the partial states of
- * decode) comes, stream-ordered, from a memory pool that the library
- * creates on each device at first use (which may be inside a stream
- * capture).  The pool keeps what is freed into
- * it mapped, so the next call of the same size maps nothing: a call that
- * needs a few GB of staging does not pay milliseconds for a fresh mapping.
- * Ownership stays with the library, and what the pool holds is bounded by
- * the largest set of buffers one call (or concurrent calls) held.
+ * the decodes, the partial weight gradients of the rotary backward, the sums
+ * of a large page step) comes, stream-ordered, from a memory pool that the
+ * library creates on each device at first use, which may be inside a stream
+ * capture.  The pool keeps what is freed into it mapped, so the next call of
+ * the same size maps nothing: a call that needs a few GB of staging does not
+ * pay milliseconds for a fresh mapping.  Ownership stays with the library,
+ * and what the pool holds is bounded by the largest set of buffers one call
+ * (or concurrent calls) held.
  *
  * ra_cached_memory -- write to *bytes the memory the current device's pool
  *   holds (in use or cached); 0 before any allocation.  RA_ERR_INVALID if
