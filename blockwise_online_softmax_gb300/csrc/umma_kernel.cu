@@ -978,15 +978,17 @@ umma_ring_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   // before the roles split the registers.
   StepVisit* rec = reinterpret_cast<StepVisit*>(smem + C::OFF_MISC + 16);
   for (int s = tid; s < a.P; s += NTHREADS) rec[s] = step_visit(a, i, s, row0, vb);
-  if (tid == 0) *abort_flag = launch_status != 0 ? 1 : 0;
+  // The early return goes by a word of its own: a warp that read the flag behind
+  // the barrier could find it raised by a faster warp's first wait, and leave
+  // alone.  (A barrier that carries the decision costs the long forward 0.3%.)
+  volatile int* stop = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  if (tid == 0) *abort_flag = *stop = launch_status != 0 ? 1 : 0;
   tc_fence_before();
-  // The barrier carries the decision: a warp that read the flag behind it
-  // could find it raised by a faster warp's first wait, and leave alone.
-  const bool stop = __syncthreads_or(launch_status) != 0;
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool no_keys = next_step(rec, a.P, 0) == a.P;
-  if (no_keys || stop) {  // uniform across the CTA
+  if (no_keys || *stop) {  // uniform across the CTA
     // Rows that see no key anywhere: O = 0 and LSE = -inf, and no pipeline.
     if (no_keys && tid < NQ * BM) {
       const long long grow = row0 + tid;

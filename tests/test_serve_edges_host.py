@@ -32,13 +32,13 @@ def test_a_cta_decides_once_whether_it_runs(name):
 
 
 def test_the_fused_ring_decides_once_whether_it_runs():
-    """The same in the fused ring forward, where the barrier in front of the
-    roles carries the decision.  (The other kernels read the flag between two
+    """The same in the fused ring forward, where the decision has a word of its
+    own that no wait writes.  (The other kernels read the flag between two
     barriers.)"""
     code = source("umma_kernel.cu")
     ring = code[code.index("umma_ring_kernel(const __grid_constant__"):]
     ring = ring[:ring.index("regs_dec")]
-    assert "__syncthreads_or(launch_status)" in ring
+    assert re.search(r"if \(no_keys \|\| \*stop\)", ring) and ring.count("*stop =") == 1
     assert not re.search(r"(if|\|\||&&|while)[^;{]*[^&\w]\*abort_flag(?!\s*=[^=])", ring)
 
 
