@@ -504,6 +504,77 @@ def test_append_offsets_past_32_bits():
     assert int((vc[-3:] != 3.0).any(-1).any(-1).sum()) == 2  # two rows written there, no other
 
 
+@pytest.mark.parametrize("n_q, H, Hkv, d", [(1, 4, 1, 64), (40, 4, 1, 64), (1, 4, 1, 128)])
+def test_decode_at_the_longest_history(n_q, H, Hkv, d):
+    """2^31 - 256 keys, the stated limit, as one page of the cache over and
+    over.  With q = 0 every weight is 1 and V of 0 and 1 sums exactly inside a
+    CTA (below 2^24); up to 304 partials and a warp's states join in fp32, a
+    rounding each, and the LSE is that of the count.  Rows of a request see
+    one key more each, which changes a mean by less than 2^-30."""
+    ps, max_pages = 256, (1 << 23) - 1
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kc = torch.randn(1, ps, Hkv, d, generator=g, device=DEV).bfloat16()
+    vc = torch.randint(0, 2, (1, ps, Hkv, d), generator=g, device=DEV).bfloat16()
+    table = torch.zeros(1, max_pages, dtype=torch.int32, device=DEV)
+    q = torch.zeros(n_q, H, d, dtype=torch.bfloat16, device=DEV)
+    out, lse = ra.ra_paged_decode(q, kc, vc, table, i32([max_pages * ps]))
+    ra.ra_device_status()
+    want = vc[0].double().mean(0)  # [Hkv, d], every page the same
+    assert ((out.double() - want.repeat_interleave(H // Hkv, 0)).abs() <= 320 * U).all()
+    assert (lse.double() - math.log(max_pages * ps)).abs().max().item() <= 320 * U + 2 * U * 22
+
+
+def test_window_wider_than_any_history():
+    q, kc, vc, table, lens, ks, vs = make_decode([300, 7], [2, 2], 8, 2, 128, 16)
+    want = ra.ra_paged_decode(q, kc, vc, table, lens)
+    for w in (2**31 - 1, 2**31, 2**62):
+        got = ra.ra_paged_decode(q, kc, vc, table, lens, window=w)
+        assert same(got, want)
+
+
+def test_pages_out_of_range_stay_with_their_request():
+    """A table entry that is no page, inside a request's length: that request's
+    result is undefined, the others' are not, and nothing else is read."""
+    for n_q, H in ((1, 8), (5, 32)):
+        q, kc, vc, table, lens, ks, vs = make_decode([300, 700, 64], [n_q] * 3, H, 2, 128, 16)
+        table[1, ::2] = torch.tensor([-1, 2**30, -2**31, kc.shape[0]], dtype=torch.int32,
+                                     device=DEV).repeat(table.shape[1])[:table[1, ::2].numel()]
+        out, lse = ra.ra_paged_decode(q, kc, vc, table, lens)
+        ra.ra_device_status()
+        for i in (0, 2):
+            rows = slice(i * n_q, (i + 1) * n_q)
+            check_decode(out[rows], lse[rows], q[rows], ks[i:i + 1], vs[i:i + 1], [n_q])
+
+
+def test_extend_and_release_without_a_page_in_the_stack():
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    table = i32([[5, -1], [6, -1]])
+    slots, _, cu, ln, count, status = ra.ra_paged_extend(
+        i32([3, 0]), i32([2, 1]), table, none, i32([0]), page_size=8, tokens=3)
+    assert status.tolist() == [1, 0, 0] and slots.tolist() == [-1] * 3 and ln.tolist() == [3, 0]
+    slots, pos, cu, ln, count, status = ra.ra_paged_extend(
+        i32([3, 0]), i32([2, 0]), table, none, i32([0]), page_size=8, tokens=3)
+    assert status.tolist() == [0, 0, 0] and slots.tolist() == [43, 44, -1] and cu.tolist() == [0, 2, 2]
+    ln, count = ra.ra_paged_release(ln, i32([1, 0]), table, none, i32([0]), page_size=8)
+    assert ln.tolist() == [0, 0] and count.tolist() == [0]
+
+
+def test_append_in_place():
+    """q_out may be q where that is dense; padding rows of it stay as they are."""
+    g = torch.Generator().manual_seed(9)
+    T, H, Hkv, d = 50, 8, 2, 128
+    q, k, v = (torch.randn(T, h, d, generator=g).bfloat16().to(DEV) for h in (H, Hkv, Hkv))
+    kc, vc = (torch.zeros(8, 16, Hkv, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    slots = torch.randperm(128, generator=g)[:T].to(DEV)
+    slots[::7] = -1
+    ph, w = ra.rope_phases(ra.rope_freqs(d)[0]).to(DEV), torch.linspace(0.5, 2.0, d, device=DEV)
+    want = ra.ra_paged_append(q, k, v, ph, kc, vc, slots, i32(np.arange(T)), q_weight=w,
+                              q_out=q.clone())
+    old = q.clone()
+    got = ra.ra_paged_append(q, k, v, ph, kc, vc, slots, i32(np.arange(T)), q_weight=w, q_out=q)
+    assert got is q and torch.equal(q, want) and torch.equal(q[::7], old[::7])
+
+
 # ------------------------------------------------------------------ two callers
 
 def test_decode_from_two_threads():
