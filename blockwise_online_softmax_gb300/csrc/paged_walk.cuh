@@ -162,10 +162,10 @@ struct Walk {
   }
 };
 
-// Prefix sum over the requests: every thread of the CTA learns how the total is cut
-// into runs of `size` or, the first `longer` of them, size + 1 units, and the first
-// unit of the CTA's own as (request, offset).  With fewer units than
-// CTAs only `ctas` of them work, so the CTAs of a cut item all hold a part of it.
+// Prefix sum over the requests: every thread of the CTA learns how the total is
+// cut into runs of `size` or, the first `longer` of them, size + 1 units, and the
+// first unit of the CTA's own as (request, offset).  With fewer units than CTAs
+// only `ctas` of them work, so the CTAs of a cut item all hold a part of it.
 // `stop`: the abort flag as the CTA's thread 0 set it.  It is read between the
 // two barriers here: a wait may raise it as soon as a warp is past the second,
 // and warps that read it later could part ways, some leaving while the others
