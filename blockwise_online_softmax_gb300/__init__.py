@@ -19,8 +19,10 @@ from .binding import (  # noqa: E402,F401
     ra_finalize,
     ra_merge,
     ra_paged_append,
+    ra_paged_append_fp8,
     ra_paged_decode,
     ra_paged_extend,
+    ra_paged_read_fp8,
     ra_paged_release,
     ra_qk_norm_rope,
     ra_qk_norm_rope_backward,

@@ -49,6 +49,8 @@ KERNEL_KINDS = {
     "paged_append": 17,
     "paged_decode": 18,
     "paged_combine": 19,
+    "paged_append_fp8": 20,
+    "paged_read_fp8": 21,
 }
 
 _lock = threading.Lock()
@@ -84,6 +86,8 @@ _SIGNATURES = {
     "ra_paged_release": ("PPiPiPiPiPPP", "i"),
     "ra_paged_append": ("PPPPPPLiiiLLLiiLLPPiiPfPPifiP", "i"),
     "ra_paged_decode": ("PPPPPLiiPPiPiiLLLiiiiiP", "i"),
+    "ra_paged_append_fp8": ("PPPPPPPPLiiiLLLiiLLLLPPiiPfPPifiP", "i"),
+    "ra_paged_read_fp8": ("PPPPPPLiPPiPiiLLLLiiP", "i"),
     "ra_device_status": ("P", "i"),
     "ra_selftest_wait_timeout": ("LP", "i"),
     "ra_cached_memory": ("P", "i"),
@@ -607,6 +611,33 @@ def ra_paged_decode(q, k_cache, v_cache, block_table, lengths, *, cu_q=None, n_q
     it); pass a bf16 `out` for that type."""
     return (_serve or _fast()).paged_decode(
         q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream)
+
+
+def ra_paged_append_fp8(q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slots, positions, *,
+                        q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, mscale: float = 1.0, q_out=None, stream=None):
+    """ra_paged_append with k and v held in 8 bits: k_cache, v_cache [n_pages,
+    page_size, kv_heads, d] float8_e4m3fn, k_scale, v_scale [n_pages, kv_heads,
+    page_size] float8_e8m0fnu.  A row of d entries has one scale, the least
+    power of two with max |x| <= 448 scales, and its codes are x / scale to
+    nearest.  page_size 16 to 256.  Returns q_out (bf16), dense like q."""
+    return (_serve or _fast()).paged_append_fp8(
+        q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slots, positions, q_weight, k_weight,
+        eps, interleaved, mscale, q_out, stream)
+
+
+def ra_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_k, *,
+                      tokens: int, k_out=None, v_out=None, stream=None):
+    """Pages in 8 bits read back: (k_out, v_out), bf16 [tokens, kv_heads, d],
+    with the newest cu_k[i + 1] - cu_k[i] tokens of request i in rows
+    [cu_k[i], cu_k[i + 1]) (cu_k int32 [n_req + 1]; the prefix sums of lengths
+    give whole histories).  Exact.  Rows that belong to no request are left as
+    they were (in outputs that are not passed in: undefined), rows before a
+    request's first token are zero.  The rows are what ra_decode_forward and
+    the ring calls take, for instance for the next chunk of a long prompt."""
+    return (_serve or _fast()).paged_read_fp8(
+        k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_k, tokens, k_out, v_out,
+        stream)
 
 
 def ra_ring_forward_noalloc(q, k, v, *, P: int, causal: bool, out=None, lse=None,

@@ -19,9 +19,11 @@
 // that; 0.8 us of the 442 below).  Sums, the norm and the rotation are fp32; the
 // one rounding to bf16 is at the store.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
+#include "fp8.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
 #include "serve_internal.h"
@@ -321,12 +323,12 @@ __device__ __forceinline__ void fold(const RopeArgs& a, const Rot<D, INTER>& rot
   }
 }
 
-// The rows of one group, normed and turned, to dst.
+// The rows of one group, normed and turned.
 template <typename T, int D, bool INTER>
-__device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, bool norm, float eps,
-                                     const uint64_t (&cw)[4], const uint64_t (&sw)[4], bool valid, T* dst) {
+__device__ __forceinline__ void turned(const Rot<D, INTER>& rot, const Vec<T>& v, bool norm, float eps,
+                                       const uint64_t (&cw)[4], const uint64_t (&sw)[4], float (&x)[8]) {
   constexpr int LPR = D / 8;
-  float x[8], p[8];
+  float p[8];
   v.get(x);
   partner_row(rot, v, x, p);
   uint64_t x2[4];
@@ -346,7 +348,33 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
   for (int e = 0; e < 4; ++e)
     f2unpack(fmul2(r2, ffma2(f2pack(p[2 * e], p[2 * e + 1]), sw[e], fmul2(x2[e], cw[e]))), x[2 * e],
              x[2 * e + 1]);
+}
+// The same to dst.
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, bool norm, float eps,
+                                     const uint64_t (&cw)[4], const uint64_t (&sw)[4], bool valid, T* dst) {
+  float x[8];
+  turned(rot, v, norm, eps, cw, sw, x);
   if (valid) Vec<T>::store(dst, x);
+}
+
+// A row of which each of its LPR lanes has eight columns, to 8 bits: codes to
+// dst, the scale, by the row's first lane, to scale.
+template <int LPR>
+__device__ __forceinline__ void put_codes(const float (&x)[8], bool valid, uint8_t* dst, uint8_t* scale) {
+  unsigned top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, finite_bits(x[e]));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+  const int byte = scale_byte(top);
+  const float inv = inverse_scale(byte);
+  if (!valid) return;
+  uint2 w;
+  w.x = codes2(x[0], x[1], inv) | codes2(x[2], x[3], inv) << 16;
+  w.y = codes2(x[4], x[5], inv) | codes2(x[6], x[7], inv) << 16;
+  *reinterpret_cast<uint2*>(dst) = w;
+  if (threadIdx.x % LPR == 0) *scale = static_cast<uint8_t>(byte);
 }
 
 // Append: the same with k and v written to their pages.  Its calls are short,
@@ -358,7 +386,11 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
 // (in three that spills: 16.9); from HBM 17.8.  The forward done this way takes 0.5 us less of a call of
 // 300 tokens and 1.2 times as long over 60K of 32/8 heads, d = 128.
 constexpr int kAppendCtas = 2;  // per SM
-template <int D, bool INTER>
+//
+// FP8: k and v in 8 bits (fp8.cuh), from the fp32 values, so rounded once.  The
+// maximum of a row costs an exchange per halving of its lanes, no pass over
+// memory.
+template <int D, bool INTER, bool FP8>
 __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(const RopeArgs a) {
   let_next_start();
   wait_for_previous();
@@ -433,10 +465,26 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
         fold(a, rot, a.kw, col, cw, sw);
         const long long page = slot >> a.page_shift;
         const long long in = (slot & ((1LL << a.page_shift) - 1)) * a.kv_heads * D + off;
-        T* const kdst = static_cast<T*>(a.kc) + page * a.kc_page + in;
-        T* const vdst = static_cast<T*>(a.vc) + page * a.vc_page + in;
-        if (k0 * RPI + sub < a.kv_heads) v_raw.put(vdst + k0 * RPI * D);
-        turn(rot, k_raw, a.kw != nullptr, a.eps, cw, sw, k0 * RPI + sub < a.kv_heads, kdst + k0 * RPI * D);
+        using Held = std::conditional_t<FP8, uint8_t, T>;
+        Held* const kdst = static_cast<Held*>(a.kc) + page * a.kc_page + in;
+        Held* const vdst = static_cast<Held*>(a.vc) + page * a.vc_page + in;
+        // Group g of k and v, as loaded, to the page.
+        auto write = [&](const Vec<T>& kr, const Vec<T>& vr, int g) {
+          const int h = g * RPI + sub;
+          const bool valid = h < a.kv_heads;
+          if constexpr (FP8) {
+            const long long at = (static_cast<long long>(h) << a.page_shift) + (slot & ((1LL << a.page_shift) - 1));
+            float x[8];
+            vr.get(x);
+            put_codes<LPR>(x, valid, vdst + g * RPI * D, static_cast<uint8_t*>(a.vs) + page * a.vs_page + at);
+            turned(rot, kr, a.kw != nullptr, a.eps, cw, sw, x);
+            put_codes<LPR>(x, valid, kdst + g * RPI * D, static_cast<uint8_t*>(a.ks) + page * a.ks_page + at);
+          } else {
+            turn(rot, kr, a.kw != nullptr, a.eps, cw, sw, valid, kdst + g * RPI * D);
+            if (valid) vr.put(vdst + g * RPI * D);
+          }
+        };
+        write(k_raw, v_raw, k0);
         for (int g = k0 + 1; g < k1; g += N) {
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -446,9 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(c
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             if (g + j >= k1) break;
-            const bool valid = (g + j) * RPI + sub < a.kv_heads;
-            turn(rot, raw[j], a.kw != nullptr, a.eps, cw, sw, valid, kdst + (g + j) * RPI * D);
-            if (valid) raw[N + j].put(vdst + (g + j) * RPI * D);
+            write(raw[j], raw[N + j], g + j);
           }
         }
       }
@@ -686,12 +732,16 @@ cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_
   return bf16 ? forward_t<__nv_bfloat16>(a, d, st) : forward_t<float>(a, d, st);
 }
 
-cudaError_t launch_rope_append(const RopeArgs& args, int d, cudaStream_t st) {
+cudaError_t launch_rope_append(const RopeArgs& args, int d, bool fp8, cudaStream_t st) {
   RopeArgs a = args;
   if (a.T == 0) return cudaSuccess;
   const unsigned grid = share(a, d, kAppendCtas, kBatch);
-  auto* kernel = d == 128 ? (a.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
-                         : (a.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
+  auto pick = [&](auto f8) {
+    constexpr bool F = decltype(f8)::value;
+    return d == 128 ? (a.interleaved ? rope_append_kernel<128, true, F> : rope_append_kernel<128, false, F>)
+                    : (a.interleaved ? rope_append_kernel<64, true, F> : rope_append_kernel<64, false, F>);
+  };
+  auto* kernel = fp8 ? pick(std::true_type{}) : pick(std::false_type{});
   return launch_early(kernel, dim3(grid), kWarps * 32, 0, st, a);
 }
 

@@ -76,6 +76,24 @@ int check_cache(const char* name, long long stride, long long page_elems) {
   return RA_OK;
 }
 
+// The same of pages in 8 bits and of their scales: strides in bytes.
+int check_cache_fp8(const char* name, long long stride, long long page_bytes) {
+  if (stride < page_bytes)
+    return fail(RA_ERR_INVALID, "%s=%lld is less than a page's %lld bytes", name, stride, page_bytes);
+  if (stride % 16 != 0) return fail(RA_ERR_INVALID, "%s=%lld is not a multiple of 16 bytes", name, stride);
+  return RA_OK;
+}
+int check_pages_fp8(int page_size, int kv_heads, int d, long long k_page, long long v_page, long long k_scale,
+                    long long v_scale) {
+  if (page_size < 16) return fail(RA_ERR_UNSUPPORTED, "page_size=%d (pages in 8 bits: 16, 32, 64, 128, 256)", page_size);
+  const long long rows = static_cast<long long>(page_size) * kv_heads;
+  int rc;
+  if ((rc = check_cache_fp8("k_page_stride", k_page, rows * d)) != RA_OK) return rc;
+  if ((rc = check_cache_fp8("v_page_stride", v_page, rows * d)) != RA_OK) return rc;
+  if ((rc = check_cache_fp8("k_scale_stride", k_scale, rows)) != RA_OK) return rc;
+  return check_cache_fp8("v_scale_stride", v_scale, rows);
+}
+
 int check_stride(const char* name, long long stride, long long row, int dtype) {
   const int unit = dtype == RA_BF16 ? 8 : 4;  // 16 bytes
   if (stride < row) return fail(RA_ERR_INVALID, "%s=%lld is less than a token's %lld elements", name, stride, row);
@@ -148,6 +166,48 @@ int rope_layout(ra::RopeArgs& a, const int* positions, int layout, int P) {
   a.P = P;
   a.c = a.T / P;
   return RA_OK;
+}
+
+// ra_paged_append and its form in 8 bits: what they share.  The strides of the
+// pages have been checked.
+int append_common(ra::RopeArgs& a, bool fp8, const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                  void* v_cache, long long T, int d, int heads, int kv_heads, long long q_stride, long long k_stride,
+                  long long v_stride, int n_pages, int page_size, long long k_page_stride, long long v_page_stride,
+                  const long long* slots, const int* positions, void* stream) {
+  int rc;
+  const long long krow = static_cast<long long>(kv_heads) * d;
+  if ((rc = check_stride("q_stride", q_stride, static_cast<long long>(heads) * d, RA_BF16)) != RA_OK) return rc;
+  if ((rc = check_stride("k_stride", k_stride, krow, RA_BF16)) != RA_OK) return rc;
+  if ((rc = check_stride("v_stride", v_stride, krow, RA_BF16)) != RA_OK) return rc;
+  if (T == 0) return RA_OK;
+  if ((rc = check_ptrs({q, k, v, q_out})) != RA_OK) return rc;
+  if (n_pages > 0 && (rc = check_ptrs({k_cache, v_cache})) != RA_OK) return rc;
+  if (n_pages > 0 && fp8 && (rc = check_ptrs({a.ks, a.vs})) != RA_OK) return rc;
+  if ((rc = check_words({slots}, 8)) != RA_OK) return rc;
+  if ((rc = check_words({positions}, 4)) != RA_OK) return rc;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_str = q_stride;
+  a.k_str = k_stride;
+  a.v_str = v_stride;
+  a.qo = q_out;
+  a.qo_str = static_cast<long long>(heads) * d;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.kc_page = k_page_stride;
+  a.vc_page = v_page_stride;
+  a.n_slots = static_cast<long long>(n_pages) * page_size;
+  a.slots = slots;
+  a.positions = positions;
+  a.layout = RA_LAYOUT_CONTIGUOUS;
+  a.P = 1;
+  a.c = T;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  TraceScope ts(fp8 ? RA_KERNEL_PAGED_APPEND_FP8 : RA_KERNEL_PAGED_APPEND, st);
+  cudaError_t e = ra::launch_rope_append(a, d, fp8, st);
+  ts.done(e == cudaSuccess);
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-append launch");
 }
 
 }  // namespace
@@ -364,40 +424,78 @@ int ra_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
   if (dtype != RA_BF16) return fail(RA_ERR_UNSUPPORTED, "the paged cache takes bf16 q, k, v");
   if ((rc = page_shift(page_size, &a.page_shift)) != RA_OK) return rc;
   if (n_pages < 0) return fail(RA_ERR_INVALID, "n_pages=%d is negative", n_pages);
-  const long long krow = static_cast<long long>(kv_heads) * d;
-  if ((rc = check_stride("q_stride", q_stride, static_cast<long long>(heads) * d, dtype)) != RA_OK) return rc;
-  if ((rc = check_stride("k_stride", k_stride, krow, dtype)) != RA_OK) return rc;
-  if ((rc = check_stride("v_stride", v_stride, krow, dtype)) != RA_OK) return rc;
-  if ((rc = check_cache("k_page_stride", k_page_stride, krow * page_size)) != RA_OK) return rc;
-  if ((rc = check_cache("v_page_stride", v_page_stride, krow * page_size)) != RA_OK) return rc;
-  if (T == 0) return RA_OK;
-  if ((rc = check_ptrs({q, k, v, q_out})) != RA_OK) return rc;
-  if (n_pages > 0 && (rc = check_ptrs({k_cache, v_cache})) != RA_OK) return rc;
-  if ((rc = check_words({slots}, 8)) != RA_OK) return rc;
-  if ((rc = check_words({positions}, 4)) != RA_OK) return rc;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_str = q_stride;
-  a.k_str = k_stride;
-  a.v_str = v_stride;
-  a.qo = q_out;
-  a.qo_str = static_cast<long long>(heads) * d;
-  a.kc = k_cache;
-  a.vc = v_cache;
+  const long long page_elems = static_cast<long long>(kv_heads) * d * page_size;
+  if ((rc = check_cache("k_page_stride", k_page_stride, page_elems)) != RA_OK) return rc;
+  if ((rc = check_cache("v_page_stride", v_page_stride, page_elems)) != RA_OK) return rc;
+  return append_common(a, false, q, k, v, q_out, k_cache, v_cache, T, d, heads, kv_heads, q_stride, k_stride, v_stride,
+                       n_pages, page_size, k_page_stride, v_page_stride, slots, positions, stream);
+}
+
+int ra_paged_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                        void* v_cache, void* k_scale, void* v_scale, long long T, int d, int heads,
+                        int kv_heads, long long q_stride, long long k_stride, long long v_stride,
+                        int n_pages, int page_size, long long k_page_stride,
+                        long long v_page_stride, long long k_scale_stride,
+                        long long v_scale_stride, const long long* slots, const int* positions,
+                        int rot_dim, int interleaved, const void* phases, float mscale,
+                        const void* q_weight, const void* k_weight, int w_dtype, float eps,
+                        int dtype, void* stream) {
+  ra::RopeArgs a{};
+  int rc = rope_common(a, T, d, heads, kv_heads, dtype, rot_dim, interleaved, phases, q_weight,
+                       k_weight, w_dtype, eps, mscale);
+  if (rc != RA_OK) return rc;
+  if (dtype != RA_BF16) return fail(RA_ERR_UNSUPPORTED, "the paged cache takes bf16 q, k, v");
+  if ((rc = page_shift(page_size, &a.page_shift)) != RA_OK) return rc;
+  if (n_pages < 0) return fail(RA_ERR_INVALID, "n_pages=%d is negative", n_pages);
+  if ((rc = check_pages_fp8(page_size, kv_heads, d, k_page_stride, v_page_stride, k_scale_stride, v_scale_stride)) != RA_OK) return rc;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.ks_page = k_scale_stride;
+  a.vs_page = v_scale_stride;
+  return append_common(a, true, q, k, v, q_out, k_cache, v_cache, T, d, heads, kv_heads, q_stride, k_stride, v_stride,
+                       n_pages, page_size, k_page_stride, v_page_stride, slots, positions, stream);
+}
+
+int ra_paged_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, void* k_out, void* v_out, long long tokens, int n_req,
+                      const int* cu_k, const int* block_table, int max_pages, const int* lengths,
+                      int n_pages, int page_size, long long k_page_stride, long long v_page_stride,
+                      long long k_scale_stride, long long v_scale_stride, int d, int kv_heads,
+                      void* stream) {
+  ra::ReadArgs a{};
+  int rc;
+  if ((rc = check_common(d, kv_heads, RA_BF16)) != RA_OK) return rc;
+  if ((rc = check_table(n_req, max_pages, page_size, &a.page_shift)) != RA_OK) return rc;
+  if (n_pages < 0) return fail(RA_ERR_INVALID, "n_pages=%d is negative", n_pages);
+  if (tokens < 0 || tokens > kMaxInt) return fail(RA_ERR_INVALID, "tokens=%lld out of range [0, 2^31 - 1]", tokens);
+  if ((rc = check_pages_fp8(page_size, kv_heads, d, k_page_stride, v_page_stride, k_scale_stride, v_scale_stride)) != RA_OK) return rc;
+  if (tokens == 0 || n_req == 0) return RA_OK;
+  if ((rc = check_ptrs({k_out, v_out})) != RA_OK) return rc;
+  if (n_pages > 0 && (rc = check_ptrs({k_cache, v_cache, k_scale, v_scale})) != RA_OK) return rc;
+  if ((rc = check_words({cu_k, block_table, lengths}, 4)) != RA_OK) return rc;
+  a.kc = static_cast<const uint8_t*>(k_cache);
+  a.vc = static_cast<const uint8_t*>(v_cache);
+  a.ks = static_cast<const uint8_t*>(k_scale);
+  a.vs = static_cast<const uint8_t*>(v_scale);
   a.kc_page = k_page_stride;
   a.vc_page = v_page_stride;
-  a.n_slots = static_cast<long long>(n_pages) * page_size;
-  a.slots = slots;
-  a.positions = positions;
-  a.layout = RA_LAYOUT_CONTIGUOUS;
-  a.P = 1;
-  a.c = T;
+  a.ks_page = k_scale_stride;
+  a.vs_page = v_scale_stride;
+  a.ko = k_out;
+  a.vo = v_out;
+  a.block_table = block_table;
+  a.lengths = lengths;
+  a.cu = cu_k;
+  a.tokens = tokens;
+  a.n_req = n_req;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.kv_heads = kv_heads;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  TraceScope ts(RA_KERNEL_PAGED_APPEND, st);
-  cudaError_t e = ra::launch_rope_append(a, d, st);
+  TraceScope ts(RA_KERNEL_PAGED_READ_FP8, st);
+  cudaError_t e = ra::launch_paged_read(a, d, st);
   ts.done(e == cudaSuccess);
-  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-append launch");
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "paged-read launch");
 }
 
 int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,

@@ -52,6 +52,8 @@ const char* type_name(ScalarType t) {
     case ScalarType::BFloat16: return "torch.bfloat16";
     case ScalarType::Int: return "torch.int32";
     case ScalarType::Long: return "torch.int64";
+    case ScalarType::Float8_e4m3fn: return "torch.float8_e4m3fn";
+    case ScalarType::Float8_e8m0fnu: return "torch.float8_e8m0fnu";
     default: return c10::toString(t);
   }
 }
@@ -200,8 +202,8 @@ struct Cache {
   int pages, page_size;
   int64_t stride;
 };
-Cache cache(const Tensor& t, const char* name, int kv_heads, int d, int dev) {
-  placed(t, name, dev, ScalarType::BFloat16);
+Cache cache(const Tensor& t, const char* name, int kv_heads, int d, int dev, ScalarType type = ScalarType::BFloat16) {
+  placed(t, name, dev, type);
   if (t.dim() != 4 || t.size(2) != kv_heads || t.size(3) != d)
     refuse(PyExc_ValueError, "%s must be [n_pages, page_size, %d, %d], got %s", name, kv_heads, d, shape_of(t).c_str());
   const int64_t n = t.size(0), ps = t.size(1), row = static_cast<int64_t>(kv_heads) * d;
@@ -214,6 +216,36 @@ Cache cache(const Tensor& t, const char* name, int kv_heads, int d, int dev) {
 void same_pages(const Cache& k, const Cache& v) {
   if (k.pages != v.pages || k.page_size != v.page_size)
     refuse(PyExc_ValueError, "k_cache and v_cache must match in pages and page size");
+}
+
+// The scales [n_pages, kv_heads, page_size] of pages in 8 bits.
+struct Scales {
+  void* p;
+  int64_t stride;
+};
+Scales scales(const Tensor& t, const char* name, const Cache& c, int kv_heads, int dev) {
+  placed(t, name, dev, ScalarType::Float8_e8m0fnu);
+  if (t.dim() != 3 || t.size(0) != c.pages || t.size(1) != kv_heads || t.size(2) != c.page_size)
+    refuse(PyExc_ValueError, "%s must be [%d, %d, %d] (pages, KV heads, page size), got %s", name, c.pages, kv_heads,
+           c.page_size, shape_of(t).c_str());
+  const int64_t n = c.pages, ps = c.page_size;
+  if (n && ((ps > 1 && t.stride(2) != 1) || (kv_heads > 1 && t.stride(1) != ps)))
+    refuse(PyExc_ValueError, "%s: a page must be dense (strides (%lld, %lld, %lld))", name,
+           static_cast<long long>(t.stride(0)), static_cast<long long>(t.stride(1)), static_cast<long long>(t.stride(2)));
+  return {t.data_ptr(), n > 1 ? t.stride(0) : ps * kv_heads};
+}
+// k_cache, v_cache, k_scale, v_scale in 8 bits.
+struct Pages8 {
+  Cache k, v;
+  Scales ks, vs;
+};
+Pages8 pages8(PyObject* const* a, int kv_heads, int d, int dev) {
+  const auto e4m3 = ScalarType::Float8_e4m3fn;
+  const Cache k = cache(tensor(a[0], "k_cache"), "k_cache", kv_heads, d, dev, e4m3);
+  const Cache v = cache(tensor(a[1], "v_cache"), "v_cache", kv_heads, d, dev, e4m3);
+  same_pages(k, v);
+  return {k, v, scales(tensor(a[2], "k_scale"), "k_scale", k, kv_heads, dev),
+          scales(tensor(a[3], "v_scale"), "v_scale", k, kv_heads, dev)};
 }
 
 // ------------------------------------------------------------------ outputs
@@ -534,6 +566,72 @@ PyObject* append(PyObject* const* a) {
   return qo.release();
 }
 
+// q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slots, positions,
+// q_weight, k_weight, eps, interleaved, mscale, q_out, stream
+PyObject* append_fp8(PyObject* const* a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  const Tensor &sl = tensor(a[8], "slots"), &pos = tensor(a[9], "positions");
+  const Heads h = qk_shapes(q, k);
+  if (v.sizes() != k.sizes() || v.scalar_type() != q.scalar_type())
+    refuse(PyExc_ValueError, "v must match k in shape and dtype");
+  Out qo(a[15], "q_out");
+  if (qo.t) same_shape(*qo.t, q, "q_out must match q in shape");
+  const int dev = device_of(q, "q");
+  const Rows rq = rows(q, "q", dev, h.type), rk = rows(k, "k", dev, h.type), rv = rows(v, "v", dev, h.type);
+  const Pages8 pg = pages8(a + 4, h.kv_heads, h.d, dev);
+  const Phases ph = phase_table(maybe(a[3], "phases"), dev);
+  const Weights w = weights(maybe(a[10], "q_weight"), maybe(a[11], "k_weight"), h.d, dev);
+  const auto* psl = reinterpret_cast<const long long*>(vec<int64_t>(sl, "slots", h.T, dev, ScalarType::Long));
+  const int* pp = ints(pos, "positions", h.T, dev);
+  const float eps = real(a[12]), ms = real(a[14]);
+  const int inter = truth(a[13]);
+  const Place at(dev, a[16]);
+  void* po = dense(qo.get(q.sizes(), h.type, at), "q_out", dev, h.type);
+  call(at, [&](void* st) {
+    return ra_paged_append_fp8(rq.p, rk.p, rv.p, po, pg.k.p, pg.v.p, pg.ks.p, pg.vs.p, h.T, h.d, h.heads, h.kv_heads,
+                               rq.stride, rk.stride, rv.stride, pg.k.pages, pg.k.page_size, pg.k.stride, pg.v.stride,
+                               pg.ks.stride, pg.vs.stride, psl, pp, ph.rot, inter, ph.p, ms, w.q, w.k, w.type, eps,
+                               type_code(h.type), st);
+  });
+  return qo.release();
+}
+
+// k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_k, tokens, k_out,
+// v_out, stream
+PyObject* read_fp8(PyObject* const* a) {
+  const Tensor& kc = tensor(a[0], "k_cache");
+  const Tensor &tab = tensor(a[4], "block_table"), &len = tensor(a[5], "lengths"), &cu = tensor(a[6], "cu_k");
+  const long long tokens = integer(a[7]);
+  Out ko(a[8], "k_out"), vo(a[9], "v_out");
+  if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache: [n_pages, page_size, kv_heads, d]");
+  if (tokens < 0) refuse(PyExc_ValueError, "tokens=%lld is negative", tokens);
+  const int64_t n = len.numel();
+  const int kv_heads = to_int(kc.size(2), "kv_heads"), d = to_int(kc.size(3), "d");
+  const int64_t sizes[3] = {tokens, kv_heads, d};
+  auto fits = [&](const Out& o, const char* name) {
+    if (o.t && o.t->sizes() != at::IntArrayRef(sizes, 3))
+      refuse(PyExc_ValueError, "%s must have shape (%lld, %d, %d), got %s", name, tokens, kv_heads, d,
+             shape_of(*o.t).c_str());
+  };
+  fits(ko, "k_out");
+  fits(vo, "v_out");
+  const int dev = device_of(kc, "k_cache");
+  const Pages8 pg = pages8(a, kv_heads, d, dev);
+  const Table tb = block_table(tab, n, dev);
+  const int* pl = ints(len, "lengths", n, dev);
+  const int* pc = ints(cu, "cu_k", n + 1, dev);
+  const Place at(dev, a[10]);
+  const auto bf16 = ScalarType::BFloat16;
+  void* pk = dense(ko.get(at::IntArrayRef(sizes, 3), bf16, at), "k_out", dev, bf16);
+  void* pv = dense(vo.get(at::IntArrayRef(sizes, 3), bf16, at), "v_out", dev, bf16);
+  call(at, [&](void* st) {
+    return ra_paged_read_fp8(pg.k.p, pg.v.p, pg.ks.p, pg.vs.p, pk, pv, tokens, tb.n_req, pc, tb.p, tb.width, pl,
+                             pg.k.pages, pg.k.page_size, pg.k.stride, pg.v.stride, pg.ks.stride, pg.vs.stride, d,
+                             kv_heads, st);
+  });
+  return pack({&ko, &vo});
+}
+
 // q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream
 PyObject* decode(PyObject* const* a) {
   const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
@@ -600,6 +698,8 @@ RA_ENTRY(extend, 14)
 RA_ENTRY(release, 9)
 RA_ENTRY(append, 15)
 RA_ENTRY(decode, 11)
+RA_ENTRY(append_fp8, 17)
+RA_ENTRY(read_fp8, 11)
 #undef RA_ENTRY
 
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
@@ -614,6 +714,8 @@ PyMethodDef g_methods[] = {
     {"paged_release", fast(release_entry), METH_FASTCALL, nullptr},
     {"paged_append", fast(append_entry), METH_FASTCALL, nullptr},
     {"paged_decode", fast(decode_entry), METH_FASTCALL, nullptr},
+    {"paged_append_fp8", fast(append_fp8_entry), METH_FASTCALL, nullptr},
+    {"paged_read_fp8", fast(read_fp8_entry), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_serve", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstdint>
+
 #include "ra_internal.h"
 
 namespace ra {
@@ -71,6 +73,9 @@ struct RopeArgs {
   void* kc;          // append: pages [n_pages, page_size, kv_heads, d] bf16
   void* vc;
   long long kc_page, vc_page;  // elements from page to page
+  void* ks;          // append in 8 bits: scales [n_pages, kv_heads, page_size], e8m0
+  void* vs;
+  long long ks_page, vs_page;
   long long n_slots;           // n_pages * page_size
   int page_shift;
   const long long* slots;
@@ -98,13 +103,36 @@ struct RopeArgs {
   int parts;
 };
 cudaError_t launch_rope_forward(const RopeArgs& a, int d, bool bf16, cudaStream_t st);
-cudaError_t launch_rope_append(const RopeArgs& a, int d, cudaStream_t st);
+// fp8: kc and vc are e4m3 with the scales ks and vs, else bf16.
+cudaError_t launch_rope_append(const RopeArgs& a, int d, bool fp8, cudaStream_t st);
 // CTAs of the backward launch, i.e. partial weight gradients it writes.
 // Sets how they share the tokens.
 int rope_grad_ctas(RopeArgs& a, int d);
 cudaError_t launch_rope_backward(const RopeArgs& a, int ctas, int d, bool bf16, cudaStream_t st);
 // dqw, dkw = the sums of the n partial weight gradients.
 cudaError_t launch_rope_weight_grad(const RopeArgs& a, int n, int d, cudaStream_t st);
+
+// ------------------------------------------------------------------ 8-bit pages read back
+struct ReadArgs {
+  const uint8_t* kc;  // pages [n_pages, page_size, kv_heads, d] e4m3
+  const uint8_t* vc;
+  const uint8_t* ks;  // their scales [n_pages, kv_heads, page_size] e8m0
+  const uint8_t* vs;
+  long long kc_page, vc_page, ks_page, vs_page;  // bytes from page to page
+  void* ko;           // [tokens, kv_heads, d] bf16
+  void* vo;
+  const int* block_table;  // [n_req, max_pages]
+  const int* lengths;      // [n_req]
+  const int* cu;           // [n_req + 1]
+  long long tokens;
+  int n_req;
+  int max_pages;
+  int n_pages;
+  int page_shift;
+  int kv_heads;
+  int per_warp;  // set by the launcher: rows that a warp takes together
+};
+cudaError_t launch_paged_read(const ReadArgs& a, int d, cudaStream_t st);
 
 // ------------------------------------------------------------------ paged decode
 struct PagedArgs {

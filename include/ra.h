@@ -127,7 +127,9 @@ typedef enum {
   RA_KERNEL_PAGED_APPEND = 17,    /* kind 14 with k and v written to their pages */
   RA_KERNEL_PAGED_DECODE = 18,    /* attention over the pages */
   RA_KERNEL_PAGED_COMBINE = 19,   /* joins the parts of a request that several CTAs took */
-  RA_KERNEL_KINDS = 20
+  RA_KERNEL_PAGED_APPEND_FP8 = 20, /* kind 17 with k and v held in 8 bits */
+  RA_KERNEL_PAGED_READ_FP8 = 21,  /* 8-bit pages as dense bf16 rows */
+  RA_KERNEL_KINDS = 22
 } ra_kernel_kind;
 
 /*
@@ -554,6 +556,50 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     int max_pages, const int* lengths, int n_pages, int page_size,
                     long long k_page_stride, long long v_page_stride, long long window, int d,
                     int heads, int kv_heads, int dtype, int out_dtype, void* stream);
+
+/*
+ * Pages in 8 bits.  The same pages, block tables and slots, with k_cache and
+ * v_cache [n_pages, page_size, kv_heads, d] of e4m3 codes (one byte; pages
+ * k_page_stride / v_page_stride bytes apart, a multiple of 16) and one scale per
+ * token and KV head: k_scale, v_scale [n_pages, kv_heads, page_size], one byte
+ * each (e8m0: byte b stands for 2^(b - 127)), dense inside a page, pages
+ * k_scale_stride / v_scale_stride bytes apart (a multiple of 16).  An entry is
+ * code * scale, which bf16 holds exactly.  A row x of d entries is held with
+ *   e = the least integer in [-117, 120] with max |x| <= 448 * 2^e
+ * (over its finite entries; e = -117 for a row of zeros), the scale 2^e and the
+ * codes x / 2^e, to nearest, halves to even; an entry that is not finite becomes
+ * NaN.  So a page takes 0.504 (d = 128) or 0.508 of its bytes in bf16, and an
+ * entry is off by at most 2^-4 of itself or 2^-10 scales.  page_size: 16, 32, 64,
+ * 128 or 256.  Scales other than those of a row so held (bytes 10 to 247) give
+ * undefined results.
+ *
+ * ra_paged_append_fp8 -- ra_paged_append with k and v so held: k as normed and
+ * turned in fp32, rounded once.  Rows whose slot is outside the pages are padding.
+ *
+ * ra_paged_read_fp8 -- the newest tokens of each request's history as dense rows:
+ * row j of the n_i = cu_k[i + 1] - cu_k[i] rows of request i is its token
+ * lengths[i] - n_i + j (cu_k with the prefix sums of lengths: all of them).
+ *   k_out, v_out: [tokens, kv_heads, d] bf16, as ra_ring_forward and
+ *     ra_decode_forward take them.  Rows outside [cu_k[0], cu_k[n_req]) or behind
+ *     `tokens` are left as they were; a row before its request's first token,
+ *     or in a page outside [0, n_pages), is zero.
+ *   cu_k: device int32 [n_req + 1], nondecreasing.
+ */
+int ra_paged_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                        void* v_cache, void* k_scale, void* v_scale, long long T, int d, int heads,
+                        int kv_heads, long long q_stride, long long k_stride, long long v_stride,
+                        int n_pages, int page_size, long long k_page_stride,
+                        long long v_page_stride, long long k_scale_stride,
+                        long long v_scale_stride, const long long* slots, const int* positions,
+                        int rot_dim, int interleaved, const void* phases, float mscale,
+                        const void* q_weight, const void* k_weight, int w_dtype, float eps,
+                        int dtype, void* stream);
+int ra_paged_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                      const void* v_scale, void* k_out, void* v_out, long long tokens, int n_req,
+                      const int* cu_k, const int* block_table, int max_pages, const int* lengths,
+                      int n_pages, int page_size, long long k_page_stride, long long v_page_stride,
+                      long long k_scale_stride, long long v_scale_stride, int d, int kv_heads,
+                      void* stream);
 
 /*
  * ra_device_status -- synchronize `stream`, then read and clear the
