@@ -51,6 +51,7 @@ KERNEL_KINDS = {
     "paged_combine": 19,
     "paged_append_fp8": 20,
     "paged_read_fp8": 21,
+    "paged_decode_fp8": 22,
 }
 
 _lock = threading.Lock()
@@ -88,6 +89,7 @@ _SIGNATURES = {
     "ra_paged_decode": ("PPPPPLiiPPiPiiLLLiiiiiP", "i"),
     "ra_paged_append_fp8": ("PPPPPPPPLiiiLLLiiLLLLPPiiPfPPifiP", "i"),
     "ra_paged_read_fp8": ("PPPPPPLiPPiPiiLLLLiiP", "i"),
+    "ra_paged_decode_fp8": ("PPPPPPPLiiPPiPiiLLLLLiiiiiP", "i"),
     "ra_device_status": ("P", "i"),
     "ra_selftest_wait_timeout": ("LP", "i"),
     "ra_cached_memory": ("P", "i"),
@@ -624,6 +626,16 @@ def ra_paged_append_fp8(q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slo
     return (_serve or _fast()).paged_append_fp8(
         q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slots, positions, q_weight, k_weight,
         eps, interleaved, mscale, q_out, stream)
+
+
+def ra_paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, *, cu_q=None,
+                        n_q: int = 0, window: int = 0, out=None, lse=None, stream=None):
+    """ra_paged_decode over pages in 8 bits (as ra_paged_append_fp8 writes
+    them); everything else, the returned (out, lse) too, as there.  For a few
+    new tokens per request; for a prompt's chunks, ra_paged_read_fp8."""
+    return (_serve or _fast()).paged_decode_fp8(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_q, n_q, window, out, lse,
+        stream)
 
 
 def ra_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_k, *,

@@ -1,0 +1,418 @@
+// Decode attention over pages in 8 bits (include/ra.h, ra_paged_decode_fp8; the
+// rows as fp8.cuh holds them).  Row, keys, work list, roles and joining launch
+// are those of paged_kernel.cu; with key t held as codes kc_t and scale 2^a_t,
+// value t as vc_t and 2^b_t:
+//   s_t = 2^a_t (q.kc_t) / sqrt(d),  m = max s,  p_t = exp(s_t - m),
+//   out = sum p_t 2^b_t vc_t / sum p_t.
+//
+// The pages' bytes are half of bf16's, so a tile's arithmetic has half the time.
+// - Codes go to the tensor core as fp16 (cvt.rn.f16x2.e4m3x2, exact, one
+//   instruction for two).  The conversion is in registers, so the order of the
+//   reduced index is free: a lane's four neighbouring bytes of a key's row are
+//   the two register halves of one m16n8k16 fragment, and the query's columns
+//   are read in the same order.  For P V, ldmatrix transposes pairs of bytes, and
+//   one byte permutation gives the pairs of keys of two neighbouring columns: of
+//   the fragment's rows g and g + 8.
+// - q is turned to fp16 once an item, with a power of two per row that brings its
+//   largest entry to [2^14, 2^15): its 8 bits are exact down to 2^-28 of that entry,
+//   and below it is off by at most 2^-39 of it.
+// - The weight of a value is p_t 2^b_t.  fp16 has no room for all scales, so a
+//   warp takes the largest 2^b of its keys of a tile out and gives it back in
+//   fp32 when the tile's product is added to O.  What is left, times 2^15, is
+//   held in two fp16 terms: 22 bits and the sign of the second, off by at most
+//   2^-23 of itself, or 2^-40 of the largest, as good as the fp32 it comes from.
+//   (bf16 pages need three terms of 8 bits.)
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp8.cuh"
+#include "paged_mma.cuh"
+
+namespace ra {
+
+__device__ int g_paged_fp8_status = 0;
+
+namespace {
+
+using namespace paged;
+
+constexpr int kThreads = kMmaThreads;
+
+// KB: blocks of 16 keys that a warp takes of a tile.
+template <int D, int NT, int KB>
+struct Cfg {
+  static constexpr int DIM = D, BT = 16 * kCons * KB;
+  static constexpr int NCH = 1, BOX = KB == 1 ? 6 : 7;
+  static constexpr uint32_t CHROW = D, CHB = BT * D;  // rows of 128 or 64 bytes, swizzled over as many
+  static constexpr bool SCALES = true;
+  static constexpr int RT = 8 * NT;
+  static constexpr int CONS_REGS = NT == 1 ? 152 : 192, PROD_REGS = 256 - CONS_REGS;
+  static constexpr int ITEMS = NT == 1 ? 3 : 2;
+  static constexpr uint32_t TILE = BT * D;
+  static constexpr uint32_t STAGE = 2 * TILE;
+  static constexpr uint32_t QT = RT * D * 2;
+  static constexpr uint32_t REC = 32 + 8 * RT;
+  static constexpr uint32_t REST = ITEMS * QT + kCons * 4 * D * 4 + 2 * kCons * RT * 4 + ITEMS * REC + 16;
+  static constexpr int NST = (115712 - REST - 2 * ITEMS * 8) / (STAGE + 2 * BT + 24);  // what two CTAs per SM leave
+  static constexpr uint32_t OFF_SCALE = NST * STAGE;  // of stage s: K's, then V's
+  static constexpr uint32_t OFF_Q = OFF_SCALE + NST * 2 * BT;
+  static constexpr uint32_t OFF_BUF = OFF_Q + ITEMS * QT;
+  static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 4 * D * 4;
+  static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * kCons * RT * 4;
+  static constexpr uint32_t OFF_BAR = OFF_ITEM + ITEMS * REC;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + (3 * NST + 2 * ITEMS) * 8;
+  static constexpr uint32_t SMEM = OFF_MISC + 16;
+  static_assert(SMEM <= 115712 && NST >= 2, "two CTAs per SM");
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 halves(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ uint32_t low2(uint32_t x) { return halves2(static_cast<uint16_t>(x)); }
+__device__ __forceinline__ uint32_t high2(uint32_t x) { return halves2(static_cast<uint16_t>(x >> 16)); }
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
+  uint32_t y;
+  asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int NT, int KB>
+__global__ void __launch_bounds__(kThreads, 2)
+paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
+  using C = Cfg<D, NT, KB>;
+  constexpr int RT = C::RT, BT = C::BT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
+  auto vfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (C::NST + s); };
+  auto empty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NST + s); };
+  auto ifull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + s); };
+  auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + C::ITEMS + s); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.heads / a.kv_heads;
+  let_next_start();
+  if (tid == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(vfull(s), 1);
+      mbar_init(empty(s), kCons);
+    }
+    for (int s = 0; s < C::ITEMS; ++s) {
+      mbar_init(ifull(s), 33);  // every lane's copies, and the record
+      mbar_init(iempty(s), kCons);
+    }
+    int abort = *reinterpret_cast<volatile int*>(&g_paged_fp8_status);
+    // The swizzled tiles need 1024-byte alignment, which the declaration asks
+    // for; a loader that ignored it would be reported, not computed with.
+    if (sb & 1023u) abort = atomicCAS(&g_paged_fp8_status, 0, 0xaf) | 0xaf;
+    *abort_flag = abort;
+    fence_mbar_init();
+  }
+  wait_for_previous();
+  if (tid == 0) static_cast<Cut*>(a.cuts)[blockIdx.x].last = -1;
+  const Run run = find_run<BT, kExtra, kPlain, kThreads>(a, g, RT, smem + C::OFF_BUF, abort_flag);  // synchronizes
+  if (run.first >= run.last || run.stop) return;
+  const long long lim = a.wait_limit;
+
+  if (warp >= kCons) {
+    // ---------------------------------------------------------------- producers
+    regs_dec<C::PROD_REGS>();
+    if (warp >= kCons + 2) return;
+    const bool is_k = warp == kCons;
+    produce<C, kPlain>(a, is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV), is_k, run, g, smem, sb, lane,
+                       abort_flag, &g_paged_fp8_status);
+    return;
+  }
+
+  // ------------------------------------------------------------------ consumers
+  // (After a wait that gave up a warp runs on to the item's first barrier, as in
+  // paged_kernel.cu.)
+  regs_inc<C::CONS_REGS>();
+  float* buf = reinterpret_cast<float*>(smem + C::OFF_BUF);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);  // [row][warp]
+  float* s_l = s_m + kCons * RT;
+  const int win = static_cast<int>(a.window);
+  bool ok = true;
+  int st = 0;  // stage and phase of the next tile
+  uint32_t par = 0;
+  constexpr int CPR = D / 16;  // 16-byte chunks of a row
+  // Of a row r: the swizzle over its chunks (128-byte rows over 8 rows, 64-byte
+  // rows over pairs of 8).
+  auto swz = [](int r) { return D == 128 ? r & 7 : (r >> 1) & 3; };
+  const int key0 = warp * 16 * KB;  // of the tile
+  const int kr = lane & 15, c2 = lane >> 4;  // ldmatrix: row of a block, chunk of a pair
+  for (int it = 0;; ++it) {
+    const int is = it % C::ITEMS;
+    ok = ok && wait_bar(ifull(is), static_cast<uint32_t>(it / C::ITEMS) & 1u, abort_flag, &g_paged_fp8_status, 0xa5, lim);
+    ok = __all_sync(kAll, ok);
+    const int* rec = reinterpret_cast<const int*>(smem + C::OFF_ITEM + is * C::REC);
+    Item item = *reinterpret_cast<const Item*>(rec);
+    if (!ok || item.last == 2) item.tiles = 0;
+    // Keys [lo, hi) of the lane's rows 8 nt + 2 (lane & 3) + {0, 1}; the keys
+    // that every row of the item sees are [lo_all, hi_all).
+    auto begin_of = [&](int end) { return win > 0 && end + item.base > win ? end - win : -item.base; };
+    int rlo[NT][2], rhi[NT][2];
+    const int hi_all = rec[8 + RT], lo_all = begin_of(rec[8 + 2 * RT - 1]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        rhi[nt][c] = rec[8 + RT + 8 * nt + 2 * (lane & 3) + c];
+        rlo[nt][c] = begin_of(rhi[nt][c]);
+      }
+    // The query rows in fp16: columns 16 c + 4 (lane % 4) + 0..3 of row lane / 4,
+    // and the factor on the lane's two scores of a key.
+    uint32_t qf[NT][CPR][2];
+    float sl2[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + (lane >> 2);
+      unsigned top = 0;
+#pragma unroll
+      for (int c = 0; c < CPR; ++c) {
+        const int ch = 2 * c + ((lane & 3) >> 1);
+        const uint2 w = lds_v2(sb + C::OFF_Q + is * C::QT + r * (D * 2) + ((ch ^ (r & 7)) << 4) + (lane & 1) * 8);
+        qf[nt][c][0] = w.x;
+        qf[nt][c][1] = w.y;
+        top = max(top, max(max(w.x << 16 & 0x7fff0000u, w.x & 0x7fff0000u), max(w.y << 16 & 0x7fff0000u, w.y & 0x7fff0000u)));
+      }
+      top = max(top, __shfl_xor_sync(kAll, top, 1));
+      top = max(top, __shfl_xor_sync(kAll, top, 2));
+      int e = static_cast<int>(top >> 23);  // largest entry in [2^(e - 127), 2^(e - 126))
+      e = e < 27 ? 27 : e;
+      const float up = __uint_as_float(static_cast<unsigned>(268 - e) << 23);  // 2^(14 - (e - 127))
+#pragma unroll
+      for (int c = 0; c < CPR; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qf[nt][c][h] = f16x2_rn(__uint_as_float(qf[nt][c][h] << 16) * up, __uint_as_float(qf[nt][c][h] & 0xffff0000u) * up);
+      const float down = a.scale_log2 * __uint_as_float(static_cast<unsigned>(e - 14) << 23);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) sl2[nt][c] = __shfl_sync(kAll, down, 8 * (lane & 3) + 4 * c);
+    }
+    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
+    }
+    for (int k = 0; k < item.tiles; ++k) {
+      const uint32_t kb = sb + st * C::STAGE, vb = kb + C::TILE, scales = sb + C::OFF_SCALE + st * 2 * BT + key0;
+      const int k0 = (item.k0 + k) * BT + key0;  // the warp's first key
+      ok = ok && wait_bar(kfull(st), par, abort_flag, &g_paged_fp8_status, 0xa2, lim);
+      ok = __all_sync(kAll, ok);
+      const bool some = k0 < item.hi && k0 + 16 * KB > item.lo;
+      const bool edge = k0 < item.lo || k0 + 16 * KB > item.hi;
+      float sc[KB][NT][4];
+      uint32_t pb[KB][NT][2][2];
+      float al[NT][2], back = 0.f;
+      if (some) {
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          const int r = key0 + 16 * b + kr;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) sc[b][nt][0] = sc[b][nt][1] = sc[b][nt][2] = sc[b][nt][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < CPR; c += 2) {
+            uint32_t w[4];  // (keys 0-7, 8-15) of chunk c, then of chunk c + 1
+            ldsm4(kb + r * D + (((c + c2) ^ swz(r)) << 4), w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t af[4] = {low2(w[2 * h]), low2(w[2 * h + 1]), high2(w[2 * h]), high2(w[2 * h + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(sc[b][nt], af, qf[nt][c + h][0], qf[nt][c + h][1]);
+            }
+          }
+        }
+        // Scales of the lane's keys lane / 4 and lane / 4 + 8 of each block.
+        uint32_t vs[KB][2], top = 0;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = 16 * b + 8 * h + (lane >> 2);
+            const float ks = scale_of(lds_u8(scales + j));
+            vs[b][h] = lds_u8(scales + BT + j);
+            if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0;  // nobody's: anything may stand there
+            top = max(top, vs[b][h]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) sc[b][nt][2 * h + c] *= ks;
+          }
+        top = warp_max(top);
+        // 2^(top - 127 - 15), below fp32's normal range too.
+        back = __uint_as_float(top > 15 ? (top - 15) << 23 : 0x400000u >> (15 - top));
+        if (k0 < lo_all || k0 + 16 * KB > hi_all) {
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int key = k0 + 16 * b + (lane >> 2) + (c >> 1) * 8;
+                if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[b][nt][c] = -INFINITY;
+              }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+#pragma unroll
+            for (int b = 1; b < KB; ++b) x = fmax3(x, sc[b][nt][c], sc[b][nt][c + 2]);
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+            const float mn = fmaxf(m[nt][c], x * sl2[nt][c]);
+            const float ref = mn == -INFINITY ? 0.f : mn;
+            al[nt][c] = ex2(m[nt][c] - ref);
+            m[nt][c] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float p = ex2(fmaf(sc[b][nt][2 * h + c], sl2[nt][c], -ref));
+                sc[b][nt][2 * h + c] = p;
+                sum += p;
+              }
+            l[nt][c] = fmaf(l[nt][c], al[nt][c], sum);
+          }
+        // The weights in two fp16 terms.
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int e = static_cast<int>(vs[b][h]) - static_cast<int>(top) + 142;
+            const float f = __uint_as_float(e > 0 ? static_cast<unsigned>(e) << 23 : 0u);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float x = sc[b][nt][2 * h] * f, y = sc[b][nt][2 * h + 1] * f;
+              const uint32_t hi = f16x2_rn(x, y);
+              const float2 v = halves(hi);
+              pb[b][nt][0][h] = transpose8x8(hi);
+              pb[b][nt][1][h] = transpose8x8(f16x2_rn(x - v.x, y - v.y));
+            }
+          }
+      }
+      ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim);
+      ok = __all_sync(kAll, ok);
+      if (some) {
+        uint32_t keep[KB][2];  // V rows outside [lo, hi) may hold anything
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = k0 + 16 * b + 8 * h + 2 * (lane & 3);
+            keep[b][h] = !edge ? kAll : (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
+                                            (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+        for (int c = 0; c < CPR; c += 2) {
+          uint32_t w[KB][4];  // (keys 0-7, 8-15) of 16 columns, then of the next 16
+#pragma unroll
+          for (int b = 0; b < KB; ++b) {
+            const int r = key0 + 16 * b + kr;
+            ldsm4_t(vb + r * D + (((c + c2) ^ swz(r)) << 4), w[b]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t af[KB][4];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                uint32_t y = w[b][2 * h + x];
+                if (edge) y &= keep[b][x];
+                y = __byte_perm(y, 0, 0x3120);  // column 2 (lane / 4) of two keys, then the next column
+                af[b][2 * x] = low2(y);
+                af[b][2 * x + 1] = high2(y);
+              }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              // The tile's product apart, small terms first, then one rounded
+              // fp32 step: the tensor core's own accumulation truncates.
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int term = 1; term >= 0; --term)
+#pragma unroll
+                for (int b = 0; b < KB; ++b) mma_f16(t, af[b], pb[b][nt][term][0], pb[b][nt][term][1]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[nt][c + h][x] = fmaf(t[x], back, o[nt][c + h][x] * al[nt][x & 1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+      if (++st == C::NST) {
+        st = 0;
+        par ^= 1u;
+      }
+    }
+    if (!join_warps<D, NT, true, kPlain>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) return;
+    if (item.last) return;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(iempty(is));
+  }
+}
+
+template <int D, int NT, int KB>
+cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_smem(paged_fp8_kernel<D, NT, KB>, Cfg<D, NT, KB>::SMEM, done);
+  if (e != cudaSuccess) return e;
+  return launch_early(paged_fp8_kernel<D, NT, KB>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D, NT, KB>::SMEM, st,
+                      tk, tv, a);
+}
+
+constexpr int kKB = 1;
+
+}  // namespace
+
+int paged_fp8_row_tile(const PagedArgs& a) { return a.n_q * (a.heads / a.kv_heads) <= 8 ? 8 : 16; }
+int paged_fp8_box_rows() { return 64 * kKB; }
+
+cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t st) {
+  if (d == 128)
+    return row_tile == 8 ? decode_t<128, 1, kKB>(a, ctas, tk, tv, st) : decode_t<128, 2, kKB>(a, ctas, tk, tv, st);
+  return row_tile == 8 ? decode_t<64, 1, kKB>(a, ctas, tk, tv, st) : decode_t<64, 2, kKB>(a, ctas, tk, tv, st);
+}
+
+cudaError_t take_paged_fp8_status(int* code) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_paged_fp8_status, sizeof(int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_paged_fp8_status, &zero, sizeof(int));
+}
+
+}  // namespace ra

@@ -35,7 +35,7 @@
 
 #include <cuda_bf16.h>
 
-#include "paged_walk.cuh"
+#include "paged_mma.cuh"
 
 namespace ra {
 
@@ -45,21 +45,20 @@ namespace {
 
 using namespace paged;
 
-constexpr int BT = 64;           // keys per tile
-constexpr int kCons = 4;         // consumer warps
-constexpr int kThreads = 256;    // a consumer warpgroup and one with the producers
-constexpr int kExtra = 1;        // what an item's beginning and end cost, in tiles
-constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
+constexpr int kThreads = kMmaThreads;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int NCH = D / 64;
+  static constexpr int DIM = D, BT = 64;         // keys per tile
+  static constexpr int NCH = D / 64, BOX = 6;
+  static constexpr uint32_t CHROW = 128, CHB = BT * CHROW;  // a 64-column chunk of a tile, 128-byte swizzle
+  static constexpr bool SCALES = false;
   static constexpr int RT = 8 * NT;              // query rows of an item
   // Registers of the two warpgroups; together the launch's 2 x 128.  (200 and
   // 56 spill in the producers: 152 requests of 128 keys, from L2, 19.3 against 18.5 us.)
   static constexpr int CONS_REGS = NT == 1 ? 152 : 192, PROD_REGS = 256 - CONS_REGS;
   static constexpr int ITEMS = NT == 1 ? 3 : 2;  // records and query tiles in flight
-  static constexpr uint32_t TILE = BT * D * 2;
+  static constexpr uint32_t TILE = BT * D * 2, STAGE = 2 * TILE;
   static constexpr int NST = D == 128 ? 3 : 6;   // stages of one K and one V tile
   static constexpr uint32_t QT = RT * D * 2;     // query rows, 16-byte chunks swizzled
   static constexpr uint32_t REC = 32 + 8 * RT;   // Item, then rows and ends of its query rows
@@ -73,55 +72,15 @@ struct Cfg {
   static_assert(SMEM <= 115712, "two CTAs per SM");
 };
 
-// An item, or the part of it that a CTA has, as its consumers need it.
-// Positions are relative to the item's first key tile.  The record goes on
-// with row[RT], each query row's index in out, and end[RT], the end of the
-// keys that it sees.
-struct Item {
-  int rows;            // query rows
-  int base;            // position of the item's first key tile
-  int lo, hi;          // keys that any row sees
-  int k0;              // first key tile here
-  int tiles;           // key tiles here
-  int slot;            // partial slot, or -1: the item is whole
-  int last;            // the CTA's last item; 2: not even an item
-};
-static_assert(sizeof(Item) == 32, "record layout");
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // ------------------------------------------------------------------ the kernel
 // NT: 8-row groups of query rows of an item.
-template <int D, int NT>
+template <int D, int NT, int MODE>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedArgs a) {
   using C = Cfg<D, NT>;
-  constexpr int RT = C::RT;
+  constexpr int RT = C::RT, BT = C::BT;
+  constexpr uint32_t CHB = C::CHB;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
@@ -132,7 +91,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
-  Cut* cuts = static_cast<Cut*>(a.cuts);
   let_next_start();
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
@@ -152,8 +110,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     fence_mbar_init();
   }
   wait_for_previous();
-  if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, kExtra, kThreads>(a, g, RT, smem + C::OFF_BUF, abort_flag);  // synchronizes
+  if (MODE == kPlain && tid == 0) static_cast<Cut*>(a.cuts)[blockIdx.x].last = -1;
+  const Run run = find_run<BT, kExtra, MODE, kThreads>(a, g, RT, smem + C::OFF_BUF, abort_flag);  // synchronizes
   if (run.first >= run.last || run.stop) return;
   const long long lim = a.wait_limit;
 
@@ -162,103 +120,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     regs_dec<C::PROD_REGS>();
     if (warp >= kCons + 2) return;
     const bool is_k = warp == kCons;
-    const void* tm = is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV);
-    const int sh = a.page_shift;
-    const int rows = sh < 6 ? 1 << sh : BT;  // of a box
-    const int npg = BT / rows;
-    const uint32_t box = static_cast<uint32_t>(rows) * 128u;
-    auto full = [&](int s) -> uint32_t { return is_k ? kfull(s) : vfull(s); };
-    Walk<BT, kExtra> w;
-    w.start(a, g, RT, run.r, run.x);
-    long long u = run.first;
-    if (w.k >= w.t.nt) {  // the run begins behind an item's last tile
-      u += w.t.nt + kExtra - w.k;
-      if (u < run.last) w.next(a, g, RT);
-      else if (is_k && lane == 0) {
-        reinterpret_cast<Item*>(smem + C::OFF_ITEM)->last = 2;
-        mbar_arrive(ifull(0));
-      }
-      if (u >= run.last && is_k) copies_arrive(ifull(0));
-    }
-    bool ok = true;
-    int i = 0;   // tiles requested
-    int it = 0;  // items begun
-    while (ok && u < run.last) {
-      const long long left = run.last - u;
-      const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
-      const long long after = u + tiles + (w.k + tiles == w.t.nt ? kExtra : 0);
-      PageIds ids;  // first: the record and the query rows hide its latency
-      ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
-      if (is_k) {
-        const int s = it % C::ITEMS;
-        if (it >= C::ITEMS) {
-          ok = wait_bar(iempty(s), (static_cast<uint32_t>(it / C::ITEMS) & 1u) ^ 1u, abort_flag,
-                        &g_paged_status, 0x84, lim);
-          ok = __all_sync(kAll, ok);
-          if (!ok) break;
-        }
-        const int n = w.t.rr1 - w.t.rr0, base = w.t.t0 * BT;
-        int* rec = reinterpret_cast<int*>(smem + C::OFF_ITEM + s * C::REC);
-        int row = 0;
-        if (lane < RT) {  // rows past the item's get its last row's keys, and no output
-          const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = token_of(rr, g);
-          row = (w.q.row0 + j) * a.heads + w.kh * g + (rr - j * g);
-          rec[8 + lane] = row;
-          rec[8 + RT + lane] = key_end(w.q, j) - base;
-        }
-        if (lane == 0) {
-          const long long item0 = u - w.k;
-          const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
-          const int me = static_cast<int>(blockIdx.x);
-          *reinterpret_cast<Item*>(rec) =
-              Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), after >= run.last};
-          if (c0 != c1 && me == c0) cuts[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ifull(s));
-        // Chunk c of row r at c ^ (r % 8): the ldmatrix rows of a column
-        // block fall into different banks.
-#pragma unroll
-        for (int x0 = 0; x0 < RT * D / 8; x0 += 32) {
-          const int x = x0 + lane, r = x / (D / 8), c = x % (D / 8);
-          const long long at = static_cast<long long>(__shfl_sync(kAll, row, r)) * D + c * 8;
-          copy16(sb + C::OFF_Q + s * C::QT + r * (D * 2) + ((c ^ (r & 7)) << 4),
-                 static_cast<const __nv_bfloat16*>(a.q) + at, r < n ? 16u : 0u);
-        }
-        copies_arrive(ifull(s));
-        ++it;
-      }
-      for (int k = 0; k < tiles; ++k, ++i) {
-        const int key0 = (w.t.t0 + w.k + k) * BT;
-        const int page = ids.get(a, key0, rows, npg, lane);
-        const bool have = page >= 0;
-        const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(kAll, have)));
-        const int s = i % C::NST;
-        if (i >= C::NST) {
-          ok = wait_bar(empty(s), (static_cast<uint32_t>(i / C::NST) & 1u) ^ 1u, abort_flag,
-                        &g_paged_status, 0x81, lim);
-          ok = __all_sync(kAll, ok);
-          if (!ok) break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(full(s), n * box * C::NCH);
-        __syncwarp();
-        if (have) {
-          const uint32_t dst = sb + s * 2 * C::TILE + (is_k ? 0 : C::TILE) + lane * box;
-          const int row = key0 & ((1 << sh) - 1);
-#pragma unroll
-          for (int ch = 0; ch < C::NCH; ++ch)
-            tma_load_4d(dst + ch * CHB, tm, full(s), ch * 64, w.kh, row, page);
-        }
-      }
-      u = after;
-      if (ok && u < run.last) w.next(a, g, RT);
-    }
-    if (!ok) {  // let the copies in flight land before the CTA leaves
-      volatile int no_abort = 0;
-      for (int j = i > C::NST ? i - C::NST : 0; j < i; ++j)
-        wait_bar(full(j % C::NST), static_cast<uint32_t>(j / C::NST) & 1u, &no_abort, nullptr, 0, lim);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    produce<C, MODE>(a, is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV), is_k, run, g, smem, sb, lane,
+                     abort_flag, &g_paged_status);
     return;
   }
 
@@ -429,118 +292,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         par ^= 1u;
       }
     }
-    // ---------------------------------------------------------------- the warps' states meet
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x = l[nt][c];
-        x += __shfl_xor_sync(kAll, x, 4);
-        x += __shfl_xor_sync(kAll, x, 8);
-        x += __shfl_xor_sync(kAll, x, 16);
-        l[nt][c] = x;
-        if (lane < 4) {
-          s_m[(8 * nt + 2 * lane + c) * kCons + warp] = m[nt][c];
-          s_l[(8 * nt + 2 * lane + c) * kCons + warp] = x;
-        }
-      }
-    if (!named_bar_and(1, 32 * kCons, ok) || item.last == 2) return;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      constexpr int H = D / 32, Q = D / 64;  // 16-column groups of a half and of a quarter
-      float inv[2], mx[2], lt[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * nt + 2 * (lane & 3) + c;
-        const float4 vm = *reinterpret_cast<const float4*>(s_m + r * kCons);
-        const float4 vl = *reinterpret_cast<const float4*>(s_l + r * kCons);
-        mx[c] = fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w));
-        const float ref = mx[c] == -INFINITY ? 0.f : mx[c];
-        lt[c] = (vl.x * ex2(vm.x - ref) + vl.y * ex2(vm.y - ref)) +
-                (vl.z * ex2(vm.z - ref) + vl.w * ex2(vm.w - ref));
-        inv[c] = item.slot >= 0 ? 1.f : (lt[c] == 0.f ? 0.f : 1.f / lt[c]);
-        const float e = ex2(m[nt][c] - ref);
-#pragma unroll
-        for (int dm = 0; dm < D / 16; ++dm) {
-          o[nt][dm][c] *= e;
-          o[nt][dm][c + 2] *= e;
-        }
-      }
-      // Warps w and w ^ 1 swap halves of the columns and add, then w and
-      // w ^ 2 quarters: warp w ends with columns [D / 4 * (2 (w & 1) + w / 2)
-      // ..) of the sum.  A warp's second message goes where it read its first.
-      const bool odd = warp & 1, high = warp & 2;
-      float* from = buf + warp * (4 * D);
-      float* to = buf + (warp ^ 1) * (4 * D);
-      if (nt > 0) named_bar_sync(1, 32 * kCons);  // the messages of group nt - 1 are read
-      float h[H][4];
-#pragma unroll
-      for (int x = 0; x < H; ++x) {
-        float y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          h[x][c] = odd ? o[nt][H + x][c] : o[nt][x][c];
-          y[c] = odd ? o[nt][x][c] : o[nt][H + x][c];
-        }
-        *reinterpret_cast<float4*>(to + (x * 32 + lane) * 4) = make_float4(y[0], y[1], y[2], y[3]);
-      }
-      named_bar_sync(1, 32 * kCons);
-#pragma unroll
-      for (int x = 0; x < H; ++x) {
-        const float4 z = *reinterpret_cast<const float4*>(from + (x * 32 + lane) * 4);
-        h[x][0] += z.x;
-        h[x][1] += z.y;
-        h[x][2] += z.z;
-        h[x][3] += z.w;
-      }
-      __syncwarp();
-      float q[Q][4];
-#pragma unroll
-      for (int x = 0; x < Q; ++x) {
-        float y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          q[x][c] = high ? h[Q + x][c] : h[x][c];
-          y[c] = high ? h[x][c] : h[Q + x][c];
-        }
-        *reinterpret_cast<float4*>(from + (x * 32 + lane) * 4) = make_float4(y[0], y[1], y[2], y[3]);
-      }
-      named_bar_sync(1, 32 * kCons);
-      const float* last = buf + (warp ^ 2) * (4 * D);
-#pragma unroll
-      for (int x = 0; x < Q; ++x) {
-        const float4 z = *reinterpret_cast<const float4*>(last + (x * 32 + lane) * 4);
-        q[x][0] += z.x;
-        q[x][1] += z.y;
-        q[x][2] += z.z;
-        q[x][3] += z.w;
-      }
-      const int d0 = (odd ? D / 2 : 0) + (high ? D / 4 : 0) + (lane >> 2);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * nt + 2 * (lane & 3) + c;
-        if (r >= item.rows) continue;
-        const long long row = item.slot >= 0 ? item.slot * RT + r : rec[8 + r];
-#pragma unroll
-        for (int x = 0; x < Q; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float y = q[x][c + 2 * e] * inv[c];
-            const long long at = row * D + d0 + 16 * x + 8 * e;
-            if (item.slot >= 0) a.po[at] = y;
-            else if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-            else static_cast<float*>(a.out)[at] = y;
-          }
-        if (warp == 0 && lane < 4) {
-          if (item.slot >= 0) {
-            a.pm[row] = mx[c];
-            a.pl[row] = lt[c];
-          } else {
-            a.lse[row] = lt[c] == 0.f ? -INFINITY : mx[c] * kLn2 + logf(lt[c]);  // (NaN stays)
-          }
-        }
-      }
-    }
+    if (!join_warps<D, NT, false, MODE>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) return;
     if (item.last) return;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));
@@ -633,13 +385,13 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int MODE>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(paged_decode_kernel<D, NT>, Cfg<D, NT>::SMEM, done);
+  cudaError_t e = allow_smem(paged_decode_kernel<D, NT, MODE>, Cfg<D, NT>::SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_early(paged_decode_kernel<D, NT>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D, NT>::SMEM, st, tk, tv,
+  return launch_early(paged_decode_kernel<D, NT, MODE>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D, NT>::SMEM, st, tk, tv,
                       a);
 }
 
@@ -668,8 +420,8 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_til
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   if (row_tile == 128) return launch_paged_tc(a, d, ctas, tk, tv, st);
   if (d == 128)
-    return row_tile == 8 ? decode_t<128, 1>(a, ctas, tk, tv, st) : decode_t<128, 2>(a, ctas, tk, tv, st);
-  return row_tile == 8 ? decode_t<64, 1>(a, ctas, tk, tv, st) : decode_t<64, 2>(a, ctas, tk, tv, st);
+    return row_tile == 8 ? decode_t<128, 1, kPlain>(a, ctas, tk, tv, st) : decode_t<128, 2, kPlain>(a, ctas, tk, tv, st);
+  return row_tile == 8 ? decode_t<64, 1, kPlain>(a, ctas, tk, tv, st) : decode_t<64, 2, kPlain>(a, ctas, tk, tv, st);
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {

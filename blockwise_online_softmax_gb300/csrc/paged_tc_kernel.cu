@@ -156,7 +156,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   }
   wait_for_previous();
   if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, 0, kThreads>(a, g, RT, smem + C::OFF_AL, abort_flag);  // synchronizes
+  const Run run = find_run<BT, 0, kPlain, kThreads>(a, g, RT, smem + C::OFF_AL, abort_flag);  // synchronizes
   if (run.first >= run.last || run.stop) return;
   if (warp == 14) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -197,7 +197,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int rows = sh < 6 ? 1 << sh : 64;  // of a box
       const int boxes = BT / rows;
       const uint32_t box = static_cast<uint32_t>(rows) * 128u;
-      Walk<BT, 0> w;
+      Walk<BT, 0, kPlain> w;
       w.start(a, g, RT, run.r, run.x);
       long long u = run.first;
       bool ok = true;

@@ -46,9 +46,23 @@ struct Request {
   int len;   // keys, the new tokens' included
 };
 
+// What the rows of a kernel are: the new tokens of requests, which see the keys up
+// to themselves (kPlain: finished here; kOwn: partial states of them, for a
+// launch that joins them with others), or all the tokens of a group of requests,
+// which see every key of the group's prefix (kShared: partial states).
+constexpr int kPlain = 0, kOwn = 1, kShared = 2;
+
+template <int MODE>
 __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
   Request q;
-  if (a.cu_q) {
+  if (MODE == kShared) {
+    // The rows of requests [b, e), whatever the arrays say inside q and out.
+    const int T = static_cast<int>(a.T), x = a.cu_req[r], y = a.cu_req[r + 1];
+    const int b = x < 0 ? 0 : (x > a.n_own ? a.n_own : x), e = y < b ? b : (y > a.n_own ? a.n_own : y);
+    const int v = a.cu_q ? a.cu_q[b] : b * static_cast<int>(a.n_q), w = a.cu_q ? a.cu_q[e] : e * static_cast<int>(a.n_q);
+    q.row0 = v < 0 ? 0 : (v > T ? T : v);
+    q.n = (w < q.row0 ? q.row0 : (w > T ? T : w)) - q.row0;
+  } else if (a.cu_q) {
     // A malformed cu_q must not reach outside q and out.
     const int T = static_cast<int>(a.T), x = a.cu_q[r], y = a.cu_q[r + 1];
     q.row0 = x < 0 ? 0 : (x > T ? T : x);
@@ -73,7 +87,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 }
 
 // Token j of the request sees keys [begin, end).
+template <int MODE>
 __device__ __forceinline__ int key_end(const Request& q, int j) {
+  if (MODE == kShared) return q.len;
   const int e = q.len - q.n + j + 1;
   return e < 0 ? 0 : e;
 }
@@ -89,15 +105,15 @@ struct RowTile {
   int t0, nt;
 };
 
-template <int BT>
+template <int BT, int MODE>
 __device__ __forceinline__ RowTile row_tile(const PagedArgs& a, const Request& q, int g, int RT,
                                             int rt) {
   RowTile t;
   t.rr0 = rt * RT;
   const int all = q.n * g;
   t.rr1 = t.rr0 + RT < all ? t.rr0 + RT : all;
-  t.hi = key_end(q, token_of(t.rr1 - 1, g));
-  t.lo = key_begin(a, key_end(q, token_of(t.rr0, g)));
+  t.hi = key_end<MODE>(q, token_of(t.rr1 - 1, g));
+  t.lo = key_begin(a, key_end<MODE>(q, token_of(t.rr0, g)));
   t.t0 = t.lo / BT;
   t.nt = t.hi > t.lo ? (t.hi - 1) / BT + 1 - t.t0 : 1;
   return t;
@@ -109,18 +125,20 @@ __device__ __forceinline__ int row_tiles(const Request& q, int g, int RT) {
 
 // The units of a request: its key tiles, and EXTRA for every item, what an
 // item's beginning and end cost in tiles.
-template <int BT, int EXTRA>
+template <int BT, int EXTRA, int MODE>
 __device__ __forceinline__ long long request_units(const PagedArgs& a, int r, int g, int RT) {
-  const Request q = load_request(a, r);
+  const Request q = load_request<MODE>(a, r);
   const int n = row_tiles(q, g, RT);
   long long u = 0;
-  for (int rt = 0; rt < n; ++rt) u += row_tile<BT>(a, q, g, RT, rt).nt + EXTRA;
+  if (MODE == kShared) u = n ? static_cast<long long>(n) * (row_tile<BT, MODE>(a, q, g, RT, 0).nt + EXTRA) : 0;
+  else
+    for (int rt = 0; rt < n; ++rt) u += row_tile<BT, MODE>(a, q, g, RT, rt).nt + EXTRA;
   return u * a.kv_heads;
 }
 
 // A walk over a CTA's run of units, item by item.  An item's units are its key
 // tiles and, after them, its EXTRA.
-template <int BT, int EXTRA>
+template <int BT, int EXTRA, int MODE>
 struct Walk {
   int r, rt, kh, nrt;
   Request q;
@@ -128,7 +146,7 @@ struct Walk {
   int k;  // key tile inside the item
 
   __device__ __forceinline__ void enter(const PagedArgs& a, int g, int RT) {
-    q = load_request(a, r);
+    q = load_request<MODE>(a, r);
     nrt = row_tiles(q, g, RT);
   }
   // Start at unit x of request r; k may be past the last tile (in the EXTRA).
@@ -136,7 +154,7 @@ struct Walk {
     r = r_;
     enter(a, g, RT);
     for (rt = 0;; ++rt) {
-      t = row_tile<BT>(a, q, g, RT, rt);
+      t = row_tile<BT, MODE>(a, q, g, RT, rt);
       const long long w = static_cast<long long>(t.nt + EXTRA) * a.kv_heads;
       if (x < w || rt + 1 >= nrt) break;
       x -= w;
@@ -158,7 +176,7 @@ struct Walk {
         enter(a, g, RT);
       } while (nrt == 0 && r + 1 < a.n_req);
     }
-    t = row_tile<BT>(a, q, g, RT, rt);
+    t = row_tile<BT, MODE>(a, q, g, RT, rt);
   }
 };
 
@@ -179,7 +197,7 @@ struct Run {
   bool stop;
 };
 
-template <int BT, int EXTRA, int kThreads>
+template <int BT, int EXTRA, int MODE, int kThreads>
 __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void* scratch,
                                         const volatile int* abort_flag) {
   long long* s_sum = static_cast<long long*>(scratch);  // [kThreads / 32], then the location
@@ -187,7 +205,7 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
   const int per = (a.n_req + kThreads - 1) / kThreads;
   const int i0 = tid * per, i1 = i0 + per < a.n_req ? i0 + per : a.n_req;
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_units<BT, EXTRA>(a, i, g, RT);
+  for (int i = i0; i < i1; ++i) mine += request_units<BT, EXTRA, MODE>(a, i, g, RT);
   long long x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -219,7 +237,7 @@ __device__ __forceinline__ Run find_run(const PagedArgs& a, int g, int RT, void*
     long long at = run.first - before;
     int i = i0;
     for (; i + 1 < i1; ++i) {
-      const long long u = request_units<BT, EXTRA>(a, i, g, RT);
+      const long long u = request_units<BT, EXTRA, MODE>(a, i, g, RT);
       if (at < u) break;
       at -= u;
     }

@@ -123,6 +123,104 @@ int page_map(CUtensorMap* map, const void* base, int n_pages, int page_size, lon
   return RA_OK;
 }
 
+// The same of pages in 8 bits: a box is a head's whole rows.  A row is 128 bytes,
+// or 64 at d = 64, and as much is fetched to L2 (see above).
+int page_map_fp8(CUtensorMap* map, const void* base, int n_pages, int page_size, long long page_stride,
+                 int kv_heads, int d) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(kv_heads),
+                              static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(kv_heads) * d,
+                                 static_cast<cuuint64_t>(page_stride)};
+  const int most = ra::paged_fp8_box_rows();
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), 1, static_cast<cuuint32_t>(page_size < most ? page_size : most), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        d == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled (8-bit pages) failed (CUresult %d)", (int)r);
+  return RA_OK;
+}
+
+// What the decode calls share: the checks of everything but the pages, which
+// fill a.
+int decode_args(ra::PagedArgs& a, const void* q, void* out, float* lse, long long T, int n_req, int n_q, const int* cu_q,
+                const int* block_table, int max_pages, const int* lengths, int n_pages, int page_size, long long window,
+                int d, int heads, int kv_heads, int dtype, int out_dtype) {
+  int rc;
+  if ((rc = check_common(d, heads, dtype)) != RA_OK) return rc;
+  if ((rc = check_heads(heads, kv_heads)) != RA_OK) return rc;
+  if (dtype != RA_BF16) return fail(RA_ERR_UNSUPPORTED, "the paged decode takes bf16 q and pages");
+  if (out_dtype != RA_F32 && out_dtype != RA_BF16) return fail(RA_ERR_INVALID, "out_dtype %d is not RA_F32 or RA_BF16", out_dtype);
+  if (heads / kv_heads > 128)
+    return fail(RA_ERR_UNSUPPORTED, "heads / kv_heads = %d query heads per KV head exceeds 128", heads / kv_heads);
+  if ((rc = check_table(n_req, max_pages, page_size, &a.page_shift)) != RA_OK) return rc;
+  if (n_pages < 0) return fail(RA_ERR_INVALID, "n_pages=%d is negative", n_pages);
+  if (T < 0 || T > kMaxInt) return fail(RA_ERR_INVALID, "T=%lld out of range [0, 2^31 - 1]", T);
+  if (n_q < 0) return fail(RA_ERR_INVALID, "n_q=%d is negative", n_q);
+  if (!cu_q && static_cast<long long>(n_req) * n_q != T)
+    return fail(RA_ERR_INVALID, "T=%lld is not n_req * n_q = %d * %d (and cu_q is NULL)", T, n_req, n_q);
+  if (T * heads > kMaxInt - 255) return fail(RA_ERR_UNSUPPORTED, "T * heads = %lld rows exceeds 2^31 - 256", T * heads);
+  if (window < 0) return fail(RA_ERR_INVALID, "window=%lld is negative", window);
+  a.q = q;
+  a.block_table = block_table;
+  a.lengths = lengths;
+  a.cu_q = cu_q;
+  a.out = out;
+  a.lse = lse;
+  a.T = T;
+  a.n_q = !cu_q || n_q > 0 || n_req == 0 ? n_q : (T + n_req - 1) / n_req;
+  a.window = window > kMaxInt ? 0 : window;  // wider than any sequence
+  a.out_bf16 = out_dtype == RA_BF16;
+  a.n_req = n_req;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+  a.wait_limit = kWaitLimit;
+  return RA_OK;
+}
+
+int decode_pointers(const ra::PagedArgs& a, std::initializer_list<const void*> pages) {
+  int rc;
+  if ((rc = check_ptrs({a.q, a.out, a.lse})) != RA_OK) return rc;
+  if (a.n_pages > 0 && (rc = check_ptrs(pages)) != RA_OK) return rc;
+  if ((rc = check_words({a.block_table, a.lengths}, 4)) != RA_OK) return rc;
+  if (a.cu_q && !aligned(a.cu_q, 4)) return fail(RA_ERR_INVALID, "cu_q is not 4-byte aligned");
+  return RA_OK;
+}
+
+// Scratch, the decode over the pages and the launch that joins its cut items.
+int decode_launch(ra::PagedArgs& a, int d, int rt, const CUtensorMap& tk, const CUtensorMap& tv, bool fp8, void* stream) {
+  const int ctas = (rt == 128 ? 1 : 2) * ra::sm_count();
+  const size_t rows = static_cast<size_t>(2) * ctas * rt;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* part = nullptr;
+  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));
+  }
+  a.po = part;
+  a.pm = part + rows * d;
+  a.pl = a.pm + rows;
+  a.cuts = a.pl + rows;
+  {
+    TraceScope ts(fp8 ? RA_KERNEL_PAGED_DECODE_FP8 : RA_KERNEL_PAGED_DECODE, st);
+    e = fp8 ? ra::launch_paged_fp8(a, d, ctas, rt, tk, tv, st) : ra::launch_paged_decode(a, d, ctas, rt, tk, tv, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (e == cudaSuccess) {
+    TraceScope ts(RA_KERNEL_PAGED_COMBINE, st);
+    e = ra::launch_paged_combine(a, d, ctas, rt, st);
+    ts.done(e == cudaSuccess);
+  }
+  const cudaError_t ef = cudaFreeAsync(part, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged-decode launch");
+  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
+}
+
 // What the three rope calls share.
 int rope_common(ra::RopeArgs& a, long long T, int d, int heads, int kv_heads, int dtype, int rot,
                 int interleaved, const void* phases, const void* qw, const void* kw, int w_dtype,
@@ -504,78 +602,45 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     long long k_page_stride, long long v_page_stride, long long window, int d,
                     int heads, int kv_heads, int dtype, int out_dtype, void* stream) {
   ra::PagedArgs a{};
-  int rc;
-  if ((rc = check_common(d, heads, dtype)) != RA_OK) return rc;
-  if ((rc = check_heads(heads, kv_heads)) != RA_OK) return rc;
-  if (dtype != RA_BF16) return fail(RA_ERR_UNSUPPORTED, "the paged decode takes bf16 q and pages");
-  if (out_dtype != RA_F32 && out_dtype != RA_BF16) return fail(RA_ERR_INVALID, "out_dtype %d is not RA_F32 or RA_BF16", out_dtype);
-  if (heads / kv_heads > 128)
-    return fail(RA_ERR_UNSUPPORTED, "heads / kv_heads = %d query heads per KV head exceeds 128", heads / kv_heads);
-  if ((rc = check_table(n_req, max_pages, page_size, &a.page_shift)) != RA_OK) return rc;
-  if (n_pages < 0) return fail(RA_ERR_INVALID, "n_pages=%d is negative", n_pages);
-  if (T < 0 || T > kMaxInt) return fail(RA_ERR_INVALID, "T=%lld out of range [0, 2^31 - 1]", T);
-  if (n_q < 0) return fail(RA_ERR_INVALID, "n_q=%d is negative", n_q);
-  if (!cu_q && static_cast<long long>(n_req) * n_q != T)
-    return fail(RA_ERR_INVALID, "T=%lld is not n_req * n_q = %d * %d (and cu_q is NULL)", T, n_req, n_q);
-  if (T * heads > kMaxInt - 255) return fail(RA_ERR_UNSUPPORTED, "T * heads = %lld rows exceeds 2^31 - 256", T * heads);
-  if (window < 0) return fail(RA_ERR_INVALID, "window=%lld is negative", window);
+  int rc = decode_args(a, q, out, lse, T, n_req, n_q, cu_q, block_table, max_pages, lengths, n_pages, page_size, window,
+                       d, heads, kv_heads, dtype, out_dtype);
+  if (rc != RA_OK) return rc;
   const long long page_elems = static_cast<long long>(page_size) * kv_heads * d;
   if ((rc = check_cache("k_page_stride", k_page_stride, page_elems)) != RA_OK) return rc;
   if ((rc = check_cache("v_page_stride", v_page_stride, page_elems)) != RA_OK) return rc;
   if (T == 0 || n_req == 0) return RA_OK;
-  if ((rc = check_ptrs({q, out, lse})) != RA_OK) return rc;
-  if (n_pages > 0 && (rc = check_ptrs({k_cache, v_cache})) != RA_OK) return rc;
-  if ((rc = check_words({block_table, lengths}, 4)) != RA_OK) return rc;
-  if (cu_q && !aligned(cu_q, 4)) return fail(RA_ERR_INVALID, "cu_q is not 4-byte aligned");
-  a.q = q;
-  a.block_table = block_table;
-  a.lengths = lengths;
-  a.cu_q = cu_q;
-  a.out = out;
-  a.lse = lse;
-  a.T = T;
-  a.n_q = !cu_q || n_q > 0 ? n_q : (T + n_req - 1) / n_req;
-  a.window = window > kMaxInt ? 0 : window;  // wider than any sequence
-  a.out_bf16 = out_dtype == RA_BF16;
-  a.n_req = n_req;
-  a.max_pages = max_pages;
-  a.n_pages = n_pages;
-  a.heads = heads;
-  a.kv_heads = kv_heads;
-  a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
-  a.wait_limit = kWaitLimit;
+  if ((rc = decode_pointers(a, {k_cache, v_cache})) != RA_OK) return rc;
   if ((rc = get_encoder()) != RA_OK) return rc;
   CUtensorMap tk, tv;
   // Without pages no load is ever issued; the maps still need an address.
   if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
-  const int rt = ra::paged_row_tile(a, d);
-  const int ctas = (rt == 128 ? 1 : 2) * ra::sm_count();
-  const size_t rows = static_cast<size_t>(2) * ctas * rt;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  float* part = nullptr;
-  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));
-  }
-  a.po = part;
-  a.pm = part + rows * d;
-  a.pl = a.pm + rows;
-  a.cuts = a.pl + rows;
-  {
-    TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
-    e = ra::launch_paged_decode(a, d, ctas, rt, tk, tv, st);
-    ts.done(e == cudaSuccess);
-  }
-  if (e == cudaSuccess) {
-    TraceScope ts(RA_KERNEL_PAGED_COMBINE, st);
-    e = ra::launch_paged_combine(a, d, ctas, rt, st);
-    ts.done(e == cudaSuccess);
-  }
-  const cudaError_t ef = cudaFreeAsync(part, st);
-  if (e != cudaSuccess) return cuda_fail(e, "paged-decode launch");
-  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
+  return decode_launch(a, d, ra::paged_row_tile(a, d), tk, tv, false, stream);
+}
+
+int ra_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                        const void* v_scale, void* out, float* lse, long long T, int n_req, int n_q,
+                        const int* cu_q, const int* block_table, int max_pages, const int* lengths,
+                        int n_pages, int page_size, long long k_page_stride,
+                        long long v_page_stride, long long k_scale_stride,
+                        long long v_scale_stride, long long window, int d, int heads, int kv_heads,
+                        int dtype, int out_dtype, void* stream) {
+  ra::PagedArgs a{};
+  int rc = decode_args(a, q, out, lse, T, n_req, n_q, cu_q, block_table, max_pages, lengths, n_pages, page_size, window,
+                       d, heads, kv_heads, dtype, out_dtype);
+  if (rc != RA_OK) return rc;
+  if ((rc = check_pages_fp8(page_size, kv_heads, d, k_page_stride, v_page_stride, k_scale_stride, v_scale_stride)) != RA_OK) return rc;
+  if (T == 0 || n_req == 0) return RA_OK;
+  if ((rc = decode_pointers(a, {k_cache, v_cache, k_scale, v_scale})) != RA_OK) return rc;
+  a.ks = static_cast<const uint8_t*>(k_scale);
+  a.vs = static_cast<const uint8_t*>(v_scale);
+  a.ks_page = k_scale_stride;
+  a.vs_page = v_scale_stride;
+  if ((rc = get_encoder()) != RA_OK) return rc;
+  CUtensorMap tk, tv;
+  if ((rc = page_map_fp8(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
+  if ((rc = page_map_fp8(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
+  return decode_launch(a, d, ra::paged_fp8_row_tile(a), tk, tv, true, stream);
 }
 
 }  // extern "C"

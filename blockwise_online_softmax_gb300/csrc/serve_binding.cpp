@@ -632,54 +632,101 @@ PyObject* read_fp8(PyObject* const* a) {
   return pack({&ko, &vo});
 }
 
+// The arguments that the decode calls share, from q, the pages' shape, block_table
+// to lse.
+struct Decode {
+  const Tensor &q, &kc, &tab, &len;
+  const Tensor* cu;
+  int expect;
+  Out out, lse;
+  int64_t n, T;
+  int heads, d, kv_heads, dev = 0;
+
+  // a: block_table, lengths, cu_q, n_q; o: out, lse
+  Decode(PyObject* q_, PyObject* kc_, PyObject* const* a, PyObject* const* o)
+      : q(tensor(q_, "q")), kc(tensor(kc_, "k_cache")), tab(tensor(a[0], "block_table")), len(tensor(a[1], "lengths")),
+        cu(maybe(a[2], "cu_q")), expect(small(a[3], "n_q")), out(o[0], "out"), lse(o[1], "lse") {
+    if (q.dim() != 3) refuse(PyExc_ValueError, "q: [T, heads, d]");
+    if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache: [n_pages, page_size, kv_heads, d]");
+    n = len.numel();
+    T = q.size(0);
+    heads = to_int(q.size(1), "heads");
+    d = to_int(q.size(2), "d");
+    kv_heads = to_int(kc.size(2), "kv_heads");
+    if (!cu && (n ? T % n != 0 : T != 0))
+      refuse(PyExc_ValueError, "T=%lld rows are not a multiple of %lld requests (and cu_q is None)",
+             static_cast<long long>(T), static_cast<long long>(n));
+    if (!cu && expect && expect * n != T)
+      refuse(PyExc_ValueError, "n_q=%d rows for each of %lld requests are not the %lld of q (and cu_q is None)", expect,
+             static_cast<long long>(n), static_cast<long long>(T));
+    if (out.t) {
+      if (out.t->sizes() != q.sizes())
+        refuse(PyExc_ValueError, "out must have shape %s, got %s", shape_of(q).c_str(), shape_of(*out.t).c_str());
+      if (out.t->scalar_type() != ScalarType::Float && out.t->scalar_type() != ScalarType::BFloat16)
+        refuse(PyExc_TypeError, "out must be float32 or bfloat16, got %s", type_name(out.t->scalar_type()));
+    }
+    if (lse.t && (lse.t->dim() != 2 || lse.t->size(0) != T || lse.t->size(1) != heads))
+      refuse(PyExc_ValueError, "lse must have shape (%lld, %d), got %s", static_cast<long long>(T), heads,
+             shape_of(*lse.t).c_str());
+    dev = device_of(q, "q");
+  }
+  // Outputs that were left out.
+  void make(const Place& at) {
+    Block made;
+    made.add(out, q.sizes(), ScalarType::Float);
+    made.add(lse, {T, heads}, ScalarType::Float);
+    made.make(at);
+  }
+  int rows_each() const { return cu ? expect : !n ? 0 : to_int(T / n, "rows per request"); }
+  int type() const { return type_code(out.t->scalar_type()); }
+  void* out_ptr() const { return dense(*out.t, "out", dev, out.t->scalar_type()); }
+  float* lse_ptr() const { return static_cast<float*>(dense(*lse.t, "lse", dev, ScalarType::Float)); }
+};
+
 // q, k_cache, v_cache, block_table, lengths, cu_q, n_q, window, out, lse, stream
 PyObject* decode(PyObject* const* a) {
-  const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
-  const Tensor &tab = tensor(a[3], "block_table"), &len = tensor(a[4], "lengths");
-  const Tensor* cu = maybe(a[5], "cu_q");
-  const int expect = small(a[6], "n_q");
+  const Tensor& vc = tensor(a[2], "v_cache");
+  Decode x(a[0], a[1], a + 3, a + 8);
   const long long window = integer(a[7]);
-  Out out(a[8], "out"), lse(a[9], "lse");
-  if (q.dim() != 3) refuse(PyExc_ValueError, "q: [T, heads, d]");
-  if (kc.dim() != 4) refuse(PyExc_ValueError, "k_cache: [n_pages, page_size, kv_heads, d]");
-  const int64_t n = len.numel(), T = q.size(0);
-  const int heads = to_int(q.size(1), "heads"), d = to_int(q.size(2), "d"), kv_heads = to_int(kc.size(2), "kv_heads");
-  if (!cu && (n ? T % n != 0 : T != 0))
-    refuse(PyExc_ValueError, "T=%lld rows are not a multiple of %lld requests (and cu_q is None)",
-           static_cast<long long>(T), static_cast<long long>(n));
-  if (!cu && expect && expect * n != T)
-    refuse(PyExc_ValueError, "n_q=%d rows for each of %lld requests are not the %lld of q (and cu_q is None)", expect,
-           static_cast<long long>(n), static_cast<long long>(T));
-  if (out.t) {
-    if (out.t->sizes() != q.sizes())
-      refuse(PyExc_ValueError, "out must have shape %s, got %s", shape_of(q).c_str(), shape_of(*out.t).c_str());
-    if (out.t->scalar_type() != ScalarType::Float && out.t->scalar_type() != ScalarType::BFloat16)
-      refuse(PyExc_TypeError, "out must be float32 or bfloat16, got %s", type_name(out.t->scalar_type()));
-  }
-  if (lse.t && (lse.t->dim() != 2 || lse.t->size(0) != T || lse.t->size(1) != heads))
-    refuse(PyExc_ValueError, "lse must have shape (%lld, %d), got %s", static_cast<long long>(T), heads,
-           shape_of(*lse.t).c_str());
-  const int dev = device_of(q, "q");
-  const void* pq = dense(q, "q", dev, ScalarType::BFloat16);
-  const Cache ck = cache(kc, "k_cache", kv_heads, d, dev), cv = cache(vc, "v_cache", kv_heads, d, dev);
+  const void* pq = dense(x.q, "q", x.dev, ScalarType::BFloat16);
+  const Cache ck = cache(x.kc, "k_cache", x.kv_heads, x.d, x.dev), cv = cache(vc, "v_cache", x.kv_heads, x.d, x.dev);
   same_pages(ck, cv);
-  const Table tb = block_table(tab, n, dev);
-  const int* pc = cu ? ints(*cu, "cu_q", n + 1, dev) : nullptr;
-  const int* pl = ints(len, "lengths", n, dev);
-  Block made;
-  made.add(out, q.sizes(), ScalarType::Float);
-  made.add(lse, {T, heads}, ScalarType::Float);
-  const Place at(dev, a[10]);
-  made.make(at);
-  const Tensor& to = *out.t;
-  void* po = dense(to, "out", dev, to.scalar_type());
-  auto* ps = static_cast<float*>(dense(*lse.t, "lse", dev, ScalarType::Float));
-  const int n_q = cu ? expect : !n ? 0 : to_int(T / n, "rows per request"), code = type_code(to.scalar_type());
+  const Table tb = block_table(x.tab, x.n, x.dev);
+  const int* pc = x.cu ? ints(*x.cu, "cu_q", x.n + 1, x.dev) : nullptr;
+  const int* pl = ints(x.len, "lengths", x.n, x.dev);
+  const Place at(x.dev, a[10]);
+  x.make(at);
+  void* po = x.out_ptr();
+  float* ps = x.lse_ptr();
+  const int n_q = x.rows_each();
   call(at, [&](void* st) {
-    return ra_paged_decode(pq, ck.p, cv.p, po, ps, T, tb.n_req, n_q, pc, tb.p, tb.width, pl, ck.pages, ck.page_size,
-                           ck.stride, cv.stride, window, d, heads, kv_heads, RA_BF16, code, st);
+    return ra_paged_decode(pq, ck.p, cv.p, po, ps, x.T, tb.n_req, n_q, pc, tb.p, tb.width, pl, ck.pages, ck.page_size,
+                           ck.stride, cv.stride, window, x.d, x.heads, x.kv_heads, RA_BF16, x.type(), st);
   });
-  return pack({&out, &lse});
+  return pack({&x.out, &x.lse});
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_q, n_q, window,
+// out, lse, stream
+PyObject* decode_fp8(PyObject* const* a) {
+  Decode x(a[0], a[1], a + 5, a + 10);
+  const long long window = integer(a[9]);
+  const void* pq = dense(x.q, "q", x.dev, ScalarType::BFloat16);
+  const Pages8 pg = pages8(a + 1, x.kv_heads, x.d, x.dev);
+  const Table tb = block_table(x.tab, x.n, x.dev);
+  const int* pc = x.cu ? ints(*x.cu, "cu_q", x.n + 1, x.dev) : nullptr;
+  const int* pl = ints(x.len, "lengths", x.n, x.dev);
+  const Place at(x.dev, a[12]);
+  x.make(at);
+  void* po = x.out_ptr();
+  float* ps = x.lse_ptr();
+  const int n_q = x.rows_each();
+  call(at, [&](void* st) {
+    return ra_paged_decode_fp8(pq, pg.k.p, pg.v.p, pg.ks.p, pg.vs.p, po, ps, x.T, tb.n_req, n_q, pc, tb.p, tb.width, pl,
+                               pg.k.pages, pg.k.page_size, pg.k.stride, pg.v.stride, pg.ks.stride, pg.vs.stride, window,
+                               x.d, x.heads, x.kv_heads, RA_BF16, x.type(), st);
+  });
+  return pack({&x.out, &x.lse});
 }
 
 PyObject* on_status(PyObject*, PyObject* f) {
@@ -700,6 +747,7 @@ RA_ENTRY(append, 15)
 RA_ENTRY(decode, 11)
 RA_ENTRY(append_fp8, 17)
 RA_ENTRY(read_fp8, 11)
+RA_ENTRY(decode_fp8, 13)
 #undef RA_ENTRY
 
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
@@ -715,6 +763,7 @@ PyMethodDef g_methods[] = {
     {"paged_append", fast(append_entry), METH_FASTCALL, nullptr},
     {"paged_decode", fast(decode_entry), METH_FASTCALL, nullptr},
     {"paged_append_fp8", fast(append_fp8_entry), METH_FASTCALL, nullptr},
+    {"paged_decode_fp8", fast(decode_fp8_entry), METH_FASTCALL, nullptr},
     {"paged_read_fp8", fast(read_fp8_entry), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

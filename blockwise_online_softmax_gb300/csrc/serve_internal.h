@@ -160,6 +160,17 @@ struct PagedArgs {
   float* pm;
   float* pl;
   void* cuts;
+  // Pages in 8 bits: their scales, bytes from page to page.
+  const uint8_t* ks;
+  const uint8_t* vs;
+  long long ks_page, vs_page;
+  // With a shared prefix.  Both launches leave states only: those of items that
+  // are not cut at index whole + row of po, pm, pl, and in parts[row] where the
+  // row's states are: {0, 0} there, or {index of the first, how many}.
+  long long whole;
+  int2* parts;        // [T * heads]
+  const int* cu_req;  // the shared launch, whose requests are groups: the requests of each
+  int n_own;          // requests
 };
 // Query rows (of one request and KV head) that a CTA takes together: 8 or 16
 // (paged_kernel.cu, two CTAs per SM) or 128 (paged_tc_kernel.cu, one).
@@ -172,6 +183,14 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_til
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st);
 cudaError_t launch_paged_tc(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk,
                             const CUtensorMap& tv, cudaStream_t st);
+// Over pages in 8 bits: row tiles of 8 or 16, two CTAs per SM, the same joining
+// launch; tk, tv as above with a box of a whole row, page_size or
+// paged_fp8_box_rows() rows.
+int paged_fp8_row_tile(const PagedArgs& a);
+int paged_fp8_box_rows();
+cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t st);
+cudaError_t take_paged_fp8_status(int* code);
 cudaError_t take_paged_status(int* code);
 cudaError_t take_paged_tc_status(int* code);
 

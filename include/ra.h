@@ -129,7 +129,8 @@ typedef enum {
   RA_KERNEL_PAGED_COMBINE = 19,   /* joins the parts of a request that several CTAs took */
   RA_KERNEL_PAGED_APPEND_FP8 = 20, /* kind 17 with k and v held in 8 bits */
   RA_KERNEL_PAGED_READ_FP8 = 21,  /* 8-bit pages as dense bf16 rows */
-  RA_KERNEL_KINDS = 22
+  RA_KERNEL_PAGED_DECODE_FP8 = 22, /* attention over 8-bit pages */
+  RA_KERNEL_KINDS = 23
 } ra_kernel_kind;
 
 /*
@@ -584,6 +585,14 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     `tokens` are left as they were; a row before its request's first token,
  *     or in a page outside [0, n_pages), is zero.
  *   cu_k: device int32 [n_req + 1], nondecreasing.
+ *
+ * ra_paged_decode_fp8 -- ra_paged_decode over pages in 8 bits, with q, out and
+ * everything else as there (bf16 q; lengths include the new tokens).  Scores
+ * and weights have fp32's precision: the result differs from that of
+ * ra_paged_decode over the same values in bf16 by fp32 roundings.  Query rows
+ * of a request and KV head are taken 16 at a time, and each 16 read its pages
+ * again: for a few new tokens (for the chunks of a prompt, ra_paged_read_fp8 and
+ * ra_decode_forward).
  */
 int ra_paged_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
                         void* v_cache, void* k_scale, void* v_scale, long long T, int d, int heads,
@@ -600,6 +609,14 @@ int ra_paged_read_fp8(const void* k_cache, const void* v_cache, const void* k_sc
                       int n_pages, int page_size, long long k_page_stride, long long v_page_stride,
                       long long k_scale_stride, long long v_scale_stride, int d, int kv_heads,
                       void* stream);
+
+int ra_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                        const void* v_scale, void* out, float* lse, long long T, int n_req, int n_q,
+                        const int* cu_q, const int* block_table, int max_pages, const int* lengths,
+                        int n_pages, int page_size, long long k_page_stride,
+                        long long v_page_stride, long long k_scale_stride,
+                        long long v_scale_stride, long long window, int d, int heads, int kv_heads,
+                        int dtype, int out_dtype, void* stream);
 
 /*
  * ra_device_status -- synchronize `stream`, then read and clear the

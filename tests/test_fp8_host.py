@@ -97,3 +97,49 @@ def test_the_plain_quantisation_is_the_types():
     assert float(y.abs().max()) <= 448 and (y.abs().amax(1) > 224)[np.arange(4000) != 5][:4].all()
     np.testing.assert_array_equal(val, y.float().to(torch.float8_e4m3fn).double().numpy())
     assert e[5] == -117
+
+
+DECODE = dict(q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, out=FAKE, lse=FAKE, T=8, n_req=4, n_q=2,
+              cu_q=0, table=FAKE, max_pages=8, lengths=FAKE, n_pages=10, page_size=16, kps=4096,
+              vps=4096, kss=32, vss=32, window=0, d=128, heads=4, kv_heads=2, dtype=1, out_dtype=0,
+              stream=None)
+
+
+@pytest.mark.parametrize("change, code, msg", [
+    (dict(dtype=0), -2, b"bf16"),
+    (dict(out_dtype=2), -1, b"out_dtype"),
+    (dict(d=80), -2, b"head dim"),
+    (dict(heads=5), -1, b"multiple of kv_heads"),
+    (dict(heads=258, kv_heads=2), -2, b"exceeds 128"),
+    (dict(T=7), -1, b"n_req * n_q"),
+    (dict(n_q=-1), -1, b"n_q"),
+    (dict(T=1 << 30, n_req=1 << 29, max_pages=1), -2, b"T * heads"),
+    (dict(window=-1), -1, b"window"),
+    (dict(page_size=8), -2, b"page_size=8 (pages in 8 bits"),
+    (dict(kps=4095), -1, b"k_page_stride"),
+    (dict(vss=16), -1, b"v_scale_stride"),
+    (dict(cu_q=FAKE + 1), -1, b"cu_q"),
+    (dict(table=0), -1, b"NULL"),
+    (dict(q=FAKE + 8), -1, b"aligned"),
+    (dict(ks=FAKE + 4), -1, b"aligned"),
+])
+def test_decode_refusals(lib, change, code, msg):  # noqa: F811
+    refused(lib, lib.ra_paged_decode_fp8(*{**DECODE, **change}.values()), code, msg)
+
+
+def test_empty_decode_is_a_no_op(lib):  # noqa: F811
+    assert lib.ra_paged_decode_fp8(*{**DECODE, "T": 0, "n_req": 0, "n_q": 0, "q": 0}.values()) == 0
+    assert lib.ra_paged_decode_fp8(*{**DECODE, "T": 0, "cu_q": FAKE, "ks": 0}.values()) == 0
+
+
+def test_two_halves_hold_a_weight():
+    """The weight's two fp16 terms, as the decode forms them: what they leave is
+    at most 2^-23 of it where the first is in fp16's normal range, else 2^-25
+    absolute, of weights scaled to at most 2^15."""
+    rng = np.random.default_rng(2)
+    w = (rng.uniform(1, 2, 200000) * 2.0 ** rng.integers(-30, 15, 200000)).astype(np.float32)
+    hi = w.astype(np.float16).astype(np.float32)
+    lo = (w - hi).astype(np.float16).astype(np.float32)
+    left = np.abs(w.astype(np.float64) - hi - lo)
+    assert (left <= np.maximum(2.0 ** -23 * w, 2.0 ** -25)).all()
+    assert np.abs(w - hi).max() > 2.0 ** -13 * 2.0 ** 14  # one term alone does not
