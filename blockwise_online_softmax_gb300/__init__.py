@@ -22,6 +22,7 @@ from .binding import (  # noqa: E402,F401
     ra_paged_append_fp8,
     ra_paged_decode,
     ra_paged_decode_fp8,
+    ra_paged_decode_prefix,
     ra_paged_extend,
     ra_paged_read_fp8,
     ra_paged_release,

@@ -52,6 +52,7 @@ KERNEL_KINDS = {
     "paged_append_fp8": 20,
     "paged_read_fp8": 21,
     "paged_decode_fp8": 22,
+    "paged_prefix": 23,
 }
 
 _lock = threading.Lock()
@@ -90,6 +91,7 @@ _SIGNATURES = {
     "ra_paged_append_fp8": ("PPPPPPPPLiiiLLLiiLLLLPPiiPfPPifiP", "i"),
     "ra_paged_read_fp8": ("PPPPPPLiPPiPiiLLLLiiP", "i"),
     "ra_paged_decode_fp8": ("PPPPPPPLiiPPiPiiLLLLLiiiiiP", "i"),
+    "ra_paged_decode_prefix": ("PPPPPLiPPiPiiPPiPiiLLiiiiiP", "i"),
     "ra_device_status": ("P", "i"),
     "ra_selftest_wait_timeout": ("LP", "i"),
     "ra_cached_memory": ("P", "i"),
@@ -626,6 +628,21 @@ def ra_paged_append_fp8(q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slo
     return (_serve or _fast()).paged_append_fp8(
         q, k, v, phases, k_cache, v_cache, k_scale, v_scale, slots, positions, q_weight, k_weight,
         eps, interleaved, mscale, q_out, stream)
+
+
+def ra_paged_decode_prefix(q, k_cache, v_cache, prefix_table, prefix_lengths, cu_req, block_table,
+                           lengths, *, cu_q=None, n_q: int = 0, out=None, lse=None, stream=None):
+    """ra_paged_decode for requests that share prefixes, whose keys are read
+    once for all of them.  Group p is the requests [cu_req[p], cu_req[p + 1])
+    (int32 [n_groups + 1]); its prefix of prefix_lengths[p] tokens (int32
+    [n_groups], any length) lies in pages prefix_table[p] (int32 [n_groups,
+    max_prefix_pages]).  block_table and lengths are of the requests' own
+    tokens, the new ones included, which stand behind the prefix: add its
+    length to their positions.  Everything else, the returned (out, lse) too,
+    as in ra_paged_decode, without a window."""
+    return (_serve or _fast()).paged_decode_prefix(
+        q, k_cache, v_cache, prefix_table, prefix_lengths, cu_req, block_table, lengths, cu_q, n_q,
+        out, lse, stream)
 
 
 def ra_paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, *, cu_q=None,

@@ -32,6 +32,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -91,7 +92,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
-  let_next_start();
+  start_early<MODE>();
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(kfull(s), 1);
@@ -109,20 +110,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     *abort_flag = abort;
     fence_mbar_init();
   }
-  wait_for_previous();
+  start_wait<MODE>();
   if (MODE == kPlain && tid == 0) static_cast<Cut*>(a.cuts)[blockIdx.x].last = -1;
   const Run run = find_run<BT, kExtra, MODE, kThreads>(a, g, RT, smem + C::OFF_BUF, abort_flag);  // synchronizes
-  if (run.first >= run.last || run.stop) return;
+  if (run.first >= run.last || run.stop) return end_wait<MODE>();
   const long long lim = a.wait_limit;
 
   if (warp >= kCons) {
     // ---------------------------------------------------------------- producers
     regs_dec<C::PROD_REGS>();
-    if (warp >= kCons + 2) return;
+    if (warp >= kCons + 2) return end_wait<MODE>();
     const bool is_k = warp == kCons;
     produce<C, MODE>(a, is_k ? static_cast<const void*>(&tmK) : static_cast<const void*>(&tmV), is_k, run, g, smem, sb, lane,
                      abort_flag, &g_paged_status);
-    return;
+    return end_wait<MODE>();
   }
 
   // ------------------------------------------------------------------ consumers
@@ -292,11 +293,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         par ^= 1u;
       }
     }
-    if (!join_warps<D, NT, false, MODE>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) return;
-    if (item.last) return;
+    if (!join_warps<D, NT, false, MODE>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) break;
+    if (item.last) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));
   }
+  end_wait<MODE>();
 }
 
 // Joins the partial states of the item that CTA c = blockIdx.x began and
@@ -385,6 +387,99 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   }
 }
 
+// Joins the states of a row from two launches (kOwn, kShared): a warp a row.  Its
+// lanes take a partial each for the maximum and the weights, so that the rows of
+// the partials, a lane D / 32 columns, are requested without waiting for one
+// another; they are added in the order of the CTAs.
+constexpr int kRowWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kRowWarps)
+paged_join_kernel(const PagedArgs own, const PagedArgs shared, int own_tile, int shared_tile) {
+  constexpr int CPL = D / 32;
+  let_next_start();
+  wait_for_previous();
+  const int lane = threadIdx.x & 31;
+  long long first = 0, end = own.T;
+  if (own.cu_q) {
+    first = own.cu_q[0] < 0 ? 0 : own.cu_q[0];
+    if (own.cu_q[own.n_req] < end) end = own.cu_q[own.n_req];
+  }
+  first *= own.heads;
+  end *= own.heads;
+  for (long long row = first + static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); row < end;
+       row += static_cast<long long>(gridDim.x) * kRowWarps) {
+    float m = -INFINITY, l = 0.f, acc[CPL] = {};
+    bool also = true;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (!also) break;
+      const PagedArgs& a = side ? shared : own;
+      const int RT = side ? shared_tile : own_tile;
+      const int2 rec = a.parts[row];
+      if (side == 0) also = rec.y & kWithPrefix;
+      const long long slots = a.whole;
+      long long at = a.whole + row;
+      int n = 1;
+      if (rec.x >= 0) {
+        // (Records of rows that arrays in disorder left to nobody must not lead outside.)
+        at = rec.x;
+        n = rec.y & (kWithPrefix - 1);
+        const long long most = (slots - 1 - at) / (2 * RT) + 1;
+        if (at >= slots) n = 0;
+        else if (n > most) n = static_cast<int>(most);
+      }
+      for (int p0 = 0; p0 < n; p0 += 32) {
+        const int p = p0 + lane;
+        const long long mine = p == 0 ? at : at + static_cast<long long>(2 * p - 1) * RT;
+        const float pm = p < n ? a.pm[mine] : -INFINITY, pl = p < n ? a.pl[mine] : 0.f;
+        float mx = pm;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+        const float old = ex2(m - ref), w = ex2(pm - ref);
+        m = mn;
+        float part = p < n ? pl * w : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+        l = fmaf(l, old, part);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[i] *= old;
+        const int np = n - p0 < 32 ? n - p0 : 32;
+#pragma unroll 4
+        for (int q = 0; q < np; ++q) {
+          const float e = __shfl_sync(kAll, w, q);
+          const int x = p0 + q;
+          const float* o = a.po + (x == 0 ? at : at + static_cast<long long>(2 * x - 1) * RT) * D + CPL * lane;
+          if constexpr (CPL == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(o);
+            acc[0] = fmaf(v.x, e, acc[0]), acc[1] = fmaf(v.y, e, acc[1]);
+            acc[2] = fmaf(v.z, e, acc[2]), acc[3] = fmaf(v.w, e, acc[3]);
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(o);
+            acc[0] = fmaf(v.x, e, acc[0]), acc[1] = fmaf(v.y, e, acc[1]);
+          }
+        }
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) acc[i] *= inv;
+    const long long at = row * D + CPL * lane;
+    if (own.out_bf16) {
+      auto* out = static_cast<__nv_bfloat16*>(own.out) + at;
+      if constexpr (CPL == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_rn(acc[0], acc[1]), bf16x2_rn(acc[2], acc[3]));
+      else
+        *reinterpret_cast<uint32_t*>(out) = bf16x2_rn(acc[0], acc[1]);
+    } else {
+      float* out = static_cast<float*>(own.out) + at;
+      if constexpr (CPL == 4) *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      else *reinterpret_cast<float2*>(out) = make_float2(acc[0], acc[1]);
+    }
+    if (lane == 0) own.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  }
+}
+
 template <int D, int NT, int MODE>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
@@ -416,12 +511,26 @@ int paged_row_tile(const PagedArgs& a, int d) {
 
 size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas); }
 
-cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
+cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  if (row_tile == 128) return launch_paged_tc(a, d, ctas, tk, tv, st);
-  if (d == 128)
-    return row_tile == 8 ? decode_t<128, 1, kPlain>(a, ctas, tk, tv, st) : decode_t<128, 2, kPlain>(a, ctas, tk, tv, st);
-  return row_tile == 8 ? decode_t<64, 1, kPlain>(a, ctas, tk, tv, st) : decode_t<64, 2, kPlain>(a, ctas, tk, tv, st);
+  if (row_tile == 128) return launch_paged_tc(a, mode, d, ctas, tk, tv, st);
+  auto run = [&](auto m) {
+    constexpr int MODE = decltype(m)::value;
+    if (d == 128)
+      return row_tile == 8 ? decode_t<128, 1, MODE>(a, ctas, tk, tv, st) : decode_t<128, 2, MODE>(a, ctas, tk, tv, st);
+    return row_tile == 8 ? decode_t<64, 1, MODE>(a, ctas, tk, tv, st) : decode_t<64, 2, MODE>(a, ctas, tk, tv, st);
+  };
+  return mode == kOwn ? run(std::integral_constant<int, kOwn>{})
+                      : (mode == kShared ? run(std::integral_constant<int, kShared>{})
+                                         : run(std::integral_constant<int, kPlain>{}));
+}
+
+cudaError_t launch_paged_join(const PagedArgs& own, const PagedArgs& shared, int d, int own_tile,
+                              int shared_tile, cudaStream_t st) {
+  const long long need = (own.T * own.heads + kRowWarps - 1) / kRowWarps, most = 8LL * sm_count();
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most));
+  return launch_early(d == 128 ? paged_join_kernel<128> : paged_join_kernel<64>, grid, 32 * kRowWarps, 0, st, own, shared,
+                      own_tile, shared_tile);
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {

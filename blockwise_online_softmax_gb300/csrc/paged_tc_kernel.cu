@@ -64,7 +64,7 @@ struct Item {
   int k0;     // first key tile here
   int tiles;  // key tiles here
   int slot;   // partial slot, or -1: the item is whole
-  int pad;
+  int parts;  // CTAs that it is cut between; + kWithPrefix (kOwn)
 };
 
 template <int D>
@@ -125,7 +125,7 @@ __device__ __forceinline__ void drop_high(float& a, float& b) {
   f2unpack(fadd2(f2pack(a, b), f2pack(na, nb)), a, b);
 }
 
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const PagedArgs a) {
@@ -138,8 +138,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   int* const status = &g_paged_tc_status;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.heads / a.kv_heads;
-  Cut* cuts = static_cast<Cut*>(a.cuts);
-  let_next_start();
+  start_early<MODE>();
   if (tid == 0) {
     for (int i = 0; i < C::NBAR; ++i) {
       uint32_t n = 1;
@@ -154,10 +153,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     *abort_flag = abort;
     fence_mbar_init();
   }
-  wait_for_previous();
-  if (tid == 0) cuts[blockIdx.x].last = -1;
-  const Run run = find_run<BT, 0, kPlain, kThreads>(a, g, RT, smem + C::OFF_AL, abort_flag);  // synchronizes
-  if (run.first >= run.last || run.stop) return;
+  start_wait<MODE>();
+  if (MODE == kPlain && tid == 0) static_cast<Cut*>(a.cuts)[blockIdx.x].last = -1;
+  const Run run = find_run<BT, 0, MODE, kThreads>(a, g, RT, smem + C::OFF_AL, abort_flag);  // synchronizes
+  if (run.first >= run.last || run.stop) return end_wait<MODE>();
   if (warp == 14) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -197,7 +196,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int rows = sh < 6 ? 1 << sh : 64;  // of a box
       const int boxes = BT / rows;
       const uint32_t box = static_cast<uint32_t>(rows) * 128u;
-      Walk<BT, 0, kPlain> w;
+      Walk<BT, 0, MODE> w;
       w.start(a, g, RT, run.r, run.x);
       long long u = run.first;
       bool ok = true;
@@ -208,15 +207,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (is_k) {
           if (it >= 2) ok = wait(C::B_IF + (it & 1), static_cast<uint32_t>(it >> 1) ^ 1u, 0x92);
           if (!ok) break;
+          const int joined = MODE == kOwn && with_prefix(a, w.r, lane) ? kWithPrefix : 0;
           if (lane == 0) {
             const long long item0 = u - w.k;
             const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
             const int me = static_cast<int>(blockIdx.x);
             const int base = w.t.t0 * BT, n = w.t.rr1 - w.t.rr0;
-            items[it & 1] = Item{n, w.t.rr0, w.q.row0, w.kh, w.q.len - w.q.n + 1 - base, base,
+            items[it & 1] = Item{n, w.t.rr0, w.q.row0, w.kh, key_end<MODE>(w.q, 0, false) - base, base,
                                  w.t.lo - base, w.t.hi - base, w.k, tiles,
-                                 c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), 0};
-            if (c0 != c1 && me == c0) cuts[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
+                                 c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), c1 - c0 + 1 + joined};
+            if (MODE == kPlain && c0 != c1 && me == c0)
+              static_cast<Cut*>(a.cuts)[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
             mbar_arrive(bar(C::B_I + (it & 1)));
           }
           __syncwarp();
@@ -364,7 +365,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       free_item(it);
       // Keys [lo, hi) of the row (rows past the item's do as its last).
       const int rr = x.rr0 + (r < x.rows ? r : x.rows - 1);
-      int hi = x.end0 + rr / g;
+      int hi = MODE == kShared ? x.end0 : x.end0 + rr / g;
       if (hi < -x.base) hi = -x.base;
       const int lo = win > 0 && hi + x.base > win ? hi - win : -x.base;
       float m = -INFINITY, l = 0.f, alpha = 0.f;
@@ -497,7 +498,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (!ok) break;
           l = fmaf(s_inv[r], alpha, l);
         }
-        s_inv[r] = x.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+        s_inv[r] = MODE != kPlain || x.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
         mbar_arrive(bar(C::B_ML));
         if (r < x.rows) {
           if (x.slot >= 0) {
@@ -505,8 +506,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             a.pl[x.slot * RT + r] = l;
           } else {
             const int j = rr / g;
-            a.lse[static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g)] =
-                l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            const long long row = static_cast<long long>(x.row0 + j) * a.heads + x.kh * g + (rr - j * g);
+            if (MODE != kPlain) {
+              a.pm[a.whole + row] = m;
+              a.pl[a.whole + row] = l;
+            } else {
+              a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+            }
           }
         }
       }
@@ -556,10 +562,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       mbar_arrive(bar(C::B_MLF + (it & 1)));
       if (r >= x.rows) continue;
       const int rr = x.rr0 + r, j0 = rr / g;
-      const long long row = x.slot >= 0 ? static_cast<long long>(x.slot) * RT + r
-                                        : static_cast<long long>(x.row0 + j0) * a.heads + x.kh * g + (rr - j0 * g);
-      const bool bf16 = x.slot < 0 && a.out_bf16;
-      float* dst = (x.slot >= 0 ? a.po : static_cast<float*>(a.out)) + row * D;
+      const long long own_row = static_cast<long long>(x.row0 + j0) * a.heads + x.kh * g + (rr - j0 * g);
+      const long long row = x.slot >= 0 ? static_cast<long long>(x.slot) * RT + r : own_row + (MODE != kPlain ? a.whole : 0);
+      const bool state = MODE != kPlain || x.slot >= 0;
+      if (MODE != kPlain && (x.slot < 0 || (x.slot & 1)))  // not cut, or begun here
+        a.parts[own_row] = part_record(x.slot < 0 ? -1 : x.slot * RT + r, x.parts);
+      const bool bf16 = !state && a.out_bf16;
+      float* dst = (state ? a.po : static_cast<float*>(a.out)) + row * D;
       __nv_bfloat16* dst16 = static_cast<__nv_bfloat16*>(a.out) + row * D;
 #pragma unroll
       for (int j = 0; j < D / 2; j += 4) {
@@ -585,22 +594,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  end_wait<MODE>();
 }
 
-template <int D>
+template <int D, int MODE>
 cudaError_t launch_d(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(paged_tc_kernel<D>, Cfg<D>::SMEM, done);
+  cudaError_t e = allow_smem(paged_tc_kernel<D, MODE>, Cfg<D>::SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_early(paged_tc_kernel<D>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D>::SMEM, st, tk, tv, a);
+  return launch_early(paged_tc_kernel<D, MODE>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D>::SMEM, st, tk, tv, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tc(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk,
+cudaError_t launch_paged_tc(const PagedArgs& a, int mode, int d, int ctas, const CUtensorMap& tk,
                             const CUtensorMap& tv, cudaStream_t st) {
-  return d == 128 ? launch_d<128>(a, ctas, tk, tv, st) : launch_d<64>(a, ctas, tk, tv, st);
+  if (mode == kOwn) return d == 128 ? launch_d<128, kOwn>(a, ctas, tk, tv, st) : launch_d<64, kOwn>(a, ctas, tk, tv, st);
+  if (mode == kShared) return d == 128 ? launch_d<128, kShared>(a, ctas, tk, tv, st) : launch_d<64, kShared>(a, ctas, tk, tv, st);
+  return d == 128 ? launch_d<128, kPlain>(a, ctas, tk, tv, st) : launch_d<64, kPlain>(a, ctas, tk, tv, st);
 }
 
 cudaError_t take_paged_tc_status(int* code) {

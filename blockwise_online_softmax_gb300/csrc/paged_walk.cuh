@@ -50,7 +50,40 @@ struct Request {
 // to themselves (kPlain: finished here; kOwn: partial states of them, for a
 // launch that joins them with others), or all the tokens of a group of requests,
 // which see every key of the group's prefix (kShared: partial states).
-constexpr int kPlain = 0, kOwn = 1, kShared = 2;
+constexpr int kPlain = kPagedPlain, kOwn = kPagedOwn, kShared = kPagedShared;
+
+// With a prefix three launches follow one another: kOwn, kShared, the join.  The
+// first two do not need each other, so kOwn lets the next start only once what was
+// before it is done, and kShared does not wait before its work but after it: its
+// CTAs take the SMs as kOwn's leave them, and its end means the end of both.
+template <int MODE>
+__device__ __forceinline__ void start_early() {
+  if (MODE != kOwn) let_next_start();
+}
+template <int MODE>
+__device__ __forceinline__ void start_wait() {
+  if (MODE != kShared) wait_for_previous();
+  if (MODE == kOwn) let_next_start();
+}
+template <int MODE>
+__device__ __forceinline__ void end_wait() {
+  if (MODE == kShared) wait_for_previous();
+}
+
+// Where the partial states of a row are: `first` and the count, -1 where the item
+// is whole; + kWithPrefix in the rows of kOwn whose request has a prefix.
+constexpr int kWithPrefix = 1 << 20;  // (more than CTAs)
+__device__ __forceinline__ int2 part_record(int first, int parts) { return make_int2(first, parts); }
+// Whether request r is one of a group.  A warp looks through 31 groups at a time.
+__device__ __forceinline__ bool with_prefix(const PagedArgs& a, int r, int lane) {
+  for (int g0 = 0; g0 < a.n_groups; g0 += 31) {
+    const int g = g0 + lane;
+    const int b = g <= a.n_groups ? a.cu_req[g] : 0;
+    const int e = __shfl_down_sync(kAll, b, 1);
+    if (__any_sync(kAll, lane < 31 && g < a.n_groups && b <= r && r < e)) return true;
+  }
+  return false;
+}
 
 template <int MODE>
 __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
@@ -88,10 +121,10 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 
 // Token j of the request sees keys [begin, end).
 template <int MODE>
-__device__ __forceinline__ int key_end(const Request& q, int j) {
+__device__ __forceinline__ int key_end(const Request& q, int j, bool clamp = true) {
   if (MODE == kShared) return q.len;
   const int e = q.len - q.n + j + 1;
-  return e < 0 ? 0 : e;
+  return clamp && e < 0 ? 0 : e;
 }
 __device__ __forceinline__ int key_begin(const PagedArgs& a, int end) {
   return a.window > 0 && end > a.window ? end - static_cast<int>(a.window) : 0;

@@ -208,7 +208,7 @@ int decode_launch(ra::PagedArgs& a, int d, int rt, const CUtensorMap& tk, const 
   a.cuts = a.pl + rows;
   {
     TraceScope ts(fp8 ? RA_KERNEL_PAGED_DECODE_FP8 : RA_KERNEL_PAGED_DECODE, st);
-    e = fp8 ? ra::launch_paged_fp8(a, d, ctas, rt, tk, tv, st) : ra::launch_paged_decode(a, d, ctas, rt, tk, tv, st);
+    e = fp8 ? ra::launch_paged_fp8(a, d, ctas, rt, tk, tv, st) : ra::launch_paged_decode(a, ra::kPagedPlain, d, ctas, rt, tk, tv, st);
     ts.done(e == cudaSuccess);
   }
   if (e == cudaSuccess) {
@@ -616,6 +616,88 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
   if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
   return decode_launch(a, d, ra::paged_row_tile(a, d), tk, tv, false, stream);
+}
+
+int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cache, void* out,
+                           float* lse, long long T, int n_groups, const int* cu_req,
+                           const int* prefix_table, int prefix_max_pages,
+                           const int* prefix_lengths, int n_req, int n_q, const int* cu_q,
+                           const int* block_table, int max_pages, const int* lengths, int n_pages,
+                           int page_size, long long k_page_stride, long long v_page_stride, int d,
+                           int heads, int kv_heads, int dtype, int out_dtype, void* stream) {
+  ra::PagedArgs own{};
+  int rc = decode_args(own, q, out, lse, T, n_req, n_q, cu_q, block_table, max_pages, lengths, n_pages, page_size, 0,
+                       d, heads, kv_heads, dtype, out_dtype);
+  if (rc != RA_OK) return rc;
+  if (n_groups < 0) return fail(RA_ERR_INVALID, "n_groups=%d is negative", n_groups);
+  int shift = 0;
+  if ((rc = check_table(n_groups, prefix_max_pages, page_size, &shift)) != RA_OK) return rc;
+  const long long page_elems = static_cast<long long>(page_size) * kv_heads * d;
+  if ((rc = check_cache("k_page_stride", k_page_stride, page_elems)) != RA_OK) return rc;
+  if ((rc = check_cache("v_page_stride", v_page_stride, page_elems)) != RA_OK) return rc;
+  if (T == 0 || n_req == 0) return RA_OK;
+  if ((rc = decode_pointers(own, {k_cache, v_cache})) != RA_OK) return rc;
+  if (n_groups > 0 && (rc = check_words({cu_req, prefix_table, prefix_lengths}, 4)) != RA_OK) return rc;
+  if ((rc = get_encoder()) != RA_OK) return rc;
+  CUtensorMap tk, tv;
+  if ((rc = page_map(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
+  if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
+  own.cu_req = cu_req;
+  own.n_groups = n_groups;
+  // The shared launch: the groups are its requests.
+  ra::PagedArgs shared = own;
+  shared.n_own = n_req;
+  shared.n_req = n_groups;
+  shared.block_table = prefix_table;
+  shared.max_pages = prefix_max_pages;
+  shared.lengths = prefix_lengths;
+  const int own_tile = ra::paged_row_tile(own, d);
+  ra::PagedArgs group = own;  // as if a group were a request
+  group.n_q = n_groups ? (T + n_groups - 1) / n_groups : 1;
+  const int shared_tile = ra::paged_row_tile(group, d);
+  // Scratch of each launch: the states of its cut items and of all rows, and a
+  // record per row.
+  const long long rows = T * heads;
+  auto ctas_of = [](int tile) { return (tile == 128 ? 1 : 2) * ra::sm_count(); };
+  auto size_of = [&](ra::PagedArgs& a, int tile) {
+    a.whole = 2LL * ctas_of(tile) * tile;
+    const size_t bytes = static_cast<size_t>(a.whole + rows) * (d + 2) * sizeof(float) + rows * sizeof(int2);
+    return (bytes + 255) / 256 * 256;
+  };
+  const size_t own_bytes = size_of(own, own_tile), shared_bytes = size_of(shared, shared_tile);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* scratch = nullptr;
+  cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&scratch), own_bytes + shared_bytes, st);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));
+  }
+  auto place = [&](ra::PagedArgs& a, char* at) {
+    a.po = reinterpret_cast<float*>(at);
+    a.pm = a.po + (a.whole + rows) * d;
+    a.pl = a.pm + (a.whole + rows);
+    a.parts = reinterpret_cast<int2*>(a.pl + (a.whole + rows));
+  };
+  place(own, scratch);
+  place(shared, scratch + own_bytes);
+  {
+    TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
+    e = ra::launch_paged_decode(own, ra::kPagedOwn, d, ctas_of(own_tile), own_tile, tk, tv, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (e == cudaSuccess && n_groups > 0) {
+    TraceScope ts(RA_KERNEL_PAGED_PREFIX, st);
+    e = ra::launch_paged_decode(shared, ra::kPagedShared, d, ctas_of(shared_tile), shared_tile, tk, tv, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (e == cudaSuccess) {
+    TraceScope ts(RA_KERNEL_PAGED_COMBINE, st);
+    e = ra::launch_paged_join(own, shared, d, own_tile, shared_tile, st);
+    ts.done(e == cudaSuccess);
+  }
+  const cudaError_t ef = cudaFreeAsync(scratch, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged-prefix launch");
+  return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
 }
 
 int ra_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,

@@ -706,6 +706,39 @@ PyObject* decode(PyObject* const* a) {
   return pack({&x.out, &x.lse});
 }
 
+// q, k_cache, v_cache, prefix_table, prefix_lengths, cu_req, block_table, lengths,
+// cu_q, n_q, out, lse, stream
+PyObject* decode_prefix(PyObject* const* a) {
+  const Tensor &vc = tensor(a[2], "v_cache"), &ptab = tensor(a[3], "prefix_table");
+  const Tensor &plen = tensor(a[4], "prefix_lengths"), &cur = tensor(a[5], "cu_req");
+  Decode x(a[0], a[1], a + 6, a + 10);
+  const int64_t groups = plen.numel();
+  if (ptab.dim() != 2 || ptab.size(0) != groups)
+    refuse(PyExc_ValueError, "prefix_table must be [n_groups=%lld, max_pages], got %s", static_cast<long long>(groups),
+           shape_of(ptab).c_str());
+  const void* pq = dense(x.q, "q", x.dev, ScalarType::BFloat16);
+  const Cache ck = cache(x.kc, "k_cache", x.kv_heads, x.d, x.dev), cv = cache(vc, "v_cache", x.kv_heads, x.d, x.dev);
+  same_pages(ck, cv);
+  const Table tb = block_table(x.tab, x.n, x.dev);
+  const int* ppt = static_cast<int*>(dense(ptab, "prefix_table", x.dev, ScalarType::Int));
+  const int* ppl = ints(plen, "prefix_lengths", groups, x.dev);
+  const int* pcr = ints(cur, "cu_req", groups + 1, x.dev);
+  const int* pc = x.cu ? ints(*x.cu, "cu_q", x.n + 1, x.dev) : nullptr;
+  const int* pl = ints(x.len, "lengths", x.n, x.dev);
+  const int n_groups = to_int(groups, "n_groups"), width = to_int(ptab.size(1), "max_pages");
+  const Place at(x.dev, a[12]);
+  x.make(at);
+  void* po = x.out_ptr();
+  float* ps = x.lse_ptr();
+  const int n_q = x.rows_each();
+  call(at, [&](void* st) {
+    return ra_paged_decode_prefix(pq, ck.p, cv.p, po, ps, x.T, n_groups, pcr, ppt, width, ppl, tb.n_req, n_q, pc, tb.p,
+                                  tb.width, pl, ck.pages, ck.page_size, ck.stride, cv.stride, x.d, x.heads, x.kv_heads,
+                                  RA_BF16, x.type(), st);
+  });
+  return pack({&x.out, &x.lse});
+}
+
 // q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_q, n_q, window,
 // out, lse, stream
 PyObject* decode_fp8(PyObject* const* a) {
@@ -748,6 +781,7 @@ RA_ENTRY(decode, 11)
 RA_ENTRY(append_fp8, 17)
 RA_ENTRY(read_fp8, 11)
 RA_ENTRY(decode_fp8, 13)
+RA_ENTRY(decode_prefix, 13)
 #undef RA_ENTRY
 
 PyCFunction fast(PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)) {
@@ -764,6 +798,7 @@ PyMethodDef g_methods[] = {
     {"paged_decode", fast(decode_entry), METH_FASTCALL, nullptr},
     {"paged_append_fp8", fast(append_fp8_entry), METH_FASTCALL, nullptr},
     {"paged_decode_fp8", fast(decode_fp8_entry), METH_FASTCALL, nullptr},
+    {"paged_decode_prefix", fast(decode_prefix_entry), METH_FASTCALL, nullptr},
     {"paged_read_fp8", fast(read_fp8_entry), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -166,22 +166,28 @@ struct PagedArgs {
   long long ks_page, vs_page;
   // With a shared prefix.  Both launches leave states only: those of items that
   // are not cut at index whole + row of po, pm, pl, and in parts[row] where the
-  // row's states are: {0, 0} there, or {index of the first, how many}.
+  // row's states are (paged_walk.cuh).
   long long whole;
   int2* parts;        // [T * heads]
-  const int* cu_req;  // the shared launch, whose requests are groups: the requests of each
-  int n_own;          // requests
+  const int* cu_req;  // [n_groups + 1] the requests of each group
+  int n_groups;
+  int n_own;          // the shared launch, whose requests are the groups: requests
 };
+// What the rows of a decode launch are: see paged_walk.cuh.
+constexpr int kPagedPlain = 0, kPagedOwn = 1, kPagedShared = 2;
 // Query rows (of one request and KV head) that a CTA takes together: 8 or 16
 // (paged_kernel.cu, two CTAs per SM) or 128 (paged_tc_kernel.cu, one).
 int paged_row_tile(const PagedArgs& a, int d);
 size_t paged_cut_bytes(int ctas);
 // tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
 // 64 x 1 x min(page_size, 64) x 1, 128-byte swizzle.
-cudaError_t launch_paged_decode(const PagedArgs& a, int d, int ctas, int row_tile,
+cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st);
-cudaError_t launch_paged_tc(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk,
+// out, lse = the states of both launches together (the row tiles are theirs).
+cudaError_t launch_paged_join(const PagedArgs& own, const PagedArgs& shared, int d, int own_tile,
+                              int shared_tile, cudaStream_t st);
+cudaError_t launch_paged_tc(const PagedArgs& a, int mode, int d, int ctas, const CUtensorMap& tk,
                             const CUtensorMap& tv, cudaStream_t st);
 // Over pages in 8 bits: row tiles of 8 or 16, two CTAs per SM, the same joining
 // launch; tk, tv as above with a box of a whole row, page_size or

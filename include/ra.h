@@ -130,7 +130,8 @@ typedef enum {
   RA_KERNEL_PAGED_APPEND_FP8 = 20, /* kind 17 with k and v held in 8 bits */
   RA_KERNEL_PAGED_READ_FP8 = 21,  /* 8-bit pages as dense bf16 rows */
   RA_KERNEL_PAGED_DECODE_FP8 = 22, /* attention over 8-bit pages */
-  RA_KERNEL_KINDS = 23
+  RA_KERNEL_PAGED_PREFIX = 23,    /* attention over prefixes that requests share */
+  RA_KERNEL_KINDS = 24
 } ra_kernel_kind;
 
 /*
@@ -557,6 +558,36 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
                     int max_pages, const int* lengths, int n_pages, int page_size,
                     long long k_page_stride, long long v_page_stride, long long window, int d,
                     int heads, int kv_heads, int dtype, int out_dtype, void* stream);
+
+/*
+ * ra_paged_decode_prefix -- ra_paged_decode for requests that share prefixes: the
+ * keys of a prefix are read once for all the rows of its group and not once per
+ * request.  Group p is the requests [cu_req[p], cu_req[p + 1]); its prefix of
+ * prefix_lengths[p] tokens lies in the pages prefix_table[p] (any length: the last
+ * page may be part full).  Every row of the group's requests sees the whole
+ * prefix and, of its request's own pages (block_table, lengths as in
+ * ra_paged_decode: the new tokens included, the prefix not), the keys up to
+ * itself.  A request's own tokens stand behind the prefix: their positions for
+ * ra_paged_append are those of ra_paged_extend plus the prefix's length.  Own
+ * pages go through ra_paged_extend and ra_paged_release as ever; the prefix's
+ * belong to nobody's row, and are handed out and taken back as a request of their
+ * own, that has no new tokens.
+ *   cu_req: device int32 [n_groups + 1], nondecreasing.  A request of no group, or
+ *     of one whose prefix has length 0, sees its own keys alone.
+ *   prefix_table: [n_groups, prefix_max_pages], prefix_lengths: [n_groups], device
+ *     int32, with the limits and clamps of block_table and lengths.
+ *   Everything else, cu_q, n_q, out and lse too, as in ra_paged_decode.  There is
+ *   no window: the keys that a window leaves of a prefix differ from row to row.
+ *   Scratch: the states of all rows twice, T * heads * (8 d + 32) bytes, from the
+ *   pool.
+ */
+int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cache, void* out,
+                           float* lse, long long T, int n_groups, const int* cu_req,
+                           const int* prefix_table, int prefix_max_pages,
+                           const int* prefix_lengths, int n_req, int n_q, const int* cu_q,
+                           const int* block_table, int max_pages, const int* lengths, int n_pages,
+                           int page_size, long long k_page_stride, long long v_page_stride, int d,
+                           int heads, int kv_heads, int dtype, int out_dtype, void* stream);
 
 /*
  * Pages in 8 bits.  The same pages, block tables and slots, with k_cache and

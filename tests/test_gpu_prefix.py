@@ -1,0 +1,379 @@
+"""Attention with shared prefixes on the GPU, against the fp64 oracle over each
+request's prefix and own keys together.  Tolerances: test_gpu_paged.py, with n
+the prefix's and the own keys, and for the join of two partial sums of a row 16 u
+more (a factor ex2 good to 6.4 u on either side, two roundings)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import blockwise_online_softmax_gb300 as ra
+import oracle
+from test_gpu_paged import check_decode, i32, make_decode
+from test_gpu_rope import np64
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24
+
+
+def make(groups, rows, H, Hkv, d, ps, *, seed=0, scale=1.5, together=False, extra=0):
+    """groups: (prefix length, own lengths of its requests) each; rows: new
+    tokens of every request.  Pages of prefixes and requests are dealt from one
+    cache, with NaN where nobody's tokens are."""
+    plens = [p for p, _ in groups]
+    own = [n for _, ls in groups for n in ls]
+    q, kc, vc, table, _, ks, vs = make_decode(plens + own, rows, H, Hkv, d, ps, seed=seed, scale=scale,
+                                              together=together, extra=extra)
+    G = len(groups)
+    cu_req = i32(np.concatenate([[0], np.cumsum([len(ls) for _, ls in groups])]))
+    args = (q, kc, vc, table[:G].contiguous(), i32(plens), cu_req, table[G:].contiguous(), i32(own))
+    of = [g for g, (_, ls) in enumerate(groups) for _ in ls]
+    k = [torch.cat((ks[g], x)) for g, x in zip(of, ks[G:])]
+    v = [torch.cat((vs[g], x)) for g, x in zip(of, vs[G:])]
+    return args, k, v
+
+
+CASES = [
+    # groups, new tokens each, heads, kv_heads, d, page size
+    ([(1, [1])], 1, 1, 1, 64, 8),
+    ([(17, [1, 5])], 1, 4, 2, 128, 16),
+    ([(100, [3, 30, 1])], 1, 8, 2, 64, 16),
+    ([(1001, [300, 1, 20, 77, 64, 65, 2, 150])], 1, 32, 8, 128, 16),
+    ([(128, [128]), (129, [127, 129])], 1, 32, 8, 128, 64),
+    ([(0, [40, 2]), (500, [9]), (0, [1])], 1, 12, 4, 64, 32),
+    ([(5000, [1] * 40)], 1, 8, 2, 128, 128),            # 160 rows of a KV head: two tiles of 128
+    ([(3000, [10] * 100), (2, [700] * 3)], 1, 8, 1, 64, 256),
+    ([(777, [33] * 9), (64, [4, 5])], 4, 32, 8, 128, 16),
+    ([(777, [40] * 9), (64, [40, 50])], 9, 32, 8, 64, 16),   # own rows on the 128-row tiles too
+    ([(20000, [300, 3])], 2, 16, 16, 128, 64),           # few rows, a long prefix: many CTAs an item
+    ([(9, [2] * 300)], 1, 64, 8, 128, 16),
+    ([(300, [6] * 3), (1, []), (40, [8])], 3, 128, 1, 128, 16),
+    ([(int(p), [int(x) for x in np.random.default_rng(p).integers(1, 200, p % 7 + 1)])
+      for p in range(0, 400, 13)], 1, 8, 2, 64, 16),     # 31 groups: over one look of a warp
+    ([(int(p), [int(p) % 50 + 1]) for p in range(1, 100)], 1, 4, 4, 128, 16),
+]
+
+
+@pytest.mark.parametrize("together", [False, True])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{[(p, len(x)) for p, x in c[0][:3]]}-q{c[1]}-h{c[2]}/{c[3]}-d{c[4]}-p{c[5]}")
+def test_prefix(case, together):
+    groups, n_q, H, Hkv, d, ps = case
+    rows = [n_q] * sum(len(x) for _, x in groups)
+    args, k, v = make(groups, rows, H, Hkv, d, ps, together=together)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    check_decode(out, lse, args[0], k, v, rows)
+    again = ra.ra_paged_decode_prefix(*args)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    bf = torch.empty(args[0].shape, dtype=torch.bfloat16, device=DEV)
+    _, lse2 = ra.ra_paged_decode_prefix(*args, out=bf)
+    check_decode(bf, lse2, args[0], k, v, rows)
+
+
+def attend(q, k, v, n_own, n_new):
+    """Oracle: rows at the last n_new positions; all see what is before the own."""
+    L = k.shape[0]
+    return oracle.attention(q.cpu(), k.cpu(), v.cpu(), causal=True, q_pos=L - n_new + np.arange(n_new),
+                            k_pos=np.arange(L))
+
+
+@pytest.mark.parametrize("rows", [[1, 0, 3, 1, 2], [0, 0, 2, 0, 0], [40, 1, 0, 7, 1]])
+def test_ragged_rows(rows):
+    """cu_q: idle requests, several rows, and rows behind the last left as they were."""
+    groups = [(300, [50, 20]), (129, [77, 10, 41])]
+    args, k, v = make(groups, rows, 8, 2, 128, 16, extra=5)
+    out = torch.full(args[0].shape, 9.0, device=DEV)
+    lse = torch.full(args[0].shape[:2], 9.0, device=DEV)
+    cu = i32(np.concatenate([[0], np.cumsum(rows)]))
+    for n_q in (0, 1, 9):
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        ra.ra_paged_decode_prefix(*args, cu_q=cu, n_q=n_q, out=out, lse=lse)
+        ra.ra_device_status()
+        check_decode(out, lse, args[0], k, v, rows)
+        assert (out[-5:] == 9.0).all() and (lse[-5:] == 9.0).all()
+
+
+def test_requests_of_no_group_see_their_own_keys():
+    groups = [(300, [50, 20]), (129, [77, 10, 41])]
+    rows = [2] * 5
+    args, k, v = make(groups, rows, 8, 2, 128, 16)
+    own = ra.ra_paged_decode(args[0], args[1], args[2], args[6], args[7])
+    for cu in ([1, 2, 4], [0, 0, 3], [2, 2, 2], [5, 5, 5]):
+        a = list(args)
+        a[5] = i32(cu)
+        out, lse = ra.ra_paged_decode_prefix(*a)
+        ra.ra_device_status()
+        for i in range(5):
+            g = next((j for j in range(2) if cu[j] <= i < cu[j + 1]), None)
+            r = slice(2 * i, 2 * i + 2)
+            if g is None:
+                check_decode(out[r], lse[r], args[0][r], [k[i][-int(args[7][i]):]], [v[i][-int(args[7][i]):]], [2])
+            else:
+                first = k[0 if g == 0 else 2][:groups[g][0]], v[0 if g == 0 else 2][:groups[g][0]]
+                n = int(args[7][i])
+                check_decode(out[r], lse[r], args[0][r], [torch.cat((first[0], k[i][-n:]))],
+                             [torch.cat((first[1], v[i][-n:]))], [2])
+    # No groups at all.
+    none = torch.empty(0, 4, dtype=torch.int32, device=DEV)
+    out, lse = ra.ra_paged_decode_prefix(*args[:3], none, i32([]), i32([0]), *args[6:])
+    ra.ra_device_status()
+    assert float((out - own[0]).abs().max()) <= 1e-5 and float((lse - own[1]).abs().max()) <= 1e-5
+
+
+def test_rows_before_the_own_keys_and_nothing_at_all():
+    """Fewer own keys than rows: the earlier rows see the prefix alone; without
+    prefix and own keys a row is 0 with an LSE of -inf."""
+    args, k, v = make([(50, [2, 0]), (0, [1, 0])], [3] * 4, 8, 2, 64, 16)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    pre = k[0][:50], v[0][:50]
+
+    def check(row, kk, vv):
+        check_decode(out[row:row + 1], lse[row:row + 1], args[0][row:row + 1], [kk], [vv], [1])
+
+    check(0, *pre)                      # rows at own positions -1, 0, 1
+    check(1, k[0][:51], v[0][:51])
+    check(2, k[0], v[0])
+    for j in range(3, 6):
+        check(j, *pre)
+    for j in (6, 7, 9, 10, 11):
+        assert (out[j] == 0).all() and torch.isneginf(lse[j]).all()
+    check(8, k[2], v[2])
+
+
+def test_equals_the_paged_decode_over_whole_tables():
+    """The same pages in every request's row: within the two calls' bars."""
+    ps, P, own = 16, 320, [40, 7, 90]  # full prefix pages
+    args, k, v = make([(P, own)], [2] * 3, 32, 8, 128, ps)
+    q, kc, vc, ptab, plens, cu, tab, lens = args
+    whole = torch.cat((ptab[:, :P // ps].expand(3, -1), tab), 1).contiguous()
+    ref, rlse = ra.ra_paged_decode(q, kc, vc, whole, lens + P)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    A = float(q.float().norm(dim=-1).max()) * max(float(x.float().norm(dim=-1).max()) for x in k) / math.sqrt(128)
+    bar = 4 * 128 * U * A + 2.0 ** -16 + 500 * 2 * U
+    assert float((out - ref).abs().max()) <= 2 * bar * max(float(x.abs().max()) for x in v)
+    assert float((lse - rlse).abs().max()) <= 2 * (2 * 128 * U * A + 500 * 2 * U + 8 * U * 12)
+
+
+@pytest.mark.parametrize("scale", [0.0, 40.0])
+def test_equal_and_large_scores(scale):
+    args, k, v = make([(700, [50, 3] * 20)], [1] * 40, 8, 2, 128, 16, scale=scale)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    check_decode(out, lse, args[0], k, v, [1] * 40)
+
+
+@pytest.mark.parametrize("n_q, per, H, Hkv, d", [(1, 2, 8, 2, 64), (1, 3, 8, 2, 128), (1, 40, 8, 2, 128), (2, 40, 8, 1, 64)])
+def test_weights_have_24_bits(n_q, per, H, Hkv, d):
+    """As the paged decode's test of that name: an output is one weight of three
+    live keys, here two in the prefix and one among the own, all others weightless:
+    99 u there where parts meet, the join of the two launches two factors of 6.4 u
+    and three roundings more: 115 u, 128 u is used."""
+    P, n = 700, 40
+    groups = [(P, [n] * per)]
+    args, ks, vs = make(groups, [n_q] * per, H, Hkv, d, 16, seed=d + per)
+    q, kc, vc, ptab, _, _, tab, _ = args
+    r = np.random.default_rng(per)
+    g = H // Hkv
+    q.zero_()
+    for t in range(per * n_q):
+        for h in range(H):
+            q[t, h, (t * g + h % g) % d] = 1.0
+    live = [100, 650]
+
+    def fill(pages, rows_k, rows_v, length):
+        for p in range(-(-length // 16)):
+            m = min(16, length - 16 * p)
+            kc[pages[p], :m] = rows_k[16 * p:16 * p + m]
+            vc[pages[p], :m] = rows_v[16 * p:16 * p + m]
+
+    def rows(length, at, first):
+        k = torch.full((length, Hkv, d), -200.0 * math.sqrt(d), device=DEV).bfloat16()
+        v = torch.randn(length, Hkv, d, device=DEV).bfloat16()
+        for j, a in enumerate(at):
+            k[a] = torch.from_numpy(r.uniform(-1, 1, (Hkv, d)) * math.sqrt(d)).to(DEV).bfloat16()
+            v[a] = 0.0
+            v[a, :, first + j::3] = 1.0
+        return k, v
+
+    pk, pv = rows(P, live, 0)
+    fill(ptab[0].tolist(), pk, pv, P)
+    own = []
+    for i in range(per):
+        own.append(rows(n, [5], 2))
+        fill(tab[i].tolist(), *own[i], n)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    for i in range(per):
+        rr = slice(i * n_q, (i + 1) * n_q)
+        k, v = torch.cat((pk, own[i][0])), torch.cat((pv, own[i][1]))
+        ro, rl = attend(q[rr], k, v, n, n_q)
+        err = np.abs(np64(out[rr]) - ro)
+        assert (err <= 128 * U * ro).all(), f"max error {(err / (U * ro)).max():.1f} u"
+        assert (np.abs(np64(lse[rr]) - rl) <= 132 * U).all()
+
+
+def test_arrays_in_disorder_stay_inside():
+    """Offsets that are no prefix sums, lengths and pages out of range: results
+    are undefined, nothing outside out and lse is written, nothing hangs."""
+    args, k, v = make([(300, [50, 20]), (129, [77, 10, 41])], [2] * 5, 8, 2, 128, 16)
+    whole = torch.full((14, 8, 128), 3.0, device=DEV)
+    wl = torch.full((14, 8), 3.0, device=DEV)
+    for cu_req in ([0, 5, 2], [-7, 3, 99], [4, 1, 0], [2**31 - 1, -2**31, 5]):
+        for plens in ([300, 129], [-5, 10**9], [2**31 - 1, -2**31]):
+            for cu_q in (None, [0, 9, 3, 99, -4, 10], [5, 4, 3, 2, 1, 0], [-9, 2, 4, 6, 8, 2**31 - 1]):
+                a = list(args)
+                a[5], a[4] = i32(cu_req), i32(plens)
+                ra.ra_paged_decode_prefix(*a, cu_q=None if cu_q is None else i32(cu_q), out=whole[2:12], lse=wl[2:12])
+    ra.ra_device_status()
+    assert (whole[:2] == 3).all() and (whole[12:] == 3).all() and (wl[:2] == 3).all() and (wl[12:] == 3).all()
+    bad = args[3].clone()
+    bad[0, ::2] = 2**30
+    bad[1, 1::2] = -1
+    a = list(args)
+    a[3] = bad
+    ra.ra_paged_decode_prefix(*a)
+    ra.ra_device_status()
+
+
+def test_captured_and_replayed_as_lengths_grow():
+    """Two graphs of one call on two streams share no workspace and bake no host value in."""
+    groups = [(500, [60, 3, 20]), (1300, [90])]
+    args, k, v = make(groups, [1] * 4, 32, 8, 128, 16)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ra.ra_paged_decode_prefix(*args))
+        graphs.append(g)
+    of = [0, 0, 0, 1]
+    for plens, own in (([500, 1300], [60, 3, 20, 90]), ([1, 700], [1, 1, 1, 50]), ([0, 129], [60, 3, 7, 90])):
+        args[4].copy_(i32(plens))
+        args[7].copy_(i32(own))
+        streams = [torch.cuda.Stream() for _ in graphs]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+
+        def part(x, i):
+            P = groups[of[i]][0]
+            return torch.cat((x[i][:plens[of[i]]], x[i][P:P + own[i]]))
+
+        for out, lse in outs:
+            check_decode(out, lse, args[0], [part(k, i) for i in range(4)], [part(v, i) for i in range(4)], [1] * 4)
+    ra.ra_device_status()
+
+
+def test_two_eager_calls_at_once_and_other_kernels_between():
+    """Calls on two streams, in turn, with the plain decode among them: the second
+    launch of a call starts before the first has ended, and touches nothing that
+    a call before it still uses."""
+    cases = [make([(900, [40, 2, 64])], [1] * 3, 32, 8, 128, 16, seed=1)[0],
+             make([(2000, [700] * 5), (3, [9])], [16] * 6, 8, 2, 128, 16, seed=2)[0]]
+    want = [ra.ra_paged_decode_prefix(*c) for c in cases]
+    plain = [ra.ra_paged_decode(c[0], c[1], c[2], c[6], c[7]) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(20):
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append((ra.ra_paged_decode_prefix(*c), ra.ra_paged_decode(c[0], c[1], c[2], c[6], c[7])))
+    torch.cuda.synchronize()
+    ra.ra_device_status()
+    for i, (a, b) in enumerate(got):
+        assert torch.equal(a[0], want[i % 2][0]) and torch.equal(a[1], want[i % 2][1])
+        assert torch.equal(b[0], plain[i % 2][0]) and torch.equal(b[1], plain[i % 2][1])
+
+
+def test_a_chain_in_one_stream_uses_what_the_call_before_wrote():
+    """Every step's keys are written by the kernel just before the call."""
+    groups = [(300, [33] * 12)]
+    args, k, v = make(groups, [1] * 12, 8, 2, 128, 16, seed=5)
+    q, kc, vc, ptab, plens, cu, tab, lens = args
+    k0, v0 = kc.clone(), vc.clone()
+    want = ra.ra_paged_decode_prefix(*args)
+    for _ in range(30):
+        kc.zero_()
+        vc.zero_()
+        kc.copy_(k0)
+        vc.copy_(v0)
+        got = ra.ra_paged_decode_prefix(*args)
+        kc.fill_(1.0)  # what follows must not reach the call either
+        vc.fill_(1.0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_tracing_counts_the_three_launches():
+    args, k, v = make([(300, [50, 20])], [1] * 2, 8, 2, 128, 16)
+    ra.ra_trace_enable()
+    ra.ra_trace_reset()
+    try:
+        out, lse = ra.ra_paged_decode_prefix(*args)
+        check_decode(out, lse, args[0], k, v, [1] * 2)
+        assert [ra.ra_trace_query(x)[0] for x in ("paged_decode", "paged_prefix", "paged_combine")] == [1, 1, 1]
+    finally:
+        ra.ra_trace_enable(False)
+
+
+def test_a_serving_loop_on_a_shared_prompt():
+    """A prompt is cached once, as a request of its own; three requests go on from
+    it, token by token, at positions behind it: extend, append, attend, captured
+    as a step would be.  Against the oracle over each whole sequence."""
+    H, Hkv, d, ps, P, steps, n = 8, 2, 128, 16, 203, 6, 3
+    g = torch.Generator(device=DEV).manual_seed(4)
+    ph = ra.rope_phases(ra.rope_freqs(d)[0]).to(DEV)
+    n_pages = 40
+    kc = torch.full((n_pages, ps, Hkv, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    vc = kc.clone()
+    free, count = torch.randperm(n_pages).int().to(DEV), i32([n_pages])
+    ptab, plen = torch.full((1, 20), -1, dtype=torch.int32, device=DEV), i32([0])
+    kp, vp = (torch.randn(P, Hkv, d, device=DEV, generator=g).bfloat16() for _ in range(2))
+    qp = torch.randn(P, H, d, device=DEV, generator=g).bfloat16()
+    slots, pos, *_ = ra.ra_paged_extend(plen, i32([P]), ptab, free, count, page_size=ps, tokens=P,
+                                        lengths_out=plen, free_count_out=count)
+    ra.ra_paged_append(qp, kp, vp, ph, kc, vc, slots, pos)
+    tab, lens = torch.full((n, 4), -1, dtype=torch.int32, device=DEV), i32([0] * n)
+    q, k, v = (torch.randn(steps, n, h, d, device=DEV, generator=g).bfloat16() for h in (H, Hkv, Hkv))
+    outs = []
+    for s in range(steps):
+        slots, pos, cu, _, _, status = ra.ra_paged_extend(
+            lens, i32([1] * n), tab, free, count, page_size=ps, tokens=n, lengths_out=lens, free_count_out=count)
+        qr = ra.ra_paged_append(q[s], k[s], v[s], ph, kc, vc, slots, pos + plen)
+        outs.append(ra.ra_paged_decode_prefix(qr, kc, vc, ptab, plen, i32([0, n]), tab, lens)[0])
+    ra.ra_device_status()
+    for i in range(n):
+        kk, vv = torch.cat((kp, k[:, i])), torch.cat((vp, v[:, i]))
+        qq = torch.cat((qp, q[:, i]))
+        qr, kr = ra.ra_qk_norm_rope(qq, kk, ph)
+        ref, _ = oracle.attention(qr[-steps:].cpu(), kr.cpu(), vv.cpu(), causal=True,
+                                  q_pos=P + np.arange(steps), k_pos=np.arange(P + steps))
+        got = np.stack([np64(o[i]) for o in outs])
+        assert np.abs(got - ref).max() <= 1e-4
+    # Own pages go back, the prefix's stay out.
+    ra.ra_paged_release(lens, i32([1] * n), tab, free, count, page_size=ps, lengths_out=lens, free_count_out=count)
+    assert int(count) == n_pages - -(-P // ps)
+
+
+def test_wrong_tensors_are_refused():
+    args, _, _ = make([(60, [30, 20])], [1] * 2, 4, 2, 64, 16)
+    run = lambda **kw: ra.ra_paged_decode_prefix(*[kw.get(n, x) for n, x in zip(  # noqa: E731
+        ("q", "kc", "vc", "ptab", "plens", "cu_req", "tab", "lens"), args)])
+    with pytest.raises(ValueError, match="prefix_table must be"):
+        run(ptab=args[3][0])
+    with pytest.raises(TypeError, match="prefix_lengths must be torch.int32"):
+        run(plens=args[4].long())
+    with pytest.raises(ValueError, match="cu_req must have shape"):
+        run(cu_req=args[5][:1])
+    with pytest.raises(TypeError, match="k_cache must be torch.bfloat16"):
+        run(kc=args[1].half())
+    with pytest.raises(ValueError, match="must match in pages"):
+        run(vc=args[2][:-1])
