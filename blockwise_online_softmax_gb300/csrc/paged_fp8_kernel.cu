@@ -16,12 +16,12 @@
 // - q is turned to fp16 once an item, with a power of two per row that brings its
 //   largest entry to [2^14, 2^15): its 8 bits are exact down to 2^-28 of that entry,
 //   and below it is off by at most 2^-39 of it.
-// - The weight of a value is p_t 2^b_t.  fp16 has no room for all scales, so a
-//   warp takes the largest 2^b of its keys of a tile out and gives it back in
-//   fp32 when the tile's product is added to O.  What is left, times 2^15, is
-//   held in two fp16 terms: 22 bits and the sign of the second, off by at most
-//   2^-23 of itself, or 2^-40 of the largest, as good as the fp32 it comes from.
-//   (bf16 pages need three terms of 8 bits.)
+// - The weight of a value is p_t 2^b_t.  fp16 has no room for all of them, so a
+//   warp scales its weights of a tile by a power of two, the largest to [2^14,
+//   2^15), and gives it back in fp32 when the tile's product is added to O.  Held
+//   in two fp16 terms (22 bits and the sign of the second) a weight is off by at
+//   most 2^-23 of itself, or 2^-39 of the largest, as good as the fp32 it comes
+//   from.  (bf16 pages need three terms of 8 bits.)
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -75,6 +75,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same with c = 0 before.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
   uint32_t d;
@@ -215,13 +223,14 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
       for (int c = 0; c < 2; ++c) sl2[nt][c] = __shfl_sync(kAll, down, 8 * (lane & 3) + 4 * c);
     }
-    float m[NT][2], l[NT][2], o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+    uint64_t o2[NT][D / 16][2];  // rows 2 (lane % 4) + {0, 1} of a column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) o[nt][x][0] = o[nt][x][1] = o[nt][x][2] = o[nt][x][3] = 0.f;
+      for (int x = 0; x < D / 16; ++x) o2[nt][x][0] = o2[nt][x][1] = f2pack(0.f, 0.f);
     }
     for (int k = 0; k < item.tiles; ++k) {
       const uint32_t kb = sb + st * C::STAGE, vb = kb + C::TILE, scales = sb + C::OFF_SCALE + st * 2 * BT + key0;
@@ -233,43 +242,54 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       float sc[KB][NT][4];
       uint32_t pb[KB][NT][2][2];
       float al[NT][2], back = 0.f;
+      bool turned = false;  // some row's maximum is a new one
       if (some) {
+        // Independent products alternate: each waits for the one before it of the
+        // same sum.  With one group of rows a sum has two halves.
+        constexpr int HALVES = NT == 1 ? 2 : 1;
+        float part[HALVES][KB][NT][4];
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-          const int r = key0 + 16 * b + kr;
+        for (int c = 0; c < CPR; c += 2) {
+          uint32_t w[KB][4];  // (keys 0-7, 8-15) of chunk c, then of chunk c + 1
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[b][nt][0] = sc[b][nt][1] = sc[b][nt][2] = sc[b][nt][3] = 0.f;
-#pragma unroll
-          for (int c = 0; c < CPR; c += 2) {
-            uint32_t w[4];  // (keys 0-7, 8-15) of chunk c, then of chunk c + 1
-            ldsm4(kb + r * D + (((c + c2) ^ swz(r)) << 4), w);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t af[4] = {low2(w[2 * h]), low2(w[2 * h + 1]), high2(w[2 * h]), high2(w[2 * h + 1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(sc[b][nt], af, qf[nt][c + h][0], qf[nt][c + h][1]);
-            }
+          for (int b = 0; b < KB; ++b) {
+            const int r = key0 + 16 * b + kr;
+            ldsm4(kb + r * D + (((c + c2) ^ swz(r)) << 4), w[b]);
           }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+              const uint32_t af[4] = {low2(w[b][2 * h]), low2(w[b][2 * h + 1]), high2(w[b][2 * h]), high2(w[b][2 * h + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float(&t)[4] = part[h % HALVES][b][nt];
+                if (c + h < HALVES) mma_f16_first(t, af, qf[nt][c + h][0], qf[nt][c + h][1]);
+                else mma_f16(t, af, qf[nt][c + h][0], qf[nt][c + h][1]);
+              }
+            }
         }
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[b][nt][x] = HALVES == 2 ? part[0][b][nt][x] + part[HALVES - 1][b][nt][x] : part[0][b][nt][x];
         // Scales of the lane's keys lane / 4 and lane / 4 + 8 of each block.
-        uint32_t vs[KB][2], top = 0;
+        float vs[KB][2];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = 16 * b + 8 * h + (lane >> 2);
             const float ks = scale_of(lds_u8(scales + j));
-            vs[b][h] = lds_u8(scales + BT + j);
-            if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0;  // nobody's: anything may stand there
-            top = max(top, vs[b][h]);
+            vs[b][h] = scale_of(lds_u8(scales + BT + j));
+            if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0.f;  // nobody's: anything may stand there
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 2; ++c) sc[b][nt][2 * h + c] *= ks;
           }
-        top = warp_max(top);
-        // 2^(top - 127 - 15), below fp32's normal range too.
-        back = __uint_as_float(top > 15 ? (top - 15) << 23 : 0x400000u >> (15 - top));
         if (k0 < lo_all || k0 + 16 * KB > hi_all) {
 #pragma unroll
           for (int b = 0; b < KB; ++b)
@@ -294,6 +314,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             const float mn = fmaxf(m[nt][c], x * sl2[nt][c]);
             const float ref = mn == -INFINITY ? 0.f : mn;
             al[nt][c] = ex2(m[nt][c] - ref);
+            turned |= mn != m[nt][c];
             m[nt][c] = mn;
             float sum = 0.f;
 #pragma unroll
@@ -301,18 +322,29 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const float p = ex2(fmaf(sc[b][nt][2 * h + c], sl2[nt][c], -ref));
-                sc[b][nt][2 * h + c] = p;
+                sc[b][nt][2 * h + c] = p * vs[b][h];
                 sum += p;
               }
             l[nt][c] = fmaf(l[nt][c], al[nt][c], sum);
           }
-        // The weights in two fp16 terms.
+        turned = __any_sync(kAll, turned);
+        // The weights in two fp16 terms, by a power of two that brings the warp's
+        // largest to [2^14, 2^15).
+        float most = 0.f;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) most = fmax3(most, sc[b][nt][c], sc[b][nt][c + 1]);
+        const uint32_t top = warp_max(__float_as_uint(most)) >> 23;  // its exponent (weights are not negative)
+        const uint32_t lift = top < 15 ? 15 : (top > 254 ? 254 : top);
+        const float f = __uint_as_float((268 - lift) << 23);  // 2^(14 - (lift - 127))
+        back = __uint_as_float(lift > 14 ? (lift - 14) << 23 : 0u);
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int e = static_cast<int>(vs[b][h]) - static_cast<int>(top) + 142;
-            const float f = __uint_as_float(e > 0 ? static_cast<unsigned>(e) << 23 : 0u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float x = sc[b][nt][2 * h] * f, y = sc[b][nt][2 * h + 1] * f;
@@ -326,6 +358,18 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim);
       ok = __all_sync(kAll, ok);
       if (some) {
+        if (turned) {  // seldom after an item's first tiles
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint64_t al2 = f2pack(al[nt][0], al[nt][1]);
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              o2[nt][x][0] = fmul2(o2[nt][x][0], al2);
+              o2[nt][x][1] = fmul2(o2[nt][x][1], al2);
+            }
+          }
+        }
+        const uint64_t back2 = f2pack(back, back);
         uint32_t keep[KB][2];  // V rows outside [lo, hi) may hold anything
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -335,40 +379,53 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             keep[b][h] = !edge ? kAll : (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
                                             (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
           }
+        constexpr int PAIRS = NT == 1 ? 2 : 1;  // of 32 columns together: four sums alternate
 #pragma unroll
-        for (int c = 0; c < CPR; c += 2) {
-          uint32_t w[KB][4];  // (keys 0-7, 8-15) of 16 columns, then of the next 16
+        for (int c0 = 0; c0 < CPR; c0 += 2 * PAIRS) {
+          uint32_t w[PAIRS][KB][4];  // (keys 0-7, 8-15) of 16 columns, then of the next 16
 #pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            const int r = key0 + 16 * b + kr;
-            ldsm4_t(vb + r * D + (((c + c2) ^ swz(r)) << 4), w[b]);
-          }
+          for (int x = 0; x < PAIRS; ++x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t af[KB][4];
+            for (int b = 0; b < KB; ++b) {
+              const int r = key0 + 16 * b + kr;
+              ldsm4_t(vb + r * D + (((c0 + 2 * x + c2) ^ swz(r)) << 4), w[x][b]);
+              if (edge) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) w[x][b][y] &= keep[b][y & 1];
+              }
+            }
+          uint32_t af[2 * PAIRS][KB][4];
+#pragma unroll
+          for (int x = 0; x < 2 * PAIRS; ++x)
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                uint32_t y = w[b][2 * h + x];
-                if (edge) y &= keep[b][x];
-                y = __byte_perm(y, 0, 0x3120);  // column 2 (lane / 4) of two keys, then the next column
-                af[b][2 * x] = low2(y);
-                af[b][2 * x + 1] = high2(y);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t y = __byte_perm(w[x >> 1][b][2 * (x & 1) + h], 0, 0x3120);
+                af[x][b][2 * h] = low2(y);  // column 2 (lane / 4) of two keys
+                af[x][b][2 * h + 1] = high2(y);  // the next column
               }
+          // A tile's product apart, small terms first, then one rounded fp32 step:
+          // the tensor core's own accumulation truncates.
+          float t[2 * PAIRS][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              // The tile's product apart, small terms first, then one rounded
-              // fp32 step: the tensor core's own accumulation truncates.
-              float t[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int term = 1; term >= 0; --term)
 #pragma unroll
-              for (int term = 1; term >= 0; --term)
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int b = 0; b < KB; ++b) mma_f16(t, af[b], pb[b][nt][term][0], pb[b][nt][term][1]);
+              for (int x = 0; x < 2 * PAIRS; ++x)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) o[nt][c + h][x] = fmaf(t[x], back, o[nt][c + h][x] * al[nt][x & 1]);
-            }
-          }
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (term == 1 && b == 0) mma_f16_first(t[x][nt], af[x][b], pb[b][nt][1][0], pb[b][nt][1][1]);
+                  else mma_f16(t[x][nt], af[x][b], pb[b][nt][term][0], pb[b][nt][term][1]);
+                }
+#pragma unroll
+          for (int x = 0; x < 2 * PAIRS; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                o2[nt][c0 + x][e] = ffma2(f2pack(t[x][nt][2 * e], t[x][nt][2 * e + 1]), back2, o2[nt][c0 + x][e]);
         }
       }
       __syncwarp();
@@ -378,6 +435,14 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         par ^= 1u;
       }
     }
+    float o[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        f2unpack(o2[nt][x][0], o[nt][x][0], o[nt][x][1]);
+        f2unpack(o2[nt][x][1], o[nt][x][2], o[nt][x][3]);
+      }
     if (!join_warps<D, NT, true, kPlain>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) return;
     if (item.last) return;
     __syncwarp();
@@ -394,7 +459,7 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
                       tk, tv, a);
 }
 
-constexpr int kKB = 1;
+constexpr int kKB = 2;
 
 }  // namespace
 
