@@ -31,12 +31,10 @@ __device__ __forceinline__ int scale_byte(unsigned top) {
 __device__ __forceinline__ float inverse_scale(int byte) { return __uint_as_float(static_cast<unsigned>(254 - byte) << 23); }
 __device__ __forceinline__ float scale_of(unsigned byte) { return __uint_as_float(byte << 23); }
 
-// Two codes, x's in the low byte.
-__device__ __forceinline__ uint32_t codes2(float x, float y, float inv) {
-  // x - x is 0, or NaN where the conversion would turn an infinity to 448.
-  const float a = fmaf(x, inv, x - x), b = fmaf(y, inv, y - y);
+// Two codes, x's in the low byte.  (An infinity would become 448.)
+__device__ __forceinline__ uint32_t codes2(float x, float y) {
   uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
   return c;
 }
 // The values of two codes as fp16 (exact), the low byte's in the low half.

@@ -388,14 +388,14 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
 }
 
 // Joins the states of a row from two launches (kOwn, kShared): a warp a row.  Its
-// lanes take a partial each for the maximum and the weights, so that the rows of
-// the partials, a lane D / 32 columns, are requested without waiting for one
-// another; they are added in the order of the CTAs.
+// lanes take a partial each for the maximum and the weights, own ones first, so
+// that all of them are requested at once; then a lane sums D / 32 columns over the
+// partials, in the order of the CTAs.  A row mostly has one or two of each.
 constexpr int kRowWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kRowWarps)
 paged_join_kernel(const PagedArgs own, const PagedArgs shared, int own_tile, int shared_tile) {
-  constexpr int CPL = D / 32;
+  constexpr int CPL = D / 32, kEarly = 2;
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
@@ -406,59 +406,80 @@ paged_join_kernel(const PagedArgs own, const PagedArgs shared, int own_tile, int
   }
   first *= own.heads;
   end *= own.heads;
-  for (long long row = first + static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); row < end;
-       row += static_cast<long long>(gridDim.x) * kRowWarps) {
-    float m = -INFINITY, l = 0.f, acc[CPL] = {};
-    bool also = true;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      if (!also) break;
-      const PagedArgs& a = side ? shared : own;
-      const int RT = side ? shared_tile : own_tile;
-      const int2 rec = a.parts[row];
-      if (side == 0) also = rec.y & kWithPrefix;
-      const long long slots = a.whole;
-      long long at = a.whole + row;
-      int n = 1;
-      if (rec.x >= 0) {
+  // A row's partials of one launch: index of the first and how many.
+  struct Parts {
+    long long at;
+    int n, step;
+    __device__ __forceinline__ Parts(const PagedArgs& a, int2 rec, int tile, long long row, bool any) : step(2 * tile) {
+      at = a.whole + row;
+      n = any ? 1 : 0;
+      if (any && rec.x >= 0) {
         // (Records of rows that arrays in disorder left to nobody must not lead outside.)
         at = rec.x;
         n = rec.y & (kWithPrefix - 1);
-        const long long most = (slots - 1 - at) / (2 * RT) + 1;
-        if (at >= slots) n = 0;
-        else if (n > most) n = static_cast<int>(most);
+        const long long most = at < a.whole ? (a.whole - 1 - at) / step + 1 : 0;
+        if (n > most) n = static_cast<int>(most);
       }
-      for (int p0 = 0; p0 < n; p0 += 32) {
-        const int p = p0 + lane;
-        const long long mine = p == 0 ? at : at + static_cast<long long>(2 * p - 1) * RT;
-        const float pm = p < n ? a.pm[mine] : -INFINITY, pl = p < n ? a.pl[mine] : 0.f;
-        float mx = pm;
+    }
+    __device__ __forceinline__ long long index(int p) const {
+      return p == 0 ? at : at + static_cast<long long>(p) * step - step / 2;
+    }
+  };
+  struct Columns {
+    float v[CPL];
+    __device__ __forceinline__ void load(const float* p) {
+      if constexpr (CPL == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        v[0] = x.x, v[1] = x.y;
+      }
+    }
+  };
+  for (long long row = first + static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); row < end;
+       row += static_cast<long long>(gridDim.x) * kRowWarps) {
+    const int2 r0 = own.parts[row], r1 = shared.parts[row];
+    const Parts a(own, r0, own_tile, row, true), b(shared, r1, shared_tile, row, r0.y & kWithPrefix);
+    const int n = a.n + b.n;
+    auto state = [&](int p) { return p < a.n ? own.po + a.index(p) * D : shared.po + b.index(p - a.n) * D; };
+    float m = -INFINITY, l = 0.f, acc[CPL] = {};
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      const int p = p0 + lane;
+      const bool mine = p < n;
+      const float* pm = p < a.n ? own.pm + a.index(p) : shared.pm + b.index(p - a.n);
+      const float* pl = p < a.n ? own.pl + a.index(p) : shared.pl + b.index(p - a.n);
+      Columns early[kEarly];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-        const float old = ex2(m - ref), w = ex2(pm - ref);
-        m = mn;
-        float part = p < n ? pl * w : 0.f;
+      for (int q = 0; q < kEarly; ++q)
+        if (p0 + q < n) early[q].load(state(p0 + q) + CPL * lane);
+      const float xm = mine ? *pm : -INFINITY, xl = mine ? *pl : 0.f;
+      float mx = xm;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
-        l = fmaf(l, old, part);
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+      const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
+      const float old = ex2(m - ref), w = ex2(xm - ref);
+      m = mn;
+      float part = xl * w;
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) acc[i] *= old;
-        const int np = n - p0 < 32 ? n - p0 : 32;
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kAll, part, o);
+      l = fmaf(l, old, part);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) acc[i] *= old;
+      const int np = n - p0 < 32 ? n - p0 : 32;
+      auto add = [&](const Columns& x, int q) {
+        const float e = __shfl_sync(kAll, w, q);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[i] = fmaf(x.v[i], e, acc[i]);
+      };
+#pragma unroll
+      for (int q = 0; q < kEarly; ++q)
+        if (q < np) add(early[q], q);
 #pragma unroll 4
-        for (int q = 0; q < np; ++q) {
-          const float e = __shfl_sync(kAll, w, q);
-          const int x = p0 + q;
-          const float* o = a.po + (x == 0 ? at : at + static_cast<long long>(2 * x - 1) * RT) * D + CPL * lane;
-          if constexpr (CPL == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(o);
-            acc[0] = fmaf(v.x, e, acc[0]), acc[1] = fmaf(v.y, e, acc[1]);
-            acc[2] = fmaf(v.z, e, acc[2]), acc[3] = fmaf(v.w, e, acc[3]);
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(o);
-            acc[0] = fmaf(v.x, e, acc[0]), acc[1] = fmaf(v.y, e, acc[1]);
-          }
-        }
+      for (int q = kEarly; q < np; ++q) {
+        Columns x;
+        x.load(state(p0 + q) + CPL * lane);
+        add(x, q);
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -359,20 +359,36 @@ __device__ __forceinline__ void turn(const Rot<D, INTER>& rot, const Vec<T>& v, 
 }
 
 // A row of which each of its LPR lanes has eight columns, to 8 bits: codes to
-// dst, the scale, by the row's first lane, to scale.
+// dst, the scale, by the row's first lane, to scale.  (The maximum passes NaN by,
+// and a NaN's code is one; infinities show in it and are dealt with apart.)
 template <int LPR>
-__device__ __forceinline__ void put_codes(const float (&x)[8], bool valid, uint8_t* dst, uint8_t* scale) {
-  unsigned top = 0;
+__device__ __forceinline__ void put_codes(float (&x)[8], bool valid, uint8_t* dst, uint8_t* scale) {
+  float mx = fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
+  mx = fmax3(mx, fabsf(x[3]), fabsf(x[4]));
+  mx = fmax3(mx, fabsf(x[5]), fabsf(x[6]));
+  mx = fmax3(mx, fabsf(x[7]), 0.f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, finite_bits(x[e]));
+  for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, o));
+  unsigned top = __float_as_uint(mx);
+  if (__any_sync(kAll, top >= 0x7f800000u)) {
+    top = 0;
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+    for (int e = 0; e < 8; ++e) {
+      top = max(top, finite_bits(x[e]));
+      x[e] += x[e] - x[e];  // NaN for an infinity
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+  }
   const int byte = scale_byte(top);
   const float inv = inverse_scale(byte);
   if (!valid) return;
+  const uint64_t inv2 = f2pack(inv, inv);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) f2unpack(fmul2(f2pack(x[e], x[e + 1]), inv2), x[e], x[e + 1]);
   uint2 w;
-  w.x = codes2(x[0], x[1], inv) | codes2(x[2], x[3], inv) << 16;
-  w.y = codes2(x[4], x[5], inv) | codes2(x[6], x[7], inv) << 16;
+  w.x = codes2(x[0], x[1]) | codes2(x[2], x[3]) << 16;
+  w.y = codes2(x[4], x[5]) | codes2(x[6], x[7]) << 16;
   *reinterpret_cast<uint2*>(dst) = w;
   if (threadIdx.x % LPR == 0) *scale = static_cast<uint8_t>(byte);
 }

@@ -130,7 +130,9 @@ struct ReadArgs {
   int n_pages;
   int page_shift;
   int kv_heads;
-  int per_warp;  // set by the launcher: rows that a warp takes together
+  // Set by the launcher: rows that a warp takes together; outputs 32-byte aligned.
+  int per_warp;
+  int wide;
 };
 cudaError_t launch_paged_read(const ReadArgs& a, int d, cudaStream_t st);
 

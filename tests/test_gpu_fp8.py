@@ -235,3 +235,20 @@ def test_what_is_appended_is_read_back():
     for out, x in zip(got, (k, v)):
         val, e = fp8_ref.quantise(x.double().cpu().numpy())
         np.testing.assert_array_equal(out.double().cpu().numpy(), val * (2.0 ** e)[..., None])
+
+
+@pytest.mark.parametrize("d, hkv", [(64, 3), (128, 1)])
+def test_read_fp8_to_outputs_at_16_bytes(d, hkv):
+    """Outputs need 16-byte alignment and no more."""
+    ps, n = 16, 100
+    kc, vc, ks, vs, kv, vv = random_pages(9, ps, hkv, d, 6)
+    table = torch.randperm(9)[:7].int().to(DEV).view(1, 7)
+    lens, cu = torch.tensor([n], dtype=torch.int32, device=DEV), torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    want = ra.ra_paged_read_fp8(kc, vc, ks, vs, table, lens, cu, tokens=n)
+    for k_off, v_off in ((8, 0), (0, 8), (8, 8)):
+        flat = [torch.full((n * hkv * d + 16,), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        ko, vo = (f[o:o + n * hkv * d].view(n, hkv, d) for f, o in zip(flat, (k_off, v_off)))
+        ra.ra_paged_read_fp8(kc, vc, ks, vs, table, lens, cu, tokens=n, k_out=ko, v_out=vo)
+        assert torch.equal(ko, want[0]) and torch.equal(vo, want[1])
+        for f, o in zip(flat, (k_off, v_off)):
+            assert (f[:o] == 3).all() and (f[o + n * hkv * d:] == 3).all()
