@@ -27,7 +27,7 @@ SERVE_SOURCE = "serve_binding.cpp"
 SOURCES = ["ra_api.cu", "state_kernels.cu", "simt_kernel.cu", "umma_kernel.cu", "decode_kernel.cu",
            "bwd_kernel.cu", "serve_api.cu", "rope_kernel.cu", "pages_kernel.cu",
            "paged_kernel.cu", "paged_tc_kernel.cu", "paged_read_kernel.cu",
-           "paged_fp8_kernel.cu"]
+           "paged_fp8_kernel.cu", "paged_prefix_kernel.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

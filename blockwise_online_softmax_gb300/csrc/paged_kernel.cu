@@ -534,7 +534,8 @@ size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  if (row_tile == 128) return launch_paged_tc(a, mode, d, ctas, tk, tv, st);
+  if (row_tile == 128)
+    return mode == kShared ? launch_paged_prefix(a, d, ctas, tk, tv, st) : launch_paged_tc(a, mode, d, ctas, tk, tv, st);
   auto run = [&](auto m) {
     constexpr int MODE = decltype(m)::value;
     if (d == 128)

@@ -365,7 +365,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       free_item(it);
       // Keys [lo, hi) of the row (rows past the item's do as its last).
       const int rr = x.rr0 + (r < x.rows ? r : x.rows - 1);
-      int hi = MODE == kShared ? x.end0 : x.end0 + rr / g;
+      int hi = x.end0 + rr / g;
       if (hi < -x.base) hi = -x.base;
       const int lo = win > 0 && hi + x.base > win ? hi - win : -x.base;
       float m = -INFINITY, l = 0.f, alpha = 0.f;
@@ -611,7 +611,6 @@ cudaError_t launch_d(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
 cudaError_t launch_paged_tc(const PagedArgs& a, int mode, int d, int ctas, const CUtensorMap& tk,
                             const CUtensorMap& tv, cudaStream_t st) {
   if (mode == kOwn) return d == 128 ? launch_d<128, kOwn>(a, ctas, tk, tv, st) : launch_d<64, kOwn>(a, ctas, tk, tv, st);
-  if (mode == kShared) return d == 128 ? launch_d<128, kShared>(a, ctas, tk, tv, st) : launch_d<64, kShared>(a, ctas, tk, tv, st);
   return d == 128 ? launch_d<128, kPlain>(a, ctas, tk, tv, st) : launch_d<64, kPlain>(a, ctas, tk, tv, st);
 }
 

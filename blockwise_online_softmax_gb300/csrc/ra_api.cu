@@ -1248,6 +1248,8 @@ int ra_device_status(void* stream) {
   int pt = 0;
   if ((e = ra::take_paged_tc_status(&pt)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
   if (p == 0) p = pt;
+  if ((e = ra::take_paged_prefix_status(&pt)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
+  if (p == 0) p = pt;
   if ((e = ra::take_paged_fp8_status(&pt)) != cudaSuccess) return cuda_fail(e, "reading the paged decode kernel status");
   if (p == 0) p = pt;
   if (a != 0 || b != 0 || c != 0 || w != 0 || p != 0)

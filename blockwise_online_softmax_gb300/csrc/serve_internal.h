@@ -199,6 +199,10 @@ int paged_fp8_box_rows();
 cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);
 cudaError_t take_paged_fp8_status(int* code);
+// The shared launch on row tiles of 128 (the other launches: launch_paged_tc).
+cudaError_t launch_paged_prefix(const PagedArgs& a, int d, int ctas, const CUtensorMap& tk, const CUtensorMap& tv,
+                                cudaStream_t st);
+cudaError_t take_paged_prefix_status(int* code);
 cudaError_t take_paged_status(int* code);
 cudaError_t take_paged_tc_status(int* code);
 

@@ -53,3 +53,29 @@ def test_binding_refusals():
         ra.ra_paged_decode_prefix(q, c, c, i.view(1, 4), None, i[:2], i.view(4, 1), i)
     with pytest.raises(ValueError, match="CUDA"):
         ra.ra_paged_decode_prefix(q, c, c, i.view(1, 4), i[:1], i[:2], i.view(4, 1), i)
+
+
+@pytest.mark.parametrize("name", ["paged_prefix_kernel.cu", "paged_fp8_kernel.cu"])
+def test_a_cta_decides_once_whether_it_runs(name):
+    """As test_serve_edges_host.py's test of the other decode kernels: the abort
+    flag is read for the early return only inside find_run, between its barriers."""
+    import re
+
+    from test_serve_edges_host import source
+
+    kernel = source(name)
+    assert "run.stop" in kernel
+    assert not re.search(r"(if|\|\||&&|while)[^;{]*[^&\w]\*abort_flag", kernel)
+
+
+def test_two_rounded_terms_are_below_a_bf16_step():
+    """With bf16 output a weight is held in two rounded bf16 terms: they leave at
+    most 2^-18 of it, 2^-9 of what rounding the output may."""
+    import numpy as np
+
+    from test_serve_edges_host import rounded
+
+    w = np.random.default_rng(0).uniform(2.0 ** -20, 1, 100000).astype(np.float32)
+    hi = rounded(w)
+    lo = rounded(w - hi)
+    assert (np.abs(w.astype(np.float64) - hi - lo) <= 2.0 ** -18 * w).all()
