@@ -15,7 +15,7 @@
 //   read of T in turn.
 // - The third terms go to shared memory (K-major, 128-byte swizzle, as Q lies) for
 //   want of columns.  With bf16 output there is none: two terms, rounded, leave
-//   2^-18 of a weight at most, half a step of the output is 2^-9.
+//   2^-17 of a weight at most, half a step of the output is 2^-8.
 // - K and V slots of their own, two each, freed by the product that reads them.
 // 2048 rows of each of 8 KV heads, 16K keys, us (the launch): d = 128 bf16 output 146
 // (941 TFLOP/s), fp32 192; d = 64 131 and 186.  What bounds it are the products: 24

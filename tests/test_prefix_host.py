@@ -69,8 +69,10 @@ def test_a_cta_decides_once_whether_it_runs(name):
 
 
 def test_two_rounded_terms_are_below_a_bf16_step():
-    """With bf16 output a weight is held in two rounded bf16 terms: they leave at
-    most 2^-18 of it, 2^-9 of what rounding the output may."""
+    """With bf16 output a weight is held in two rounded bf16 terms (8 bits each).
+    For w in [1, 2): the first leaves at most half of its step 2^-7, that is 2^-8;
+    what is at most 2^-8 has a step of at most 2^-16 (2^-8 itself is exact), of
+    which the second leaves half: 2^-17, 2^-9 of what rounding the output may."""
     import numpy as np
 
     from test_serve_edges_host import rounded
@@ -78,4 +80,6 @@ def test_two_rounded_terms_are_below_a_bf16_step():
     w = np.random.default_rng(0).uniform(2.0 ** -20, 1, 100000).astype(np.float32)
     hi = rounded(w)
     lo = rounded(w - hi)
-    assert (np.abs(w.astype(np.float64) - hi - lo) <= 2.0 ** -18 * w).all()
+    left = np.abs(w.astype(np.float64) - hi - lo)
+    assert (left <= 2.0 ** -17 * w).all()
+    assert (np.abs(w - hi) > 2.0 ** -9 * w).any()  # one term alone is as coarse as the output
