@@ -41,25 +41,26 @@ namespace {
 using namespace paged;
 
 constexpr int kThreads = kMmaThreads;
+constexpr int kKB = 2;
 
-// KB: blocks of 16 keys that a warp takes of a tile.
-template <int D, int NT, int KB>
+// KB: blocks of 16 keys that a warp takes of a tile.  HP: KV heads of an item.
+template <int D, int NT, int KB, int HP>
 struct Cfg {
-  static constexpr int DIM = D, BT = 16 * kCons * KB;
+  static constexpr int DIM = D, BT = 16 * kCons * KB, HEADS = HP;
   static constexpr int NCH = 1, BOX = KB == 1 ? 6 : 7;
-  static constexpr uint32_t CHROW = D, CHB = BT * D;  // rows of 128 or 64 bytes, swizzled over as many
+  static constexpr uint32_t CHROW = D * HP, CHB = BT * CHROW;  // rows of 128 or 64 bytes, swizzled over as many
   static constexpr bool SCALES = true;
   static constexpr int RT = 8 * NT;
   static constexpr int CONS_REGS = NT == 1 ? 152 : 192, PROD_REGS = 256 - CONS_REGS;
   static constexpr int ITEMS = NT == 1 ? 3 : 2;
-  static constexpr uint32_t TILE = BT * D;
+  static constexpr uint32_t TILE = CHB;
   static constexpr uint32_t STAGE = 2 * TILE;
-  static constexpr uint32_t QT = RT * D * 2;
+  static constexpr uint32_t QT = HP * RT * D * 2;
   static constexpr uint32_t REC = 32 + 8 * RT;
   static constexpr uint32_t REST = ITEMS * QT + kCons * 4 * D * 4 + 2 * kCons * RT * 4 + ITEMS * REC + 16;
-  static constexpr int NST = (115712 - REST - 2 * ITEMS * 8) / (STAGE + 2 * BT + 24);  // what two CTAs per SM leave
-  static constexpr uint32_t OFF_SCALE = NST * STAGE;  // of stage s: K's, then V's
-  static constexpr uint32_t OFF_Q = OFF_SCALE + NST * 2 * BT;
+  static constexpr int NST = (115712 - REST - 2 * ITEMS * 8) / (STAGE + 2 * HP * BT + 24);  // what two CTAs per SM leave
+  static constexpr uint32_t OFF_SCALE = NST * STAGE;  // of stage s: K's by head, then V's
+  static constexpr uint32_t OFF_Q = OFF_SCALE + NST * 2 * HP * BT;
   static constexpr uint32_t OFF_BUF = OFF_Q + ITEMS * QT;
   static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 4 * D * 4;
   static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * kCons * RT * 4;
@@ -108,11 +109,11 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t x) {
   return y;
 }
 
-template <int D, int NT, int KB>
+template <int D, int NT, int KB, int HP>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
-  using C = Cfg<D, NT, KB>;
-  constexpr int RT = C::RT, BT = C::BT;
+  using C = Cfg<D, NT, KB, HP>;
+  constexpr int RT = C::RT, BT = C::BT, ROW = D * HP;  // bytes of a key's row
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   auto kfull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * s; };
@@ -122,7 +123,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + C::ITEMS + s); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = a.heads / a.kv_heads;
+  const int g = a.heads / (a.kv_heads * HP);
   let_next_start();
   if (tid == 0) {
     for (int s = 0; s < C::NST; ++s) {
@@ -171,7 +172,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   constexpr int CPR = D / 16;  // 16-byte chunks of a row
   // Of a row r: the swizzle over its chunks (128-byte rows over 8 rows, 64-byte
   // rows over pairs of 8).
-  auto swz = [](int r) { return D == 128 ? r & 7 : (r >> 1) & 3; };
+  auto swz = [](int r) { return ROW == 128 ? r & 7 : (r >> 1) & 3; };
   const int key0 = warp * 16 * KB;  // of the tile
   const int kr = lane & 15, c2 = lane >> 4;  // ldmatrix: row of a block, chunk of a pair
   for (int it = 0;; ++it) {
@@ -195,18 +196,19 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
     // The query rows in fp16: columns 16 c + 4 (lane % 4) + 0..3 of row lane / 4,
     // and the factor on the lane's two scores of a key.
-    uint32_t qf[NT][CPR][2];
-    float sl2[NT][2];
+    uint32_t qf[HP][NT][CPR][2];
+    float sl2[HP][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int sn = 0; sn < HP * NT; ++sn) {
+      const int s = sn / NT, nt = sn % NT;
       const int r = 8 * nt + (lane >> 2);
       unsigned top = 0;
 #pragma unroll
       for (int c = 0; c < CPR; ++c) {
         const int ch = 2 * c + ((lane & 3) >> 1);
-        const uint2 w = lds_v2(sb + C::OFF_Q + is * C::QT + r * (D * 2) + ((ch ^ (r & 7)) << 4) + (lane & 1) * 8);
-        qf[nt][c][0] = w.x;
-        qf[nt][c][1] = w.y;
+        const uint2 w = lds_v2(sb + C::OFF_Q + is * C::QT + (s * RT + r) * (D * 2) + ((ch ^ (r & 7)) << 4) + (lane & 1) * 8);
+        qf[s][nt][c][0] = w.x;
+        qf[s][nt][c][1] = w.y;
         top = max(top, max(max(w.x << 16 & 0x7fff0000u, w.x & 0x7fff0000u), max(w.y << 16 & 0x7fff0000u, w.y & 0x7fff0000u)));
       }
       top = max(top, __shfl_xor_sync(kAll, top, 1));
@@ -218,214 +220,220 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       for (int c = 0; c < CPR; ++c)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          qf[nt][c][h] = f16x2_rn(__uint_as_float(qf[nt][c][h] << 16) * up, __uint_as_float(qf[nt][c][h] & 0xffff0000u) * up);
+          qf[s][nt][c][h] = f16x2_rn(__uint_as_float(qf[s][nt][c][h] << 16) * up, __uint_as_float(qf[s][nt][c][h] & 0xffff0000u) * up);
       const float down = a.scale_log2 * __uint_as_float(static_cast<unsigned>(e - 14) << 23);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) sl2[nt][c] = __shfl_sync(kAll, down, 8 * (lane & 3) + 4 * c);
+      for (int c = 0; c < 2; ++c) sl2[s][nt][c] = __shfl_sync(kAll, down, 8 * (lane & 3) + 4 * c);
     }
-    float m[NT][2], l[NT][2];
-    uint64_t o2[NT][D / 16][2];  // rows 2 (lane % 4) + {0, 1} of a column
+    float m[HP][NT][2], l[HP][NT][2];
+    uint64_t o2[HP][NT][D / 16][2];  // rows 2 (lane % 4) + {0, 1} of a column
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+    for (int sn = 0; sn < HP * NT; ++sn) {
+      const int s = sn / NT, nt = sn % NT;
+      m[s][nt][0] = m[s][nt][1] = -INFINITY;
+      l[s][nt][0] = l[s][nt][1] = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) o2[nt][x][0] = o2[nt][x][1] = f2pack(0.f, 0.f);
+      for (int x = 0; x < D / 16; ++x) o2[s][nt][x][0] = o2[s][nt][x][1] = f2pack(0.f, 0.f);
     }
     for (int k = 0; k < item.tiles; ++k) {
-      const uint32_t kb = sb + st * C::STAGE, vb = kb + C::TILE, scales = sb + C::OFF_SCALE + st * 2 * BT + key0;
+      const uint32_t kb = sb + st * C::STAGE, vb = kb + C::TILE, scales = sb + C::OFF_SCALE + st * 2 * HP * BT + key0;
       const int k0 = (item.k0 + k) * BT + key0;  // the warp's first key
       ok = ok && wait_bar(kfull(st), par, abort_flag, &g_paged_fp8_status, 0xa2, lim);
       ok = __all_sync(kAll, ok);
       const bool some = k0 < item.hi && k0 + 16 * KB > item.lo;
       const bool edge = k0 < item.lo || k0 + 16 * KB > item.hi;
-      float sc[KB][NT][4];
-      uint32_t pb[KB][NT][2][2];
-      float al[NT][2], back = 0.f;
-      bool turned = false;  // some row's maximum is a new one
-      if (some) {
-        // Independent products alternate: each waits for the one before it of the
-        // same sum.  With one group of rows a sum has two halves.
-        constexpr int HALVES = NT == 1 ? 2 : 1;
-        float part[HALVES][KB][NT][4];
 #pragma unroll
-        for (int c = 0; c < CPR; c += 2) {
-          uint32_t w[KB][4];  // (keys 0-7, 8-15) of chunk c, then of chunk c + 1
+      for (int s = 0; s < HP; ++s) {  // the item's heads in turn: their columns of the rows
+        float sc[KB][NT][4];
+        uint32_t pb[KB][NT][2][2];
+        float al[NT][2], back = 0.f;
+        bool turned = false;  // some row's maximum is a new one
+        if (some) {
+          // Independent products alternate: each waits for the one before it of the
+          // same sum.  With one group of rows a sum has two halves.
+          constexpr int HALVES = NT == 1 ? 2 : 1;
+          float part[HALVES][KB][NT][4];
 #pragma unroll
-          for (int b = 0; b < KB; ++b) {
-            const int r = key0 + 16 * b + kr;
-            ldsm4(kb + r * D + (((c + c2) ^ swz(r)) << 4), w[b]);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < CPR; c += 2) {
+            uint32_t w[KB][4];  // (keys 0-7, 8-15) of chunk c, then of chunk c + 1
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
-              const uint32_t af[4] = {low2(w[b][2 * h]), low2(w[b][2 * h + 1]), high2(w[b][2 * h]), high2(w[b][2 * h + 1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float(&t)[4] = part[h % HALVES][b][nt];
-                if (c + h < HALVES) mma_f16_first(t, af, qf[nt][c + h][0], qf[nt][c + h][1]);
-                else mma_f16(t, af, qf[nt][c + h][0], qf[nt][c + h][1]);
-              }
+              const int r = key0 + 16 * b + kr;
+              ldsm4(kb + r * ROW + (((s * CPR + c + c2) ^ swz(r)) << 4), w[b]);
             }
-        }
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+              for (int b = 0; b < KB; ++b) {
+                const uint32_t af[4] = {low2(w[b][2 * h]), low2(w[b][2 * h + 1]), high2(w[b][2 * h]), high2(w[b][2 * h + 1])};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) sc[b][nt][x] = HALVES == 2 ? part[0][b][nt][x] + part[HALVES - 1][b][nt][x] : part[0][b][nt][x];
-        // Scales of the lane's keys lane / 4 and lane / 4 + 8 of each block.
-        float vs[KB][2];
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int j = 16 * b + 8 * h + (lane >> 2);
-            const float ks = scale_of(lds_u8(scales + j));
-            vs[b][h] = scale_of(lds_u8(scales + BT + j));
-            if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0.f;  // nobody's: anything may stand there
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) sc[b][nt][2 * h + c] *= ks;
+                for (int nt = 0; nt < NT; ++nt) {
+                  float(&t)[4] = part[h % HALVES][b][nt];
+                  if (c + h < HALVES) mma_f16_first(t, af, qf[s][nt][c + h][0], qf[s][nt][c + h][1]);
+                  else mma_f16(t, af, qf[s][nt][c + h][0], qf[s][nt][c + h][1]);
+                }
+              }
           }
-        if (k0 < lo_all || k0 + 16 * KB > hi_all) {
 #pragma unroll
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int key = k0 + 16 * b + (lane >> 2) + (c >> 1) * 8;
-                if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[b][nt][c] = -INFINITY;
-              }
-        }
+              for (int x = 0; x < 4; ++x) sc[b][nt][x] = HALVES == 2 ? part[0][b][nt][x] + part[HALVES - 1][b][nt][x] : part[0][b][nt][x];
+          // Scales of the lane's keys lane / 4 and lane / 4 + 8 of each block.
+          float vs[KB][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int b = 0; b < KB; ++b)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+            for (int h = 0; h < 2; ++h) {
+              const int j = 16 * b + 8 * h + (lane >> 2);
+              const float ks = scale_of(lds_u8(scales + s * BT + j));
+              vs[b][h] = scale_of(lds_u8(scales + (HP + s) * BT + j));
+              if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0.f;  // nobody's: anything may stand there
 #pragma unroll
-            for (int b = 1; b < KB; ++b) x = fmax3(x, sc[b][nt][c], sc[b][nt][c + 2]);
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-            const float mn = fmaxf(m[nt][c], x * sl2[nt][c]);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            al[nt][c] = ex2(m[nt][c] - ref);
-            turned |= mn != m[nt][c];
-            m[nt][c] = mn;
-            float sum = 0.f;
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) sc[b][nt][2 * h + c] *= ks;
+            }
+          if (k0 < lo_all || k0 + 16 * KB > hi_all) {
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float p = ex2(fmaf(sc[b][nt][2 * h + c], sl2[nt][c], -ref));
-                sc[b][nt][2 * h + c] = p * vs[b][h];
-                sum += p;
-              }
-            l[nt][c] = fmaf(l[nt][c], al[nt][c], sum);
-          }
-        turned = __any_sync(kAll, turned);
-        // The weights in two fp16 terms, by a power of two that brings the warp's
-        // largest to [2^14, 2^15).
-        float most = 0.f;
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+                for (int c = 0; c < 4; ++c) {
+                  const int key = k0 + 16 * b + (lane >> 2) + (c >> 1) * 8;
+                  if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[b][nt][c] = -INFINITY;
+                }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; c += 2) most = fmax3(most, sc[b][nt][c], sc[b][nt][c + 1]);
-        const uint32_t top = warp_max(__float_as_uint(most)) >> 23;  // its exponent (weights are not negative)
-        const uint32_t lift = top < 15 ? 15 : (top > 254 ? 254 : top);
-        const float f = __uint_as_float((268 - lift) << 23);  // 2^(14 - (lift - 127))
-        back = __uint_as_float(lift > 14 ? (lift - 14) << 23 : 0u);
+            for (int c = 0; c < 2; ++c) {
+              float x = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+              for (int b = 1; b < KB; ++b) x = fmax3(x, sc[b][nt][c], sc[b][nt][c + 2]);
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+              const float mn = fmaxf(m[s][nt][c], x * sl2[s][nt][c]);
+              const float ref = mn == -INFINITY ? 0.f : mn;
+              al[nt][c] = ex2(m[s][nt][c] - ref);
+              turned |= mn != m[s][nt][c];
+              m[s][nt][c] = mn;
+              float sum = 0.f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+              for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float x = sc[b][nt][2 * h] * f, y = sc[b][nt][2 * h + 1] * f;
-              const uint32_t hi = f16x2_rn(x, y);
-              const float2 v = halves(hi);
-              pb[b][nt][0][h] = transpose8x8(hi);
-              pb[b][nt][1][h] = transpose8x8(f16x2_rn(x - v.x, y - v.y));
-            }
-          }
-      }
-      ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim);
-      ok = __all_sync(kAll, ok);
-      if (some) {
-        if (turned) {  // seldom after an item's first tiles
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint64_t al2 = f2pack(al[nt][0], al[nt][1]);
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              o2[nt][x][0] = fmul2(o2[nt][x][0], al2);
-              o2[nt][x][1] = fmul2(o2[nt][x][1], al2);
-            }
-          }
-        }
-        const uint64_t back2 = f2pack(back, back);
-        uint32_t keep[KB][2];  // V rows outside [lo, hi) may hold anything
-#pragma unroll
-        for (int b = 0; b < KB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = k0 + 16 * b + 8 * h + 2 * (lane & 3);
-            keep[b][h] = !edge ? kAll : (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
-                                            (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
-          }
-        constexpr int PAIRS = NT == 1 ? 2 : 1;  // of 32 columns together: four sums alternate
-#pragma unroll
-        for (int c0 = 0; c0 < CPR; c0 += 2 * PAIRS) {
-          uint32_t w[PAIRS][KB][4];  // (keys 0-7, 8-15) of 16 columns, then of the next 16
-#pragma unroll
-          for (int x = 0; x < PAIRS; ++x)
-#pragma unroll
-            for (int b = 0; b < KB; ++b) {
-              const int r = key0 + 16 * b + kr;
-              ldsm4_t(vb + r * D + (((c0 + 2 * x + c2) ^ swz(r)) << 4), w[x][b]);
-              if (edge) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) w[x][b][y] &= keep[b][y & 1];
-              }
-            }
-          uint32_t af[2 * PAIRS][KB][4];
-#pragma unroll
-          for (int x = 0; x < 2 * PAIRS; ++x)
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t y = __byte_perm(w[x >> 1][b][2 * (x & 1) + h], 0, 0x3120);
-                af[x][b][2 * h] = low2(y);  // column 2 (lane / 4) of two keys
-                af[x][b][2 * h + 1] = high2(y);  // the next column
-              }
-          // A tile's product apart, small terms first, then one rounded fp32 step:
-          // the tensor core's own accumulation truncates.
-          float t[2 * PAIRS][NT][4];
-#pragma unroll
-          for (int term = 1; term >= 0; --term)
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-              for (int x = 0; x < 2 * PAIRS; ++x)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if (term == 1 && b == 0) mma_f16_first(t[x][nt], af[x][b], pb[b][nt][1][0], pb[b][nt][1][1]);
-                  else mma_f16(t[x][nt], af[x][b], pb[b][nt][term][0], pb[b][nt][term][1]);
+                for (int h = 0; h < 2; ++h) {
+                  const float p = ex2(fmaf(sc[b][nt][2 * h + c], sl2[s][nt][c], -ref));
+                  sc[b][nt][2 * h + c] = p * vs[b][h];
+                  sum += p;
                 }
+              l[s][nt][c] = fmaf(l[s][nt][c], al[nt][c], sum);
+            }
+          turned = __any_sync(kAll, turned);
+          // The weights in two fp16 terms, by a power of two that brings the warp's
+          // largest to [2^14, 2^15).
+          float most = 0.f;
 #pragma unroll
-          for (int x = 0; x < 2 * PAIRS; ++x)
+          for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                o2[nt][c0 + x][e] = ffma2(f2pack(t[x][nt][2 * e], t[x][nt][2 * e + 1]), back2, o2[nt][c0 + x][e]);
+              for (int c = 0; c < 4; c += 2) most = fmax3(most, sc[b][nt][c], sc[b][nt][c + 1]);
+          const uint32_t top = warp_max(__float_as_uint(most)) >> 23;  // its exponent (weights are not negative)
+          const uint32_t lift = top < 15 ? 15 : (top > 254 ? 254 : top);
+          const float f = __uint_as_float((268 - lift) << 23);  // 2^(14 - (lift - 127))
+          back = __uint_as_float(lift > 14 ? (lift - 14) << 23 : 0u);
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float x = sc[b][nt][2 * h] * f, y = sc[b][nt][2 * h + 1] * f;
+                const uint32_t hi = f16x2_rn(x, y);
+                const float2 v = halves(hi);
+                pb[b][nt][0][h] = transpose8x8(hi);
+                pb[b][nt][1][h] = transpose8x8(f16x2_rn(x - v.x, y - v.y));
+              }
+            }
+        }
+        if (s == 0) {
+          ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim);
+          ok = __all_sync(kAll, ok);
+        }
+        if (some) {
+          if (turned) {  // seldom after an item's first tiles
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint64_t al2 = f2pack(al[nt][0], al[nt][1]);
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) {
+                o2[s][nt][x][0] = fmul2(o2[s][nt][x][0], al2);
+                o2[s][nt][x][1] = fmul2(o2[s][nt][x][1], al2);
+              }
+            }
+          }
+          const uint64_t back2 = f2pack(back, back);
+          uint32_t keep[KB][2];  // V rows outside [lo, hi) may hold anything
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = k0 + 16 * b + 8 * h + 2 * (lane & 3);
+              keep[b][h] = !edge ? kAll : (key >= item.lo && key < item.hi ? 0xffffu : 0u) |
+                                              (key + 1 >= item.lo && key + 1 < item.hi ? 0xffff0000u : 0u);
+            }
+          constexpr int PAIRS = NT == 1 ? 2 : 1;  // of 32 columns together: four sums alternate
+#pragma unroll
+          for (int c0 = 0; c0 < CPR; c0 += 2 * PAIRS) {
+            uint32_t w[PAIRS][KB][4];  // (keys 0-7, 8-15) of 16 columns, then of the next 16
+#pragma unroll
+            for (int x = 0; x < PAIRS; ++x)
+#pragma unroll
+              for (int b = 0; b < KB; ++b) {
+                const int r = key0 + 16 * b + kr;
+                ldsm4_t(vb + r * ROW + (((s * CPR + c0 + 2 * x + c2) ^ swz(r)) << 4), w[x][b]);
+                if (edge) {
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) w[x][b][y] &= keep[b][y & 1];
+                }
+              }
+            uint32_t af[2 * PAIRS][KB][4];
+#pragma unroll
+            for (int x = 0; x < 2 * PAIRS; ++x)
+#pragma unroll
+              for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t y = __byte_perm(w[x >> 1][b][2 * (x & 1) + h], 0, 0x3120);
+                  af[x][b][2 * h] = low2(y);  // column 2 (lane / 4) of two keys
+                  af[x][b][2 * h + 1] = high2(y);  // the next column
+                }
+            // A tile's product apart, small terms first, then one rounded fp32 step:
+            // the tensor core's own accumulation truncates.
+            float t[2 * PAIRS][NT][4];
+#pragma unroll
+            for (int term = 1; term >= 0; --term)
+#pragma unroll
+              for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int x = 0; x < 2 * PAIRS; ++x)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    if (term == 1 && b == 0) mma_f16_first(t[x][nt], af[x][b], pb[b][nt][1][0], pb[b][nt][1][1]);
+                    else mma_f16(t[x][nt], af[x][b], pb[b][nt][term][0], pb[b][nt][term][1]);
+                  }
+#pragma unroll
+            for (int x = 0; x < 2 * PAIRS; ++x)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  o2[s][nt][c0 + x][e] = ffma2(f2pack(t[x][nt][2 * e], t[x][nt][2 * e + 1]), back2, o2[s][nt][c0 + x][e]);
+          }
         }
       }
       __syncwarp();
@@ -435,42 +443,55 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         par ^= 1u;
       }
     }
-    float o[NT][D / 16][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int s = 0; s < HP; ++s) {
+      float o[NT][D / 16][4];
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        f2unpack(o2[nt][x][0], o[nt][x][0], o[nt][x][1]);
-        f2unpack(o2[nt][x][1], o[nt][x][2], o[nt][x][3]);
-      }
-    if (!join_warps<D, NT, true, kPlain>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) return;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          f2unpack(o2[s][nt][x][0], o[nt][x][0], o[nt][x][1]);
+          f2unpack(o2[s][nt][x][1], o[nt][x][2], o[nt][x][3]);
+        }
+      Item part = item;
+      if (item.slot >= 0) part.slot = item.slot * HP + s;
+      if (!join_warps<D, NT, true, kPlain>(a, part, rec, s * g, m[s], l[s], o, ok, s_m, s_l, buf, warp, lane)) return;
+    }
     if (item.last) return;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));
   }
 }
 
-template <int D, int NT, int KB>
+template <int D, int NT, int HP>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(paged_fp8_kernel<D, NT, KB>, Cfg<D, NT, KB>::SMEM, done);
+  constexpr uint32_t smem = Cfg<D, NT, kKB, HP>::SMEM;
+  cudaError_t e = allow_smem(paged_fp8_kernel<D, NT, kKB, HP>, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_early(paged_fp8_kernel<D, NT, KB>, dim3(static_cast<unsigned>(ctas)), kThreads, Cfg<D, NT, KB>::SMEM, st,
-                      tk, tv, a);
+  return launch_early(paged_fp8_kernel<D, NT, kKB, HP>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, st, tk, tv, a);
 }
-
-constexpr int kKB = 2;
 
 }  // namespace
 
 int paged_fp8_row_tile(const PagedArgs& a) { return a.n_q * (a.heads / a.kv_heads) <= 8 ? 8 : 16; }
+// At d = 64 and up to 8 rows two KV heads make an item, where they come in pairs: a
+// key's rows of both are 128 bytes, which HBM gives at a better rate than 64.  One
+// head and two, us: 1.2M keys, 4 heads, 3 rows 175 and 148; 152 requests of up to 6K
+// keys, 4 heads 54.7 and 48.9, 8 heads 87.0 and 81.0.  With 16 rows the arithmetic is
+// the longer part, and half as many items share the work worse: 60 requests of 4K
+// keys, 4 heads, 9 rows 36.5 and 46.3, 1.2M keys 176 and 182.
+int paged_fp8_item_heads(int d, int kv_heads, int row_tile) {
+  return d == 64 && kv_heads % 2 == 0 && row_tile == 8 ? 2 : 1;
+}
 int paged_fp8_box_rows() { return 64 * kKB; }
 
 cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {
   if (d == 128)
-    return row_tile == 8 ? decode_t<128, 1, kKB>(a, ctas, tk, tv, st) : decode_t<128, 2, kKB>(a, ctas, tk, tv, st);
-  return row_tile == 8 ? decode_t<64, 1, kKB>(a, ctas, tk, tv, st) : decode_t<64, 2, kKB>(a, ctas, tk, tv, st);
+    return row_tile == 8 ? decode_t<128, 1, 1>(a, ctas, tk, tv, st) : decode_t<128, 2, 1>(a, ctas, tk, tv, st);
+  if (a.item_heads == 2) return decode_t<64, 1, 2>(a, ctas, tk, tv, st);
+  return row_tile == 8 ? decode_t<64, 1, 1>(a, ctas, tk, tv, st) : decode_t<64, 2, 1>(a, ctas, tk, tv, st);
 }
 
 cudaError_t take_paged_fp8_status(int* code) {

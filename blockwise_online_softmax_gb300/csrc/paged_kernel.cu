@@ -51,6 +51,7 @@ constexpr int kThreads = kMmaThreads;
 template <int D, int NT>
 struct Cfg {
   static constexpr int DIM = D, BT = 64;         // keys per tile
+  static constexpr int HEADS = 1;
   static constexpr int NCH = D / 64, BOX = 6;
   static constexpr uint32_t CHROW = 128, CHB = BT * CHROW;  // a 64-column chunk of a tile, 128-byte swizzle
   static constexpr bool SCALES = false;
@@ -293,7 +294,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         par ^= 1u;
       }
     }
-    if (!join_warps<D, NT, false, MODE>(a, item, rec, m, l, o, ok, s_m, s_l, buf, warp, lane)) break;
+    if (!join_warps<D, NT, false, MODE>(a, item, rec, 0, m, l, o, ok, s_m, s_l, buf, warp, lane)) break;
     if (item.last) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));
@@ -342,8 +343,12 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   const bool early = warp < 2 && c + warp < static_cast<int>(gridDim.x);
   if (early) x = load(warp, blockIdx.y);
   if (cut.last < 0) return;
-  const int np = cut.last - c + 1, g = a.heads / a.kv_heads;
-  for (int r = blockIdx.y; r < cut.rows; r += gridDim.y) {
+  const int np = cut.last - c + 1, g = a.heads / (a.kv_heads * a.item_heads);
+  // (Row h RT + r of a slot is row r of the item's head h.)
+  const int tile = RT / a.item_heads;
+  for (int r = blockIdx.y; r < RT; r += gridDim.y) {
+    const int h = r >= tile ? 1 : 0;
+    if (r - h * tile >= cut.rows) continue;
     float m = -INFINITY, l = 0.f, acc[CPL] = {};
     for (int p = warp; p < np; p += kJoin) {
       if (!early || p != warp || r != static_cast<int>(blockIdx.y)) x = load(p, r);
@@ -373,8 +378,9 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
       l = fmaf(s_l[w], e[w], l);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int rr = cut.rr0 + r, j = rr / g;
-    const long long row = static_cast<long long>(cut.row0 + j) * a.heads + cut.kh * g + (rr - j * g);
+    const int rr = cut.rr0 + r - h * tile, j = rr / g;
+    const long long row =
+        static_cast<long long>(cut.row0 + j) * a.heads + (cut.kh * a.item_heads + h) * g + (rr - j * g);
     for (int i = threadIdx.x; i < D; i += 32 * kJoin) {
       float y = 0.f;
 #pragma unroll
@@ -558,10 +564,12 @@ cudaError_t launch_paged_join(const PagedArgs& own, const PagedArgs& shared, int
 cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_tile, cudaStream_t st) {
   // A CTA per row; no more than an item can have, where that is known here.
   long long rows = row_tile < 16 ? row_tile : 16;
-  if (!a.cu_q && a.n_q * (a.heads / a.kv_heads) < rows) rows = a.n_q * (a.heads / a.kv_heads);
+  const int g = a.heads / (a.kv_heads * a.item_heads);
+  if (!a.cu_q && a.item_heads == 1 && a.n_q * g < rows) rows = a.n_q * g;
+  rows *= a.item_heads;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(rows));
   return launch_early(d == 128 ? paged_combine_kernel<128> : paged_combine_kernel<64>, grid, 32 * kJoin, 0, st, a,
-                      row_tile);
+                      row_tile * a.item_heads);
 }
 
 cudaError_t take_paged_status(int* code) {

@@ -2,7 +2,8 @@
 // paged_fp8_kernel.cu, pages in 8 bits): the item records, the producer warps and
 // the meeting of the consumer warps' states.  Device code only.
 //
-// A kernel's configuration C gives the key tiles BT, the ring (NST stages of STAGE
+// A kernel's configuration C gives the KV heads of an item HEADS (their rows lie side
+// by side in the tiles; a.kv_heads then counts their groups), the key tiles BT, the ring (NST stages of STAGE
 // bytes: a K and a V tile of TILE bytes; where SCALES, BT scales of each in another),
 // the tile's NCH chunks of CHB bytes with rows of CHROW, log2 of the rows of a
 // box BOX, the row tile RT, the item ring (ITEMS) and the offsets in shared memory.
@@ -115,7 +116,7 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
       int row = 0;
       if (lane < RT) {  // rows past the item's get its last row's keys, and no output
         const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = token_of(rr, g);
-        row = (w.q.row0 + j) * a.heads + w.kh * g + (rr - j * g);
+        row = (w.q.row0 + j) * a.heads + w.kh * (C::HEADS * g) + (rr - j * g);
         rec[8 + lane] = row;
         rec[8 + RT + lane] = key_end<MODE>(w.q, j) - base;
       }
@@ -138,12 +139,14 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
       // Chunk c of row r at c ^ (r % 8): the ldmatrix rows of a column
       // block fall into different banks.
 #pragma unroll
-      for (int x0 = 0; x0 < RT * D / 8; x0 += 32) {
-        const int x = x0 + lane, r = x / (D / 8), c = x % (D / 8);
-        const long long at = static_cast<long long>(__shfl_sync(kAll, row, r)) * D + c * 8;
-        copy16(sb + C::OFF_Q + s * C::QT + r * (D * 2) + ((c ^ (r & 7)) << 4),
-               static_cast<const __nv_bfloat16*>(a.q) + at, r < n ? 16u : 0u);
-      }
+      for (int h = 0; h < C::HEADS; ++h)
+#pragma unroll
+        for (int x0 = 0; x0 < RT * D / 8; x0 += 32) {
+          const int x = x0 + lane, r = x / (D / 8), c = x % (D / 8);
+          const long long at = static_cast<long long>(__shfl_sync(kAll, row, r) + h * g) * D + c * 8;
+          copy16(sb + C::OFF_Q + s * C::QT + (h * RT + r) * (D * 2) + ((c ^ (r & 7)) << 4),
+                 static_cast<const __nv_bfloat16*>(a.q) + at, r < n ? 16u : 0u);
+        }
       copies_arrive(ifull(s));
       ++it;
     }
@@ -159,7 +162,7 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
         ok = __all_sync(kAll, ok);
         if (!ok) break;
       }
-      if (lane == 0) mbar_arrive_expect_tx(full(s), n * (box * C::NCH + (C::SCALES && is_k ? 2u * rows : 0u)));
+      if (lane == 0) mbar_arrive_expect_tx(full(s), n * (box * C::NCH + (C::SCALES && is_k ? 2u * C::HEADS * rows : 0u)));
       __syncwarp();
       if (have) {
         const uint32_t dst = sb + s * C::STAGE + (is_k ? 0 : C::TILE) + lane * box;
@@ -169,10 +172,13 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
           tma_load_4d(dst + ch * C::CHB, tm, full(s), ch * 64, w.kh, row, page);
         if constexpr (C::SCALES) {
           if (is_k) {  // both tensors' scales come with the keys
-            const uint32_t to = sb + C::OFF_SCALE + s * 2 * BT + lane * rows;
-            const long long at = (static_cast<long long>(w.kh) << sh) + row;
-            bulk_load(to, a.ks + page * a.ks_page + at, rows, full(s));
-            bulk_load(to + BT, a.vs + page * a.vs_page + at, rows, full(s));
+#pragma unroll
+            for (int h = 0; h < C::HEADS; ++h) {
+              const uint32_t to = sb + C::OFF_SCALE + (s * 2 * C::HEADS + h) * BT + lane * rows;
+              const long long at = (static_cast<long long>(w.kh * C::HEADS + h) << sh) + row;
+              bulk_load(to, a.ks + page * a.ks_page + at, rows, full(s));
+              bulk_load(to + C::HEADS * BT, a.vs + page * a.vs_page + at, rows, full(s));
+            }
           }
         }
       }
@@ -191,9 +197,10 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
 // The states (m, l, o) of the consumer warps, each over its own keys of the item,
 // become one, and go to out and lse, or to partial states.  o[nt][x][c + 2 e] is
 // row 8 nt + 2 (lane % 4) + c, column 16 x + 8 e + lane / 4, or, with PAIRS, column
-// 16 x + 2 (lane / 4) + e.  False: the CTA gives up.
+// 16 x + 2 (lane / 4) + e.  head is added to the record's rows.  False: the CTA gives
+// up.
 template <int D, int NT, bool PAIRS, int MODE>
-__device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item, const int* rec, const float (&m)[NT][2],
+__device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item, const int* rec, int head, const float (&m)[NT][2],
                                            float (&l)[NT][2], float (&o)[NT][D / 16][4], bool ok, float* s_m, float* s_l,
                                            float* buf, int warp, int lane) {
   constexpr int RT = 8 * NT;
@@ -288,7 +295,7 @@ __device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item,
       const int r = 8 * nt + 2 * (lane & 3) + c;
       if (r >= item.rows) continue;
       const bool state = MODE != kPlain || item.slot >= 0;
-      long long row = item.slot >= 0 ? item.slot * RT + r : rec[8 + r];
+      long long row = item.slot >= 0 ? item.slot * RT + r : rec[8 + r] + head;
       if (MODE != kPlain && item.slot < 0) row += a.whole;
 #pragma unroll
       for (int x = 0; x < Q; ++x) {

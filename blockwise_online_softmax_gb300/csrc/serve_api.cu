@@ -123,8 +123,8 @@ int page_map(CUtensorMap* map, const void* base, int n_pages, int page_size, lon
   return RA_OK;
 }
 
-// The same of pages in 8 bits: a box is a head's whole rows.  A row is 128 bytes,
-// or 64 at d = 64, and as much is fetched to L2 (see above).
+// The same of pages in 8 bits: a box is the whole rows of a head, or of two with
+// twice the d.  A row is 128 bytes, or 64, and as much is fetched to L2 (see above).
 int page_map_fp8(CUtensorMap* map, const void* base, int n_pages, int page_size, long long page_stride,
                  int kv_heads, int d) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(kv_heads),
@@ -177,6 +177,7 @@ int decode_args(ra::PagedArgs& a, const void* q, void* out, float* lse, long lon
   a.n_pages = n_pages;
   a.heads = heads;
   a.kv_heads = kv_heads;
+  a.item_heads = 1;
   a.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   a.wait_limit = kWaitLimit;
   return RA_OK;
@@ -194,7 +195,7 @@ int decode_pointers(const ra::PagedArgs& a, std::initializer_list<const void*> p
 // Scratch, the decode over the pages and the launch that joins its cut items.
 int decode_launch(ra::PagedArgs& a, int d, int rt, const CUtensorMap& tk, const CUtensorMap& tv, bool fp8, void* stream) {
   const int ctas = (rt == 128 ? 1 : 2) * ra::sm_count();
-  const size_t rows = static_cast<size_t>(2) * ctas * rt;
+  const size_t rows = static_cast<size_t>(2) * ctas * rt * a.item_heads;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* part = nullptr;
   cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&part), rows * (d + 2) * sizeof(float) + ra::paged_cut_bytes(ctas), st);
@@ -720,9 +721,12 @@ int ra_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
   a.vs_page = v_scale_stride;
   if ((rc = get_encoder()) != RA_OK) return rc;
   CUtensorMap tk, tv;
-  if ((rc = page_map_fp8(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, kv_heads, d)) != RA_OK) return rc;
-  if ((rc = page_map_fp8(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
-  return decode_launch(a, d, ra::paged_fp8_row_tile(a), tk, tv, true, stream);
+  const int row_tile = ra::paged_fp8_row_tile(a);
+  a.item_heads = ra::paged_fp8_item_heads(d, kv_heads, row_tile);
+  a.kv_heads = kv_heads / a.item_heads;
+  if ((rc = page_map_fp8(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, a.kv_heads, d * a.item_heads)) != RA_OK) return rc;
+  if ((rc = page_map_fp8(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, a.kv_heads, d * a.item_heads)) != RA_OK) return rc;
+  return decode_launch(a, d, row_tile, tk, tv, true, stream);
 }
 
 }  // extern "C"

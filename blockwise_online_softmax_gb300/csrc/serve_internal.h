@@ -166,6 +166,7 @@ struct PagedArgs {
   const uint8_t* ks;
   const uint8_t* vs;
   long long ks_page, vs_page;
+  int item_heads;  // KV heads of an item: 1, or 2 of them, whose pairs kv_heads then counts
   // With a shared prefix.  Both launches leave states only: those of items that
   // are not cut at index whole + row of po, pm, pl, and in parts[row] where the
   // row's states are (paged_walk.cuh).
@@ -195,6 +196,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a, int mode, int d, int ctas, const
 // launch; tk, tv as above with a box of a whole row, page_size or
 // paged_fp8_box_rows() rows.
 int paged_fp8_row_tile(const PagedArgs& a);
+int paged_fp8_item_heads(int d, int kv_heads, int row_tile);
 int paged_fp8_box_rows();
 cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);
