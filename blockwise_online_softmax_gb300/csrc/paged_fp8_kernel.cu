@@ -477,12 +477,18 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
 int paged_fp8_row_tile(const PagedArgs& a) { return a.n_q * (a.heads / a.kv_heads) <= 8 ? 8 : 16; }
 // At d = 64 and up to 8 rows two KV heads make an item, where they come in pairs: a
 // key's rows of both are 128 bytes, which HBM gives at a better rate than 64.  One
-// head and two, us: 1.2M keys, 4 heads, 3 rows 175 and 148; 152 requests of up to 6K
-// keys, 4 heads 54.7 and 48.9, 8 heads 87.0 and 81.0.  With 16 rows the arithmetic is
-// the longer part, and half as many items share the work worse: 60 requests of 4K
-// keys, 4 heads, 9 rows 36.5 and 46.3, 1.2M keys 176 and 182.
-int paged_fp8_item_heads(int d, int kv_heads, int row_tile) {
-  return d == 64 && kv_heads % 2 == 0 && row_tile == 8 ? 2 : 1;
+// head and two, us: 1.2M keys, 4 heads, 3 rows 174 and 146; 152 requests of up to 6K
+// keys, 4 heads 54.5 and 46.4, 8 heads 87.7 and 77.1; 64 of up to 500, 16 heads 19.5
+// and 19.1.  A short call takes a longer step with two: 16 requests of up to 2000
+// keys, 4 heads 10.8 and 12.0, 8 heads 12.2 and 13.7, 4 of up to 300 8.6 and 11.0; so
+// not where the block table has no room for more than 48 MB of pages.  With 16 rows
+// the arithmetic is the longer part, and half as many items share the work worse: 60
+// requests of 4K keys, 4 heads, 9 rows 36.5 and 46.3, 1.2M keys 176 and 182.  At d =
+// 128 pairs take 0.92 of the time for 600K keys, and more for all shorter ones (152
+// requests of up to 3000 keys 69 and 78, 16 of up to 2000 13.4 and 16.1).
+int paged_fp8_item_heads(const PagedArgs& a, int d, int row_tile) {
+  const long long tokens = (static_cast<long long>(a.n_req) * a.max_pages) << a.page_shift;
+  return d == 64 && a.kv_heads % 2 == 0 && row_tile == 8 && tokens * a.kv_heads > (48LL << 20) / (2 * 64) ? 2 : 1;
 }
 int paged_fp8_box_rows() { return 64 * kKB; }
 

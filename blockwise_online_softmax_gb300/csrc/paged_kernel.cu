@@ -337,21 +337,21 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   let_next_start();
   wait_for_previous();
   const Cut cut = static_cast<const Cut*>(a.cuts)[c];
+  // Row h tile + r of a slot is row r of the item's head h (of one, or of two).
+  const bool two = a.item_heads == 2;
+  const int tile = two ? RT >> 1 : RT, turn = static_cast<int>(two ? gridDim.y >> 1 : gridDim.y);
+  const int h = static_cast<int>(blockIdx.y) >= turn ? 1 : 0, r0 = static_cast<int>(blockIdx.y) - h * turn;
   // Of the CTA's first row, and of the two partials that most cut items have;
   // whatever the scratch holds when the item has no such partial.
   Part x{};
   const bool early = warp < 2 && c + warp < static_cast<int>(gridDim.x);
-  if (early) x = load(warp, blockIdx.y);
+  if (early) x = load(warp, h * tile + r0);
   if (cut.last < 0) return;
   const int np = cut.last - c + 1, g = a.heads / (a.kv_heads * a.item_heads);
-  // (Row h RT + r of a slot is row r of the item's head h.)
-  const int tile = RT / a.item_heads;
-  for (int r = blockIdx.y; r < RT; r += gridDim.y) {
-    const int h = r >= tile ? 1 : 0;
-    if (r - h * tile >= cut.rows) continue;
+  for (int r = r0; r < cut.rows; r += turn) {
     float m = -INFINITY, l = 0.f, acc[CPL] = {};
     for (int p = warp; p < np; p += kJoin) {
-      if (!early || p != warp || r != static_cast<int>(blockIdx.y)) x = load(p, r);
+      if (!early || p != warp || r != r0) x = load(p, h * tile + r);
       const float mn = fmaxf(m, x.m), ref = mn == -INFINITY ? 0.f : mn;
       const float e0 = ex2(m - ref), e1 = ex2(x.m - ref);
       m = mn;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
       l = fmaf(s_l[w], e[w], l);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int rr = cut.rr0 + r - h * tile, j = rr / g;
+    const int rr = cut.rr0 + r, j = rr / g;
     const long long row =
         static_cast<long long>(cut.row0 + j) * a.heads + (cut.kh * a.item_heads + h) * g + (rr - j * g);
     for (int i = threadIdx.x; i < D; i += 32 * kJoin) {
@@ -565,7 +565,7 @@ cudaError_t launch_paged_combine(const PagedArgs& a, int d, int ctas, int row_ti
   // A CTA per row; no more than an item can have, where that is known here.
   long long rows = row_tile < 16 ? row_tile : 16;
   const int g = a.heads / (a.kv_heads * a.item_heads);
-  if (!a.cu_q && a.item_heads == 1 && a.n_q * g < rows) rows = a.n_q * g;
+  if (!a.cu_q && a.n_q * g < rows) rows = a.n_q * g;
   rows *= a.item_heads;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(rows));
   return launch_early(d == 128 ? paged_combine_kernel<128> : paged_combine_kernel<64>, grid, 32 * kJoin, 0, st, a,

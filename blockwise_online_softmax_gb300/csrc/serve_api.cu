@@ -722,7 +722,7 @@ int ra_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
   if ((rc = get_encoder()) != RA_OK) return rc;
   CUtensorMap tk, tv;
   const int row_tile = ra::paged_fp8_row_tile(a);
-  a.item_heads = ra::paged_fp8_item_heads(d, kv_heads, row_tile);
+  a.item_heads = ra::paged_fp8_item_heads(a, d, row_tile);
   a.kv_heads = kv_heads / a.item_heads;
   if ((rc = page_map_fp8(&tk, n_pages ? k_cache : q, n_pages ? n_pages : 1, page_size, k_page_stride, a.kv_heads, d * a.item_heads)) != RA_OK) return rc;
   if ((rc = page_map_fp8(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, a.kv_heads, d * a.item_heads)) != RA_OK) return rc;

@@ -196,7 +196,7 @@ cudaError_t launch_paged_tc(const PagedArgs& a, int mode, int d, int ctas, const
 // launch; tk, tv as above with a box of a whole row, page_size or
 // paged_fp8_box_rows() rows.
 int paged_fp8_row_tile(const PagedArgs& a);
-int paged_fp8_item_heads(int d, int kv_heads, int row_tile);
+int paged_fp8_item_heads(const PagedArgs& a, int d, int row_tile);
 int paged_fp8_box_rows();
 cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);

@@ -104,6 +104,57 @@ def test_decode_fp8(case, together, spread):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+def widen(table, heads):
+    """The same table with room for so many pages that pairs of KV heads of 64
+    columns make an item (pages behind a request's last are never read)."""
+    width = (1 << 19) // (table.shape[0] * 16 * heads) + table.shape[1]
+    wide = torch.full((table.shape[0], width), 2**30, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+PAIRS = [
+    # lengths, rows per request, heads, kv_heads, page size, window
+    ([1, 0, 2], 1, 8, 2, 16, 0),
+    ([700, 255, 256, 257], 1, 12, 4, 128, 0),
+    ([4097, 600], 1, 16, 8, 32, 100),
+    ([333, 64, 2000], 2, 16, 4, 16, 37),
+    ([50, 4, 900], 4, 8, 4, 64, 0),
+    ([3, 1000, 2], 3, 16, 16, 256, 0),            # rows before the first key
+    ([40000, 9, 12345], 1, 32, 8, 64, 0),
+    ([int(x) for x in np.random.default_rng(1).integers(0, 300, 300)], 1, 8, 2, 16, 0),
+]
+
+
+@pytest.mark.parametrize("together, spread", [(False, 0), (True, 12)])
+@pytest.mark.parametrize("case", PAIRS, ids=lambda c: f"{str(c[0][:4])}-q{c[1]}-h{c[2]}/{c[3]}-p{c[4]}-w{c[5]}")
+def test_pairs_of_heads(case, together, spread):
+    lengths, n_q, H, Hkv, ps, window = case
+    rows = [n_q] * len(lengths)
+    q, pages, table, lens, ks, vs = make8(lengths, rows, H, Hkv, 64, ps, together=together, spread=spread, seed=7)
+    wide = widen(table, Hkv)
+    out, lse = ra.ra_paged_decode_fp8(q, *pages, wide, lens, window=window)
+    ra.ra_device_status()
+    check_decode(out, lse, q, ks, vs, rows, window)
+    again = ra.ra_paged_decode_fp8(q, *pages, wide, lens, window=window)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    bf = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+    _, lse2 = ra.ra_paged_decode_fp8(q, *pages, wide, lens, window=window, out=bf)
+    assert torch.equal(bf, out.bfloat16()) and torch.equal(lse2, lse)
+
+
+def test_pairs_of_heads_with_ragged_rows():
+    for rows in ([1, 0, 3, 1], [0, 0, 2, 0], [40, 1, 0, 7]):
+        q, pages, table, lens, ks, vs = make8([500, 77, 300, 1025], rows, 8, 2, 64, 16, extra=5)
+        out = torch.full(q.shape, 9.0, device=DEV)
+        lse = torch.full(q.shape[:2], 9.0, device=DEV)
+        cu = i32(np.concatenate([[0], np.cumsum(rows)]))
+        ra.ra_paged_decode_fp8(q, *pages, widen(table, 2), lens, cu_q=cu, n_q=1, out=out, lse=lse)
+        ra.ra_device_status()
+        check_decode(out, lse, q, ks, vs, rows)
+        assert (out[-5:] == 9.0).all() and (lse[-5:] == 9.0).all()
+
+
 @pytest.mark.parametrize("rows", [[1, 0, 3, 1], [0, 0, 2, 0], [40, 1, 0, 7]])
 def test_ragged_rows(rows):
     """cu_q: idle requests, several rows, and rows behind the last request
