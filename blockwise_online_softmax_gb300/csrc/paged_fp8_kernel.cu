@@ -244,7 +244,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const bool edge = k0 < item.lo || k0 + 16 * KB > item.hi;
 #pragma unroll
       for (int s = 0; s < HP; ++s) {  // the item's heads in turn: their columns of the rows
-        float sc[KB][NT][4];
+        uint64_t sc[KB][NT][2];  // of the lane's two rows, keys lane / 4 and lane / 4 + 8 of a block
         uint32_t pb[KB][NT][2][2];
         float al[NT][2], back = 0.f;
         bool turned = false;  // some row's maximum is a new one
@@ -279,7 +279,10 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) sc[b][nt][x] = HALVES == 2 ? part[0][b][nt][x] + part[HALVES - 1][b][nt][x] : part[0][b][nt][x];
+              for (int h = 0; h < 2; ++h) {
+                sc[b][nt][h] = f2pack(part[0][b][nt][2 * h], part[0][b][nt][2 * h + 1]);
+                if (HALVES == 2) sc[b][nt][h] = fadd2(sc[b][nt][h], f2pack(part[HALVES - 1][b][nt][2 * h], part[HALVES - 1][b][nt][2 * h + 1]));
+              }
           // Scales of the lane's keys lane / 4 and lane / 4 + 8 of each block.
           float vs[KB][2];
 #pragma unroll
@@ -291,9 +294,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               vs[b][h] = scale_of(lds_u8(scales + (HP + s) * BT + j));
               if (edge && (k0 + j < item.lo || k0 + j >= item.hi)) vs[b][h] = 0.f;  // nobody's: anything may stand there
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) sc[b][nt][2 * h + c] *= ks;
+              for (int nt = 0; nt < NT; ++nt) sc[b][nt][h] = fmul2(sc[b][nt][h], f2pack(ks, ks));
             }
           if (k0 < lo_all || k0 + 16 * KB > hi_all) {
 #pragma unroll
@@ -301,37 +302,54 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  const int key = k0 + 16 * b + (lane >> 2) + (c >> 1) * 8;
-                  if (key < rlo[nt][c & 1] || key >= rhi[nt][c & 1]) sc[b][nt][c] = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                  const int key = k0 + 16 * b + (lane >> 2) + h * 8;
+                  float x[2];
+                  f2unpack(sc[b][nt][h], x[0], x[1]);
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (key < rlo[nt][c] || key >= rhi[nt][c]) x[c] = -INFINITY;
+                  sc[b][nt][h] = f2pack(x[0], x[1]);
                 }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[KB][2][2], ref[2], sum[2];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) f2unpack(sc[b][nt][h], x[b][h][0], x[b][h][1]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float x = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+              float mx = fmaxf(x[0][0][c], x[0][1][c]);
 #pragma unroll
-              for (int b = 1; b < KB; ++b) x = fmax3(x, sc[b][nt][c], sc[b][nt][c + 2]);
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-              const float mn = fmaxf(m[s][nt][c], x * sl2[s][nt][c]);
-              const float ref = mn == -INFINITY ? 0.f : mn;
-              al[nt][c] = ex2(m[s][nt][c] - ref);
+              for (int b = 1; b < KB; ++b) mx = fmax3(mx, x[b][0][c], x[b][1][c]);
+              mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+              const float mn = fmaxf(m[s][nt][c], mx * sl2[s][nt][c]);
+              ref[c] = mn == -INFINITY ? 0.f : mn;
+              al[nt][c] = ex2(m[s][nt][c] - ref[c]);
               turned |= mn != m[s][nt][c];
               m[s][nt][c] = mn;
-              float sum = 0.f;
-#pragma unroll
-              for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float p = ex2(fmaf(sc[b][nt][2 * h + c], sl2[s][nt][c], -ref));
-                  sc[b][nt][2 * h + c] = p * vs[b][h];
-                  sum += p;
-                }
-              l[s][nt][c] = fmaf(l[s][nt][c], al[nt][c], sum);
             }
+            // Two rows at a time: exponentials, their sum, and times the values' scales.
+            const uint64_t nref = f2pack(-ref[0], -ref[1]), by = f2pack(sl2[s][nt][0], sl2[s][nt][1]);
+            uint64_t both = f2pack(0.f, 0.f);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float p0, p1;
+                f2unpack(ffma2(sc[b][nt][h], by, nref), p0, p1);
+                const uint64_t p = f2pack(ex2(p0), ex2(p1));
+                both = fadd2(both, p);
+                sc[b][nt][h] = fmul2(p, f2pack(vs[b][h], vs[b][h]));
+              }
+            f2unpack(both, sum[0], sum[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) l[s][nt][c] = fmaf(l[s][nt][c], al[nt][c], sum[c]);
+          }
           turned = __any_sync(kAll, turned);
           // The weights in two fp16 terms, by a power of two that brings the warp's
           // largest to [2^14, 2^15).
@@ -341,7 +359,11 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; c += 2) most = fmax3(most, sc[b][nt][c], sc[b][nt][c + 1]);
+              for (int h = 0; h < 2; ++h) {
+                float w0, w1;
+                f2unpack(sc[b][nt][h], w0, w1);
+                most = fmax3(most, w0, w1);
+              }
           const uint32_t top = warp_max(__float_as_uint(most)) >> 23;  // its exponent (weights are not negative)
           const uint32_t lift = top < 15 ? 15 : (top > 254 ? 254 : top);
           const float f = __uint_as_float((268 - lift) << 23);  // 2^(14 - (lift - 127))
@@ -352,11 +374,14 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const float x = sc[b][nt][2 * h] * f, y = sc[b][nt][2 * h + 1] * f;
+                const uint64_t w = fmul2(sc[b][nt][h], f2pack(f, f));
+                float x, y;
+                f2unpack(w, x, y);
                 const uint32_t hi = f16x2_rn(x, y);
                 const float2 v = halves(hi);
+                f2unpack(ffma2(f2pack(v.x, v.y), f2pack(-1.f, -1.f), w), x, y);
                 pb[b][nt][0][h] = transpose8x8(hi);
-                pb[b][nt][1][h] = transpose8x8(f16x2_rn(x - v.x, y - v.y));
+                pb[b][nt][1][h] = transpose8x8(f16x2_rn(x, y));
               }
             }
         }
