@@ -77,14 +77,18 @@ struct Cfg {
   static constexpr uint32_t OFF_X = OFF_AL + kA * RT * 4;  // running maximum
   static constexpr uint32_t OFF_INV = OFF_X + RT * 4;      // l of one group
   static constexpr uint32_t OFF_ITEM = OFF_INV + RT * 4;
-  // Barriers: K and V slots filled and free; S(k) (four by turns); P(k); T(k)
+  // Barriers: K and V slots filled and free; S(k) (four by turns); P(k) (four); T(k)
   // ready, which also frees P(k) and its third terms (four); T(k) and alpha(k) read
-  // (four); alpha(k) (three); running maximum after k there, and read; query rows
-  // read; item records in and read; an item's l handed over and its end read; the
-  // two issuers' drains.  A wait names its phase by parity: each is for a phase
-  // whose successor on the same barrier needs what follows the wait.
+  // (four); alpha(k) (three); running maximum after k, by group; query rows read;
+  // item records in and read; an item's l handed over and its end read; the two
+  // issuers' drains.  A wait names its phase by parity: each is for a phase whose
+  // successor on the same barrier needs what follows the wait.  And the warps of a
+  // role may be tiles apart: where they arrive together, the barrier's next phase
+  // needs the one before it complete.  (A group's warp may be at its weights of k + 2
+  // while another is at those of k, so P(k) and P(k + 2) have barriers of their own;
+  // P(k + 4) needs S(k + 4), that needs T(k + 1), and that P(k).)
   static constexpr int B_KF = 0, B_KE = B_KF + 2, B_VF = B_KE + 2, B_VE = B_VF + 2, B_S = B_VE + 2, B_P = B_S + 4,
-                       B_T = B_P + 2, B_TF = B_T + 4, B_AL = B_TF + 4, B_M = B_AL + kA, B_QF = B_M + 2, B_I = B_QF + 1,
+                       B_T = B_P + 4, B_TF = B_T + 4, B_AL = B_TF + 4, B_M = B_AL + kA, B_QF = B_M + 2, B_I = B_QF + 1,
                        B_IF = B_I + 2, B_L = B_IF + 2, B_ML = B_L + 1, B_MLF = B_ML + 1, B_DRAIN = B_MLF + 2,
                        NBAR = B_DRAIN + 2;
   static constexpr uint32_t OFF_BAR = OFF_ITEM + 2 * sizeof(Item);
@@ -333,7 +337,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           const int before = D == 128 ? k - 1 : k - 2;
           ok = wait1(C::B_VF + (k & 1), static_cast<uint32_t>(k >> 1), 0xc8) &&
                (before < 0 || wait1((D == 128 ? C::B_T : C::B_TF) + (before & 3), by4(before), 0xc9)) &&
-               wait1(C::B_P + (k & 1), static_cast<uint32_t>(k >> 1), 0xc7);
+               wait1(C::B_P + (k & 3), by4(k), 0xc7);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(sb + C::OFF_V + static_cast<uint32_t>(k & 1) * C::TILE, CHB, 1024);
@@ -494,7 +498,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::B_P + gi));
+        mbar_arrive(bar(C::B_P + (k & 3)));
         float sa, sc;
         f2unpack(fadd2(acc0, acc1), sa, sc);
         l += sa + sc;

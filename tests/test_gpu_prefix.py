@@ -377,3 +377,29 @@ def test_wrong_tensors_are_refused():
         run(kc=args[1].half())
     with pytest.raises(ValueError, match="must match in pages"):
         run(vc=args[2][:-1])
+
+
+@pytest.mark.parametrize("d, bf16", [(128, True), (128, False), (64, True), (64, False)])
+def test_warps_that_are_tiles_apart(d, bf16):
+    """Few rows and many short runs of tiles, keys from HBM and from L2 in turn: the
+    warps that form a tile's weights drift apart by as much as the kernel lets
+    them.  A weight handed over for another tile's shows as a wait that runs out,
+    or as another result.  Every call's result is the first one's."""
+    groups = [(16000, [int(x) for x in np.random.default_rng(d).integers(1, 300, 16)])]
+    sets = [make(groups, [1] * 16, 32, 8, d, 16, seed=s) for s in range(3)]
+    outs = [torch.empty(16, 32, d, dtype=torch.bfloat16 if bf16 else torch.float32, device=DEV) for _ in sets]
+    want = []
+    for (args, k, v), out in zip(sets, outs):
+        _, lse = ra.ra_paged_decode_prefix(*args, out=out)
+        ra.ra_device_status()
+        check_decode(out, lse, args[0], k, v, [1] * 16)
+        want.append((out.clone(), lse))
+    for rep in range(12):
+        cold = torch.empty(1 << 28, dtype=torch.uint8, device=DEV).fill_(rep)  # L2 holds something else
+        got = []
+        for i in range(3 if rep < 8 else 60):
+            got.append((i % 3, ra.ra_paged_decode_prefix(*sets[i % 3][0], out=torch.empty_like(outs[0]))))
+        ra.ra_device_status()
+        for i, (out, lse) in got:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+        del cold
