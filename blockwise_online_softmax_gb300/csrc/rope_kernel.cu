@@ -375,7 +375,7 @@ __device__ __forceinline__ void put_codes(float (&x)[8], bool valid, uint8_t* ds
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       top = max(top, finite_bits(x[e]));
-      x[e] += x[e] - x[e];  // NaN for an infinity
+      x[e] = fmaf(0.f, x[e], x[e]);  // NaN for an infinity; zeros keep their sign
     }
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));

@@ -152,6 +152,33 @@ def test_codes_of_k_are_those_of_the_plain_form():
         np.testing.assert_array_equal(bytes_of(s).transpose(0, 2, 1).reshape(-1, hkv)[:T], e + 127)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_that_is_not_finite_leaves_its_neighbours_alone(d):
+    """Every byte of the other rows is as without it, a zero's sign among them."""
+    T, hkv, ps = 6, 8, 16
+    x = torch.randn(T, hkv, d).bfloat16()
+    x[:, :, ::3] = -0.0
+    x[:, :, 1::6] = 0.0
+    other = x.clone()
+    other[2, 3, 5], other[4, 0, 1], other[4, 7, d - 1] = float("inf"), float("nan"), -float("inf")
+    slots = torch.arange(T, device=DEV)
+    pos = torch.zeros(T, dtype=torch.int32, device=DEV)
+    held = []
+    for y in (x.to(DEV), other.to(DEV)):
+        pages = make_pages(1, ps, hkv, d)
+        ra.ra_paged_append_fp8(y, y, y, None, *pages, slots, pos)
+        held.append([bytes_of(p) for p in pages])
+    ra.ra_device_status()
+    same = np.ones((1, ps, hkv), bool)
+    same[0, [2, 4, 4], [3, 0, 7]] = False
+    for a, b in zip(held[0][:2], held[1][:2]):
+        np.testing.assert_array_equal(a[same], b[same])
+    v = held[0][1][0, :T]
+    assert (v[..., ::3] == 0x80).all() and (v[..., 1::6] == 0).all()
+    for a, b in zip(held[0][2:], held[1][2:]):
+        np.testing.assert_array_equal(a.transpose(0, 2, 1)[same], b.transpose(0, 2, 1)[same])
+
+
 # ------------------------------------------------------------------ read
 
 def read_expected(vals, table, lens, cu, tokens, ps, before):
