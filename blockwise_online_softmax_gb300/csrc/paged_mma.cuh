@@ -82,6 +82,7 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
   auto empty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (2 * C::NST + s); };
   auto ifull = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + s); };
   auto iempty = [&](int s) -> uint32_t { return sb + C::OFF_BAR + 8u * (3 * C::NST + C::ITEMS + s); };
+  const Joined joined(a);
   Walk<BT, kExtra, MODE> w;
   w.start(a, g, RT, run.r, run.x);
   long long u = run.first;
@@ -120,13 +121,12 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
         rec[8 + lane] = row;
         rec[8 + RT + lane] = key_end<MODE>(w.q, j) - base;
       }
-      const int joined = MODE == kOwn && with_prefix(a, w.r, lane) ? kWithPrefix : 0;
       if (MODE != kPlain || lane == 0) {
         const long long item0 = u - w.k;
         const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
         const int me = static_cast<int>(blockIdx.x);
         if (MODE != kPlain && lane < n && me == c0)
-          a.parts[row] = part_record(c0 == c1 ? -1 : (2 * me + 1) * RT + lane, c1 - c0 + 1 + joined);
+          a.parts[row] = part_record(c0 == c1 ? -1 : (2 * me + 1) * RT + lane, c1 - c0 + 1 + (MODE == kOwn ? joined.mark(w.r) : 0));
         if (lane == 0) {
           *reinterpret_cast<Item*>(rec) =
               Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), after >= run.last};

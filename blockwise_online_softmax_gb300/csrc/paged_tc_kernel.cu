@@ -196,6 +196,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int rows = sh < 6 ? 1 << sh : 64;  // of a box
       const int boxes = BT / rows;
       const uint32_t box = static_cast<uint32_t>(rows) * 128u;
+      const Joined joined(a);
       Walk<BT, 0, MODE> w;
       w.start(a, g, RT, run.r, run.x);
       long long u = run.first;
@@ -207,7 +208,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (is_k) {
           if (it >= 2) ok = wait(C::B_IF + (it & 1), static_cast<uint32_t>(it >> 1) ^ 1u, 0x92);
           if (!ok) break;
-          const int joined = MODE == kOwn && with_prefix(a, w.r, lane) ? kWithPrefix : 0;
           if (lane == 0) {
             const long long item0 = u - w.k;
             const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
@@ -215,7 +215,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const int base = w.t.t0 * BT, n = w.t.rr1 - w.t.rr0;
             items[it & 1] = Item{n, w.t.rr0, w.q.row0, w.kh, key_end<MODE>(w.q, 0, false) - base, base,
                                  w.t.lo - base, w.t.hi - base, w.k, tiles,
-                                 c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), c1 - c0 + 1 + joined};
+                                 c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), c1 - c0 + 1 + (MODE == kOwn ? joined.mark(w.r) : 0)};
             if (MODE == kPlain && c0 != c1 && me == c0)
               static_cast<Cut*>(a.cuts)[me] = Cut{c1, w.q.row0, w.t.rr0, n, w.kh};
             mbar_arrive(bar(C::B_I + (it & 1)));

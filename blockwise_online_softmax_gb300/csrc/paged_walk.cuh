@@ -74,16 +74,17 @@ __device__ __forceinline__ void end_wait() {
 // is whole; + kWithPrefix in the rows of kOwn whose request has a prefix.
 constexpr int kWithPrefix = 1 << 20;  // (more than CTAs)
 __device__ __forceinline__ int2 part_record(int first, int parts) { return make_int2(first, parts); }
-// Whether request r is one of a group.  A warp looks through 31 groups at a time.
-__device__ __forceinline__ bool with_prefix(const PagedArgs& a, int r, int lane) {
-  for (int g0 = 0; g0 < a.n_groups; g0 += 31) {
-    const int g = g0 + lane;
-    const int b = g <= a.n_groups ? a.cu_req[g] : 0;
-    const int e = __shfl_down_sync(kAll, b, 1);
-    if (__any_sync(kAll, lane < 31 && g < a.n_groups && b <= r && r < e)) return true;
+// The requests that are one of a group: groups follow one another.
+struct Joined {
+  int first = 0, end = 0;
+  __device__ __forceinline__ Joined(const PagedArgs& a) {
+    if (a.n_groups > 0) {
+      first = a.cu_req[0];
+      end = a.cu_req[a.n_groups];
+    }
   }
-  return false;
-}
+  __device__ __forceinline__ int mark(int r) const { return first <= r && r < end ? kWithPrefix : 0; }
+};
 
 template <int MODE>
 __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
