@@ -279,3 +279,77 @@ def test_read_fp8_to_outputs_at_16_bytes(d, hkv):
         assert torch.equal(ko, want[0]) and torch.equal(vo, want[1])
         for f, o in zip(flat, (k_off, v_off)):
             assert (f[:o] == 3).all() and (f[o + n * hkv * d:] == 3).all()
+
+
+def test_append_in_place_and_captured():
+    """q_out = q; a graph replayed with other slots and inputs; eps = 0."""
+    T, heads, hkv, d, ps = 40, 8, 2, 128, 16
+    g = torch.Generator(device=DEV).manual_seed(2)
+    data = [torch.randn(T, heads + 2 * hkv, d, generator=g, device=DEV).bfloat16() for _ in range(3)]
+    w = torch.rand(d, generator=g, device=DEV) + 0.5
+    freqs, _ = ra.rope_freqs(d)
+    phases = ra.rope_phases(freqs).to(DEV)
+    slots = [torch.randperm(64, generator=g, device=DEV)[:T] for _ in range(3)]
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+
+    def split(x):
+        return [y.contiguous() for y in x.split([heads, hkv, hkv], 1)]
+
+    def fresh():
+        return make_pages(4, ps, hkv, d)
+
+    kw = dict(q_weight=w, k_weight=w, eps=0.0)
+    q, k, v = split(data[0])
+    at, pages = slots[0].clone(), fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert ra.ra_paged_append_fp8(q, k, v, phases, *pages, at, pos, q_out=q, **kw) is q
+    for x, s in zip(data, slots):
+        want = fresh()
+        x3 = split(x)
+        qw = ra.ra_paged_append_fp8(*x3, phases, *want, s, pos, **kw)
+        for y, z in zip((q, k, v), x3):
+            y.copy_(z)
+        at.copy_(s)
+        for p in pages:
+            p.view(torch.uint8).fill_(0x55)
+        graph.replay()
+        ra.ra_device_status()
+        assert torch.equal(q, qw) and qw.isfinite().all()
+        for a, b in zip(pages, want):
+            np.testing.assert_array_equal(bytes_of(a), bytes_of(b))
+
+
+def test_read_of_more_requests_than_threads_captured():
+    """Most of them without a row; replayed with other lengths and offsets."""
+    n, ps, hkv, d = 5000, 16, 2, 64
+    rng = np.random.default_rng(3)
+    kc, vc, ks, vs, kx, vx = random_pages(600, ps, hkv, d, 4)
+    table = torch.from_numpy(rng.integers(0, 600, (n, 3)).astype(np.int32)).to(DEV)
+    lens = torch.zeros(n, dtype=torch.int32, device=DEV)
+    cu = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    tokens = 4000
+    ko, vo = (torch.full((tokens, hkv, d), 5.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ra.ra_paged_read_fp8(kc, vc, ks, vs, table, lens, cu, tokens=tokens, k_out=ko, v_out=vo)
+    for seed in range(3):
+        r = np.random.default_rng(seed)
+        length = r.integers(0, 3 * ps + 1, n)
+        rows = np.where(r.random(n) < 0.03, r.integers(0, length + 1), 0)
+        lens.copy_(torch.from_numpy(length.astype(np.int32)))
+        offs = np.concatenate([[0], np.cumsum(rows)])
+        assert 0 < offs[-1] < tokens
+        cu.copy_(torch.from_numpy(offs.astype(np.int32)))
+        ko.fill_(5.0)
+        vo.fill_(5.0)
+        graph.replay()
+        ra.ra_device_status()
+        for out, x in ((ko, kx), (vo, vx)):
+            got = out.double().cpu().numpy()
+            for i in np.flatnonzero(rows):
+                h = x[table[i].cpu().numpy()].reshape(-1, hkv, d)[length[i] - rows[i]:length[i]]
+                np.testing.assert_array_equal(got[offs[i]:offs[i + 1]], h)
+            assert (got[offs[-1]:] == 5.0).all()

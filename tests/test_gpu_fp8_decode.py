@@ -601,3 +601,17 @@ def test_a_prompt_in_chunks_and_tokens_one_by_one():
     ref, _ = oracle.attention(qr.cpu(), kd.cpu(), vd.cpu(), causal=True)
     err = np.abs(np64(torch.cat(outs)) - ref)
     assert err[:697].max() <= 1e-2 and err[697:].max() <= 1e-4
+
+
+@pytest.mark.parametrize("d, Hkv", [(64, 4), (128, 2)])
+def test_more_rows_than_expected_and_windows_past_the_history(d, Hkv):
+    rows = [1, 30, 2, 0, 1]
+    q, pages, table, lens, ks, vs = make8([700, 90, 3, 40, 1], rows, 4 * Hkv, Hkv, d, 16, extra=3)
+    cu = i32(np.concatenate([[0], np.cumsum(rows)]))
+    for window in (0, 700, 2**31 - 1, 2**31, 2**62):
+        out = torch.full(q.shape, 9.0, device=DEV)
+        lse = torch.full(q.shape[:2], 9.0, device=DEV)
+        ra.ra_paged_decode_fp8(q, *pages, table, lens, cu_q=cu, n_q=1, window=window, out=out, lse=lse)
+        ra.ra_device_status()
+        check_decode(out, lse, q, ks, vs, rows)
+        assert (out[-3:] == 9.0).all() and (lse[-3:] == 9.0).all()

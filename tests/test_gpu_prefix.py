@@ -3,6 +3,10 @@ request's prefix and own keys together.  Tolerances: test_gpu_paged.py, with n
 the prefix's and the own keys, and for the join of two partial sums of a row 16 u
 more (a factor ex2 good to 6.4 u on either side, two roundings)."""
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -51,7 +55,7 @@ CASES = [
     ([(9, [2] * 300)], 1, 64, 8, 128, 16),
     ([(300, [6] * 3), (1, []), (40, [8])], 3, 128, 1, 128, 16),
     ([(int(p), [int(x) for x in np.random.default_rng(p).integers(1, 200, p % 7 + 1)])
-      for p in range(0, 400, 13)], 1, 8, 2, 64, 16),     # 31 groups: over one look of a warp
+      for p in range(0, 400, 13)], 1, 8, 2, 64, 16),     # 31 groups
     ([(int(p), [int(p) % 50 + 1]) for p in range(1, 100)], 1, 4, 4, 128, 16),
 ]
 
@@ -403,3 +407,127 @@ def test_warps_that_are_tiles_apart(d, bf16):
         for i, (out, lse) in got:
             assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
         del cold
+
+
+def test_more_groups_than_threads():
+    """Every CTA looks through all of them; many are of no request or no key."""
+    r = np.random.default_rng(7)
+    groups = [(int(r.integers(0, 24)), [int(x) for x in r.integers(1, 12, int(r.integers(0, 3)))]) for _ in range(1200)]
+    rows = [1] * sum(len(x) for _, x in groups)
+    args, k, v = make(groups, rows, 2, 1, 64, 8)
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    check_decode(out, lse, args[0], k, v, rows)
+
+
+def test_cache_without_pages():
+    q = torch.randn(4, 8, 128, device=DEV).bfloat16()
+    none = torch.empty(0, 16, 2, 128, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(2, 3, dtype=torch.int32, device=DEV)
+    cu, zero = i32([0, 1, 2]), i32([0, 0])
+    out, lse = ra.ra_paged_decode_prefix(q, none, none, table, zero, cu, table, zero)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    ra.ra_paged_decode_prefix(q, none, none, table, i32([40, 3]), cu, table, i32([2, 48]))  # pages that are not there
+    ra.ra_device_status()
+
+
+@pytest.mark.parametrize("per", [2, 40])
+@pytest.mark.parametrize("what", ["key", "value"])
+def test_nan_in_a_prefix_stays_with_its_group(per, what):
+    groups = [(300, [20] * per), (300, [20] * per)]
+    args, k, v = make(groups, [1] * 2 * per, 8, 2, 128, 16)
+    want = ra.ra_paged_decode_prefix(*args)
+    page = int(args[3][0, 200 // 16])
+    (args[1] if what == "key" else args[2])[page, 200 % 16, 1, 5] = float("nan")
+    out, lse = ra.ra_paged_decode_prefix(*args)
+    ra.ra_device_status()
+    assert torch.equal(out[per:], want[0][per:]) and torch.equal(lse[per:], want[1][per:])
+    assert torch.equal(out[:per, :4], want[0][:per, :4])  # the other KV head's rows
+    if what == "key":
+        assert out[:per, 4:].isnan().all() and lse[:per, 4:].isnan().all()
+    else:
+        assert out[:per, 4:, 5].isnan().all() and torch.equal(lse[:per], want[1][:per])
+
+
+def test_outputs_left_out_on_another_stream():
+    args, k, v = make([(900, [40, 2, 64])], [1] * 3, 32, 8, 128, 16)
+    want = ra.ra_paged_decode_prefix(*args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for st in (side, side.cuda_stream):
+        got = ra.ra_paged_decode_prefix(*args, stream=st)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_threads_on_streams_of_their_own():
+    cases = [make([(900, [40, 2, 64])], [1] * 3, 32, 8, 128, 16, seed=1)[0],
+             make([(2000, [70] * 25), (3, [9])], [2] * 26, 8, 2, 128, 16, seed=2)[0]]
+    want = [ra.ra_paged_decode_prefix(*c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(30):
+                out, lse = ra.ra_paged_decode_prefix(*cases[i])
+                st.synchronize()
+                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    ra.ra_device_status()
+    assert not bad
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import blockwise_online_softmax_gb300 as ra
+from test_gpu_prefix import check_decode, make
+args, k, v = make([(700, [64, 3] * 10), (50, [4])], [1] * 21, 8, 2, 128, 16)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out, lse = ra.ra_paged_decode_prefix(*args)
+for _ in range(3):
+    g.replay()
+torch.cuda.synchronize()
+check_decode(out, lse, args[0], k, v, [1] * 21)
+ra.ra_device_status()
+print("captured first")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.slow
+def test_rows_past_32_bit_offsets():
+    """Outputs and states of more than 2^31 elements: the first and the last rows."""
+    n_req, H, ps, P = 66000, 256, 8, 100
+    assert n_req * H * 128 > 2**31
+    g = torch.Generator(device=DEV).manual_seed(1)
+    kv = torch.randn(2, n_req + 13, ps, 2, 128, generator=g, device=DEV).bfloat16()
+    q = torch.empty(n_req, H, 128, dtype=torch.bfloat16, device=DEV)
+    for part in q.split(6000):
+        part.copy_(torch.randn(part.shape, generator=g, device=DEV))
+    table = torch.arange(n_req, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    ptab = torch.arange(n_req, n_req + 13, dtype=torch.int32, device=DEV)[None].contiguous()
+    lens = torch.arange(n_req, dtype=torch.int32, device=DEV) % 8 + 1
+    out = torch.empty_like(q)
+    _, lse = ra.ra_paged_decode_prefix(q, kv[0], kv[1], ptab, i32([P]), i32([0, n_req]), table, lens, out=out)
+    ra.ra_device_status()
+    for i in (0, 1, n_req // 2, n_req - 2, n_req - 1):
+        k, v = (torch.cat((x[n_req:].reshape(-1, 2, 128)[:P], x[i, :int(lens[i])])) for x in kv)
+        check_decode(out[i:i + 1], lse[i:i + 1], q[i:i + 1], [k], [v], [1])
