@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
   }
 }
 
-// Joins the states of a row from two launches (kOwn, kShared), WPR warps a row; warp
-// w of them takes partials w, w + WPR, ..., own ones first.  Its lanes take a
+// Joins the states of a row over its own keys and over its prefix, WPR warps a row;
+// warp w of them takes partials w, w + WPR, ..., own ones first.  Its lanes take a
 // partial each for the maximum and the weights, so that all of them are requested
 // at once; then a lane sums D / 32 columns over the partials, in the order of the
 // CTAs.  A row mostly has one or two partials of each launch, and a warp is enough;
@@ -569,12 +569,31 @@ int paged_row_tile(const PagedArgs& a, int d) {
   return rows <= 8 ? 8 : (rows <= (d == 64 ? 32 : 16) ? 16 : 128);
 }
 
+// A group's rows on 16-row tiles beside the own rows, in one launch, or on 128-row
+// tiles in a launch of their own (paged_prefix_kernel.cu), which costs some 8 us more.
+// From there the tiles decide: 16 rows take 1.4 us per 64 keys and CTA, and an item as
+// much as 256 keys more; 128 rows 1.5 us per 128 keys, and 384.  Keys are those the
+// prefix table has room for.  One launch and two, us, 8 KV heads, d = 128, 4 rows a
+// request, own histories of up to 300 keys, groups x requests x keys of the prefix:
+//   1 x 8 x 1000   13.3/20.9    1 x 16 x 4000   22.0/24.4    1 x 256 x 64    56.7/44.3
+//   1 x 64 x 300   23.9/30.2    1 x 8 x 30000   46.2/42.3    1 x 128 x 900   47.9/40.2
+//   10 x 32 x 100  48.8/44.8    20 x 8 x 1000   51.1/49.8    1 x 16 x 16000  49.0/33.6
+// (With at most 16 rows one launch always: 300 x 2 x 300 98/111, 1 x 4 x 30000 33.5/39.4.)
+bool paged_prefix_both(const PagedArgs& group) {
+  const long long rows = group.n_q * (group.heads / group.kv_heads);
+  const double keys = static_cast<double>(group.max_pages) * (1 << group.page_shift);
+  const double heads = static_cast<double>(group.n_req) * group.kv_heads / sm_count();
+  const double one = heads / 2 * ((rows + 15) / 16) * (keys / 64 + 4) * 1.4;
+  const double two = 8 + heads * ((rows + 127) / 128) * (keys / 128 + 3) * 1.5;
+  return rows <= 16 || one <= two;
+}
+
 size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas); }
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  if (row_tile == 128)
-    return mode == kShared ? launch_paged_prefix(a, d, ctas, tk, tv, st) : launch_paged_tc(a, mode, d, ctas, tk, tv, st);
+  if (mode == kShared) return launch_paged_prefix(a, d, ctas, tk, tv, st);
+  if (row_tile == 128) return launch_paged_tc(a, mode, d, ctas, tk, tv, st);
   auto run = [&](auto m) {
     constexpr int MODE = decltype(m)::value;
     if (d == 128)
@@ -582,8 +601,8 @@ cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, i
     return row_tile == 8 ? decode_t<64, 1, MODE>(a, ctas, tk, tv, st) : decode_t<64, 2, MODE>(a, ctas, tk, tv, st);
   };
   return mode == kOwn ? run(std::integral_constant<int, kOwn>{})
-                      : (mode == kShared ? run(std::integral_constant<int, kShared>{})
-                                         : run(std::integral_constant<int, kPlain>{}));
+                      : (mode == kBoth ? run(std::integral_constant<int, kBoth>{})
+                                       : run(std::integral_constant<int, kPlain>{}));
 }
 
 cudaError_t launch_paged_join(const PagedArgs& own, const PagedArgs& shared, int d, int own_tile,

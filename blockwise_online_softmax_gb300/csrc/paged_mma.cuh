@@ -103,7 +103,7 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
     const int tiles = left < w.t.nt - w.k ? static_cast<int>(left) : w.t.nt - w.k;
     const long long after = u + tiles + (w.k + tiles == w.t.nt ? kExtra : 0);
     PageIds ids;  // first: the record and the query rows hide its latency
-    ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
+    ids.start<MODE>(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
     if (is_k) {
       const int s = it % C::ITEMS;
       if (it >= C::ITEMS) {
@@ -115,10 +115,11 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
       const int n = w.t.rr1 - w.t.rr0, base = w.t.t0 * BT;
       int* rec = reinterpret_cast<int*>(smem + C::OFF_ITEM + s * C::REC);
       int row = 0;
+      const int states = MODE == kBoth && w.q.group ? static_cast<int>(a.T) * a.heads : 0;  // behind those of own rows
       if (lane < RT) {  // rows past the item's get its last row's keys, and no output
         const int rr = w.t.rr0 + (lane < n ? lane : n - 1), j = token_of(rr, g);
         row = (w.q.row0 + j) * a.heads + w.kh * (C::HEADS * g) + (rr - j * g);
-        rec[8 + lane] = row;
+        rec[8 + lane] = row + states;
         rec[8 + RT + lane] = key_end<MODE>(w.q, j) - base;
       }
       if (MODE != kPlain || lane == 0) {
@@ -126,7 +127,7 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
         const int c0 = cta_of(item0, run), c1 = cta_of(item0 + w.t.nt - 1, run);
         const int me = static_cast<int>(blockIdx.x);
         if (MODE != kPlain && lane < n && me == c0)
-          a.parts[row] = part_record(c0 == c1 ? -1 : (2 * me + 1) * RT + lane, c1 - c0 + 1 + (MODE == kOwn ? joined.mark(w.r) : 0));
+          a.parts[row + states] = part_record(c0 == c1 ? -1 : (2 * me + 1) * RT + lane, c1 - c0 + 1 + (MODE == kOwn || MODE == kBoth ? joined.mark(w.r) : 0));
         if (lane == 0) {
           *reinterpret_cast<Item*>(rec) =
               Item{n, base, w.t.lo - base, w.t.hi - base, w.k, tiles, c0 == c1 ? -1 : 2 * me + (me == c0 ? 1 : 0), after >= run.last};

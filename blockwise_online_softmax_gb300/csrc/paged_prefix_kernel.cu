@@ -1,5 +1,6 @@
-// Shared prefixes for more than 16 rows of a group and KV head (include/ra.h,
-// ra_paged_decode_prefix; paged_walk.cuh, kShared): row tiles of 128 on tcgen05.
+// Shared prefixes of groups with more than 16 rows of a KV head, but for the smallest
+// works (include/ra.h, ra_paged_decode_prefix; paged_walk.cuh, kShared; the border,
+// paged_prefix_both): row tiles of 128 on tcgen05.
 // Every row sees the same keys, so a group's rows are one matrix Q and the launch
 // is S = Q K^T, P = exp(S - m), O = P V with no mask but at a prefix's end:
 // matrix products, bound by the tensor cores where the decode is bound by HBM.
@@ -236,7 +237,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           ++it;
         }
         PageIds ids;
-        ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
+        ids.start<kShared>(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
         for (int k = 0; k < tiles; ++k, ++i) {
           const int key0 = (w.t.t0 + w.k + k) * BT;
           const int page = ids.get(a, key0, rows, boxes, lane);

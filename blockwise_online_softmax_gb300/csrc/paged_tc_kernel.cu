@@ -224,7 +224,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           ++it;
         }
         PageIds ids;
-        ids.start(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
+        ids.start<MODE>(a, w.r, w.t.lo, w.t.hi, (w.t.t0 + w.k) * BT, lane);
         for (int k = 0; k < tiles; ++k, ++i) {
           const int key0 = (w.t.t0 + w.k + k) * BT;
           const int page = ids.get(a, key0, rows, boxes, lane);

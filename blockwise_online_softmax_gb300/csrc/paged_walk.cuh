@@ -44,15 +44,17 @@ struct Request {
   int row0;  // first row of q
   int n;     // new tokens
   int len;   // keys, the new tokens' included
+  bool group;  // kBoth: a group of requests
 };
 
 // What the rows of a kernel are: the new tokens of requests, which see the keys up
 // to themselves (kPlain: finished here; kOwn: partial states of them, for a
 // launch that joins them with others), or all the tokens of a group of requests,
-// which see every key of the group's prefix (kShared: partial states).
-constexpr int kPlain = kPagedPlain, kOwn = kPagedOwn, kShared = kPagedShared;
+// which see every key of the group's prefix (kShared: partial states), or the one
+// after the other in one launch (kBoth: the groups are its requests n_own and on).
+constexpr int kPlain = kPagedPlain, kOwn = kPagedOwn, kShared = kPagedShared, kBoth = kPagedBoth;
 
-// With a prefix three launches follow one another: kOwn, kShared, the join.  The
+// With kBoth two launches follow one another, else three: kOwn, kShared, the join.  The
 // first two do not need each other, so kOwn lets the next start only once what was
 // before it is done, and kShared does not wait before its work but after it: its
 // CTAs take the SMs as kOwn's leave them, and its end means the end of both.
@@ -71,7 +73,7 @@ __device__ __forceinline__ void end_wait() {
 }
 
 // Where the partial states of a row are: `first` and the count, -1 where the item
-// is whole; + kWithPrefix in the rows of kOwn whose request has a prefix.
+// is whole; + kWithPrefix in the own rows of requests that have a prefix.
 constexpr int kWithPrefix = 1 << 20;  // (more than CTAs)
 __device__ __forceinline__ int2 part_record(int first, int parts) { return make_int2(first, parts); }
 // The requests that are one of a group: groups follow one another.
@@ -89,7 +91,15 @@ struct Joined {
 template <int MODE>
 __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
   Request q;
-  if (MODE == kShared) {
+  q.group = MODE == kShared || (MODE == kBoth && r >= a.n_own);
+  const int* lengths = a.lengths;
+  int pages = a.max_pages;
+  if (q.group) {
+    if (MODE == kBoth) {
+      r -= a.n_own;
+      lengths = a.prefix_lengths;
+      pages = a.prefix_pages;
+    }
     // The rows of requests [b, e), whatever the arrays say inside q and out.
     const int T = static_cast<int>(a.T), x = a.cu_req[r], y = a.cu_req[r + 1];
     const int b = x < 0 ? 0 : (x > a.n_own ? a.n_own : x), e = y < b ? b : (y > a.n_own ? a.n_own : y);
@@ -105,7 +115,7 @@ __device__ __forceinline__ Request load_request(const PagedArgs& a, int r) {
     q.row0 = r * static_cast<int>(a.n_q);
     q.n = static_cast<int>(a.n_q);
   }
-  const int most = a.max_pages << a.page_shift, len = a.lengths[r];
+  const int most = pages << a.page_shift, len = lengths[r];
   q.len = len < 0 ? 0 : (len > most ? most : len);
   return q;
 }
@@ -123,7 +133,7 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 // Token j of the request sees keys [begin, end).
 template <int MODE>
 __device__ __forceinline__ int key_end(const Request& q, int j, bool clamp = true) {
-  if (MODE == kShared) return q.len;
+  if (MODE == kShared || (MODE == kBoth && q.group)) return q.len;
   const int e = q.len - q.n + j + 1;
   return clamp && e < 0 ? 0 : e;
 }
@@ -164,7 +174,7 @@ __device__ __forceinline__ long long request_units(const PagedArgs& a, int r, in
   const Request q = load_request<MODE>(a, r);
   const int n = row_tiles(q, g, RT);
   long long u = 0;
-  if (MODE == kShared) u = n ? static_cast<long long>(n) * (row_tile<BT, MODE>(a, q, g, RT, 0).nt + EXTRA) : 0;
+  if (q.group) u = n ? static_cast<long long>(n) * (row_tile<BT, MODE>(a, q, g, RT, 0).nt + EXTRA) : 0;
   else
     for (int rt = 0; rt < n; ++rt) u += row_tile<BT, MODE>(a, q, g, RT, rt).nt + EXTRA;
   return u * a.kv_heads;
@@ -301,8 +311,10 @@ struct PageIds {
   int ids, more;
 
   __device__ __forceinline__ int at(int p) const { return p >= begin && p < end ? table[p] : -1; }
+  template <int MODE>
   __device__ __forceinline__ void start(const PagedArgs& a, int r, int lo, int hi, int key0, int lane) {
-    table = a.block_table + static_cast<long long>(r) * a.max_pages;
+    table = MODE == kBoth && r >= a.n_own ? a.prefix_table + static_cast<long long>(r - a.n_own) * a.prefix_pages
+                                          : a.block_table + static_cast<long long>(r) * a.max_pages;
     end = hi > lo ? ((hi - 1) >> a.page_shift) + 1 : 0;
     begin = lo >> a.page_shift;
     first = key0 >> a.page_shift;

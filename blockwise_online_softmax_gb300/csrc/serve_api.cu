@@ -645,27 +645,43 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
   if ((rc = page_map(&tv, n_pages ? v_cache : q, n_pages ? n_pages : 1, page_size, v_page_stride, kv_heads, d)) != RA_OK) return rc;
   own.cu_req = cu_req;
   own.n_groups = n_groups;
-  // The shared launch: the groups are its requests.
-  ra::PagedArgs shared = own;
-  shared.n_own = n_req;
-  shared.n_req = n_groups;
-  shared.block_table = prefix_table;
-  shared.max_pages = prefix_max_pages;
-  shared.lengths = prefix_lengths;
-  const int own_tile = ra::paged_row_tile(own, d);
+  const long long rows = T * heads;
   ra::PagedArgs group = own;  // as if a group were a request
   group.n_q = n_groups ? (T + n_groups - 1) / n_groups : 1;
-  const int shared_tile = ra::paged_row_tile(group, d);
-  // Scratch of each launch: the states of its cut items and of all rows, and a
-  // record per row.
-  const long long rows = T * heads;
-  auto ctas_of = [](int tile) { return (tile == 128 ? 1 : 2) * ra::sm_count(); };
-  auto size_of = [&](ra::PagedArgs& a, int tile) {
-    a.whole = 2LL * ctas_of(tile) * tile;
-    const size_t bytes = static_cast<size_t>(a.whole + rows) * (d + 2) * sizeof(float) + rows * sizeof(int2);
+  group.n_req = n_groups;
+  group.max_pages = prefix_max_pages;
+  const int own_tile = ra::paged_row_tile(own, d), group_tile = ra::paged_row_tile(group, d);
+  const bool both = own_tile <= 16 && ra::paged_prefix_both(group) && 2 * rows <= kMaxInt &&
+                    static_cast<long long>(n_req) + n_groups <= kMaxInt;
+  // Launches: one of both, or the own and then the shared one, whose requests are
+  // the groups.
+  ra::PagedArgs shared = own;
+  int shared_tile = 128;
+  if (both) {
+    own.n_req = n_req + n_groups;
+    own.n_own = n_req;
+    own.prefix_table = prefix_table;
+    own.prefix_lengths = prefix_lengths;
+    own.prefix_pages = prefix_max_pages;
+    shared_tile = own_tile > group_tile ? own_tile : (group_tile < 16 ? group_tile : 16);
+  } else {
+    shared.n_own = n_req;
+    shared.n_req = n_groups;
+    shared.block_table = prefix_table;
+    shared.max_pages = prefix_max_pages;
+    shared.lengths = prefix_lengths;
+  }
+  const int tile = both ? shared_tile : own_tile;
+  // Scratch of a launch: the states of its cut items and of all rows (of both, own
+  // ones first), and as many records.
+  auto ctas_of = [](int t) { return (t == 128 ? 1 : 2) * ra::sm_count(); };
+  auto size_of = [&](ra::PagedArgs& a, int t, long long n) {
+    a.whole = 2LL * ctas_of(t) * t;
+    const size_t bytes = static_cast<size_t>(a.whole + n) * (d + 2) * sizeof(float) + n * sizeof(int2);
     return (bytes + 255) / 256 * 256;
   };
-  const size_t own_bytes = size_of(own, own_tile), shared_bytes = size_of(shared, shared_tile);
+  const long long own_rows = both ? 2 * rows : rows;
+  const size_t own_bytes = size_of(own, tile, own_rows), shared_bytes = both ? 0 : size_of(shared, shared_tile, rows);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* scratch = nullptr;
   cudaError_t e = scratch_alloc(reinterpret_cast<void**>(&scratch), own_bytes + shared_bytes, st);
@@ -673,27 +689,34 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
     cudaGetLastError();
     return fail(RA_ERR_ALLOC, "pool allocation of the partial states failed: %s", cudaGetErrorString(e));
   }
-  auto place = [&](ra::PagedArgs& a, char* at) {
+  auto place = [&](ra::PagedArgs& a, char* at, long long n) {
     a.po = reinterpret_cast<float*>(at);
-    a.pm = a.po + (a.whole + rows) * d;
-    a.pl = a.pm + (a.whole + rows);
-    a.parts = reinterpret_cast<int2*>(a.pl + (a.whole + rows));
+    a.pm = a.po + (a.whole + n) * d;
+    a.pl = a.pm + (a.whole + n);
+    a.parts = reinterpret_cast<int2*>(a.pl + (a.whole + n));
   };
-  place(own, scratch);
-  place(shared, scratch + own_bytes);
+  place(own, scratch, own_rows);
+  if (both) {
+    shared = own;
+    shared.whole += rows;
+    shared.parts += rows;
+  } else {
+    place(shared, scratch + own_bytes, rows);
+  }
   {
-    TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
-    e = ra::launch_paged_decode(own, ra::kPagedOwn, d, ctas_of(own_tile), own_tile, tk, tv, st);
+    TraceScope ts(both ? RA_KERNEL_PAGED_PREFIX : RA_KERNEL_PAGED_DECODE, st);
+    e = ra::launch_paged_decode(own, both ? ra::kPagedBoth : ra::kPagedOwn, d, ctas_of(tile), tile, tk, tv, st);
     ts.done(e == cudaSuccess);
   }
-  if (e == cudaSuccess && n_groups > 0) {
+  if (e == cudaSuccess && !both && n_groups > 0) {
     TraceScope ts(RA_KERNEL_PAGED_PREFIX, st);
     e = ra::launch_paged_decode(shared, ra::kPagedShared, d, ctas_of(shared_tile), shared_tile, tk, tv, st);
     ts.done(e == cudaSuccess);
   }
   if (e == cudaSuccess) {
+    own.n_req = n_req;
     TraceScope ts(RA_KERNEL_PAGED_COMBINE, st);
-    e = ra::launch_paged_join(own, shared, d, own_tile, shared_tile, st);
+    e = ra::launch_paged_join(own, shared, d, tile, shared_tile, st);
     ts.done(e == cudaSuccess);
   }
   const cudaError_t ef = cudaFreeAsync(scratch, st);

@@ -174,13 +174,19 @@ struct PagedArgs {
   int2* parts;        // [T * heads]
   const int* cu_req;  // [n_groups + 1] the requests of each group
   int n_groups;
-  int n_own;          // the shared launch, whose requests are the groups: requests
+  int n_own;          // where the groups are among the requests, or all of them: requests
+  // Where they follow the requests: n_req counts both, and of the groups
+  const int* prefix_table;    // [n_groups, prefix_pages]
+  const int* prefix_lengths;  // [n_groups]
+  int prefix_pages;
 };
 // What the rows of a decode launch are: see paged_walk.cuh.
-constexpr int kPagedPlain = 0, kPagedOwn = 1, kPagedShared = 2;
+constexpr int kPagedPlain = 0, kPagedOwn = 1, kPagedShared = 2, kPagedBoth = 3;
 // Query rows (of one request and KV head) that a CTA takes together: 8 or 16
 // (paged_kernel.cu, two CTAs per SM) or 128 (paged_tc_kernel.cu, one).
 int paged_row_tile(const PagedArgs& a, int d);
+// Whether the own rows and those of groups go in one launch; group: the groups as requests.
+bool paged_prefix_both(const PagedArgs& group);
 size_t paged_cut_bytes(int ctas);
 // tk, tv: maps over the pages, dims (d, kv_heads, page_size, n_pages), box
 // 64 x 1 x min(page_size, 64) x 1, 128-byte swizzle.

@@ -130,7 +130,8 @@ typedef enum {
   RA_KERNEL_PAGED_APPEND_FP8 = 20, /* kind 17 with k and v held in 8 bits */
   RA_KERNEL_PAGED_READ_FP8 = 21,  /* 8-bit pages as dense bf16 rows */
   RA_KERNEL_PAGED_DECODE_FP8 = 22, /* attention over 8-bit pages */
-  RA_KERNEL_PAGED_PREFIX = 23,    /* attention over prefixes that requests share */
+  RA_KERNEL_PAGED_PREFIX = 23,    /* attention over prefixes that requests share (small works: and over
+                                     their own keys, else kind 18) */
   RA_KERNEL_KINDS = 24
 } ra_kernel_kind;
 

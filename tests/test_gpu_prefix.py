@@ -22,17 +22,19 @@ DEV = torch.device("cuda:0")
 U = 2.0 ** -24
 
 
-def make(groups, rows, H, Hkv, d, ps, *, seed=0, scale=1.5, together=False, extra=0):
+def make(groups, rows, H, Hkv, d, ps, *, seed=0, scale=1.5, together=False, extra=0, room=False):
     """groups: (prefix length, own lengths of its requests) each; rows: new
     tokens of every request.  Pages of prefixes and requests are dealt from one
-    cache, with NaN where nobody's tokens are."""
+    cache, with NaN where nobody's tokens are.  room: a prefix table for 2^18 keys
+    and more, with which groups of more than 16 rows get a launch of their own."""
     plens = [p for p, _ in groups]
     own = [n for _, ls in groups for n in ls]
     q, kc, vc, table, _, ks, vs = make_decode(plens + own, rows, H, Hkv, d, ps, seed=seed, scale=scale,
                                               together=together, extra=extra)
     G = len(groups)
     cu_req = i32(np.concatenate([[0], np.cumsum([len(ls) for _, ls in groups])]))
-    args = (q, kc, vc, table[:G].contiguous(), i32(plens), cu_req, table[G:].contiguous(), i32(own))
+    ptab = torch.nn.functional.pad(table[:G], (0, 2**18 // ps + 1 if room else 0), value=2**30).contiguous()
+    args = (q, kc, vc, ptab, i32(plens), cu_req, table[G:].contiguous(), i32(own))
     of = [g for g, (_, ls) in enumerate(groups) for _ in ls]
     k = [torch.cat((ks[g], x)) for g, x in zip(of, ks[G:])]
     v = [torch.cat((vs[g], x)) for g, x in zip(of, vs[G:])]
@@ -60,12 +62,12 @@ CASES = [
 ]
 
 
-@pytest.mark.parametrize("together", [False, True])
+@pytest.mark.parametrize("together, room", [(False, False), (True, False), (False, True), (True, True)])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"{[(p, len(x)) for p, x in c[0][:3]]}-q{c[1]}-h{c[2]}/{c[3]}-d{c[4]}-p{c[5]}")
-def test_prefix(case, together):
+def test_prefix(case, together, room):
     groups, n_q, H, Hkv, d, ps = case
     rows = [n_q] * sum(len(x) for _, x in groups)
-    args, k, v = make(groups, rows, H, Hkv, d, ps, together=together)
+    args, k, v = make(groups, rows, H, Hkv, d, ps, together=together, room=room)
     out, lse = ra.ra_paged_decode_prefix(*args)
     ra.ra_device_status()
     check_decode(out, lse, args[0], k, v, rows)
@@ -83,11 +85,12 @@ def attend(q, k, v, n_own, n_new):
                             k_pos=np.arange(L))
 
 
+@pytest.mark.parametrize("room", [False, True])
 @pytest.mark.parametrize("rows", [[1, 0, 3, 1, 2], [0, 0, 2, 0, 0], [40, 1, 0, 7, 1]])
-def test_ragged_rows(rows):
+def test_ragged_rows(rows, room):
     """cu_q: idle requests, several rows, and rows behind the last left as they were."""
     groups = [(300, [50, 20]), (129, [77, 10, 41])]
-    args, k, v = make(groups, rows, 8, 2, 128, 16, extra=5)
+    args, k, v = make(groups, rows, 8, 2, 128, 16, extra=5, room=room)
     out = torch.full(args[0].shape, 9.0, device=DEV)
     lse = torch.full(args[0].shape[:2], 9.0, device=DEV)
     cu = i32(np.concatenate([[0], np.cumsum(rows)]))
@@ -163,23 +166,25 @@ def test_equals_the_paged_decode_over_whole_tables():
     assert float((lse - rlse).abs().max()) <= 2 * (2 * 128 * U * A + 500 * 2 * U + 8 * U * 12)
 
 
+@pytest.mark.parametrize("room", [False, True])
 @pytest.mark.parametrize("scale", [0.0, 40.0])
-def test_equal_and_large_scores(scale):
-    args, k, v = make([(700, [50, 3] * 20)], [1] * 40, 8, 2, 128, 16, scale=scale)
+def test_equal_and_large_scores(scale, room):
+    args, k, v = make([(700, [50, 3] * 20)], [1] * 40, 8, 2, 128, 16, scale=scale, room=room)
     out, lse = ra.ra_paged_decode_prefix(*args)
     ra.ra_device_status()
     check_decode(out, lse, args[0], k, v, [1] * 40)
 
 
+@pytest.mark.parametrize("room", [False, True])
 @pytest.mark.parametrize("n_q, per, H, Hkv, d", [(1, 2, 8, 2, 64), (1, 3, 8, 2, 128), (1, 40, 8, 2, 128), (2, 40, 8, 1, 64)])
-def test_weights_have_24_bits(n_q, per, H, Hkv, d):
+def test_weights_have_24_bits(n_q, per, H, Hkv, d, room):
     """As the paged decode's test of that name: an output is one weight of three
     live keys, here two in the prefix and one among the own, all others weightless:
     99 u there where parts meet, the join of the two launches two factors of 6.4 u
     and three roundings more: 115 u, 128 u is used."""
     P, n = 700, 40
     groups = [(P, [n] * per)]
-    args, ks, vs = make(groups, [n_q] * per, H, Hkv, d, 16, seed=d + per)
+    args, ks, vs = make(groups, [n_q] * per, H, Hkv, d, 16, seed=d + per, room=room)
     q, kc, vc, ptab, _, _, tab, _ = args
     r = np.random.default_rng(per)
     g = H // Hkv
@@ -221,20 +226,22 @@ def test_weights_have_24_bits(n_q, per, H, Hkv, d):
         assert (np.abs(np64(lse[rr]) - rl) <= 132 * U).all()
 
 
-def test_arrays_in_disorder_stay_inside():
+@pytest.mark.parametrize("n_q, room", [(2, False), (8, True)])
+def test_arrays_in_disorder_stay_inside(n_q, room):
     """Offsets that are no prefix sums, lengths and pages out of range: results
     are undefined, nothing outside out and lse is written, nothing hangs."""
-    args, k, v = make([(300, [50, 20]), (129, [77, 10, 41])], [2] * 5, 8, 2, 128, 16)
-    whole = torch.full((14, 8, 128), 3.0, device=DEV)
-    wl = torch.full((14, 8), 3.0, device=DEV)
+    args, k, v = make([(300, [50, 20]), (129, [77, 10, 41])], [n_q] * 5, 8, 2, 128, 16, room=room)
+    T = 5 * n_q
+    whole = torch.full((T + 4, 8, 128), 3.0, device=DEV)
+    wl = torch.full((T + 4, 8), 3.0, device=DEV)
     for cu_req in ([0, 5, 2], [-7, 3, 99], [4, 1, 0], [2**31 - 1, -2**31, 5]):
         for plens in ([300, 129], [-5, 10**9], [2**31 - 1, -2**31]):
-            for cu_q in (None, [0, 9, 3, 99, -4, 10], [5, 4, 3, 2, 1, 0], [-9, 2, 4, 6, 8, 2**31 - 1]):
+            for cu_q in (None, [0, 9, 3, 99, -4, T], [5, 4, 3, 2, 1, 0], [-9, 2, 4, 6, 8, 2**31 - 1]):
                 a = list(args)
                 a[5], a[4] = i32(cu_req), i32(plens)
-                ra.ra_paged_decode_prefix(*a, cu_q=None if cu_q is None else i32(cu_q), out=whole[2:12], lse=wl[2:12])
+                ra.ra_paged_decode_prefix(*a, cu_q=None if cu_q is None else i32(cu_q), out=whole[2:T + 2], lse=wl[2:T + 2])
     ra.ra_device_status()
-    assert (whole[:2] == 3).all() and (whole[12:] == 3).all() and (wl[:2] == 3).all() and (wl[12:] == 3).all()
+    assert (whole[:2] == 3).all() and (whole[T + 2:] == 3).all() and (wl[:2] == 3).all() and (wl[T + 2:] == 3).all()
     bad = args[3].clone()
     bad[0, ::2] = 2**30
     bad[1, 1::2] = -1
@@ -244,10 +251,11 @@ def test_arrays_in_disorder_stay_inside():
     ra.ra_device_status()
 
 
-def test_captured_and_replayed_as_lengths_grow():
+@pytest.mark.parametrize("n_q, room", [(1, False), (6, True)])
+def test_captured_and_replayed_as_lengths_grow(n_q, room):
     """Two graphs of one call on two streams share no workspace and bake no host value in."""
     groups = [(500, [60, 3, 20]), (1300, [90])]
-    args, k, v = make(groups, [1] * 4, 32, 8, 128, 16)
+    args, k, v = make(groups, [n_q] * 4, 32, 8, 128, 16, room=room)
     torch.cuda.synchronize()
     graphs, outs = [], []
     for _ in range(2):
@@ -267,12 +275,13 @@ def test_captured_and_replayed_as_lengths_grow():
                     g.replay()
         torch.cuda.synchronize()
 
-        def part(x, i):
+        def part(x, i, j):  # what row j of request i sees: the prefix, however few its own keys are
             P = groups[of[i]][0]
-            return torch.cat((x[i][:plens[of[i]]], x[i][P:P + own[i]]))
+            return torch.cat((x[i][:plens[of[i]]], x[i][P:P + max(0, own[i] - n_q + j + 1)]))
 
+        each = [(i, j) for i in range(4) for j in range(n_q)]
         for out, lse in outs:
-            check_decode(out, lse, args[0], [part(k, i) for i in range(4)], [part(v, i) for i in range(4)], [1] * 4)
+            check_decode(out, lse, args[0], [part(k, *e) for e in each], [part(v, *e) for e in each], [1] * 4 * n_q)
     ra.ra_device_status()
 
 
@@ -281,7 +290,7 @@ def test_two_eager_calls_at_once_and_other_kernels_between():
     launch of a call starts before the first has ended, and touches nothing that
     a call before it still uses."""
     cases = [make([(900, [40, 2, 64])], [1] * 3, 32, 8, 128, 16, seed=1)[0],
-             make([(2000, [700] * 5), (3, [9])], [16] * 6, 8, 2, 128, 16, seed=2)[0]]
+             make([(2000, [700] * 5), (3, [9])], [16] * 6, 8, 2, 128, 16, seed=2, room=True)[0]]
     want = [ra.ra_paged_decode_prefix(*c) for c in cases]
     plain = [ra.ra_paged_decode(c[0], c[1], c[2], c[6], c[7]) for c in cases]
     torch.cuda.synchronize()
@@ -298,10 +307,11 @@ def test_two_eager_calls_at_once_and_other_kernels_between():
         assert torch.equal(b[0], plain[i % 2][0]) and torch.equal(b[1], plain[i % 2][1])
 
 
-def test_a_chain_in_one_stream_uses_what_the_call_before_wrote():
+@pytest.mark.parametrize("room", [False, True])
+def test_a_chain_in_one_stream_uses_what_the_call_before_wrote(room):
     """Every step's keys are written by the kernel just before the call."""
     groups = [(300, [33] * 12)]
-    args, k, v = make(groups, [1] * 12, 8, 2, 128, 16, seed=5)
+    args, k, v = make(groups, [1] * 12, 8, 2, 128, 16, seed=5, room=room)
     q, kc, vc, ptab, plens, cu, tab, lens = args
     k0, v0 = kc.clone(), vc.clone()
     want = ra.ra_paged_decode_prefix(*args)
@@ -316,14 +326,16 @@ def test_a_chain_in_one_stream_uses_what_the_call_before_wrote():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-def test_tracing_counts_the_three_launches():
-    args, k, v = make([(300, [50, 20])], [1] * 2, 8, 2, 128, 16)
+@pytest.mark.parametrize("per, room, launches", [(2, True, [0, 1, 1]), (100, False, [0, 1, 1]), (100, True, [1, 1, 1])])
+def test_tracing_counts_the_launches(per, room, launches):
+    """Few rows or a short prefix: the own keys and the prefix in one launch."""
+    args, k, v = make([(300, [50, 20] * (per // 2))], [1] * per, 8, 2, 128, 16, room=room)
     ra.ra_trace_enable()
     ra.ra_trace_reset()
     try:
         out, lse = ra.ra_paged_decode_prefix(*args)
-        check_decode(out, lse, args[0], k, v, [1] * 2)
-        assert [ra.ra_trace_query(x)[0] for x in ("paged_decode", "paged_prefix", "paged_combine")] == [1, 1, 1]
+        check_decode(out, lse, args[0], k, v, [1] * per)
+        assert [ra.ra_trace_query(x)[0] for x in ("paged_decode", "paged_prefix", "paged_combine")] == launches
     finally:
         ra.ra_trace_enable(False)
 
@@ -431,11 +443,11 @@ def test_cache_without_pages():
     ra.ra_device_status()
 
 
-@pytest.mark.parametrize("per", [2, 40])
+@pytest.mark.parametrize("per, room", [(2, False), (40, False), (40, True)])
 @pytest.mark.parametrize("what", ["key", "value"])
-def test_nan_in_a_prefix_stays_with_its_group(per, what):
+def test_nan_in_a_prefix_stays_with_its_group(per, room, what):
     groups = [(300, [20] * per), (300, [20] * per)]
-    args, k, v = make(groups, [1] * 2 * per, 8, 2, 128, 16)
+    args, k, v = make(groups, [1] * 2 * per, 8, 2, 128, 16, room=room)
     want = ra.ra_paged_decode_prefix(*args)
     page = int(args[3][0, 200 // 16])
     (args[1] if what == "key" else args[2])[page, 200 % 16, 1, 5] = float("nan")
@@ -462,7 +474,7 @@ def test_outputs_left_out_on_another_stream():
 
 def test_two_threads_on_streams_of_their_own():
     cases = [make([(900, [40, 2, 64])], [1] * 3, 32, 8, 128, 16, seed=1)[0],
-             make([(2000, [70] * 25), (3, [9])], [2] * 26, 8, 2, 128, 16, seed=2)[0]]
+             make([(2000, [70] * 25), (3, [9])], [2] * 26, 8, 2, 128, 16, seed=2, room=True)[0]]
     want = [ra.ra_paged_decode_prefix(*c) for c in cases]
     torch.cuda.synchronize()
     bad = []
@@ -491,7 +503,7 @@ sys.path[:0] = [{root!r}, {tests!r}]
 import torch
 import blockwise_online_softmax_gb300 as ra
 from test_gpu_prefix import check_decode, make
-args, k, v = make([(700, [64, 3] * 10), (50, [4])], [1] * 21, 8, 2, 128, 16)
+args, k, v = make([(700, [64, 3] * 10), (50, [4])], [1] * 21, 8, 2, 128, 16, room=True)
 torch.cuda.synchronize()
 g = torch.cuda.CUDAGraph()
 with torch.cuda.graph(g):
