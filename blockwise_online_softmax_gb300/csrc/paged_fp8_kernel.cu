@@ -22,6 +22,16 @@
 //   in two fp16 terms (22 bits and the sign of the second) a weight is off by at
 //   most 2^-23 of itself, or 2^-39 of the largest, as good as the fp32 it comes
 //   from.  (bf16 pages need three terms of 8 bits.)
+// - A consumer warp takes 32 keys of a tile (16: 128 requests of up to 8K keys 156 against
+//   128 us, 1M keys 680 against 512), and O is scaled only under a new maximum.
+//
+// 32/8 heads, d = 128, one row: 128 requests of up to 8K keys 123 to 136 us with the
+// machine, 5.4 to 5.9 TB/s (0.79 to 0.87 of the copy rate; rows of 128 bytes some
+// distance apart); bound by HBM and the ends of items.  16 rows (1M and some keys, 4
+// new tokens): 512 us, 5.3 TB/s (0.78); bound by the latency of a tile's chain with two
+// warps a scheduler and no registers to overlap two tiles.  d = 64 with 9 rows (1.2M
+// keys, 4 heads): 154 us, 4.0 TB/s; bound by issue, some 1000 cycles a warp and tile.  16
+// requests of up to 2000 keys 13.5 us: two launches and their chains of loads.
 #include <atomic>
 #include <cmath>
 #include <cstdint>

@@ -398,9 +398,9 @@ __global__ void __launch_bounds__(32 * kJoin) paged_combine_kernel(const PagedAr
 // partial each for the maximum and the weights, so that all of them are requested
 // at once; then a lane sums D / 32 columns over the partials, in the order of the
 // CTAs.  A row mostly has one or two partials of each launch, and a warp is enough;
-// with few rows and a long prefix it has some 20, and eight warps share them (the
-// whole call, 8 requests of 4 rows of 8 KV heads, 4K keys 35.0 -> 24.0 us, 1K keys
-// 23.6 -> 21.4).
+// with few rows and a long prefix it has some 20, and eight warps share them (8
+// requests of 4 rows of 8 KV heads, a call in three launches: 4K keys 35.0 -> 24.0 us,
+// 1K keys 23.6 -> 21.4).
 constexpr int kRowWarps = 8;
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kRowWarps)
