@@ -543,3 +543,29 @@ def test_rows_past_32_bit_offsets():
     for i in (0, 1, n_req // 2, n_req - 2, n_req - 1):
         k, v = (torch.cat((x[n_req:].reshape(-1, 2, 128)[:P], x[i, :int(lens[i])])) for x in kv)
         check_decode(out[i:i + 1], lse[i:i + 1], q[i:i + 1], [k], [v], [1])
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "steps", "one"])
+@pytest.mark.parametrize("d, bf16", [(64, False), (64, True), (128, False), (128, True)])
+def test_scores_far_above_those_before(order, d, bf16):
+    """A row's first keys say nothing of the others: scores that climb by hundreds
+    inside a tile and from tile to tile, fall, or stand out once in every 32 keys."""
+    n, P = 24, 1500
+    args, k, v = make([(P, [5] * n)], [1] * n, 8, 2, d, 16, seed=3, room=True)
+    q, kc, ptab = args[0], args[1], args[3]
+    u = torch.randn(2, d, device=DEV)
+    u /= u.norm(dim=-1, keepdim=True)
+    q[:] = (u.repeat_interleave(4, 0)[None] * torch.linspace(0.5, 3, n, device=DEV)[:, None, None]).bfloat16()
+    at = torch.arange(P, device=DEV, dtype=torch.float32)
+    size = {"rising": at * 0.4, "falling": (P - at) * 0.4, "steps": torch.floor(at / 90) * 30,
+            "one": torch.where(at % 37 == 36, at * 0.3, -at * 0.1)}[order]
+    rows = (u[None] * size[:, None, None] + 0.2 * torch.randn(P, 2, d, device=DEV)).bfloat16()
+    for p in range(-(-P // 16)):
+        part = rows[16 * p:16 * p + 16]
+        kc[ptab[0, p], :len(part)] = part
+    for x in k:
+        x[:P] = rows
+    out = torch.empty(q.shape, dtype=torch.bfloat16 if bf16 else torch.float32, device=DEV)
+    _, lse = ra.ra_paged_decode_prefix(*args, out=out)
+    ra.ra_device_status()
+    check_decode(out, lse, q, k, v, [1] * n)
