@@ -332,13 +332,22 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       // -------------------------------------------------------------- T(k) = P(k) V(k) (warp 14)
       if (lane == 0) {
         constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
-        bool ok = true;
+        // A wait costs some 200 cycles even where nothing is left to wait for, so what
+        // tile k + 1 needs besides its weights is waited for while products of tile k
+        // are still queued.
+        constexpr bool EARLY = TERMS == 3;
+        bool ok = !EARLY || wait1(C::B_VF, 0, 0xc8);
         for (int k = 0; k < total && ok; ++k) {
-          // The columns of T(k) are free: P(k - 1) has been read, or T(k - 2).
-          const int before = D == 128 ? k - 1 : k - 2;
-          ok = wait1(C::B_VF + (k & 1), static_cast<uint32_t>(k >> 1), 0xc8) &&
-               (before < 0 || wait1((D == 128 ? C::B_T : C::B_TF) + (before & 3), by4(before), 0xc9)) &&
-               wait1(C::B_P + (k & 3), by4(k), 0xc7);
+          // The columns of T(k) are free: P(k - 1) has been read (d = 64: T(k - 2)).
+          if (EARLY) {
+            ok = wait1(C::B_P + (k & 3), by4(k), 0xc7);
+            if (D == 128 && ok && k > 0) ok = wait1(C::B_T + ((k - 1) & 3), by4(k - 1), 0xc9);
+          } else {
+            const int before = D == 128 ? k - 1 : k - 2;
+            ok = wait1(C::B_VF + (k & 1), static_cast<uint32_t>(k >> 1), 0xc8) &&
+                 (before < 0 || wait1((D == 128 ? C::B_T : C::B_TF) + (before & 3), by4(before), 0xc9)) &&
+                 wait1(C::B_P + (k & 3), by4(k), 0xc7);
+          }
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = sdesc_sw128(sb + C::OFF_V + static_cast<uint32_t>(k & 1) * C::TILE, CHB, 1024);
@@ -352,12 +361,18 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               mma_ss(tbuf, ld + (((kk >> 2) * CHB + (kk & 3) * 32) >> 4), vd + static_cast<uint64_t>((kk * 2048) >> 4),
                      idesc_pv, kk > 0 ? 1u : 0u);
           }
-#pragma unroll 1
-          for (int x = 1; x >= 0; --x)
 #pragma unroll
-            for (int kk = 0; kk < BT / 16; ++kk)
-              mma_ts(tbuf, pbuf + x * 8 + kk * 16, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
-                     TERMS == 3 || x == 0 || kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < BT / 16; ++kk)
+            mma_ts(tbuf, pbuf + 8 + kk * 16, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                   TERMS == 3 || kk > 0 ? 1u : 0u);
+          if (EARLY && k + 1 < total) {
+            ok = wait1(C::B_VF + ((k + 1) & 1), static_cast<uint32_t>((k + 1) >> 1), 0xc8);
+            if (D == 64 && ok && k > 0) ok = wait1(C::B_TF + ((k - 1) & 3), by4(k - 1), 0xc9);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int kk = 0; kk < BT / 16; ++kk)
+            mma_ts(tbuf, pbuf + kk * 16, vd + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, 1u);
           tc_commit(bar(C::B_VE + (k & 1)));
           tc_commit(bar(C::B_T + (k & 3)));
         }
