@@ -66,6 +66,15 @@ struct Item {
   int pad;
 };
 
+// True in one lane of the warp.  (The compiler knows that, and keeps what the lane's
+// products share in uniform registers: with `lane == 0` it moved the operands of
+// each there one by one, some 97 cycles a product whatever its width.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 template <int D, int TERMS>
 struct Cfg {
   static constexpr int NCH = D / 64;
@@ -181,7 +190,7 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   tc_fence_before();
   __syncthreads();  // also: the scratch of find_run has been read
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kAll, *tmem_slot, 0);
   const long long lim = a.wait_limit;
   const int total = static_cast<int>(run.last - run.first);  // tiles of this CTA
   Item* items = reinterpret_cast<Item*>(smem + C::OFF_ITEM);
@@ -301,7 +310,9 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {  // one lane issues at the pipe's rate, a predicated warp does not
+        const bool lead = elect_one();
+        const int leader = __ffs(__ballot_sync(kAll, lead)) - 1;
+        if (lead) {
           for (int t = 0; t < x.tiles && ok; ++t, ++k) {
             // The slot is free: T(k - 3) has been read, or P(k - 3).
             ok = wait1(C::B_KF + (k & 1), static_cast<uint32_t>(k >> 1), 0xc6) &&
@@ -320,17 +331,17 @@ paged_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           }
           if (ok) tc_commit(bar(C::B_QF));
         }
-        k = __shfl_sync(kAll, k, 0);
-        ok = __shfl_sync(kAll, ok ? 1 : 0, 0) != 0;
+        k = __shfl_sync(kAll, k, leader);
+        ok = __shfl_sync(kAll, ok ? 1 : 0, leader) != 0;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         volatile int no_abort = 0;
         tc_commit(bar(C::B_DRAIN));
         wait_bar(bar(C::B_DRAIN), 0, &no_abort, nullptr, 0, lim);
       }
     } else {
       // -------------------------------------------------------------- T(k) = P(k) V(k) (warp 14)
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t idesc_pv = idesc_bf16(RT, D, 1);
         // A wait costs some 200 cycles even where nothing is left to wait for, so what
         // tile k + 1 needs besides its weights is waited for while products of tile k
