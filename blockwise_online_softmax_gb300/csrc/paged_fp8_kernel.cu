@@ -22,13 +22,14 @@
 //   in two fp16 terms (22 bits and the sign of the second) a weight is off by at
 //   most 2^-23 of itself, or 2^-39 of the largest, as good as the fp32 it comes
 //   from.  (bf16 pages need three terms of 8 bits.)
-// - A consumer warp takes 32 keys of a tile (16: 128 requests of up to 8K keys 156 against
-//   128 us, 1M keys 680 against 512), and O is scaled only under a new maximum.
+// - A consumer warp takes 32 keys of a tile, and O is scaled only under a new maximum
+//   (with 16, scaled each time: 128 requests of up to 8K keys 156 against 128 us, 1M
+//   keys 680 against 512).
 //
 // 32/8 heads, d = 128, one row: 128 requests of up to 8K keys 123 to 136 us with the
 // machine, 5.4 to 5.9 TB/s (0.79 to 0.87 of the copy rate; rows of 128 bytes some
 // distance apart); bound by HBM and the ends of items.  16 rows (1M and some keys, 4
-// new tokens): 512 us, 5.3 TB/s (0.78); bound by the latency of a tile's chain with two
+// new tokens): 488 us, 5.5 TB/s (0.82); bound by the latency of a tile's chain with two
 // warps a scheduler and no registers to overlap two tiles.  d = 64 with 9 rows (1.2M
 // keys, 4 heads): 154 us, 4.0 TB/s; bound by issue, some 1000 cycles a warp and tile.  16
 // requests of up to 2000 keys 13.5 us: two launches and their chains of loads.
@@ -69,12 +70,18 @@ struct Cfg {
   static constexpr uint32_t STAGE = 2 * TILE;
   static constexpr uint32_t QT = HP * RT * D * 2;
   static constexpr uint32_t REC = 32 + 8 * RT;
-  static constexpr uint32_t REST = ITEMS * QT + kCons * 4 * D * 4 + 2 * kCons * RT * 4 + ITEMS * REC + 16;
+  // The messages of warps 2 and 3 at an item's end take the place of its query rows,
+  // which are in registers by then, where they fit (at d = 128 that is a third stage: 1M
+  // keys, 16 rows 512 -> 488 us, with both waits of a tile ahead of it).
+  static constexpr bool IN_Q = NT == 2;
+  static constexpr uint32_t BUF = (IN_Q ? 2 : kCons) * 4 * D * 4;
+  static_assert(!IN_Q || QT >= 2 * 4 * D * 4, "messages fit");
+  static constexpr uint32_t REST = ITEMS * QT + BUF + 2 * kCons * RT * 4 + ITEMS * REC + 16;
   static constexpr int NST = (115712 - REST - 2 * ITEMS * 8) / (STAGE + 2 * HP * BT + 24);  // what two CTAs per SM leave
   static constexpr uint32_t OFF_SCALE = NST * STAGE;  // of stage s: K's by head, then V's
   static constexpr uint32_t OFF_Q = OFF_SCALE + NST * 2 * HP * BT;
   static constexpr uint32_t OFF_BUF = OFF_Q + ITEMS * QT;
-  static constexpr uint32_t OFF_ML = OFF_BUF + kCons * 4 * D * 4;
+  static constexpr uint32_t OFF_ML = OFF_BUF + BUF;
   static constexpr uint32_t OFF_ITEM = OFF_ML + 2 * kCons * RT * 4;
   static constexpr uint32_t OFF_BAR = OFF_ITEM + ITEMS * REC;
   static constexpr uint32_t OFF_MISC = OFF_BAR + (3 * NST + 2 * ITEMS) * 8;
@@ -126,12 +133,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
   using C = Cfg<D, NT, KB, HP>;
   // AHEAD: the scores of a tile (and head) are multiplied while the softmax of the one
-  // before, a long chain of dependent steps, is under way, in one block of straight
-  // code.  600K keys, d = 128, 4 rows 229 -> 214 us, 128 requests of up to 8K keys 144 ->
+  // before, a long chain of dependent steps, is under way.  600K keys, d = 128, 4 rows 229 -> 214 us, 128 requests of up to 8K keys 144 ->
   // 134; 1.2M keys, d = 64, 9 rows 172 -> 157; 16 requests of up to 2000 keys 13.3 ->
   // 13.6.  (With the wait for V after the softmax most works are slower than without
-  // AHEAD, by up to 5%.)
-  // 16 rows at d = 128 have no registers left for it (1M keys 512 -> 640).
+  // AHEAD, by up to 5%.)  16 rows at d = 128 have few registers left for it: 64 requests
+  // of up to 4000 keys and 64 rows 192 -> 214, 1M keys 480 either way; with the query
+  // rows read from shared memory for each tile 220 and 463.
   constexpr bool AHEAD = D == 64 || NT == 1;
   constexpr int RT = C::RT, BT = C::BT, ROW = D * HP;  // bytes of a key's row
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -296,11 +303,10 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const bool edge = k0 < item.lo || k0 + 16 * KB > item.hi;
       const bool more = k + 1 < item.tiles;
       const int then = st + 1 == C::NST ? 0 : st + 1;
-      if constexpr (AHEAD)
-        ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim) &&
-             (!more || wait_bar(kfull(then), then ? par : par ^ 1u, abort_flag, &g_paged_fp8_status, 0xa2, lim));
-      else
-        ok = ok && wait_bar(kfull(st), par, abort_flag, &g_paged_fp8_status, 0xa2, lim);
+      // Both waits ahead of the tile's work, which is then one block of straight code.
+      ok = ok && (AHEAD || wait_bar(kfull(st), par, abort_flag, &g_paged_fp8_status, 0xa2, lim)) &&
+           wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim) &&
+           (!AHEAD || !more || wait_bar(kfull(then), then ? par : par ^ 1u, abort_flag, &g_paged_fp8_status, 0xa2, lim));
       ok = __all_sync(kAll, ok);
 #pragma unroll
       for (int s = 0; s < HP; ++s) {  // the item's heads in turn: their columns of the rows
@@ -429,10 +435,6 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             softmax();
           }
         }
-        if (!AHEAD && s == 0) {
-          ok = ok && wait_bar(vfull(st), par, abort_flag, &g_paged_fp8_status, 0xa3, lim);
-          ok = __all_sync(kAll, ok);
-        }
         if (some) {
           if (turned) {  // seldom after an item's first tiles
 #pragma unroll
@@ -512,6 +514,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         par ^= 1u;
       }
     }
+    float* buf2 = C::IN_Q ? reinterpret_cast<float*>(smem + C::OFF_Q + is * C::QT) : buf + 2 * (4 * D);
 #pragma unroll
     for (int s = 0; s < HP; ++s) {
       float o[NT][D / 16][4];
@@ -524,7 +527,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
       Item part = item;
       if (item.slot >= 0) part.slot = item.slot * HP + s;
-      if (!join_warps<D, NT, true, kPlain>(a, part, rec, s * g, m[s], l[s], o, ok, s_m, s_l, buf, warp, lane)) return;
+      if (!join_warps<D, NT, true, kPlain>(a, part, rec, s * g, m[s], l[s], o, ok, s_m, s_l, buf, buf2, warp, lane)) return;
     }
     if (item.last) return;
     __syncwarp();

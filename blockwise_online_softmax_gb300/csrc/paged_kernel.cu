@@ -294,7 +294,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         par ^= 1u;
       }
     }
-    if (!join_warps<D, NT, false, MODE>(a, item, rec, 0, m, l, o, ok, s_m, s_l, buf, warp, lane)) break;
+    if (!join_warps<D, NT, false, MODE>(a, item, rec, 0, m, l, o, ok, s_m, s_l, buf, buf + 2 * (4 * D), warp, lane)) break;
     if (item.last) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(iempty(is));

@@ -198,12 +198,13 @@ __device__ __forceinline__ void produce(const PagedArgs& a, const void* tm, bool
 // The states (m, l, o) of the consumer warps, each over its own keys of the item,
 // become one, and go to out and lse, or to partial states.  o[nt][x][c + 2 e] is
 // row 8 nt + 2 (lane % 4) + c, column 16 x + 8 e + lane / 4, or, with PAIRS, column
-// 16 x + 2 (lane / 4) + e.  head is added to the record's rows.  False: the CTA gives
-// up.
+// 16 x + 2 (lane / 4) + e.  head is added to the record's rows.  buf and buf2 hold two
+// warps' messages each, 4 D floats.  False: the CTA gives up.
 template <int D, int NT, bool PAIRS, int MODE>
 __device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item, const int* rec, int head, const float (&m)[NT][2],
                                            float (&l)[NT][2], float (&o)[NT][D / 16][4], bool ok, float* s_m, float* s_l,
-                                           float* buf, int warp, int lane) {
+                                           float* buf, float* buf2, int warp, int lane) {
+  auto message = [&](int w) { return (w & 2 ? buf2 : buf) + (w & 1) * (4 * D); };
   constexpr int RT = 8 * NT;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -245,8 +246,8 @@ __device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item,
     // w ^ 2 quarters: warp w ends with columns [D / 4 * (2 (w & 1) + w / 2)
     // ..) of the sum.  A warp's second message goes where it read its first.
     const bool odd = warp & 1, high = warp & 2;
-    float* from = buf + warp * (4 * D);
-    float* to = buf + (warp ^ 1) * (4 * D);
+    float* from = message(warp);
+    float* to = message(warp ^ 1);
     if (nt > 0) named_bar_sync(1, 32 * kCons);  // the messages of group nt - 1 are read
     float h[H][4];
 #pragma unroll
@@ -281,7 +282,7 @@ __device__ __forceinline__ bool join_warps(const PagedArgs& a, const Item& item,
       *reinterpret_cast<float4*>(from + (x * 32 + lane) * 4) = make_float4(y[0], y[1], y[2], y[3]);
     }
     named_bar_sync(1, 32 * kCons);
-    const float* last = buf + (warp ^ 2) * (4 * D);
+    const float* last = message(warp ^ 2);
 #pragma unroll
     for (int x = 0; x < Q; ++x) {
       const float4 z = *reinterpret_cast<const float4*>(last + (x * 32 + lane) * 4);

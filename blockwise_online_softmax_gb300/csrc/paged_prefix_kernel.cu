@@ -18,13 +18,18 @@
 //   want of columns.  With bf16 output there is none: two terms, rounded, leave
 //   2^-17 of a weight at most, half a step of the output is 2^-8.
 // - K and V slots of their own, two each, freed by the product that reads them.
-// 2048 rows of each of 8 KV heads, 16K keys, us (the launch): d = 128 bf16 output 146
-// (941 TFLOP/s), fp32 192; d = 64 131 and 186.  What bounds it are the products: 24
-// or 32 of 128 x 128 x 16 a tile (28 and 20 at d = 64, half as wide) at 100 to 110
-// cycles each, where one after the other alone they take 65 (from shared memory) to
-// 77 (P from TMEM, at any width): they wait for the softmax's and the sum's traffic
-// in TMEM.  Tried on top and no faster: scores and T requested ahead of use (146 to
-// 155 and 192 to 198), P V by halves of the keys as their weights come (165, 217).
+// - One lane issues the products, the one that elect.sync names (elect_one), and what
+//   the next tile's P V needs is waited for under this one's.
+// 2048 rows of each of 8 KV heads, 16K keys, us (the launch): d = 128 bf16 output 145
+// (948 TFLOP/s), fp32 179; d = 64 115 and 150.  What bounds it: at d = 128 the products,
+// 24 or 32 of 128 x 128 x 16 a tile at 77 to 65 cycles each (the tensor pipe is 64 and
+// 69% busy), and the chain from one to the next, for there are four slots; at d = 64
+// the softmax, some 2400 of a tile's 2570 cycles of a scheduler with three terms (the
+// tensor pipe 49%).  Tried on top and no faster: scores and T requested ahead of use
+// (146 to 155 and 192 to 198), P V by halves of the keys as their weights come (165,
+// 217), a reference that is raised only for scores far above it, so one pass over S
+// and no maximum to hand on (the call 227 -> 242 us for fp32 at d = 128, 191 for bf16
+// either way).
 //
 // Roles of the 16 warps: 0-3 and 4-7 softmax, a thread has a row, the two groups
 // take a CTA's tiles in turn and hand the running maximum on; 8-11 the output sum;
