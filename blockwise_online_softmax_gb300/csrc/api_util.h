@@ -35,9 +35,14 @@ struct TraceScope {
 // returned with cudaFreeAsync like any other.
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t st);
 
-// Looks cuTensorMapEncodeTiled up once; g_encode is set when it is RA_OK.
+// Looks cuTensorMapEncodeTiled up once; encode_tiled may be called when it is RA_OK.
 int get_encoder();
-extern PFN_cuTensorMapEncodeTiled_v12000 g_encode;
+// cuTensorMapEncodeTiled, which wants a current context.  A thread that has made no
+// call of the runtime with work for the device yet has none: there it is made current.
+CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* estr,
+                      CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                      CUtensorMapFloatOOBfill fill);
 
 int check_common(int d, int heads, int dtype);
 int check_heads(int heads, int kv_heads);

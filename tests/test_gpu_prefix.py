@@ -480,13 +480,16 @@ def test_two_threads_on_streams_of_their_own():
     bad = []
 
     def work(i):
-        st = torch.cuda.Stream()
-        with torch.cuda.stream(st):
-            for _ in range(30):
-                out, lse = ra.ra_paged_decode_prefix(*cases[i])
-                st.synchronize()
-                if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
-                    bad.append(i)
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(30):
+                    out, lse = ra.ra_paged_decode_prefix(*cases[i])
+                    st.synchronize()
+                    if not (torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])):
+                        bad.append(i)
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
 
     ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
     for t in ts:
