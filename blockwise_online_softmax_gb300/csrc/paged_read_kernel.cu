@@ -139,7 +139,10 @@ cudaError_t launch_paged_read(const ReadArgs& args, int d, cudaStream_t st) {
   a.wide = ((reinterpret_cast<uintptr_t>(a.ko) | reinterpret_cast<uintptr_t>(a.vo)) & 31) == 0;
   const long long most = 8LL * sm_count() * kWarps;  // two turns of what is resident: 7.1 us against 7.7 for 6000 rows
   const long long per = (a.tokens + most - 1) / most;
-  a.per_warp = static_cast<int>(per < 1 ? 1 : (per > 8 ? 8 : per));
+  // At most 512 chunks of each side, or a row for each lane: with 8 rows of one head, d =
+  // 64, a lane had one load a side (970K tokens 67 -> 46 us; four heads 334 -> 327).
+  const int chunks = a.kv_heads * (d / CH), cap = chunks >= 64 ? 8 : (chunks > 16 ? 512 / chunks : 32);
+  a.per_warp = static_cast<int>(per < 1 ? 1 : (per > cap ? cap : per));
   const long long need = (a.tokens + static_cast<long long>(a.per_warp) * kWarps - 1) / (a.per_warp * kWarps);
   const unsigned grid = static_cast<unsigned>(need < most / kWarps ? need : most / kWarps);
   return launch_early(d == 128 ? paged_read_kernel<128> : paged_read_kernel<64>, dim3(grid), kWarps * 32, 0, st, a);

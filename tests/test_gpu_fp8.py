@@ -353,3 +353,24 @@ def test_read_of_more_requests_than_threads_captured():
                 h = x[table[i].cpu().numpy()].reshape(-1, hkv, d)[length[i] - rows[i]:length[i]]
                 np.testing.assert_array_equal(got[offs[i]:offs[i + 1]], h)
             assert (got[offs[-1]:] == 5.0).all()
+
+
+@pytest.mark.parametrize("hkv, d", [(1, 64), (3, 64), (3, 128), (9, 64)])
+def test_read_of_long_histories(hkv, d):
+    """So many tokens that a warp takes as many rows together as it can."""
+    ps, n_pages = 32, 3000
+    kc, vc, ks, vs, kx, vx = random_pages(n_pages, ps, hkv, d, hkv)
+    rng = np.random.default_rng(d)
+    lens = np.array([250000, 1, 0, 99999, 7, 180001])
+    table = rng.integers(0, n_pages, (6, 8000)).astype(np.int32)
+    rows = lens - np.array([33, 0, 0, 5, 7, 0])
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    dev = [torch.from_numpy(x.astype(np.int32)).to(DEV) for x in (table, lens, cu)]
+    got = ra.ra_paged_read_fp8(kc, vc, ks, vs, *dev, tokens=int(cu[-1]))
+    ra.ra_device_status()
+    for out, x in zip(got, (kx, vx)):
+        pages = torch.from_numpy(x).to(DEV).to(torch.bfloat16)  # exact
+        for i in range(6):
+            t = torch.arange(int(lens[i] - rows[i]), int(lens[i]), device=DEV)
+            want = pages[dev[0][i].long()[t // ps], t % ps]
+            assert torch.equal(out[int(cu[i]):int(cu[i + 1])], want)
