@@ -401,7 +401,7 @@ constexpr int kRowWarps = 8;
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kRowWarps)
 paged_join_kernel(const PagedArgs own, const PagedArgs shared, int own_tile, int shared_tile) {
-  constexpr int CPL = D / 32, kEarly = WPR == 1 ? 2 : 4, kRows = kRowWarps / WPR;
+  constexpr int CPL = D / 32, kEarly = WPR == 1 ? 2 : 4, kRows = kRowWarps / WPR, kFew = WPR == 1 ? 2 : 0;
   __shared__ float s_m[kRowWarps], s_l[kRowWarps], s_o[WPR > 1 ? kRowWarps : 1][D];
   let_next_start();
   wait_for_previous();
@@ -452,7 +452,34 @@ paged_join_kernel(const PagedArgs own, const PagedArgs shared, int own_tile, int
     const int n = a.n + b.n;
     auto state = [&](int p) { return p < a.n ? own.po + a.index(p) * D : shared.po + b.index(p - a.n) * D; };
     float m = -INFINITY, l = 0.f, acc[CPL] = {};
-    for (int p0 = w0; p0 < n; p0 += 32 * WPR) {
+    // Two, as mostly, are weighed by every lane, without an exchange (81K rows, d = 64: the
+    // call 122 -> 114 us; four 1.02 times slower where items are cut often).
+    if (n <= kFew) {
+      Columns x[kFew + 1];
+      float xm[kFew + 1], xl[kFew + 1];
+#pragma unroll
+      for (int p = 0; p < kFew; ++p) {
+        xm[p] = -INFINITY;
+        xl[p] = 0.f;
+        if (p < n) {
+          const long long at = p < a.n ? a.index(p) : b.index(p - a.n);
+          xm[p] = (p < a.n ? own.pm : shared.pm)[at];
+          xl[p] = (p < a.n ? own.pl : shared.pl)[at];
+          x[p].load((p < a.n ? own.po : shared.po) + at * D + CPL * lane);
+        }
+        m = fmaxf(m, xm[p]);
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int p = 0; p < kFew; ++p) {
+        if (p >= n) break;
+        const float w = ex2(xm[p] - ref);
+        l = fmaf(xl[p], w, l);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) acc[i] = fmaf(x[p].v[i], w, acc[i]);
+      }
+    }
+    for (int p0 = n <= kFew ? n : w0; p0 < n; p0 += 32 * WPR) {
       const int p = p0 + lane * WPR;
       const bool mine = p < n;
       const float* pm = p < a.n ? own.pm + a.index(p) : shared.pm + b.index(p - a.n);
