@@ -581,6 +581,8 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *   no window: the keys that a window leaves of a prefix differ from row to row.
  *   Scratch: the states of all rows twice, T * heads * (8 d + 32) bytes, from the
  *   pool.
+ *   prefix_max_pages says how long a prefix may be and so picks the kernels (any
+ *   width is computed right): short prefixes want a narrow table.
  */
 int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cache, void* out,
                            float* lse, long long T, int n_groups, const int* cu_req,
