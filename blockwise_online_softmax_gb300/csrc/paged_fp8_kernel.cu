@@ -16,12 +16,15 @@
 // - q is turned to fp16 once an item, with a power of two per row that brings its
 //   largest entry to [2^14, 2^15): its 8 bits are exact down to 2^-28 of that entry,
 //   and below it is off by at most 2^-39 of it.
-// - The weight of a value is p_t 2^b_t.  fp16 has no room for all of them, so a
-//   warp scales its weights of a tile by a power of two, the largest to [2^14,
+// - The weight of a value is p_t 2^b_t.  fp16 has no room for all of them, so a row
+//   scales its weights of a warp's 32 keys by a power of two, the largest to [2^14,
 //   2^15), and gives it back in fp32 when the tile's product is added to O.  Held
 //   in two fp16 terms (22 bits and the sign of the second) a weight is off by at
-//   most 2^-23 of itself, or 2^-39 of the largest, as good as the fp32 it comes
-//   from.  (bf16 pages need three terms of 8 bits.)
+//   most 2^-23 of itself, or 2^-39 of the row's largest there.  Rows have powers of
+//   their own: what one weighs, another may not see.  (One power for the warp, found by
+//   one instruction, took 487 for 504 us at 1M keys and 155 for 166 at 1.2M, d = 64, 9
+//   rows, and lost a row's weights beside another's of a far larger scale.  bf16 pages
+//   need three terms of 8 bits.)
 // - A consumer warp takes 32 keys of a tile, and O is scaled only under a new maximum
 //   (with 16, scaled each time: 128 requests of up to 8K keys 156 against 128 us, 1M
 //   keys 680 against 512).
@@ -121,11 +124,6 @@ __device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
-}
-__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
-  uint32_t y;
-  asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(y) : "r"(x));
-  return y;
 }
 
 template <int D, int NT, int KB, int HP>
@@ -312,7 +310,8 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       for (int s = 0; s < HP; ++s) {  // the item's heads in turn: their columns of the rows
         uint64_t sc[KB][NT][2];  // of the lane's two rows, keys lane / 4 and lane / 4 + 8 of a block
         uint32_t pb[KB][NT][2][2];
-        float al[NT][2], back = 0.f;
+        float al[NT][2];
+        uint64_t back2[NT];
         bool turned = false;  // some row's maximum is a new one
         if (some) {
           if (!AHEAD) products(st, s);
@@ -394,30 +393,36 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               for (int c = 0; c < 2; ++c) l[s][nt][c] = fmaf(l[s][nt][c], al[nt][c], sum[c]);
             }
             turned = __any_sync(kAll, turned);
-            // The weights in two fp16 terms, by a power of two that brings the warp's
-            // largest to [2^14, 2^15).
-            float most = 0.f;
+            // The weights in two fp16 terms, by a power of two per row that brings its
+            // largest to [2^14, 2^15).  Its exponent is in the high half of an fp32 word,
+            // so the lane's two rows go through the exchanges as one.  (Weights are not
+            // negative; a NaN is passed by.)
+            uint64_t f2[NT];
 #pragma unroll
-            for (int b = 0; b < KB; ++b)
+            for (int nt = 0; nt < NT; ++nt) {
+              float most[2] = {0.f, 0.f};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int b = 0; b < KB; ++b) {
+                float w[2][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float w0, w1;
-                  f2unpack(sc[b][nt][h], w0, w1);
-                  most = fmax3(most, w0, w1);
-                }
-            const uint32_t top = warp_max(__float_as_uint(most)) >> 23;  // its exponent (weights are not negative)
-            const uint32_t lift = top < 15 ? 15 : (top > 254 ? 254 : top);
-            const float f = __uint_as_float((268 - lift) << 23);  // 2^(14 - (lift - 127))
-            back = __uint_as_float(lift > 14 ? (lift - 14) << 23 : 0u);
+                for (int h = 0; h < 2; ++h) f2unpack(sc[b][nt][h], w[h][0], w[h][1]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) most[c] = fmax3(most[c], w[0][c], w[1][c]);
+              }
+              uint32_t top = __byte_perm(__float_as_uint(most[0]), __float_as_uint(most[1]), 0x7632);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kAll, top, o));
+              const uint32_t e0 = max(top >> 7 & 0x1ffu, 15u), e1 = max(top >> 23, 15u);
+              f2[nt] = f2pack(__uint_as_float((268 - e0) << 23), __uint_as_float((268 - e1) << 23));  // 2^(14 - (e - 127))
+              back2[nt] = f2pack(__uint_as_float((e0 - 14) << 23), __uint_as_float((e1 - 14) << 23));
+            }
 #pragma unroll
             for (int b = 0; b < KB; ++b)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  const uint64_t w = fmul2(sc[b][nt][h], f2pack(f, f));
+                  const uint64_t w = fmul2(sc[b][nt][h], f2[nt]);
                   float x, y;
                   f2unpack(w, x, y);
                   const uint32_t hi = f16x2_rn(x, y);
@@ -447,7 +452,6 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               }
             }
           }
-          const uint64_t back2 = f2pack(back, back);
           uint32_t keep[KB][2];  // V rows outside [lo, hi) may hold anything
 #pragma unroll
           for (int b = 0; b < KB; ++b)
@@ -503,7 +507,7 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  o2[s][nt][c0 + x][e] = ffma2(f2pack(t[x][nt][2 * e], t[x][nt][2 * e + 1]), back2, o2[s][nt][c0 + x][e]);
+                  o2[s][nt][c0 + x][e] = ffma2(f2pack(t[x][nt][2 * e], t[x][nt][2 * e + 1]), back2[nt], o2[s][nt][c0 + x][e]);
           }
         }
       }

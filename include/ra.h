@@ -621,10 +621,13 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
  *   cu_k: device int32 [n_req + 1], nondecreasing.
  *
  * ra_paged_decode_fp8 -- ra_paged_decode over pages in 8 bits, with q, out and
- * everything else as there (bf16 q; lengths include the new tokens).  Scores
- * and weights have fp32's precision: the result differs from that of
- * ra_paged_decode over the same values in bf16 by fp32 roundings (keys above 2^105
- * may overflow them).  Query rows
+ * everything else as there (bf16 q; lengths include the new tokens).  Scores and
+ * sums are fp32, and the result differs from that of ra_paged_decode over the
+ * same values in bf16 by fp32 roundings (keys above 2^105 may overflow the scores)
+ * and by what is held in fp16 terms on the way: an entry of q to 2^-39 of its
+ * row's largest, or exactly, and a value's weight times its scale to 2^-23 of
+ * itself or to 2^-39 of the largest that the same row has among 32 keys, whichever
+ * is more.  What one row weighs does not change another.  Query rows
  * of a request and KV head are taken 16 at a time, and each 16 read its pages
  * again: for a few new tokens (for the chunks of a prompt, ra_paged_read_fp8 and
  * ra_decode_forward).
