@@ -647,7 +647,8 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
   own.n_groups = n_groups;
   const long long rows = T * heads;
   ra::PagedArgs group = own;  // as if a group were a request
-  group.n_q = n_groups ? (T + n_groups - 1) / n_groups : 1;
+  const long long expected = own.n_q * n_req < T ? own.n_q * n_req : T;  // rows; without a word of the caller's T
+  group.n_q = n_groups ? (expected + n_groups - 1) / n_groups : 1;
   group.n_req = n_groups;
   group.max_pages = prefix_max_pages;
   const int own_tile = ra::paged_row_tile(own, d), group_tile = ra::paged_row_tile(group, d);

@@ -581,8 +581,10 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *   no window: the keys that a window leaves of a prefix differ from row to row.
  *   Scratch: the states of all rows twice, T * heads * (8 d + 32) bytes, from the
  *   pool.
- *   prefix_max_pages says how long a prefix may be and so picks the kernels (any
- *   width is computed right): short prefixes want a narrow table.
+ *   prefix_max_pages says how long a prefix may be, and n_q how many rows a group
+ *   should be expected to have (its share of n_req * n_q, or of T); they pick the
+ *   kernels, and any are computed right: short prefixes want a narrow table, steps
+ *   with padding rows n_q.
  */
 int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cache, void* out,
                            float* lse, long long T, int n_groups, const int* cu_req,
