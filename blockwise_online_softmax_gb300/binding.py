@@ -660,10 +660,11 @@ def ra_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, lengths, 
     """Pages in 8 bits read back: (k_out, v_out), bf16 [tokens, kv_heads, d],
     with the newest cu_k[i + 1] - cu_k[i] tokens of request i in rows
     [cu_k[i], cu_k[i + 1]) (cu_k int32 [n_req + 1]; the prefix sums of lengths
-    give whole histories).  Exact.  Rows that belong to no request are left as
-    they were (in outputs that are not passed in: undefined), rows before a
-    request's first token are zero.  The rows are what ra_decode_forward and
-    the ring calls take, for instance for the next chunk of a long prompt."""
+    give whole histories).  Exact; an entry that was 1.9375 * 2^127 or more is
+    an infinity.  Rows that belong to no request are left as they were (in
+    outputs that are not passed in: undefined), rows before a request's first
+    token are zero.  The rows are what ra_decode_forward and the ring calls
+    take, for instance for the next chunk of a long prompt."""
     return (_serve or _fast()).paged_read_fp8(
         k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_k, tokens, k_out, v_out,
         stream)

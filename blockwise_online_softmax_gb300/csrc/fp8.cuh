@@ -9,9 +9,11 @@
 // read back is a bf16 value, and every implementation gets the same codes.
 // (With scales max |x| / 448, bf16 rows divide to within an ulp of the middle
 // between two codes in one of some 400 entries, where the division's rounding
-// would decide.)  The scale is one byte (e8m0) of some 130.  The range of e
-// keeps every value that a code and a scale stand for a normal fp32 (and bf16)
-// number.  Entries that are not finite become NaN and do not count in max |x|.
+// would decide.)  The scale is one byte (e8m0) of 238.  The range of e keeps every
+// value that a code and a scale stand for a normal fp32 (and bf16) number, but for
+// the codes from 256 on with e = 120: entries from 248 2^120 = 1.9375 2^127 on, of a
+// largest fp32 below 256 2^120, round to 2^128 and are read as infinities.  Entries
+// that are not finite become NaN and do not count in max |x|.
 #pragma once
 #include <cstdint>
 

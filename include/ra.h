@@ -601,12 +601,14 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
  * token and KV head: k_scale, v_scale [n_pages, kv_heads, page_size], one byte
  * each (e8m0: byte b stands for 2^(b - 127)), dense inside a page, pages
  * k_scale_stride / v_scale_stride bytes apart (a multiple of 16).  An entry is
- * code * scale, which bf16 holds exactly.  A row x of d entries is held with
+ * code * scale, which bf16 holds exactly where it is below 2^128 (the codes 256
+ * and above with e = 120 are not, and stand for an infinity: entries of 248 * 2^120,
+ * 1.9375 * 2^127, and more become that).  A row x of d entries is held with
  *   e = the least integer in [-117, 120] with max |x| <= 448 * 2^e
  * (over its finite entries; e = -117 for a row of zeros), the scale 2^e and the
  * codes x / 2^e, to nearest, halves to even; an entry that is not finite becomes
- * NaN.  So a page takes 0.504 (d = 128) or 0.508 of its bytes in bf16, and an
- * entry is off by at most 2^-4 of itself or 2^-10 scales.  page_size: 16, 32, 64,
+ * NaN.  So a page takes 0.504 (d = 128) or 0.508 of its bytes in bf16, and any
+ * other entry is off by at most 2^-4 of itself or 2^-10 scales.  page_size: 16, 32, 64,
  * 128 or 256.  Scales other than those of a row so held (bytes 10 to 247) give
  * undefined results.
  *
