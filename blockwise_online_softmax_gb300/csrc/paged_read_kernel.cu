@@ -41,6 +41,19 @@ __device__ __forceinline__ int request_of(const int* cu, int n_req, long long t,
   return lo;
 }
 
+// The same for one lane, from a request lo with cu[lo] <= t on: mostly lo itself, else
+// by steps that double and then halve.  (Where few of many requests have rows, one by
+// one were as many loads in turn as there are idle requests: two of 5000, 30K tokens
+// each, 365 us against 58.)
+__device__ __forceinline__ int request_from(const int* cu, int n_req, int lo, long long t) {
+  auto below = [&](unsigned step) { return step < static_cast<unsigned>(n_req - lo) && cu[lo + step] <= t; };
+  unsigned step = 1;
+  for (; below(step); step *= 2) lo += static_cast<int>(step);
+  for (step /= 2; step > 0; step /= 2)
+    if (below(step)) lo += static_cast<int>(step);
+  return lo;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 4) paged_read_kernel(const ReadArgs a) {
   let_next_start();
@@ -55,12 +68,12 @@ __global__ void __launch_bounds__(kWarps * 32, 4) paged_read_kernel(const ReadAr
   for (long long t0 = first + (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.per_warp; t0 < end;
        t0 += warps * a.per_warp) {
     const int rows = static_cast<int>(end - t0 < a.per_warp ? end - t0 : a.per_warp);
-    int req = request_of(a.cu, a.n_req, t0, lane);
+    const int req0 = request_of(a.cu, a.n_req, t0, lane);
     // Row t0 + lane: its page (-1: none, zeros) and its row there.
     int page = -1, in = 0;
     if (lane < rows) {
       const long long t = t0 + lane;
-      while (req + 1 < a.n_req && a.cu[req + 1] <= t) ++req;
+      const int req = request_from(a.cu, a.n_req, req0, t);
       const long long most = static_cast<long long>(a.max_pages) << a.page_shift;
       long long len = a.lengths[req];
       if (len > most) len = most;
