@@ -1,9 +1,12 @@
 // Launches of the serving kernels with programmatic dependence: a kernel may be
 // put on the SMs while the one in front of it in the stream still drains, and
-// waits for its end (wait_for_previous) before it touches global memory (but for
-// the decode kernels' status word, which only says that nothing more need be
-// done).  Each of these kernels is a few microseconds, of which a full launch
-// behind another kernel is one or two.
+// waits for its end (wait_for_previous) before it touches global memory.  Two
+// exceptions: the decode kernels' status word, which only says that nothing more
+// need be done, and the launch over shared prefixes (kShared in paged_walk.cuh).
+// That one directly follows the launch over the own keys (kOwn), which lets it start
+// only after a wait, works beside it and waits for its end at its own.  Each of these
+// kernels is a few microseconds, of which a full launch behind another kernel is
+// one or two.
 #pragma once
 #include <cuda_runtime.h>
 

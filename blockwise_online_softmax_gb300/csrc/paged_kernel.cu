@@ -615,7 +615,9 @@ size_t paged_cut_bytes(int ctas) { return sizeof(Cut) * static_cast<size_t>(ctas
 
 cudaError_t launch_paged_decode(const PagedArgs& a, int mode, int d, int ctas, int row_tile,
                                 const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  if (mode == kShared) return launch_paged_prefix(a, d, ctas, tk, tv, st);
+  // Groups alone are taken 128 rows at a time, groups and own rows in one launch 8 or 16.
+  if (mode == kShared) return row_tile == 128 ? launch_paged_prefix(a, d, ctas, tk, tv, st) : cudaErrorInvalidValue;
+  if (mode == kBoth && row_tile > 16) return cudaErrorInvalidValue;
   if (row_tile == 128) return launch_paged_tc(a, mode, d, ctas, tk, tv, st);
   auto run = [&](auto m) {
     constexpr int MODE = decltype(m)::value;

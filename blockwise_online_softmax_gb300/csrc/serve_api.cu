@@ -222,6 +222,25 @@ int decode_launch(ra::PagedArgs& a, int d, int rt, const CUtensorMap& tk, const 
   return ef == cudaSuccess ? RA_OK : cuda_fail(ef, "cudaFreeAsync");
 }
 
+// A prefix call's own rows and, right behind them, its groups' rows.  The second
+// launch starts before the first has ended and reads without a wait of its own what
+// was there before both: the first lets it start only after waiting for that
+// (start_wait in paged_walk.cuh).  So the two are made here and nowhere else.
+cudaError_t launch_apart(const ra::PagedArgs& own, int own_tile, int own_ctas, const ra::PagedArgs& shared, int shared_tile,
+                         int shared_ctas, int d, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  cudaError_t e;
+  {
+    TraceScope ts(RA_KERNEL_PAGED_DECODE, st);
+    e = ra::launch_paged_decode(own, ra::kPagedOwn, d, own_ctas, own_tile, tk, tv, st);
+    ts.done(e == cudaSuccess);
+  }
+  if (e != cudaSuccess || shared.n_groups == 0) return e;
+  TraceScope ts(RA_KERNEL_PAGED_PREFIX, st);
+  e = ra::launch_paged_decode(shared, ra::kPagedShared, d, shared_ctas, shared_tile, tk, tv, st);
+  ts.done(e == cudaSuccess);
+  return e;
+}
+
 // What the three rope calls share.
 int rope_common(ra::RopeArgs& a, long long T, int d, int heads, int kv_heads, int dtype, int rot,
                 int interleaved, const void* phases, const void* qw, const void* kw, int w_dtype,
@@ -704,15 +723,12 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
   } else {
     place(shared, scratch + own_bytes, rows);
   }
-  {
-    TraceScope ts(both ? RA_KERNEL_PAGED_PREFIX : RA_KERNEL_PAGED_DECODE, st);
-    e = ra::launch_paged_decode(own, both ? ra::kPagedBoth : ra::kPagedOwn, d, ctas_of(tile), tile, tk, tv, st);
-    ts.done(e == cudaSuccess);
-  }
-  if (e == cudaSuccess && !both && n_groups > 0) {
+  if (both) {
     TraceScope ts(RA_KERNEL_PAGED_PREFIX, st);
-    e = ra::launch_paged_decode(shared, ra::kPagedShared, d, ctas_of(shared_tile), shared_tile, tk, tv, st);
+    e = ra::launch_paged_decode(own, ra::kPagedBoth, d, ctas_of(tile), tile, tk, tv, st);
     ts.done(e == cudaSuccess);
+  } else {
+    e = launch_apart(own, tile, ctas_of(tile), shared, shared_tile, ctas_of(shared_tile), d, tk, tv, st);
   }
   if (e == cudaSuccess) {
     own.n_req = n_req;
