@@ -636,7 +636,7 @@ def ra_paged_decode_prefix(q, k_cache, v_cache, prefix_table, prefix_lengths, cu
     once for all of them.  Group p is the requests [cu_req[p], cu_req[p + 1])
     (int32 [n_groups + 1]); its prefix of prefix_lengths[p] tokens (int32
     [n_groups], any length) lies in pages prefix_table[p] (int32 [n_groups,
-    max_prefix_pages]).  block_table and lengths are of the requests' own
+    prefix_max_pages]).  block_table and lengths are of the requests' own
     tokens, the new ones included, which stand behind the prefix: add its
     length to their positions.  Everything else, the returned (out, lse) too,
     as in ra_paged_decode, without a window."""

@@ -55,15 +55,20 @@ int page_shift(int page_size, int* shift) {
   return fail(RA_ERR_UNSUPPORTED, "page_size=%d (supported: 8, 16, 32, 64, 128, 256)", page_size);
 }
 
-int check_table(int n_req, int max_pages, int page_size, int* shift) {
+// prefix: the table is of prefixes, [n_groups, prefix_max_pages].
+int check_table(int n, int pages, int page_size, int* shift, bool prefix = false) {
+  const char* n_name = prefix ? "n_groups" : "n_req";
+  const char* pages_name = prefix ? "prefix_max_pages" : "max_pages";
   int rc;
   if ((rc = page_shift(page_size, shift)) != RA_OK) return rc;
-  if (n_req < 0) return fail(RA_ERR_INVALID, "n_req=%d is negative", n_req);
-  if (max_pages < 1) return fail(RA_ERR_INVALID, "max_pages=%d must be >= 1", max_pages);
-  if (static_cast<long long>(n_req) * max_pages > kMaxInt)
-    return fail(RA_ERR_UNSUPPORTED, "n_req * max_pages = %lld exceeds 2^31 - 1", static_cast<long long>(n_req) * max_pages);
-  if (static_cast<long long>(max_pages) * page_size > kMaxInt - 255)  // a tile of headroom for the kernels' 32-bit positions
-    return fail(RA_ERR_UNSUPPORTED, "max_pages * page_size = %lld exceeds 2^31 - 256", static_cast<long long>(max_pages) * page_size);
+  if (n < 0) return fail(RA_ERR_INVALID, "%s=%d is negative", n_name, n);
+  if (pages < 1) return fail(RA_ERR_INVALID, "%s=%d must be >= 1", pages_name, pages);
+  if (static_cast<long long>(n) * pages > kMaxInt)
+    return fail(RA_ERR_UNSUPPORTED, "%s * %s = %lld exceeds 2^31 - 1%s", n_name, pages_name,
+                static_cast<long long>(n) * pages, prefix ? ", as n_req * max_pages may not" : "");
+  if (static_cast<long long>(pages) * page_size > kMaxInt - 255)  // a tile of headroom for the kernels' 32-bit positions
+    return fail(RA_ERR_UNSUPPORTED, "%s * page_size = %lld exceeds 2^31 - 256", pages_name,
+                static_cast<long long>(pages) * page_size);
   return RA_OK;
 }
 
@@ -649,9 +654,8 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
   int rc = decode_args(own, q, out, lse, T, n_req, n_q, cu_q, block_table, max_pages, lengths, n_pages, page_size, 0,
                        d, heads, kv_heads, dtype, out_dtype);
   if (rc != RA_OK) return rc;
-  if (n_groups < 0) return fail(RA_ERR_INVALID, "n_groups=%d is negative", n_groups);
   int shift = 0;
-  if ((rc = check_table(n_groups, prefix_max_pages, page_size, &shift)) != RA_OK) return rc;
+  if ((rc = check_table(n_groups, prefix_max_pages, page_size, &shift, true)) != RA_OK) return rc;
   const long long page_elems = static_cast<long long>(page_size) * kv_heads * d;
   if ((rc = check_cache("k_page_stride", k_page_stride, page_elems)) != RA_OK) return rc;
   if ((rc = check_cache("v_page_stride", v_page_stride, page_elems)) != RA_OK) return rc;

@@ -714,7 +714,7 @@ PyObject* decode_prefix(PyObject* const* a) {
   Decode x(a[0], a[1], a + 6, a + 10);
   const int64_t groups = plen.numel();
   if (ptab.dim() != 2 || ptab.size(0) != groups)
-    refuse(PyExc_ValueError, "prefix_table must be [n_groups=%lld, max_pages], got %s", static_cast<long long>(groups),
+    refuse(PyExc_ValueError, "prefix_table must be [n_groups=%lld, prefix_max_pages], got %s", static_cast<long long>(groups),
            shape_of(ptab).c_str());
   const void* pq = dense(x.q, "q", x.dev, ScalarType::BFloat16);
   const Cache ck = cache(x.kc, "k_cache", x.kv_heads, x.d, x.dev), cv = cache(vc, "v_cache", x.kv_heads, x.d, x.dev);
@@ -725,7 +725,7 @@ PyObject* decode_prefix(PyObject* const* a) {
   const int* pcr = ints(cur, "cu_req", groups + 1, x.dev);
   const int* pc = x.cu ? ints(*x.cu, "cu_q", x.n + 1, x.dev) : nullptr;
   const int* pl = ints(x.len, "lengths", x.n, x.dev);
-  const int n_groups = to_int(groups, "n_groups"), width = to_int(ptab.size(1), "max_pages");
+  const int n_groups = to_int(groups, "n_groups"), width = to_int(ptab.size(1), "prefix_max_pages");
   const Place at(x.dev, a[12]);
   x.make(at);
   void* po = x.out_ptr();
