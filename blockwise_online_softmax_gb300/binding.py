@@ -639,7 +639,8 @@ def ra_paged_decode_prefix(q, k_cache, v_cache, prefix_table, prefix_lengths, cu
     prefix_max_pages]).  block_table and lengths are of the requests' own
     tokens, the new ones included, which stand behind the prefix: add its
     length to their positions.  Everything else, the returned (out, lse) too,
-    as in ra_paged_decode, without a window."""
+    as in ra_paged_decode, without a window; with a bf16 out the weights over
+    a long prefix are held to 2^-17 of themselves, with fp32 to 24 bits."""
     return (_serve or _fast()).paged_decode_prefix(
         q, k_cache, v_cache, prefix_table, prefix_lengths, cu_req, block_table, lengths, cu_q, n_q,
         out, lse, stream)

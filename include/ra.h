@@ -577,7 +577,11 @@ int ra_paged_decode(const void* q, const void* k_cache, const void* v_cache, voi
  *     of one whose prefix has length 0, sees its own keys alone.
  *   prefix_table: [n_groups, prefix_max_pages], prefix_lengths: [n_groups], device
  *     int32, with the limits and clamps of block_table and lengths.
- *   Everything else, cu_q, n_q, out and lse too, as in ra_paged_decode.  There is
+ *   Everything else, cu_q, n_q, out and lse too, as in ra_paged_decode, but for the
+ *   weights over a prefix where out is bf16: 17 bits and more of them are kept
+ *   (each is off by at most 2^-17 of itself, and a row's sum of p v by that part of
+ *   the sum of |p v|; rounding out takes up to 2^-8 of it), or all 24 where the
+ *   kernel for few rows or a short prefix is taken.  With fp32 out all 24.  There is
  *   no window: the keys that a window leaves of a prefix differ from row to row.
  *   Scratch: the states of all rows twice, T * heads * (8 d + 32) bytes, from the
  *   pool.
