@@ -55,13 +55,13 @@ namespace {
 using namespace paged;
 
 constexpr int kThreads = kMmaThreads;
-constexpr int kKB = 2;
+constexpr int KB = 2;  // blocks of 16 keys that a warp takes of a tile
 
-// KB: blocks of 16 keys that a warp takes of a tile.  HP: KV heads of an item.
-template <int D, int NT, int KB, int HP>
+// NT: 8-row groups of query rows, HP: KV heads of an item.
+template <int D, int NT, int HP>
 struct Cfg {
   static constexpr int DIM = D, BT = 16 * kCons * KB, HEADS = HP;
-  static constexpr int NCH = 1, BOX = KB == 1 ? 6 : 7;
+  static constexpr int NCH = 1, BOX = 7;
   static constexpr uint32_t CHROW = D * HP, CHB = BT * CHROW;  // rows of 128 or 64 bytes, swizzled over as many
   static constexpr bool SCALES = true;
   static constexpr int RT = 8 * NT;
@@ -126,10 +126,10 @@ __device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
   return v;
 }
 
-template <int D, int NT, int KB, int HP>
+template <int D, int NT, int HP>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
-  using C = Cfg<D, NT, KB, HP>;
+  using C = Cfg<D, NT, HP>;
   // AHEAD: the scores of a tile (and head) are multiplied while the softmax of the one
   // before, a long chain of dependent steps, is under way.  600K keys, d = 128, 4 rows 229 -> 214 us, 128 requests of up to 8K keys 144 ->
   // 134; 1.2M keys, d = 64, 9 rows 172 -> 157; 16 requests of up to 2000 keys 13.3 ->
@@ -542,10 +542,10 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 template <int D, int NT, int HP>
 cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  constexpr uint32_t smem = Cfg<D, NT, kKB, HP>::SMEM;
-  cudaError_t e = allow_smem(paged_fp8_kernel<D, NT, kKB, HP>, smem, done);
+  constexpr uint32_t smem = Cfg<D, NT, HP>::SMEM;
+  cudaError_t e = allow_smem(paged_fp8_kernel<D, NT, HP>, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_early(paged_fp8_kernel<D, NT, kKB, HP>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, st, tk, tv, a);
+  return launch_early(paged_fp8_kernel<D, NT, HP>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, st, tk, tv, a);
 }
 
 }  // namespace
@@ -566,7 +566,7 @@ int paged_fp8_item_heads(const PagedArgs& a, int d, int row_tile) {
   const long long tokens = (static_cast<long long>(a.n_req) * a.max_pages) << a.page_shift;
   return d == 64 && a.kv_heads % 2 == 0 && row_tile == 8 && tokens * a.kv_heads > (48LL << 20) / (2 * 64) ? 2 : 1;
 }
-int paged_fp8_box_rows() { return 64 * kKB; }
+int paged_fp8_box_rows() { return 16 * kCons * KB; }
 
 cudaError_t launch_paged_fp8(const PagedArgs& a, int d, int ctas, int row_tile, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {
