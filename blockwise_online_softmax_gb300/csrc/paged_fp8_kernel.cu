@@ -22,7 +22,7 @@
 //   in two fp16 terms (22 bits and the sign of the second) a weight is off by at
 //   most 2^-23 of itself, or 2^-39 of the row's largest there.  Rows have powers of
 //   their own: what one weighs, another may not see.  (One power for the warp, found by
-//   one instruction, took 487 for 504 us at 1M keys and 155 for 166 at 1.2M, d = 64, 9
+//   one instruction, took 487 for 503 us at 1M keys and 155 for 162 at 1.2M, d = 64, 9
 //   rows, and lost a row's weights beside another's of a far larger scale.  bf16 pages
 //   need three terms of 8 bits.)
 // - A consumer warp takes 32 keys of a tile, and O is scaled only under a new maximum
@@ -32,10 +32,12 @@
 // 32/8 heads, d = 128, one row: 128 requests of up to 8K keys 123 to 136 us with the
 // machine, 5.4 to 5.9 TB/s (0.79 to 0.87 of the copy rate; rows of 128 bytes some
 // distance apart); bound by HBM and the ends of items.  16 rows (1M and some keys, 4
-// new tokens): 488 us, 5.5 TB/s (0.82); bound by the latency of a tile's chain with two
-// warps a scheduler and no registers to overlap two tiles.  d = 64 with 9 rows (1.2M
-// keys, 4 heads): 154 us, 4.0 TB/s; bound by issue, some 1000 cycles a warp and tile.  16
-// requests of up to 2000 keys 13.5 us: two launches and their chains of loads.
+// new tokens): 503 us, 5.4 TB/s (0.79); d = 64 with 9 rows (1.2M keys, 4 heads) 162 us,
+// 3.8 TB/s, with 3 rows, two heads an item, 141 us, 4.4 TB/s.  These three are bound by
+// the latency of a tile's chain (products, maximum, exponentials, weights' power,
+// products) with two consumer warps a scheduler: of the issue slots 42, 46 and 40% are
+// busy, of the tensor pipe 40, 30 and 18%, of DRAM 63, 47 and 58%.  16 requests of up to
+// 2000 keys 13.5 us: two launches and their chains of loads.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -130,14 +132,15 @@ template <int D, int NT, int HP>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedArgs a) {
   using C = Cfg<D, NT, HP>;
-  // AHEAD: the scores of a tile (and head) are multiplied while the softmax of the one
-  // before, a long chain of dependent steps, is under way.  600K keys, d = 128, 4 rows 229 -> 214 us, 128 requests of up to 8K keys 144 ->
-  // 134; 1.2M keys, d = 64, 9 rows 172 -> 157; 16 requests of up to 2000 keys 13.3 ->
-  // 13.6.  (With the wait for V after the softmax most works are slower than without
-  // AHEAD, by up to 5%.)  16 rows at d = 128 have few registers left for it: 64 requests
-  // of up to 4000 keys and 64 rows 192 -> 214, 1M keys 480 either way; with the query
-  // rows read from shared memory for each tile 220 and 463.
-  constexpr bool AHEAD = D == 64 || NT == 1;
+  // AHEAD: the scores of a tile are multiplied while the softmax of the one before, a
+  // long chain of dependent steps, is under way.  Without and with, us: 128 requests of
+  // up to 8K keys 145 and 136, 600K keys 228 and 215 (16 requests of up to 2000 keys 13.3
+  // and 13.6).  At d = 64 a tile's products are half as long: 60 requests of a 4K window,
+  // 9 rows 34.3 and 36.0, 1.2M keys 163 and 166, 16 requests of up to 2000 keys 10.7 and
+  // 11.4.  16 rows at d = 128 have few registers left for it: 64 requests of up to 4000
+  // keys and 64 rows 199 and 218, 1M keys 504 and 500.
+  constexpr bool AHEAD = D == 128 && NT == 1;
+  static_assert(!AHEAD || HP == 1, "one head's scores ahead");
   constexpr int RT = C::RT, BT = C::BT, ROW = D * HP;  // bytes of a key's row
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -433,8 +436,8 @@ paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 }
               }
           };
-          if (AHEAD && (s + 1 < HP || more)) {
-            products(s + 1 < HP ? st : then, s + 1 < HP ? s + 1 : 0);
+          if (AHEAD && more) {
+            products(then, 0);
             softmax();
           } else {
             softmax();
@@ -553,15 +556,16 @@ cudaError_t decode_t(const PagedArgs& a, int ctas, const CUtensorMap& tk, const 
 int paged_fp8_row_tile(const PagedArgs& a) { return a.n_q * (a.heads / a.kv_heads) <= 8 ? 8 : 16; }
 // At d = 64 and up to 8 rows two KV heads make an item, where they come in pairs: a
 // key's rows of both are 128 bytes, which HBM gives at a better rate than 64.  One
-// head and two, us: 1.2M keys, 4 heads, 3 rows 174 and 146; 152 requests of up to 6K
-// keys, 4 heads 54.5 and 46.4, 8 heads 87.7 and 77.1; 64 of up to 500, 16 heads 19.5
-// and 19.1.  A short call takes a longer step with two: 16 requests of up to 2000
-// keys, 4 heads 10.8 and 12.0, 8 heads 12.2 and 13.7, 4 of up to 300 8.6 and 11.0; so
+// head and two, us: 1.2M keys, 4 heads, 3 rows 168 and 141; 152 requests of up to 6K
+// keys, 4 heads 52.8 and 45.4, 8 heads 80.6 and 75.2; 64 of up to 500, 16 heads 18.9
+// and 18.7.  A short call takes a longer step with two: 16 requests of up to 2000
+// keys, 4 heads 10.8 and 11.8, 8 heads 11.9 and 13.5, 4 of up to 300 9.2 and 11.0; so
 // not where the block table has no room for more than 48 MB of pages.  With 16 rows
 // the arithmetic is the longer part, and half as many items share the work worse: 60
 // requests of 4K keys, 4 heads, 9 rows 36.5 and 46.3, 1.2M keys 176 and 182.  At d =
 // 128 pairs take 0.92 of the time for 600K keys, and more for all shorter ones (152
-// requests of up to 3000 keys 69 and 78, 16 of up to 2000 13.4 and 16.1).
+// requests of up to 3000 keys 69 and 78, 16 of up to 2000 13.4 and 16.1; these and
+// those of 16 rows with the scores ahead and one power of two for a warp's weights).
 int paged_fp8_item_heads(const PagedArgs& a, int d, int row_tile) {
   const long long tokens = (static_cast<long long>(a.n_req) * a.max_pages) << a.page_shift;
   return d == 64 && a.kv_heads % 2 == 0 && row_tile == 8 && tokens * a.kv_heads > (48LL << 20) / (2 * 64) ? 2 : 1;
