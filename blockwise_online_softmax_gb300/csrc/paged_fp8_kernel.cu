@@ -36,7 +36,7 @@
 // 3.8 TB/s, with 3 rows, two heads an item, 141 us, 4.4 TB/s.  These three are bound by
 // the latency of a tile's chain (products, maximum, exponentials, weights' power,
 // products) with two consumer warps a scheduler: of the issue slots 42, 46 and 40% are
-// busy, of the tensor pipe 40, 30 and 18%, of DRAM 63, 47 and 58%.  16 requests of up to
+// busy, of the tensor pipe 40, 31 and 18%, of DRAM 63, 48 and 58%.  16 requests of up to
 // 2000 keys 13.5 us: two launches and their chains of loads.
 #include <atomic>
 #include <cmath>

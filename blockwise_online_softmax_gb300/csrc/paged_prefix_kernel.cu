@@ -24,8 +24,9 @@
 // (948 TFLOP/s), fp32 179; d = 64 115 and 150.  What bounds it: at d = 128 the products,
 // 24 or 32 of 128 x 128 x 16 a tile at 77 to 65 cycles each (the tensor pipe is 64 and
 // 69% busy), and the chain from one to the next, for there are four slots; at d = 64
-// the softmax, some 2400 of a tile's 2570 cycles of a scheduler with three terms (the
-// tensor pipe 49%).  Tried on top and no faster: scores and T requested ahead of use
+// a softmax warp's chain (scores from TMEM, exponentials, three cuts, stores, 16 keys at
+// a time), which two softmax warps and one of the sum on a scheduler do not cover: no
+// unit is full (issue slots 61%, tensor pipe 49%).  Tried on top and no faster: scores and T requested ahead of use
 // (146 to 155 and 192 to 198), P V by halves of the keys as their weights come (165,
 // 217), a reference that is raised only for scores far above it, so one pass over S
 // and no maximum to hand on (the call 227 -> 242 us for fp32 at d = 128, 191 for bf16
@@ -71,9 +72,10 @@ struct Item {
   int pad;
 };
 
-// True in one lane of the warp.  (The compiler knows that, and keeps what the lane's
-// products share in uniform registers: with `lane == 0` it moved the operands of
-// each there one by one, some 97 cycles a product whatever its width.)
+// True in one lane of the warp.  (With `lane == 0` in its place a product took some 97
+// cycles to issue whatever its width; with this it is 46 to 80.  The likely reason is
+// that the compiler knows of this form that one lane is left, and so keeps what the
+// products share in uniform registers; that has not been looked at.)
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));

@@ -6,9 +6,9 @@
 // in which every step narrows 32-fold, its page from the table); then the lanes
 // take sixteen columns each of the rows' k, then of their v, in order, with
 // kBatch loads of a lane in flight, and store 32 bytes at once where the output is
-// aligned to them.  348K tokens of 8 heads, d = 128: 356 us, 6.2 TB/s (0.91 of the
+// aligned to them.  348K tokens of 8 heads, d = 128: 358 us, 6.2 TB/s (0.91 of the
 // copy rate); as two 16-byte stores 382, eight columns a lane 368; 6000 tokens 7.1,
-// 10.2 and 7.5 us (floor 5.4).
+// 10.2 and 7.5 us (floor 5.4), and 8.0 where other work comes between the calls.
 #include <cstdint>
 
 #include <cuda_bf16.h>

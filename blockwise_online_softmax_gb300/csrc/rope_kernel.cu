@@ -406,8 +406,9 @@ constexpr int kAppendCtas = 2;  // per SM
 // FP8: k and v in 8 bits (fp8.cuh), from the fp32 values, so rounded once.  The
 // maximum of a row costs an exchange per halving of its lanes, no pass over
 // memory.  20K tokens of 12/4 heads, d = 64: 22.5 us, 4.1 TB/s (0.60 of the copy rate),
-// bound by issue (63% of the slots: angles, maxima, codes); 256 tokens of 32/8 heads 4.8
-// us, the launch and one chain of loads.
+// where no unit is full (61% of the issue slots, 30% of DRAM's nominal rate) and a warp
+// waits for its own steps: loads, angles, then v's maximum and k's by exchanges in turn;
+// 256 tokens of 32/8 heads 4.8 us, the launch and one chain of loads.
 template <int D, bool INTER, bool FP8>
 __global__ void __launch_bounds__(kWarps * 32, kAppendCtas) rope_append_kernel(const RopeArgs a) {
   let_next_start();

@@ -637,7 +637,9 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
  * itself or to 2^-39 of the largest that the same row has among 32 keys, whichever
  * is more.  What one row weighs does not change another.  Query rows
  * of a request and KV head are taken 16 at a time, and each 16 read its pages
- * again: for a few new tokens (for the chunks of a prompt, ra_paged_read_fp8 and
+ * again: for a few new tokens (64 requests of 1000 to 4000 keys, 8 KV heads, d = 128:
+ * 8 rows 57 us, 16 85, 32 153, 64 291, where ra_paged_decode over bf16 pages takes 71,
+ * 99, 145 and 156; for the chunks of a prompt, ra_paged_read_fp8 and
  * ra_decode_forward).
  */
 int ra_paged_append_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
