@@ -42,7 +42,7 @@
 
 #include <cuda_bf16.h>
 
-#include "paged_walk.cuh"
+#include "paged_umma.cuh"
 
 namespace ra {
 
@@ -51,12 +51,9 @@ __device__ int g_paged_prefix_status = 0;
 namespace {
 
 using namespace paged;
+using namespace paged::umma;
 
-constexpr int BT = 128;          // keys per tile
-constexpr int RT = 128;          // query rows of an item
-constexpr int kThreads = 512;
-constexpr uint32_t CHB = BT * 128;  // one 64-column chunk of a tile, 128-byte swizzle
-constexpr int kA = 3;               // alpha slots
+constexpr int kA = 3;  // alpha slots
 
 // An item, or the part of it that a CTA has.
 struct Item {
@@ -122,40 +119,14 @@ struct Cfg {
   }
 };
 
-// 32 lanes x 8 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// 32 lanes x 16 consecutive 32-bit columns (valid after tmem_wait_ld).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[j]));
 }
 
-// The two values cut to bf16, the first in the low half.
-__device__ __forceinline__ uint32_t high_halves(float a, float b) {
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-// What a pair of bf16 values leaves of two, exactly.
+// What a pair of rounded bf16 values leaves of two, exactly (drop_high: of cut ones).
 __device__ __forceinline__ void drop(float& a, float& b, uint32_t h) {
   const float na = __uint_as_float((h << 16) ^ 0x80000000u), nb = __uint_as_float((h & 0xffff0000u) ^ 0x80000000u);
-  f2unpack(fadd2(f2pack(a, b), f2pack(na, nb)), a, b);
-}
-// The same for a cut pair, without going through it.
-__device__ __forceinline__ void drop_high(float& a, float& b) {
-  const float na = __uint_as_float((__float_as_uint(a) & 0xffff0000u) ^ 0x80000000u);
-  const float nb = __uint_as_float((__float_as_uint(b) & 0xffff0000u) ^ 0x80000000u);
   f2unpack(fadd2(f2pack(a, b), f2pack(na, nb)), a, b);
 }
 
