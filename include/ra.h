@@ -635,7 +635,8 @@ int ra_paged_decode_prefix(const void* q, const void* k_cache, const void* v_cac
  * and by what is held in fp16 terms on the way: an entry of q to 2^-39 of its
  * row's largest, or exactly, and a value's weight times its scale to 2^-23 of
  * itself or to 2^-39 of the largest that the same row has among 32 keys, whichever
- * is more.  What one row weighs does not change another.  Query rows
+ * is more (and no finer than fp32's least step, 2^-149).  What one row weighs does
+ * not change another.  Query rows
  * of a request and KV head are taken 16 at a time, and each 16 read its pages
  * again: for a few new tokens (64 requests of 1000 to 4000 keys, 8 KV heads, d = 128:
  * 8 rows 57 us, 16 85, 32 153, 64 291, where ra_paged_decode over bf16 pages takes 71,
